@@ -333,6 +333,179 @@ DFLASH_API int dflash_prepare_inputs(const int32_t* idx_mapping, const int32_t* 
                                      int32_t* sample_idx_mapping, int32_t* status, dflash_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------------------
+ * Decoding over the paged store: rotary positions, attention of one new token, the selection
+ * over beams and vocabulary, and the pages of the store. One beam-search step is
+ *   dflash_reserve_pages -> dflash_rotary (k and v to the slots) -> dflash_decode_attention_paged
+ *   -> (projections, logits) -> dflash_beam_select -> dflash_fork_pages (parents),
+ * all lengths, positions, slots and tables on the device: one captured graph replays it.
+ * ---------------------------------------------------------------------------------------
+ */
+
+/*
+ * dflash_rotary -- rotary positions of queries and keys, with an optional store write.
+ *
+ *   For pair i < rotary_dim / 2 of a head at position p, t = p * inv_freq[i], a = amplitude:
+ *     u' = a (u cos t - v sin t),  v' = a (v cos t + u sin t)   (inverse: sin t negated)
+ *   (u, v) = elements (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved. Elements from
+ *   rotary_dim on are copied. The inverse is the transpose: applied to the gradient of the
+ *   outputs it gives the gradient of the inputs.
+ *
+ *   q, k     [n, Hq, Dh], [n, Hkv, Dh] of `dtype` (DFLASH_OUT_BF16 or DFLASH_OUT_F32); element
+ *            (t, h, d) at t * *_tok + h * *_head + d (strides in elements, so slices of a fused
+ *            projection do). Hq = 0 or Hkv = 0 leaves one out.
+ *   v        [n, Hkv, Dh] or NULL: copied to v_out (with k's slots)
+ *   q_out    like q; may be q itself with the same strides
+ *   k_out, v_out  row t, or row slot[t] where slot is given: [capacity, Hkv, Dh] with their own
+ *            strides. Without slots k_out may be k itself (same strides) and n <= capacity.
+ *            Other overlaps of inputs and outputs are not allowed.
+ *   positions int32 [n]    any sign; the angle is exact to 1e-6 rad below 2^24
+ *   slot     int32 [n] or NULL; -1 = the row is not stored (padding); a slot >= capacity is not
+ *            stored and reported through status. Slots must be distinct.
+ *   inv_freq HOST double [rotary_dim / 2], |.| <= 1: read during the call (a captured graph
+ *            keeps their values)
+ *   dh in [2, 1024], rotary_dim even, in [2, min(dh, 256)]; any alignment of elements (16-byte
+ *   aligned rows and sizes in multiples of 16 bytes run fastest).
+ *   status   int32 device word or NULL, as dflash_context_kv
+ *   f32 arithmetic, one rounding to `dtype`. One launch.
+ */
+DFLASH_API int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void* q_out, int64_t q_out_tok,
+                             int64_t q_out_head, int hq, const void* k, int64_t k_tok, int64_t k_head, void* k_out,
+                             int64_t k_out_tok, int64_t k_out_head, int hkv, const void* v, int64_t v_tok,
+                             int64_t v_head, void* v_out, int64_t v_out_tok, int64_t v_out_head,
+                             const int32_t* positions, const int32_t* slot, int64_t n, int64_t capacity, int dh,
+                             int rotary_dim, const double* inv_freq, double amplitude, int interleaved, int inverse,
+                             int dtype, int32_t* status, dflash_stream_t stream);
+
+/* Bytes of workspace of dflash_decode_attention_paged on the current device (0 and a message if the
+ * arguments are invalid). It needs no initialisation; concurrent calls must not share one. */
+DFLASH_API size_t dflash_decode_workspace_size(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int window);
+
+/*
+ * dflash_decode_attention_paged -- attention of one new token per sequence over the paged store.
+ *
+ *   out[r, h] = sum_j p_j v_j / sum_j p_j, p_j = exp(scale <q[r, h], k_j>), over the stored rows
+ *   j of kv head h / (Hq / Hkv) with max(0, L - window) <= j < L (window = 0: all), L = seq_lens[r].
+ *   The token's own key and value are stored rows like the others (its length already counts them).
+ *
+ *   q          bf16 [num_reqs, Hq, Dh], heads contiguous, q_stride elements between sequences;
+ *              final queries (normed, rotated)
+ *   k_pool, v_pool  bf16 [num_pages, page_size, Hkv, Dh], any page_size >= 1
+ *   block_table int32 [num_reqs, max_pages_per_req], block_table_stride entries between rows:
+ *              row j of sequence r is row j % page_size of page block_table[r, j / page_size].
+ *              Sequences may share pages.
+ *   seq_lens   int32 [num_reqs] device. A length of 0 gives zeros and a log-sum of -inf; one that
+ *              is negative or above max_ctx_len is reported and treated as 0.
+ *   max_ctx_len host bound of the lengths (<= max_pages_per_req * page_size); sizes the grid and
+ *              the workspace, and is otherwise free: work follows the device lengths
+ *   scale      <= 0 means 1/sqrt(Dh)
+ *   out        bf16 or f32 [num_reqs, Hq, Dh] (out_dtype)
+ *   lse        f32 [num_reqs, Hq] or NULL: log sum_j p_j
+ *   status     int32 device word or NULL: DFLASH_STATUS_METADATA is ORed in for a bad length or a
+ *              table entry outside [0, num_pages) (page 0 is read in its place)
+ *   Dh in {64, 128}; Hq % Hkv == 0, any group size. bf16 products are exact, sums f32; the weights
+ *   keep 16 bits for a bf16 output and 24 for an f32 one. Two launches (attention, join); one when
+ *   no sequence can be split. Results do not depend on timing.
+ */
+DFLASH_API int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const dflash_bf16* k_pool,
+                                             const dflash_bf16* v_pool, const int32_t* block_table,
+                                             int64_t block_table_stride, const int32_t* seq_lens, int num_reqs, int hq,
+                                             int hkv, int dh, int64_t num_pages, int page_size, int max_pages_per_req,
+                                             int max_ctx_len, float scale, int window, int out_dtype, void* out,
+                                             float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                                             dflash_stream_t stream);
+
+/* Bytes of workspace of dflash_beam_select on the current device (0 and a message if the arguments
+ * are invalid). It needs no initialisation; concurrent calls must not share one. */
+DFLASH_API size_t dflash_beam_workspace_size(int num_reqs, int beams, int beams_out, int vocab, int dtype);
+
+/*
+ * dflash_beam_select -- the K = beams_out best continuations of W = beams beams per request.
+ *
+ *   Candidate (w, t): score[w] + logits[w, t] - log sum_u exp(logits[w, u]); a finished beam has
+ *   the one candidate (w, eos) with its own score. The K largest, in descending order, ties to the
+ *   lowest w * vocab + t; a candidate of -inf is none, and a beam with a NaN or +inf logit or
+ *   score NaN has none.
+ *
+ *   logits   [num_reqs, W, vocab] of `dtype`, the last dimension contiguous, req_stride and
+ *            beam_stride elements apart; -inf masks a token
+ *   scores   f32 [num_reqs, W]; -inf = the beam is not live
+ *   finished uint8 [num_reqs, W] or NULL (then none is); needs eos >= 0
+ *   eos      end token, or -1: none
+ *   outputs  [num_reqs, K]: scores f32; tokens int32; parents int32 = r * W + w (the row of
+ *            dflash_fork_pages where K = W); finished uint8 = the parent's, or token == eos. Slots
+ *            without a candidate hold -inf, -1, -1 and 0.
+ *   1 <= W, K <= 32. Logits of one beam are compared exactly; scores of different beams in 64 bits,
+ *   each exponential within 2^-19 and their sum held in two f32 terms. Two launches.
+ */
+DFLASH_API int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stride, const float* scores,
+                                  const uint8_t* finished, int num_reqs, int beams, int beams_out, int vocab, int eos,
+                                  int dtype, float* out_scores, int32_t* out_tokens, int32_t* out_parents,
+                                  uint8_t* out_finished, void* workspace, size_t workspace_bytes,
+                                  dflash_stream_t stream);
+
+/*
+ * The pages of a store. A table row holds the pages of a sequence: entries >= 0 are held, unused
+ * entries are -1. page_refs int32 [num_pages] counts for every page the entries that name it;
+ * 0 = free. The calls keep the two consistent; a store starts with tables of -1 and counts of 0.
+ * All three work in place, on at most 16384 table rows. `pools` is a HOST array of num_pools <= 256
+ * device pointers (K and V of every layer), each [num_pages, page_bytes] with rows of a multiple of
+ * 16 bytes; the list may be empty (metadata alone). status: int32 device word or NULL.
+ */
+
+/* Bytes of workspace of dflash_reserve_pages and dflash_compact_pages. */
+DFLASH_API size_t dflash_pages_workspace_size(int num_reqs, int64_t num_pages);
+
+/*
+ * dflash_fork_pages -- row i continues the sequence of row parent[i]: its table row and length
+ * become the parent's (as they were before the call) and the counts follow. parent[i] = -1 frees
+ * row i (table -1, length 0); parent[i] = i leaves it. So one call reorders, forks and frees.
+ * Nothing is copied: forked rows share pages until dflash_reserve_pages lets one write.
+ *   parent int32 [num_reqs] device; outside [-1, num_reqs): reported, the row stays as it is.
+ *   A table entry outside the pages is reported and not counted. One launch.
+ */
+DFLASH_API int dflash_fork_pages(const int32_t* parent, int32_t* seq_lens, int32_t* block_table,
+                                 int64_t block_table_stride, int32_t* page_refs, int num_reqs, int max_pages_per_req,
+                                 int64_t num_pages, int32_t* status, dflash_stream_t stream);
+
+/*
+ * dflash_reserve_pages -- makes room for the rows new_start_loc[r] .. new_start_loc[r+1] that
+ * follow sequence r's stored seq_lens[r] rows, in pages that only it holds, and says where they go.
+ *
+ *   Every page that the new rows touch and that the sequence does not hold, or shares (count > 1),
+ *   is taken from the free ones: the lowest first, row by row in order. A shared page is given up
+ *   (its count falls by one for every row that leaves it) and, if it holds rows of the sequence,
+ *   those rows are copied to the new page in every pool. Which pages are free and shared is as at
+ *   the start of the call. A sequence is served while the pages taken so far, its own included, do
+ *   not exceed the free ones; the first that does not fit and every later one that needs a page
+ *   are refused: unchanged, slots -1, reported. So is one whose rows would not fit its table, or
+ *   whose entries are inconsistent.
+ *   slots, positions int32 [n]: row t of the pools' rows and position of every new row (-1 and 0 for
+ *              a refused sequence's and outside [new_start_loc[0], new_start_loc[num_reqs]))
+ *   advance    1: seq_lens of served sequences grow by their new rows (for callers that write the
+ *              rows themselves at the slots, e.g. dflash_rotary); 0: they stay (dflash_paged_append
+ *              advances them)
+ *   new_start_loc not nondecreasing within [0, n]: reported, nothing changes. Three launches.
+ */
+DFLASH_API int dflash_reserve_pages(const int32_t* new_start_loc, int32_t* seq_lens, int32_t* block_table,
+                                    int64_t block_table_stride, int32_t* page_refs, void* const* pools, int num_pools,
+                                    int64_t page_bytes, int num_reqs, int64_t n, int max_pages_per_req, int page_size,
+                                    int64_t num_pages, int advance, int32_t* slots, int32_t* positions,
+                                    void* workspace, size_t workspace_bytes, int32_t* status, dflash_stream_t stream);
+
+/*
+ * dflash_compact_pages -- moves the used pages together: with U pages in use, the used ones at
+ * U and behind go, in order, to the free ones before U, in every pool; tables and counts follow.
+ *   used     int32 device word: U
+ *   A table entry behind U that is no page, or one with a count of 0, stays and is reported.
+ *   Three launches.
+ */
+DFLASH_API int dflash_compact_pages(int32_t* block_table, int64_t block_table_stride, int32_t* page_refs,
+                                    void* const* pools, int num_pools, int64_t page_bytes, int num_reqs,
+                                    int max_pages_per_req, int64_t num_pages, int32_t* used, void* workspace,
+                                    size_t workspace_bytes, int32_t* status, dflash_stream_t stream);
+
+/*
  * Reads the device error word the last dflash_block_attention call on this workspace
  * left (waits for `stream`). Returns DFLASH_OK, DFLASH_ERR_DEVICE_TIMEOUT or
  * DFLASH_ERR_DEVICE_METADATA; the word is cleared by the next attention call.

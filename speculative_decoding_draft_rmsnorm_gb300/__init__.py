@@ -12,6 +12,8 @@ Entry points mirror include/dflash.h:
     block_attention(...)     -> dflash_block_attention
     workspace_size(...)      -> dflash_block_attention_workspace_size
     check_error(workspace)   -> dflash_check_error
+and, from decode.py, a decode step over the paged store: rotary, decode_attention_paged, beam_select,
+fork_pages, reserve_pages, compact_pages.
 """
 from __future__ import annotations
 
@@ -19,11 +21,18 @@ import ctypes
 import os
 import threading
 
+from . import decode as _decode
+from .decode import (beam_select, beam_workspace_size, compact_pages, decode_attention_paged,  # noqa: F401
+                     decode_workspace_size, fork_pages, pages_workspace_size, reserve_pages, rotary,
+                     rotary_frequencies)
+
 __all__ = ["load", "lib_path", "context_kv", "paged_append", "prepare_inputs", "STATUS_METADATA", "block_attention", "block_attention_paged", "workspace_size", "plan",
            "alloc_workspace",
            "check_error", "DFlashError", "OUT_BF16", "OUT_F32", "FLAG_FORCE_SPLIT", "FLAG_NO_SPLIT",
            "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_WORKSPACE", "ERR_CUDA", "ERR_DEVICE_TIMEOUT",
-           "ERR_DEVICE_METADATA"]
+           "ERR_DEVICE_METADATA", "rotary", "rotary_frequencies", "decode_attention_paged", "decode_workspace_size",
+           "beam_select", "beam_workspace_size", "fork_pages", "reserve_pages", "compact_pages",
+           "pages_workspace_size"]
 
 OUT_BF16, OUT_F32 = 0, 1
 STATUS_METADATA = 2  # bit ORed into the status word of context_kv / paged_append / prepare_inputs
@@ -83,6 +92,7 @@ def load(build_if_missing: bool = True):
         lib.dflash_prepare_inputs.restype = I32
         lib.dflash_prepare_inputs.argtypes = ([P] * 8 + [I32, I32, I64, I32, I32, I32, I32, I32, I64, I32, I32] +
                                               [P] * 12)
+        _decode.declare(lib)
         _lib = lib
         return lib
 
