@@ -8,12 +8,14 @@
 // second, tiny kernel turns W K candidates into scores -- in 64 bits, so that candidates of different
 // beams are not reordered by rounding.
 //
-// What bounds it: HBM, one read of the logits (2 or 4 bytes for ~8 operations and one exponential).
-// A warp streams a contiguous piece of a row, 16 bytes a lane and kVec such loads in flight, and keeps
-// its K best as a sorted list, one per lane. An element enters only if it beats the K-th; testing
-// costs one maximum and one vote per batch of loads. What makes insertions rare from the start: before
-// the first batch is inserted its lanes' maxima are sorted and the K-th largest is a bound that at
-// least K elements reach; warps of a block share the best bound so far in shared memory.
+// What bounds it: HBM, one read of the logits (2 or 4 bytes for ~6 operations and one exponential).
+// A block streams a piece of a row, 16 bytes a thread and kVec such loads in flight, and only keeps
+// maxima: one per thread and slot (a few batches of loads). The K-th largest of the block's 256 thread
+// maxima is a bound that at least K elements reach, so whatever is below it is out; the slots whose
+// maximum reaches it -- a dozen or two in the block -- are read once more (from L2) and their elements at
+// or above the bound become candidates, which are ranked against one another. Keeping sorted lists while
+// streaming instead cost 52 instructions an element against ~8. Only where ties flood the candidates
+// (a constant row) does a block go over its piece again with such lists, one a warp.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,7 +33,10 @@ constexpr int kScanThreads = kWarps * 32;
 constexpr int kMergeThreads = 512;
 constexpr int kMaxBeams = 32;         // W and K
 constexpr int kMaxCandidates = 4096;  // per request, W * splits * K
-constexpr int kVec = 4;               // 16-byte loads a lane has in flight
+constexpr int kVec = 4;               // 16-byte loads a thread has in flight
+constexpr int kSlots = 8;             // maxima a thread keeps
+constexpr int kRoom = 1024;           // candidates of a block
+constexpr int kMaxVocab = 1 << 26;    // W * vocab < 2^31
 
 // A sum in two f32 terms (Knuth's two-sum): 48 bits, so that what small terms add to a sum that a few
 // large ones dominate still orders beams whose large logits are equal.
@@ -105,88 +110,147 @@ __device__ __forceinline__ float exp_below(float x, float m) {
   return ex2_approx(fmaf(d, 1.925963033500e-8f, d * 1.442695021629f));
 }
 
-// The warp's best elements: lane i holds the i-th, by (value descending, index ascending); only the
-// first K matter. Offered in ascending index order, an element equal to the list's K-th never enters.
-// `floor` is a value that at least K elements of the row are known to reach: what is below it cannot be
-// among the row's K best, but an element equal to it can (it may come before those others).
+// A warp's best elements: lane i holds the i-th, by (value descending, index ascending); only the first
+// K matter. Offered in ascending index order, an element equal to the list's K-th never enters.
 struct TopList {
   float val = -INFINITY;
   int32_t idx = -1;
-  float floor = -INFINITY;
-  float bound = -INFINITY;  // the test in force: v > bound when strict, else v >= bound (and v > -inf)
-  bool strict = false;
+  float bound = -INFINITY;  // elements above it enter
 
-  __device__ __forceinline__ bool enters(float v) const { return strict ? v > bound : v >= bound && v > -INFINITY; }
-  __device__ __forceinline__ void raise_floor(float f, int k) {
-    if (f > floor) {
-      floor = f;
-      settle(k);
-    }
-  }
-  __device__ __forceinline__ void settle(int k) {
-    const bool have = __shfl_sync(0xffffffffu, idx, k - 1) >= 0;
-    const float kth = __shfl_sync(0xffffffffu, val, k - 1);
-    strict = have && kth >= floor;
-    bound = strict ? kth : floor;
-  }
   __device__ __forceinline__ void insert(float v, int32_t i, int k, int lane) {
     const int at = __popc(__ballot_sync(0xffffffffu, idx >= 0 && val >= v));
     const float pv = __shfl_up_sync(0xffffffffu, val, 1);
     const int32_t pi = __shfl_up_sync(0xffffffffu, idx, 1);
     if (lane > at) val = pv, idx = pi;
     if (lane == at) val = v, idx = i;
-    settle(k);
+    bound = __shfl_sync(0xffffffffu, val, k - 1);  // -inf until the list is full
   }
   // Offers x[0..N) of every lane (indices first + i, ascending over the lanes); most = their maximum.
   template <int N>
   __device__ __forceinline__ void offer(const float (&x)[N], int32_t first, float most, int k, int lane) {
-    uint32_t hits = __ballot_sync(0xffffffffu, enters(most));
+    uint32_t hits = __ballot_sync(0xffffffffu, most > bound);
     while (hits) {
       const int src = __ffs(hits) - 1;
       const int32_t f = __shfl_sync(0xffffffffu, first, src);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float v = __shfl_sync(0xffffffffu, x[i], src);
-        if (enters(v)) insert(v, f + i, k, lane);
+        if (v > bound) insert(v, f + i, k, lane);
       }
       hits &= hits - 1;
-      hits &= __ballot_sync(0xffffffffu, enters(most));
+      hits &= __ballot_sync(0xffffffffu, most > bound);
     }
   }
 };
+
+// A block's piece of a row: elements [0, head) and [tail, vocab) one by one (the first and the last
+// piece), 16-byte vectors [lo, hi) between.
+struct Piece {
+  const char* base;
+  const uint4* vec;
+  int head, tail, vocab, lo, hi;
+  bool first, last;
+};
+
+// The block's K best by sorted lists: warps take consecutive parts in index order.
+template <bool F32>
+__device__ __noinline__ void piece_lists(const Piece& p, int K, float* s_val, int32_t* s_idx) {
+  using V = Vec<F32>;
+  constexpr int E = V::kElems;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lo = p.lo + static_cast<int>(static_cast<int64_t>(p.hi - p.lo) * warp / kWarps);
+  const int hi = p.lo + static_cast<int>(static_cast<int64_t>(p.hi - p.lo) * (warp + 1) / kWarps);
+  TopList top;
+  auto single = [&](int i, bool have) {
+    float x[1] = {have ? V::one(p.base, i) : -INFINITY};
+    top.offer(x, i, x[0], K, lane);
+  };
+  if (p.first && warp == 0) single(lane, lane < p.head);
+  for (int v0 = lo; v0 < hi; v0 += 32) {
+    const int v = v0 + lane;
+    float x[E], most = -INFINITY;
+    const uint4 raw = v < hi ? ld_stream(p.vec + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      x[i] = V::at(raw, i);
+      if (v < hi) most = fmaxf(most, x[i]);
+    }
+    top.offer(x, p.head + v * E, most, K, lane);
+  }
+  if (p.last && warp == kWarps - 1) single(p.tail + lane, p.tail + lane < p.vocab);
+  if (lane < K) {
+    s_val[warp * K + lane] = top.val;
+    s_idx[warp * K + lane] = top.idx;
+  }
+}
+
+// max of the elements of a vector, NaN ignored.
+template <bool F32>
+__device__ __forceinline__ float max_of(const uint4& v) {
+  if constexpr (F32) {
+    return fmax3(__uint_as_float(v.x), __uint_as_float(v.y), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else {
+    uint32_t a, b;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return fmaxf(bf16lo_to_f32(a), bf16hi_to_f32(a));
+  }
+}
+
+// Sum of exp(x - ref) over a vector: two elements an instruction (see exp_below).
+template <bool F32>
+__device__ __forceinline__ float exp_sum(const uint4& v, float ref) {
+  using V = Vec<F32>;
+  const uint64_t off = f32x2(-ref, -ref), c = f32x2(1.442695021629f, 1.442695021629f),
+                 tail = f32x2(1.925963033500e-8f, 1.925963033500e-8f), zero = f32x2(0.0f, 0.0f);
+  uint64_t sum = zero;
+#pragma unroll
+  for (int i = 0; i < V::kElems; i += 2) {
+    const uint64_t d = add_f32x2(f32x2(V::at(v, i), V::at(v, i + 1)), off);
+    const uint64_t t = fma_f32x2(d, tail, fma_f32x2(d, c, zero));
+    float a, b;
+    f32x2_split(t, a, b);
+    sum = add_f32x2(sum, f32x2(ex2_approx(a), ex2_approx(b)));
+  }
+  float a, b;
+  f32x2_split(sum, a, b);
+  return a + b;
+}
 
 template <bool F32>
 __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
   using V = Vec<F32>;
   constexpr int E = V::kElems;
-  __shared__ uint32_t s_bound;      // order key of a value that >= K elements of the block's piece reach
-  __shared__ float s_val[kWarps * kMaxBeams];
-  __shared__ int32_t s_idx[kWarps * kMaxBeams];
+  constexpr int kBatch = kScanThreads * kVec;  // vectors of a batch
   __shared__ float s_max[kWarps];
   __shared__ Sum s_sum[kWarps];
+  __shared__ float s_bound;
+  __shared__ int s_count;
+  __shared__ float s_val[kRoom];
+  __shared__ int32_t s_idx[kRoom];
   const int row = blockIdx.x / a.splits, split = blockIdx.x - row * a.splits;
   const int n = row / a.beams, b = row - n * a.beams;
   if (a.finished && a.finished[row]) return;  // its one candidate needs no logits
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int K = a.out_beams;
-  if (tid == 0) s_bound = order_key(-INFINITY);
-  __syncthreads();
   constexpr size_t kSize = F32 ? 4 : 2;
-  const char* base = static_cast<const char*>(a.logits) + (n * a.req_stride + b * a.beam_stride) * static_cast<int64_t>(kSize);
-  // whole 16-byte vectors from the first boundary; what is left at the ends goes element by element
-  const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(base) & 15u) / static_cast<int>(kSize);
-  const int head = min(a.vocab, mis ? E - mis : 0);
-  const int vecs = (a.vocab - head) / E;
-  const int tail = head + vecs * E;
-  const uint4* vp = reinterpret_cast<const uint4*>(base + head * kSize);
-  const int pieces = a.splits * kWarps, piece = split * kWarps + warp;
-  const int v_lo = static_cast<int>(static_cast<int64_t>(vecs) * piece / pieces);
-  const int v_hi = static_cast<int>(static_cast<int64_t>(vecs) * (piece + 1) / pieces);
+  Piece p;
+  p.base = static_cast<const char*>(a.logits) + (n * a.req_stride + b * a.beam_stride) * static_cast<int64_t>(kSize);
+  const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(p.base) & 15u) / static_cast<int>(kSize);
+  p.vocab = a.vocab;
+  p.head = min(a.vocab, mis ? E - mis : 0);
+  const int vecs = (a.vocab - p.head) / E;
+  p.tail = p.head + vecs * E;
+  p.vec = reinterpret_cast<const uint4*>(p.base + p.head * kSize);
+  p.lo = static_cast<int>(static_cast<int64_t>(vecs) * split / a.splits);
+  p.hi = static_cast<int>(static_cast<int64_t>(vecs) * (split + 1) / a.splits);
+  p.first = split == 0, p.last = split == a.splits - 1;
+  if (tid == 0) s_count = 0;
 
+  // ---- one pass: maximum, sum of exponentials, slot maxima
   float m = -INFINITY;
   Sum s;  // of exp(x - m)
-  TopList top;
-
   auto raise_max = [&](float most) {  // returns what exponentials are taken relative to
     if (most > m) {
       s.scale(m == -INFINITY ? (s.hi == 0.0f ? 0.0f : 1.0f) : exp_below(m, most));  // a NaN stays one
@@ -194,84 +258,41 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     }
     return m == -INFINITY ? 0.0f : m;
   };
-  auto single = [&](int i, bool have) {  // one element per lane
-    float x[1] = {have ? V::one(base, i) : -INFINITY};
-    const float ref = raise_max(x[0]);
-    if (have) s.add(exp_below(x[0], ref));
-    top.offer(x, i, x[0], K, lane);
-  };
-
-  if (piece == 0 && head > 0) single(lane, lane < head);
-  bool first_batch = true;
-  for (int v0 = v_lo; v0 < v_hi; v0 += 32 * kVec) {
-    uint4 raw[kVec];
+  // at most 14 elements at the ends of a row, one a thread
+  int edge_at = -1;
+  if (p.first && tid < p.head) edge_at = tid;
+  else if (p.last && tid >= 32 && p.tail + tid - 32 < a.vocab) edge_at = p.tail + tid - 32;
+  float edge = -INFINITY;
+  if (edge_at >= 0) {
+    edge = V::one(p.base, edge_at);
+    s.add(exp_below(edge, raise_max(edge)));
+  }
+  const int batches = (p.hi - p.lo + kBatch - 1) / kBatch, per_slot = (batches + kSlots - 1) / kSlots;
+  float slot[kSlots];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const int v = v0 + j * 32 + lane;
-      if (v < v_hi) raw[j] = ld_stream(vp + v);
-    }
-    float mx[kVec], batch = -INFINITY;
+  for (int q = 0; q < kSlots; ++q) {
+    slot[q] = -INFINITY;
+    const int end = min((q + 1) * per_slot, batches);
+    for (int i = q * per_slot; i < end; ++i) {
+      const int v0 = p.lo + i * kBatch + tid;
+      uint4 raw[kVec];
+      float batch = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      mx[j] = -INFINITY;
-      if (v0 + j * 32 + lane < v_hi) {
+      for (int j = 0; j < kVec; ++j)
+        if (v0 + j * kScanThreads < p.hi) raw[j] = ld_stream(p.vec + v0 + j * kScanThreads);
 #pragma unroll
-        for (int i = 0; i < E; ++i) mx[j] = fmaxf(mx[j], V::at(raw[j], i));
-      }
-      batch = fmaxf(batch, mx[j]);
-    }
-    const float ref = raise_max(batch);
+      for (int j = 0; j < kVec; ++j)
+        if (v0 + j * kScanThreads < p.hi) batch = fmaxf(batch, max_of<F32>(raw[j]));
+      const float ref = raise_max(batch);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      if (v0 + j * 32 + lane < v_hi) {
-        float part[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) part[i] = exp_below(V::at(raw[j], i), ref);
-#pragma unroll
-        for (int w = E / 2; w > 0; w /= 2)
-#pragma unroll
-          for (int i = 0; i < w; ++i) part[i] += part[i + w];
-        s.add(part[0]);
-      }
-    }
-    if (first_batch) {
-      first_batch = false;
-      // the K-th largest of the lanes' maxima: at least K elements are at or above it
-      uint32_t key = order_key(batch);
-#pragma unroll
-      for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-        for (int d = size / 2; d > 0; d /= 2) {
-          const uint32_t other = __shfl_xor_sync(0xffffffffu, key, d);
-          const bool descend = (lane & size) == 0, low = (lane & d) == 0;
-          key = (descend == low) ? max(key, other) : min(key, other);
-        }
-      const uint32_t kth = __shfl_sync(0xffffffffu, key, K - 1);
-      top.raise_floor(from_key(kth), K);
-      if (lane == 0) atomicMax(&s_bound, kth);
-    }
-    top.raise_floor(from_key(__shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&s_bound), 0)), K);
-    if (__any_sync(0xffffffffu, top.enters(batch))) {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        float x[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = V::at(raw[j], i);
-        const bool have = v0 + j * 32 + lane < v_hi;
-        top.offer(x, head + (v0 + j * 32 + lane) * E, have ? mx[j] : -INFINITY, K, lane);
-      }
-      if (lane == 0 && top.strict) atomicMax(&s_bound, order_key(top.bound));
+      for (int j = 0; j < kVec; ++j)
+        if (v0 + j * kScanThreads < p.hi) s.add(exp_sum<F32>(raw[j], ref));
+      slot[q] = fmaxf(slot[q], batch);
     }
   }
-  if (piece == pieces - 1 && tail < a.vocab) single(tail + lane, tail + lane < a.vocab);
+  grid_dependents_launch();
 
-  // ---- the block's maximum and sum, and its K best of the warps' lists by rank
-  auto join = [&](float most, float om, Sum o) {  // this sum and another, both relative to `most`
-    const float ref = most == -INFINITY ? 0.0f : most;
-    o.scale(om == -INFINITY ? 1.0f : exp_below(om, ref));
-    s.add(o.hi);
-    s.lo += o.lo;
-  };
+  // ---- the block's maximum and sum; the bound
   float most = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -283,30 +304,85 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     s.lo += lo;
   }
   if (lane == 0) s_max[warp] = most, s_sum[warp] = s;
-  if (lane < K) {
-    s_val[warp * K + lane] = top.idx >= 0 ? top.val : -INFINITY;
-    s_idx[warp * K + lane] = top.idx;
+  {
+    uint32_t key = order_key(m);  // sorted over the warp, largest first (bitonic)
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+      for (int d = size / 2; d > 0; d /= 2) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, key, d);
+        const bool descend = (lane & size) == 0, low = (lane & d) == 0;
+        key = (descend == low) ? max(key, other) : min(key, other);
+      }
+    if (lane < K) s_val[warp * K + lane] = from_key(key);
   }
   __syncthreads();
   const int64_t at = static_cast<int64_t>(row) * a.splits + split;
-  if (tid == 0) {
+  if (tid < kWarps * K) {  // the K-th largest of the threads' maxima
+    const float v = s_val[tid];
+    int rank = 0;
+    for (int i = 0; i < kWarps * K; ++i) rank += s_val[i] > v || (s_val[i] == v && i < tid);
+    if (rank == K - 1) s_bound = v;
+  }
+  if (tid == kScanThreads - 1) {
     for (int i = 0; i < kWarps; ++i) most = fmaxf(most, s_max[i]);
     s = Sum{};
-    for (int i = 0; i < kWarps; ++i) join(most, s_max[i], s_sum[i]);
+    for (int i = 0; i < kWarps; ++i) {
+      Sum o = s_sum[i];
+      if (s_max[i] != -INFINITY) o.scale(exp_below(s_max[i], most));
+      s.add(o.hi);
+      s.lo += o.lo;
+    }
     a.part_max[at] = most;
     a.part_sum[at] = s;
   }
-  const int count = kWarps * K;  // at most one candidate per thread
-  if (tid < count) {
-    const float v = s_val[tid];
-    const int32_t id = s_idx[tid];
-    int rank = 0;
+  __syncthreads();
+
+  // ---- candidates: what is at or above the bound, -inf excepted
+  const float bound = s_bound;
+  auto push = [&](float v, int32_t i) {
+    if (v >= bound && v > -INFINITY) {
+      const int c = atomicAdd(&s_count, 1);
+      if (c < kRoom) s_val[c] = v, s_idx[c] = i;
+    }
+  };
+  if (edge_at >= 0) push(edge, edge_at);
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    if (slot[q] >= bound && slot[q] > -INFINITY) {
+      const int end = min((q + 1) * per_slot, batches);
+      for (int i = q * per_slot; i < end; ++i)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const int v = p.lo + i * kBatch + j * kScanThreads + tid;
+          if (v >= p.hi) continue;
+          const uint4 raw = p.vec[v];
+          if (max_of<F32>(raw) < bound) continue;
+#pragma unroll
+          for (int x = 0; x < E; ++x) push(V::at(raw, x), p.head + v * E + x);
+        }
+    }
+  }
+  __syncthreads();
+  int count = s_count;
+  if (count > kRoom) {  // many equal elements
+    __syncthreads();
+    piece_lists<F32>(p, K, s_val, s_idx);
+    count = kWarps * K;
+    __syncthreads();
+  }
+  for (int c = tid; c < max(count, K); c += kScanThreads) {
+    if (c >= count) {  // fewer candidates than beams
+      a.part_idx[at * K + c] = -1;
+      continue;
+    }
+    const float v = s_val[c];
+    const int32_t id = s_idx[c];
+    int rank = 0;  // places without an element (from lists that did not fill) come last
     for (int i = 0; i < count; ++i) {
       const float o = s_val[i];
       const int32_t oi = s_idx[i];
-      // lists lie in index order and are sorted, so position breaks ties; the empty ones come last
-      rank += oi >= 0 && (id < 0 || o > v || (o == v && i < tid));
-      rank += oi < 0 && id < 0 && i < tid;
+      rank += id < 0 ? (oi >= 0 || i < c) : (oi >= 0 && (o > v || (o == v && oi < id)));
     }
     if (rank < K) {
       a.part_val[at * K + rank] = v;
@@ -315,104 +391,115 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
   }
 }
 
+// Candidates are compared by the order-preserving integer of their score in 64 bits (the FP64 units are
+// few: comparing doubles cost 30 us a call). 0 = none.
 struct Best {
-  double score;
-  int64_t at;  // w V + t; -1: none
+  uint64_t key;
+  int32_t at;  // w V + t
 };
 __device__ __forceinline__ bool better(const Best& x, const Best& y) {
-  if (x.at < 0) return false;
-  return y.at < 0 || x.score > y.score || (x.score == y.score && x.at < y.at);
+  return x.key > y.key || (x.key == y.key && x.at < y.at);
+}
+__device__ __forceinline__ Best best_of_warp(Best b) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Best y{__shfl_xor_sync(0xffffffffu, b.key, o), __shfl_xor_sync(0xffffffffu, b.at, o)};
+    if (better(y, b)) b = y;
+  }
+  return b;
 }
 
 // One block per request: every thread holds up to kPer candidates; K rounds of a block-wide maximum.
-__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
-  constexpr int kPer = kMaxCandidates / kMergeThreads;
+template <int kThreads, int kPer>
+__global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
   __shared__ double s_lse[kMaxBeams];
-  __shared__ Best s_best[kMergeThreads / 32];
+  __shared__ Best s_best[2][kThreads / 32];
   grid_dependency_wait();
   const int n = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = a.beams, K = a.out_beams, S = a.splits;
-  for (int w = warp; w < W; w += kMergeThreads / 32) {
+  for (int w = warp; w < W; w += kThreads / 32) {
     const int row = n * W + w;
-    double sum = 0.0;
+    if (a.finished && a.finished[row]) continue;
+    const float* mx = a.part_max + static_cast<int64_t>(row) * S;
+    const Sum* ps = a.part_sum + static_cast<int64_t>(row) * S;
     float m = -INFINITY;
-    const bool ended = a.finished && a.finished[row];
-    if (!ended) {
-      const float* mx = a.part_max + static_cast<int64_t>(row) * S;
-      const Sum* ps = a.part_sum + static_cast<int64_t>(row) * S;
-      for (int i = lane; i < S; i += 32) m = fmaxf(m, mx[i]);
+    for (int i = lane; i < S; i += 32) m = fmaxf(m, mx[i]);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      for (int i = lane; i < S; i += 32) {
-        const double x = static_cast<double>(ps[i].hi) + ps[i].lo;
-        sum += mx[i] == -INFINITY ? x : x * exp(static_cast<double>(mx[i]) - m);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    Sum sum;
+    for (int i = lane; i < S; i += 32) {
+      Sum x = ps[i];
+      if (mx[i] != -INFINITY) x.scale(exp_below(mx[i], m));
+      sum.add(x.hi);
+      sum.lo += x.lo;
     }
-    if (lane == 0) s_lse[w] = ended ? 0.0 : m + log(sum);  // no live logit: -inf + log 0; NaN: NaN
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float hi = __shfl_down_sync(0xffffffffu, sum.hi, o), lo = __shfl_down_sync(0xffffffffu, sum.lo, o);
+      sum.add(hi);
+      sum.lo += lo;
+    }
+    // no live logit: -inf + log 0; NaN: NaN
+    if (lane == 0) s_lse[w] = m + log(static_cast<double>(sum.hi) + sum.lo);
   }
   __syncthreads();
   Best mine[kPer];
   const int total = W * S * K;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    mine[j] = Best{0.0, -1};
-    const int i = j * kMergeThreads + tid;
+    mine[j] = Best{0, 0};
+    const int i = j * kThreads + tid;
     if (i < total) {
       const int w = i / (S * K), rest = i - w * S * K, row = n * W + w;
-      const float score = a.scores[row];
+      double score = -INFINITY;
       if (a.finished && a.finished[row]) {
-        if (rest == 0) mine[j] = Best{static_cast<double>(score), static_cast<int64_t>(w) * a.vocab + a.eos};
+        if (rest == 0) score = a.scores[row], mine[j].at = w * a.vocab + a.eos;
       } else {
         const int32_t t = a.part_idx[static_cast<int64_t>(row) * S * K + rest];
-        if (t >= 0)
-          mine[j] = Best{static_cast<double>(score) + (static_cast<double>(a.part_val[static_cast<int64_t>(row) * S * K + rest]) - s_lse[w]),
-                         static_cast<int64_t>(w) * a.vocab + t};
+        if (t >= 0) {
+          score = static_cast<double>(a.scores[row]) +
+                  (static_cast<double>(a.part_val[static_cast<int64_t>(row) * S * K + rest]) - s_lse[w]);
+          mine[j].at = w * a.vocab + t;
+        }
       }
-      if (!(mine[j].score > -INFINITY)) mine[j].at = -1;  // -inf and NaN are no candidates
+      if (score > -INFINITY) {  // -inf and NaN are no candidates
+        const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(score + 0.0));  // -0 becomes 0
+        mine[j].key = bits ^ ((bits >> 63) ? ~0ull : (1ull << 63));
+      }
     }
   }
   for (int k = 0; k < K; ++k) {
-    Best b{0.0, -1};
+    Best b{0, 0};
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
       if (better(mine[j], b)) b = mine[j];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Best y{__shfl_xor_sync(0xffffffffu, b.score, o), __shfl_xor_sync(0xffffffffu, b.at, o)};
-      if (better(y, b)) b = y;
-    }
-    if (lane == 0) s_best[warp] = b;
-    __syncthreads();
-    b = s_best[lane < kMergeThreads / 32 ? lane : 0];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Best y{__shfl_xor_sync(0xffffffffu, b.score, o), __shfl_xor_sync(0xffffffffu, b.at, o)};
-      if (better(y, b)) b = y;
-    }
-    __syncthreads();
+    b = best_of_warp(b);
+    if (lane == 0) s_best[k & 1][warp] = b;
+    __syncthreads();  // the other buffer is read before the next round's barrier
+    b = best_of_warp(s_best[k & 1][lane < kThreads / 32 ? lane : 0]);
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (mine[j].at == b.at) mine[j].at = -1;
+      if (mine[j].at == b.at) mine[j].key = 0;
     if (tid == 0) {
       const int64_t o = static_cast<int64_t>(n) * K + k;
-      const int w = b.at < 0 ? 0 : static_cast<int>(b.at / a.vocab);
-      const int t = b.at < 0 ? -1 : static_cast<int>(b.at - static_cast<int64_t>(w) * a.vocab);
-      a.out_scores[o] = b.at < 0 ? -INFINITY : static_cast<float>(b.score);
+      const bool none = b.key == 0;
+      const int w = b.at / a.vocab, t = none ? -1 : b.at - w * a.vocab;
+      const uint64_t bits = b.key ^ ((b.key >> 63) ? (1ull << 63) : ~0ull);
+      a.out_scores[o] = none ? -INFINITY : static_cast<float>(__longlong_as_double(static_cast<long long>(bits)));
       a.out_tokens[o] = t;
-      a.out_parents[o] = b.at < 0 ? -1 : n * W + w;
-      a.out_finished[o] = b.at >= 0 && (t == a.eos || (a.finished && a.finished[n * W + w]));
+      a.out_parents[o] = none ? -1 : n * W + w;
+      a.out_finished[o] = !none && (t == a.eos || (a.finished && a.finished[n * W + w]));
     }
   }
 }
 
-// Blocks per row: enough for every SM to hold a few, no piece below two batches a warp, and no more
-// candidates than the merge holds.
+// Blocks per row: enough for every SM to hold a few, no piece below half a batch, at most kSlots batches
+// where that fits, and no more candidates than the merge holds.
 int splits_for(int reqs, int beams, int out_beams, int vocab, int elem, int sms) {
   const int64_t rows = static_cast<int64_t>(reqs) * beams;
-  const int64_t want = (static_cast<int64_t>(sms) * 4 + rows - 1) / rows;
-  const int64_t fine = vocab / (kScanThreads * kVec * (16 / elem) * 2);
+  const int64_t batch = kScanThreads * kVec * (16 / elem);
+  const int64_t want = std::max((static_cast<int64_t>(sms) * 4 + rows - 1) / rows, (vocab + batch * kSlots - 1) / (batch * kSlots));
+  const int64_t fine = (2 * static_cast<int64_t>(vocab) + batch - 1) / batch;
   const int64_t most = kMaxCandidates / (beams * out_beams);
   return static_cast<int>(std::max<int64_t>(1, std::min(want, std::min(fine, most))));
 }
@@ -424,8 +511,8 @@ int check(int reqs, int beams, int out_beams, int vocab, int dtype) {
     return errorf(DFLASH_ERR_INVALID_ARG, "beams, beams_out and vocab must be positive, num_reqs >= 0");
   if (beams > kMaxBeams || out_beams > kMaxBeams)
     return errorf(DFLASH_ERR_UNSUPPORTED, "at most %d beams in and out (%d, %d)", kMaxBeams, beams, out_beams);
-  if (static_cast<int64_t>(reqs) * beams > 0x3fffff || vocab > 0x40000000)
-    return errorf(DFLASH_ERR_UNSUPPORTED, "more than 2^22 - 1 beams or 2^30 tokens");
+  if (static_cast<int64_t>(reqs) * beams > 0x3fffff || vocab >= kMaxVocab)
+    return errorf(DFLASH_ERR_UNSUPPORTED, "more than 2^22 - 1 beams or 2^26 - 1 tokens");
   return DFLASH_OK;
 }
 
@@ -492,14 +579,16 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "beam scan launch: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(num_reqs));
-  cfg.blockDim = dim3(kMergeThreads);
+  const bool few = beams * a.splits * beams_out <= 512;
+  cfg.blockDim = dim3(few ? 128 : kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, beam_merge_kernel, a);
+  e = few ? cudaLaunchKernelEx(&cfg, beam_merge_kernel<128, 4>, a)
+          : cudaLaunchKernelEx(&cfg, beam_merge_kernel<kMergeThreads, kMaxCandidates / kMergeThreads>, a);
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "beam merge launch: %s", cudaGetErrorString(e));
   return report_error(DFLASH_OK, "");
 }

@@ -13,10 +13,11 @@
 // - The worker is a WARP, not a block: it owns a contiguous range of 16-row steps of the batch laid
 //   end to end (sequence, then kv head, then steps), keeps its own (m, l, O), and never synchronises
 //   with another warp. Ranges are equal to within a step, whatever the raggedness.
-// - Each lane copies with cp.async exactly the 16-byte pieces that it will itself use as matrix
-//   fragments, into shared memory that only it reads. The order of a contraction's terms is free, so
-//   fragments are 8 consecutive elements instead of the instruction's 2 + 2: no transposition, no
-//   bank conflicts, no barrier, and kStages steps in flight a warp (24 KB at Dh = 128).
+// - A warp copies its rows with cp.async into shared memory of its own, whole rows by neighbouring
+//   lanes (pieces chosen by who will use them fetched every sector twice: 4.0 TB/s), 16-byte pieces
+//   permuted within a row so that the fragment reads are free of bank conflicts. The order of a
+//   contraction's terms is free, so a lane's fragment is 8 consecutive elements of a row instead of the
+//   instruction's 2 + 2: 16-byte reads, and V needs no transposition beyond pairing rows in registers.
 // - The group's heads are the 16 rows of mma.m16n8k16 (K and V rows are its columns). At <= 8 heads the
 //   spare rows 8..15 carry the rounding remainder of P, so P has 16 significant bits at no cost; f32
 //   outputs add a third term (24 bits). The idle rows cost nothing that matters: tensor work is a few
@@ -35,11 +36,19 @@
 namespace dflash {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;       // rows per step
 constexpr int kMinSteps = 4;    // steps per worker before another worker is used
-constexpr int kScan = kThreads; // chunks of the prefix over sequences
+constexpr float kSlack = 8.0f;  // the running maximum may lag by 2^8
+
+// Warps of a block and steps that a warp has in flight: what registers and 224 KB of shared memory allow.
+template <int DH, int GT>
+struct Shape {
+  static constexpr int kWarps = GT == 8 ? 12 : 8;
+  static constexpr int kStageBytes = kStep * DH * 4;  // K and V
+  static constexpr int kStages = (GT == 8 ? 2 : 3) * (128 / DH);
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kBytes = kWarps * kStages * kStageBytes;
+};
 
 struct Plan {  // what the join kernel needs of the schedule
   int64_t total;
@@ -92,7 +101,7 @@ __device__ __forceinline__ int steps_of(const DecodeArgs& a, int len) {
   return (len - first_row(a, len) + kStep - 1) / kStep;
 }
 
-// Worker w takes the steps [start(w), start(w + 1)). total < 2^50 and workers < 2^12: no overflow.
+// Worker w takes the steps [start(w), start(w + 1)). total <= 10^12 and workers < 2^12: no overflow.
 __device__ __forceinline__ int64_t worker_start(int64_t w, int64_t total, int64_t workers) {
   return w * total / workers;
 }
@@ -100,8 +109,8 @@ __device__ __forceinline__ int64_t worker_of(int64_t x, int64_t total, int64_t w
   return ((x + 1) * workers - 1) / total;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int size) {  // size 0: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -115,39 +124,42 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// A worker's place: step `step` of `steps` of group (r, hh).
+// A worker's place: step `step` of `steps` of group (r, hh); first = the sequence's first row.
 struct Cursor {
-  int r, hh, len, steps, step;
+  int r, hh, len, first, steps, step;
 };
 
-// The next group with steps after c's; true unless the batch is at its end (which a worker's range
-// never passes).
+__device__ __forceinline__ void set_len(const DecodeArgs& a, Cursor& c, int len) {
+  c.len = len;
+  c.first = first_row(a, len);
+  c.steps = (len - c.first + kStep - 1) / kStep;
+}
+
+// The next group with steps after c's; c.steps = 0 at the end of the batch (which a worker's range never
+// passes).
 __device__ __forceinline__ void next_group(const DecodeArgs& a, Cursor& c, int heads) {
   c.step = 0;
   if (++c.hh < heads) return;
   c.hh = 0;
   c.steps = 0;
-  while (c.steps == 0 && ++c.r < a.num_reqs) {
-    c.len = valid_len(a, a.lens[c.r]);
-    c.steps = steps_of(a, c.len);
-  }
+  while (c.steps == 0 && ++c.r < a.num_reqs) set_len(a, c, valid_len(a, a.lens[c.r]));
 }
 
 template <int DH, int GT, bool F32>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
-  constexpr int KC = DH / 32;          // 16-byte pieces of a K row per lane
-  constexpr int VH = DH / 64;          // 64-column parts of a V row
-  constexpr int kPieces = 2 * KC + 4 * VH;
-  constexpr int kStages = DH == 128 ? 3 : 6;
-  constexpr int R = GT / 8;            // head rows per lane
-  constexpr int kStageBytes = kPieces * 512;
+__global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
+  using S = Shape<DH, GT>;
+  constexpr int KC = DH / 32;  // 16-byte pieces of a K row per lane
+  constexpr int VH = DH / 64;  // 64-column parts of a V row
+  constexpr int R = GT / 8;    // head rows per lane
+  constexpr int kWarps = S::kWarps, kStages = S::kStages, kStageBytes = S::kStageBytes;
+  constexpr int kScan = S::kThreads;  // chunks of the prefix over sequences
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int64_t s_prefix[kScan + 1];
   __shared__ int64_t s_warp[kWarps];
@@ -203,7 +215,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       }
       int64_t base = s_prefix[b];
       c.r = b * per;
-      c.len = c.steps = 0;
       for (int i = 0; i < per; i += 32) {
         const int r = b * per + i + lane;
         const int len = i + lane < per && r < a.num_reqs ? valid_len(a, a.lens[r]) : 0;
@@ -218,8 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         if (hit) {
           const int src = __ffs(hit) - 1;
           c.r = b * per + i + src;
-          c.len = __shfl_sync(0xffffffffu, len, src);
-          c.steps = __shfl_sync(0xffffffffu, n, src);
+          set_len(a, c, __shfl_sync(0xffffffffu, len, src));
           base += __shfl_sync(0xffffffffu, x, src) - c.steps;
           break;
         }
@@ -229,51 +239,52 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       c.hh = static_cast<int>(rest / c.steps);
       c.step = static_cast<int>(rest - static_cast<int64_t>(c.hh) * c.steps);
     }
+    const int n_steps = static_cast<int>(hi - lo);  // below 2^31: at most 10^12 over 8 warps an SM, or kMinSteps each
     if (lane == 0) a.rec[w] = WorkerRecord{lo - c.step, c.steps, c.r, c.hh};
 
-    const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes) + lane * 16;
-    const int64_t row_elems = static_cast<int64_t>(a.hkv) * DH;
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
+    const int64_t row_bytes = static_cast<int64_t>(a.hkv) * DH * 2;
 
     // ---- loads. Lane l & 15 looks up row l & 15 of a step, one step ahead of the step's copies.
     Cursor ld = c;
-    int64_t ahead = lo;      // step whose rows are looked up next
-    int64_t row_off = -1;    // its pool row (elements); -1: no row
-    int row_hh = 0;
+    int ahead = 0;     // steps looked up
+    int row = -1;      // this lane's row of the pools; -1: none
+    int head_off = 0;  // bytes to the kv head
     auto look_up = [&]() {
-      if (ahead < hi) {
-        const int j = first_row(a, ld.len) + ld.step * kStep + (lane & 15);
-        row_off = -1;
-        row_hh = ld.hh;
+      if (ahead < n_steps) {
+        const int j = ld.first + ld.step * kStep + (lane & 15);
+        row = -1;
+        head_off = (a.tiles == 1 ? ld.hh : ld.hh / a.tiles) * (DH * 2);
         if (j < ld.len) {
           const int p = page_of(a, j);
-          int64_t id = a.table[static_cast<int64_t>(ld.r) * a.table_stride + p];
+          int id = a.table[static_cast<int64_t>(ld.r) * a.table_stride + p];
           if (id < 0 || id >= a.num_pages) {
             if (a.err) atomicOr(a.err, kErrMetadata);
             id = 0;
           }
-          row_off = (id * a.page + (j - p * a.page)) * row_elems;
+          row = id * a.page + (j - p * a.page);
         }
         if (++ld.step == ld.steps) next_group(a, ld, heads);
       }
       ++ahead;
     };
-    auto copy_step = [&](int64_t s, int stage) {  // the step looked up last
-      if (s < hi) {
+    // one instruction copies kRows whole rows; 16-byte piece x of row y lies at piece x ^ f(y) of the row,
+    // f(y) = (y & 1) * 4 for K and (y / 2 & 3) * 2 for V
+    constexpr int kRowBytes = DH * 2, kRowPieces = DH / 8, kRows = 32 / kRowPieces;
+    const int my_row = lane / kRowPieces, my_piece = lane % kRowPieces;
+    const char* k_lane = reinterpret_cast<const char*>(a.k) + my_piece * 16;
+    const char* v_lane = reinterpret_cast<const char*>(a.v) + my_piece * 16;
+    auto copy_step = [&](int i, int stage) {  // the step looked up last
+      if (i < n_steps) {
         const uint32_t dst = ring + stage * kStageBytes;
-        const int64_t head = static_cast<int64_t>(row_hh / a.tiles) * DH;
 #pragma unroll
-        for (int jt = 0; jt < 2; ++jt) {
-          const int64_t off = __shfl_sync(0xffffffffu, row_off, jt * 8 + g);
-          const uint16_t* src = a.k + (off < 0 ? 0 : off + head + t * 8);
-#pragma unroll
-          for (int i = 0; i < KC; ++i) cp_async16(dst + (jt * KC + i) * 512, off < 0 ? a.k : src + i * 32, off >= 0);
-        }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const int64_t off = __shfl_sync(0xffffffffu, row_off, (kk >> 1) * 8 + 2 * t + (kk & 1));
-          const uint16_t* src = a.v + (off < 0 ? 0 : off + head + g * 8);
-#pragma unroll
-          for (int i = 0; i < VH; ++i) cp_async16(dst + (2 * KC + kk * VH + i) * 512, off < 0 ? a.v : src + i * 64, off >= 0);
+        for (int y = 0; y < kStep / kRows; ++y) {
+          const int at = y * kRows + my_row;
+          const int x = __shfl_sync(0xffffffffu, row, at);
+          const int64_t off = max(x, 0) * row_bytes + head_off;
+          const int size = x < 0 ? 0 : 16;
+          cp_async16(dst + at * kRowBytes + (my_piece ^ ((at & 1) * 4)) * 16, k_lane + off, size);
+          cp_async16(dst + (kStep + at) * kRowBytes + (my_piece ^ ((at >> 1 & 3) * 2)) * 16, v_lane + off, size);
         }
       }
       cp_async_commit();
@@ -281,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     look_up();
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
-      copy_step(lo + i, i);
+      copy_step(i, i);
       look_up();
     }
 
@@ -313,27 +324,40 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     reset();
     bool from_start = c.step == 0;  // this worker holds the group's first step
     int stage = 0;
-    for (int64_t s = lo; s < hi; ++s) {
+    for (int s = 0; s < n_steps; ++s) {
       cp_async_wait<kStages - 1>();
+      __syncwarp();
       const uint32_t src = ring + stage * kStageBytes;
+      uint4 kf[2][KC];
+#pragma unroll
+      for (int jt = 0; jt < 2; ++jt)
+#pragma unroll
+        for (int i = 0; i < KC; ++i) kf[jt][i] = lds128(src + (jt * 8 + g) * kRowBytes + ((i * 4 + t) ^ ((g & 1) * 4)) * 16);
       float sc[2][4];
 #pragma unroll
       for (int jt = 0; jt < 2; ++jt) {
-        sc[jt][0] = sc[jt][1] = sc[jt][2] = sc[jt][3] = 0.0f;
+        // f32 outputs: a chain of sums per 32 columns, so that no sum rounds at the size of all of them
+        float part[F32 ? KC : 1][4];
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
-          const uint4 kf = lds128(src + (jt * KC + i) * 512);
-          if constexpr (R == 1) {
-            mma_bf16(sc[jt], qf[0][i].x, 0u, qf[0][i].y, 0u, kf.x, kf.y);
-            mma_bf16(sc[jt], qf[0][i].z, 0u, qf[0][i].w, 0u, kf.z, kf.w);
-          } else {
-            mma_bf16(sc[jt], qf[0][i].x, qf[R - 1][i].x, qf[0][i].y, qf[R - 1][i].y, kf.x, kf.y);
-            mma_bf16(sc[jt], qf[0][i].z, qf[R - 1][i].z, qf[0][i].w, qf[R - 1][i].w, kf.z, kf.w);
+          float(&d)[4] = part[F32 ? i : 0];
+          if (F32 || i == 0) d[0] = d[1] = d[2] = d[3] = 0.0f;
+          mma_bf16(d, qf[0][i].x, R == 1 ? 0u : qf[R - 1][i].x, qf[0][i].y, R == 1 ? 0u : qf[R - 1][i].y, kf[jt][i].x,
+                   kf[jt][i].y);
+          mma_bf16(d, qf[0][i].z, R == 1 ? 0u : qf[R - 1][i].z, qf[0][i].w, R == 1 ? 0u : qf[R - 1][i].w, kf[jt][i].z,
+                   kf[jt][i].w);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          sc[jt][x] = part[0][x];
+          if constexpr (F32) {
+#pragma unroll
+            for (int i = 1; i < KC; ++i) sc[jt][x] += part[i][x];
           }
         }
       }
       // rows past the length weigh nothing
-      const int left = c.len - (first_row(a, c.len) + c.step * kStep);
+      const int left = c.len - (c.first + c.step * kStep);
       if (left < kStep) {
 #pragma unroll
         for (int jt = 0; jt < 2; ++jt)
@@ -348,14 +372,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         mx[i] = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1])) * a.scale_log2;
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        grow |= mx[i] > m[i];
+        grow |= mx[i] > m[i] + kSlack;  // m = -inf at first
       }
       if (__any_sync(0xffffffffu, grow)) {
         float al[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const float n = fmaxf(m[i], mx[i]);
-          al[i] = m[i] == -INFINITY ? 0.0f : exp2f(m[i] - n);
+          al[i] = m[i] == -INFINITY ? 0.0f : ex2_approx(m[i] - n);
           m[i] = n;
           l[i] *= al[i];
         }
@@ -390,7 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       for (int i = 0; i < VH; ++i) {
         uint4 vf[4];
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) vf[kk] = lds128(src + (2 * KC + kk * VH + i) * 512);
+        for (int kk = 0; kk < 4; ++kk)  // rows 2t, 2t + 1, 8 + 2t, 9 + 2t: f = 2t
+          vf[kk] = lds128(src + (kStep + (kk >> 1) * 8 + 2 * t + (kk & 1)) * kRowBytes + ((i * 8 + g) ^ (2 * t)) * 16);
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           const uint32_t sel = (x & 1) ? 0x7632u : 0x5410u;
@@ -406,12 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           }
         }
       }
-      // every piece of this stage has been used: refill it
+      __syncwarp();  // every lane has read this stage: refill it
       copy_step(s + kStages, stage);
       look_up();
       if (++stage == kStages) stage = 0;
 
-      if (c.step + 1 == c.steps || s + 1 == hi) {  // the group, or this worker's part of it, is done
+      if (c.step + 1 == c.steps || s + 1 == n_steps) {  // the group, or this worker's part of it, is done
         const bool to_end = c.step + 1 == c.steps;
         const int kvh = c.hh / a.tiles, h0 = (c.hh - kvh * a.tiles) * GT;
 #pragma unroll
@@ -455,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             }
           }
         }
-        if (s + 1 < hi) {
+        if (s + 1 < n_steps) {
           next_group(a, c, heads);
           from_start = true;
           load_q();
@@ -555,6 +580,10 @@ struct Layout {
 };
 
 int head_tile(int g) { return g <= 8 ? 8 : 16; }
+int warps_of(int dh, int gt) {
+  return dh == 128 ? (gt == 8 ? Shape<128, 8>::kWarps : Shape<128, 16>::kWarps)
+                   : (gt == 8 ? Shape<64, 8>::kWarps : Shape<64, 16>::kWarps);
+}
 
 Layout layout_of(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int window, int sms) {
   Layout y{};
@@ -564,7 +593,7 @@ Layout layout_of(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int win
   const int64_t rows = window > 0 ? std::min(max_ctx_len, window) : max_ctx_len;
   const int64_t steps = (rows + kStep - 1) / kStep;
   y.bound = static_cast<double>(steps) * hkv * y.tiles * num_reqs;
-  const int64_t most = static_cast<int64_t>(sms) * kWarps;
+  const int64_t most = static_cast<int64_t>(sms) * warps_of(dh, y.gt);
   const double need = std::ceil(y.bound / kMinSteps);
   y.workers = need < static_cast<double>(most) ? std::max<int64_t>(1, static_cast<int64_t>(need)) : most;
   y.grid = static_cast<int>(std::min<int64_t>(sms, y.workers));
@@ -591,11 +620,10 @@ int check(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int window) {
 
 template <int DH, int GT, bool F32>
 cudaError_t launch(const DecodeArgs& a, const Layout& y, cudaStream_t st) {
-  constexpr int kPieces = 2 * (DH / 32) + 4 * (DH / 64);
-  constexpr int kBytes = kWarps * (DH == 128 ? 3 : 6) * kPieces * 512;
+  constexpr int kBytes = Shape<DH, GT>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<DH, GT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  decode_kernel<DH, GT, F32><<<y.grid, kThreads, kBytes, st>>>(a);
+  decode_kernel<DH, GT, F32><<<y.grid, Shape<DH, GT>::kThreads, kBytes, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !y.split) return e;
   cudaLaunchConfig_t cfg{};
@@ -658,7 +686,7 @@ int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const 
   rc = query_sms(&sms);
   if (rc != DFLASH_OK) return rc;
   const Layout y = layout_of(num_reqs, hq, hkv, dh, max_ctx_len, window, sms);
-  if (y.bound > 1e15) return errorf(DFLASH_ERR_UNSUPPORTED, "too many rows for one call (%.3g steps)", y.bound);
+  if (y.bound > 1e12) return errorf(DFLASH_ERR_UNSUPPORTED, "too many rows for one call (%.3g steps)", y.bound);
   if (workspace_bytes < y.total)
     return errorf(DFLASH_ERR_WORKSPACE, "workspace has %zu bytes; %zu are needed", workspace_bytes, y.total);
   char* ws = static_cast<char*>(workspace);
