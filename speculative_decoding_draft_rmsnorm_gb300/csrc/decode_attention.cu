@@ -22,8 +22,10 @@
 //   spare rows 8..15 carry the rounding remainder of P, so P has 16 significant bits at no cost; f32
 //   outputs add a third term (24 bits). The idle rows cost nothing that matters: tensor work is a few
 //   per cent of the step's time, set by the loads.
-// - A worker stores a group that it holds whole; else it leaves (m, l, O) in one of its two slots, and
-//   the join kernel merges the slots in a fixed order: the result does not depend on timing.
+// - A worker stores a group that it holds whole; else it leaves (m, l, O) in one of its two slots. The
+//   warps of a block hold consecutive ranges, so the block joins what its warps share, and the join
+//   kernel what blocks share: at most two parts a block. All merges go in a fixed order: the result does
+//   not depend on timing. (Joining a lone 32000-row sequence from 1824 warps' parts took 20 us more.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -52,10 +54,10 @@ struct Shape {
 
 struct Plan {  // what the join kernel needs of the schedule
   int64_t total;
-  int64_t workers;
+  int32_t workers, per_block;
 };
 
-struct WorkerRecord {  // the first group of a worker
+struct Record {  // the first group of a block
   int64_t group_start;  // its first step, counted over the whole batch
   int64_t group_steps;
   int32_t r, hh;
@@ -73,9 +75,12 @@ struct DecodeArgs {
   float* lse;
   uint32_t* err;
   Plan* plan;
-  WorkerRecord* rec;
+  Record* rec;
+  // slot 2w: the part of a group that began before worker w; 2w + 1: of one that it began and did not end
   float* part_o;   // [2 * workers][GT][DH]
   float* part_ml;  // [2 * workers][GT][2]
+  float* block_o;  // the same of blocks
+  float* block_ml;
   int num_reqs, hq, hkv, g, tiles;  // tiles = query-head tiles of a kv head
   int64_t num_pages;
   int page, max_pages, window;
@@ -152,6 +157,69 @@ __device__ __forceinline__ void next_group(const DecodeArgs& a, Cursor& c, int h
   while (c.steps == 0 && ++c.r < a.num_reqs) set_len(a, c, valid_len(a, a.lens[c.r]));
 }
 
+// What a worker left in its slots.
+struct Segments {
+  bool continues = false;  // slot 2w: a part of a group that began before
+  bool ends = false;       // ... with its last step
+  bool opens = false;      // slot 2w + 1
+  int r_first = 0, hh_first = 0, r_last = 0, hh_last = 0;
+};
+
+// One head's row of `n` parts, by a warp: DH / 32 columns a lane. Part p is row slot(p) of part_o and
+// part_ml. The result is relative to the maximum m over the parts.
+template <int DH, typename Slot>
+__device__ __forceinline__ void merge_parts(const float* part_o, const float* part_ml, int n, int from, int step, Slot slot,
+                                            float (&o)[DH / 32], float& m, float& l) {
+  const int lane = threadIdx.x & 31;
+  m = -INFINITY;
+  for (int p = lane; p < n; p += 32) m = fmaxf(m, part_ml[slot(p) * 2]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  l = 0.0f;
+#pragma unroll
+  for (int x = 0; x < DH / 32; ++x) o[x] = 0.0f;
+#pragma unroll 4
+  for (int p = from; p < n; p += step) {
+    const int64_t at = slot(p);
+    const float2 ml = *reinterpret_cast<const float2*>(part_ml + at * 2);
+    const float e = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - m);
+    l += ml.y * e;
+    if constexpr (DH == 128) {
+      const float4 v = *reinterpret_cast<const float4*>(part_o + at * DH + lane * 4);
+      o[0] += v.x * e, o[1] += v.y * e, o[2] += v.z * e, o[3] += v.w * e;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(part_o + at * DH + lane * 2);
+      o[0] += v.x * e, o[1] += v.y * e;
+    }
+  }
+}
+
+template <int DH>
+__device__ __forceinline__ void store_row(float* dst, const float (&o)[DH / 32], float f) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (DH == 128)
+    *reinterpret_cast<float4*>(dst + lane * 4) = make_float4(o[0] * f, o[1] * f, o[2] * f, o[3] * f);
+  else
+    *reinterpret_cast<float2*>(dst + lane * 2) = make_float2(o[0] * f, o[1] * f);
+}
+
+// A finished head: its output row and log-sum.
+template <int DH>
+__device__ __forceinline__ void store_head(const DecodeArgs& a, int64_t o_row, const float (&o)[DH / 32], float m, float l) {
+  const int lane = threadIdx.x & 31;
+  const float inv = 1.0f / l;
+  if (a.out_f32) {
+    store_row<DH>(static_cast<float*>(a.out) + o_row * DH, o, inv);
+  } else {
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + o_row * DH;
+    if constexpr (DH == 128)
+      *reinterpret_cast<uint2*>(dst + lane * 4) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst + lane * 2) = pack_bf16x2(o[0] * inv, o[1] * inv);
+  }
+  if (a.lse && lane == 0) a.lse[o_row] = (m + log2f(l)) * 0.693147180559945309f;
+}
+
 template <int DH, int GT, bool F32>
 __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
   using S = Shape<DH, GT>;
@@ -163,9 +231,12 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int64_t s_prefix[kScan + 1];
   __shared__ int64_t s_warp[kWarps];
+  __shared__ Segments s_seg[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int heads = a.hkv * a.tiles;
+
+  grid_dependents_launch();  // the join's launch overlaps; it waits for this grid's end
 
   // ---- the schedule: a prefix over the sequences' steps, one chunk of sequences per thread
   const int per = (a.num_reqs + kScan - 1) / kScan;
@@ -197,13 +268,14 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
   const int64_t total = s_prefix[kScan] * heads;
   int64_t workers = (total + kMinSteps - 1) / kMinSteps;
   if (workers > a.max_workers) workers = a.max_workers;
-  const int64_t w = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // neighbours on different SMs
-  if (w == 0 && lane == 0) {
-    a.plan->total = total;
-    a.plan->workers = workers;
-  }
+  // few workers are spread over the SMs; a block's are consecutive
+  const int per_block = static_cast<int>((workers + gridDim.x - 1) / gridDim.x);
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * per_block + warp;
+  if (blockIdx.x == 0 && tid == 0) *a.plan = Plan{total, static_cast<int32_t>(workers), per_block};
+  const bool works = warp < per_block && w < workers;
+  if (lane == 0) s_seg[warp] = Segments{};
 
-  if (w < workers) {
+  if (works) {
     const int64_t lo = worker_start(w, total, workers), hi = worker_start(w + 1, total, workers);
     // ---- the group that holds step lo: its chunk by bisection, then its sequence by a warp scan
     Cursor c;
@@ -240,7 +312,7 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
       c.step = static_cast<int>(rest - static_cast<int64_t>(c.hh) * c.steps);
     }
     const int n_steps = static_cast<int>(hi - lo);  // below 2^31: at most 10^12 over 8 warps an SM, or kMinSteps each
-    if (lane == 0) a.rec[w] = WorkerRecord{lo - c.step, c.steps, c.r, c.hh};
+    if (warp == 0 && lane == 0) a.rec[blockIdx.x] = Record{lo - c.step, c.steps, c.r, c.hh};
 
     const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
     const int64_t row_bytes = static_cast<int64_t>(a.hkv) * DH * 2;
@@ -323,6 +395,8 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
     load_q();
     reset();
     bool from_start = c.step == 0;  // this worker holds the group's first step
+    Segments seg;
+    seg.r_first = c.r, seg.hh_first = c.hh;
     int stage = 0;
     for (int s = 0; s < n_steps; ++s) {
       cp_async_wait<kStages - 1>();
@@ -438,6 +512,8 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
 
       if (c.step + 1 == c.steps || s + 1 == n_steps) {  // the group, or this worker's part of it, is done
         const bool to_end = c.step + 1 == c.steps;
+        if (!from_start) seg.continues = true, seg.ends = to_end;
+        else if (!to_end) seg.opens = true, seg.r_last = c.r, seg.hh_last = c.hh;
         const int kvh = c.hh / a.tiles, h0 = (c.hh - kvh * a.tiles) * GT;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -491,11 +567,44 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
       }
     }
     cp_async_wait<0>();
+    if (lane == 0) s_seg[warp] = seg;
   }
-  grid_dependents_launch();
+  __syncthreads();  // and the slots that the warps wrote to global memory
+
+  // ---- join what the block's warps share, a (run of parts, head) per warp and turn. Run 0 is the group
+  // that began in an earlier block, run i + 1 the one that warp i began and did not end.
+  const int active = static_cast<int>(min(static_cast<int64_t>(per_block), max(workers - static_cast<int64_t>(blockIdx.x) * per_block, static_cast<int64_t>(0))));
+  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * per_block;
+  for (int item = warp; item < (active + 1) * GT; item += kWarps) {
+    const int run = item / GT, h = item - run * GT;
+    const bool inherited = run == 0;
+    if (inherited ? !s_seg[0].continues : !s_seg[run - 1].opens) continue;
+    const int r = inherited ? s_seg[0].r_first : s_seg[run - 1].r_last;
+    const int hh = inherited ? s_seg[0].hh_first : s_seg[run - 1].hh_last;
+    const int kvh = hh / a.tiles, h0 = (hh - kvh * a.tiles) * GT;
+    if (h0 + h >= a.g) continue;
+    int n = 1;  // warps from the run's first that hold a part; it ends with the group or with the block
+    int last = inherited ? 0 : run - 1;
+    bool ended = inherited && s_seg[0].ends;
+    while (!ended && last + 1 < active) {
+      ++last, ++n;
+      ended = s_seg[last].ends;
+    }
+    const int64_t first = w0 + (inherited ? 0 : run - 1);
+    float o[DH / 32], m, l;
+    merge_parts<DH>(a.part_o, a.part_ml, n, 0, 1,
+                    [&](int p) { return (2 * (first + p) + (p == 0 && !inherited ? 1 : 0)) * GT + h; }, o, m, l);
+    if (!inherited && ended) {
+      store_head<DH>(a, static_cast<int64_t>(r) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + h, o, m, l);
+    } else {
+      const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + (inherited ? 0 : 1)) * GT + h;
+      store_row<DH>(a.block_o + at * DH, o, 1.0f);
+      if (lane == 0) a.block_ml[at * 2] = m, a.block_ml[at * 2 + 1] = l;
+    }
+  }
 
   // ---- sequences without rows: zeros, and the log-sum of nothing
-  for (int64_t r = w; r < a.num_reqs; r += static_cast<int64_t>(gridDim.x) * kWarps) {
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + warp; r < a.num_reqs; r += static_cast<int64_t>(gridDim.x) * kWarps) {
     if (valid_len(a, a.lens[r]) != 0) continue;
     const int64_t n = static_cast<int64_t>(a.hq) * DH;
     for (int64_t i = lane; i < n; i += 32) {
@@ -507,68 +616,43 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
   }
 }
 
-// Joins the parts of every group that workers share: block b looks at the boundary between workers b
-// and b + 1, and the first boundary inside a group has it. A thread owns 4 columns of one head and
-// one of `lanes` interleaved shares of the parts; shares are joined in shared memory in order.
-constexpr int kJoinThreads = 512;
+// Joins the parts of every group that blocks share: join block b looks at the boundary between attention
+// blocks b and b + 1, and the first boundary inside a group has it. A warp takes one head and one of
+// `shares` interleaved shares of the parts; shares are joined in shared memory in order.
+constexpr int kJoinWarps = 16;
 template <int DH, int GT>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ DecodeArgs a) {
+  __shared__ float s_o[kJoinWarps][DH];
+  __shared__ float s_l[kJoinWarps];
   grid_dependency_wait();
-  const int64_t total = a.plan->total, workers = a.plan->workers;
+  const Plan plan = *a.plan;
   const int64_t b = blockIdx.x;
-  if (b + 1 >= workers) return;
-  const WorkerRecord rec = a.rec[b + 1];
-  const int64_t lo = worker_start(b + 1, total, workers);
-  if (rec.group_start == lo) return;                                // no group crosses this boundary
-  if (worker_of(rec.group_start, total, workers) != b) return;      // an earlier boundary has it
-  const int64_t last = worker_of(rec.group_start + rec.group_steps - 1, total, workers);
-  const int64_t parts = last - b + 1;
+  if ((b + 1) * plan.per_block >= plan.workers) return;
+  const Record rec = a.rec[b + 1];
+  if (rec.group_start == worker_start((b + 1) * plan.per_block, plan.total, plan.workers)) return;  // nothing crosses
+  if (worker_of(rec.group_start, plan.total, plan.workers) / plan.per_block != b) return;  // an earlier boundary has it
+  const int64_t last = worker_of(rec.group_start + rec.group_steps - 1, plan.total, plan.workers) / plan.per_block;
+  const int parts = static_cast<int>(last - b + 1);
   const int kvh = rec.hh / a.tiles, h0 = (rec.hh - kvh * a.tiles) * GT;
-  const int n_heads = min(GT, a.g - h0);
-  constexpr int kCols = DH / 4;
-  const int cols = n_heads * kCols;
-  __shared__ float s_o[kJoinThreads][4];
-  __shared__ float s_ml[kJoinThreads][2];
-  const int shares = kJoinThreads / cols > 0 ? kJoinThreads / cols : 1;
-  const int share = threadIdx.x / cols, col = threadIdx.x - share * cols;
+  const int heads = min(GT, a.g - h0), shares = kJoinWarps / heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = warp % heads, share = warp / heads;
+  float o[DH / 32], m = -INFINITY, l = 0.0f;
   if (share < shares) {
-    const int h = col / kCols, d = (col - h * kCols) * 4;
-    float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int64_t p = share; p < parts; p += shares) {
-      const int64_t slot = p == 0 ? 2 * b + 1 : 2 * (b + p);
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot * GT + h) * 2);
-      const float4 x = *reinterpret_cast<const float4*>(a.part_o + (slot * GT + h) * DH + d);
-      const float n = fmaxf(m, ml.x);
-      const float f = m == -INFINITY ? 0.0f : exp2f(m - n), e = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - n);
-      o = make_float4(o.x * f + x.x * e, o.y * f + x.y * e, o.z * f + x.z * e, o.w * f + x.w * e);
-      l = l * f + ml.y * e;
-      m = n;
-    }
-    s_o[threadIdx.x][0] = o.x, s_o[threadIdx.x][1] = o.y, s_o[threadIdx.x][2] = o.z, s_o[threadIdx.x][3] = o.w;
-    s_ml[threadIdx.x][0] = m, s_ml[threadIdx.x][1] = l;
+    merge_parts<DH>(a.block_o, a.block_ml, parts, share, shares, [&](int p) { return (2 * (b + p) + (p == 0 ? 1 : 0)) * GT + h; }, o,
+                    m, l);
+#pragma unroll
+    for (int x = 0; x < DH / 32; ++x) s_o[warp][lane * (DH / 32) + x] = o[x];
+    if (lane == 0) s_l[warp] = l;
   }
   __syncthreads();
-  if (threadIdx.x >= cols) return;
-  float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i = 0; i < shares; ++i) m = fmaxf(m, s_ml[i * cols + threadIdx.x][0]);
-  for (int i = 0; i < shares; ++i) {
-    const int at = i * cols + threadIdx.x;
-    const float e = s_ml[at][0] == -INFINITY ? 0.0f : exp2f(s_ml[at][0] - m);
-    l += s_ml[at][1] * e;
+  if (share != 0) return;
+  for (int i = 1; i < shares; ++i) {  // all relative to the same maximum
+    l += s_l[i * heads + h];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) o[y] += s_o[at][y] * e;
+    for (int x = 0; x < DH / 32; ++x) o[x] += s_o[i * heads + h][lane * (DH / 32) + x];
   }
-  const int h = threadIdx.x / kCols, d = (threadIdx.x - h * kCols) * 4;
-  const int64_t o_row = static_cast<int64_t>(rec.r) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + h;
-  const float inv = 1.0f / l;
-  if (a.out_f32)
-    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o_row * DH + d) =
-        make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-  else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o_row * DH + d) =
-        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-  if (a.lse && d == 0) a.lse[o_row] = (m + log2f(l)) * 0.693147180559945309f;
+  store_head<DH>(a, static_cast<int64_t>(rec.r) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + h, o, m, l);
 }
 
 struct Layout {
@@ -576,7 +660,7 @@ struct Layout {
   int64_t workers;
   double bound;  // most steps of a call
   bool split;
-  size_t plan, rec, ml, o, total;
+  size_t plan, rec, ml, o, block_ml, block_o, total;
 };
 
 int head_tile(int g) { return g <= 8 ? 8 : 16; }
@@ -597,13 +681,16 @@ Layout layout_of(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int win
   const double need = std::ceil(y.bound / kMinSteps);
   y.workers = need < static_cast<double>(most) ? std::max<int64_t>(1, static_cast<int64_t>(need)) : most;
   y.grid = static_cast<int>(std::min<int64_t>(sms, y.workers));
-  y.split = steps > 1 && y.workers > 1;
+  y.split = steps > 1 && y.grid > 1;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   y.plan = 0;
   y.rec = 256;
-  y.ml = y.rec + up(static_cast<size_t>(y.workers) * sizeof(WorkerRecord));
-  y.o = y.ml + up(static_cast<size_t>(y.workers) * 2 * y.gt * 2 * sizeof(float));
-  y.total = y.o + up(static_cast<size_t>(y.workers) * 2 * y.gt * dh * sizeof(float));
+  const size_t row = static_cast<size_t>(2) * y.gt * sizeof(float);
+  y.ml = y.rec + up(static_cast<size_t>(y.grid) * sizeof(Record));
+  y.o = y.ml + up(y.workers * row * 2);
+  y.block_ml = y.o + up(y.workers * row * dh);
+  y.block_o = y.block_ml + up(y.grid * row * 2);
+  y.total = y.block_o + up(y.grid * row * dh);
   return y;
 }
 
@@ -627,8 +714,8 @@ cudaError_t launch(const DecodeArgs& a, const Layout& y, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess || !y.split) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(y.workers - 1));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(y.grid - 1));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -695,7 +782,9 @@ int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const 
   a.table = block_table, a.table_stride = block_table_stride, a.lens = seq_lens;
   a.out = out, a.lse = lse, a.err = reinterpret_cast<uint32_t*>(status);
   a.plan = reinterpret_cast<Plan*>(ws + y.plan);
-  a.rec = reinterpret_cast<WorkerRecord*>(ws + y.rec);
+  a.rec = reinterpret_cast<Record*>(ws + y.rec);
+  a.block_ml = reinterpret_cast<float*>(ws + y.block_ml);
+  a.block_o = reinterpret_cast<float*>(ws + y.block_o);
   a.part_ml = reinterpret_cast<float*>(ws + y.ml);
   a.part_o = reinterpret_cast<float*>(ws + y.o);
   a.num_reqs = num_reqs, a.hq = hq, a.hkv = hkv, a.g = hq / hkv, a.tiles = y.tiles;
