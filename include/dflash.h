@@ -404,8 +404,9 @@ DFLASH_API size_t dflash_decode_workspace_size(int num_reqs, int hq, int hkv, in
  *   status     int32 device word or NULL: DFLASH_STATUS_METADATA is ORed in for a bad length or a
  *              table entry outside [0, num_pages) (page 0 is read in its place)
  *   Dh in {64, 128}; Hq % Hkv == 0, any group size. bf16 products are exact, sums f32; the weights
- *   keep 16 bits for a bf16 output and 24 for an f32 one. Two launches (attention, join); one when
- *   no sequence can be split. Results do not depend on timing.
+ *   keep 16 bits for a bf16 output and 24 for an f32 one. Two launches (attention, join), or one
+ *   where max_ctx_len (or the window) is at most 512 and there are no more (sequence, kv head)
+ *   pairs than SMs. Results do not depend on timing.
  */
 DFLASH_API int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const dflash_bf16* k_pool,
                                              const dflash_bf16* v_pool, const int32_t* block_table,

@@ -39,28 +39,27 @@ namespace dflash {
 namespace {
 
 constexpr int kStep = 16;       // rows per step
-constexpr int kMinSteps = 4;    // steps per worker before another worker is used
+// A group of up to so many steps has a block to itself where there are SMs enough: no prefix over the
+// sequences, no join. 256 rows of one sequence: 7.5 us against 8.5 cut; 700 rows: 10.8 against 9.4.
+constexpr int kLoneSteps = 32;
 constexpr float kSlack = 8.0f;  // the running maximum may lag by 2^8
 
-// Warps of a block and steps that a warp has in flight: what registers and 224 KB of shared memory allow.
+// Warps of a block and steps that a warp has in flight. 128 KB in flight an SM are several times what the
+// latency needs, and more is slower: a ragged batch of 64 sequences took 381 us with 8 warps of 2 steps,
+// 400 with 8 of 3, 418 with 6 of 3, 426 with 12 of 2 and 456 with 7 of 4.
 template <int DH, int GT>
 struct Shape {
-  static constexpr int kWarps = GT == 8 ? 12 : 8;
+  static constexpr int kWarps = 8;
   static constexpr int kStageBytes = kStep * DH * 4;  // K and V
-  static constexpr int kStages = (GT == 8 ? 2 : 3) * (128 / DH);
+  static constexpr int kStages = 2;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kBytes = kWarps * kStages * kStageBytes;
 };
 
-struct Plan {  // what the join kernel needs of the schedule
-  int64_t total;
-  int32_t workers, per_block;
-};
-
-struct Record {  // the first group of a block
-  int64_t group_start;  // its first step, counted over the whole batch
-  int64_t group_steps;
-  int32_t r, hh;
+// The group that the boundary before a block cuts: blocks first .. last hold its parts. first = -1 where
+// nothing is cut, or an earlier boundary cuts the same group.
+struct Record {
+  int32_t r, hh, first, last;
 };
 
 struct DecodeArgs {
@@ -74,14 +73,17 @@ struct DecodeArgs {
   void* out;
   float* lse;
   uint32_t* err;
-  Plan* plan;
-  Record* rec;
-  // slot 2w: the part of a group that began before worker w; 2w + 1: of one that it began and did not end
-  float* part_o;   // [2 * workers][GT][DH]
-  float* part_ml;  // [2 * workers][GT][2]
-  float* block_o;  // the same of blocks
-  float* block_ml;
-  int num_reqs, hq, hkv, g, tiles;  // tiles = query-head tiles of a kv head
+  Record* rec;  // [blocks]
+  // the part of a group that began before worker w, where w goes on to others
+  float* part_o;   // [workers][GT][DH]
+  float* part_ml;  // [workers][GT][2]
+  // slot 2b: the part of a group that began before block b; 2b + 1: of one that it began and did not end
+  float* block_o;   // [2 * blocks][GT][DH]
+  float* block_ml;  // [2 * blocks][GT][2]
+  int num_reqs, hq, hkv, g;
+  int unit;        // warps that read the same rows, each for a head tile of its own
+  int tile_units;  // units that a kv head's tiles make
+  int lone;        // block b has group b to itself
   int64_t num_pages;
   int page, max_pages, window;
   int64_t max_len;  // longest valid length
@@ -106,21 +108,47 @@ __device__ __forceinline__ int steps_of(const DecodeArgs& a, int len) {
   return (len - first_row(a, len) + kStep - 1) / kStep;
 }
 
-// Worker w takes the steps [start(w), start(w + 1)). total <= 10^12 and workers < 2^12: no overflow.
-__device__ __forceinline__ int64_t worker_start(int64_t w, int64_t total, int64_t workers) {
-  return w * total / workers;
-}
-__device__ __forceinline__ int64_t worker_of(int64_t x, int64_t total, int64_t workers) {
-  return ((x + 1) * workers - 1) / total;
+// 64-bit division, kept out of line: inlined it made a third of the kernel's code, all of it fetched cold.
+__device__ __noinline__ int64_t divide(int64_t x, int64_t y) {
+  return x < (1ll << 32) && y < (1ll << 32) ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int size) {  // size 0: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+// The workers' ranges: equal to within one step. total <= 10^12.
+struct Ranges {
+  int64_t total, each;
+  int workers, extra;  // the first `extra` workers take each + 1 steps
+
+  Ranges() = default;
+  __device__ __forceinline__ Ranges(int64_t total_, int64_t max_workers) : total(total_) {
+    workers = static_cast<int>(min(total, max_workers));
+    each = workers ? divide(total, workers) : 0;
+    extra = static_cast<int>(total - each * workers);
+  }
+  __device__ __forceinline__ int64_t start(int w) const { return w * each + min(w, extra); }
+  __device__ __forceinline__ int owner(int64_t x) const {  // of step x
+    const int64_t cut = extra * (each + 1);
+    return static_cast<int>(x < cut ? divide(x, each + 1) : extra + divide(x - cut, each));
+  }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int size, uint64_t policy) {  // size 0: zeros
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(size), "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Four 8 x 8 blocks of b16, transposed: lane l gives the address of row l % 8 of block l / 8 and gets, of
+// every block, the elements (2 (l % 4), l / 4) and (2 (l % 4) + 1, l / 4).
+__device__ __forceinline__ uint4 ldmatrix_t(uint32_t addr) {
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -134,7 +162,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // A worker's place: step `step` of `steps` of group (r, hh); first = the sequence's first row.
 struct Cursor {
@@ -154,43 +181,76 @@ __device__ __forceinline__ void next_group(const DecodeArgs& a, Cursor& c, int h
   if (++c.hh < heads) return;
   c.hh = 0;
   c.steps = 0;
+#pragma unroll 1
   while (c.steps == 0 && ++c.r < a.num_reqs) set_len(a, c, valid_len(a, a.lens[c.r]));
 }
 
-// What a worker left in its slots.
+// What a warp left to be joined: at its range's end in shared memory, or (mid) a group's end that it
+// passed before, in global memory.
 struct Segments {
-  bool continues = false;  // slot 2w: a part of a group that began before
-  bool ends = false;       // ... with its last step
-  bool opens = false;      // slot 2w + 1
-  int r_first = 0, hh_first = 0, r_last = 0, hh_last = 0;
+  bool continues;  // its first group began before
+  bool ends;       // ... and ended here
+  bool mid;        // ... before the range did
+  bool opens;      // its last group began here and goes on
+  int r_first, hh_first, r_last, hh_last;
 };
 
-// One head's row of `n` parts, by a warp: DH / 32 columns a lane. Part p is row slot(p) of part_o and
-// part_ml. The result is relative to the maximum m over the parts.
-template <int DH, typename Slot>
-__device__ __forceinline__ void merge_parts(const float* part_o, const float* part_ml, int n, int from, int step, Slot slot,
-                                            float (&o)[DH / 32], float& m, float& l) {
+// Group hh covers the head tiles of one unit: tile `tile` of it holds the group's heads from h0 on.
+template <int GT>
+__device__ __forceinline__ void head_tile_of(const DecodeArgs& a, int hh, int tile, int& kvh, int& h0) {
+  kvh = a.tile_units == 1 ? hh : hh / a.tile_units;
+  h0 = ((hh - kvh * a.tile_units) * a.unit + tile) * GT;
+}
+
+struct Part {
+  const float* o;   // a head's DH sums
+  const float* ml;  // its maximum and weight
+};
+
+// Joins parts from, from + step, .. below n of one head, by a warp: DH / 32 columns a lane.
+template <int DH, typename At>
+__device__ __forceinline__ void merge_parts(int n, int from, int step, At at, float (&o)[DH / 32], float& m, float& l) {
+  constexpr int C = DH / 32, U = 4;
   const int lane = threadIdx.x & 31;
-  m = -INFINITY;
-  for (int p = lane; p < n; p += 32) m = fmaxf(m, part_ml[slot(p) * 2]);
+  m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  l = 0.0f;
+  for (int x = 0; x < C; ++x) o[x] = 0.0f;
+#pragma unroll 1
+  for (int p0 = from; p0 < n; p0 += step * U) {
+    float2 ml[U];
+    float v[U][C];
 #pragma unroll
-  for (int x = 0; x < DH / 32; ++x) o[x] = 0.0f;
-#pragma unroll 4
-  for (int p = from; p < n; p += step) {
-    const int64_t at = slot(p);
-    const float2 ml = *reinterpret_cast<const float2*>(part_ml + at * 2);
-    const float e = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - m);
-    l += ml.y * e;
-    if constexpr (DH == 128) {
-      const float4 v = *reinterpret_cast<const float4*>(part_o + at * DH + lane * 4);
-      o[0] += v.x * e, o[1] += v.y * e, o[2] += v.z * e, o[3] += v.w * e;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(part_o + at * DH + lane * 2);
-      o[0] += v.x * e, o[1] += v.y * e;
+    for (int u = 0; u < U; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int x = 0; x < C; ++x) v[u][x] = 0.0f;
+      if (p0 + u * step < n) {
+        const Part part = at(p0 + u * step);
+        ml[u] = *reinterpret_cast<const float2*>(part.ml);
+        if constexpr (C == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(part.o + lane * 4);
+          v[u][0] = f.x, v[u][1] = f.y, v[u][2] = f.z, v[u][3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(part.o + lane * 2);
+          v[u][0] = f.x, v[u][1] = f.y;
+        }
+      }
     }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+    const float f = m == -INFINITY ? 0.0f : ex2_approx(m - top);
+    l *= f;
+#pragma unroll
+    for (int x = 0; x < C; ++x) o[x] *= f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float e = ml[u].x == -INFINITY ? 0.0f : ex2_approx(ml[u].x - top);
+      l += ml[u].y * e;
+#pragma unroll
+      for (int x = 0; x < C; ++x) o[x] += v[u][x] * e;
+    }
+    m = top;
   }
 }
 
@@ -217,304 +277,336 @@ __device__ __forceinline__ void store_head(const DecodeArgs& a, int64_t o_row, c
     else
       *reinterpret_cast<uint32_t*>(dst + lane * 2) = pack_bf16x2(o[0] * inv, o[1] * inv);
   }
-  if (a.lse && lane == 0) a.lse[o_row] = (m + log2f(l)) * 0.693147180559945309f;
+  if (a.lse && lane == 0) a.lse[o_row] = (m + __log2f(l)) * 0.693147180559945309f;
 }
 
 template <int DH, int GT, bool F32>
 __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
   using S = Shape<DH, GT>;
   constexpr int KC = DH / 32;  // 16-byte pieces of a K row per lane
-  constexpr int VH = DH / 64;  // 64-column parts of a V row
   constexpr int R = GT / 8;    // head rows per lane
   constexpr int kWarps = S::kWarps, kStages = S::kStages, kStageBytes = S::kStageBytes;
   constexpr int kScan = S::kThreads;  // chunks of the prefix over sequences
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t s_prefix[kScan + 1];
+  extern __shared__ __align__(256) uint8_t smem[];
   __shared__ int64_t s_warp[kWarps];
   __shared__ Segments s_seg[kWarps];
+  struct Start {
+    int64_t before;  // steps of a kv head before the chunk of sequences
+    int r, len;      // its first sequence, and that one's length
+  };
+  __shared__ Start s_start[kWarps];
+  struct First {
+    int64_t start;  // of the block's first group, over the whole batch
+    int steps, r, hh;
+  };
+  __shared__ First s_first;
+  __shared__ Ranges s_ranges;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int heads = a.hkv * a.tiles;
-
+  const int heads = a.hkv * a.tile_units;
   grid_dependents_launch();  // the join's launch overlaps; it waits for this grid's end
 
-  // ---- the schedule: a prefix over the sequences' steps, one chunk of sequences per thread
-  const int per = (a.num_reqs + kScan - 1) / kScan;
-  {
-    int64_t mine = 0;
+  const int my_unit = warp / a.unit, tile_in_unit = warp - my_unit * a.unit;
+  if (lane == 0) s_seg[warp] = Segments{};
+  int w0 = 0, active, n_steps = 0;  // the block's first unit and how many have work; this one's steps
+  int units = 0;
+  int64_t block_lo = 0;
+  Cursor c;
+  if (a.lone) {
+    c.r = blockIdx.x / heads, c.hh = blockIdx.x - c.r * heads;
+    const int raw = a.lens[c.r], len = valid_len(a, raw);
+    if (raw != len && tid == 0 && a.err) atomicOr(a.err, kErrMetadata);
+    set_len(a, c, len);
+    active = min(kWarps / a.unit, c.steps);
+    c.step = 0;
+    if (my_unit < active) {
+      c.step = my_unit * c.steps / active;
+      n_steps = (my_unit + 1) * c.steps / active - c.step;
+    }
+    __syncthreads();
+  } else {
+    // ---- the schedule: a prefix over the sequences' steps, one chunk of sequences per thread; the thread
+    // whose chunk holds a unit's first step tells its warps
+    const int per = (a.num_reqs + kScan - 1) / kScan;
+    int64_t mine = 0, upto;
+    int my_len = 0;
     bool bad = false;
+#pragma unroll 1
     for (int i = 0; i < per; ++i) {
       const int r = tid * per + i;
       if (r < a.num_reqs) {
         const int raw = a.lens[r], len = valid_len(a, raw);
         bad |= len != raw;
+        if (i == 0) my_len = len;
         mine += steps_of(a, len);
       }
     }
     if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, kErrMetadata);
-    int64_t x = mine;
+    upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
     }
-    if (lane == 31) s_warp[warp] = x;
+    if (lane == 31) s_warp[warp] = upto;
     __syncthreads();
-    for (int i = 0; i < warp; ++i) x += s_warp[i];
-    s_prefix[tid + 1] = x;
-    if (tid == 0) s_prefix[0] = 0;
-    __syncthreads();
-  }
-  const int64_t total = s_prefix[kScan] * heads;
-  int64_t workers = (total + kMinSteps - 1) / kMinSteps;
-  if (workers > a.max_workers) workers = a.max_workers;
-  // few workers are spread over the SMs; a block's are consecutive
-  const int per_block = static_cast<int>((workers + gridDim.x - 1) / gridDim.x);
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * per_block + warp;
-  if (blockIdx.x == 0 && tid == 0) *a.plan = Plan{total, static_cast<int32_t>(workers), per_block};
-  const bool works = warp < per_block && w < workers;
-  if (lane == 0) s_seg[warp] = Segments{};
-
-  if (works) {
-    const int64_t lo = worker_start(w, total, workers), hi = worker_start(w + 1, total, workers);
-    // ---- the group that holds step lo: its chunk by bisection, then its sequence by a warp scan
-    Cursor c;
-    {
-      int b = 0, e = kScan;  // prefix[b] * heads <= lo < prefix[e] * heads
-      while (e - b > 1) {
-        const int mid = (b + e) >> 1;
-        if (s_prefix[mid] * heads <= lo) b = mid; else e = mid;
-      }
-      int64_t base = s_prefix[b];
-      c.r = b * per;
-      for (int i = 0; i < per; i += 32) {
-        const int r = b * per + i + lane;
-        const int len = i + lane < per && r < a.num_reqs ? valid_len(a, a.lens[r]) : 0;
-        const int n = steps_of(a, len);
-        int64_t x = n;
+    int64_t total = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) upto += s_warp[i];
+      total += s_warp[i];
+    }
+    const Ranges ranges(total * heads, a.max_workers);
+    // few workers are spread over the SMs; a block's are consecutive
+    units = (ranges.workers + gridDim.x - 1) / gridDim.x;  // of a block, at most
+    w0 = blockIdx.x * units;
+    active = max(0, min(units, ranges.workers - w0));
+#pragma unroll 1
+    for (int i = 0; i < active; ++i) {
+      const int64_t lo = ranges.start(w0 + i);
+      if (lo >= (upto - mine) * heads && lo < upto * heads) s_start[i] = Start{upto - mine, tid * per, my_len};
+    }
+    block_lo = ranges.start(w0);
+    if (tid == 0) s_ranges = ranges;
+    __syncthreads();
+    if (my_unit < active) {
+      // ---- the group that holds step lo
+      const int64_t lo = ranges.start(w0 + my_unit);
+      n_steps = static_cast<int>(ranges.start(w0 + my_unit + 1) - lo);  // at most 10^12 over 8 warps an SM
+      const Start at = s_start[my_unit];
+      int64_t base = at.before;
+      c.r = at.r;
+      set_len(a, c, at.len);
+      if (per > 1) {  // the sequence within the chunk, by warp scans
+#pragma unroll 1
+        for (int i = 0; i < per; i += 32) {
+          const int r = at.r + i + lane;
+          const int len = i + lane < per && r < a.num_reqs ? valid_len(a, a.lens[r]) : 0;
+          const int n = steps_of(a, len);
+          int64_t x = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          const uint32_t hit = __ballot_sync(0xffffffffu, (base + x) * heads > lo);
+          if (hit) {
+            const int src = __ffs(hit) - 1;
+            c.r = at.r + i + src;
+            set_len(a, c, __shfl_sync(0xffffffffu, len, src));
+            base += __shfl_sync(0xffffffffu, x, src) - c.steps;
+            break;
+          }
+          base += __shfl_sync(0xffffffffu, x, 31);
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, (base + x) * heads > lo);
-        if (hit) {
-          const int src = __ffs(hit) - 1;
-          c.r = b * per + i + src;
-          set_len(a, c, __shfl_sync(0xffffffffu, len, src));
-          base += __shfl_sync(0xffffffffu, x, src) - c.steps;
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, x, 31);
       }
       const int64_t rest = lo - base * heads;
-      c.hh = static_cast<int>(rest / c.steps);
+      c.hh = static_cast<int>(divide(rest, c.steps));
       c.step = static_cast<int>(rest - static_cast<int64_t>(c.hh) * c.steps);
+      if (warp == 0 && lane == 0) s_first = First{lo - c.step, c.steps, c.r, c.hh};
     }
-    const int n_steps = static_cast<int>(hi - lo);  // below 2^31: at most 10^12 over 8 warps an SM, or kMinSteps each
-    if (warp == 0 && lane == 0) a.rec[blockIdx.x] = Record{lo - c.step, c.steps, c.r, c.hh};
+  }
 
+  if (my_unit < active) {
+    const int w = w0 + my_unit;
     const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
     const int64_t row_bytes = static_cast<int64_t>(a.hkv) * DH * 2;
 
-    // ---- loads. Lane l & 15 looks up row l & 15 of a step, one step ahead of the step's copies.
+    // ---- loads. Steps are looked up in pairs, a row per lane, at least two turns before they are copied.
     Cursor ld = c;
-    int ahead = 0;     // steps looked up
-    int row = -1;      // this lane's row of the pools; -1: none
-    int head_off = 0;  // bytes to the kv head
-    auto look_up = [&]() {
-      if (ahead < n_steps) {
-        const int j = ld.first + ld.step * kStep + (lane & 15);
-        row = -1;
-        head_off = (a.tiles == 1 ? ld.hh : ld.hh / a.tiles) * (DH * 2);
-        if (j < ld.len) {
-          const int p = page_of(a, j);
-          int id = a.table[static_cast<int64_t>(ld.r) * a.table_stride + p];
-          if (id < 0 || id >= a.num_pages) {
-            if (a.err) atomicOr(a.err, kErrMetadata);
-            id = 0;
-          }
-          row = id * a.page + (j - p * a.page);
-        }
-        if (++ld.step == ld.steps) next_group(a, ld, heads);
+    int row = -1, next_row = -1;      // this lane's row of the pools (lanes 0-15: the first step's); -1: none
+    int heads_at[2] = {0, 0}, next_at[2];  // bytes to the kv heads of the two steps
+    auto look_up = [&](int i) {  // steps i and i + 1
+      Cursor mine = ld;
+      bool have = i < n_steps;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        next_at[u] = (a.tile_units == 1 ? ld.hh : ld.hh / a.tile_units) * (DH * 2);
+        if (u == 1 && lane >= 16) mine = ld, have = i + 1 < n_steps;
+        if (i + u < n_steps && ++ld.step == ld.steps) next_group(a, ld, heads);
       }
-      ++ahead;
+      const int j = mine.first + mine.step * kStep + (lane & 15);
+      next_row = -1;
+      if (have && j < mine.len) {
+        const int p = page_of(a, j);
+        int id = a.table[static_cast<int64_t>(mine.r) * a.table_stride + p];
+        if (id < 0 || id >= a.num_pages) {
+          if (a.err) atomicOr(a.err, kErrMetadata);
+          id = 0;
+        }
+        next_row = id * a.page + (j - p * a.page);
+      }
     };
-    // one instruction copies kRows whole rows; 16-byte piece x of row y lies at piece x ^ f(y) of the row,
-    // f(y) = (y & 1) * 4 for K and (y / 2 & 3) * 2 for V
+    look_up(0);
+
+    // One instruction copies kRows whole rows. 16-byte piece x of row y lies at piece x ^ f(y) of the row:
+    // f(y) = (y & 1) * 4 for K, read 16 bytes a lane, and y & 7 for V, read as 8 x 8 blocks.
     constexpr int kRowBytes = DH * 2, kRowPieces = DH / 8, kRows = 32 / kRowPieces;
+    const uint64_t policy = l2_policy_evict_first();  // rows are read once: 1-2 us a call
     const int my_row = lane / kRowPieces, my_piece = lane % kRowPieces;
     const char* k_lane = reinterpret_cast<const char*>(a.k) + my_piece * 16;
     const char* v_lane = reinterpret_cast<const char*>(a.v) + my_piece * 16;
-    auto copy_step = [&](int i, int stage) {  // the step looked up last
-      if (i < n_steps) {
-        const uint32_t dst = ring + stage * kStageBytes;
+    const uint32_t k_read = ring + g * kRowBytes + (t ^ ((g & 1) * 4)) * 16;
+    const uint32_t v_read = ring + (kStep + (lane & 15)) * kRowBytes;
+    const int v_piece = (lane >> 4) ^ (lane & 7);
+
+    uint4 qf[R][KC];
+    float acc[DH / 8][4], m[R], l[R];  // column block x: columns 8x .. 8x + 7
+    constexpr int kBlocks = DH / 8;
+    bool fresh = true, from_start = c.step == 0;  // a group begins for this warp; it holds the group's first step
+    Segments seg{};
+    seg.r_first = c.r, seg.hh_first = c.hh;
+    // Every step is copied kStages turns before it is used, in one loop, so that its code is there once
+    // (the code of a first turn is fetched cold).
+#pragma unroll 1
+    for (int s = -kStages; s < n_steps; ++s) {
+      if (s >= 0) {
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        if (fresh) {
+          fresh = false;
+          int kvh, h0;
+          head_tile_of<GT>(a, c.hh, tile_in_unit, kvh, h0);
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const int h = h0 + g + 8 * i;
+            const uint16_t* src = a.q + c.r * a.q_tok + (static_cast<int64_t>(kvh) * a.g + h) * DH + t * 8;
+#pragma unroll
+            for (int x = 0; x < KC; ++x)
+              qf[i][x] = h < a.g ? *reinterpret_cast<const uint4*>(src + x * 32) : make_uint4(0, 0, 0, 0);
+            m[i] = -INFINITY, l[i] = 0.0f;
+          }
+#pragma unroll
+          for (int x = 0; x < kBlocks; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) acc[x][y] = 0.0f;
+        }
+        const uint32_t stage = (s & 1) * kStageBytes;
+        float sc[2][4];
+#pragma unroll
+        for (int jt = 0; jt < 2; ++jt) {
+          uint4 kf[KC];
+#pragma unroll
+          for (int i = 0; i < KC; ++i)  // piece (4 i + t) ^ ((g & 1) * 4)
+            kf[i] = lds128((k_read + stage + jt * 8 * kRowBytes) ^ (i * 64));
+          // f32 outputs: a chain of sums per 32 columns, so that no sum rounds at the size of all of them
+          float part[F32 ? KC : 1][4];
+#pragma unroll
+          for (int i = 0; i < KC; ++i) {
+            float(&d)[4] = part[F32 ? i : 0];
+            if (F32 || i == 0) d[0] = d[1] = d[2] = d[3] = 0.0f;
+            mma_bf16(d, qf[0][i].x, R == 1 ? 0u : qf[R - 1][i].x, qf[0][i].y, R == 1 ? 0u : qf[R - 1][i].y, kf[i].x, kf[i].y);
+            mma_bf16(d, qf[0][i].z, R == 1 ? 0u : qf[R - 1][i].z, qf[0][i].w, R == 1 ? 0u : qf[R - 1][i].w, kf[i].z, kf[i].w);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            sc[jt][x] = part[0][x];
+            if constexpr (F32) {
+#pragma unroll
+              for (int i = 1; i < KC; ++i) sc[jt][x] += part[i][x];
+            }
+          }
+        }
+        // rows past the length weigh nothing
+        const int left = c.len - (c.first + c.step * kStep);
+        if (left < kStep) {
+#pragma unroll
+          for (int jt = 0; jt < 2; ++jt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (jt * 8 + 2 * t + (x & 1) >= left) sc[jt][x] = -INFINITY;
+        }
+        float mx[R];
+        bool grow = false;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          mx[i] = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1])) * a.scale_log2;
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+          grow |= mx[i] > m[i] + kSlack;  // m = -inf at first
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+          float al[R];
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const float n = fmaxf(m[i], mx[i]);
+            al[i] = m[i] == -INFINITY ? 0.0f : ex2_approx(m[i] - n);
+            m[i] = n;
+            l[i] *= al[i];
+          }
+#pragma unroll
+          for (int x = 0; x < kBlocks; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) acc[x][y] *= al[R == 1 ? 0 : y >> 1];
+        }
+        // weights, as bf16 terms: hi (and, where rows are spare or the output is f32, remainders)
+        constexpr int kTerms = F32 ? 3 : 2;
+        uint32_t pw[R][kTerms][2];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const float ref = m[i] == -INFINITY ? 0.0f : m[i];
+#pragma unroll
+          for (int jt = 0; jt < 2; ++jt) {
+            float p0 = ex2_approx(fmaf(sc[jt][2 * i], a.scale_log2, -ref));
+            float p1 = ex2_approx(fmaf(sc[jt][2 * i + 1], a.scale_log2, -ref));
+            l[i] += p0 + p1;
+#pragma unroll
+            for (int x = 0; x < kTerms; ++x) {
+              const uint32_t h = pack_bf16x2(p0, p1);
+              pw[i][x][jt] = h;
+              p0 -= bf16lo_to_f32(h);
+              p1 -= bf16hi_to_f32(h);
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < kBlocks; x += 2) {  // two column blocks of all 16 rows
+          const uint4 v = ldmatrix_t(v_read + stage + (x ^ v_piece) * 16);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t b0 = y ? v.z : v.x, b1 = y ? v.w : v.y;
+            if constexpr (R == 1) {
+              mma_bf16(acc[x + y], pw[0][0][0], pw[0][1][0], pw[0][0][1], pw[0][1][1], b0, b1);
+              if constexpr (F32) mma_bf16(acc[x + y], pw[0][2][0], 0u, pw[0][2][1], 0u, b0, b1);
+            } else {
+#pragma unroll
+              for (int z = 0; z < kTerms; ++z)
+                mma_bf16(acc[x + y], pw[0][z][0], pw[R - 1][z][0], pw[0][z][1], pw[R - 1][z][1], b0, b1);
+            }
+          }
+        }
+        __syncwarp();  // every lane has read this stage
+      }
+      const int half = s & 1;  // kStages is even: the step copied has the parity of the one just used
+      if (half == 0) {
+        row = next_row, heads_at[0] = next_at[0], heads_at[1] = next_at[1];
+        look_up(s + kStages + 2);
+      }
+      if (s + kStages < n_steps) {
+        const uint32_t dst = ring + half * kStageBytes;
+        const int head = half ? heads_at[1] : heads_at[0];
 #pragma unroll
         for (int y = 0; y < kStep / kRows; ++y) {
           const int at = y * kRows + my_row;
-          const int x = __shfl_sync(0xffffffffu, row, at);
-          const int64_t off = max(x, 0) * row_bytes + head_off;
+          const int x = __shfl_sync(0xffffffffu, row, half * 16 + at);
+          const int64_t off = max(x, 0) * row_bytes + head;
           const int size = x < 0 ? 0 : 16;
-          cp_async16(dst + at * kRowBytes + (my_piece ^ ((at & 1) * 4)) * 16, k_lane + off, size);
-          cp_async16(dst + (kStep + at) * kRowBytes + (my_piece ^ ((at >> 1 & 3) * 2)) * 16, v_lane + off, size);
+          cp_async16(dst + at * kRowBytes + (my_piece ^ ((at & 1) * 4)) * 16, k_lane + off, size, policy);
+          cp_async16(dst + (kStep + at) * kRowBytes + (my_piece ^ (at & 7)) * 16, v_lane + off, size, policy);
         }
       }
       cp_async_commit();
-    };
-    look_up();
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) {
-      copy_step(i, i);
-      look_up();
-    }
-
-    // ---- compute
-    uint4 qf[R][KC];
-    auto load_q = [&]() {
-      const int kvh = c.hh / a.tiles, h0 = (c.hh - kvh * a.tiles) * GT;
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int h = h0 + g + 8 * i;
-        const uint16_t* src = a.q + c.r * a.q_tok + (static_cast<int64_t>(kvh) * a.g + h) * DH + t * 8;
-#pragma unroll
-        for (int x = 0; x < KC; ++x)
-          qf[i][x] = h < a.g ? *reinterpret_cast<const uint4*>(src + x * 32) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    float acc[VH][8][4], m[R], l[R];
-    auto reset = [&]() {
-#pragma unroll
-      for (int i = 0; i < VH; ++i)
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) acc[i][x][y] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < R; ++i) m[i] = -INFINITY, l[i] = 0.0f;
-    };
-    load_q();
-    reset();
-    bool from_start = c.step == 0;  // this worker holds the group's first step
-    Segments seg;
-    seg.r_first = c.r, seg.hh_first = c.hh;
-    int stage = 0;
-    for (int s = 0; s < n_steps; ++s) {
-      cp_async_wait<kStages - 1>();
-      __syncwarp();
-      const uint32_t src = ring + stage * kStageBytes;
-      uint4 kf[2][KC];
-#pragma unroll
-      for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-        for (int i = 0; i < KC; ++i) kf[jt][i] = lds128(src + (jt * 8 + g) * kRowBytes + ((i * 4 + t) ^ ((g & 1) * 4)) * 16);
-      float sc[2][4];
-#pragma unroll
-      for (int jt = 0; jt < 2; ++jt) {
-        // f32 outputs: a chain of sums per 32 columns, so that no sum rounds at the size of all of them
-        float part[F32 ? KC : 1][4];
-#pragma unroll
-        for (int i = 0; i < KC; ++i) {
-          float(&d)[4] = part[F32 ? i : 0];
-          if (F32 || i == 0) d[0] = d[1] = d[2] = d[3] = 0.0f;
-          mma_bf16(d, qf[0][i].x, R == 1 ? 0u : qf[R - 1][i].x, qf[0][i].y, R == 1 ? 0u : qf[R - 1][i].y, kf[jt][i].x,
-                   kf[jt][i].y);
-          mma_bf16(d, qf[0][i].z, R == 1 ? 0u : qf[R - 1][i].z, qf[0][i].w, R == 1 ? 0u : qf[R - 1][i].w, kf[jt][i].z,
-                   kf[jt][i].w);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          sc[jt][x] = part[0][x];
-          if constexpr (F32) {
-#pragma unroll
-            for (int i = 1; i < KC; ++i) sc[jt][x] += part[i][x];
-          }
-        }
-      }
-      // rows past the length weigh nothing
-      const int left = c.len - (c.first + c.step * kStep);
-      if (left < kStep) {
-#pragma unroll
-        for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (jt * 8 + 2 * t + (x & 1) >= left) sc[jt][x] = -INFINITY;
-      }
-      float mx[R];
-      bool grow = false;
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        mx[i] = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1])) * a.scale_log2;
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        grow |= mx[i] > m[i] + kSlack;  // m = -inf at first
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-        float al[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const float n = fmaxf(m[i], mx[i]);
-          al[i] = m[i] == -INFINITY ? 0.0f : ex2_approx(m[i] - n);
-          m[i] = n;
-          l[i] *= al[i];
-        }
-#pragma unroll
-        for (int i = 0; i < VH; ++i)
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) acc[i][x][y] *= al[R == 1 ? 0 : y >> 1];
-      }
-      // weights, as bf16 terms: hi (and, where rows are spare or the output is f32, remainders)
-      constexpr int kTerms = F32 ? 3 : 2;
-      uint32_t pw[R][kTerms][2];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float ref = m[i] == -INFINITY ? 0.0f : m[i];
-#pragma unroll
-        for (int jt = 0; jt < 2; ++jt) {
-          float p0 = ex2_approx(fmaf(sc[jt][2 * i], a.scale_log2, -ref));
-          float p1 = ex2_approx(fmaf(sc[jt][2 * i + 1], a.scale_log2, -ref));
-          l[i] += p0 + p1;
-#pragma unroll
-          for (int x = 0; x < kTerms; ++x) {
-            const uint32_t h = pack_bf16x2(p0, p1);
-            pw[i][x][jt] = h;
-            p0 -= bf16lo_to_f32(h);
-            p1 -= bf16hi_to_f32(h);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < VH; ++i) {
-        uint4 vf[4];
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // rows 2t, 2t + 1, 8 + 2t, 9 + 2t: f = 2t
-          vf[kk] = lds128(src + (kStep + (kk >> 1) * 8 + 2 * t + (kk & 1)) * kRowBytes + ((i * 8 + g) ^ (2 * t)) * 16);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const uint32_t sel = (x & 1) ? 0x7632u : 0x5410u;
-          const uint32_t b0 = __byte_perm(word(vf[0], x >> 1), word(vf[1], x >> 1), sel);
-          const uint32_t b1 = __byte_perm(word(vf[2], x >> 1), word(vf[3], x >> 1), sel);
-          if constexpr (R == 1) {
-            mma_bf16(acc[i][x], pw[0][0][0], pw[0][1][0], pw[0][0][1], pw[0][1][1], b0, b1);
-            if constexpr (F32) mma_bf16(acc[i][x], pw[0][2][0], 0u, pw[0][2][1], 0u, b0, b1);
-          } else {
-#pragma unroll
-            for (int y = 0; y < kTerms; ++y)
-              mma_bf16(acc[i][x], pw[0][y][0], pw[R - 1][y][0], pw[0][y][1], pw[R - 1][y][1], b0, b1);
-          }
-        }
-      }
-      __syncwarp();  // every lane has read this stage: refill it
-      copy_step(s + kStages, stage);
-      look_up();
-      if (++stage == kStages) stage = 0;
+      if (s < 0) continue;
 
       if (c.step + 1 == c.steps || s + 1 == n_steps) {  // the group, or this worker's part of it, is done
-        const bool to_end = c.step + 1 == c.steps;
-        if (!from_start) seg.continues = true, seg.ends = to_end;
+        const bool to_end = c.step + 1 == c.steps, at_end = s + 1 == n_steps, whole = from_start && to_end;
+        if (!from_start) seg.continues = true, seg.ends = to_end, seg.mid = to_end && !at_end;
         else if (!to_end) seg.opens = true, seg.r_last = c.r, seg.hh_last = c.hh;
-        const int kvh = c.hh / a.tiles, h0 = (c.hh - kvh * a.tiles) * GT;
+        int kvh, h0;
+        head_tile_of<GT>(a, c.hh, tile_in_unit, kvh, h0);
+        float* keep_o = at_end ? reinterpret_cast<float*>(smem + warp * (kStages * kStageBytes))
+                               : a.part_o + static_cast<int64_t>(w * a.unit + tile_in_unit) * GT * DH;
+        float* keep_ml = at_end ? keep_o + GT * DH : a.part_ml + static_cast<int64_t>(w * a.unit + tile_in_unit) * GT * 2;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -522,45 +614,33 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
           const int h = h0 + g + 8 * i;
           if (h >= a.g) continue;
           const int64_t o_row = static_cast<int64_t>(c.r) * a.hq + static_cast<int64_t>(kvh) * a.g + h;
-          const bool whole = from_start && to_end;
-          const int64_t slot = 2 * w + (from_start ? 1 : 0);
           const float inv = whole ? 1.0f / l[i] : 1.0f;
           if (t == 0) {
             if (!whole) {
-              a.part_ml[(slot * GT + g + 8 * i) * 2] = m[i];
-              a.part_ml[(slot * GT + g + 8 * i) * 2 + 1] = l[i];
+              keep_ml[(g + 8 * i) * 2] = m[i];
+              keep_ml[(g + 8 * i) * 2 + 1] = l[i];
             } else if (a.lse) {
-              a.lse[o_row] = (m[i] + log2f(l[i])) * 0.693147180559945309f;
+              a.lse[o_row] = (m[i] + __log2f(l[i])) * 0.693147180559945309f;
             }
           }
+          if (whole && !F32) {
+            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + o_row * DH + 2 * t);
 #pragma unroll
-          for (int x = 0; x < VH; ++x) {
-            // columns x * 64 + 16 t + 0..15: eight from each of the two n columns of this lane
-            float o[16];
+            for (int x = 0; x < kBlocks; ++x)
+              dst[x * 4] = pack_bf16x2((R == 1 ? acc[x][0] + acc[x][2] : acc[x][2 * i]) * inv,
+                                       (R == 1 ? acc[x][1] + acc[x][3] : acc[x][2 * i + 1]) * inv);
+          } else {
+            float* base = whole ? static_cast<float*>(a.out) + o_row * DH : keep_o + (g + 8 * i) * DH;
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              o[y] = (R == 1 ? acc[x][y][0] + acc[x][y][2] : acc[x][y][2 * i]) * inv;
-              o[y + 8] = (R == 1 ? acc[x][y][1] + acc[x][y][3] : acc[x][y][2 * i + 1]) * inv;
-            }
-            if (whole && !F32) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + o_row * DH + x * 64 + 16 * t);
-              dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                  pack_bf16x2(o[6], o[7]));
-              dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]),
-                                  pack_bf16x2(o[14], o[15]));
-            } else {
-              float* base = whole ? static_cast<float*>(a.out) + o_row * DH : a.part_o + (slot * GT + g + 8 * i) * DH;
-              float4* dst = reinterpret_cast<float4*>(base + x * 64 + 16 * t);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-            }
+            for (int x = 0; x < kBlocks; ++x)
+              *reinterpret_cast<float2*>(base + x * 8 + 2 * t) =
+                  make_float2((R == 1 ? acc[x][0] + acc[x][2] : acc[x][2 * i]) * inv,
+                              (R == 1 ? acc[x][1] + acc[x][3] : acc[x][2 * i + 1]) * inv);
           }
         }
-        if (s + 1 < n_steps) {
+        if (!at_end) {
           next_group(a, c, heads);
-          from_start = true;
-          load_q();
-          reset();
+          from_start = fresh = true;
         }
       } else {
         ++c.step;
@@ -571,47 +651,78 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
   }
   __syncthreads();  // and the slots that the warps wrote to global memory
 
-  // ---- join what the block's warps share, a (run of parts, head) per warp and turn. Run 0 is the group
-  // that began in an earlier block, run i + 1 the one that warp i began and did not end.
-  const int active = static_cast<int>(min(static_cast<int64_t>(per_block), max(workers - static_cast<int64_t>(blockIdx.x) * per_block, static_cast<int64_t>(0))));
-  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * per_block;
-  for (int item = warp; item < (active + 1) * GT; item += kWarps) {
-    const int run = item / GT, h = item - run * GT;
-    const bool inherited = run == 0;
-    if (inherited ? !s_seg[0].continues : !s_seg[run - 1].opens) continue;
-    const int r = inherited ? s_seg[0].r_first : s_seg[run - 1].r_last;
-    const int hh = inherited ? s_seg[0].hh_first : s_seg[run - 1].hh_last;
-    const int kvh = hh / a.tiles, h0 = (hh - kvh * a.tiles) * GT;
-    if (h0 + h >= a.g) continue;
-    int n = 1;  // warps from the run's first that hold a part; it ends with the group or with the block
-    int last = inherited ? 0 : run - 1;
-    bool ended = inherited && s_seg[0].ends;
-    while (!ended && last + 1 < active) {
-      ++last, ++n;
-      ended = s_seg[last].ends;
+  // ---- join what the block's units share, a (run of parts, tile, head) per warp and turn. Run 0 is the
+  // group that began in an earlier block, run i + 1 the one that unit i began and did not end.
+  // A lane looks at one item: (active + 1) * unit <= 16, GT <= 16, 8 warps: at most 32 a warp.
+  int my_run = -1, my_tile = 0, my_last = 0;
+  bool my_ended = false;
+  if (active > 0) {
+    const int item = warp + lane * kWarps, x = item / GT;
+    const int run = x / a.unit, tile = x - run * a.unit;
+    if (run <= active) {
+      const int first = run == 0 ? 0 : run - 1;
+      const Segments& head = s_seg[first * a.unit];
+      if (run == 0 ? head.continues : head.opens) {
+        my_run = run, my_tile = tile;
+        my_ended = run == 0 && head.ends;
+        my_last = first;  // the run ends with its group or with the block
+#pragma unroll 1
+        while (!my_ended && my_last + 1 < active) my_ended = s_seg[++my_last * a.unit].ends;
+      }
     }
-    const int64_t first = w0 + (inherited ? 0 : run - 1);
+  }
+  uint32_t hits = __ballot_sync(0xffffffffu, my_run >= 0);
+#pragma unroll 1
+  for (; hits; hits &= hits - 1) {
+    const int src = __ffs(hits) - 1;
+    const int run = __shfl_sync(0xffffffffu, my_run, src), tile = __shfl_sync(0xffffffffu, my_tile, src);
+    const int last = __shfl_sync(0xffffffffu, my_last, src), h = (warp + src * kWarps) % GT;
+    const bool ended = __shfl_sync(0xffffffffu, my_ended, src), inherited = run == 0;
+    const int first = inherited ? 0 : run - 1;
+    const Segments& head = s_seg[first * a.unit];
+    int kvh, h0;
+    head_tile_of<GT>(a, inherited ? head.hh_first : head.hh_last, tile, kvh, h0);
+    if (h0 + h >= a.g) continue;
     float o[DH / 32], m, l;
-    merge_parts<DH>(a.part_o, a.part_ml, n, 0, 1,
-                    [&](int p) { return (2 * (first + p) + (p == 0 && !inherited ? 1 : 0)) * GT + h; }, o, m, l);
+    merge_parts<DH>(last - first + 1, 0, 1, [&](int p) {
+      const int x = (first + p) * a.unit + tile;
+      if ((p > 0 || inherited) && s_seg[x].mid) {
+        const int64_t at = (static_cast<int64_t>(w0 + first + p) * a.unit + tile) * GT + h;
+        return Part{a.part_o + at * DH, a.part_ml + at * 2};
+      }
+      const float* base = reinterpret_cast<const float*>(smem + x * (kStages * kStageBytes));
+      return Part{base + h * DH, base + GT * DH + h * 2};
+    }, o, m, l);
     if (!inherited && ended) {
-      store_head<DH>(a, static_cast<int64_t>(r) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + h, o, m, l);
+      store_head<DH>(a, static_cast<int64_t>(head.r_last) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + h, o, m, l);
     } else {
-      const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + (inherited ? 0 : 1)) * GT + h;
+      const int64_t at = ((2 * static_cast<int64_t>(blockIdx.x) + (inherited ? 0 : 1)) * a.unit + tile) * GT + h;
       store_row<DH>(a.block_o + at * DH, o, 1.0f);
       if (lane == 0) a.block_ml[at * 2] = m, a.block_ml[at * 2 + 1] = l;
     }
   }
+  if (tid == kScan - 1 && !a.lone) {  // for the join kernel
+    Record rec{0, 0, -1, -1};
+    if (active > 0 && s_first.start < block_lo) {
+      const int from = s_ranges.owner(s_first.start) / units;
+      if (from == static_cast<int>(blockIdx.x) - 1)
+        rec = Record{s_first.r, s_first.hh, from, s_ranges.owner(s_first.start + s_first.steps - 1) / units};
+    }
+    a.rec[blockIdx.x] = rec;
+  }
 
   // ---- sequences without rows: zeros, and the log-sum of nothing
+#pragma unroll 1
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + warp; r < a.num_reqs; r += static_cast<int64_t>(gridDim.x) * kWarps) {
     if (valid_len(a, a.lens[r]) != 0) continue;
     const int64_t n = static_cast<int64_t>(a.hq) * DH;
+#pragma unroll 1
     for (int64_t i = lane; i < n; i += 32) {
       if (F32) static_cast<float*>(a.out)[r * n + i] = 0.0f;
       else static_cast<uint16_t*>(a.out)[r * n + i] = 0;
     }
     if (a.lse)
+#pragma unroll 1
       for (int h = lane; h < a.hq; h += 32) a.lse[r * a.hq + h] = -INFINITY;
   }
 }
@@ -623,44 +734,56 @@ constexpr int kJoinWarps = 16;
 template <int DH, int GT>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ DecodeArgs a) {
   __shared__ float s_o[kJoinWarps][DH];
-  __shared__ float s_l[kJoinWarps];
+  __shared__ float s_ml[kJoinWarps][2];
   grid_dependency_wait();
-  const Plan plan = *a.plan;
-  const int64_t b = blockIdx.x;
-  if ((b + 1) * plan.per_block >= plan.workers) return;
-  const Record rec = a.rec[b + 1];
-  if (rec.group_start == worker_start((b + 1) * plan.per_block, plan.total, plan.workers)) return;  // nothing crosses
-  if (worker_of(rec.group_start, plan.total, plan.workers) / plan.per_block != b) return;  // an earlier boundary has it
-  const int64_t last = worker_of(rec.group_start + rec.group_steps - 1, plan.total, plan.workers) / plan.per_block;
-  const int parts = static_cast<int>(last - b + 1);
-  const int kvh = rec.hh / a.tiles, h0 = (rec.hh - kvh * a.tiles) * GT;
-  const int heads = min(GT, a.g - h0), shares = kJoinWarps / heads;
+  const Record rec = a.rec[blockIdx.x + 1];
+  if (rec.first < 0) return;
+  const int tile = blockIdx.y;
+  int kvh, h0;
+  head_tile_of<GT>(a, rec.hh, tile, kvh, h0);
+  const int heads = min(GT, a.g - h0);
+  if (heads <= 0) return;
+  const int parts = rec.last - rec.first + 1, shares = kJoinWarps / heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = warp % heads, share = warp / heads;
   float o[DH / 32], m = -INFINITY, l = 0.0f;
   if (share < shares) {
-    merge_parts<DH>(a.block_o, a.block_ml, parts, share, shares, [&](int p) { return (2 * (b + p) + (p == 0 ? 1 : 0)) * GT + h; }, o,
-                    m, l);
+    merge_parts<DH>(parts, share, shares, [&](int p) {
+      const int64_t at = ((2 * static_cast<int64_t>(rec.first + p) + (p == 0 ? 1 : 0)) * a.unit + tile) * GT + h;
+      return Part{a.block_o + at * DH, a.block_ml + at * 2};
+    }, o, m, l);
+    if (share > 0) {
 #pragma unroll
-    for (int x = 0; x < DH / 32; ++x) s_o[warp][lane * (DH / 32) + x] = o[x];
-    if (lane == 0) s_l[warp] = l;
+      for (int x = 0; x < DH / 32; ++x) s_o[warp][lane * (DH / 32) + x] = o[x];
+      if (lane == 0) s_ml[warp][0] = m, s_ml[warp][1] = l;
+    }
   }
   __syncthreads();
   if (share != 0) return;
-  for (int i = 1; i < shares; ++i) {  // all relative to the same maximum
-    l += s_l[i * heads + h];
+  float top = m;
+#pragma unroll 1
+  for (int i = 1; i < shares; ++i) top = fmaxf(top, s_ml[i * heads + h][0]);
+  const float f = m == -INFINITY ? 0.0f : ex2_approx(m - top);
+  l *= f;
 #pragma unroll
-    for (int x = 0; x < DH / 32; ++x) o[x] += s_o[i * heads + h][lane * (DH / 32) + x];
+  for (int x = 0; x < DH / 32; ++x) o[x] *= f;
+#pragma unroll 1
+  for (int i = 1; i < shares; ++i) {
+    const int at = i * heads + h;
+    const float e = s_ml[at][0] == -INFINITY ? 0.0f : ex2_approx(s_ml[at][0] - top);
+    l += s_ml[at][1] * e;
+#pragma unroll
+    for (int x = 0; x < DH / 32; ++x) o[x] += s_o[at][lane * (DH / 32) + x] * e;
   }
-  store_head<DH>(a, static_cast<int64_t>(rec.r) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + h, o, m, l);
+  store_head<DH>(a, static_cast<int64_t>(rec.r) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + h, o, top, l);
 }
 
 struct Layout {
-  int gt, tiles, grid;
+  int gt, tiles, unit, tile_units, grid;
   int64_t workers;
   double bound;  // most steps of a call
-  bool split;
-  size_t plan, rec, ml, o, block_ml, block_o, total;
+  bool lone, split;
+  size_t rec, ml, o, block_ml, block_o, total;
 };
 
 int head_tile(int g) { return g <= 8 ? 8 : 16; }
@@ -674,23 +797,28 @@ Layout layout_of(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int win
   const int g = hq / hkv;
   y.gt = head_tile(g);
   y.tiles = (g + y.gt - 1) / y.gt;
+  // a unit's warps read the same rows, so that they come from HBM once; at most a block's warps
+  const int warps = warps_of(dh, y.gt);
+  y.tile_units = (y.tiles + warps - 1) / warps;
+  y.unit = (y.tiles + y.tile_units - 1) / y.tile_units;
   const int64_t rows = window > 0 ? std::min(max_ctx_len, window) : max_ctx_len;
   const int64_t steps = (rows + kStep - 1) / kStep;
-  y.bound = static_cast<double>(steps) * hkv * y.tiles * num_reqs;
-  const int64_t most = static_cast<int64_t>(sms) * warps_of(dh, y.gt);
-  const double need = std::ceil(y.bound / kMinSteps);
-  y.workers = need < static_cast<double>(most) ? std::max<int64_t>(1, static_cast<int64_t>(need)) : most;
+  y.bound = static_cast<double>(steps) * hkv * y.tile_units * num_reqs;
+  const int64_t most = static_cast<int64_t>(sms) * (warps / y.unit);
+  y.workers = y.bound < static_cast<double>(most) ? std::max<int64_t>(1, static_cast<int64_t>(y.bound)) : most;
   y.grid = static_cast<int>(std::min<int64_t>(sms, y.workers));
-  y.split = steps > 1 && y.grid > 1;
+  const double groups = static_cast<double>(num_reqs) * hkv * y.tile_units;
+  y.lone = groups <= sms && steps <= kLoneSteps;
+  if (y.lone) y.grid = std::max(1, static_cast<int>(groups));
+  y.split = !y.lone && y.grid > 1;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  y.plan = 0;
-  y.rec = 256;
-  const size_t row = static_cast<size_t>(2) * y.gt * sizeof(float);
+  const size_t row = static_cast<size_t>(y.unit) * y.gt * sizeof(float);
+  y.rec = 0;
   y.ml = y.rec + up(static_cast<size_t>(y.grid) * sizeof(Record));
   y.o = y.ml + up(y.workers * row * 2);
   y.block_ml = y.o + up(y.workers * row * dh);
-  y.block_o = y.block_ml + up(y.grid * row * 2);
-  y.total = y.block_o + up(y.grid * row * dh);
+  y.block_o = y.block_ml + up(2 * y.grid * row * 2);
+  y.total = y.block_o + up(2 * y.grid * row * dh);
   return y;
 }
 
@@ -714,7 +842,7 @@ cudaError_t launch(const DecodeArgs& a, const Layout& y, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess || !y.split) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(y.grid - 1));
+  cfg.gridDim = dim3(static_cast<unsigned>(y.grid - 1), static_cast<unsigned>(y.unit));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -781,13 +909,13 @@ int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const 
   a.q = q, a.q_tok = q_stride, a.k = k_pool, a.v = v_pool;
   a.table = block_table, a.table_stride = block_table_stride, a.lens = seq_lens;
   a.out = out, a.lse = lse, a.err = reinterpret_cast<uint32_t*>(status);
-  a.plan = reinterpret_cast<Plan*>(ws + y.plan);
   a.rec = reinterpret_cast<Record*>(ws + y.rec);
   a.block_ml = reinterpret_cast<float*>(ws + y.block_ml);
   a.block_o = reinterpret_cast<float*>(ws + y.block_o);
   a.part_ml = reinterpret_cast<float*>(ws + y.ml);
   a.part_o = reinterpret_cast<float*>(ws + y.o);
-  a.num_reqs = num_reqs, a.hq = hq, a.hkv = hkv, a.g = hq / hkv, a.tiles = y.tiles;
+  a.num_reqs = num_reqs, a.hq = hq, a.hkv = hkv, a.g = hq / hkv;
+  a.unit = y.unit, a.tile_units = y.tile_units, a.lone = y.lone;
   a.num_pages = num_pages, a.page = page_size, a.max_pages = max_pages_per_req, a.window = window;
   a.max_len = max_ctx_len;
   if ((page_size & (page_size - 1)) == 0) {

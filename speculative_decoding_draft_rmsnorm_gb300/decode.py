@@ -13,7 +13,6 @@ a call allocates belong to that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -50,68 +49,98 @@ def _base():
     return pkg
 
 
-_NO_GUARD = contextlib.nullcontext()
+_torch = _lib = _raw_stream = None
 
 
-class _Call:
-    """The device and stream of a call; allocations made inside belong to that stream."""
+def _load():
+    """The library's handle; the first call also brings in torch."""
+    global _torch, _lib, _raw_stream
+    import torch
+    _torch = torch
+    # the current stream's handle without building a Stream object (1 us less), where torch has it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _lib = _base().load()
+    return _lib
 
-    __slots__ = ("lib", "device", "handle", "guard")
 
-    def __init__(self, first, stream):
-        import torch
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError("tensors must live on a CUDA device")
-        self.lib = _base().load()
-        self.device = first.device
-        index = self.device.index
+def _device(t) -> int:
+    """The index of the CUDA device that a call's first tensor lives on."""
+    try:
+        index = t.get_device()
+    except AttributeError:
+        raise TypeError("tensors must be torch.Tensor") from None
+    if index < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    return index
+
+
+def _ptr(name, t, dtype, shape, index, contiguous=True):
+    """Checks a tensor (None passes; shape None = any) and returns its address."""
+    if t is None:
+        return None
+    try:
+        if (t.dtype is dtype and t.get_device() == index and (shape is None or t.shape == shape) and
+                (not contiguous or t.is_contiguous())):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on cuda:{index}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+class _On:
+    """Where a call runs: `handle` is its stream; inside the context the device is current, and what is
+    allocated belongs to that stream (nothing is entered when both already hold)."""
+
+    __slots__ = ("handle", "guard")
+
+    def __init__(self, index, stream):
         if stream is None:
-            s = torch.cuda.current_stream(index)
-            self.handle = s.cuda_stream
-            self.guard = _NO_GUARD if torch.cuda.current_device() == index else torch.cuda.device(index)
+            self.handle = _raw_stream(index)
+            self.guard = None if _torch.cuda.current_device() == index else _torch.cuda.device(index)
         else:
-            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=self.device)
+            s = stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(int(stream), device=index)
             self.handle = s.cuda_stream
-            self.guard = torch.cuda.stream(s)
+            self.guard = _torch.cuda.stream(s)
 
-    def tensor(self, name, t, dtype, shape, contiguous=True):
-        """Checks a tensor (None passes) and returns its address."""
-        if t is None:
-            return None
-        import torch
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the call's tensors are on {self.device}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if contiguous and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
 
-    def run(self, fn, *args):
-        rc = fn(*args, self.handle)
-        if rc != 0:
-            _base()._raise(rc)
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _fail(rc):
+    _base()._raise(rc)
 
 
 def _rows(name, t, dims):
-    """Checks the dimensions of a tensor whose last one must be contiguous."""
-    if t.dim() != dims:
+    """Checks the dimensions of a tensor whose last one must be contiguous; returns its strides."""
+    st = t.stride()
+    if len(st) != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
+    return st
 
 
-def _workspace(call, workspace, nbytes):
-    import torch
-    if nbytes == 0:
-        _base()._raise(_base().ERR_INVALID_ARG)
+def _scratch(workspace, nbytes, index):
+    """(tensor, address, bytes) of a call's workspace: the given one, or a new one of nbytes()."""
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=call.device)
-    return call.tensor("workspace", workspace, torch.uint8, None), workspace.numel()
+        n = nbytes()
+        if n == 0:
+            _fail(_base().ERR_INVALID_ARG)
+        workspace = _torch.empty(n, dtype=_torch.uint8, device=index)
+    return workspace, _ptr("workspace", workspace, _torch.uint8, None, index), workspace.numel()
 
 
 # ------------------------------------------------------------------------------------- rotary
@@ -163,68 +192,76 @@ def rotary(q, positions, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_
     [num_pages, page_size, Hkv, Dh]; -1 = not stored. inverse=True applies the transpose: the gradient
     of the inputs from that of the outputs. q may be None.
     """
-    import torch
+    lib = _lib or _load()
     first = q if q is not None else k
     if first is None:
         raise ValueError("pass q, k or both")
-    c = _Call(first, stream)
-    dtype = first.dtype
-    if dtype not in (torch.bfloat16, torch.float32):
+    index, dtype, i32 = _device(first), first.dtype, _torch.int32
+    if dtype is _torch.bfloat16:
+        code = OUT_BF16
+    elif dtype is _torch.float32:
+        code = OUT_F32
+    else:
         raise TypeError(f"rotary takes bfloat16 or float32, got {dtype}")
-    freq = inv_freq if isinstance(inv_freq, np.ndarray) else np.asarray(inv_freq, dtype=np.float64)
-    if freq.dtype != np.float64 or freq.ndim != 1 or not freq.flags.c_contiguous:
+    freq = inv_freq
+    if type(freq) is not np.ndarray or freq.dtype != np.float64 or freq.ndim != 1 or not freq.flags.c_contiguous:
         freq = np.ascontiguousarray(freq, dtype=np.float64).reshape(-1)
-    _rows("q" if q is not None else "k", first, 3)
-    n, _, dh = first.shape
     if (v is None) != (v_out is None):
         raise ValueError("pass v and v_out together")
     if v is not None and k is None:
         raise ValueError("v needs k")
     if slot is not None and (k is None or k_out is None):
         raise ValueError("slot needs k and k_out")
-    p_pos = c.tensor("positions", positions, torch.int32, (n,))
-    p_slot = c.tensor("slot", slot, torch.int32, (n,))
-    p_status = c.tensor("status", status, torch.int32, (1,))
-    with c.guard:
-        parts = [None, 0, 0, None, 0, 0, 0, None, 0, 0, None, 0, 0, 0, None, 0, 0, None, 0, 0]
-        capacity = n
-        if q is not None:
+    _rows("q" if q is not None else "k", first, 3)
+    n, _, dh = first.shape
+    with _On(index, stream) as handle:
+        a, capacity = [], n
+        if q is None:
+            a += (None, 0, 0, None, 0, 0, 0)
+        else:
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=dtype, device=c.device)
-            _rows("q_out", q_out, 3)
-            parts[0:7] = [c.tensor("q", q, dtype, None, False), q.stride(0), q.stride(1),
-                          c.tensor("q_out", q_out, dtype, q.shape, False), q_out.stride(0), q_out.stride(1), q.shape[1]]
-        if k is not None:
-            _rows("k", k, 3)
-            if k.shape[0] != n or k.shape[2] != dh:
+                q_out = _torch.empty(q.shape, dtype=dtype, device=index)
+            st, so = q.stride(), _rows("q_out", q_out, 3)
+            a += (q.data_ptr(), st[0], st[1], _ptr("q_out", q_out, dtype, q.shape, index, False), so[0], so[1], q.shape[1])
+        if k is None:
+            a += (None, 0, 0, None, 0, 0, 0)
+        else:
+            st, ks = _rows("k", k, 3), k.shape
+            hkv = ks[1]
+            if ks[0] != n or ks[2] != dh:
                 raise ValueError("k must be [n, Hkv, Dh] like q")
-            hkv = k.shape[1]
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=dtype, device=c.device)
-
-            def store(name, t):
-                if t.dim() == 4:
-                    t = t.view(-1, t.shape[2], t.shape[3])
-                _rows(name, t, 3)
-                if t.shape[1] != hkv or t.shape[2] != dh or (slot is None and t.shape[0] != n):
-                    raise ValueError(f"{name} must be [{'capacity' if slot is not None else 'n'}, Hkv, Dh]")
-                return t
-
-            ko = store("k_out", k_out)
-            capacity = ko.shape[0]
-            parts[7:14] = [c.tensor("k", k, dtype, None, False), k.stride(0), k.stride(1),
-                           c.tensor("k_out", ko, dtype, None, False), ko.stride(0), ko.stride(1), hkv]
-            if v is not None:
-                _rows("v", v, 3)
-                vo = store("v_out", v_out)
-                if vo.shape[0] != capacity:
-                    raise ValueError("v_out must have as many rows as k_out")
-                parts[14:20] = [c.tensor("v", v, dtype, k.shape, False), v.stride(0), v.stride(1),
-                                c.tensor("v_out", vo, dtype, None, False), vo.stride(0), vo.stride(1)]
-        c.run(c.lib.dflash_rotary, *parts, p_pos, p_slot, n, capacity, dh, 2 * freq.shape[0], freq.ctypes.data,
-              float(amplitude), int(bool(interleaved)), int(bool(inverse)), OUT_F32 if dtype == torch.float32 else OUT_BF16,
-              p_status)
+                k_out = _torch.empty(ks, dtype=dtype, device=index)
+            ko = _store_rows("k_out", k_out, ks, slot is None)
+            capacity, so = ko.shape[0], ko.stride()
+            a += (_ptr("k", k, dtype, None, index, False), st[0], st[1], _ptr("k_out", ko, dtype, None, index, False), so[0], so[1],
+                  hkv)
+        if v is None:
+            a += (None, 0, 0, None, 0, 0)
+        else:
+            st = _rows("v", v, 3)
+            vo = _store_rows("v_out", v_out, k.shape, slot is None)
+            so = vo.stride()
+            if vo.shape[0] != capacity:
+                raise ValueError("v_out must have as many rows as k_out")
+            a += (_ptr("v", v, dtype, k.shape, index, False), st[0], st[1], _ptr("v_out", vo, dtype, None, index, False), so[0], so[1])
+        rc = lib.dflash_rotary(*a, _ptr("positions", positions, i32, (n,), index), _ptr("slot", slot, i32, (n,), index), n, capacity,
+                               dh, 2 * freq.shape[0], freq.ctypes.data, amplitude, 1 if interleaved else 0, 1 if inverse else 0, code,
+                               _ptr("status", status, i32, (1,), index), handle)
+        if rc:
+            _fail(rc)
     return q_out, k_out
+
+
+def _store_rows(name, t, like, dense):
+    """A destination of k or v as [rows, Hkv, Dh]; dense: as many rows as k."""
+    if t.dim() == 4:
+        t = t.view(-1, t.shape[2], t.shape[3])
+    _rows(name, t, 3)
+    s = t.shape
+    if s[1] != like[1] or s[2] != like[2] or (dense and s[0] != like[0]):
+        raise ValueError(f"{name} must be [{'n' if dense else 'capacity'}, Hkv, Dh]")
+    return t
 
 
 # ------------------------------------------------------------------------------------- attention
@@ -244,43 +281,39 @@ def decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, *, max_ctx_
     [N, Hq, Dh], or (out, lse [N, Hq] f32) with return_lse=True or an lse tensor. A length of 0 gives
     zeros and -inf. max_ctx_len bounds the lengths (grid and workspace size only).
     """
-    import torch
-    c = _Call(q, stream)
-    _rows("q", q, 3)
+    lib = _lib or _load()
+    index, bf16, i32 = _device(q), _torch.bfloat16, _torch.int32
+    sq = _rows("q", q, 3)
     n, hq, dh = q.shape
     if k_pool.dim() != 4 or block_table.dim() != 2:
         raise ValueError("k_pool must be [num_pages, page_size, Hkv, Dh] and block_table [N, max_pages]")
     pages, page, hkv, kdh = k_pool.shape
-    width = block_table.shape[1]
-    bf16, i32 = torch.bfloat16, torch.int32
+    width, stb = block_table.shape[1], block_table.stride()
     if kdh != dh:
         raise ValueError(f"q has head_dim {dh}, the pools {kdh}")
-    if hq > 1 and n and q.stride(1) != dh:
+    if hq > 1 and sq[1] != dh and n:
         raise ValueError("q: the heads of a sequence must be contiguous")
-    if width > 1 and block_table.stride(1) != 1:
+    if width > 1 and stb[1] != 1:
         raise ValueError("block_table: a row must be contiguous")
-    p_q = c.tensor("q", q, bf16, None, False)
-    p_k = c.tensor("k_pool", k_pool, bf16, None)
-    p_v = c.tensor("v_pool", v_pool, bf16, k_pool.shape)
-    p_t = c.tensor("block_table", block_table, i32, (n, width), False)
-    p_l = c.tensor("seq_lens", seq_lens, i32, (n,))
-    p_status = c.tensor("status", status, i32, (1,))
-    odt = torch.float32 if out_dtype == OUT_F32 else bf16
-    lib = c.lib
-    with c.guard:
+    if out_dtype != OUT_BF16 and out_dtype != OUT_F32:
+        raise ValueError("out_dtype must be OUT_BF16 or OUT_F32")
+    odt = _torch.float32 if out_dtype == OUT_F32 else bf16
+    p_q, p_k = _ptr("q", q, bf16, None, index, False), _ptr("k_pool", k_pool, bf16, None, index)
+    p_v, p_t = _ptr("v_pool", v_pool, bf16, k_pool.shape, index), _ptr("block_table", block_table, i32, (n, width), index, False)
+    p_l = _ptr("seq_lens", seq_lens, i32, (n,), index)
+    with _On(index, stream) as handle:
         if out is None:
-            out = torch.empty((n, hq, dh), dtype=odt, device=c.device)
+            out = _torch.empty((n, hq, dh), dtype=odt, device=index)
         if lse is None and return_lse:
-            lse = torch.empty((n, hq), dtype=torch.float32, device=c.device)
-        p_o = c.tensor("out", out, odt, (n, hq, dh))
-        p_lse = c.tensor("lse", lse, torch.float32, (n, hq))
-        if workspace is None:
-            p_w, w_bytes = _workspace(c, None, lib.dflash_decode_workspace_size(n, hq, hkv, dh, max_ctx_len, window))
-        else:
-            p_w, w_bytes = _workspace(c, workspace, 1)
-        c.run(lib.dflash_decode_attention_paged, p_q, q.stride(0) if n > 1 else hq * dh, p_k, p_v, p_t,
-              block_table.stride(0) if n > 1 else width, p_l, n, hq, hkv, dh, pages, page, width, max_ctx_len, scale, window,
-              out_dtype, p_o, p_lse, p_w, w_bytes, p_status)
+            lse = _torch.empty((n, hq), dtype=_torch.float32, device=index)
+        workspace, p_w, w_bytes = _scratch(
+            workspace, lambda: lib.dflash_decode_workspace_size(n, hq, hkv, dh, max_ctx_len, window), index)
+        rc = lib.dflash_decode_attention_paged(
+            p_q, sq[0] if n > 1 else hq * dh, p_k, p_v, p_t, stb[0] if n > 1 else width, p_l, n, hq, hkv, dh, pages, page, width,
+            max_ctx_len, scale, window, out_dtype, _ptr("out", out, odt, (n, hq, dh), index),
+            _ptr("lse", lse, _torch.float32, (n, hq), index), p_w, w_bytes, _ptr("status", status, i32, (1,), index), handle)
+        if rc:
+            _fail(rc)
     return out if lse is None else (out, lse)
 
 
@@ -297,33 +330,36 @@ def beam_select(logits, scores, *, beams_out=None, finished=None, eos=-1, out=No
     fork_pages takes them), finished bool; slots without a candidate hold -inf, -1, -1, False.
     `out` may hold preallocated outputs, e.g. for graph capture.
     """
-    import torch
-    c = _Call(logits, stream)
-    _rows("logits", logits, 3)
+    lib = _lib or _load()
+    index, f32, i32, flag = _device(logits), _torch.float32, _torch.int32, _torch.bool
+    st = _rows("logits", logits, 3)
     n, w, vocab = logits.shape
     k = w if beams_out is None else int(beams_out)
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
-    dt = OUT_F32 if logits.dtype == torch.float32 else OUT_BF16
-    p_x = c.tensor("logits", logits, logits.dtype, None, False)
-    p_s = c.tensor("scores", scores, torch.float32, (n, w))
-    p_f = c.tensor("finished", finished, torch.bool, (n, w))
+    dtype = logits.dtype
+    if dtype is f32:
+        code = OUT_F32
+    elif dtype is _torch.bfloat16:
+        code = OUT_BF16
+    else:
+        raise TypeError(f"logits must be bfloat16 or float32, got {dtype}")
     if k <= 0:
         raise ValueError("beams_out must be positive")
-    lib = c.lib
-    with c.guard:
+    shape = (n, k)
+    p_s, p_f = _ptr("scores", scores, f32, (n, w), index), _ptr("finished", finished, flag, (n, w), index)
+    with _On(index, stream) as handle:
         out = dict(out) if out else {}
         ptr = []
-        for name, dtype in zip(BEAM_OUTPUTS, (torch.float32, torch.int32, torch.int32, torch.bool)):
-            if name not in out:
-                out[name] = torch.empty((n, k), dtype=dtype, device=c.device)
-            ptr.append(c.tensor(name, out[name], dtype, (n, k)))
-        if workspace is None:
-            p_w, w_bytes = _workspace(c, None, lib.dflash_beam_workspace_size(n, w, k, vocab, dt))
-        else:
-            p_w, w_bytes = _workspace(c, workspace, 1)
-        c.run(lib.dflash_beam_select, p_x, logits.stride(0), logits.stride(1), p_s, p_f, n, w, k, vocab, int(eos), dt, *ptr,
-              p_w, w_bytes)
+        for name, dt in zip(BEAM_OUTPUTS, (f32, i32, i32, flag)):
+            t = out.get(name)
+            if t is None:
+                t = out[name] = _torch.empty(shape, dtype=dt, device=index)
+                ptr.append(t.data_ptr())
+            else:
+                ptr.append(_ptr(name, t, dt, shape, index))
+        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_beam_workspace_size(n, w, k, vocab, code), index)
+        rc = lib.dflash_beam_select(logits.data_ptr(), st[0], st[1], p_s, p_f, n, w, k, vocab, eos, code, *ptr, p_w, w_bytes, handle)
+        if rc:
+            _fail(rc)
     return out
 
 
@@ -342,32 +378,34 @@ def pages_workspace_size(num_reqs, num_pages) -> int:
     return int(n)
 
 
-def _table(c, block_table, page_refs, rows=None):
-    import torch
-    if block_table.dim() != 2 or page_refs.dim() != 1:
+def _table(block_table, page_refs, index):
+    """(rows, width, stride, address of the table, of the counts, pages)."""
+    st = block_table.stride()
+    if len(st) != 2 or page_refs.dim() != 1:
         raise ValueError("block_table must be [N, max_pages] and page_refs [num_pages]")
     n, width = block_table.shape
-    if width > 1 and block_table.stride(1) != 1:
+    if width > 1 and st[1] != 1:
         raise ValueError("block_table: a row must be contiguous")
-    if n > 1 and block_table.stride(0) < width:
+    if n > 1 and st[0] < width:
         raise ValueError("block_table: rows must not overlap")
-    p_t = c.tensor("block_table", block_table, torch.int32, None, False)
-    p_r = c.tensor("page_refs", page_refs, torch.int32, None)
-    return n, width, block_table.stride(0) if n > 1 else width, p_t, p_r, page_refs.shape[0]
+    return (n, width, st[0] if n > 1 else width, _ptr("block_table", block_table, _torch.int32, None, index, False),
+            _ptr("page_refs", page_refs, _torch.int32, None, index), page_refs.shape[0])
 
 
-def _pools(c, pools, num_pages):
+def _pools(pools, num_pages, index):
     """(host array of addresses, count, bytes per page, rows per page) of a list of pools."""
     size = page = None
+    addr = []
     for i, t in enumerate(pools):
-        if t.device != c.device or not t.is_contiguous() or t.dim() < 2 or t.shape[0] != num_pages:
-            raise ValueError(f"pool {i} must be a contiguous [num_pages, page_size, ...] tensor on {c.device}")
-        b = t.element_size() * math.prod(t.shape[1:])
-        if size is not None and (b != size or t.shape[1] != page):
+        s = t.shape
+        if t.get_device() != index or not t.is_contiguous() or len(s) < 2 or s[0] != num_pages:
+            raise ValueError(f"pool {i} must be a contiguous [num_pages, page_size, ...] tensor on cuda:{index}")
+        b = t.element_size() * math.prod(s[1:])
+        if size is not None and (b != size or s[1] != page):
             raise ValueError("all pools must have pages of the same size")
-        size, page = b, t.shape[1]
-    arr = (ctypes.c_void_p * max(1, len(pools)))(*[t.data_ptr() for t in pools])
-    return arr, len(pools), size or 0, page
+        size, page = b, s[1]
+        addr.append(t.data_ptr())
+    return (ctypes.c_void_p * max(1, len(addr)))(*addr), len(addr), size or 0, page
 
 
 def fork_pages(parent, seq_lens, block_table, page_refs, *, status=None, stream=None) -> None:
@@ -376,14 +414,16 @@ def fork_pages(parent, seq_lens, block_table, page_refs, *, status=None, stream=
     page_refs [num_pages] int32 counts the table entries that name a page (0 = free) and follows. Nothing
     is copied: reserve_pages gives a row its own copy of a shared page before it is written.
     """
-    import torch
-    c = _Call(block_table, stream)
-    n, width, stride, p_t, p_r, pages = _table(c, block_table, page_refs)
-    p_p = c.tensor("parent", parent.view(-1) if isinstance(parent, torch.Tensor) and parent.dim() > 1 else parent, torch.int32, (n,))
-    p_l = c.tensor("seq_lens", seq_lens, torch.int32, (n,))
-    p_status = c.tensor("status", status, torch.int32, (1,))
-    with c.guard:
-        c.run(c.lib.dflash_fork_pages, p_p, p_l, p_t, stride, p_r, n, width, pages, p_status)
+    lib = _lib or _load()
+    index, i32 = _device(block_table), _torch.int32
+    n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
+    if parent.dim() > 1:
+        parent = parent.view(-1)
+    with _On(index, stream) as handle:
+        rc = lib.dflash_fork_pages(_ptr("parent", parent, i32, (n,), index), _ptr("seq_lens", seq_lens, i32, (n,), index), p_t, stride,
+                                   p_r, n, width, pages, _ptr("status", status, i32, (1,), index), handle)
+        if rc:
+            _fail(rc)
 
 
 def reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, *, num_new, page_size=None, advance=False,
@@ -396,10 +436,10 @@ def reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, *, num
     sequence was refused (no pages left, or its table is full), which status reports. advance=True also
     adds the new rows to seq_lens. page_size is needed only with an empty list of pools.
     """
-    import torch
-    c = _Call(block_table, stream)
-    n, width, stride, p_t, p_r, pages = _table(c, block_table, page_refs)
-    arr, count, page_bytes, page = _pools(c, pools, pages)
+    lib = _lib or _load()
+    index, i32 = _device(block_table), _torch.int32
+    n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
+    arr, count, page_bytes, page = _pools(pools, pages, index)
     if page is None:
         if page_size is None:
             raise ValueError("page_size is needed without pools")
@@ -409,23 +449,19 @@ def reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, *, num
     num_new = int(num_new)
     if num_new < 0:
         raise ValueError("num_new must be >= 0")
-    i32 = torch.int32
-    p_s = c.tensor("new_start_loc", new_start_loc, i32, (n + 1,))
-    p_l = c.tensor("seq_lens", seq_lens, i32, (n,))
-    p_status = c.tensor("status", status, i32, (1,))
-    with c.guard:
+    with _On(index, stream) as handle:
         if slots is None:
-            slots = torch.empty(num_new, dtype=i32, device=c.device)
+            slots = _torch.empty(num_new, dtype=i32, device=index)
         if positions is None:
-            positions = torch.empty(num_new, dtype=i32, device=c.device)
-        p_slots = c.tensor("slots", slots, i32, (num_new,))
-        p_pos = c.tensor("positions", positions, i32, (num_new,))
-        if workspace is None:
-            p_w, w_bytes = _workspace(c, None, c.lib.dflash_pages_workspace_size(n, pages))
-        else:
-            p_w, w_bytes = _workspace(c, workspace, 1)
-        c.run(c.lib.dflash_reserve_pages, p_s, p_l, p_t, stride, p_r, arr, count, page_bytes, n, num_new, width, page, pages,
-              int(bool(advance)), p_slots, p_pos, p_w, w_bytes, p_status)
+            positions = _torch.empty(num_new, dtype=i32, device=index)
+        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index)
+        rc = lib.dflash_reserve_pages(
+            _ptr("new_start_loc", new_start_loc, i32, (n + 1,), index), _ptr("seq_lens", seq_lens, i32, (n,), index), p_t, stride, p_r,
+            arr, count, page_bytes, n, num_new, width, page, pages, 1 if advance else 0,
+            _ptr("slots", slots, i32, (num_new,), index), _ptr("positions", positions, i32, (num_new,), index), p_w, w_bytes,
+            _ptr("status", status, i32, (1,), index), handle)
+        if rc:
+            _fail(rc)
     return slots, positions
 
 
@@ -434,19 +470,17 @@ def compact_pages(block_table, page_refs, pools, *, used=None, workspace=None, s
 
     Returns `used`, an int32 device word: the number of pages in use, which are now the first ones.
     """
-    import torch
-    c = _Call(block_table, stream)
-    n, width, stride, p_t, p_r, pages = _table(c, block_table, page_refs)
-    arr, count, page_bytes, _ = _pools(c, pools, pages)
-    p_status = c.tensor("status", status, torch.int32, (1,))
-    with c.guard:
+    lib = _lib or _load()
+    index, i32 = _device(block_table), _torch.int32
+    n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
+    arr, count, page_bytes, _ = _pools(pools, pages, index)
+    with _On(index, stream) as handle:
         if used is None:
-            used = torch.empty(1, dtype=torch.int32, device=c.device)
-        p_u = c.tensor("used", used, torch.int32, (1,))
-        if workspace is None:
-            p_w, w_bytes = _workspace(c, None, c.lib.dflash_pages_workspace_size(n, pages))
-        else:
-            p_w, w_bytes = _workspace(c, workspace, 1)
-        c.run(c.lib.dflash_compact_pages, p_t, stride, p_r, arr, count, page_bytes, n, width, pages, p_u, p_w, w_bytes,
-              p_status)
+            used = _torch.empty(1, dtype=i32, device=index)
+        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index)
+        rc = lib.dflash_compact_pages(p_t, stride, p_r, arr, count, page_bytes, n, width, pages,
+                                      _ptr("used", used, i32, (1,), index), p_w, w_bytes, _ptr("status", status, i32, (1,), index),
+                                      handle)
+        if rc:
+            _fail(rc)
     return used
