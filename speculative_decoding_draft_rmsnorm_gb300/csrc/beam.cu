@@ -10,8 +10,8 @@
 //
 // What bounds it: HBM, one read of the logits (2 or 4 bytes for ~6 operations and one exponential).
 // A block streams a piece of a row, 16 bytes a thread and kVec such loads in flight, and only keeps
-// maxima: one per thread and slot (a few batches of loads). The K-th largest of the block's 256 thread
-// maxima is a bound that at least K elements reach, so whatever is below it is out; the slots whose
+// maxima: one per thread and slot (a few batches of loads). The K-th largest of the maxima of 32 groups of
+// threads is a bound that at least K elements reach, so whatever is below it is out; the slots whose
 // maximum reaches it -- a dozen or two in the block -- are read once more (from L2) and their elements at
 // or above the bound become candidates, which are ranked against one another. Keeping sorted lists while
 // streaming instead cost 52 instructions an element against ~8. Only where ties flood the candidates
@@ -34,7 +34,7 @@ constexpr int kMergeThreads = 512;
 constexpr int kMaxBeams = 32;         // W and K
 constexpr int kMaxCandidates = 4096;  // per request, W * splits * K
 constexpr int kVec = 4;               // 16-byte loads a thread has in flight
-constexpr int kSlots = 8;             // maxima a thread keeps
+constexpr int kSlots = 4;             // maxima a thread keeps
 constexpr int kRoom = 1024;           // candidates of a block
 constexpr int kMaxVocab = 1 << 26;    // W * vocab < 2^31
 
@@ -223,10 +223,10 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
   using V = Vec<F32>;
   constexpr int E = V::kElems;
   constexpr int kBatch = kScanThreads * kVec;  // vectors of a batch
-  __shared__ float s_max[kWarps];
+  __shared__ float s_max[32], s_warp_max[kWarps];
   __shared__ Sum s_sum[kWarps];
-  __shared__ float s_bound;
   __shared__ int s_count;
+  __shared__ float s_slot[kSlots][kScanThreads];
   __shared__ float s_val[kRoom];
   __shared__ int32_t s_idx[kRoom];
   const int row = blockIdx.x / a.splits, split = blockIdx.x - row * a.splits;
@@ -268,34 +268,38 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     s.add(exp_below(edge, raise_max(edge)));
   }
   const int batches = (p.hi - p.lo + kBatch - 1) / kBatch, per_slot = (batches + kSlots - 1) / kSlots;
-  float slot[kSlots];
+  float slot = -INFINITY;
+  int left = per_slot, q = 0;  // batches until the slot is full
+#pragma unroll 1
+  for (int v0 = p.lo + tid; v0 - tid < p.hi; v0 += kBatch) {
+    uint4 raw[kVec];
+    float batch = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < kSlots; ++q) {
-    slot[q] = -INFINITY;
-    const int end = min((q + 1) * per_slot, batches);
-    for (int i = q * per_slot; i < end; ++i) {
-      const int v0 = p.lo + i * kBatch + tid;
-      uint4 raw[kVec];
-      float batch = -INFINITY;
+    for (int j = 0; j < kVec; ++j)
+      if (v0 + j * kScanThreads < p.hi) raw[j] = ld_stream(p.vec + v0 + j * kScanThreads);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (v0 + j * kScanThreads < p.hi) raw[j] = ld_stream(p.vec + v0 + j * kScanThreads);
+    for (int j = 0; j < kVec; ++j)
+      if (v0 + j * kScanThreads < p.hi) batch = fmaxf(batch, max_of<F32>(raw[j]));
+    const float ref = raise_max(batch);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (v0 + j * kScanThreads < p.hi) batch = fmaxf(batch, max_of<F32>(raw[j]));
-      const float ref = raise_max(batch);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (v0 + j * kScanThreads < p.hi) s.add(exp_sum<F32>(raw[j], ref));
-      slot[q] = fmaxf(slot[q], batch);
+    for (int j = 0; j < kVec; ++j)
+      if (v0 + j * kScanThreads < p.hi) s.add(exp_sum<F32>(raw[j], ref));
+    slot = fmaxf(slot, batch);
+    if (--left == 0) {
+      s_slot[q++][tid] = slot;
+      slot = -INFINITY, left = per_slot;
     }
   }
+  if (left < per_slot) s_slot[q++][tid] = slot;
   grid_dependents_launch();
 
-  // ---- the block's maximum and sum; the bound
+  // ---- the block's maximum and sum; the bound: the K-th largest of the maxima of 32 groups of 8 threads
   float most = m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if ((lane & 7) == 0) s_max[tid >> 3] = most;
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   if (m != -INFINITY) s.scale(exp_below(m, most));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -303,64 +307,59 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     s.add(hi);
     s.lo += lo;
   }
-  if (lane == 0) s_max[warp] = most, s_sum[warp] = s;
-  {
-    uint32_t key = order_key(m);  // sorted over the warp, largest first (bitonic)
-#pragma unroll
-    for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-      for (int d = size / 2; d > 0; d /= 2) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, key, d);
-        const bool descend = (lane & size) == 0, low = (lane & d) == 0;
-        key = (descend == low) ? max(key, other) : min(key, other);
-      }
-    if (lane < K) s_val[warp * K + lane] = from_key(key);
-  }
+  if (lane == 0) s_warp_max[warp] = most, s_sum[warp] = s;
   __syncthreads();
   const int64_t at = static_cast<int64_t>(row) * a.splits + split;
-  if (tid < kWarps * K) {  // the K-th largest of the threads' maxima
-    const float v = s_val[tid];
-    int rank = 0;
-    for (int i = 0; i < kWarps * K; ++i) rank += s_val[i] > v || (s_val[i] == v && i < tid);
-    if (rank == K - 1) s_bound = v;
-  }
   if (tid == kScanThreads - 1) {
-    for (int i = 0; i < kWarps; ++i) most = fmaxf(most, s_max[i]);
+    for (int i = 0; i < kWarps; ++i) most = fmaxf(most, s_warp_max[i]);
     s = Sum{};
+#pragma unroll 1
     for (int i = 0; i < kWarps; ++i) {
       Sum o = s_sum[i];
-      if (s_max[i] != -INFINITY) o.scale(exp_below(s_max[i], most));
+      if (s_warp_max[i] != -INFINITY) o.scale(exp_below(s_warp_max[i], most));
       s.add(o.hi);
       s.lo += o.lo;
     }
     a.part_max[at] = most;
     a.part_sum[at] = s;
   }
-  __syncthreads();
+  float bound;
+  {
+    const float v = s_max[lane];
+    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float o = s_max[i];
+      rank += o > v || (o == v && i < lane);
+    }
+    bound = __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, rank == K - 1)) - 1);
+  }
 
   // ---- candidates: what is at or above the bound, -inf excepted
-  const float bound = s_bound;
   auto push = [&](float v, int32_t i) {
-    if (v >= bound && v > -INFINITY) {
-      const int c = atomicAdd(&s_count, 1);
-      if (c < kRoom) s_val[c] = v, s_idx[c] = i;
-    }
+    const int c = atomicAdd(&s_count, 1);
+    if (c < kRoom) s_val[c] = v, s_idx[c] = i;
   };
-  if (edge_at >= 0) push(edge, edge_at);
+  if (edge >= bound && edge > -INFINITY) push(edge, edge_at);
+#pragma unroll 1
+  for (int i = 0; i < q; ++i) {
+    const float top = s_slot[i][tid];
+    if (!(top >= bound && top > -INFINITY)) continue;
+    const int v1 = min(p.lo + (i + 1) * per_slot * kBatch, p.hi);
+#pragma unroll 1
+    for (int v = p.lo + i * per_slot * kBatch + tid; v < v1; v += kScanThreads) {
+      const uint4 raw = p.vec[v];
+      uint32_t mask = 0;
 #pragma unroll
-  for (int q = 0; q < kSlots; ++q) {
-    if (slot[q] >= bound && slot[q] > -INFINITY) {
-      const int end = min((q + 1) * per_slot, batches);
-      for (int i = q * per_slot; i < end; ++i)
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const int v = p.lo + i * kBatch + j * kScanThreads + tid;
-          if (v >= p.hi) continue;
-          const uint4 raw = p.vec[v];
-          if (max_of<F32>(raw) < bound) continue;
-#pragma unroll
-          for (int x = 0; x < E; ++x) push(V::at(raw, x), p.head + v * E + x);
-        }
+      for (int x = 0; x < E; ++x) {
+        const float e = V::at(raw, x);
+        mask |= (e >= bound && e > -INFINITY ? 1u : 0u) << x;
+      }
+#pragma unroll 1
+      for (; mask; mask &= mask - 1) {
+        const int32_t x = p.head + v * E + __ffs(mask) - 1;
+        push(V::one(p.base, x), x);
+      }
     }
   }
   __syncthreads();
@@ -371,6 +370,7 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     count = kWarps * K;
     __syncthreads();
   }
+#pragma unroll 1
   for (int c = tid; c < max(count, K); c += kScanThreads) {
     if (c >= count) {  // fewer candidates than beams
       a.part_idx[at * K + c] = -1;
@@ -391,42 +391,96 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
   }
 }
 
-// Candidates are compared by the order-preserving integer of their score in 64 bits (the FP64 units are
-// few: comparing doubles cost 30 us a call). 0 = none.
+// A score is held in two f32 terms, the first the nearest f32 to it, and compared by the order-preserving
+// integers of the two. (The FP64 units are few: scores in doubles cost 30 us a call as they were compared,
+// and one logarithm from the library more than 2.)
 struct Best {
-  uint64_t key;
-  int32_t at;  // w V + t
+  uint32_t hi, lo;  // 0, 0: none
+  int32_t at;       // w V + t
 };
 __device__ __forceinline__ bool better(const Best& x, const Best& y) {
-  return x.key > y.key || (x.key == y.key && x.at < y.at);
+  return x.hi != y.hi ? x.hi > y.hi : x.lo != y.lo ? x.lo > y.lo : x.at < y.at;
 }
-__device__ __forceinline__ Best best_of_warp(Best b) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Best y{__shfl_xor_sync(0xffffffffu, b.key, o), __shfl_xor_sync(0xffffffffu, b.at, o)};
-    if (better(y, b)) b = y;
-  }
-  return b;
+__device__ __forceinline__ Best best_of_warp(const Best& b) {
+  Best r;
+  r.hi = __reduce_max_sync(0xffffffffu, b.hi);
+  r.lo = __reduce_max_sync(0xffffffffu, b.hi == r.hi ? b.lo : 0u);
+  r.at = __reduce_min_sync(0xffffffffu, b.hi == r.hi && b.lo == r.lo ? b.at : 0x7fffffff);
+  return r;
+}
+
+// m + log(s.hi + s.lo) in 64 bits with few FP64 instructions: s = 2^e f, f in [2/3, 4/3), and
+// log f = 2 atanh(q), q = (f - 1) / (f + 1), |q| <= 1/5, by its series (the first term left out is below
+// 2 * 5^-23 / 23 = 8e-18).
+__device__ __forceinline__ double log_plus(float m, const Sum& s) {
+  const double x = static_cast<double>(s.hi) + s.lo;
+  if (!(s.hi > 0.0f) || m == -INFINITY || s.hi == INFINITY) return static_cast<double>(m) + static_cast<double>(__logf(s.hi));
+  const int e = static_cast<int>((__float_as_uint(s.hi * 0.75f) >> 23) & 255u) - 126;  // hi in [2/3, 4/3) 2^e
+  const double f = x * __longlong_as_double(static_cast<long long>(1023 - e) << 52);
+  const double num = f - 1.0, den = f + 1.0;
+  const double r = static_cast<double>(1.0f / static_cast<float>(den));
+  double q = num * r;
+  q = fma(r, fma(-q, den, num), q);
+  const double z = q * q;
+  double p = 1.0 / 21.0;
+  p = fma(p, z, 1.0 / 19.0);
+  p = fma(p, z, 1.0 / 17.0);
+  p = fma(p, z, 1.0 / 15.0);
+  p = fma(p, z, 1.0 / 13.0);
+  p = fma(p, z, 1.0 / 11.0);
+  p = fma(p, z, 1.0 / 9.0);
+  p = fma(p, z, 1.0 / 7.0);
+  p = fma(p, z, 1.0 / 5.0);
+  p = fma(p, z, 1.0 / 3.0);
+  p = fma(p, z, 1.0);
+  return fma(static_cast<double>(e), 0.693147180559945309, static_cast<double>(m)) + 2.0 * q * p;
 }
 
 // One block per request: every thread holds up to kPer candidates; K rounds of a block-wide maximum.
 template <int kThreads, int kPer>
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
-  __shared__ double s_lse[kMaxBeams];
-  __shared__ Best s_best[2][kThreads / 32];
+  constexpr int kMergeWarps = kThreads / 32;
+  __shared__ float s_max[kMaxBeams];
+  __shared__ Sum s_lse[kMaxBeams];  // first the sums, then their logarithms in two terms
+  __shared__ Best s_best[2][kMergeWarps];
   grid_dependency_wait();
   const int n = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = a.beams, K = a.out_beams, S = a.splits;
-  for (int w = warp; w < W; w += kThreads / 32) {
+  const int total = W * S * K;
+  // the candidates' loads first: they do not depend on the sums
+  float val[kPer], score[kPer];
+  int32_t idx[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = j * kThreads + tid;
+    idx[j] = -1, val[j] = score[j] = 0.0f;
+    if (i < total) {
+      const int w = i / (S * K), rest = i - w * S * K, row = n * W + w;
+      score[j] = a.scores[row];
+      if (a.finished && a.finished[row]) {
+        if (rest == 0) idx[j] = a.eos;
+      } else {
+        idx[j] = a.part_idx[static_cast<int64_t>(row) * S * K + rest];
+        val[j] = a.part_val[static_cast<int64_t>(row) * S * K + rest];
+      }
+    }
+  }
+#pragma unroll 1
+  for (int w = warp; w < W; w += kMergeWarps) {
     const int row = n * W + w;
-    if (a.finished && a.finished[row]) continue;
+    if (a.finished && a.finished[row]) {  // its candidate is its score
+      if (lane == 0) s_max[w] = 0.0f, s_lse[w] = Sum{1.0f, 0.0f};
+      continue;
+    }
     const float* mx = a.part_max + static_cast<int64_t>(row) * S;
     const Sum* ps = a.part_sum + static_cast<int64_t>(row) * S;
     float m = -INFINITY;
+#pragma unroll 1
     for (int i = lane; i < S; i += 32) m = fmaxf(m, mx[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     Sum sum;
+#pragma unroll 1
     for (int i = lane; i < S; i += 32) {
       Sum x = ps[i];
       if (mx[i] != -INFINITY) x.scale(exp_below(mx[i], m));
@@ -439,53 +493,57 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
       sum.add(hi);
       sum.lo += lo;
     }
-    // no live logit: -inf + log 0; NaN: NaN
-    if (lane == 0) s_lse[w] = m + log(static_cast<double>(sum.hi) + sum.lo);
+    if (lane == 0) s_max[w] = m, s_lse[w] = sum;
+  }
+  __syncthreads();
+  if (warp == 0 && lane < W) {  // one logarithm for all beams
+    const double lse = log_plus(s_max[lane], s_lse[lane]);
+    const float hi = static_cast<float>(lse);
+    s_lse[lane] = Sum{hi, static_cast<float>(lse - static_cast<double>(hi))};
   }
   __syncthreads();
   Best mine[kPer];
-  const int total = W * S * K;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    mine[j] = Best{0, 0};
     const int i = j * kThreads + tid;
-    if (i < total) {
-      const int w = i / (S * K), rest = i - w * S * K, row = n * W + w;
-      double score = -INFINITY;
-      if (a.finished && a.finished[row]) {
-        if (rest == 0) score = a.scores[row], mine[j].at = w * a.vocab + a.eos;
-      } else {
-        const int32_t t = a.part_idx[static_cast<int64_t>(row) * S * K + rest];
-        if (t >= 0) {
-          score = static_cast<double>(a.scores[row]) +
-                  (static_cast<double>(a.part_val[static_cast<int64_t>(row) * S * K + rest]) - s_lse[w]);
-          mine[j].at = w * a.vocab + t;
-        }
-      }
-      if (score > -INFINITY) {  // -inf and NaN are no candidates
-        const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(score + 0.0));  // -0 becomes 0
-        mine[j].key = bits ^ ((bits >> 63) ? ~0ull : (1ull << 63));
+    const int w = i / (S * K);
+    mine[j] = Best{0, 0, 0x7fffffff};
+    if (idx[j] >= 0) {
+      // score + value - lse, each sum with its rounding error
+      const Sum lse = s_lse[w];
+      Sum c{score[j], 0.0f};
+      c.add(val[j]);
+      c.add(-lse.hi);
+      const float lo = c.lo - lse.lo;
+      float hi = c.hi + lo;
+      const float z = hi - c.hi;
+      float rest = (c.hi - (hi - z)) + (lo - z);
+      if (!(fabsf(hi) < INFINITY)) hi = score[j] + val[j] - lse.hi, rest = 0.0f;
+      if (hi > -INFINITY) {  // -inf and NaN are no candidates
+        mine[j].hi = order_key(hi + 0.0f);
+        mine[j].lo = order_key(rest + 0.0f);
+        mine[j].at = w * a.vocab + idx[j];
       }
     }
   }
+#pragma unroll 1
   for (int k = 0; k < K; ++k) {
-    Best b{0, 0};
+    Best b = mine[0];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
+    for (int j = 1; j < kPer; ++j)
       if (better(mine[j], b)) b = mine[j];
     b = best_of_warp(b);
     if (lane == 0) s_best[k & 1][warp] = b;
     __syncthreads();  // the other buffer is read before the next round's barrier
-    b = best_of_warp(s_best[k & 1][lane < kThreads / 32 ? lane : 0]);
+    b = best_of_warp(s_best[k & 1][lane < kMergeWarps ? lane : 0]);
+    const bool none = b.hi == 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (mine[j].at == b.at) mine[j].key = 0;
+      if (mine[j].at == b.at) mine[j].hi = mine[j].lo = 0;
     if (tid == 0) {
       const int64_t o = static_cast<int64_t>(n) * K + k;
-      const bool none = b.key == 0;
-      const int w = b.at / a.vocab, t = none ? -1 : b.at - w * a.vocab;
-      const uint64_t bits = b.key ^ ((b.key >> 63) ? (1ull << 63) : ~0ull);
-      a.out_scores[o] = none ? -INFINITY : static_cast<float>(__longlong_as_double(static_cast<long long>(bits)));
+      const int w = none ? 0 : b.at / a.vocab, t = none ? -1 : b.at - w * a.vocab;
+      a.out_scores[o] = none ? -INFINITY : from_key(b.hi);
       a.out_tokens[o] = t;
       a.out_parents[o] = none ? -1 : n * W + w;
       a.out_finished[o] = !none && (t == a.eos || (a.finished && a.finished[n * W + w]));
