@@ -32,10 +32,13 @@ constexpr int kWarps = 8;
 constexpr int kScanThreads = kWarps * 32;
 constexpr int kMergeThreads = 512;
 constexpr int kMaxBeams = 32;         // W and K
-constexpr int kMaxCandidates = 4096;  // per request, W * splits * K
+constexpr int kMaxCandidates = 4096;  // per request, W * lists * K
 constexpr int kVec = 4;               // 16-byte loads a thread has in flight
-constexpr int kSlots = 4;             // maxima a thread keeps
-constexpr int kRoom = 1024;           // candidates of a block
+constexpr int kSlots = 16;            // maxima a thread keeps
+constexpr int kRoom = kWarps * kMaxBeams;  // candidates of a block
+constexpr int kTile = 512;            // vectors at most: 4096 bf16 or 2048 f32 elements
+constexpr int kBlocksPerSm = 4;
+constexpr int kWaves = 1;
 constexpr int kMaxVocab = 1 << 26;    // W * vocab < 2^31
 
 // A sum in two f32 terms (Knuth's two-sum): 48 bits, so that what small terms add to a sum that a few
@@ -55,10 +58,13 @@ struct BeamArgs {
   int64_t req_stride, beam_stride;  // elements
   const float* scores;
   const uint8_t* finished;  // null: none
-  int beams, out_beams, vocab, eos, splits;
-  float* part_max;    // [rows][splits] maximum
-  Sum* part_sum;      // [rows][splits] sum relative to it
-  float* part_val;    // [rows][splits][K]
+  int beams, out_beams, vocab, eos;
+  // The rows' tiles (kTile vectors) laid end to end are dealt out in equal consecutive shares, one a block;
+  // what block b finds in row r goes to list b + r.
+  int rows, tiles, per_block, most_lists;  // tiles of a row, of a block; most lists of a row
+  float* part_max;    // [lists] maximum
+  Sum* part_sum;      // [lists] sum relative to it
+  float* part_val;    // [lists][K]
   int32_t* part_idx;  // -1: none
   float* out_scores;
   int32_t* out_tokens;
@@ -103,11 +109,13 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   return v;
 }
 
+constexpr float kLog2e = 1.442695021629f, kLog2eTail = 1.925963033500e-8f;  // log2(e) in two terms
+
 // exp(x - m) for x <= m. The product with log2(e) carries its rounding in the constant's tail: the sum
 // of the exponentials has no bias from it.
 __device__ __forceinline__ float exp_below(float x, float m) {
   const float d = x - m;
-  return ex2_approx(fmaf(d, 1.925963033500e-8f, d * 1.442695021629f));
+  return ex2_approx(fmaf(d, kLog2eTail, d * kLog2e));
 }
 
 // A warp's best elements: lane i holds the i-th, by (value descending, index ascending); only the first
@@ -198,43 +206,93 @@ __device__ __forceinline__ float max_of(const uint4& v) {
   }
 }
 
-// Sum of exp(x - ref) over a vector: two elements an instruction (see exp_below).
-template <bool F32>
-__device__ __forceinline__ float exp_sum(const uint4& v, float ref) {
-  using V = Vec<F32>;
-  const uint64_t off = f32x2(-ref, -ref), c = f32x2(1.442695021629f, 1.442695021629f),
-                 tail = f32x2(1.925963033500e-8f, 1.925963033500e-8f), zero = f32x2(0.0f, 0.0f);
-  uint64_t sum = zero;
-#pragma unroll
-  for (int i = 0; i < V::kElems; i += 2) {
-    const uint64_t d = add_f32x2(f32x2(V::at(v, i), V::at(v, i + 1)), off);
-    const uint64_t t = fma_f32x2(d, tail, fma_f32x2(d, c, zero));
-    float a, b;
-    f32x2_split(t, a, b);
-    sum = add_f32x2(sum, f32x2(ex2_approx(a), ex2_approx(b)));
+// What a thread takes exponentials relative to: the largest element so far (0 while all are -inf).
+// exp(x - ref) = 2^(x c - r) fix with c = log2(e) rounded, r = ref c rounded and fix the factor that the two
+// roundings leave out: the difference is one FMA, exact but for its last bit. Beyond 2^27 the last bit of r
+// is no small factor, and the difference is taken first.
+struct Reference {
+  float ref, r, fix;
+  bool direct;
+  __device__ __forceinline__ void set(float m) {
+    ref = m == -INFINITY ? 0.0f : m;
+    r = ref * kLog2e;
+    fix = fmaf(fmaf(-ref, kLog2e, r) - ref * kLog2eTail, 0.693147180559945309f, 1.0f);
+    direct = !(fabsf(ref) < 134217728.0f);
   }
+};
+
+// The sum of exp(x - ref) over kVec vectors: two elements an instruction.
+template <bool F32>
+__device__ __forceinline__ float exp_sum(const uint4 (&v)[kVec], const Reference& f) {
+  using V = Vec<F32>;
+  if (f.direct) {
+    float s = 0.0f;
+#pragma unroll 1
+    for (int x = 0; x < V::kElems; ++x)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) s += exp_below(V::at(v[j], x), f.ref);
+    return s;
+  }
+  const uint64_t c = f32x2(kLog2e, kLog2e), off = f32x2(-f.r, -f.r);
+  uint64_t part[kVec];
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) {
+#pragma unroll
+    for (int x = 0; x < V::kElems; x += 2) {
+      float a, b;
+      f32x2_split(fma_f32x2(f32x2(V::at(v[j], x), V::at(v[j], x + 1)), c, off), a, b);
+      const uint64_t e = f32x2(ex2_approx(a), ex2_approx(b));
+      part[j] = x == 0 ? e : add_f32x2(part[j], e);
+    }
+  }
+#pragma unroll
+  for (int w = kVec / 2; w > 0; w /= 2)
+#pragma unroll
+    for (int j = 0; j < w; ++j) part[j] = add_f32x2(part[j], part[j + w]);
   float a, b;
-  f32x2_split(sum, a, b);
-  return a + b;
+  f32x2_split(part[0], a, b);
+  return (a + b) * f.fix;
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
+__device__ __forceinline__ float max_of(const uint4 (&v)[kVec]) {
+  if constexpr (F32) {
+    float m = max_of<true>(v[0]);
+#pragma unroll
+    for (int j = 1; j < kVec; ++j) m = fmaxf(m, max_of<true>(v[j]));
+    return m;
+  } else {
+    uint4 m = v[0];
+    auto take = [](uint32_t& x, uint32_t y) { asm("max.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(y)); };
+#pragma unroll
+    for (int j = 1; j < kVec; ++j) take(m.x, v[j].x), take(m.y, v[j].y), take(m.z, v[j].z), take(m.w, v[j].w);
+    return max_of<false>(m);
+  }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
   using V = Vec<F32>;
   constexpr int E = V::kElems;
   constexpr int kBatch = kScanThreads * kVec;  // vectors of a batch
-  __shared__ float s_max[32], s_warp_max[kWarps];
+  __shared__ float s_max[32], s_warp_max[kWarps], s_bound;
   __shared__ Sum s_sum[kWarps];
-  __shared__ int s_count;
+  __shared__ int s_count, s_hits;
+  __shared__ int32_t s_hit[kRoom];
   __shared__ float s_slot[kSlots][kScanThreads];
   __shared__ float s_val[kRoom];
   __shared__ int32_t s_idx[kRoom];
-  const int row = blockIdx.x / a.splits, split = blockIdx.x - row * a.splits;
-  const int n = row / a.beams, b = row - n * a.beams;
-  if (a.finished && a.finished[row]) return;  // its one candidate needs no logits
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int K = a.out_beams;
   constexpr size_t kSize = F32 ? 4 : 2;
+  const int64_t tile_end = min((static_cast<int64_t>(blockIdx.x) + 1) * a.per_block, static_cast<int64_t>(a.rows) * a.tiles);
+#pragma unroll 1
+  for (int64_t tile = static_cast<int64_t>(blockIdx.x) * a.per_block; tile < tile_end;) {
+  const int row = static_cast<int>(tile / a.tiles), from = static_cast<int>(tile - static_cast<int64_t>(row) * a.tiles);
+  const int upto = static_cast<int>(min(static_cast<int64_t>(a.tiles), from + (tile_end - tile)));
+  tile += upto - from;
+  if (a.finished && a.finished[row]) continue;  // its one candidate needs no logits
+  const int n = row / a.beams, b = row - n * a.beams;
   Piece p;
   p.base = static_cast<const char*>(a.logits) + (n * a.req_stride + b * a.beam_stride) * static_cast<int64_t>(kSize);
   const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(p.base) & 15u) / static_cast<int>(kSize);
@@ -243,20 +301,23 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
   const int vecs = (a.vocab - p.head) / E;
   p.tail = p.head + vecs * E;
   p.vec = reinterpret_cast<const uint4*>(p.base + p.head * kSize);
-  p.lo = static_cast<int>(static_cast<int64_t>(vecs) * split / a.splits);
-  p.hi = static_cast<int>(static_cast<int64_t>(vecs) * (split + 1) / a.splits);
-  p.first = split == 0, p.last = split == a.splits - 1;
-  if (tid == 0) s_count = 0;
+  // equal tiles: a short one at the end would hold too few elements for a bound
+  p.lo = static_cast<int>(static_cast<int64_t>(vecs) * from / a.tiles);
+  p.hi = static_cast<int>(static_cast<int64_t>(vecs) * upto / a.tiles);
+  p.first = from == 0, p.last = upto == a.tiles;
+  if (tid == 0) s_count = s_hits = 0;
 
   // ---- one pass: maximum, sum of exponentials, slot maxima
   float m = -INFINITY;
   Sum s;  // of exp(x - m)
-  auto raise_max = [&](float most) {  // returns what exponentials are taken relative to
+  Reference ref;
+  ref.set(m);
+  auto raise_max = [&](float most) {
     if (most > m) {
       s.scale(m == -INFINITY ? (s.hi == 0.0f ? 0.0f : 1.0f) : exp_below(m, most));  // a NaN stays one
       m = most;
+      ref.set(m);
     }
-    return m == -INFINITY ? 0.0f : m;
   };
   // at most 14 elements at the ends of a row, one a thread
   int edge_at = -1;
@@ -265,7 +326,8 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
   float edge = -INFINITY;
   if (edge_at >= 0) {
     edge = V::one(p.base, edge_at);
-    s.add(exp_below(edge, raise_max(edge)));
+    raise_max(edge);
+    s.add(exp_below(edge, ref.ref));
   }
   const int batches = (p.hi - p.lo + kBatch - 1) / kBatch, per_slot = (batches + kSlots - 1) / kSlots;
   float slot = -INFINITY;
@@ -273,17 +335,15 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
 #pragma unroll 1
   for (int v0 = p.lo + tid; v0 - tid < p.hi; v0 += kBatch) {
     uint4 raw[kVec];
-    float batch = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j)
+    for (int j = 0; j < kVec; ++j) {
+      constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80ff80u;  // -inf
+      raw[j] = make_uint4(kNone, kNone, kNone, kNone);
       if (v0 + j * kScanThreads < p.hi) raw[j] = ld_stream(p.vec + v0 + j * kScanThreads);
-#pragma unroll
-    for (int j = 0; j < kVec; ++j)
-      if (v0 + j * kScanThreads < p.hi) batch = fmaxf(batch, max_of<F32>(raw[j]));
-    const float ref = raise_max(batch);
-#pragma unroll
-    for (int j = 0; j < kVec; ++j)
-      if (v0 + j * kScanThreads < p.hi) s.add(exp_sum<F32>(raw[j], ref));
+    }
+    const float batch = max_of<F32>(raw);
+    raise_max(batch);
+    s.add(exp_sum<F32>(raw, ref));
     slot = fmaxf(slot, batch);
     if (--left == 0) {
       s_slot[q++][tid] = slot;
@@ -291,8 +351,6 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     }
   }
   if (left < per_slot) s_slot[q++][tid] = slot;
-  grid_dependents_launch();
-
   // ---- the block's maximum and sum; the bound: the K-th largest of the maxima of 32 groups of 8 threads
   float most = m;
 #pragma unroll
@@ -309,22 +367,26 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
   }
   if (lane == 0) s_warp_max[warp] = most, s_sum[warp] = s;
   __syncthreads();
-  const int64_t at = static_cast<int64_t>(row) * a.splits + split;
-  if (tid == kScanThreads - 1) {
-    for (int i = 0; i < kWarps; ++i) most = fmaxf(most, s_warp_max[i]);
-    s = Sum{};
-#pragma unroll 1
-    for (int i = 0; i < kWarps; ++i) {
-      Sum o = s_sum[i];
-      if (s_warp_max[i] != -INFINITY) o.scale(exp_below(s_warp_max[i], most));
-      s.add(o.hi);
-      s.lo += o.lo;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) + row;
+  if (warp == kWarps - 1) {  // the block's sum, a warp's per lane
+    const float wm = s_warp_max[lane % kWarps];
+    most = wm;
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    s = s_sum[lane % kWarps];
+    if (wm != -INFINITY) s.scale(exp_below(wm, most));
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+      const float hi = __shfl_down_sync(0xffffffffu, s.hi, o), lo = __shfl_down_sync(0xffffffffu, s.lo, o);
+      s.add(hi);
+      s.lo += lo;
     }
-    a.part_max[at] = most;
-    a.part_sum[at] = s;
+    if (lane == 0) {
+      a.part_max[at] = most;
+      a.part_sum[at] = s;
+    }
   }
-  float bound;
-  {
+  if (warp == 0) {
     const float v = s_max[lane];
     int rank = 0;
 #pragma unroll
@@ -332,39 +394,53 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
       const float o = s_max[i];
       rank += o > v || (o == v && i < lane);
     }
-    bound = __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, rank == K - 1)) - 1);
+    if (rank == K - 1) s_bound = v;
   }
+  __syncthreads();
+  const float bound = s_bound;
 
   // ---- candidates: what is at or above the bound, -inf excepted
+  // Slots that reach the bound, of any thread, are listed, and kVec threads share one: their loads go
+  // together (a thread going through its own, slot after slot, took a quarter of the block's time).
   auto push = [&](float v, int32_t i) {
     const int c = atomicAdd(&s_count, 1);
     if (c < kRoom) s_val[c] = v, s_idx[c] = i;
   };
   if (edge >= bound && edge > -INFINITY) push(edge, edge_at);
-#pragma unroll 1
+#pragma unroll 4
   for (int i = 0; i < q; ++i) {
     const float top = s_slot[i][tid];
-    if (!(top >= bound && top > -INFINITY)) continue;
-    const int v1 = min(p.lo + (i + 1) * per_slot * kBatch, p.hi);
-#pragma unroll 1
-    for (int v = p.lo + i * per_slot * kBatch + tid; v < v1; v += kScanThreads) {
-      const uint4 raw = p.vec[v];
-      uint32_t mask = 0;
+    if (top >= bound && top > -INFINITY) {
+      const int h = atomicAdd(&s_hits, 1);
+      if (h < kRoom) s_hit[h] = i * kScanThreads + tid;
+    }
+  }
+  __syncthreads();
+  const int hits = s_hits;
+  if (hits <= kRoom) {
+    for (int h = tid / kVec; h < hits; h += kScanThreads / kVec) {
+      const int i = s_hit[h] / kScanThreads, t = s_hit[h] - i * kScanThreads;
+      const int v1 = min(p.lo + (i + 1) * per_slot * kBatch, p.hi);
+      for (int v = p.lo + i * per_slot * kBatch + t + tid % kVec * kScanThreads; v < v1; v += kBatch) {
+        const uint4 raw = p.vec[v];
+        if (!(max_of<F32>(raw) >= bound)) continue;
+        uint32_t mask = 0;
 #pragma unroll
-      for (int x = 0; x < E; ++x) {
-        const float e = V::at(raw, x);
-        mask |= (e >= bound && e > -INFINITY ? 1u : 0u) << x;
-      }
+        for (int x = 0; x < E; ++x) {
+          const float e = V::at(raw, x);
+          mask |= (e >= bound && e > -INFINITY ? 1u : 0u) << x;
+        }
 #pragma unroll 1
-      for (; mask; mask &= mask - 1) {
-        const int32_t x = p.head + v * E + __ffs(mask) - 1;
-        push(V::one(p.base, x), x);
+        for (; mask; mask &= mask - 1) {
+          const int32_t x = p.head + v * E + __ffs(mask) - 1;
+          push(V::one(p.base, x), x);
+        }
       }
     }
   }
   __syncthreads();
   int count = s_count;
-  if (count > kRoom) {  // many equal elements
+  if (count > kRoom || hits > kRoom) {  // many equal elements, or too few for a bound
     __syncthreads();
     piece_lists<F32>(p, K, s_val, s_idx);
     count = kWarps * K;
@@ -379,6 +455,7 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     const float v = s_val[c];
     const int32_t id = s_idx[c];
     int rank = 0;  // places without an element (from lists that did not fill) come last
+#pragma unroll 4
     for (int i = 0; i < count; ++i) {
       const float o = s_val[i];
       const int32_t oi = s_idx[i];
@@ -389,6 +466,9 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
       a.part_idx[at * K + rank] = id;
     }
   }
+  __syncthreads();  // before the next row's piece reuses the shared arrays
+  }
+  grid_dependents_launch();
 }
 
 // A score is held in two f32 terms, the first the nearest f32 to it, and compared by the order-preserving
@@ -436,6 +516,18 @@ __device__ __forceinline__ double log_plus(float m, const Sum& s) {
   return fma(static_cast<double>(e), 0.693147180559945309, static_cast<double>(m)) + 2.0 * q * p;
 }
 
+struct Lists {
+  int64_t first;
+  int count;
+};
+__device__ __forceinline__ Lists lists_of(const BeamArgs& a, int row) {
+  const int64_t lo = static_cast<int64_t>(row) * a.tiles;
+  int64_t b0, b1;
+  if (lo + a.tiles < (1ll << 31)) b0 = static_cast<uint32_t>(lo) / a.per_block, b1 = static_cast<uint32_t>(lo + a.tiles - 1) / a.per_block;
+  else b0 = lo / a.per_block, b1 = (lo + a.tiles - 1) / a.per_block;
+  return Lists{b0 + row, static_cast<int>(b1 - b0) + 1};
+}
+
 // One block per request: every thread holds up to kPer candidates; K rounds of a block-wide maximum.
 template <int kThreads, int kPer>
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
@@ -445,55 +537,58 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
   __shared__ Best s_best[2][kMergeWarps];
   grid_dependency_wait();
   const int n = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int W = a.beams, K = a.out_beams, S = a.splits;
+  const int W = a.beams, K = a.out_beams, S = a.most_lists;
   const int total = W * S * K;
-  // the candidates' loads first: they do not depend on the sums
+  // every load first, whether it will count or not: none depends on another's value
   float val[kPer], score[kPer];
   int32_t idx[kPer];
+  uint8_t ended[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = j * kThreads + tid;
-    idx[j] = -1, val[j] = score[j] = 0.0f;
+    idx[j] = -1, val[j] = score[j] = 0.0f, ended[j] = 0;
     if (i < total) {
-      const int w = i / (S * K), rest = i - w * S * K, row = n * W + w;
+      const int w = i / (S * K), rest = i - w * S * K, s = rest / K, row = n * W + w;
+      const Lists lists = lists_of(a, row);
       score[j] = a.scores[row];
-      if (a.finished && a.finished[row]) {
-        if (rest == 0) idx[j] = a.eos;
-      } else {
-        idx[j] = a.part_idx[static_cast<int64_t>(row) * S * K + rest];
-        val[j] = a.part_val[static_cast<int64_t>(row) * S * K + rest];
+      ended[j] = a.finished ? a.finished[row] : 0;
+      if (s < lists.count) {
+        const int64_t at = (lists.first + s) * K + (rest - s * K);
+        idx[j] = a.part_idx[at];
+        val[j] = a.part_val[at];
       }
     }
   }
 #pragma unroll 1
   for (int w = warp; w < W; w += kMergeWarps) {
     const int row = n * W + w;
-    if (a.finished && a.finished[row]) {  // its candidate is its score
-      if (lane == 0) s_max[w] = 0.0f, s_lse[w] = Sum{1.0f, 0.0f};
-      continue;
-    }
-    const float* mx = a.part_max + static_cast<int64_t>(row) * S;
-    const Sum* ps = a.part_sum + static_cast<int64_t>(row) * S;
+    const Lists lists = lists_of(a, row);
+    const bool finished = a.finished && a.finished[row];
     float m = -INFINITY;
-#pragma unroll 1
-    for (int i = lane; i < S; i += 32) m = fmaxf(m, mx[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     Sum sum;
 #pragma unroll 1
-    for (int i = lane; i < S; i += 32) {
-      Sum x = ps[i];
-      if (mx[i] != -INFINITY) x.scale(exp_below(mx[i], m));
-      sum.add(x.hi);
-      sum.lo += x.lo;
+    for (int i = lane; i < lists.count; i += 32) {
+      const float om = a.part_max[lists.first + i];
+      Sum o = a.part_sum[lists.first + i];
+      const float top = fmaxf(m, om);
+      if (m != -INFINITY) sum.scale(exp_below(m, top));
+      if (om != -INFINITY) o.scale(exp_below(om, top));
+      sum.add(o.hi);
+      sum.lo += o.lo;
+      m = top;
     }
+    float top = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (m != -INFINITY) sum.scale(exp_below(m, top));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const float hi = __shfl_down_sync(0xffffffffu, sum.hi, o), lo = __shfl_down_sync(0xffffffffu, sum.lo, o);
       sum.add(hi);
       sum.lo += lo;
     }
-    if (lane == 0) s_max[w] = m, s_lse[w] = sum;
+    // a finished beam's candidate is its score: log 1
+    if (lane == 0) s_max[w] = finished ? 0.0f : top, s_lse[w] = finished ? Sum{1.0f, 0.0f} : sum;
   }
   __syncthreads();
   if (warp == 0 && lane < W) {  // one logarithm for all beams
@@ -508,7 +603,8 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
     const int i = j * kThreads + tid;
     const int w = i / (S * K);
     mine[j] = Best{0, 0, 0x7fffffff};
-    if (idx[j] >= 0) {
+    if (ended[j]) idx[j] = i - w * S * K == 0 ? a.eos : -1, val[j] = 0.0f;
+    if (idx[j] >= 0 && i < total) {
       // score + value - lse, each sum with its rounding error
       const Sum lse = s_lse[w];
       Sum c{score[j], 0.0f};
@@ -551,15 +647,28 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
   }
 }
 
-// Blocks per row: enough for every SM to hold a few, no piece below half a batch, at most kSlots batches
-// where that fits, and no more candidates than the merge holds.
-int splits_for(int reqs, int beams, int out_beams, int vocab, int elem, int sms) {
+struct Shares {
+  int tiles, per_block, most_lists;
+  int64_t blocks, lists;
+};
+
+// One wave of blocks, all with the same number of tiles (of which rows keep boundaries: a block may hold
+// the ends of several), and no more candidates a request than the merge holds.
+Shares shares_of(int reqs, int beams, int out_beams, int vocab, int elem, int sms) {
+  Shares y{};
   const int64_t rows = static_cast<int64_t>(reqs) * beams;
-  const int64_t batch = kScanThreads * kVec * (16 / elem);
-  const int64_t want = std::max((static_cast<int64_t>(sms) * 4 + rows - 1) / rows, (vocab + batch * kSlots - 1) / (batch * kSlots));
-  const int64_t fine = (2 * static_cast<int64_t>(vocab) + batch - 1) / batch;
-  const int64_t most = kMaxCandidates / (beams * out_beams);
-  return static_cast<int>(std::max<int64_t>(1, std::min(want, std::min(fine, most))));
+  const int per_tile = kTile * (16 / elem);
+  y.tiles = (vocab + per_tile - 1) / per_tile;
+  const int64_t total = rows * y.tiles;
+  const int64_t wave = static_cast<int64_t>(sms) * kBlocksPerSm * kWaves;
+  const int most = kMaxCandidates / (beams * out_beams);  // lists of a row: at least 4
+  // a row lies in at most (tiles - 2) / per_block + 2 blocks, and in at most `tiles`
+  const int64_t least = most >= y.tiles ? 1 : (y.tiles - 2) / (most - 1) + 1;
+  y.per_block = static_cast<int>(std::max<int64_t>({(total + wave - 1) / wave, least, 1}));
+  y.most_lists = static_cast<int>(std::min<int64_t>(y.tiles, (y.tiles - 2 + y.per_block) / y.per_block + 1));
+  y.blocks = (total + y.per_block - 1) / y.per_block;
+  y.lists = y.blocks + rows;
+  return y;
 }
 
 int check(int reqs, int beams, int out_beams, int vocab, int dtype) {
@@ -574,9 +683,8 @@ int check(int reqs, int beams, int out_beams, int vocab, int dtype) {
   return DFLASH_OK;
 }
 
-size_t bytes_of(int reqs, int beams, int out_beams, int splits) {
-  const size_t lists = static_cast<size_t>(reqs) * beams * splits;
-  return 256 + lists * 12 + lists * out_beams * 8;
+size_t bytes_of(const Shares& y, int out_beams) {
+  return 256 + static_cast<size_t>(y.lists) * (12 + 8 * static_cast<size_t>(out_beams));
 }
 
 }  // namespace
@@ -590,8 +698,7 @@ size_t dflash_beam_workspace_size(int num_reqs, int beams, int beams_out, int vo
   int sms = 0;
   if (query_sms(&sms) != DFLASH_OK) return 0;
   report_error(DFLASH_OK, "");
-  return bytes_of(num_reqs, beams, beams_out,
-                  num_reqs ? splits_for(num_reqs, beams, beams_out, vocab, dtype == DFLASH_OUT_F32 ? 4 : 2, sms) : 1);
+  return bytes_of(shares_of(std::max(num_reqs, 1), beams, beams_out, vocab, dtype == DFLASH_OUT_F32 ? 4 : 2, sms), beams_out);
 }
 
 int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stride, const float* scores,
@@ -616,11 +723,11 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   rc = query_sms(&sms);
   if (rc != DFLASH_OK) return rc;
   BeamArgs a{};
-  a.splits = splits_for(num_reqs, beams, beams_out, vocab, es, sms);
-  const size_t need = bytes_of(num_reqs, beams, beams_out, a.splits);
-  if (workspace_bytes < need)
-    return errorf(DFLASH_ERR_WORKSPACE, "workspace has %zu bytes; %zu are needed", workspace_bytes, need);
-  const size_t lists = static_cast<size_t>(num_reqs) * beams * a.splits;
+  const Shares y = shares_of(num_reqs, beams, beams_out, vocab, es, sms);
+  if (workspace_bytes < bytes_of(y, beams_out))
+    return errorf(DFLASH_ERR_WORKSPACE, "workspace has %zu bytes; %zu are needed", workspace_bytes, bytes_of(y, beams_out));
+  const size_t lists = static_cast<size_t>(y.lists);
+  a.rows = num_reqs * beams, a.tiles = y.tiles, a.per_block = y.per_block, a.most_lists = y.most_lists;
   a.logits = logits, a.req_stride = req_stride, a.beam_stride = beam_stride;
   a.scores = scores, a.finished = finished;
   a.beams = beams, a.out_beams = beams_out, a.vocab = vocab, a.eos = eos;
@@ -630,14 +737,14 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   a.part_idx = reinterpret_cast<int32_t*>(a.part_val + lists * beams_out);
   a.out_scores = out_scores, a.out_tokens = out_tokens, a.out_parents = out_parents, a.out_finished = out_finished;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(lists);
+  const unsigned grid = static_cast<unsigned>(y.blocks);
   if (es == 4) beam_scan_kernel<true><<<grid, kScanThreads, 0, st>>>(a);
   else beam_scan_kernel<false><<<grid, kScanThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "beam scan launch: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(num_reqs));
-  const bool few = beams * a.splits * beams_out <= 512;
+  const bool few = beams * y.most_lists * beams_out <= 512;
   cfg.blockDim = dim3(few ? 128 : kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
