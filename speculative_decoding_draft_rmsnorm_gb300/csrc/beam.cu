@@ -36,8 +36,9 @@ constexpr int kMaxCandidates = 4096;  // per request, W * lists * K
 constexpr int kVec = 4;               // 16-byte loads a thread has in flight
 constexpr int kSlots = 16;            // maxima a thread keeps
 constexpr int kRoom = kWarps * kMaxBeams;  // candidates of a block
+constexpr int kMergeRoom = 128;            // and of a request, past the bound
 constexpr int kTile = 512;            // vectors at most: 4096 bf16 or 2048 f32 elements
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 5;
 constexpr int kWaves = 1;
 constexpr int kMaxVocab = 1 << 26;    // W * vocab < 2^31
 
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
   __shared__ float s_slot[kSlots][kScanThreads];
   __shared__ float s_val[kRoom];
   __shared__ int32_t s_idx[kRoom];
+  grid_dependents_launch();  // all blocks are resident: the merge's waiting ones take no place from them
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int K = a.out_beams;
   constexpr size_t kSize = F32 ? 4 : 2;
@@ -468,7 +470,6 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
   }
   __syncthreads();  // before the next row's piece reuses the shared arrays
   }
-  grid_dependents_launch();
 }
 
 // A score is held in two f32 terms, the first the nearest f32 to it, and compared by the order-preserving
@@ -484,14 +485,21 @@ __device__ __forceinline__ bool better(const Best& x, const Best& y) {
 __device__ __forceinline__ Best best_of_warp(const Best& b) {
   Best r;
   r.hi = __reduce_max_sync(0xffffffffu, b.hi);
-  r.lo = __reduce_max_sync(0xffffffffu, b.hi == r.hi ? b.lo : 0u);
-  r.at = __reduce_min_sync(0xffffffffu, b.hi == r.hi && b.lo == r.lo ? b.at : 0x7fffffff);
+  const uint32_t at_top = __ballot_sync(0xffffffffu, b.hi == r.hi);
+  if ((at_top & (at_top - 1)) == 0) {  // one lane alone, as a rule
+    const int src = __ffs(at_top) - 1;
+    r.lo = __shfl_sync(0xffffffffu, b.lo, src);
+    r.at = __shfl_sync(0xffffffffu, b.at, src);
+  } else {
+    r.lo = __reduce_max_sync(0xffffffffu, b.hi == r.hi ? b.lo : 0u);
+    r.at = __reduce_min_sync(0xffffffffu, b.hi == r.hi && b.lo == r.lo ? b.at : 0x7fffffff);
+  }
   return r;
 }
 
 // m + log(s.hi + s.lo) in 64 bits with few FP64 instructions: s = 2^e f, f in [2/3, 4/3), and
 // log f = 2 atanh(q), q = (f - 1) / (f + 1), |q| <= 1/5, by its series (the first term left out is below
-// 2 * 5^-23 / 23 = 8e-18).
+// 2 * 5^-19 / 19 = 6e-15).
 __device__ __forceinline__ double log_plus(float m, const Sum& s) {
   const double x = static_cast<double>(s.hi) + s.lo;
   if (!(s.hi > 0.0f) || m == -INFINITY || s.hi == INFINITY) return static_cast<double>(m) + static_cast<double>(__logf(s.hi));
@@ -502,9 +510,7 @@ __device__ __forceinline__ double log_plus(float m, const Sum& s) {
   double q = num * r;
   q = fma(r, fma(-q, den, num), q);
   const double z = q * q;
-  double p = 1.0 / 21.0;
-  p = fma(p, z, 1.0 / 19.0);
-  p = fma(p, z, 1.0 / 17.0);
+  double p = 1.0 / 17.0;
   p = fma(p, z, 1.0 / 15.0);
   p = fma(p, z, 1.0 / 13.0);
   p = fma(p, z, 1.0 / 11.0);
@@ -528,18 +534,28 @@ __device__ __forceinline__ Lists lists_of(const BeamArgs& a, int row) {
   return Lists{b0 + row, static_cast<int>(b1 - b0) + 1};
 }
 
-// One block per request: every thread holds up to kPer candidates; K rounds of a block-wide maximum.
+// One block per request: every thread holds up to kPer candidates.
 template <int kThreads, int kPer>
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
   constexpr int kMergeWarps = kThreads / 32;
+  __shared__ Lists s_lists[kMaxBeams];
+  __shared__ bool s_ended[kMaxBeams];
   __shared__ float s_max[kMaxBeams];
   __shared__ Sum s_lse[kMaxBeams];  // first the sums, then their logarithms in two terms
-  __shared__ Best s_best[2][kMergeWarps];
+  __shared__ Best s_best[2][kMergeWarps], s_list[kMergeRoom];
+  __shared__ uint32_t s_group[32];
+  __shared__ int s_count;
   grid_dependency_wait();
   const int n = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = a.beams, K = a.out_beams, S = a.most_lists;
   const int total = W * S * K;
-  // every load first, whether it will count or not: none depends on another's value
+  if (tid < W) s_lists[tid] = lists_of(a, n * W + tid);
+  if (tid < 32) s_group[tid] = 0;
+  if (tid == 0) s_count = 0;
+  __syncthreads();
+  // every load first, whether it will count or not: none depends on another's value. Candidate i is number
+  // i % K of list i / K % S of beam i / (S K); i < 2^12, so that products with a reciprocal divide exactly
+  const float per_beam = 1.0f / static_cast<float>(S * K), per_list = 1.0f / static_cast<float>(K);
   float val[kPer], score[kPer];
   int32_t idx[kPer];
   uint8_t ended[kPer];
@@ -548,8 +564,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
     const int i = j * kThreads + tid;
     idx[j] = -1, val[j] = score[j] = 0.0f, ended[j] = 0;
     if (i < total) {
-      const int w = i / (S * K), rest = i - w * S * K, s = rest / K, row = n * W + w;
-      const Lists lists = lists_of(a, row);
+      const int w = static_cast<int>((i + 0.5f) * per_beam), rest = i - w * S * K;
+      const int s = static_cast<int>((rest + 0.5f) * per_list), row = n * W + w;
+      const Lists lists = s_lists[w];
       score[j] = a.scores[row];
       ended[j] = a.finished ? a.finished[row] : 0;
       if (s < lists.count) {
@@ -562,7 +579,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
 #pragma unroll 1
   for (int w = warp; w < W; w += kMergeWarps) {
     const int row = n * W + w;
-    const Lists lists = lists_of(a, row);
+    const Lists lists = s_lists[w];
     const bool finished = a.finished && a.finished[row];
     float m = -INFINITY;
     Sum sum;
@@ -588,7 +605,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
       sum.lo += lo;
     }
     // a finished beam's candidate is its score: log 1
-    if (lane == 0) s_max[w] = finished ? 0.0f : top, s_lse[w] = finished ? Sum{1.0f, 0.0f} : sum;
+    if (lane == 0) s_max[w] = finished ? 0.0f : top, s_lse[w] = finished ? Sum{1.0f, 0.0f} : sum, s_ended[w] = finished;
   }
   __syncthreads();
   if (warp == 0 && lane < W) {  // one logarithm for all beams
@@ -601,7 +618,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = j * kThreads + tid;
-    const int w = i / (S * K);
+    const int w = min(W - 1, static_cast<int>((i + 0.5f) * per_beam));
     mine[j] = Best{0, 0, 0x7fffffff};
     if (ended[j]) idx[j] = i - w * S * K == 0 ? a.eos : -1, val[j] = 0.0f;
     if (idx[j] >= 0 && i < total) {
@@ -622,8 +639,56 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
       }
     }
   }
+  auto write = [&](int k, const Best& b) {
+    const int64_t o = static_cast<int64_t>(n) * K + k;
+    const bool none = b.hi == 0;
+    const int w = none ? 0 : b.at / a.vocab, t = none ? -1 : b.at - w * a.vocab;
+    a.out_scores[o] = none ? -INFINITY : from_key(b.hi);
+    a.out_tokens[o] = t;
+    a.out_parents[o] = none ? -1 : n * W + w;
+    a.out_finished[o] = !none && (t == a.eos || s_ended[w]);
+  };
+  // As in the scan: the K-th largest of 32 groups' maxima is a bound, and what reaches it is ranked.
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) top = max(top, mine[j].hi);
+  if (top) atomicMax(&s_group[lane], top);
+  __syncthreads();
+  {
+    const uint32_t v = s_group[lane];
+    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t o = s_group[i];
+      rank += o > v || (o == v && i < lane);
+    }
+    top = __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, rank == K - 1)) - 1);
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (mine[j].hi && mine[j].hi >= top) {
+      const int c = atomicAdd(&s_count, 1);
+      if (c < kMergeRoom) s_list[c] = mine[j];
+    }
+  }
+  __syncthreads();
+  const int count = s_count;
+  if (count <= kMergeRoom) {
+    for (int c = tid; c < max(count, K); c += kThreads) {
+      if (c >= count) {  // fewer candidates than beams
+        write(c, Best{0, 0, 0});
+        continue;
+      }
+      const Best b = s_list[c];
+      int rank = 0;
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) rank += better(s_list[i], b);
+      if (rank < K) write(rank, b);
+    }
+    return;
+  }
 #pragma unroll 1
-  for (int k = 0; k < K; ++k) {
+  for (int k = 0; k < K; ++k) {  // too many for that: a maximum over the block each
     Best b = mine[0];
 #pragma unroll
     for (int j = 1; j < kPer; ++j)
@@ -632,18 +697,10 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
     if (lane == 0) s_best[k & 1][warp] = b;
     __syncthreads();  // the other buffer is read before the next round's barrier
     b = best_of_warp(s_best[k & 1][lane < kMergeWarps ? lane : 0]);
-    const bool none = b.hi == 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
       if (mine[j].at == b.at) mine[j].hi = mine[j].lo = 0;
-    if (tid == 0) {
-      const int64_t o = static_cast<int64_t>(n) * K + k;
-      const int w = none ? 0 : b.at / a.vocab, t = none ? -1 : b.at - w * a.vocab;
-      a.out_scores[o] = none ? -INFINITY : from_key(b.hi);
-      a.out_tokens[o] = t;
-      a.out_parents[o] = none ? -1 : n * W + w;
-      a.out_finished[o] = !none && (t == a.eos || (a.finished && a.finished[n * W + w]));
-    }
+    if (tid == 0) write(k, b);
   }
 }
 
@@ -745,14 +802,14 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(num_reqs));
   const bool few = beams * y.most_lists * beams_out <= 512;
-  cfg.blockDim = dim3(few ? 128 : kMergeThreads);
+  cfg.blockDim = dim3(few ? 256 : kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = few ? cudaLaunchKernelEx(&cfg, beam_merge_kernel<128, 4>, a)
+  e = few ? cudaLaunchKernelEx(&cfg, beam_merge_kernel<256, 2>, a)
           : cudaLaunchKernelEx(&cfg, beam_merge_kernel<kMergeThreads, kMaxCandidates / kMergeThreads>, a);
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "beam merge launch: %s", cudaGetErrorString(e));
   return report_error(DFLASH_OK, "");
