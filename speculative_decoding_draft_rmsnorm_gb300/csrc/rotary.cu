@@ -13,14 +13,16 @@
 // set of pairs of one token and walks over heads with it, so that each angle is computed once per
 // `head group` instead of once per head, and nothing is staged in shared memory.
 //
-// A thread's elements are two chunks of E: [uE, uE + E) and [rd/2 + uE, rd/2 + uE + E), each one load
+// A rotating thread's elements are two chunks of E: [uE, uE + E) and [rd/2 + uE, rd/2 + uE + E), each one load
 // of up to 16 bytes; lanes of consecutive u cover consecutive chunks. Both layouts use the same two
 // chunks: the half layout pairs them with each other, the interleaved one pairs neighbours inside
 // each. E is the largest power of two that divides rd/2 and the rest of the head and that the
 // pointers' and strides' alignment allows, so odd sizes run the same code with narrower accesses.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "../../include/dflash.h"
 #include "internal.h"
@@ -31,7 +33,7 @@ namespace dflash {
 namespace {
 
 constexpr int kMaxPairs = 128;  // rotary_dim <= 256
-constexpr int kUnroll = 4;      // heads whose loads a thread has in flight
+constexpr int kUnroll = 2;      // heads whose loads a thread has in flight
 constexpr int kThreads = 256;
 
 struct RotaryTensor {
@@ -44,9 +46,11 @@ struct RotaryArgs {
   RotaryTensor t[3];  // q, k, v
   int hq, hkv, hv;    // heads of each (hv = 0: no v)
   int64_t n;
-  int units, rot_units;  // units per head; those below rot_units rotate, the rest are copied
-  int rd, dh, groups;    // groups = threads (of one unit) that share a token's heads
-  int q_pass, k_pass;    // whether the copied units have to be written (not in place)
+  // Threads of a token: `groups` share its heads in each range. Rotating: rot_units chunk pairs of the q and
+  // k heads; copying: tail_units chunks of their elements behind rd, v_units chunks of the v heads.
+  int rot_units, tail_units, v_units, groups;
+  int tail_bytes, v_bytes;  // of a copied chunk
+  int rd;
   const int32_t* pos;
   const int32_t* slot;  // k and v rows go to row slot[t] of their destination
   int64_t capacity;
@@ -54,6 +58,35 @@ struct RotaryArgs {
   uint32_t* err;
   float hi[kMaxPairs], lo[kMaxPairs];  // turns per position, head and tail
 };
+
+// Copies a chunk of heads h, h + step, .. below end of one tensor, kUnroll loads in flight.
+template <typename W>
+__device__ __forceinline__ void copy_heads(const char* src, char* dst, int64_t src_step, int64_t dst_step, int h, int end, int step) {
+#pragma unroll 1
+  for (; h < end; h += step * kUnroll) {
+    W x[kUnroll];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+      if (h + j * step < end) x[j] = *reinterpret_cast<const W*>(src + (h + j * step) * src_step);
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+      if (h + j * step < end) *reinterpret_cast<W*>(dst + (h + j * step) * dst_step) = x[j];
+  }
+}
+
+// Chunk u, of `bytes` bytes from byte `from` on, of all heads of a tensor's row.
+__device__ __forceinline__ void copy_chunk(const RotaryTensor& x, int64_t src_row, int64_t dst_row, int heads, int es, int64_t from, int u,
+                                           int bytes, int g, int groups) {
+  const char* src = static_cast<const char*>(x.src) + src_row * x.src_tok * es + from + static_cast<int64_t>(u) * bytes;
+  char* dst = static_cast<char*>(x.dst) + dst_row * x.dst_tok * es + from + static_cast<int64_t>(u) * bytes;
+  const int64_t ss = x.src_head * es, ds = x.dst_head * es;
+  switch (bytes) {
+    case 16: return copy_heads<uint4>(src, dst, ss, ds, g, heads, groups);
+    case 8: return copy_heads<uint2>(src, dst, ss, ds, g, heads, groups);
+    case 4: return copy_heads<uint32_t>(src, dst, ss, ds, g, heads, groups);
+    default: return copy_heads<uint16_t>(src, dst, ss, ds, g, heads, groups);
+  }
+}
 
 template <typename T, int E>
 struct Chunk {  // E elements, moved with one access
@@ -114,12 +147,10 @@ __device__ __forceinline__ Chunk<T, E> pack_chunk(const float (&x)[E]) {
 template <typename T, bool INTER, int E>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int per_token = a.units * a.groups;
+  const int rot = a.rot_units * a.groups, tail = a.tail_units * a.groups, per_token = rot + tail + a.v_units * a.groups;
   const int64_t t = item / per_token;
   if (t >= a.n) return;
-  const int rest = static_cast<int>(item - t * per_token);
-  const int g = rest / a.units, u = rest - g * a.units;
-  const bool rotates = u < a.rot_units;
+  int rest = static_cast<int>(item - t * per_token);
   // where k and v of this token go
   int64_t row = t;
   bool stored = true;
@@ -128,13 +159,29 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     stored = row >= 0 && row < a.capacity;
     if (row >= a.capacity && rest == 0 && a.err) atomicOr(a.err, kErrMetadata);
   }
-  // this unit's elements: two chunks that rotate, or one that is copied
+  if (rest >= rot) {  // a copied chunk
+    rest -= rot;
+    if (rest < tail) {
+      const int g = rest / a.tail_units, u = rest - g * a.tail_units;
+      const int64_t from = static_cast<int64_t>(a.rd) * sizeof(T);
+      if (a.hq && a.t[0].src != a.t[0].dst) copy_chunk(a.t[0], t, t, a.hq, sizeof(T), from, u, a.tail_bytes, g, a.groups);
+      if (a.hkv && a.t[1].src != a.t[1].dst && stored)
+        copy_chunk(a.t[1], t, row, a.hkv, sizeof(T), from, u, a.tail_bytes, g, a.groups);
+    } else if (stored) {
+      rest -= tail;
+      const int g = rest / a.v_units, u = rest - g * a.v_units;
+      copy_chunk(a.t[2], t, row, a.hv, sizeof(T), 0, u, a.v_bytes, g, a.groups);
+    }
+    return;
+  }
+  const int g = rest / a.rot_units, u = rest - g * a.rot_units;
+  // this unit's elements: two chunks
   const bool pairwise = INTER && E == 1;  // one pair of neighbours
-  const int e0 = rotates ? (pairwise ? 2 * u : u * E) : a.rd + (u - a.rot_units) * E;
-  const int e1 = rotates ? (pairwise ? 2 * u + 1 : a.rd / 2 + u * E) : e0;
+  const int e0 = pairwise ? 2 * u : u * E;
+  const int e1 = pairwise ? 2 * u + 1 : a.rd / 2 + u * E;
 
   float cs[E], sn[E];
-  if (rotates) {
+  {
     const int p = a.pos[t];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -145,7 +192,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       sn[e] *= a.amp * a.sin_sign;
     }
   }
-  const int turned = a.hq + a.hkv, total = turned + a.hv;
+  const int total = a.hq + a.hkv;
+#pragma unroll 1
   for (int h0 = g; h0 < total; h0 += a.groups * kUnroll) {
     Chunk<T, E> x[kUnroll], y[kUnroll];
     T* dst[kUnroll];
@@ -153,54 +201,46 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     for (int j = 0; j < kUnroll; ++j) {
       const int h = h0 + j * a.groups;
       dst[j] = nullptr;
-      if (h < total) {
-        const int which = h < a.hq ? 0 : h < turned ? 1 : 2;
-        const int head = h - (which == 0 ? 0 : which == 1 ? a.hq : turned);
-        const RotaryTensor& X = a.t[which];
-        const bool write = which == 0 ? (rotates || a.q_pass) : (stored && (which == 2 || rotates || a.k_pass));
-        if (write) {
-          const T* src = static_cast<const T*>(X.src) + t * X.src_tok + head * X.src_head;
-          dst[j] = static_cast<T*>(X.dst) + (which == 0 ? t : row) * X.dst_tok + head * X.dst_head;
-          x[j] = load_chunk<T, E>(src + e0);
-          if (rotates) y[j] = load_chunk<T, E>(src + e1);
-        }
+      if (h < total && (h < a.hq || stored)) {
+        const RotaryTensor& X = a.t[h < a.hq ? 0 : 1];
+        const int head = h < a.hq ? h : h - a.hq;
+        const T* src = static_cast<const T*>(X.src) + t * X.src_tok + head * X.src_head;
+        dst[j] = static_cast<T*>(X.dst) + (h < a.hq ? t : row) * X.dst_tok + head * X.dst_head;
+        x[j] = load_chunk<T, E>(src + e0);
+        y[j] = load_chunk<T, E>(src + e1);
       }
     }
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
       if (!dst[j]) continue;
-      if (rotates && h0 + j * a.groups < turned) {
-        float p[E], q[E];
-        if constexpr (!INTER || E == 1) {
+      float p[E], q[E];
+      if constexpr (!INTER || E == 1) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float c = element<T, E>(x[j], e), d = element<T, E>(y[j], e);
-            p[e] = fmaf(-d, sn[e], c * cs[e]);
-            q[e] = fmaf(c, sn[e], d * cs[e]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            const float c = element<T, E>(x[j], 2 * e), d = element<T, E>(x[j], 2 * e + 1);
-            p[2 * e] = fmaf(-d, sn[e], c * cs[e]);
-            p[2 * e + 1] = fmaf(c, sn[e], d * cs[e]);
-            const float v = element<T, E>(y[j], 2 * e), w = element<T, E>(y[j], 2 * e + 1);
-            q[2 * e] = fmaf(-w, sn[E / 2 + e], v * cs[E / 2 + e]);
-            q[2 * e + 1] = fmaf(v, sn[E / 2 + e], w * cs[E / 2 + e]);
-          }
+        for (int e = 0; e < E; ++e) {
+          const float c = element<T, E>(x[j], e), d = element<T, E>(y[j], e);
+          p[e] = fmaf(-d, sn[e], c * cs[e]);
+          q[e] = fmaf(c, sn[e], d * cs[e]);
         }
-        x[j] = pack_chunk<T, E>(p);
-        y[j] = pack_chunk<T, E>(q);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const float c = element<T, E>(x[j], 2 * e), d = element<T, E>(x[j], 2 * e + 1);
+          p[2 * e] = fmaf(-d, sn[e], c * cs[e]);
+          p[2 * e + 1] = fmaf(c, sn[e], d * cs[e]);
+          const float v = element<T, E>(y[j], 2 * e), w = element<T, E>(y[j], 2 * e + 1);
+          q[2 * e] = fmaf(-w, sn[E / 2 + e], v * cs[E / 2 + e]);
+          q[2 * e + 1] = fmaf(v, sn[E / 2 + e], w * cs[E / 2 + e]);
+        }
       }
-      store_chunk<T, E>(dst[j] + e0, x[j]);
-      if (rotates) store_chunk<T, E>(dst[j] + e1, y[j]);
+      store_chunk<T, E>(dst[j] + e0, pack_chunk<T, E>(p));
+      store_chunk<T, E>(dst[j] + e1, pack_chunk<T, E>(q));
     }
   }
 }
 
 template <typename T, bool INTER, int E>
 void launch(const RotaryArgs& a, cudaStream_t st) {
-  const int64_t items = a.n * a.units * a.groups;
+  const int64_t items = a.n * (a.rot_units + a.tail_units + a.v_units) * a.groups;
   rotary_kernel<T, INTER, E><<<static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
 }
 
@@ -261,29 +301,37 @@ extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void*
   a.t[1] = RotaryTensor{k, k_out, k_tok, k_head, k_out_tok, k_out_head};
   a.t[2] = RotaryTensor{v, v_out, v_tok, v_head, v_out_tok, v_out_head};
   const int heads[3] = {hq, hkv, v ? hkv : 0};
-  // the widest access that sizes, strides and pointers allow; single elements always work
-  int e = static_cast<int>(16 / es);
-  for (; e > 1; e /= 2) {
-    bool ok = (rotary_dim / 2) % e == 0 && (dh - rotary_dim) % e == 0;
-    for (int i = 0; i < 3 && ok; ++i) {
-      if (!heads[i]) continue;
-      const RotaryTensor& X = a.t[i];
-      const bool head_ok = heads[i] == 1 || (X.src_head % e == 0 && X.dst_head % e == 0);
-      const bool tok_ok = (n == 1 && !slot) || (X.src_tok % e == 0 && X.dst_tok % e == 0);
-      ok = head_ok && tok_ok && reinterpret_cast<uintptr_t>(X.src) % (e * es) == 0 &&
-           reinterpret_cast<uintptr_t>(X.dst) % (e * es) == 0;
+  // the widest access that the strides and pointers of tensors [from, to) allow, and that divides every one
+  // of `parts`; single elements always work
+  auto widest = [&](int from, int to, std::initializer_list<int> parts) {
+    int e = static_cast<int>(16 / es);
+    for (; e > 1; e /= 2) {
+      bool ok = true;
+      for (int x : parts) ok &= x % e == 0;
+      for (int i = from; i < to && ok; ++i) {
+        if (!heads[i]) continue;
+        const RotaryTensor& X = a.t[i];
+        const bool head_ok = heads[i] == 1 || (X.src_head % e == 0 && X.dst_head % e == 0);
+        const bool tok_ok = (n == 1 || X.src_tok % e == 0) && ((n == 1 && !(slot && i)) || X.dst_tok % e == 0);
+        ok = head_ok && tok_ok && reinterpret_cast<uintptr_t>(X.src) % (e * es) == 0 &&
+             reinterpret_cast<uintptr_t>(X.dst) % (e * es) == 0;
+      }
+      if (ok) break;
     }
-    if (ok) break;
-  }
+    return e;
+  };
   for (int i = 0; i < 3; ++i)
     if (heads[i] && (reinterpret_cast<uintptr_t>(a.t[i].src) % es || reinterpret_cast<uintptr_t>(a.t[i].dst) % es))
       return errorf(DFLASH_ERR_INVALID_ARG, "tensor pointers must be aligned to their elements");
   a.hq = heads[0], a.hkv = heads[1], a.hv = heads[2];
   a.n = n;
-  a.rd = rotary_dim, a.dh = dh;
+  a.rd = rotary_dim;
+  const int e = widest(0, 2, {rotary_dim / 2}), te = widest(0, 2, {rotary_dim, dh - rotary_dim}), ve = widest(2, 3, {dh});
+  const bool tails = (hq && q != q_out) || (hkv && k != k_out);  // in place they are where they belong
   a.rot_units = rotary_dim / 2 / e;
-  a.units = a.rot_units + (dh - rotary_dim) / e;
-  a.q_pass = q != q_out, a.k_pass = k != k_out;
+  a.tail_units = tails ? (dh - rotary_dim) / te : 0;
+  a.v_units = a.hv ? dh / ve : 0;
+  a.tail_bytes = static_cast<int>(te * es), a.v_bytes = static_cast<int>(ve * es);
   a.pos = positions, a.slot = slot, a.capacity = capacity;
   a.amp = static_cast<float>(amplitude), a.sin_sign = inverse ? -1.0f : 1.0f;
   a.err = reinterpret_cast<uint32_t*>(status);
@@ -297,12 +345,10 @@ extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void*
   if (rc != DFLASH_OK) return rc;
   // Threads that share a token's heads: as few as keep the GPU full, since each computes the angles
   // anew; never more than one head a thread.
-  const int total = a.hq + a.hkv + a.hv;
-  const int64_t want = static_cast<int64_t>(sms) * 2048, have = n * a.units;
-  int64_t groups = (want + have - 1) / have;
-  const int most = total;
-  a.groups = static_cast<int>(groups < 1 ? 1 : groups > most ? most : groups);
-  const int64_t items = n * a.units * a.groups;
+  const int64_t want = static_cast<int64_t>(sms) * 2048, have = n * (a.rot_units + a.tail_units + a.v_units);
+  const int64_t groups = (want + have - 1) / have;
+  a.groups = static_cast<int>(std::min<int64_t>(groups, a.hq + a.hkv));
+  const int64_t items = have * a.groups;
   if ((items + kThreads - 1) / kThreads > 0x7fffffff)
     return errorf(DFLASH_ERR_UNSUPPORTED, "too many rows for one call (%lld)", static_cast<long long>(n));
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -133,14 +133,14 @@ def _rows(name, t, dims):
     return st
 
 
-def _scratch(workspace, nbytes, index):
+def _scratch(workspace, nbytes, index, dev):
     """(tensor, address, bytes) of a call's workspace: the given one, or a new one of nbytes()."""
     if workspace is None:
         n = nbytes()
         if n == 0:
             _fail(_base().ERR_INVALID_ARG)
-        workspace = _torch.empty(n, dtype=_torch.uint8, device=index)
-    return workspace, _ptr("workspace", workspace, _torch.uint8, None, index), workspace.numel()
+        workspace = _torch.empty(n, dtype=_torch.uint8, device=dev)
+    return workspace, _ptr("workspace", workspace, _torch.uint8, None, index, dev), workspace.numel()
 
 
 # ------------------------------------------------------------------------------------- rotary
@@ -196,7 +196,7 @@ def rotary(q, positions, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_
     first = q if q is not None else k
     if first is None:
         raise ValueError("pass q, k or both")
-    index, dtype, i32 = _device(first), first.dtype, _torch.int32
+    index, dev, dtype, i32 = _device(first), first.device, first.dtype, _torch.int32
     if dtype is _torch.bfloat16:
         code = OUT_BF16
     elif dtype is _torch.float32:
@@ -220,7 +220,7 @@ def rotary(q, positions, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_
             a += (None, 0, 0, None, 0, 0, 0)
         else:
             if q_out is None:
-                q_out = _torch.empty(q.shape, dtype=dtype, device=index)
+                q_out = _torch.empty(q.shape, dtype=dtype, device=dev)
             st, so = q.stride(), _rows("q_out", q_out, 3)
             a += (q.data_ptr(), st[0], st[1], _ptr("q_out", q_out, dtype, q.shape, index, False), so[0], so[1], q.shape[1])
         if k is None:
@@ -231,7 +231,7 @@ def rotary(q, positions, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_
             if ks[0] != n or ks[2] != dh:
                 raise ValueError("k must be [n, Hkv, Dh] like q")
             if k_out is None:
-                k_out = _torch.empty(ks, dtype=dtype, device=index)
+                k_out = _torch.empty(ks, dtype=dtype, device=dev)
             ko = _store_rows("k_out", k_out, ks, slot is None)
             capacity, so = ko.shape[0], ko.stride()
             a += (_ptr("k", k, dtype, None, index, False), st[0], st[1], _ptr("k_out", ko, dtype, None, index, False), so[0], so[1],
@@ -246,11 +246,15 @@ def rotary(q, positions, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_
                 raise ValueError("v_out must have as many rows as k_out")
             a += (_ptr("v", v, dtype, k.shape, index, False), st[0], st[1], _ptr("v_out", vo, dtype, None, index, False), so[0], so[1])
         rc = lib.dflash_rotary(*a, _ptr("positions", positions, i32, (n,), index), _ptr("slot", slot, i32, (n,), index), n, capacity,
-                               dh, 2 * freq.shape[0], freq.ctypes.data, amplitude, 1 if interleaved else 0, 1 if inverse else 0, code,
+                               dh, 2 * freq.shape[0], _address(freq), amplitude, 1 if interleaved else 0, 1 if inverse else 0, code,
                                _ptr("status", status, i32, (1,), index), handle)
         if rc:
             _fail(rc)
     return q_out, k_out
+
+
+def _address(a):
+    return a.__array_interface__["data"][0]
 
 
 def _store_rows(name, t, like, dense):
@@ -282,7 +286,7 @@ def decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, *, max_ctx_
     zeros and -inf. max_ctx_len bounds the lengths (grid and workspace size only).
     """
     lib = _lib or _load()
-    index, bf16, i32 = _device(q), _torch.bfloat16, _torch.int32
+    index, dev, bf16, i32 = _device(q), q.device, _torch.bfloat16, _torch.int32
     sq = _rows("q", q, 3)
     n, hq, dh = q.shape
     if k_pool.dim() != 4 or block_table.dim() != 2:
@@ -303,11 +307,11 @@ def decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, *, max_ctx_
     p_l = _ptr("seq_lens", seq_lens, i32, (n,), index)
     with _On(index, stream) as handle:
         if out is None:
-            out = _torch.empty((n, hq, dh), dtype=odt, device=index)
+            out = _torch.empty((n, hq, dh), dtype=odt, device=dev)
         if lse is None and return_lse:
-            lse = _torch.empty((n, hq), dtype=_torch.float32, device=index)
+            lse = _torch.empty((n, hq), dtype=_torch.float32, device=dev)
         workspace, p_w, w_bytes = _scratch(
-            workspace, lambda: lib.dflash_decode_workspace_size(n, hq, hkv, dh, max_ctx_len, window), index)
+            workspace, lambda: lib.dflash_decode_workspace_size(n, hq, hkv, dh, max_ctx_len, window), index, dev)
         rc = lib.dflash_decode_attention_paged(
             p_q, sq[0] if n > 1 else hq * dh, p_k, p_v, p_t, stb[0] if n > 1 else width, p_l, n, hq, hkv, dh, pages, page, width,
             max_ctx_len, scale, window, out_dtype, _ptr("out", out, odt, (n, hq, dh), index),
@@ -331,7 +335,7 @@ def beam_select(logits, scores, *, beams_out=None, finished=None, eos=-1, out=No
     `out` may hold preallocated outputs, e.g. for graph capture.
     """
     lib = _lib or _load()
-    index, f32, i32, flag = _device(logits), _torch.float32, _torch.int32, _torch.bool
+    index, dev, f32, i32, flag = _device(logits), logits.device, _torch.float32, _torch.int32, _torch.bool
     st = _rows("logits", logits, 3)
     n, w, vocab = logits.shape
     k = w if beams_out is None else int(beams_out)
@@ -352,11 +356,11 @@ def beam_select(logits, scores, *, beams_out=None, finished=None, eos=-1, out=No
         for name, dt in zip(BEAM_OUTPUTS, (f32, i32, i32, flag)):
             t = out.get(name)
             if t is None:
-                t = out[name] = _torch.empty(shape, dtype=dt, device=index)
+                t = out[name] = _torch.empty(shape, dtype=dt, device=dev)
                 ptr.append(t.data_ptr())
             else:
                 ptr.append(_ptr(name, t, dt, shape, index))
-        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_beam_workspace_size(n, w, k, vocab, code), index)
+        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_beam_workspace_size(n, w, k, vocab, code), index, dev)
         rc = lib.dflash_beam_select(logits.data_ptr(), st[0], st[1], p_s, p_f, n, w, k, vocab, eos, code, *ptr, p_w, w_bytes, handle)
         if rc:
             _fail(rc)
@@ -415,7 +419,7 @@ def fork_pages(parent, seq_lens, block_table, page_refs, *, status=None, stream=
     is copied: reserve_pages gives a row its own copy of a shared page before it is written.
     """
     lib = _lib or _load()
-    index, i32 = _device(block_table), _torch.int32
+    index, dev, i32 = _device(block_table), block_table.device, _torch.int32
     n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
     if parent.dim() > 1:
         parent = parent.view(-1)
@@ -437,7 +441,7 @@ def reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, *, num
     adds the new rows to seq_lens. page_size is needed only with an empty list of pools.
     """
     lib = _lib or _load()
-    index, i32 = _device(block_table), _torch.int32
+    index, dev, i32 = _device(block_table), block_table.device, _torch.int32
     n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
     arr, count, page_bytes, page = _pools(pools, pages, index)
     if page is None:
@@ -451,10 +455,10 @@ def reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, *, num
         raise ValueError("num_new must be >= 0")
     with _On(index, stream) as handle:
         if slots is None:
-            slots = _torch.empty(num_new, dtype=i32, device=index)
+            slots = _torch.empty(num_new, dtype=i32, device=dev)
         if positions is None:
-            positions = _torch.empty(num_new, dtype=i32, device=index)
-        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index)
+            positions = _torch.empty(num_new, dtype=i32, device=dev)
+        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index, dev)
         rc = lib.dflash_reserve_pages(
             _ptr("new_start_loc", new_start_loc, i32, (n + 1,), index), _ptr("seq_lens", seq_lens, i32, (n,), index), p_t, stride, p_r,
             arr, count, page_bytes, n, num_new, width, page, pages, 1 if advance else 0,
@@ -471,13 +475,13 @@ def compact_pages(block_table, page_refs, pools, *, used=None, workspace=None, s
     Returns `used`, an int32 device word: the number of pages in use, which are now the first ones.
     """
     lib = _lib or _load()
-    index, i32 = _device(block_table), _torch.int32
+    index, dev, i32 = _device(block_table), block_table.device, _torch.int32
     n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
     arr, count, page_bytes, _ = _pools(pools, pages, index)
     with _On(index, stream) as handle:
         if used is None:
-            used = _torch.empty(1, dtype=i32, device=index)
-        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index)
+            used = _torch.empty(1, dtype=i32, device=dev)
+        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index, dev)
         rc = lib.dflash_compact_pages(p_t, stride, p_r, arr, count, page_bytes, n, width, pages,
                                       _ptr("used", used, i32, (1,), index), p_w, w_bytes, _ptr("status", status, i32, (1,), index),
                                       handle)
