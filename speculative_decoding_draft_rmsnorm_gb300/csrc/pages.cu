@@ -388,6 +388,7 @@ struct CompactArgs {
   int32_t* from;    // [k] the k-th used page at or behind the number of used pages
   int32_t* to;      // [k] the k-th free page before it
   int32_t* rank;    // [num_pages] k of such a used page
+  int32_t* moved;   // how many there are
 };
 
 __global__ void __launch_bounds__(kThreads) compact_count_kernel(const __grid_constant__ CompactArgs a) {
@@ -410,6 +411,7 @@ __global__ void __launch_bounds__(kThreads) compact_rank_kernel(const __grid_con
   for (int i = threadIdx.x; i < at; i += kThreads) part += a.counts[i];
   for (int64_t i = static_cast<int64_t>(at) * a.chunk + threadIdx.x; i < all; i += kThreads) part += a.refs[i] != 0;
   const int below = block_sum(part);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.moved = all - below;
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk, hi = min(lo + a.chunk, a.num_pages);
   for (int64_t i0 = lo; i0 < hi; i0 += kThreads) {
     const int64_t i = i0 + threadIdx.x;
@@ -434,15 +436,7 @@ __global__ void __launch_bounds__(kThreads) compact_apply_kernel(const __grid_co
                                                                  int meta) {
   grid_dependency_wait();
   const int64_t all = *a.used;
-  int moved = 0;  // holes before `all` = all - used pages before it; counted where a mover exists
-  {
-    // movers are the used pages at or behind `all`; their number ends the list `from`
-    const int at = min(static_cast<int>(all / a.chunk), a.chunks - 1);
-    for (int i = at + 1 + threadIdx.x; i < a.chunks; i += kThreads) moved += a.counts[i];
-    const int64_t end = min((static_cast<int64_t>(at) + 1) * a.chunk, a.num_pages);
-    for (int64_t i = all + threadIdx.x; i < end; i += kThreads) moved += a.rank[i] >= 0;
-    moved = block_sum(moved);
-  }
+  const int moved = *a.moved;
   if (static_cast<int>(blockIdx.x) < meta) {
     const int64_t cells = static_cast<int64_t>(a.rows) * a.width, step = static_cast<int64_t>(meta) * kThreads;
     bool bad = false;
@@ -662,6 +656,8 @@ int dflash_compact_pages(int32_t* block_table, int64_t block_table_stride, int32
   const size_t pages = up(static_cast<size_t>(num_pages) * 4);
   a.counts = reinterpret_cast<int32_t*>(ws);
   ws += up(kMaxChunks * 4);
+  a.moved = reinterpret_cast<int32_t*>(ws);
+  ws += 256;
   a.from = reinterpret_cast<int32_t*>(ws);
   a.to = reinterpret_cast<int32_t*>(ws + pages);
   a.rank = reinterpret_cast<int32_t*>(ws + 2 * pages);
@@ -672,7 +668,7 @@ int dflash_compact_pages(int32_t* block_table, int64_t block_table_stride, int32
   if (e == cudaSuccess) {
     const int64_t cells = static_cast<int64_t>(num_reqs) * max_pages_per_req;
     const int meta = static_cast<int>(std::min<int64_t>(sms, std::max<int64_t>(1, (std::max(cells, num_pages) + 2047) / 2048)));
-    const unsigned copies = num_pools ? static_cast<unsigned>(sms) * 8 : 0;
+    const unsigned copies = num_pools ? static_cast<unsigned>(sms) * 32 : 0;
     e = launch_after(compact_apply_kernel, static_cast<unsigned>(meta) + copies, st, a, p, page_bytes, meta);
   }
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "compact launch: %s", cudaGetErrorString(e));

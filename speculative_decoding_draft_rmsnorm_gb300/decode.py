@@ -49,17 +49,18 @@ def _base():
     return pkg
 
 
-_torch = _lib = _raw_stream = None
+_torch = _lib = _raw_stream = _current_device = None
 
 
 def _load():
     """The library's handle; the first call also brings in torch."""
-    global _torch, _lib, _raw_stream
+    global _torch, _lib, _raw_stream, _current_device
     import torch
     _torch = torch
     # the current stream's handle without building a Stream object (1 us less), where torch has it
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = torch.cuda.current_device
     _lib = _base().load()
     return _lib
 
@@ -94,29 +95,12 @@ def _ptr(name, t, dtype, shape, index, contiguous=True):
     raise ValueError(f"{name} must be contiguous")
 
 
-class _On:
-    """Where a call runs: `handle` is its stream; inside the context the device is current, and what is
-    allocated belongs to that stream (nothing is entered when both already hold)."""
-
-    __slots__ = ("handle", "guard")
-
-    def __init__(self, index, stream):
-        if stream is None:
-            self.handle = _raw_stream(index)
-            self.guard = None if _torch.cuda.current_device() == index else _torch.cuda.device(index)
-        else:
-            s = stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(int(stream), device=index)
-            self.handle = s.cuda_stream
-            self.guard = _torch.cuda.stream(s)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _elsewhere(index, stream):
+    """The context that a call has to enter first, so that the device is current and its current stream the
+    one asked for (what is allocated then belongs to it); None where both already hold."""
+    if stream is None:
+        return None if _current_device() == index else _torch.cuda.device(index)
+    return _torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(int(stream), device=index))
 
 
 def _fail(rc):
@@ -197,6 +181,11 @@ def rotary(q, positions, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_
     if first is None:
         raise ValueError("pass q, k or both")
     index, dev, dtype, i32 = _device(first), first.device, first.dtype, _torch.int32
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return rotary(q, positions, inv_freq, k=k, v=v, q_out=q_out, k_out=k_out, v_out=v_out, slot=slot, amplitude=amplitude,
+                          interleaved=interleaved, inverse=inverse, status=status)
     if dtype is _torch.bfloat16:
         code = OUT_BF16
     elif dtype is _torch.float32:
@@ -214,47 +203,42 @@ def rotary(q, positions, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_
         raise ValueError("slot needs k and k_out")
     _rows("q" if q is not None else "k", first, 3)
     n, _, dh = first.shape
-    with _On(index, stream) as handle:
-        a, capacity = [], n
-        if q is None:
-            a += (None, 0, 0, None, 0, 0, 0)
-        else:
-            if q_out is None:
-                q_out = _torch.empty(q.shape, dtype=dtype, device=dev)
-            st, so = q.stride(), _rows("q_out", q_out, 3)
-            a += (q.data_ptr(), st[0], st[1], _ptr("q_out", q_out, dtype, q.shape, index, False), so[0], so[1], q.shape[1])
-        if k is None:
-            a += (None, 0, 0, None, 0, 0, 0)
-        else:
-            st, ks = _rows("k", k, 3), k.shape
-            hkv = ks[1]
-            if ks[0] != n or ks[2] != dh:
-                raise ValueError("k must be [n, Hkv, Dh] like q")
-            if k_out is None:
-                k_out = _torch.empty(ks, dtype=dtype, device=dev)
-            ko = _store_rows("k_out", k_out, ks, slot is None)
-            capacity, so = ko.shape[0], ko.stride()
-            a += (_ptr("k", k, dtype, None, index, False), st[0], st[1], _ptr("k_out", ko, dtype, None, index, False), so[0], so[1],
-                  hkv)
-        if v is None:
-            a += (None, 0, 0, None, 0, 0)
-        else:
-            st = _rows("v", v, 3)
-            vo = _store_rows("v_out", v_out, k.shape, slot is None)
-            so = vo.stride()
-            if vo.shape[0] != capacity:
-                raise ValueError("v_out must have as many rows as k_out")
-            a += (_ptr("v", v, dtype, k.shape, index, False), st[0], st[1], _ptr("v_out", vo, dtype, None, index, False), so[0], so[1])
-        rc = lib.dflash_rotary(*a, _ptr("positions", positions, i32, (n,), index), _ptr("slot", slot, i32, (n,), index), n, capacity,
-                               dh, 2 * freq.shape[0], _address(freq), amplitude, 1 if interleaved else 0, 1 if inverse else 0, code,
-                               _ptr("status", status, i32, (1,), index), handle)
-        if rc:
-            _fail(rc)
+    a, capacity = [], n
+    if q is None:
+        a += (None, 0, 0, None, 0, 0, 0)
+    else:
+        if q_out is None:
+            q_out = _torch.empty(q.shape, dtype=dtype, device=dev)
+        st, so = q.stride(), _rows("q_out", q_out, 3)
+        a += (q.data_ptr(), st[0], st[1], _ptr("q_out", q_out, dtype, q.shape, index, False), so[0], so[1], q.shape[1])
+    if k is None:
+        a += (None, 0, 0, None, 0, 0, 0)
+    else:
+        st, ks = _rows("k", k, 3), k.shape
+        hkv = ks[1]
+        if ks[0] != n or ks[2] != dh:
+            raise ValueError("k must be [n, Hkv, Dh] like q")
+        if k_out is None:
+            k_out = _torch.empty(ks, dtype=dtype, device=dev)
+        ko = _store_rows("k_out", k_out, ks, slot is None)
+        capacity, so = ko.shape[0], ko.stride()
+        a += (_ptr("k", k, dtype, None, index, False), st[0], st[1], _ptr("k_out", ko, dtype, None, index, False), so[0], so[1],
+              hkv)
+    if v is None:
+        a += (None, 0, 0, None, 0, 0)
+    else:
+        st = _rows("v", v, 3)
+        vo = _store_rows("v_out", v_out, k.shape, slot is None)
+        so = vo.stride()
+        if vo.shape[0] != capacity:
+            raise ValueError("v_out must have as many rows as k_out")
+        a += (_ptr("v", v, dtype, k.shape, index, False), st[0], st[1], _ptr("v_out", vo, dtype, None, index, False), so[0], so[1])
+    rc = lib.dflash_rotary(*a, _ptr("positions", positions, i32, (n,), index), _ptr("slot", slot, i32, (n,), index), n, capacity,
+                           dh, 2 * freq.shape[0], freq.tobytes(), float(amplitude), 1 if interleaved else 0, 1 if inverse else 0, code,
+                           _ptr("status", status, i32, (1,), index), _raw_stream(index))
+    if rc:
+        _fail(rc)
     return q_out, k_out
-
-
-def _address(a):
-    return a.__array_interface__["data"][0]
 
 
 def _store_rows(name, t, like, dense):
@@ -287,6 +271,12 @@ def decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, *, max_ctx_
     """
     lib = _lib or _load()
     index, dev, bf16, i32 = _device(q), q.device, _torch.bfloat16, _torch.int32
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, max_ctx_len=max_ctx_len, out=out, lse=lse,
+                                          return_lse=return_lse, workspace=workspace, scale=scale, window=window,
+                                          out_dtype=out_dtype, status=status)
     sq = _rows("q", q, 3)
     n, hq, dh = q.shape
     if k_pool.dim() != 4 or block_table.dim() != 2:
@@ -299,25 +289,25 @@ def decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, *, max_ctx_
         raise ValueError("q: the heads of a sequence must be contiguous")
     if width > 1 and stb[1] != 1:
         raise ValueError("block_table: a row must be contiguous")
+    max_ctx_len, window = int(max_ctx_len), int(window)
     if out_dtype != OUT_BF16 and out_dtype != OUT_F32:
         raise ValueError("out_dtype must be OUT_BF16 or OUT_F32")
     odt = _torch.float32 if out_dtype == OUT_F32 else bf16
     p_q, p_k = _ptr("q", q, bf16, None, index, False), _ptr("k_pool", k_pool, bf16, None, index)
     p_v, p_t = _ptr("v_pool", v_pool, bf16, k_pool.shape, index), _ptr("block_table", block_table, i32, (n, width), index, False)
     p_l = _ptr("seq_lens", seq_lens, i32, (n,), index)
-    with _On(index, stream) as handle:
-        if out is None:
-            out = _torch.empty((n, hq, dh), dtype=odt, device=dev)
-        if lse is None and return_lse:
-            lse = _torch.empty((n, hq), dtype=_torch.float32, device=dev)
-        workspace, p_w, w_bytes = _scratch(
-            workspace, lambda: lib.dflash_decode_workspace_size(n, hq, hkv, dh, max_ctx_len, window), index, dev)
-        rc = lib.dflash_decode_attention_paged(
-            p_q, sq[0] if n > 1 else hq * dh, p_k, p_v, p_t, stb[0] if n > 1 else width, p_l, n, hq, hkv, dh, pages, page, width,
-            max_ctx_len, scale, window, out_dtype, _ptr("out", out, odt, (n, hq, dh), index),
-            _ptr("lse", lse, _torch.float32, (n, hq), index), p_w, w_bytes, _ptr("status", status, i32, (1,), index), handle)
-        if rc:
-            _fail(rc)
+    if out is None:
+        out = _torch.empty((n, hq, dh), dtype=odt, device=dev)
+    if lse is None and return_lse:
+        lse = _torch.empty((n, hq), dtype=_torch.float32, device=dev)
+    workspace, p_w, w_bytes = _scratch(
+        workspace, lambda: lib.dflash_decode_workspace_size(n, hq, hkv, dh, max_ctx_len, window), index, dev)
+    rc = lib.dflash_decode_attention_paged(
+        p_q, sq[0] if n > 1 else hq * dh, p_k, p_v, p_t, stb[0] if n > 1 else width, p_l, n, hq, hkv, dh, pages, page, width,
+        max_ctx_len, float(scale), window, out_dtype, _ptr("out", out, odt, (n, hq, dh), index),
+        _ptr("lse", lse, _torch.float32, (n, hq), index), p_w, w_bytes, _ptr("status", status, i32, (1,), index), _raw_stream(index))
+    if rc:
+        _fail(rc)
     return out if lse is None else (out, lse)
 
 
@@ -336,6 +326,10 @@ def beam_select(logits, scores, *, beams_out=None, finished=None, eos=-1, out=No
     """
     lib = _lib or _load()
     index, dev, f32, i32, flag = _device(logits), logits.device, _torch.float32, _torch.int32, _torch.bool
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return beam_select(logits, scores, beams_out=beams_out, finished=finished, eos=eos, out=out, workspace=workspace)
     st = _rows("logits", logits, 3)
     n, w, vocab = logits.shape
     k = w if beams_out is None else int(beams_out)
@@ -350,20 +344,19 @@ def beam_select(logits, scores, *, beams_out=None, finished=None, eos=-1, out=No
         raise ValueError("beams_out must be positive")
     shape = (n, k)
     p_s, p_f = _ptr("scores", scores, f32, (n, w), index), _ptr("finished", finished, flag, (n, w), index)
-    with _On(index, stream) as handle:
-        out = dict(out) if out else {}
-        ptr = []
-        for name, dt in zip(BEAM_OUTPUTS, (f32, i32, i32, flag)):
-            t = out.get(name)
-            if t is None:
-                t = out[name] = _torch.empty(shape, dtype=dt, device=dev)
-                ptr.append(t.data_ptr())
-            else:
-                ptr.append(_ptr(name, t, dt, shape, index))
-        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_beam_workspace_size(n, w, k, vocab, code), index, dev)
-        rc = lib.dflash_beam_select(logits.data_ptr(), st[0], st[1], p_s, p_f, n, w, k, vocab, eos, code, *ptr, p_w, w_bytes, handle)
-        if rc:
-            _fail(rc)
+    out = dict(out) if out else {}
+    ptr = []
+    for name, dt in zip(BEAM_OUTPUTS, (f32, i32, i32, flag)):
+        t = out.get(name)
+        if t is None:
+            t = out[name] = _torch.empty(shape, dtype=dt, device=dev)
+            ptr.append(t.data_ptr())
+        else:
+            ptr.append(_ptr(name, t, dt, shape, index))
+    workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_beam_workspace_size(n, w, k, vocab, code), index, dev)
+    rc = lib.dflash_beam_select(logits.data_ptr(), st[0], st[1], p_s, p_f, n, w, k, vocab, int(eos), code, *ptr, p_w, w_bytes, _raw_stream(index))
+    if rc:
+        _fail(rc)
     return out
 
 
@@ -420,14 +413,17 @@ def fork_pages(parent, seq_lens, block_table, page_refs, *, status=None, stream=
     """
     lib = _lib or _load()
     index, dev, i32 = _device(block_table), block_table.device, _torch.int32
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return fork_pages(parent, seq_lens, block_table, page_refs, status=status)
     n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
     if parent.dim() > 1:
         parent = parent.view(-1)
-    with _On(index, stream) as handle:
-        rc = lib.dflash_fork_pages(_ptr("parent", parent, i32, (n,), index), _ptr("seq_lens", seq_lens, i32, (n,), index), p_t, stride,
-                                   p_r, n, width, pages, _ptr("status", status, i32, (1,), index), handle)
-        if rc:
-            _fail(rc)
+    rc = lib.dflash_fork_pages(_ptr("parent", parent, i32, (n,), index), _ptr("seq_lens", seq_lens, i32, (n,), index), p_t, stride,
+                               p_r, n, width, pages, _ptr("status", status, i32, (1,), index), _raw_stream(index))
+    if rc:
+        _fail(rc)
 
 
 def reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, *, num_new, page_size=None, advance=False,
@@ -442,6 +438,11 @@ def reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, *, num
     """
     lib = _lib or _load()
     index, dev, i32 = _device(block_table), block_table.device, _torch.int32
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, num_new=num_new, page_size=page_size,
+                                 advance=advance, slots=slots, positions=positions, workspace=workspace, status=status)
     n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
     arr, count, page_bytes, page = _pools(pools, pages, index)
     if page is None:
@@ -453,19 +454,18 @@ def reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, *, num
     num_new = int(num_new)
     if num_new < 0:
         raise ValueError("num_new must be >= 0")
-    with _On(index, stream) as handle:
-        if slots is None:
-            slots = _torch.empty(num_new, dtype=i32, device=dev)
-        if positions is None:
-            positions = _torch.empty(num_new, dtype=i32, device=dev)
-        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index, dev)
-        rc = lib.dflash_reserve_pages(
-            _ptr("new_start_loc", new_start_loc, i32, (n + 1,), index), _ptr("seq_lens", seq_lens, i32, (n,), index), p_t, stride, p_r,
-            arr, count, page_bytes, n, num_new, width, page, pages, 1 if advance else 0,
-            _ptr("slots", slots, i32, (num_new,), index), _ptr("positions", positions, i32, (num_new,), index), p_w, w_bytes,
-            _ptr("status", status, i32, (1,), index), handle)
-        if rc:
-            _fail(rc)
+    if slots is None:
+        slots = _torch.empty(num_new, dtype=i32, device=dev)
+    if positions is None:
+        positions = _torch.empty(num_new, dtype=i32, device=dev)
+    workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index, dev)
+    rc = lib.dflash_reserve_pages(
+        _ptr("new_start_loc", new_start_loc, i32, (n + 1,), index), _ptr("seq_lens", seq_lens, i32, (n,), index), p_t, stride, p_r,
+        arr, count, page_bytes, n, num_new, width, page, pages, 1 if advance else 0,
+        _ptr("slots", slots, i32, (num_new,), index), _ptr("positions", positions, i32, (num_new,), index), p_w, w_bytes,
+        _ptr("status", status, i32, (1,), index), _raw_stream(index))
+    if rc:
+        _fail(rc)
     return slots, positions
 
 
@@ -476,15 +476,18 @@ def compact_pages(block_table, page_refs, pools, *, used=None, workspace=None, s
     """
     lib = _lib or _load()
     index, dev, i32 = _device(block_table), block_table.device, _torch.int32
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return compact_pages(block_table, page_refs, pools, used=used, workspace=workspace, status=status)
     n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
     arr, count, page_bytes, _ = _pools(pools, pages, index)
-    with _On(index, stream) as handle:
-        if used is None:
-            used = _torch.empty(1, dtype=i32, device=dev)
-        workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index, dev)
-        rc = lib.dflash_compact_pages(p_t, stride, p_r, arr, count, page_bytes, n, width, pages,
-                                      _ptr("used", used, i32, (1,), index), p_w, w_bytes, _ptr("status", status, i32, (1,), index),
-                                      handle)
-        if rc:
-            _fail(rc)
+    if used is None:
+        used = _torch.empty(1, dtype=i32, device=dev)
+    workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index, dev)
+    rc = lib.dflash_compact_pages(p_t, stride, p_r, arr, count, page_bytes, n, width, pages,
+                                  _ptr("used", used, i32, (1,), index), p_w, w_bytes, _ptr("status", status, i32, (1,), index),
+                                  _raw_stream(index))
+    if rc:
+        _fail(rc)
     return used
