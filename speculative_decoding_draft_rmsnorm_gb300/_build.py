@@ -25,6 +25,9 @@ LIB_PATH = os.path.join(LIB_DIR, LIB_NAME)
 SOURCES = ["api.cu", "attention.cu", "norm_rope.cu", "noalloc.cu", "draft_step.cu", "rotary.cu",
            "decode_attention.cu", "beam.cu", "pages.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "norm_rope.cuh"]
+# The marshalling module of decode.py: host C++ against torch and the product library.
+BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
+BIND_PATH = os.path.join(LIB_DIR, "_decode_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-DDFLASH_BUILD"]
@@ -49,20 +52,57 @@ def _inputs() -> list[str]:
     return files
 
 
-def up_to_date(path: str = LIB_PATH) -> bool:
+def up_to_date(path: str | None = None) -> bool:
+    """Whether a library is there and newer than its sources; without a path, the product library and the
+    marshalling module."""
+    if path is None:
+        return up_to_date(LIB_PATH) and up_to_date(BIND_PATH)
     if not os.path.exists(path):
         return False
     t = os.path.getmtime(path)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    files = [BIND_SOURCE, os.path.join(ROOT, "include", "dflash.h")] if path == BIND_PATH else _inputs()
+    return all(os.path.getmtime(f) <= t for f in files)
+
+
+def _compile_bind() -> str:
+    """bind.cpp to an object (the library it links to is not needed yet)."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(OBJ_DIR, "bind.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + inc,
+           "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), "-I" + sysconfig.get_paths()["include"], "-I" + cuda,
+           "-c", BIND_SOURCE, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-L" + LIB_DIR, "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking the marshalling module failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND_PATH)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Builds both libraries (every translation unit of both in one parallel pass) and
     returns the product library's path."""
     todo = [t for t in TARGETS if force or not up_to_date(t[0])]
-    if not todo:
+    bind = force or not up_to_date(BIND_PATH)
+    if not todo and not bind:
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
+    os.makedirs(OBJ_DIR, exist_ok=True)
     cc = nvcc()
 
     def compile_one(job) -> str:
@@ -80,9 +120,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     for _, extra, obj_dir in todo:
         os.makedirs(obj_dir, exist_ok=True)
         jobs += [(src, extra, obj_dir) for src in SOURCES]
-    workers = max(1, min(len(jobs), os.cpu_count() or 1))
+    workers = max(1, min(len(jobs) + bind, os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(workers) as ex:
+        bind_obj = ex.submit(_compile_bind) if bind else None
         objs = list(ex.map(compile_one, jobs))
+        bind_obj = bind_obj.result() if bind else None
     for i, (path, _, _) in enumerate(todo):
         tmp = path + f".tmp{os.getpid()}"
         mine = objs[i * len(SOURCES):(i + 1) * len(SOURCES)]
@@ -90,6 +132,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, path)
+    if bind:
+        _link_bind(bind_obj)
     return LIB_PATH
 
 

@@ -7,9 +7,9 @@
     reserve_pages(...)          -> dflash_reserve_pages
     compact_pages(...)          -> dflash_compact_pages
 
-Like the rest of the package these only marshal arguments. All tensors of a call live on one device;
-the call runs there, on `stream` (default: that device's current stream). Outputs and workspaces that
-a call allocates belong to that stream.
+Like the rest of the package these only marshal arguments (csrc/bind.cpp checks them and makes the call).
+All tensors of a call live on one device; the call runs there, on `stream` (default: that device's current
+stream). Outputs and workspaces that a call allocates belong to that stream.
 """
 from __future__ import annotations
 
@@ -49,82 +49,40 @@ def _base():
     return pkg
 
 
-_torch = _lib = _raw_stream = _current_device = None
+_bind = None  # the marshalling module (csrc/bind.cpp)
 
 
 def _load():
-    """The library's handle; the first call also brings in torch."""
-    global _torch, _lib, _raw_stream, _current_device
-    import torch
-    _torch = torch
-    # the current stream's handle without building a Stream object (1 us less), where torch has it
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-        lambda index: torch.cuda.current_stream(index).cuda_stream)
-    _current_device = torch.cuda.current_device
-    _lib = _base().load()
-    return _lib
+    """Loads the marshalling module, and with it the library and torch, which it is built against."""
+    global _bind
+    import importlib.machinery
+    import importlib.util
 
+    import torch  # noqa: F401  (the module links to it)
 
-def _device(t) -> int:
-    """The index of the CUDA device that a call's first tensor lives on."""
-    try:
-        index = t.get_device()
-    except AttributeError:
-        raise TypeError("tensors must be torch.Tensor") from None
-    if index < 0:
-        raise ValueError("tensors must live on a CUDA device")
-    return index
-
-
-def _ptr(name, t, dtype, shape, index, contiguous=True):
-    """Checks a tensor (None passes; shape None = any) and returns its address."""
-    if t is None:
-        return None
-    try:
-        if (t.dtype is dtype and t.get_device() == index and (shape is None or t.shape == shape) and
-                (not contiguous or t.is_contiguous())):
-            return t.data_ptr()
-    except AttributeError:
-        raise TypeError(f"{name} must be a torch.Tensor") from None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the call's tensors are on cuda:{index}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _elsewhere(index, stream):
-    """The context that a call has to enter first, so that the device is current and its current stream the
-    one asked for (what is allocated then belongs to it); None where both already hold."""
-    if stream is None:
-        return None if _current_device() == index else _torch.cuda.device(index)
-    return _torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(int(stream), device=index))
+    from . import _build
+    _base().load()
+    loader = importlib.machinery.ExtensionFileLoader("_decode_bind", _build.BIND_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_decode_bind", loader))
+    loader.exec_module(module)
+    _bind = module
+    return module
 
 
 def _fail(rc):
     _base()._raise(rc)
 
 
-def _rows(name, t, dims):
-    """Checks the dimensions of a tensor whose last one must be contiguous; returns its strides."""
-    st = t.stride()
-    if len(st) != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    if st[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return st
-
-
-def _scratch(workspace, nbytes, index, dev):
-    """(tensor, address, bytes) of a call's workspace: the given one, or a new one of nbytes()."""
-    if workspace is None:
-        n = nbytes()
-        if n == 0:
-            _fail(_base().ERR_INVALID_ARG)
-        workspace = _torch.empty(n, dtype=_torch.uint8, device=dev)
-    return workspace, _ptr("workspace", workspace, _torch.uint8, None, index, dev), workspace.numel()
+def _on(stream, first):
+    """The context in which `stream` (a torch stream or a raw handle) is current on the tensors' device."""
+    import torch
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+    elif stream.device != first.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {first.device}")
+    return torch.cuda.stream(stream)
 
 
 # ------------------------------------------------------------------------------------- rotary
@@ -176,80 +134,17 @@ def rotary(q, positions, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_
     [num_pages, page_size, Hkv, Dh]; -1 = not stored. inverse=True applies the transpose: the gradient
     of the inputs from that of the outputs. q may be None.
     """
-    lib = _lib or _load()
-    first = q if q is not None else k
-    if first is None:
-        raise ValueError("pass q, k or both")
-    index, dev, dtype, i32 = _device(first), first.device, first.dtype, _torch.int32
-    away = _elsewhere(index, stream)
-    if away is not None:
-        with away:
+    bind = _bind or _load()
+    if stream is not None:
+        with _on(stream, k if q is None else q):
             return rotary(q, positions, inv_freq, k=k, v=v, q_out=q_out, k_out=k_out, v_out=v_out, slot=slot, amplitude=amplitude,
                           interleaved=interleaved, inverse=inverse, status=status)
-    if dtype is _torch.bfloat16:
-        code = OUT_BF16
-    elif dtype is _torch.float32:
-        code = OUT_F32
-    else:
-        raise TypeError(f"rotary takes bfloat16 or float32, got {dtype}")
-    freq = inv_freq
-    if type(freq) is not np.ndarray or freq.dtype != np.float64 or freq.ndim != 1 or not freq.flags.c_contiguous:
-        freq = np.ascontiguousarray(freq, dtype=np.float64).reshape(-1)
-    if (v is None) != (v_out is None):
-        raise ValueError("pass v and v_out together")
-    if v is not None and k is None:
-        raise ValueError("v needs k")
-    if slot is not None and (k is None or k_out is None):
-        raise ValueError("slot needs k and k_out")
-    _rows("q" if q is not None else "k", first, 3)
-    n, _, dh = first.shape
-    a, capacity = [], n
-    if q is None:
-        a += (None, 0, 0, None, 0, 0, 0)
-    else:
-        if q_out is None:
-            q_out = _torch.empty(q.shape, dtype=dtype, device=dev)
-        st, so = q.stride(), _rows("q_out", q_out, 3)
-        a += (q.data_ptr(), st[0], st[1], _ptr("q_out", q_out, dtype, q.shape, index, False), so[0], so[1], q.shape[1])
-    if k is None:
-        a += (None, 0, 0, None, 0, 0, 0)
-    else:
-        st, ks = _rows("k", k, 3), k.shape
-        hkv = ks[1]
-        if ks[0] != n or ks[2] != dh:
-            raise ValueError("k must be [n, Hkv, Dh] like q")
-        if k_out is None:
-            k_out = _torch.empty(ks, dtype=dtype, device=dev)
-        ko = _store_rows("k_out", k_out, ks, slot is None)
-        capacity, so = ko.shape[0], ko.stride()
-        a += (_ptr("k", k, dtype, None, index, False), st[0], st[1], _ptr("k_out", ko, dtype, None, index, False), so[0], so[1],
-              hkv)
-    if v is None:
-        a += (None, 0, 0, None, 0, 0)
-    else:
-        st = _rows("v", v, 3)
-        vo = _store_rows("v_out", v_out, k.shape, slot is None)
-        so = vo.stride()
-        if vo.shape[0] != capacity:
-            raise ValueError("v_out must have as many rows as k_out")
-        a += (_ptr("v", v, dtype, k.shape, index, False), st[0], st[1], _ptr("v_out", vo, dtype, None, index, False), so[0], so[1])
-    rc = lib.dflash_rotary(*a, _ptr("positions", positions, i32, (n,), index), _ptr("slot", slot, i32, (n,), index), n, capacity,
-                           dh, 2 * freq.shape[0], freq.tobytes(), float(amplitude), 1 if interleaved else 0, 1 if inverse else 0, code,
-                           _ptr("status", status, i32, (1,), index), _raw_stream(index))
-    if rc:
-        _fail(rc)
-    return q_out, k_out
-
-
-def _store_rows(name, t, like, dense):
-    """A destination of k or v as [rows, Hkv, Dh]; dense: as many rows as k."""
-    if t.dim() == 4:
-        t = t.view(-1, t.shape[2], t.shape[3])
-    _rows(name, t, 3)
-    s = t.shape
-    if s[1] != like[1] or s[2] != like[2] or (dense and s[0] != like[0]):
-        raise ValueError(f"{name} must be [{'n' if dense else 'capacity'}, Hkv, Dh]")
-    return t
+    if type(inv_freq) is not np.ndarray or inv_freq.dtype != np.float64 or not inv_freq.flags.c_contiguous:
+        inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    out = bind.rotary(q, positions, inv_freq, k, v, q_out, k_out, v_out, slot, amplitude, interleaved, inverse, status)
+    if type(out) is int:
+        _fail(out)
+    return out
 
 
 # ------------------------------------------------------------------------------------- attention
@@ -269,46 +164,17 @@ def decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, *, max_ctx_
     [N, Hq, Dh], or (out, lse [N, Hq] f32) with return_lse=True or an lse tensor. A length of 0 gives
     zeros and -inf. max_ctx_len bounds the lengths (grid and workspace size only).
     """
-    lib = _lib or _load()
-    index, dev, bf16, i32 = _device(q), q.device, _torch.bfloat16, _torch.int32
-    away = _elsewhere(index, stream)
-    if away is not None:
-        with away:
+    bind = _bind or _load()
+    if stream is not None:
+        with _on(stream, q):
             return decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, max_ctx_len=max_ctx_len, out=out, lse=lse,
                                           return_lse=return_lse, workspace=workspace, scale=scale, window=window,
                                           out_dtype=out_dtype, status=status)
-    sq = _rows("q", q, 3)
-    n, hq, dh = q.shape
-    if k_pool.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("k_pool must be [num_pages, page_size, Hkv, Dh] and block_table [N, max_pages]")
-    pages, page, hkv, kdh = k_pool.shape
-    width, stb = block_table.shape[1], block_table.stride()
-    if kdh != dh:
-        raise ValueError(f"q has head_dim {dh}, the pools {kdh}")
-    if hq > 1 and sq[1] != dh and n:
-        raise ValueError("q: the heads of a sequence must be contiguous")
-    if width > 1 and stb[1] != 1:
-        raise ValueError("block_table: a row must be contiguous")
-    max_ctx_len, window = int(max_ctx_len), int(window)
-    if out_dtype != OUT_BF16 and out_dtype != OUT_F32:
-        raise ValueError("out_dtype must be OUT_BF16 or OUT_F32")
-    odt = _torch.float32 if out_dtype == OUT_F32 else bf16
-    p_q, p_k = _ptr("q", q, bf16, None, index, False), _ptr("k_pool", k_pool, bf16, None, index)
-    p_v, p_t = _ptr("v_pool", v_pool, bf16, k_pool.shape, index), _ptr("block_table", block_table, i32, (n, width), index, False)
-    p_l = _ptr("seq_lens", seq_lens, i32, (n,), index)
-    if out is None:
-        out = _torch.empty((n, hq, dh), dtype=odt, device=dev)
-    if lse is None and return_lse:
-        lse = _torch.empty((n, hq), dtype=_torch.float32, device=dev)
-    workspace, p_w, w_bytes = _scratch(
-        workspace, lambda: lib.dflash_decode_workspace_size(n, hq, hkv, dh, max_ctx_len, window), index, dev)
-    rc = lib.dflash_decode_attention_paged(
-        p_q, sq[0] if n > 1 else hq * dh, p_k, p_v, p_t, stb[0] if n > 1 else width, p_l, n, hq, hkv, dh, pages, page, width,
-        max_ctx_len, float(scale), window, out_dtype, _ptr("out", out, odt, (n, hq, dh), index),
-        _ptr("lse", lse, _torch.float32, (n, hq), index), p_w, w_bytes, _ptr("status", status, i32, (1,), index), _raw_stream(index))
-    if rc:
-        _fail(rc)
-    return out if lse is None else (out, lse)
+    got = bind.decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, int(max_ctx_len), out, lse, return_lse, workspace,
+                                      scale, int(window), out_dtype, status)
+    if type(got) is int:
+        _fail(got)
+    return got
 
 
 # ------------------------------------------------------------------------------------- beams
@@ -324,40 +190,16 @@ def beam_select(logits, scores, *, beams_out=None, finished=None, eos=-1, out=No
     fork_pages takes them), finished bool; slots without a candidate hold -inf, -1, -1, False.
     `out` may hold preallocated outputs, e.g. for graph capture.
     """
-    lib = _lib or _load()
-    index, dev, f32, i32, flag = _device(logits), logits.device, _torch.float32, _torch.int32, _torch.bool
-    away = _elsewhere(index, stream)
-    if away is not None:
-        with away:
+    bind = _bind or _load()
+    if stream is not None:
+        with _on(stream, logits):
             return beam_select(logits, scores, beams_out=beams_out, finished=finished, eos=eos, out=out, workspace=workspace)
-    st = _rows("logits", logits, 3)
-    n, w, vocab = logits.shape
-    k = w if beams_out is None else int(beams_out)
-    dtype = logits.dtype
-    if dtype is f32:
-        code = OUT_F32
-    elif dtype is _torch.bfloat16:
-        code = OUT_BF16
-    else:
-        raise TypeError(f"logits must be bfloat16 or float32, got {dtype}")
-    if k <= 0:
-        raise ValueError("beams_out must be positive")
-    shape = (n, k)
-    p_s, p_f = _ptr("scores", scores, f32, (n, w), index), _ptr("finished", finished, flag, (n, w), index)
-    out = dict(out) if out else {}
-    ptr = []
-    for name, dt in zip(BEAM_OUTPUTS, (f32, i32, i32, flag)):
-        t = out.get(name)
-        if t is None:
-            t = out[name] = _torch.empty(shape, dtype=dt, device=dev)
-            ptr.append(t.data_ptr())
-        else:
-            ptr.append(_ptr(name, t, dt, shape, index))
-    workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_beam_workspace_size(n, w, k, vocab, code), index, dev)
-    rc = lib.dflash_beam_select(logits.data_ptr(), st[0], st[1], p_s, p_f, n, w, k, vocab, int(eos), code, *ptr, p_w, w_bytes, _raw_stream(index))
-    if rc:
-        _fail(rc)
-    return out
+    s, t, p, f = (out.get("scores"), out.get("tokens"), out.get("parents"), out.get("finished")) if out else (None,) * 4
+    got = bind.beam_select(logits, scores, scores.shape[1] if beams_out is None else int(beams_out), finished, int(eos), s, t, p, f,
+                           workspace)
+    if type(got) is int:
+        _fail(got)
+    return dict(zip(BEAM_OUTPUTS, got))
 
 
 def beam_workspace_size(num_reqs, beams, beams_out, vocab, dtype=OUT_BF16) -> int:
@@ -375,55 +217,19 @@ def pages_workspace_size(num_reqs, num_pages) -> int:
     return int(n)
 
 
-def _table(block_table, page_refs, index):
-    """(rows, width, stride, address of the table, of the counts, pages)."""
-    st = block_table.stride()
-    if len(st) != 2 or page_refs.dim() != 1:
-        raise ValueError("block_table must be [N, max_pages] and page_refs [num_pages]")
-    n, width = block_table.shape
-    if width > 1 and st[1] != 1:
-        raise ValueError("block_table: a row must be contiguous")
-    if n > 1 and st[0] < width:
-        raise ValueError("block_table: rows must not overlap")
-    return (n, width, st[0] if n > 1 else width, _ptr("block_table", block_table, _torch.int32, None, index, False),
-            _ptr("page_refs", page_refs, _torch.int32, None, index), page_refs.shape[0])
-
-
-def _pools(pools, num_pages, index):
-    """(host array of addresses, count, bytes per page, rows per page) of a list of pools."""
-    size = page = None
-    addr = []
-    for i, t in enumerate(pools):
-        s = t.shape
-        if t.get_device() != index or not t.is_contiguous() or len(s) < 2 or s[0] != num_pages:
-            raise ValueError(f"pool {i} must be a contiguous [num_pages, page_size, ...] tensor on cuda:{index}")
-        b = t.element_size() * math.prod(s[1:])
-        if size is not None and (b != size or s[1] != page):
-            raise ValueError("all pools must have pages of the same size")
-        size, page = b, s[1]
-        addr.append(t.data_ptr())
-    return (ctypes.c_void_p * max(1, len(addr)))(*addr), len(addr), size or 0, page
-
-
 def fork_pages(parent, seq_lens, block_table, page_refs, *, status=None, stream=None) -> None:
     """Row i of block_table [N, max_pages] and seq_lens [N] becomes row parent[i]'s, in place; -1 frees it.
 
     page_refs [num_pages] int32 counts the table entries that name a page (0 = free) and follows. Nothing
     is copied: reserve_pages gives a row its own copy of a shared page before it is written.
     """
-    lib = _lib or _load()
-    index, dev, i32 = _device(block_table), block_table.device, _torch.int32
-    away = _elsewhere(index, stream)
-    if away is not None:
-        with away:
+    bind = _bind or _load()
+    if stream is not None:
+        with _on(stream, block_table):
             return fork_pages(parent, seq_lens, block_table, page_refs, status=status)
-    n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
-    if parent.dim() > 1:
-        parent = parent.view(-1)
-    rc = lib.dflash_fork_pages(_ptr("parent", parent, i32, (n,), index), _ptr("seq_lens", seq_lens, i32, (n,), index), p_t, stride,
-                               p_r, n, width, pages, _ptr("status", status, i32, (1,), index), _raw_stream(index))
-    if rc:
-        _fail(rc)
+    got = bind.fork_pages(parent, seq_lens, block_table, page_refs, status)
+    if type(got) is int:
+        _fail(got)
 
 
 def reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, *, num_new, page_size=None, advance=False,
@@ -436,37 +242,16 @@ def reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, *, num
     sequence was refused (no pages left, or its table is full), which status reports. advance=True also
     adds the new rows to seq_lens. page_size is needed only with an empty list of pools.
     """
-    lib = _lib or _load()
-    index, dev, i32 = _device(block_table), block_table.device, _torch.int32
-    away = _elsewhere(index, stream)
-    if away is not None:
-        with away:
+    bind = _bind or _load()
+    if stream is not None:
+        with _on(stream, block_table):
             return reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, num_new=num_new, page_size=page_size,
                                  advance=advance, slots=slots, positions=positions, workspace=workspace, status=status)
-    n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
-    arr, count, page_bytes, page = _pools(pools, pages, index)
-    if page is None:
-        if page_size is None:
-            raise ValueError("page_size is needed without pools")
-        page = int(page_size)
-    elif page_size is not None and page_size != page:
-        raise ValueError("page_size is not the pools'")
-    num_new = int(num_new)
-    if num_new < 0:
-        raise ValueError("num_new must be >= 0")
-    if slots is None:
-        slots = _torch.empty(num_new, dtype=i32, device=dev)
-    if positions is None:
-        positions = _torch.empty(num_new, dtype=i32, device=dev)
-    workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index, dev)
-    rc = lib.dflash_reserve_pages(
-        _ptr("new_start_loc", new_start_loc, i32, (n + 1,), index), _ptr("seq_lens", seq_lens, i32, (n,), index), p_t, stride, p_r,
-        arr, count, page_bytes, n, num_new, width, page, pages, 1 if advance else 0,
-        _ptr("slots", slots, i32, (num_new,), index), _ptr("positions", positions, i32, (num_new,), index), p_w, w_bytes,
-        _ptr("status", status, i32, (1,), index), _raw_stream(index))
-    if rc:
-        _fail(rc)
-    return slots, positions
+    got = bind.reserve_pages(new_start_loc, seq_lens, block_table, page_refs, pools, num_new, page_size, advance, slots,
+                            positions, workspace, status)
+    if type(got) is int:
+        _fail(got)
+    return got
 
 
 def compact_pages(block_table, page_refs, pools, *, used=None, workspace=None, status=None, stream=None):
@@ -474,20 +259,11 @@ def compact_pages(block_table, page_refs, pools, *, used=None, workspace=None, s
 
     Returns `used`, an int32 device word: the number of pages in use, which are now the first ones.
     """
-    lib = _lib or _load()
-    index, dev, i32 = _device(block_table), block_table.device, _torch.int32
-    away = _elsewhere(index, stream)
-    if away is not None:
-        with away:
+    bind = _bind or _load()
+    if stream is not None:
+        with _on(stream, block_table):
             return compact_pages(block_table, page_refs, pools, used=used, workspace=workspace, status=status)
-    n, width, stride, p_t, p_r, pages = _table(block_table, page_refs, index)
-    arr, count, page_bytes, _ = _pools(pools, pages, index)
-    if used is None:
-        used = _torch.empty(1, dtype=i32, device=dev)
-    workspace, p_w, w_bytes = _scratch(workspace, lambda: lib.dflash_pages_workspace_size(n, pages), index, dev)
-    rc = lib.dflash_compact_pages(p_t, stride, p_r, arr, count, page_bytes, n, width, pages,
-                                  _ptr("used", used, i32, (1,), index), p_w, w_bytes, _ptr("status", status, i32, (1,), index),
-                                  _raw_stream(index))
-    if rc:
-        _fail(rc)
-    return used
+    got = bind.compact_pages(block_table, page_refs, pools, used, workspace, status)
+    if type(got) is int:
+        _fail(got)
+    return got

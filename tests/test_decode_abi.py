@@ -127,3 +127,26 @@ def test_frequency_tables():
                dict(scaling="parts", original_len=10, fast=1.0, slow=2.0)):
         with pytest.raises(ValueError):
             D.rotary_frequencies(**{**dict(rotary_dim=8), **kw})
+
+
+def test_bindings_refuse_what_is_no_cuda_tensor():
+    import torch
+    q, pos, f = torch.zeros(2, 4, 64), torch.zeros(2, dtype=torch.int32), np.full(32, 0.5)
+    with pytest.raises(ValueError):
+        D.rotary(q, pos, f)
+    with pytest.raises(ValueError):
+        D.rotary(None, pos, f)
+    with pytest.raises(TypeError):
+        D.rotary([1.0], pos, f)
+    with pytest.raises(ValueError):
+        D.decode_attention_paged(q, q, q, pos, pos, max_ctx_len=4)
+    with pytest.raises(ValueError):
+        D.beam_select(q, q)
+    with pytest.raises(TypeError):
+        D.fork_pages(pos, pos, None, pos)
+    with pytest.raises(ValueError):
+        D.reserve_pages(pos, pos, q, pos, [], num_new=1)
+    with pytest.raises(ValueError):
+        D.compact_pages(q, pos, [])
+    with pytest.raises(ValueError):
+        D.rotary(q, pos, f, stream=0)
