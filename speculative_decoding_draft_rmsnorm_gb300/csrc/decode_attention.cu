@@ -565,13 +565,20 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const uint32_t b0 = y ? v.z : v.x, b1 = y ? v.w : v.y;
+            // f32 outputs: a step's products by themselves, added with a rounded addition. The matrix unit cuts
+            // sums off instead of rounding them, which over hundreds of steps adds up (8e-6 over 270).
+            float step[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float(&d)[4] = F32 ? step : acc[x + y];
             if constexpr (R == 1) {
-              mma_bf16(acc[x + y], pw[0][0][0], pw[0][1][0], pw[0][0][1], pw[0][1][1], b0, b1);
-              if constexpr (F32) mma_bf16(acc[x + y], pw[0][2][0], 0u, pw[0][2][1], 0u, b0, b1);
+              mma_bf16(d, pw[0][0][0], pw[0][1][0], pw[0][0][1], pw[0][1][1], b0, b1);
+              if constexpr (F32) mma_bf16(d, pw[0][2][0], 0u, pw[0][2][1], 0u, b0, b1);
             } else {
 #pragma unroll
-              for (int z = 0; z < kTerms; ++z)
-                mma_bf16(acc[x + y], pw[0][z][0], pw[R - 1][z][0], pw[0][z][1], pw[R - 1][z][1], b0, b1);
+              for (int z = 0; z < kTerms; ++z) mma_bf16(d, pw[0][z][0], pw[R - 1][z][0], pw[0][z][1], pw[R - 1][z][1], b0, b1);
+            }
+            if constexpr (F32) {
+#pragma unroll
+              for (int z = 0; z < 4; ++z) acc[x + y][z] += step[z];
             }
           }
         }
