@@ -486,7 +486,7 @@ DFLASH_API int dflash_fork_pages(const int32_t* parent, int32_t* seq_lens, int32
  *   advance    1: seq_lens of served sequences grow by their new rows (for callers that write the
  *              rows themselves at the slots, e.g. dflash_rotary); 0: they stay (dflash_paged_append
  *              advances them)
- *   new_start_loc not nondecreasing within [0, n]: reported, nothing changes. Three launches.
+ *   new_start_loc not nondecreasing within [0, n]: reported, nothing changes. Two launches.
  */
 DFLASH_API int dflash_reserve_pages(const int32_t* new_start_loc, int32_t* seq_lens, int32_t* block_table,
                                     int64_t block_table_stride, int32_t* page_refs, void* const* pools, int num_pools,

@@ -161,13 +161,11 @@ struct ReserveArgs {
   int32_t* positions;
   uint32_t* err;
   // workspace
-  int32_t* bad_starts;  // whether new_start_loc is inconsistent
   int32_t* counts;    // [chunks] free pages
   int32_t* need;      // [rows] pages a row takes; kBadRow, kBadStarts
   int32_t* copy_src;  // [rows] shared page whose live rows are copied, or -1
   int32_t* copy_live; // [rows] how many
-  int32_t* first;     // [rows] rank of its first page among the free ones; -1: refused
-  int32_t* fresh;     // [num_pages] the free pages in order
+  int32_t* fresh;     // [chunks][chunk] the free pages of every chunk in order
 };
 constexpr int kBadRow = -1, kBadStarts = -2;
 
@@ -180,8 +178,17 @@ __device__ __forceinline__ void touched(const ReserveArgs& a, int len, int count
 __global__ void __launch_bounds__(kThreads) reserve_count_kernel(const __grid_constant__ ReserveArgs a) {
   grid_dependents_launch();
   if (static_cast<int>(blockIdx.x) < a.chunks) {
-    const int n = count_chunk(a.refs, a.num_pages, a.chunk, false);
-    if (threadIdx.x == 0) a.counts[blockIdx.x] = n;
+    const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk, hi = min(lo + a.chunk, a.num_pages);
+    int found = 0;
+    for (int64_t i0 = lo; i0 < hi; i0 += kThreads) {
+      const int64_t i = i0 + threadIdx.x;
+      const bool free = i < hi && a.refs[i] == 0;
+      int count;
+      const int rank = block_rank(free, &count);
+      if (free) a.fresh[lo + found + rank] = static_cast<int32_t>(i);
+      found += count;
+    }
+    if (threadIdx.x == 0) a.counts[blockIdx.x] = found;
     return;
   }
   // one warp per row
@@ -234,59 +241,6 @@ __global__ void __launch_bounds__(kThreads) reserve_count_kernel(const __grid_co
   }
 }
 
-__global__ void __launch_bounds__(kThreads) reserve_rank_kernel(const __grid_constant__ ReserveArgs a) {
-  grid_dependency_wait();
-  grid_dependents_launch();
-  int base, free_pages;
-  chunk_prefix(a.counts, a.chunks, &base, &free_pages);
-  if (blockIdx.x == 0) {
-    // the rows' first ranks: a running sum over the rows, kThreads at a time
-    int64_t run = 0;
-    bool bad_starts = false;
-    for (int r = threadIdx.x; r < a.rows; r += kThreads) bad_starts |= a.need[r] == kBadStarts;
-    bad_starts = __syncthreads_or(bad_starts);
-    if (threadIdx.x == 0) *a.bad_starts = bad_starts;
-    __shared__ int64_t s_warp[kThreads / 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    bool refused = bad_starts;
-    for (int r0 = 0; r0 < a.rows; r0 += kThreads) {
-      const int r = r0 + threadIdx.x;
-      const int need = r < a.rows ? a.need[r] : 0;
-      int64_t x = need > 0 ? need : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_warp[warp] = x;
-      __syncthreads();
-      int64_t all = 0;
-      for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) x += s_warp[i];
-        all += s_warp[i];
-      }
-      if (r < a.rows) {
-        const int64_t end = run + x;
-        const bool served = !bad_starts && need >= 0 && (need == 0 || end <= free_pages);
-        a.first[r] = served ? static_cast<int>(end - need) : -1;
-        refused |= !served;
-      }
-      run += all;
-    }
-    if (__syncthreads_or(refused) && threadIdx.x == 0) report(a.err);
-  }
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk, hi = min(lo + a.chunk, a.num_pages);
-  for (int64_t i0 = lo; i0 < hi; i0 += kThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool free = i < hi && a.refs[i] == 0;
-    int count;
-    const int rank = block_rank(free, &count);
-    if (free) a.fresh[base + rank] = static_cast<int32_t>(i);
-    base += count;
-  }
-}
-
 // 16-byte copies of `bytes` (a multiple of 16) by the block.
 __device__ __forceinline__ void block_copy(void* dst, const void* src, int64_t bytes) {
   uint4* d = static_cast<uint4*>(dst);
@@ -304,32 +258,87 @@ __device__ __forceinline__ void block_copy(void* dst, const void* src, int64_t b
   }
 }
 
-// Blocks [0, rows): the table, the counts, the slots and the length of a row each. The others copy the
-// live rows of shared pages, which nothing else in this launch touches.
+// Sum over the block of x in 64 bits (every thread gets it).
+__device__ __forceinline__ int64_t block_sum64(int64_t x) {
+  __shared__ int64_t s_part[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) x += s_part[i];
+  return x;
+}
+
+// Blocks (r, y) serve row r: y = 0 its table, counts, slots and length, all of them a share of the copy of
+// its live rows out of a shared page (which nothing else in this launch touches). Where a row's pages start
+// among the free ones is a sum over the rows before it, taken by every block for itself: it is shorter than
+// another launch.
 __global__ void __launch_bounds__(kThreads) reserve_apply_kernel(const __grid_constant__ ReserveArgs a,
                                                                  const __grid_constant__ Pools pools, int64_t page_bytes) {
+  extern __shared__ int32_t s_ends[];  // [chunks] free pages up to and with a chunk
   grid_dependency_wait();
-  if (static_cast<int>(blockIdx.x) >= a.rows) {
-    const int64_t row_bytes = page_bytes / a.page;
-    const int pieces = static_cast<int>((page_bytes + kPiece - 1) / kPiece);
-    const int64_t per_row = static_cast<int64_t>(pools.n) * pieces, items = per_row * a.rows;
-    for (int64_t i = blockIdx.x - a.rows; i < items; i += gridDim.x - a.rows) {
-      const int r = static_cast<int>(i / per_row);
-      const int first = a.first[r], src = a.copy_src[r];
-      if (first < 0 || src < 0) continue;
-      const int rest = static_cast<int>(i - r * per_row), pool = rest / pieces;
-      const int64_t at = static_cast<int64_t>(rest - pool * pieces) * kPiece;
-      const int64_t bytes = min(a.copy_live[r] * row_bytes - at, static_cast<int64_t>(kPiece));
-      if (bytes <= 0) continue;
-      char* base = static_cast<char*>(pools.p[pool]) + at;
-      block_copy(base + a.fresh[first] * page_bytes, base + src * page_bytes, bytes);
-    }
-    return;
-  }
   const int r = blockIdx.x;
-  const int first = a.first[r], need = a.need[r], len = a.lens[r];
+  const int need = a.need[r], len = a.lens[r];
   const int s0 = a.starts[r], s1 = a.starts[r + 1];
-  const bool served = first >= 0;
+  int64_t before = 0;
+  bool bad_starts = false;
+  for (int i = threadIdx.x; i < a.rows; i += kThreads) {
+    const int n = a.need[i];
+    bad_starts |= n == kBadStarts;
+    if (i < r && n > 0) before += n;
+  }
+  bad_starts = __syncthreads_or(bad_starts);
+  before = block_sum64(before);
+  int free_pages = 0;  // a running sum over the chunks, kThreads at a time
+  for (int i0 = 0; i0 < a.chunks; i0 += kThreads) {
+    const int i = i0 + threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ int s_warp[kThreads / 32];
+    int x = i < a.chunks ? a.counts[i] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) x += s_warp[w];
+      all += s_warp[w];
+    }
+    if (i < a.chunks) s_ends[i] = free_pages + x;
+    free_pages += all;
+  }
+  __syncthreads();
+  const bool served = !bad_starts && need >= 0 && (need == 0 || before + need <= free_pages);
+  auto free_page = [&](int k) {  // the k-th free page: its chunk by bisection
+    int lo = 0, hi = a.chunks - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_ends[mid] > k) hi = mid; else lo = mid + 1;
+    }
+    return a.fresh[static_cast<int64_t>(lo) * a.chunk + (k - (lo ? s_ends[lo - 1] : 0))];
+  };
+
+  const int src = a.copy_src[r];
+  if (served && src >= 0) {
+    const int dst = free_page(static_cast<int>(before));  // the partial page is the first that the row takes
+    const int64_t bytes = a.copy_live[r] * (page_bytes / a.page);
+    const int pieces = static_cast<int>((bytes + kPiece - 1) / kPiece);
+    for (int i = blockIdx.y; i < pools.n * pieces; i += gridDim.y) {
+      const int pool = i / pieces;
+      const int64_t at = static_cast<int64_t>(i - pool * pieces) * kPiece;
+      char* base = static_cast<char*>(pools.p[pool]) + at;
+      block_copy(base + dst * page_bytes, base + src * page_bytes, min(bytes - at, static_cast<int64_t>(kPiece)));
+    }
+  }
+  if (blockIdx.y != 0) return;
+
   int32_t* row = a.table + r * a.stride;
   if (threadIdx.x < 32 && need > 0) {
     const int lane = threadIdx.x;
@@ -340,7 +349,7 @@ __global__ void __launch_bounds__(kThreads) reserve_apply_kernel(const __grid_co
       const int e = p < hi ? row[p] : 0;
       const uint32_t mask = __ballot_sync(0xffffffffu, e < 0);
       if (e < 0 && served) {
-        const int page = a.fresh[first + done + __popc(mask & ((1u << lane) - 1))];
+        const int page = free_page(static_cast<int>(before) + done + __popc(mask & ((1u << lane) - 1)));
         row[p] = page;
         a.refs[page] = 1;
         if (e < -1) atomicSub(a.refs + (-2 - e), 1);
@@ -351,6 +360,12 @@ __global__ void __launch_bounds__(kThreads) reserve_apply_kernel(const __grid_co
     }
   }
   __syncthreads();
+  if (!served && threadIdx.x == 0) report(a.err);
+  if (bad_starts) {  // no sequence takes a row
+    for (int64_t t = static_cast<int64_t>(r) * kThreads + threadIdx.x; t < a.n; t += static_cast<int64_t>(a.rows) * kThreads)
+      a.slots[t] = -1, a.positions[t] = 0;
+    return;
+  }
   if (served) {
     for (int t = s0 + threadIdx.x; t < s1; t += kThreads) {
       const int p = len + (t - s0), page = p / a.page;
@@ -358,15 +373,10 @@ __global__ void __launch_bounds__(kThreads) reserve_apply_kernel(const __grid_co
       a.positions[t] = p;
     }
     if (threadIdx.x == 0 && a.advance) a.lens[r] = len + (s1 - s0);
-  }
-  // new rows that no sequence takes: a refused one's, and those outside [starts[0], starts[rows])
-  if (*a.bad_starts) {
-    for (int64_t t = static_cast<int64_t>(r) * kThreads + threadIdx.x; t < a.n; t += static_cast<int64_t>(a.rows) * kThreads)
-      a.slots[t] = -1, a.positions[t] = 0;
-    return;
-  }
-  if (!served)
+  } else {
     for (int t = s0 + threadIdx.x; t < s1; t += kThreads) a.slots[t] = -1, a.positions[t] = 0;
+  }
+  // new rows outside [starts[0], starts[rows])
   if (r == 0)
     for (int t = threadIdx.x; t < s0; t += kThreads) a.slots[t] = -1, a.positions[t] = 0;
   if (r == a.rows - 1)
@@ -478,14 +488,15 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t workspace_of(int rows, int64_t num_pages) {
   const size_t pages = up(static_cast<size_t>(num_pages) * 4), r = up(static_cast<size_t>(rows) * 4);
-  return up(kMaxChunks * 4) + std::max(4 * r + pages, 3 * pages) + 256;
+  return up(kMaxChunks * 4) + std::max(3 * r + pages, 3 * pages + 256);
 }
 
 template <typename K, typename... A>
-cudaError_t launch_after(K kernel, unsigned grid, cudaStream_t st, const A&... args) {
+cudaError_t launch_after(K kernel, dim3 grid, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -607,23 +618,20 @@ int dflash_reserve_pages(const int32_t* new_start_loc, int32_t* seq_lens, int32_
   const size_t r = up(static_cast<size_t>(num_reqs) * 4);
   a.counts = reinterpret_cast<int32_t*>(ws);
   ws += up(kMaxChunks * 4);
-  a.bad_starts = reinterpret_cast<int32_t*>(ws);
-  ws += 256;
   a.need = reinterpret_cast<int32_t*>(ws);
   a.copy_src = reinterpret_cast<int32_t*>(ws + r);
   a.copy_live = reinterpret_cast<int32_t*>(ws + 2 * r);
-  a.first = reinterpret_cast<int32_t*>(ws + 3 * r);
-  a.fresh = reinterpret_cast<int32_t*>(ws + 4 * r);
+  a.fresh = reinterpret_cast<int32_t*>(ws + 3 * r);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned row_blocks = static_cast<unsigned>((num_reqs + kThreads / 32 - 1) / (kThreads / 32));
   reserve_count_kernel<<<a.chunks + row_blocks, kThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_after(reserve_rank_kernel, static_cast<unsigned>(a.chunks), st, a);
   if (e == cudaSuccess) {
-    const int64_t pieces = (page_bytes + kPiece - 1) / kPiece;
-    const int64_t items = num_pools ? static_cast<int64_t>(num_reqs) * num_pools * pieces : 0;
-    const unsigned copies = static_cast<unsigned>(std::min<int64_t>(items, static_cast<int64_t>(sms) * 8));
-    e = launch_after(reserve_apply_kernel, static_cast<unsigned>(num_reqs) + copies, st, a, p, page_bytes);
+    // blocks of a row: its copy in pieces, as many as give every SM a few
+    const int64_t pieces = num_pools ? num_pools * ((page_bytes + kPiece - 1) / kPiece) : 1;
+    const int64_t shares = std::max<int64_t>(1, std::min<int64_t>({pieces, static_cast<int64_t>(sms) * 8 / num_reqs, 65535}));
+    e = launch_after(reserve_apply_kernel, dim3(static_cast<unsigned>(num_reqs), static_cast<unsigned>(shares)),
+                     static_cast<size_t>(a.chunks) * 4, st, a, p, page_bytes);
   }
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "reserve launch: %s", cudaGetErrorString(e));
   return report_error(DFLASH_OK, "");
@@ -664,12 +672,12 @@ int dflash_compact_pages(int32_t* block_table, int64_t block_table_stride, int32
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   compact_count_kernel<<<a.chunks, kThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_after(compact_rank_kernel, static_cast<unsigned>(a.chunks), st, a);
+  if (e == cudaSuccess) e = launch_after(compact_rank_kernel, dim3(static_cast<unsigned>(a.chunks)), 0, st, a);
   if (e == cudaSuccess) {
     const int64_t cells = static_cast<int64_t>(num_reqs) * max_pages_per_req;
     const int meta = static_cast<int>(std::min<int64_t>(sms, std::max<int64_t>(1, (std::max(cells, num_pages) + 2047) / 2048)));
     const unsigned copies = num_pools ? static_cast<unsigned>(sms) * 32 : 0;
-    e = launch_after(compact_apply_kernel, static_cast<unsigned>(meta) + copies, st, a, p, page_bytes, meta);
+    e = launch_after(compact_apply_kernel, dim3(static_cast<unsigned>(meta) + copies), 0, st, a, p, page_bytes, meta);
   }
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "compact launch: %s", cudaGetErrorString(e));
   return report_error(DFLASH_OK, "");
