@@ -449,7 +449,7 @@ DFLASH_API int dflash_beam_select(const void* logits, int64_t req_stride, int64_
  * The pages of a store. A table row holds the pages of a sequence: entries >= 0 are held, unused
  * entries are -1. page_refs int32 [num_pages] counts for every page the entries that name it;
  * 0 = free. The calls keep the two consistent; a store starts with tables of -1 and counts of 0.
- * All three work in place, on at most 16384 table rows. `pools` is a HOST array of num_pools <= 256
+ * All three work in place, on at most 14000 table rows. `pools` is a HOST array of num_pools <= 256
  * device pointers (K and V of every layer), each [num_pages, page_bytes] with rows of a multiple of
  * 16 bytes; the list may be empty (metadata alone). status: int32 device word or NULL.
  */

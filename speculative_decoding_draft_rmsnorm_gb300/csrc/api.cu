@@ -81,16 +81,6 @@ int check_sizes(int num_reqs, int64_t total_q, int hq, int hkv, int dh, int64_t 
 
 namespace dflash {
 int report_error(int code, const char* msg) { return fail(code, "%s", msg); }
-
-int errorf(int code, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  std::vsnprintf(g_msg, sizeof g_msg, fmt, ap);
-  va_end(ap);
-  return code;
-}
-
-int query_sms(int* out) { return device_sms(out); }
 }  // namespace dflash
 
 extern "C" {

@@ -22,6 +22,7 @@
 #include <cmath>
 
 #include "../../include/dflash.h"
+#include "decode_host.h"
 #include "internal.h"
 #include "ptx.cuh"
 

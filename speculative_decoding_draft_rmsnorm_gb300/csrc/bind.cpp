@@ -122,13 +122,16 @@ bool scratch(const Place& at, PyObject* o, Need need, Scratch* s) {
   return true;
 }
 
+// The call, without the interpreter's lock, on the current stream of the place.
 template <typename F>
-int run(F call) {
-  int rc;
-  Py_BEGIN_ALLOW_THREADS;
-  rc = call();
-  Py_END_ALLOW_THREADS;
-  return rc;
+int run(const Place& at, F call) {
+  struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+  };
+  const cudaStream_t stream = at.stream();
+  Unlocked unlocked;
+  return call(stream);
 }
 
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
@@ -202,15 +205,18 @@ PyObject* rotary(PyObject* const* a) {
   const double amplitude = number(a[9]);
   const int inter = truth(a[10]), inverse = truth(a[11]);
   const int hq = dim32(q.heads, "Hq"), hkv = dim32(k.heads, "Hkv"), d = dim32(dh, "Dh");
-  Py_buffer freq;
-  if (PyObject_GetBuffer(a[2], &freq, PyBUF_C_CONTIGUOUS) != 0) throw Raised{};
-  const int rc = run([&] {
+  struct Buffer : Py_buffer {
+    explicit Buffer(PyObject* o) {
+      if (PyObject_GetBuffer(o, this, PyBUF_C_CONTIGUOUS) != 0) throw Raised{};
+    }
+    ~Buffer() { PyBuffer_Release(this); }
+  } freq(a[2]);
+  const int rc = run(at, [&](cudaStream_t stream) {
     return dflash_rotary(q.src, q.tok, q.head, q.dst, q.out_tok, q.out_head, hq, k.src, k.tok, k.head, k.dst, k.out_tok, k.out_head, hkv,
                          v.src, v.tok, v.head, v.dst, v.out_tok, v.out_head, pos, slot_p, n, capacity, d,
                          static_cast<int>(2 * (freq.len / static_cast<Py_ssize_t>(sizeof(double)))), static_cast<const double*>(freq.buf),
-                         amplitude, inter, inverse, type == at::kFloat ? DFLASH_OUT_F32 : DFLASH_OUT_BF16, status, at.stream());
+                         amplitude, inter, inverse, type == at::kFloat ? DFLASH_OUT_F32 : DFLASH_OUT_BF16, status, stream);
   });
-  PyBuffer_Release(&freq);
   if (rc) return PyLong_FromLong(rc);
   return Py_BuildValue("(NN)", has_q ? given(a[5], new_q) : Py_NewRef(Py_None), has_k ? given(a[6], new_k) : Py_NewRef(Py_None));
 }
@@ -247,10 +253,10 @@ PyObject* decode_attention_paged(PyObject* const* a) {
   Scratch ws;
   if (!scratch(at, a[9], [&] { return dflash_decode_workspace_size(n, hq, hkv, dh, longest, window); }, &ws))
     return PyLong_FromLong(DFLASH_ERR_INVALID_ARG);
-  const int rc = run([&] {
+  const int rc = run(at, [&](cudaStream_t stream) {
     return dflash_decode_attention_paged(pq, n > 1 ? q.stride(0) : static_cast<int64_t>(hq) * dh, pk, pv, pt, n > 1 ? table.stride(0) : width,
                                          pl, n, hq, hkv, dh, kp.size(0), page, width, longest, scale, window, dtype, out, lse, ws.p,
-                                         ws.bytes, status, at.stream());
+                                         ws.bytes, status, stream);
   });
   if (rc) return PyLong_FromLong(rc);
   if (!lse && !(a[7] != Py_None || new_lse.defined())) return given(a[6], new_out);
@@ -286,10 +292,10 @@ PyObject* beam_select(PyObject* const* a) {
   Scratch ws;
   if (!scratch(at, a[9], [&] { return dflash_beam_workspace_size(n, w, k, vocab, dtype); }, &ws))
     return PyLong_FromLong(DFLASH_ERR_INVALID_ARG);
-  const int rc = run([&] {
+  const int rc = run(at, [&](cudaStream_t stream) {
     return dflash_beam_select(x.data_ptr(), x.stride(0), x.stride(1), scores, finished, n, w, k, vocab, eos, dtype, static_cast<float*>(out[0]),
                               static_cast<int32_t*>(out[1]), static_cast<int32_t*>(out[2]), static_cast<uint8_t*>(out[3]), ws.p, ws.bytes,
-                              at.stream());
+                              stream);
   });
   if (rc) return PyLong_FromLong(rc);
   return Py_BuildValue("(NNNN)", given(a[5], made[0]), given(a[6], made[1]), given(a[7], made[2]), given(a[8], made[3]));
@@ -351,7 +357,7 @@ PyObject* fork_pages(PyObject* const* a) {
   const auto* pp = static_cast<const int32_t*>(at.plain("parent", parent, at::kInt));
   auto* lens = static_cast<int32_t*>(at.address("seq_lens", a[1], at::kInt, {t.rows}));
   auto* status = static_cast<int32_t*>(at.address("status", a[4], at::kInt, {1}));
-  const int rc = run([&] { return dflash_fork_pages(pp, lens, t.table, t.stride, t.refs, t.rows, t.width, t.pages, status, at.stream()); });
+  const int rc = run(at, [&](cudaStream_t stream) { return dflash_fork_pages(pp, lens, t.table, t.stride, t.refs, t.rows, t.width, t.pages, status, stream); });
   if (rc) return PyLong_FromLong(rc);
   Py_RETURN_NONE;
 }
@@ -383,9 +389,9 @@ PyObject* reserve_pages(PyObject* const* a) {
   const int advance = truth(a[7]), page32 = dim32(page, "page_size");
   Scratch ws;
   if (!scratch(at, a[10], [&] { return dflash_pages_workspace_size(t.rows, t.pages); }, &ws)) return PyLong_FromLong(DFLASH_ERR_INVALID_ARG);
-  const int rc = run([&] {
+  const int rc = run(at, [&](cudaStream_t stream) {
     return dflash_reserve_pages(starts, lens, t.table, t.stride, t.refs, pools.p.data(), static_cast<int>(pools.p.size()), pools.bytes, t.rows,
-                                num_new, t.width, page32, t.pages, advance, slots, pos, ws.p, ws.bytes, status, at.stream());
+                                num_new, t.width, page32, t.pages, advance, slots, pos, ws.p, ws.bytes, status, stream);
   });
   if (rc) return PyLong_FromLong(rc);
   return Py_BuildValue("(NN)", given(a[8], new_slots), given(a[9], new_pos));
@@ -403,9 +409,9 @@ PyObject* compact_pages(PyObject* const* a) {
   auto* used = static_cast<int32_t*>(made.defined() ? made.data_ptr() : at.address("used", a[3], at::kInt, {1}));
   Scratch ws;
   if (!scratch(at, a[4], [&] { return dflash_pages_workspace_size(t.rows, t.pages); }, &ws)) return PyLong_FromLong(DFLASH_ERR_INVALID_ARG);
-  const int rc = run([&] {
+  const int rc = run(at, [&](cudaStream_t stream) {
     return dflash_compact_pages(t.table, t.stride, t.refs, pools.p.data(), static_cast<int>(pools.p.size()), pools.bytes, t.rows, t.width,
-                                t.pages, used, ws.p, ws.bytes, status, at.stream());
+                                t.pages, used, ws.p, ws.bytes, status, stream);
   });
   if (rc) return PyLong_FromLong(rc);
   return given(a[3], made);

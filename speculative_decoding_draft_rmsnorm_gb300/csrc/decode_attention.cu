@@ -32,6 +32,7 @@
 #include <cmath>
 
 #include "../../include/dflash.h"
+#include "decode_host.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -85,7 +86,7 @@ struct DecodeArgs {
   int tile_units;  // units that a kv head's tiles make
   int lone;        // block b has group b to itself
   int64_t num_pages;
-  int page, max_pages, window;
+  int page, window;
   int64_t max_len;  // longest valid length
   uint32_t page_mul, page_shift;  // j / page
   float scale_log2;
@@ -923,7 +924,7 @@ int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const 
   a.part_o = reinterpret_cast<float*>(ws + y.o);
   a.num_reqs = num_reqs, a.hq = hq, a.hkv = hkv, a.g = hq / hkv;
   a.unit = y.unit, a.tile_units = y.tile_units, a.lone = y.lone;
-  a.num_pages = num_pages, a.page = page_size, a.max_pages = max_pages_per_req, a.window = window;
+  a.num_pages = num_pages, a.page = page_size, a.window = window;
   a.max_len = max_ctx_len;
   if ((page_size & (page_size - 1)) == 0) {
     while ((1 << a.page_shift) < page_size) ++a.page_shift;

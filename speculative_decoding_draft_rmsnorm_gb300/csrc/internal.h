@@ -135,9 +135,5 @@ cudaError_t launch_attention(const AttnHost& h, cudaStream_t stream, char* msg, 
 
 // Records `msg` as the thread's last error (what dflash_last_error returns) and returns code.
 int report_error(int code, const char* msg);
-// report_error with a printf format.
-int errorf(int code, const char* fmt, ...);
-// SM count of the current device; DFLASH_ERR_UNSUPPORTED (with its message) unless it is sm_103.
-int query_sms(int* out);
 
 }  // namespace dflash

@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "../../include/dflash.h"
+#include "decode_host.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -24,7 +25,7 @@ constexpr int kMaxPools = 256;
 constexpr int kThreads = 256;
 constexpr int kMaxChunks = 1024;   // pieces of page_refs that a block counts and ranks
 constexpr int kMinChunk = 1024;    // pages per piece
-constexpr int kMaxRows = 16384;    // table rows of a call (a prefix over them lies in shared memory)
+constexpr int kMaxRows = 14000;    // table rows of a call (fork keeps a column of them in shared memory)
 constexpr int kPiece = 16384;      // bytes a block copies at a time
 
 struct Pools {

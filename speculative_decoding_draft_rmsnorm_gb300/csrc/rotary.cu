@@ -25,6 +25,7 @@
 #include <initializer_list>
 
 #include "../../include/dflash.h"
+#include "decode_host.h"
 #include "internal.h"
 #include "norm_rope.cuh"
 #include "ptx.cuh"
