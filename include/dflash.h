@@ -358,7 +358,8 @@ DFLASH_API int dflash_prepare_inputs(const int32_t* idx_mapping, const int32_t* 
  *   q_out    like q; may be q itself with the same strides
  *   k_out, v_out  row t, or row slot[t] where slot is given: [capacity, Hkv, Dh] with their own
  *            strides. Without slots k_out may be k itself (same strides) and n <= capacity.
- *            Other overlaps of inputs and outputs are not allowed.
+ *            Other overlaps of inputs and outputs are not allowed; an output whose rows or heads
+ *            overlap one another is refused.
  *   positions int32 [n]    any sign; the angle is exact to 1e-6 rad below 2^24
  *   slot     int32 [n] or NULL; -1 = the row is not stored (padding); a slot >= capacity is not
  *            stored and reported through status. Slots must be distinct.
@@ -406,7 +407,8 @@ DFLASH_API size_t dflash_decode_workspace_size(int num_reqs, int hq, int hkv, in
  *   Dh in {64, 128}; Hq % Hkv == 0, any group size. bf16 products are exact, sums f32; the weights
  *   keep 16 bits for a bf16 output and 24 for an f32 one. Two launches (attention, join), or one
  *   where max_ctx_len (or the window) is at most 512 and there are no more (sequence, kv head)
- *   pairs than SMs. Results do not depend on timing.
+ *   pairs than SMs. Results do not depend on timing. Rows outside the lengths and the window may hold
+ *   anything; a stored value that is infinite gives NaN in its column.
  */
 DFLASH_API int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const dflash_bf16* k_pool,
                                              const dflash_bf16* v_pool, const int32_t* block_table,

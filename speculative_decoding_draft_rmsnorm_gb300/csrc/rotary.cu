@@ -239,6 +239,15 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   }
 }
 
+// Whether rows and heads of an output lie apart: the tighter of its two strides holds a head, the wider one
+// all that the tighter one runs through.
+bool apart(int64_t rows, int64_t row_stride, int heads, int64_t head_stride, int dh) {
+  if (rows <= 1) return heads <= 1 || head_stride >= dh;
+  if (heads <= 1) return row_stride >= dh;
+  if (head_stride <= row_stride) return head_stride >= dh && (row_stride - dh) / head_stride >= heads - 1;
+  return row_stride >= dh && (head_stride - dh) / row_stride >= rows - 1;
+}
+
 template <typename T, bool INTER, int E>
 void launch(const RotaryArgs& a, cudaStream_t st) {
   const int64_t items = a.n * (a.rot_units + a.tail_units + a.v_units) * a.groups;
@@ -272,6 +281,7 @@ extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void*
     return errorf(DFLASH_ERR_INVALID_ARG, "head counts must be >= 0 and not both 0 (Hq=%d, Hkv=%d)", hq, hkv);
   if (hq > 65536 || hkv > 65536) return errorf(DFLASH_ERR_UNSUPPORTED, "more than 65536 heads");
   if (n < 0 || capacity < 0) return errorf(DFLASH_ERR_INVALID_ARG, "negative row count");
+  if (n > (1ll << 32)) return errorf(DFLASH_ERR_UNSUPPORTED, "too many rows for one call (%lld)", static_cast<long long>(n));
   if (dh <= 0 || rotary_dim <= 0 || rotary_dim > dh || (rotary_dim & 1))
     return errorf(DFLASH_ERR_INVALID_ARG, "rotary_dim %d must be even and in [2, head_dim=%d]", rotary_dim, dh);
   if (rotary_dim > 2 * kMaxPairs || dh > 1024)
@@ -296,6 +306,12 @@ extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void*
     return errorf(DFLASH_ERR_INVALID_ARG, "q in place needs equal strides");
   if (hkv && k == k_out && (k_tok != k_out_tok || (hkv > 1 && k_head != k_out_head)))
     return errorf(DFLASH_ERR_INVALID_ARG, "k in place needs equal strides");
+  if (v && v == v_out && (v_tok != v_out_tok || (hkv > 1 && v_head != v_out_head)))
+    return errorf(DFLASH_ERR_INVALID_ARG, "v in place needs equal strides");
+  const int64_t stored = slot ? capacity : n;
+  if ((hq && !apart(n, q_out_tok, hq, q_out_head, dh)) || (hkv && !apart(stored, k_out_tok, hkv, k_out_head, dh)) ||
+      (v && !apart(stored, v_out_tok, hkv, v_out_head, dh)))
+    return errorf(DFLASH_ERR_INVALID_ARG, "rows or heads of an output overlap");
   const size_t es = dtype == DFLASH_OUT_F32 ? 4 : 2;
   RotaryArgs a{};
   a.t[0] = RotaryTensor{q, q_out, q_tok, q_head, q_out_tok, q_out_head};
