@@ -41,16 +41,22 @@ constexpr int kMergeRoom = 128;            // and of a request, past the bound
 constexpr int kTile = 512;            // vectors at most: 4096 bf16 or 2048 f32 elements
 constexpr int kBlocksPerSm = 5;
 constexpr int kWaves = 1;
-constexpr int kMaxVocab = 1 << 26;    // W * vocab < 2^31
+constexpr int kVocabBits = 26;
+constexpr int kMaxVocab = 1 << kVocabBits;
 
 // A sum in two f32 terms (Knuth's two-sum): 48 bits, so that what small terms add to a sum that a few
 // large ones dominate still orders beams whose large logits are equal.
 struct Sum {
   float hi = 0.0f, lo = 0.0f;
   __device__ __forceinline__ void add(float x) {
-    const float t = hi + x, z = t - hi;
+    const float t = __fadd_rn(hi, x), z = t - hi;
     lo += (hi - (t - z)) + (x - z);
     hi = t;
+  }
+  // The same with hi the nearest f32 to the sum, for |lo| <= |hi|.
+  __device__ __forceinline__ Sum settled() const {
+    const float t = __fadd_rn(hi, lo);
+    return Sum{t, lo - (t - hi)};
   }
   __device__ __forceinline__ void scale(float f) { hi *= f, lo *= f; }
 };
@@ -95,6 +101,10 @@ struct Vec<false> {
   static __device__ __forceinline__ float one(const void* p, int64_t i) {
     return bf16lo_to_f32(static_cast<const uint16_t*>(p)[i]);
   }
+  static __device__ __forceinline__ float pick(const uint4& v, int i) {  // at() for an index not known before
+    const uint32_t w = i & 4 ? (i & 2 ? v.w : v.z) : (i & 2 ? v.y : v.x);
+    return (i & 1) ? bf16hi_to_f32(w) : bf16lo_to_f32(w);
+  }
 };
 template <>
 struct Vec<true> {
@@ -103,6 +113,9 @@ struct Vec<true> {
     return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
   }
   static __device__ __forceinline__ float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+  static __device__ __forceinline__ float pick(const uint4& v, int i) {
+    return __uint_as_float(i & 2 ? (i & 1 ? v.w : v.z) : (i & 1 ? v.y : v.x));
+  }
 };
 
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
 #pragma unroll 1
         for (; mask; mask &= mask - 1) {
           const int32_t x = p.head + v * E + __ffs(mask) - 1;
-          push(V::one(p.base, x), x);
+          push(V::pick(raw, __ffs(mask) - 1), x);
         }
       }
     }
@@ -478,7 +491,7 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
 // and one logarithm from the library more than 2.)
 struct Best {
   uint32_t hi, lo;  // 0, 0: none
-  int32_t at;       // w V + t
+  int32_t at;       // beam and token: w 2^26 + t, in the order of w V + t
 };
 __device__ __forceinline__ bool better(const Best& x, const Best& y) {
   return x.hi != y.hi ? x.hi > y.hi : x.lo != y.lo ? x.lo > y.lo : x.at < y.at;
@@ -498,29 +511,49 @@ __device__ __forceinline__ Best best_of_warp(const Best& b) {
   return r;
 }
 
-// m + log(s.hi + s.lo) in 64 bits with few FP64 instructions: s = 2^e f, f in [2/3, 4/3), and
-// log f = 2 atanh(q), q = (f - 1) / (f + 1), |q| <= 1/5, by its series (the first term left out is below
-// 2 * 5^-19 / 19 = 6e-15).
-__device__ __forceinline__ double log_plus(float m, const Sum& s) {
-  const double x = static_cast<double>(s.hi) + s.lo;
-  if (!(s.hi > 0.0f) || m == -INFINITY || s.hi == INFINITY) return static_cast<double>(m) + static_cast<double>(__logf(s.hi));
+// m + log(s.hi + s.lo) in two f32 terms, to 2^-42 (FP64 instructions for it took 1.1 us more): s = 2^e f, f in
+// [2/3, 4/3), and log f = 2 atanh(q), q = (f - 1) / (f + 1), |q| <= 1/5, by its series 2 q (1 + z / 3 + z^2 / 5 + ..),
+// z = q^2 (the first term left out is below 2 * 5^-21 / 21 = 2^-51). The terms from z^4 on need f32 only.
+__device__ __forceinline__ Sum log_plus(float m, const Sum& sum) {
+  if (!(sum.hi > 0.0f) || m == -INFINITY || sum.hi == INFINITY) return Sum{m + __logf(sum.hi), 0.0f};
+  const Sum s = sum.settled();
   const int e = static_cast<int>((__float_as_uint(s.hi * 0.75f) >> 23) & 255u) - 126;  // hi in [2/3, 4/3) 2^e
-  const double f = x * __longlong_as_double(static_cast<long long>(1023 - e) << 52);
-  const double num = f - 1.0, den = f + 1.0;
-  const double r = static_cast<double>(1.0f / static_cast<float>(den));
-  double q = num * r;
-  q = fma(r, fma(-q, den, num), q);
-  const double z = q * q;
-  double p = 1.0 / 17.0;
-  p = fma(p, z, 1.0 / 15.0);
-  p = fma(p, z, 1.0 / 13.0);
-  p = fma(p, z, 1.0 / 11.0);
-  p = fma(p, z, 1.0 / 9.0);
-  p = fma(p, z, 1.0 / 7.0);
-  p = fma(p, z, 1.0 / 5.0);
-  p = fma(p, z, 1.0 / 3.0);
-  p = fma(p, z, 1.0);
-  return fma(static_cast<double>(e), 0.693147180559945309, static_cast<double>(m)) + 2.0 * q * p;
+  const float scale = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  const Sum num = Sum{s.hi * scale - 1.0f, s.lo * scale}.settled();  // f - 1 is exact
+  Sum den{2.0f, num.lo};
+  den.add(num.hi);
+  const float r = __fdividef(1.0f, den.hi), q0 = num.hi * r;
+  const Sum q = Sum{q0, (fmaf(-q0, den.hi, num.hi) + fmaf(-q0, den.lo, num.lo)) * r}.settled();
+  const float z = q.hi * q.hi, z_lo = fmaf(q.hi, q.hi, -z) + 2.0f * q.hi * q.lo;
+  float t = 1.0f / 19.0f;
+  t = fmaf(t, z, 1.0f / 17.0f);
+  t = fmaf(t, z, 1.0f / 15.0f);
+  t = fmaf(t, z, 1.0f / 13.0f);
+  t = fmaf(t, z, 1.0f / 11.0f);
+  t = fmaf(t, z, 1.0f / 9.0f);
+  Sum p{t, 0.0f};
+  auto horner = [&](double c) {  // p = c + z p, c a constant
+    const float h = __fmul_rn(z, p.hi), l = fmaf(z, p.hi, -h) + fmaf(z, p.lo, z_lo * p.hi);
+    p.hi = static_cast<float>(c), p.lo = static_cast<float>(c - static_cast<double>(p.hi));
+    p.add(h);
+    p.lo += l;
+  };
+  horner(1.0 / 7.0);
+  horner(1.0 / 5.0);
+  horner(1.0 / 3.0);
+  horner(1.0);
+  const float h = __fmul_rn(q.hi, p.hi), l = fmaf(q.hi, p.hi, -h) + fmaf(q.hi, p.lo, q.lo * p.hi);
+  // e log 2 in three products, the first exact (16 bits of the constant)
+  constexpr float kLn2 = 0.693145751953125f;
+  constexpr double kRest = 0.693147180559945309417 - static_cast<double>(kLn2);
+  constexpr float kRestHi = static_cast<float>(kRest), kRestLo = static_cast<float>(kRest - static_cast<double>(kRestHi));
+  const float x = static_cast<float>(e), b = __fmul_rn(x, kRestHi);
+  Sum out{m, 0.0f};
+  out.add(x * kLn2);
+  out.add(b);
+  out.add(2.0f * h);
+  out.lo += fmaf(x, kRestHi, -b) + x * kRestLo + 2.0f * l;
+  return out.settled();
 }
 
 struct Lists {
@@ -541,12 +574,10 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
   constexpr int kMergeWarps = kThreads / 32;
   __shared__ Lists s_lists[kMaxBeams];
   __shared__ bool s_ended[kMaxBeams];
-  __shared__ float s_max[kMaxBeams];
-  __shared__ Sum s_lse[kMaxBeams];  // first the sums, then their logarithms in two terms
+  __shared__ Sum s_lse[kMaxBeams];  // log-sums in two terms
   __shared__ Best s_best[2][kMergeWarps], s_list[kMergeRoom];
   __shared__ uint32_t s_group[32];
   __shared__ int s_count;
-  grid_dependency_wait();
   const int n = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = a.beams, K = a.out_beams, S = a.most_lists;
   const int total = W * S * K;
@@ -554,40 +585,52 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
   if (tid < 32) s_group[tid] = 0;
   if (tid == 0) s_count = 0;
   __syncthreads();
-  // every load first, whether it will count or not: none depends on another's value. Candidate i is number
+  // Every load first, whether it will count or not: none depends on another's value, and the call's inputs do not
+  // wait for the scan. Candidate i is number
   // i % K of list i / K % S of beam i / (S K); i < 2^12, so that products with a reciprocal divide exactly
   const float per_beam = 1.0f / static_cast<float>(S * K), per_list = 1.0f / static_cast<float>(K);
   float val[kPer], score[kPer];
   int32_t idx[kPer];
   uint8_t ended[kPer];
+  int64_t at[kPer];  // in the lists; -1: none
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = j * kThreads + tid;
-    idx[j] = -1, val[j] = score[j] = 0.0f, ended[j] = 0;
+    at[j] = -1, score[j] = 0.0f, ended[j] = 0;
     if (i < total) {
       const int w = static_cast<int>((i + 0.5f) * per_beam), rest = i - w * S * K;
       const int s = static_cast<int>((rest + 0.5f) * per_list), row = n * W + w;
       const Lists lists = s_lists[w];
       score[j] = a.scores[row];
       ended[j] = a.finished ? a.finished[row] : 0;
-      if (s < lists.count) {
-        const int64_t at = (lists.first + s) * K + (rest - s * K);
-        idx[j] = a.part_idx[at];
-        val[j] = a.part_val[at];
-      }
+      if (s < lists.count) at[j] = (lists.first + s) * K + (rest - s * K);
     }
+  }
+  const bool one = warp < W && lane < s_lists[warp].count;  // a list of the warp's first beam
+  const bool first_ended = warp < W && a.finished && a.finished[n * W + warp];
+  grid_dependency_wait();
+  float first_max = -INFINITY;
+  Sum first_sum;
+  if (one) {
+    first_max = a.part_max[s_lists[warp].first + lane];
+    first_sum = a.part_sum[s_lists[warp].first + lane];
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    idx[j] = at[j] < 0 ? -1 : a.part_idx[at[j]];
+    val[j] = at[j] < 0 ? 0.0f : a.part_val[at[j]];
   }
 #pragma unroll 1
   for (int w = warp; w < W; w += kMergeWarps) {
-    const int row = n * W + w;
     const Lists lists = s_lists[w];
-    const bool finished = a.finished && a.finished[row];
+    const bool finished = w == warp ? first_ended : a.finished && a.finished[n * W + w];
     float m = -INFINITY;
     Sum sum;
 #pragma unroll 1
     for (int i = lane; i < lists.count; i += 32) {
-      const float om = a.part_max[lists.first + i];
-      Sum o = a.part_sum[lists.first + i];
+      const bool here = w == warp && i == lane;
+      const float om = here ? first_max : a.part_max[lists.first + i];
+      Sum o = here ? first_sum : a.part_sum[lists.first + i];
       const float top = fmaxf(m, om);
       if (m != -INFINITY) sum.scale(exp_below(m, top));
       if (om != -INFINITY) o.scale(exp_below(om, top));
@@ -605,14 +648,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
       sum.add(hi);
       sum.lo += lo;
     }
-    // a finished beam's candidate is its score: log 1
-    if (lane == 0) s_max[w] = finished ? 0.0f : top, s_lse[w] = finished ? Sum{1.0f, 0.0f} : sum, s_ended[w] = finished;
-  }
-  __syncthreads();
-  if (warp == 0 && lane < W) {  // one logarithm for all beams
-    const double lse = log_plus(s_max[lane], s_lse[lane]);
-    const float hi = static_cast<float>(lse);
-    s_lse[lane] = Sum{hi, static_cast<float>(lse - static_cast<double>(hi))};
+    // a finished beam's candidate is its score
+    const Sum lse = finished ? Sum{0.0f, 0.0f} : log_plus(top, sum);
+    if (lane == 0) s_lse[w] = lse, s_ended[w] = finished;
   }
   __syncthreads();
   Best mine[kPer];
@@ -636,14 +674,14 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
       if (hi > -INFINITY) {  // -inf and NaN are no candidates
         mine[j].hi = order_key(hi + 0.0f);
         mine[j].lo = order_key(rest + 0.0f);
-        mine[j].at = w * a.vocab + idx[j];
+        mine[j].at = w << kVocabBits | idx[j];
       }
     }
   }
   auto write = [&](int k, const Best& b) {
     const int64_t o = static_cast<int64_t>(n) * K + k;
     const bool none = b.hi == 0;
-    const int w = none ? 0 : b.at / a.vocab, t = none ? -1 : b.at - w * a.vocab;
+    const int w = none ? 0 : b.at >> kVocabBits, t = none ? -1 : b.at & (kMaxVocab - 1);
     a.out_scores[o] = none ? -INFINITY : from_key(b.hi);
     a.out_tokens[o] = t;
     a.out_parents[o] = none ? -1 : n * W + w;

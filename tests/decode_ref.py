@@ -57,7 +57,7 @@ def beams(logits, scores, k, finished=None, eos=-1):
             x = logits[r, b].astype(np.float64)
             m = x.max()
             with np.errstate(all="ignore"):
-                c = float(scores[r, b]) + (x - (m + np.log(np.exp(x - m).sum())))
+                c = float(scores[r, b]) + ((x - m) - np.log(np.exp(x - m).sum()))  # m + log would lose it at 3e38
             c[np.isnan(c)] = -np.inf
             # the K best of a beam are enough; a stable sort keeps ties in token order
             for t in np.argsort(-c, kind="stable")[:k]:
