@@ -285,6 +285,23 @@ __device__ __forceinline__ float max_of(const uint4 (&v)[kVec]) {
   }
 }
 
+// The rank of value tid / 8 among 32 in shared memory (equal ones by their place), by 256 threads, 8 lanes each.
+template <typename T>
+__device__ __forceinline__ int rank_of_32(const T* x, int tid) {
+  const int at = tid / 8;
+  const T v = x[at];
+  int rank = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = tid % 8 + 8 * j;
+    const T o = x[i];
+    rank += o > v || (o == v && i < at);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  return rank;
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
   using V = Vec<F32>;
@@ -301,12 +318,14 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int K = a.out_beams;
   constexpr size_t kSize = F32 ? 4 : 2;
-  const int64_t tile_end = min((static_cast<int64_t>(blockIdx.x) + 1) * a.per_block, static_cast<int64_t>(a.rows) * a.tiles);
+  // the block's share: `left` tiles from tile `from` of row `row` on
+  const int64_t tile = static_cast<int64_t>(blockIdx.x) * a.per_block, all = static_cast<int64_t>(a.rows) * a.tiles;
+  int64_t left_tiles = min(static_cast<int64_t>(a.per_block), all - tile);
+  int row = static_cast<int>(all < (1ll << 32) ? static_cast<uint32_t>(tile) / static_cast<uint32_t>(a.tiles) : tile / a.tiles);
+  int from = static_cast<int>(tile - static_cast<int64_t>(row) * a.tiles), upto;
 #pragma unroll 1
-  for (int64_t tile = static_cast<int64_t>(blockIdx.x) * a.per_block; tile < tile_end;) {
-  const int row = static_cast<int>(tile / a.tiles), from = static_cast<int>(tile - static_cast<int64_t>(row) * a.tiles);
-  const int upto = static_cast<int>(min(static_cast<int64_t>(a.tiles), from + (tile_end - tile)));
-  tile += upto - from;
+  for (; left_tiles > 0; left_tiles -= upto - from, from = 0, ++row) {
+  upto = static_cast<int>(min(static_cast<int64_t>(a.tiles), from + left_tiles));
   if (a.finished && a.finished[row]) continue;  // its one candidate needs no logits
   const int n = row / a.beams, b = row - n * a.beams;
   Piece p;
@@ -318,8 +337,9 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
   p.tail = p.head + vecs * E;
   p.vec = reinterpret_cast<const uint4*>(p.base + p.head * kSize);
   // equal tiles: a short one at the end would hold too few elements for a bound
-  p.lo = static_cast<int>(static_cast<int64_t>(vecs) * from / a.tiles);
-  p.hi = static_cast<int>(static_cast<int64_t>(vecs) * upto / a.tiles);
+  const int each = static_cast<int>(static_cast<uint32_t>(vecs) / static_cast<uint32_t>(a.tiles)), longer = vecs - each * a.tiles;
+  p.lo = from * each + min(from, longer);
+  p.hi = upto * each + min(upto, longer);
   p.first = from == 0, p.last = upto == a.tiles;
   if (tid == 0) s_count = s_hits = 0;
 
@@ -402,16 +422,7 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
       a.part_sum[at] = s;
     }
   }
-  if (warp == 0) {
-    const float v = s_max[lane];
-    int rank = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float o = s_max[i];
-      rank += o > v || (o == v && i < lane);
-    }
-    if (rank == K - 1) s_bound = v;
-  }
+  if (rank_of_32(s_max, tid) == K - 1 && tid % 8 == 0) s_bound = s_max[tid / 8];
   __syncthreads();
   const float bound = s_bound;
 
@@ -463,21 +474,21 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
     __syncthreads();
   }
 #pragma unroll 1
-  for (int c = tid; c < max(count, K); c += kScanThreads) {
-    if (c >= count) {  // fewer candidates than beams
-      a.part_idx[at * K + c] = -1;
-      continue;
-    }
-    const float v = s_val[c];
-    const int32_t id = s_idx[c];
+  for (int c0 = 0; c0 < max(count, K); c0 += kScanThreads / 8) {  // 8 lanes rank one candidate
+    const int c = c0 + tid / 8;
+    const float v = c < count ? s_val[c] : 0.0f;
+    const int32_t id = c < count ? s_idx[c] : -1;  // fewer candidates than beams
     int rank = 0;  // places without an element (from lists that did not fill) come last
-#pragma unroll 4
-    for (int i = 0; i < count; ++i) {
+#pragma unroll 2
+    for (int i = tid % 8; i < count; i += 8) {
       const float o = s_val[i];
       const int32_t oi = s_idx[i];
-      rank += id < 0 ? (oi >= 0 || i < c) : (oi >= 0 && (o > v || (o == v && oi < id)));
+      rank += id < 0 ? (oi >= 0) | (i < c) : (oi >= 0) & ((o > v) | ((o == v) & (oi < id)));
     }
-    if (rank < K) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (c >= count) rank = c;
+    if (tid % 8 == 0 && rank < K) {
       a.part_val[at * K + rank] = v;
       a.part_idx[at * K + rank] = id;
     }
@@ -494,7 +505,8 @@ struct Best {
   int32_t at;       // beam and token: w 2^26 + t, in the order of w V + t
 };
 __device__ __forceinline__ bool better(const Best& x, const Best& y) {
-  return x.hi != y.hi ? x.hi > y.hi : x.lo != y.lo ? x.lo > y.lo : x.at < y.at;
+  // no branches
+  return (x.hi > y.hi) | ((x.hi == y.hi) & ((x.lo > y.lo) | ((x.lo == y.lo) & (x.at < y.at))));
 }
 __device__ __forceinline__ Best best_of_warp(const Best& b) {
   Best r;
@@ -556,6 +568,9 @@ __device__ __forceinline__ Sum log_plus(float m, const Sum& sum) {
   return out.settled();
 }
 
+// Has a kernel parameter read here: the first read of its line in the constant bank takes as long as one of memory.
+__device__ __forceinline__ void fetch(const void* p) { asm volatile("" ::"l"(p)); }
+
 struct Lists {
   int64_t first;
   int count;
@@ -576,7 +591,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
   __shared__ bool s_ended[kMaxBeams];
   __shared__ Sum s_lse[kMaxBeams];  // log-sums in two terms
   __shared__ Best s_best[2][kMergeWarps], s_list[kMergeRoom];
-  __shared__ uint32_t s_group[32];
+  __shared__ uint32_t s_group[32], s_bound;
   __shared__ int s_count;
   const int n = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = a.beams, K = a.out_beams, S = a.most_lists;
@@ -608,6 +623,8 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
   }
   const bool one = warp < W && lane < s_lists[warp].count;  // a list of the warp's first beam
   const bool first_ended = warp < W && a.finished && a.finished[n * W + warp];
+  fetch(a.part_max), fetch(a.part_sum), fetch(a.part_val), fetch(a.part_idx);
+  fetch(a.out_scores), fetch(a.out_tokens), fetch(a.out_parents), fetch(a.out_finished);
   grid_dependency_wait();
   float first_max = -INFINITY;
   Sum first_sum;
@@ -693,16 +710,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
   for (int j = 0; j < kPer; ++j) top = max(top, mine[j].hi);
   if (top) atomicMax(&s_group[lane], top);
   __syncthreads();
-  {
-    const uint32_t v = s_group[lane];
-    int rank = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t o = s_group[i];
-      rank += o > v || (o == v && i < lane);
-    }
-    top = __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, rank == K - 1)) - 1);
-  }
+  if (tid < 256 && rank_of_32(s_group, tid) == K - 1 && tid % 8 == 0) s_bound = s_group[tid / 8];
+  __syncthreads();
+  top = s_bound;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     if (mine[j].hi && mine[j].hi >= top) {
@@ -713,16 +723,17 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const __grid_const
   __syncthreads();
   const int count = s_count;
   if (count <= kMergeRoom) {
-    for (int c = tid; c < max(count, K); c += kThreads) {
-      if (c >= count) {  // fewer candidates than beams
-        write(c, Best{0, 0, 0});
-        continue;
-      }
-      const Best b = s_list[c];
+#pragma unroll 1
+    for (int c0 = 0; c0 < max(count, K); c0 += kThreads / 8) {  // 8 lanes rank one candidate
+      const int c = c0 + tid / 8;
+      const Best b = c < count ? s_list[c] : Best{0, 0, 0};  // none: fewer candidates than beams
       int rank = 0;
-#pragma unroll 4
-      for (int i = 0; i < count; ++i) rank += better(s_list[i], b);
-      if (rank < K) write(rank, b);
+#pragma unroll 2
+      for (int i = tid % 8; i < count; i += 8) rank += better(s_list[i], b);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+      if (c >= count) rank = c;
+      if (tid % 8 == 0 && rank < K) write(rank, b);
     }
     return;
   }
@@ -840,15 +851,16 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "beam scan launch: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(num_reqs));
-  const bool few = beams * y.most_lists * beams_out <= 512;
-  cfg.blockDim = dim3(few ? 256 : kMergeThreads);
+  const int most = beams * y.most_lists * beams_out;
+  cfg.blockDim = dim3(most <= 512 ? 256 : kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = few ? cudaLaunchKernelEx(&cfg, beam_merge_kernel<256, 2>, a)
+  e = most <= 512 ? cudaLaunchKernelEx(&cfg, beam_merge_kernel<256, 2>, a)
+      : most <= 1024 ? cudaLaunchKernelEx(&cfg, beam_merge_kernel<kMergeThreads, 2>, a)
           : cudaLaunchKernelEx(&cfg, beam_merge_kernel<kMergeThreads, kMaxCandidates / kMergeThreads>, a);
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "beam merge launch: %s", cudaGetErrorString(e));
   return report_error(DFLASH_OK, "");
