@@ -398,7 +398,8 @@ DFLASH_API size_t dflash_decode_workspace_size(int num_reqs, int hq, int hkv, in
  *   seq_lens   int32 [num_reqs] device. A length of 0 gives zeros and a log-sum of -inf; one that
  *              is negative or above max_ctx_len is reported and treated as 0.
  *   max_ctx_len host bound of the lengths (<= max_pages_per_req * page_size); sizes the grid and
- *              the workspace, and is otherwise free: work follows the device lengths
+ *              the workspace, and is otherwise free: work follows the device lengths. num_reqs x Hkv x
+ *              max_ctx_len (or the window) must stay below 2^36
  *   scale      <= 0 means 1/sqrt(Dh)
  *   out        bf16 or f32 [num_reqs, Hq, Dh] (out_dtype)
  *   lse        f32 [num_reqs, Hq] or NULL: log sum_j p_j

@@ -48,14 +48,11 @@ constexpr float kSlack = 8.0f;  // the running maximum may lag by 2^8
 // Warps of a block and steps that a warp has in flight. 128 KB in flight an SM are several times what the
 // latency needs, and more is slower: a ragged batch of 64 sequences took 381 us with 8 warps of 2 steps,
 // 400 with 8 of 3, 418 with 6 of 3, 426 with 12 of 2 and 456 with 7 of 4.
-template <int DH, int GT>
-struct Shape {
-  static constexpr int kWarps = 8;
-  static constexpr int kStageBytes = kStep * DH * 4;  // K and V
-  static constexpr int kStages = 2;
-  static constexpr int kThreads = kWarps * 32;
-  static constexpr int kBytes = kWarps * kStages * kStageBytes;
-};
+constexpr int kWarps = 8, kStages = 2, kThreads = kWarps * 32;
+template <int DH>
+constexpr int kStageBytes = kStep * DH * 4;  // K and V
+template <int DH>
+constexpr int kRingBytes = kWarps * kStages * kStageBytes<DH>;
 
 // The group that the boundary before a block cuts: blocks first .. last hold its parts. first = -1 where
 // nothing is cut, or an earlier boundary cuts the same group.
@@ -91,7 +88,7 @@ struct DecodeArgs {
   uint32_t page_mul, page_shift;  // j / page
   float scale_log2;
   int out_f32;
-  int64_t max_workers;
+  int max_workers;
 };
 
 __device__ __forceinline__ int page_of(const DecodeArgs& a, int j) {
@@ -109,26 +106,21 @@ __device__ __forceinline__ int steps_of(const DecodeArgs& a, int len) {
   return (len - first_row(a, len) + kStep - 1) / kStep;
 }
 
-// 64-bit division, kept out of line: inlined it made a third of the kernel's code, all of it fetched cold.
-__device__ __noinline__ int64_t divide(int64_t x, int64_t y) {
-  return x < (1ll << 32) && y < (1ll << 32) ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
-}
-
-// The workers' ranges: equal to within one step. total <= 10^12.
+// The workers' ranges: equal to within one step. A call has fewer than 2^32 steps.
 struct Ranges {
-  int64_t total, each;
-  int workers, extra;  // the first `extra` workers take each + 1 steps
+  uint32_t total, each, extra;  // the first `extra` workers take each + 1 steps
+  int workers;
 
   Ranges() = default;
-  __device__ __forceinline__ Ranges(int64_t total_, int64_t max_workers) : total(total_) {
-    workers = static_cast<int>(min(total, max_workers));
-    each = workers ? divide(total, workers) : 0;
-    extra = static_cast<int>(total - each * workers);
+  __device__ __forceinline__ Ranges(uint32_t total_, int max_workers) : total(total_) {
+    workers = static_cast<int>(min(total, static_cast<uint32_t>(max_workers)));
+    each = workers ? total / workers : 0;
+    extra = total - each * workers;
   }
-  __device__ __forceinline__ int64_t start(int w) const { return w * each + min(w, extra); }
-  __device__ __forceinline__ int owner(int64_t x) const {  // of step x
-    const int64_t cut = extra * (each + 1);
-    return static_cast<int>(x < cut ? divide(x, each + 1) : extra + divide(x - cut, each));
+  __device__ __forceinline__ uint32_t start(int w) const { return w * each + min(static_cast<uint32_t>(w), extra); }
+  __device__ __forceinline__ int owner(uint32_t x) const {  // of step x
+    const uint32_t cut = extra * (each + 1);
+    return static_cast<int>(x < cut ? x / (each + 1) : extra + (x - cut) / each);
   }
 };
 
@@ -282,22 +274,17 @@ __device__ __forceinline__ void store_head(const DecodeArgs& a, int64_t o_row, c
 }
 
 template <int DH, int GT, bool F32>
-__global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
-  using S = Shape<DH, GT>;
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int KC = DH / 32;  // 16-byte pieces of a K row per lane
   constexpr int R = GT / 8;    // head rows per lane
-  constexpr int kWarps = S::kWarps, kStages = S::kStages, kStageBytes = S::kStageBytes;
-  constexpr int kScan = S::kThreads;  // chunks of the prefix over sequences
+  constexpr int kStageBytes = dflash::kStageBytes<DH>;
+  constexpr int kScan = kThreads;  // chunks of the prefix over sequences
   extern __shared__ __align__(256) uint8_t smem[];
-  __shared__ int64_t s_warp[kWarps];
+  __shared__ uint32_t s_warp[kWarps], s_upto[kScan];  // steps of a kv head: of a warp's chunks, of a warp's up to a chunk
+  __shared__ int s_len[kScan];                        // of a chunk's first sequence
   __shared__ Segments s_seg[kWarps];
-  struct Start {
-    int64_t before;  // steps of a kv head before the chunk of sequences
-    int r, len;      // its first sequence, and that one's length
-  };
-  __shared__ Start s_start[kWarps];
   struct First {
-    int64_t start;  // of the block's first group, over the whole batch
+    uint32_t start;  // of the block's first group, over the whole batch
     int steps, r, hh;
   };
   __shared__ First s_first;
@@ -311,7 +298,6 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
   if (lane == 0) s_seg[warp] = Segments{};
   int w0 = 0, active, n_steps = 0;  // the block's first unit and how many have work; this one's steps
   int units = 0;
-  int64_t block_lo = 0;
   Cursor c;
   if (a.lone) {
     c.r = blockIdx.x / heads, c.hh = blockIdx.x - c.r * heads;
@@ -326,10 +312,10 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
     }
     __syncthreads();
   } else {
-    // ---- the schedule: a prefix over the sequences' steps, one chunk of sequences per thread; the thread
-    // whose chunk holds a unit's first step tells its warps
+    // ---- the schedule: a prefix over the sequences' steps, one chunk of sequences per thread, in which every
+    // warp looks its first step up
     const int per = (a.num_reqs + kScan - 1) / kScan;
-    int64_t mine = 0, upto;
+    uint32_t upto = 0;
     int my_len = 0;
     bool bad = false;
 #pragma unroll 1
@@ -339,61 +325,62 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
         const int raw = a.lens[r], len = valid_len(a, raw);
         bad |= len != raw;
         if (i == 0) my_len = len;
-        mine += steps_of(a, len);
+        upto += steps_of(a, len);
       }
     }
     if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, kErrMetadata);
-    upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
+    s_upto[tid] = upto, s_len[tid] = my_len;
     if (lane == 31) s_warp[warp] = upto;
     __syncthreads();
-    int64_t total = 0;
+    uint32_t total = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) upto += s_warp[i];
-      total += s_warp[i];
-    }
+    for (int i = 0; i < kWarps; ++i) total += s_warp[i];
     const Ranges ranges(total * heads, a.max_workers);
     // few workers are spread over the SMs; a block's are consecutive
-    units = (ranges.workers + gridDim.x - 1) / gridDim.x;  // of a block, at most
+    units = static_cast<int>((ranges.workers + gridDim.x - 1) / gridDim.x);  // of a block, at most
     w0 = blockIdx.x * units;
     active = max(0, min(units, ranges.workers - w0));
-#pragma unroll 1
-    for (int i = 0; i < active; ++i) {
-      const int64_t lo = ranges.start(w0 + i);
-      if (lo >= (upto - mine) * heads && lo < upto * heads) s_start[i] = Start{upto - mine, tid * per, my_len};
-    }
-    block_lo = ranges.start(w0);
     if (tid == 0) s_ranges = ranges;
-    __syncthreads();
     if (my_unit < active) {
-      // ---- the group that holds step lo
-      const int64_t lo = ranges.start(w0 + my_unit);
-      n_steps = static_cast<int>(ranges.start(w0 + my_unit + 1) - lo);  // at most 10^12 over 8 warps an SM
-      const Start at = s_start[my_unit];
-      int64_t base = at.before;
-      c.r = at.r;
-      set_len(a, c, at.len);
-      if (per > 1) {  // the sequence within the chunk, by warp scans
+      // ---- the group that holds step lo: the warp's chunks, the chunk, the sequence
+      const uint32_t lo = ranges.start(w0 + my_unit);
+      n_steps = static_cast<int>(ranges.start(w0 + my_unit + 1) - lo);
+      uint32_t base = 0, sum = 0;
+      int from = 0;
+#pragma unroll
+      for (int i = 0; i + 1 < kWarps; ++i) {
+        sum += s_warp[i];
+        if (sum * heads <= lo) base = sum, from = 32 * (i + 1);
+      }
+      {
+        const uint32_t x = s_upto[from + lane];
+        const int src = __ffs(__ballot_sync(0xffffffffu, (base + x) * heads > lo)) - 1;
+        const uint32_t y = __shfl_sync(0xffffffffu, x, max(src - 1, 0));
+        if (src > 0) base += y;
+        from += src;
+      }
+      c.r = from * per;
+      set_len(a, c, s_len[from]);
+      if (per > 1) {
 #pragma unroll 1
         for (int i = 0; i < per; i += 32) {
-          const int r = at.r + i + lane;
+          const int r = from * per + i + lane;
           const int len = i + lane < per && r < a.num_reqs ? valid_len(a, a.lens[r]) : 0;
-          const int n = steps_of(a, len);
-          int64_t x = n;
+          uint32_t x = steps_of(a, len);
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
           }
           const uint32_t hit = __ballot_sync(0xffffffffu, (base + x) * heads > lo);
           if (hit) {
             const int src = __ffs(hit) - 1;
-            c.r = at.r + i + src;
+            c.r = from * per + i + src;
             set_len(a, c, __shfl_sync(0xffffffffu, len, src));
             base += __shfl_sync(0xffffffffu, x, src) - c.steps;
             break;
@@ -401,9 +388,9 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
           base += __shfl_sync(0xffffffffu, x, 31);
         }
       }
-      const int64_t rest = lo - base * heads;
-      c.hh = static_cast<int>(divide(rest, c.steps));
-      c.step = static_cast<int>(rest - static_cast<int64_t>(c.hh) * c.steps);
+      const uint32_t rest = lo - base * heads;
+      c.hh = static_cast<int>(rest / c.steps);
+      c.step = static_cast<int>(rest - static_cast<uint32_t>(c.hh) * c.steps);
       if (warp == 0 && lane == 0) s_first = First{lo - c.step, c.steps, c.r, c.hh};
     }
   }
@@ -661,22 +648,22 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
 
   // ---- join what the block's units share, a (run of parts, tile, head) per warp and turn. Run 0 is the
   // group that began in an earlier block, run i + 1 the one that unit i began and did not end.
-  // A lane looks at one item: (active + 1) * unit <= 16, GT <= 16, 8 warps: at most 32 a warp.
+  // A lane looks at one item: (active + 1) * unit <= 16, GT <= 16, 8 warps: at most 32 a warp. Units' flags are
+  // bits; all tiles of a unit have the same.
+  const Segments flags = s_seg[lane < active ? lane * a.unit : 0];
+  const uint32_t ends = __ballot_sync(0xffffffffu, lane < active && flags.ends);
+  const uint32_t opens = __ballot_sync(0xffffffffu, lane < active && flags.opens);
+  const uint32_t mids = __ballot_sync(0xffffffffu, lane < active && flags.mid);
+  const bool continues = s_seg[0].continues && active > 0;
   int my_run = -1, my_tile = 0, my_last = 0;
   bool my_ended = false;
-  if (active > 0) {
-    const int item = warp + lane * kWarps, x = item / GT;
-    const int run = x / a.unit, tile = x - run * a.unit;
-    if (run <= active) {
-      const int first = run == 0 ? 0 : run - 1;
-      const Segments& head = s_seg[first * a.unit];
-      if (run == 0 ? head.continues : head.opens) {
-        my_run = run, my_tile = tile;
-        my_ended = run == 0 && head.ends;
-        my_last = first;  // the run ends with its group or with the block
-#pragma unroll 1
-        while (!my_ended && my_last + 1 < active) my_ended = s_seg[++my_last * a.unit].ends;
-      }
+  {
+    const int x = (warp + lane * kWarps) / GT, run = x / a.unit, first = run == 0 ? 0 : run - 1;
+    if (run <= active && (run == 0 ? continues : (opens >> first & 1) != 0)) {
+      my_run = run, my_tile = x - run * a.unit;
+      const uint32_t end = ends >> run << run;  // the run ends with its group or with the block
+      my_ended = end != 0;
+      my_last = end ? __ffs(end) - 1 : active - 1;
     }
   }
   uint32_t hits = __ballot_sync(0xffffffffu, my_run >= 0);
@@ -694,7 +681,7 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
     float o[DH / 32], m, l;
     merge_parts<DH>(last - first + 1, 0, 1, [&](int p) {
       const int x = (first + p) * a.unit + tile;
-      if ((p > 0 || inherited) && s_seg[x].mid) {
+      if ((p > 0 || inherited) && (mids >> (first + p) & 1)) {
         const int64_t at = (static_cast<int64_t>(w0 + first + p) * a.unit + tile) * GT + h;
         return Part{a.part_o + at * DH, a.part_ml + at * 2};
       }
@@ -711,7 +698,7 @@ __global__ void __launch_bounds__(Shape<DH, GT>::kThreads, 1) decode_kernel(cons
   }
   if (tid == kScan - 1 && !a.lone) {  // for the join kernel
     Record rec{0, 0, -1, -1};
-    if (active > 0 && s_first.start < block_lo) {
+    if (active > 0 && s_first.start < s_ranges.start(w0)) {
       const int from = s_ranges.owner(s_first.start) / units;
       if (from == static_cast<int>(blockIdx.x) - 1)
         rec = Record{s_first.r, s_first.hh, from, s_ranges.owner(s_first.start + s_first.steps - 1) / units};
@@ -787,36 +774,34 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 }
 
 struct Layout {
-  int gt, tiles, unit, tile_units, grid;
-  int64_t workers;
-  double bound;  // most steps of a call
+  int gt, unit, tile_units, grid;
+  int workers;
   bool lone, split;
   size_t rec, ml, o, block_ml, block_o, total;
 };
 
 int head_tile(int g) { return g <= 8 ? 8 : 16; }
-int warps_of(int dh, int gt) {
-  return dh == 128 ? (gt == 8 ? Shape<128, 8>::kWarps : Shape<128, 16>::kWarps)
-                   : (gt == 8 ? Shape<64, 8>::kWarps : Shape<64, 16>::kWarps);
+int head_tiles(int hq, int hkv) { return (hq / hkv + head_tile(hq / hkv) - 1) / head_tile(hq / hkv); }
+// units of a kv head: a unit's warps, at most a block's, read the same rows, so that they come from HBM once
+int tile_units(int hq, int hkv) { return (head_tiles(hq, hkv) + kWarps - 1) / kWarps; }
+int64_t most_steps(int max_ctx_len, int window) {  // of a sequence and kv head
+  return ((window > 0 ? std::min(max_ctx_len, window) : max_ctx_len) + static_cast<int64_t>(kStep) - 1) / kStep;
+}
+double most_steps_of_call(int num_reqs, int hq, int hkv, int max_ctx_len, int window) {
+  return static_cast<double>(most_steps(max_ctx_len, window)) * hkv * tile_units(hq, hkv) * num_reqs;
 }
 
 Layout layout_of(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int window, int sms) {
   Layout y{};
-  const int g = hq / hkv;
-  y.gt = head_tile(g);
-  y.tiles = (g + y.gt - 1) / y.gt;
-  // a unit's warps read the same rows, so that they come from HBM once; at most a block's warps
-  const int warps = warps_of(dh, y.gt);
-  y.tile_units = (y.tiles + warps - 1) / warps;
-  y.unit = (y.tiles + y.tile_units - 1) / y.tile_units;
-  const int64_t rows = window > 0 ? std::min(max_ctx_len, window) : max_ctx_len;
-  const int64_t steps = (rows + kStep - 1) / kStep;
-  y.bound = static_cast<double>(steps) * hkv * y.tile_units * num_reqs;
-  const int64_t most = static_cast<int64_t>(sms) * (warps / y.unit);
-  y.workers = y.bound < static_cast<double>(most) ? std::max<int64_t>(1, static_cast<int64_t>(y.bound)) : most;
-  y.grid = static_cast<int>(std::min<int64_t>(sms, y.workers));
+  y.gt = head_tile(hq / hkv);
+  y.tile_units = tile_units(hq, hkv);
+  const int tiles = head_tiles(hq, hkv);
+  y.unit = (tiles + y.tile_units - 1) / y.tile_units;
+  y.workers = static_cast<int>(std::min(static_cast<double>(sms * (kWarps / y.unit)),
+                                        std::max(1.0, most_steps_of_call(num_reqs, hq, hkv, max_ctx_len, window))));
+  y.grid = std::min(sms, y.workers);
   const double groups = static_cast<double>(num_reqs) * hkv * y.tile_units;
-  y.lone = groups <= sms && steps <= kLoneSteps;
+  y.lone = groups <= sms && most_steps(max_ctx_len, window) <= kLoneSteps;
   if (y.lone) y.grid = std::max(1, static_cast<int>(groups));
   y.split = !y.lone && y.grid > 1;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -838,15 +823,17 @@ int check(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int window) {
   if (num_reqs < 0 || max_ctx_len < 0) return errorf(DFLASH_ERR_INVALID_ARG, "negative size argument");
   if (window < 0) return errorf(DFLASH_ERR_INVALID_ARG, "window must be >= 0");
   if (max_ctx_len > 0x7fffffff - 64) return errorf(DFLASH_ERR_UNSUPPORTED, "max_ctx_len must be below 2^31 - 64");
+  if (most_steps_of_call(num_reqs, hq, hkv, max_ctx_len, window) > 4294967295.0)
+    return errorf(DFLASH_ERR_UNSUPPORTED, "too many rows for one call: num_reqs x Hkv x max_ctx_len must stay below 2^36");
   return DFLASH_OK;
 }
 
 template <int DH, int GT, bool F32>
 cudaError_t launch(const DecodeArgs& a, const Layout& y, cudaStream_t st) {
-  constexpr int kBytes = Shape<DH, GT>::kBytes;
+  constexpr int kBytes = kRingBytes<DH>;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<DH, GT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  decode_kernel<DH, GT, F32><<<y.grid, Shape<DH, GT>::kThreads, kBytes, st>>>(a);
+  decode_kernel<DH, GT, F32><<<y.grid, kThreads, kBytes, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !y.split) return e;
   cudaLaunchConfig_t cfg{};
@@ -909,7 +896,6 @@ int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const 
   rc = query_sms(&sms);
   if (rc != DFLASH_OK) return rc;
   const Layout y = layout_of(num_reqs, hq, hkv, dh, max_ctx_len, window, sms);
-  if (y.bound > 1e12) return errorf(DFLASH_ERR_UNSUPPORTED, "too many rows for one call (%.3g steps)", y.bound);
   if (workspace_bytes < y.total)
     return errorf(DFLASH_ERR_WORKSPACE, "workspace has %zu bytes; %zu are needed", workspace_bytes, y.total);
   char* ws = static_cast<char*>(workspace);

@@ -54,7 +54,7 @@ def _decode(n=2, hq=8, hkv=2, dh=64, pages=8, page=16, width=4, most=64, scale=0
     (dict(page=0), D.ERR_INVALID_ARG), (dict(most=65), D.ERR_INVALID_ARG), (dict(window=-1), D.ERR_INVALID_ARG),
     (dict(scale=math.inf), D.ERR_INVALID_ARG), (dict(dt=2), D.ERR_INVALID_ARG), (dict(stride=3), D.ERR_INVALID_ARG),
     (dict(pages=0), D.ERR_INVALID_ARG), (dict(pages=1 << 28), D.ERR_UNSUPPORTED), (dict(qs=100), D.ERR_INVALID_ARG),
-    (dict(qs=504), D.ERR_INVALID_ARG), (dict(q=None), D.ERR_INVALID_ARG), (dict(ws=128), D.ERR_WORKSPACE),
+    (dict(n=1 << 20, width=1 << 13, stride=1 << 13, most=1 << 17), D.ERR_UNSUPPORTED), (dict(qs=504), D.ERR_INVALID_ARG), (dict(q=None), D.ERR_INVALID_ARG), (dict(ws=128), D.ERR_WORKSPACE),
 ])
 def test_decode_refusals(kw, code):
     assert _decode(**kw) == code and D.load().dflash_last_error()
