@@ -44,7 +44,7 @@ struct ForkArgs {
   int32_t* table;
   int64_t stride;
   int32_t* refs;
-  int rows, width, cols;  // cols = table columns per block
+  int rows, width, shift;  // 2^shift table columns per block
   int64_t num_pages;
   uint32_t* err;
 };
@@ -53,33 +53,35 @@ struct ForkArgs {
 // counts by (children - 1) of the row an entry was in, and writes every row's columns from its parent's.
 __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ ForkArgs a) {
   extern __shared__ int32_t s_mem[];
-  int32_t* s_old = s_mem;                                      // [rows][cols]
-  int32_t* s_par = s_old + static_cast<int64_t>(a.rows) * a.cols;
+  const int wide = 1 << a.shift;
+  int32_t* s_old = s_mem;  // [rows][wide]
+  int32_t* s_par = s_old + (static_cast<int64_t>(a.rows) << a.shift);
   int32_t* s_children = s_par + a.rows;
   int32_t* s_lens = s_children + a.rows;
-  const int c0 = blockIdx.x * a.cols, cols = min(a.cols, a.width - c0);
-  const int cells = a.rows * a.cols;
+  const int c0 = blockIdx.x << a.shift, cols = min(wide, a.width - c0);
+  const int cells = a.rows << a.shift;
   for (int r = threadIdx.x; r < a.rows; r += kThreads) {
+    s_par[r] = a.parent[r];
     s_children[r] = 0;
     if (blockIdx.x == 0) s_lens[r] = a.lens[r];
   }
+#pragma unroll 8
   for (int i = threadIdx.x; i < cells; i += kThreads) {
-    const int r = i / a.cols, c = i - r * a.cols;
+    const int r = i >> a.shift, c = i & (wide - 1);
     s_old[i] = c < cols ? a.table[r * a.stride + c0 + c] : -1;
   }
   __syncthreads();
   for (int r = threadIdx.x; r < a.rows; r += kThreads) {
-    int p = a.parent[r];
+    int p = s_par[r];
     if (p < -1 || p >= a.rows) {
       if (blockIdx.x == 0) report(a.err);
-      p = r;  // such a row stays as it is
+      s_par[r] = p = r;  // such a row stays as it is
     }
-    s_par[r] = p;
     if (p >= 0) atomicAdd(&s_children[p], 1);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < cells; i += kThreads) {
-    const int r = i / a.cols, c = i - r * a.cols;
+    const int r = i >> a.shift, c = i & (wide - 1);
     if (c >= cols) continue;
     const int old = s_old[i], more = s_children[r] - 1;
     if (old >= 0 && more != 0) {
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
       else report(a.err);
     }
     const int p = s_par[r];
-    if (p != r) a.table[r * a.stride + c0 + c] = p < 0 ? -1 : s_old[p * a.cols + c];
+    if (p != r) a.table[r * a.stride + c0 + c] = p < 0 ? -1 : s_old[(p << a.shift) + c];
   }
   if (blockIdx.x == 0)
     for (int r = threadIdx.x; r < a.rows; r += kThreads)
@@ -95,23 +97,30 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ counting and ranking pages
-// Flags of up to kThreads consecutive pages: this thread's rank among the flagged ones of the block,
-// and their number. Every thread of the block calls it.
-__device__ __forceinline__ int block_rank(bool flag, int* count) {
-  __shared__ int s_warp[kThreads / 32];
+constexpr int kRun = 4;  // consecutive pages of a thread
+
+// Sum of n over the threads before this one, and over all. Calls in a row pass round = 0, 1, 2, ..: each has
+// one barrier, and uses the array of the call before the last.
+__device__ __forceinline__ int block_prefix(int n, int round, int* all) {
+  __shared__ int s_warp[2][kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t mask = __ballot_sync(0xffffffffu, flag);
+  int x = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[round & 1][warp] = x;
   __syncthreads();
-  if (lane == 0) s_warp[warp] = __popc(mask);
-  __syncthreads();
-  int before = __popc(mask & ((1u << lane) - 1)), all = 0;
+  x -= n;
+  int sum = 0;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += s_warp[i];
-    all += s_warp[i];
+    if (i < warp) x += s_warp[round & 1][i];
+    sum += s_warp[round & 1][i];
   }
-  *count = all;
-  return before;
+  *all = sum;
+  return x;
 }
 
 // Sum over the block of x (every thread gets it).
@@ -128,10 +137,11 @@ __device__ __forceinline__ int block_sum(int x) {
   return x;
 }
 
-__device__ __forceinline__ int count_chunk(const int32_t* refs, int64_t num_pages, int chunk, bool want_used) {
+__device__ __forceinline__ int count_chunk(const int32_t* refs, int64_t num_pages, int chunk) {
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * chunk, hi = min(lo + chunk, num_pages);
   int n = 0;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) n += (refs[i] != 0) == want_used;
+#pragma unroll 4
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) n += refs[i] != 0;
   return block_sum(n);
 }
 
@@ -180,13 +190,17 @@ __global__ void __launch_bounds__(kThreads) reserve_count_kernel(const __grid_co
   grid_dependents_launch();
   if (static_cast<int>(blockIdx.x) < a.chunks) {
     const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk, hi = min(lo + a.chunk, a.num_pages);
-    int found = 0;
-    for (int64_t i0 = lo; i0 < hi; i0 += kThreads) {
-      const int64_t i = i0 + threadIdx.x;
-      const bool free = i < hi && a.refs[i] == 0;
-      int count;
-      const int rank = block_rank(free, &count);
-      if (free) a.fresh[lo + found + rank] = static_cast<int32_t>(i);
+    int found = 0, round = 0;
+    for (int64_t i0 = lo; i0 < hi; i0 += kThreads * kRun, ++round) {
+      const int64_t i = i0 + threadIdx.x * kRun;
+      bool free[kRun];
+      int n = 0, count;
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) n += free[j] = i + j < hi && a.refs[i + j] == 0;
+      int64_t at = lo + found + block_prefix(n, round, &count);
+#pragma unroll
+      for (int j = 0; j < kRun; ++j)
+        if (free[j]) a.fresh[at++] = static_cast<int32_t>(i + j);
       found += count;
     }
     if (threadIdx.x == 0) a.counts[blockIdx.x] = found;
@@ -207,7 +221,8 @@ __global__ void __launch_bounds__(kThreads) reserve_count_kernel(const __grid_co
       int lo, hi;
       touched(a, len, count, &lo, &hi);
       int32_t* row = a.table + r * a.stride;
-      for (int p0 = lo; p0 < hi; p0 += 32) {
+      int p0 = lo;
+      for (; p0 < hi && !bad; p0 += 32) {
         const int p = p0 + lane;
         bool take = false, wrong = false;
         int e = -1;
@@ -223,15 +238,15 @@ __global__ void __launch_bounds__(kThreads) reserve_count_kernel(const __grid_co
             if (take && partial) src = e, live = len % a.page;
           }
         }
-        bad |= __any_sync(0xffffffffu, wrong);
+        bad = __any_sync(0xffffffffu, wrong);
         need += __popc(__ballot_sync(0xffffffffu, take));
+        // mark the shared pages among them for the apply launch, which must not look at the counts that
+        // other rows are lowering: entry e becomes -2 - e
+        if (!bad && take && e >= 0) row[p] = -2 - e;
       }
-      // mark the shared pages among them for the apply launch, which must not look at the counts that
-      // other rows are lowering: entry e becomes -2 - e
-      for (int p = lo + lane; p < hi && !bad; p += 32) {
-        const int e = row[p];
-        if (e >= 0 && a.refs[e] > 1) row[p] = -2 - e;
-      }
+      // entries of the steps before the one found bad are as they should be: their marks are taken back
+      for (int p = lo + lane; bad && p < p0 - 32; p += 32)
+        if (row[p] < -1) row[p] = -2 - row[p];
     }
     if (bad) need = kBadRow, src = -1;
   }
@@ -242,36 +257,21 @@ __global__ void __launch_bounds__(kThreads) reserve_count_kernel(const __grid_co
   }
 }
 
-// 16-byte copies of `bytes` (a multiple of 16) by the block.
-__device__ __forceinline__ void block_copy(void* dst, const void* src, int64_t bytes) {
-  uint4* d = static_cast<uint4*>(dst);
-  const uint4* s = static_cast<const uint4*>(src);
-  const int64_t n = bytes / 16;
-  constexpr int U = 4;
-  for (int64_t i = threadIdx.x; i < n; i += kThreads * U) {
-    uint4 v[U];
+// A copy of up to kPiece bytes (a multiple of 16) by the block, in 16-byte accesses, as its two halves.
+constexpr int kLoads = kPiece / 16 / kThreads;
+struct Piece {
+  uint4 v[kLoads];
+  __device__ __forceinline__ void load(const void* src, int bytes) {
 #pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (i + j * kThreads < n) v[j] = s[i + j * kThreads];
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (i + j * kThreads < n) d[i + j * kThreads] = v[j];
+    for (int j = 0; j < kLoads; ++j)
+      if (threadIdx.x + j * kThreads < bytes / 16) v[j] = static_cast<const uint4*>(src)[threadIdx.x + j * kThreads];
   }
-}
-
-// Sum over the block of x in 64 bits (every thread gets it).
-__device__ __forceinline__ int64_t block_sum64(int64_t x) {
-  __shared__ int64_t s_part[kThreads / 32];
+  __device__ __forceinline__ void store(void* dst, int bytes) const {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) x += s_part[i];
-  return x;
-}
+    for (int j = 0; j < kLoads; ++j)
+      if (threadIdx.x + j * kThreads < bytes / 16) static_cast<uint4*>(dst)[threadIdx.x + j * kThreads] = v[j];
+  }
+};
 
 // Blocks (r, y) serve row r: y = 0 its table, counts, slots and length, all of them a share of the copy of
 // its live rows out of a shared page (which nothing else in this launch touches). Where a row's pages start
@@ -280,41 +280,60 @@ __device__ __forceinline__ int64_t block_sum64(int64_t x) {
 __global__ void __launch_bounds__(kThreads) reserve_apply_kernel(const __grid_constant__ ReserveArgs a,
                                                                  const __grid_constant__ Pools pools, int64_t page_bytes) {
   extern __shared__ int32_t s_ends[];  // [chunks] free pages up to and with a chunk
+  __shared__ int64_t s_sum[kThreads / 32];
+  __shared__ int32_t s_page[32];  // of the first pages that the row's new rows touch
   grid_dependency_wait();
-  const int r = blockIdx.x;
+  // the loads first, so that they wait together
+  const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first_need = threadIdx.x < a.rows ? a.need[threadIdx.x] : 0;
+  const int first_count = threadIdx.x < a.chunks ? a.counts[threadIdx.x] : 0;
   const int need = a.need[r], len = a.lens[r];
-  const int s0 = a.starts[r], s1 = a.starts[r + 1];
-  int64_t before = 0;
-  bool bad_starts = false;
-  for (int i = threadIdx.x; i < a.rows; i += kThreads) {
-    const int n = a.need[i];
-    bad_starts |= n == kBadStarts;
-    if (i < r && n > 0) before += n;
+  const int s0 = a.starts[r], s1 = a.starts[r + 1], src = a.copy_src[r];
+  // this block's share of the copy: pieces blockIdx.y, blockIdx.y + gridDim.y, .. of all pools' (in the first
+  // before the page that it goes to is known)
+  const int64_t bytes = src >= 0 ? a.copy_live[r] * (page_bytes / a.page) : 0;
+  const int per_pool = static_cast<int>((bytes + kPiece - 1) / kPiece), pieces = pools.n * per_pool;
+  auto place = [&](int i, int* size) {
+    const int pool = i / per_pool;
+    const int64_t at = static_cast<int64_t>(i - pool * per_pool) * kPiece;
+    *size = static_cast<int>(min(bytes - at, static_cast<int64_t>(kPiece)));
+    return static_cast<char*>(pools.p[pool]) + at;
+  };
+  Piece piece;
+  char* base = nullptr;
+  int size = 0, next = blockIdx.y;
+  if (next < pieces) {
+    base = place(next, &size);
+    piece.load(base + src * page_bytes, size);
   }
-  bad_starts = __syncthreads_or(bad_starts);
-  before = block_sum64(before);
+  int32_t* row = a.table + r * a.stride;
+  int lo = 0, hi = 0, first_entry = 0;
+  if (need >= 0) touched(a, len, s1 - s0, &lo, &hi);
+  if (blockIdx.y == 0 && warp == 0 && lo + lane < hi) first_entry = row[lo + lane];
+  // pages that the rows before take, and rows of bad starts in the bits above
+  constexpr int64_t kBad = 1ll << 48;
+  int64_t sum = 0;
+  for (int i = threadIdx.x; i < a.rows; i += kThreads) {
+    const int n = i < kThreads ? first_need : a.need[i];
+    if (n == kBadStarts) sum += kBad;
+    if (i < r && n > 0) sum += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[warp] = sum;
   int free_pages = 0;  // a running sum over the chunks, kThreads at a time
-  for (int i0 = 0; i0 < a.chunks; i0 += kThreads) {
-    const int i = i0 + threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    __shared__ int s_warp[kThreads / 32];
-    int x = i < a.chunks ? a.counts[i] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    int all = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) x += s_warp[w];
-      all += s_warp[w];
-    }
-    if (i < a.chunks) s_ends[i] = free_pages + x;
+  for (int i0 = 0, round = 0; i0 < a.chunks; i0 += kThreads, ++round) {
+    const int i = i0 + threadIdx.x, n = i0 == 0 ? first_count : i < a.chunks ? a.counts[i] : 0;
+    int all;
+    const int x = block_prefix(n, round, &all);
+    if (i < a.chunks) s_ends[i] = free_pages + x + n;
     free_pages += all;
   }
+  sum = 0;  // at least one barrier has passed
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) sum += s_sum[i];
+  const bool bad_starts = sum >= kBad;
+  const int64_t before = sum & (kBad - 1);
   __syncthreads();
   const bool served = !bad_starts && need >= 0 && (need == 0 || before + need <= free_pages);
   auto free_page = [&](int k) {  // the k-th free page: its chunk by bisection
@@ -326,37 +345,33 @@ __global__ void __launch_bounds__(kThreads) reserve_apply_kernel(const __grid_co
     return a.fresh[static_cast<int64_t>(lo) * a.chunk + (k - (lo ? s_ends[lo - 1] : 0))];
   };
 
-  const int src = a.copy_src[r];
-  if (served && src >= 0) {
-    const int dst = free_page(static_cast<int>(before));  // the partial page is the first that the row takes
-    const int64_t bytes = a.copy_live[r] * (page_bytes / a.page);
-    const int pieces = static_cast<int>((bytes + kPiece - 1) / kPiece);
-    for (int i = blockIdx.y; i < pools.n * pieces; i += gridDim.y) {
-      const int pool = i / pieces;
-      const int64_t at = static_cast<int64_t>(i - pool * pieces) * kPiece;
-      char* base = static_cast<char*>(pools.p[pool]) + at;
-      block_copy(base + dst * page_bytes, base + src * page_bytes, min(bytes - at, static_cast<int64_t>(kPiece)));
+  if (served && next < pieces) {
+    const int64_t dst = free_page(static_cast<int>(before)) * page_bytes;  // the partial page is the first that the row takes
+    piece.store(base + dst, size);
+    for (next += gridDim.y; next < pieces; next += gridDim.y) {
+      base = place(next, &size);
+      piece.load(base + src * page_bytes, size);
+      piece.store(base + dst, size);
     }
   }
   if (blockIdx.y != 0) return;
 
-  int32_t* row = a.table + r * a.stride;
-  if (threadIdx.x < 32 && need > 0) {
-    const int lane = threadIdx.x;
-    int lo, hi, done = 0;
-    touched(a, len, s1 - s0, &lo, &hi);
+  if (warp == 0) {
+    int done = 0;
     for (int p0 = lo; p0 < hi; p0 += 32) {
       const int p = p0 + lane;
-      const int e = p < hi ? row[p] : 0;
+      int e = p0 == lo ? first_entry : p < hi ? row[p] : 0;
       const uint32_t mask = __ballot_sync(0xffffffffu, e < 0);
       if (e < 0 && served) {
         const int page = free_page(static_cast<int>(before) + done + __popc(mask & ((1u << lane) - 1)));
         row[p] = page;
         a.refs[page] = 1;
         if (e < -1) atomicSub(a.refs + (-2 - e), 1);
+        e = page;
       } else if (e < -1) {
         row[p] = -2 - e;  // refused: as it was
       }
+      if (p0 == lo) s_page[lane] = e;
       done += __popc(mask);
     }
   }
@@ -370,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) reserve_apply_kernel(const __grid_co
   if (served) {
     for (int t = s0 + threadIdx.x; t < s1; t += kThreads) {
       const int p = len + (t - s0), page = p / a.page;
-      a.slots[t] = row[page] * a.page + (p - page * a.page);
+      a.slots[t] = (page - lo < 32 ? s_page[page - lo] : row[page]) * a.page + (p - page * a.page);
       a.positions[t] = p;
     }
     if (threadIdx.x == 0 && a.advance) a.lens[r] = len + (s1 - s0);
@@ -404,7 +419,7 @@ struct CompactArgs {
 
 __global__ void __launch_bounds__(kThreads) compact_count_kernel(const __grid_constant__ CompactArgs a) {
   grid_dependents_launch();
-  const int n = count_chunk(a.refs, a.num_pages, a.chunk, true);
+  const int n = count_chunk(a.refs, a.num_pages, a.chunk);
   if (threadIdx.x == 0) a.counts[blockIdx.x] = n;
 }
 
@@ -424,18 +439,24 @@ __global__ void __launch_bounds__(kThreads) compact_rank_kernel(const __grid_con
   const int below = block_sum(part);
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.moved = all - below;
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk, hi = min(lo + a.chunk, a.num_pages);
-  for (int64_t i0 = lo; i0 < hi; i0 += kThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool used = i < hi && a.refs[i] != 0;
-    int count;
-    const int u = before + block_rank(used, &count);  // used pages before page i
-    if (i < hi) {
-      if (i < all) {
-        if (!used) a.to[i - u] = static_cast<int32_t>(i);
-      } else {
-        a.rank[i] = used ? u - below : -1;
-        if (used) a.from[u - below] = static_cast<int32_t>(i);
+  int round = 0;
+  for (int64_t i0 = lo; i0 < hi; i0 += kThreads * kRun, ++round) {
+    const int64_t i = i0 + threadIdx.x * kRun;
+    bool used[kRun];
+    int n = 0, count;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) n += used[j] = i + j < hi && a.refs[i + j] != 0;
+    int u = before + block_prefix(n, round, &count);  // used pages before page i + j
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      const int64_t page = i + j;
+      if (page < all) {
+        if (!used[j] && page < hi) a.to[page - u] = static_cast<int32_t>(page);
+      } else if (page < hi) {
+        a.rank[page] = used[j] ? u - below : -1;
+        if (used[j]) a.from[u - below] = static_cast<int32_t>(page);
       }
+      u += used[j];
     }
     before += count;
   }
@@ -475,7 +496,10 @@ __global__ void __launch_bounds__(kThreads) compact_apply_kernel(const __grid_co
     const int rest = static_cast<int>(i - k * per), pool = rest / pieces;
     const int64_t at = static_cast<int64_t>(rest - pool * pieces) * kPiece;
     char* base = static_cast<char*>(pools.p[pool]) + at;
-    block_copy(base + a.to[k] * page_bytes, base + a.from[k] * page_bytes, min(page_bytes - at, static_cast<int64_t>(kPiece)));
+    const int size = static_cast<int>(min(page_bytes - at, static_cast<int64_t>(kPiece)));
+    Piece piece;
+    piece.load(base + a.from[k] * page_bytes, size);
+    piece.store(base + a.to[k] * page_bytes, size);
   }
 }
 
@@ -566,7 +590,7 @@ int dflash_fork_pages(const int32_t* parent, int32_t* seq_lens, int32_t* block_t
   auto bytes = [&](int c) { return (static_cast<int64_t>(c) + 3) * num_reqs * 4; };
   while (cols > 1 && bytes(cols) > kSmem) cols /= 2;
   if (bytes(cols) > kSmem) return errorf(DFLASH_ERR_UNSUPPORTED, "too many table rows to fork at once (%d)", num_reqs);
-  a.cols = cols;
+  while ((1 << a.shift) < cols) ++a.shift;
   cudaError_t e = cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "fork set-up: %s", cudaGetErrorString(e));
   const unsigned grid = static_cast<unsigned>(std::max(1, (max_pages_per_req + cols - 1) / cols));
@@ -628,9 +652,10 @@ int dflash_reserve_pages(const int32_t* new_start_loc, int32_t* seq_lens, int32_
   reserve_count_kernel<<<a.chunks + row_blocks, kThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) {
-    // blocks of a row: its copy in pieces, as many as give every SM a few
+    // blocks of a row: its copy in pieces, as many as are resident at once (four an SM; eight: 1.4 us more for a
+    // step of 256 rows, since every block sums the rows before its own)
     const int64_t pieces = num_pools ? num_pools * ((page_bytes + kPiece - 1) / kPiece) : 1;
-    const int64_t shares = std::max<int64_t>(1, std::min<int64_t>({pieces, static_cast<int64_t>(sms) * 8 / num_reqs, 65535}));
+    const int64_t shares = std::max<int64_t>(1, std::min<int64_t>({pieces, static_cast<int64_t>(sms) * 4 / num_reqs, 65535}));
     e = launch_after(reserve_apply_kernel, dim3(static_cast<unsigned>(num_reqs), static_cast<unsigned>(shares)),
                      static_cast<size_t>(a.chunks) * 4, st, a, p, page_bytes);
   }
