@@ -407,8 +407,8 @@ DFLASH_API size_t dflash_decode_workspace_size(int num_reqs, int hq, int hkv, in
  *              table entry outside [0, num_pages) (page 0 is read in its place)
  *   Dh in {64, 128}; Hq % Hkv == 0, any group size. bf16 products are exact, sums f32; the weights
  *   keep 16 bits for a bf16 output and 24 for an f32 one. Two launches (attention, join), or one
- *   where max_ctx_len (or the window) is at most 512 and there are no more (sequence, kv head)
- *   pairs than SMs. Results do not depend on timing. Rows outside the lengths and the window may hold
+ *   where max_ctx_len (or the window) is at most 512 (less past 16 heads a group) and there are no
+ *   more (sequence, kv head) pairs than SMs. Results do not depend on timing. Rows outside the lengths and the window may hold
  *   anything; a stored value that is infinite gives NaN in its column.
  */
 DFLASH_API int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const dflash_bf16* k_pool,

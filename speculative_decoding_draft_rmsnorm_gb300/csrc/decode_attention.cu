@@ -11,21 +11,28 @@
 // take over. So the design is about keeping loads in flight and nothing else waiting:
 //
 // - The worker is a WARP, not a block: it owns a contiguous range of 16-row steps of the batch laid
-//   end to end (sequence, then kv head, then steps), keeps its own (m, l, O), and never synchronises
-//   with another warp. Ranges are equal to within a step, whatever the raggedness.
+//   end to end (sequence, then kv head, then steps), keeps its own (m, l, O), and synchronises with no
+//   other warp before its range is done. Ranges are equal to within a step, whatever the raggedness.
 // - A warp copies its rows with cp.async into shared memory of its own, whole rows by neighbouring
 //   lanes (pieces chosen by who will use them fetched every sector twice: 4.0 TB/s), 16-byte pieces
 //   permuted within a row so that the fragment reads are free of bank conflicts. The order of a
-//   contraction's terms is free, so a lane's fragment is 8 consecutive elements of a row instead of the
-//   instruction's 2 + 2: 16-byte reads, and V needs no transposition beyond pairing rows in registers.
+//   contraction's terms is free, so a lane's fragment of Q and K is 8 consecutive elements of a row instead
+//   of the instruction's 2 + 2: one 16-byte read. V is read transposed (ldmatrix).
 // - The group's heads are the 16 rows of mma.m16n8k16 (K and V rows are its columns). At <= 8 heads the
 //   spare rows 8..15 carry the rounding remainder of P, so P has 16 significant bits at no cost; f32
-//   outputs add a third term (24 bits). The idle rows cost nothing that matters: tensor work is a few
-//   per cent of the step's time, set by the loads.
-// - A worker stores a group that it holds whole; else it leaves (m, l, O) in one of its two slots. The
-//   warps of a block hold consecutive ranges, so the block joins what its warps share, and the join
-//   kernel what blocks share: at most two parts a block. All merges go in a fixed order: the result does
-//   not depend on timing. (Joining a lone 32000-row sequence from 1824 warps' parts took 20 us more.)
+//   outputs add a third term (24 bits). The idle rows cost nothing that matters: the tensor pipe is active
+//   in 17% of a batch's cycles, waiting for the loads. Past 16 heads a group that ends: each tile of 16 heads is
+//   a warp that copies the same rows for itself (from L2), and 32 heads a group take 69 us where 16 take 52
+//   (32 sequences of 4096 rows, 537 MB; floor 39.5). Rings shared by such warps were slower (84 us): it is the
+//   work of a step that bounds them, not its copy.
+// - A worker stores a group that it holds whole; of others it leaves (m, l, O), at its range's end in shared
+//   memory. The warps of a block hold consecutive ranges, so the block joins what its warps share, and the join
+//   kernel what blocks share: at most two parts a block. All merges go in a fixed order: the result does not
+//   depend on timing. (Joining a lone 32000-row sequence from all warps' parts took 20 us more.)
+//
+// Measured: a ragged batch of 64 sequences, 610,000 rows of 8 kv heads (2.5 GB), 366-377 us, 98-100% of the copy
+// bandwidth; one sequence of 32000 rows (131 MB) 28.3 us, of which the floor is 19.3, the schedule before the first
+// load 2, the two joins 4, the launches the rest; one of 700 rows 8.5 us, of 16 rows 4.6: dependent latencies.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -40,9 +47,10 @@ namespace dflash {
 namespace {
 
 constexpr int kStep = 16;       // rows per step
-// A group of up to so many steps has a block to itself where there are SMs enough: no prefix over the
-// sequences, no join. 256 rows of one sequence: 7.5 us against 8.5 cut; 700 rows: 10.8 against 9.4.
-constexpr int kLoneSteps = 32;
+// A group of up to so many steps a unit of warps (512 rows at a unit a warp) has a block to itself where there are
+// SMs enough: no prefix over the sequences, no join. 256 rows of one sequence: 7.2 us against 8.2 cut; 700 rows:
+// 10.8 against 8.5; 500 rows of 32 heads a group (4 units a block): 15.7 against 14.0.
+constexpr int kLoneSteps = 4;
 constexpr float kSlack = 8.0f;  // the running maximum may lag by 2^8
 
 // Warps of a block and steps that a warp has in flight. 128 KB in flight an SM are several times what the
@@ -801,7 +809,7 @@ Layout layout_of(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int win
                                         std::max(1.0, most_steps_of_call(num_reqs, hq, hkv, max_ctx_len, window))));
   y.grid = std::min(sms, y.workers);
   const double groups = static_cast<double>(num_reqs) * hkv * y.tile_units;
-  y.lone = groups <= sms && most_steps(max_ctx_len, window) <= kLoneSteps;
+  y.lone = groups <= sms && most_steps(max_ctx_len, window) <= kLoneSteps * (kWarps / y.unit);
   if (y.lone) y.grid = std::max(1, static_cast<int>(groups));
   y.split = !y.lone && y.grid > 1;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
