@@ -41,7 +41,13 @@ constexpr int kMaxCandidates = 4096;  // per request, W * lists * K
 constexpr int kVec = 4;               // 16-byte loads a thread has in flight
 constexpr int kSlots = 16;            // maxima a thread keeps
 constexpr int kRoom = kWarps * kMaxBeams;  // candidates of a block
-constexpr int kMergeRoom = 128;            // and of a request, past the bound
+constexpr int kMergeRoom = 256;            // and of a request, past the bound
+// Groups whose maxima give a bound. Of random elements about G log(G / (G - K)) reach the K-th largest of G
+// maxima: 9 of 32 groups for K = 8, 22 for K = 16, but 130 for K = 32 (44 of 64 groups). More take longer to rank.
+// 17 x 5 beams: 8.7 us with 32 groups, 9.7 with 64; 8 x 16 -> 32 beams of 100000: 73 and 17, since 32 groups let so
+// many equal bf16 values through that blocks fall back to lists.
+constexpr int kFewGroups = 32, kManyGroups = 64;
+int groups_of(int out_beams) { return out_beams <= 16 ? kFewGroups : kManyGroups; }
 constexpr int kTile = 512;            // vectors at most: 4096 bf16 or 2048 f32 elements
 constexpr int kBlocksPerSm = 5;
 constexpr int kVocabBits = 26;
@@ -71,8 +77,8 @@ struct BeamArgs {
   const uint8_t* finished;  // null: none
   int beams, out_beams, vocab, eos;
   // The rows' tiles (kTile vectors) laid end to end are dealt out in equal consecutive shares, one a block;
-  // what block b finds in row r goes to list b + r.
-  int rows, tiles, per_block, most_lists;  // tiles of a row, of a block; most lists of a row
+  // what block b finds in row r goes to list b + r. (row_tiles >= tiles: rows may be filled up to whole shares.)
+  int rows, tiles, row_tiles, per_block, most_lists;  // tiles of a row, of a block; most lists of a row
   float* part_max;    // [lists] maximum
   Sum* part_sum;      // [lists] sum relative to it
   float* part_val;    // [lists][K]
@@ -288,29 +294,31 @@ __device__ __forceinline__ float max_of(const uint4 (&v)[kVec]) {
   }
 }
 
-// The rank of value tid / 8 among 32 in shared memory (equal ones by their place), by 256 threads, 8 lanes each.
-template <typename T>
-__device__ __forceinline__ int rank_of_32(const T* x, int tid) {
-  const int at = tid / 8;
+// Whether this thread is to write the bound: the K-th largest of kGroups values in shared memory (equal ones by
+// their place). kThreads / kGroups lanes rank one value.
+template <int kThreads, int kGroups, typename T>
+__device__ __forceinline__ bool holds_bound(const T* x, int tid, int K) {
+  constexpr int kLanes = kThreads / kGroups;
+  const int at = tid / kLanes;
   const T v = x[at];
   int rank = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int i = tid % 8 + 8 * j;
+#pragma unroll 4
+  for (int i = tid % kLanes; i < kGroups; i += kLanes) {
     const T o = x[i];
-    rank += o > v || (o == v && i < at);
+    rank += (o > v) | ((o == v) & (i < at));
   }
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-  return rank;
+  for (int o = 1; o < kLanes; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  return rank == K - 1 && tid % kLanes == 0;
 }
 
-template <bool F32>
+template <bool F32, int kGroups>
 __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
   using V = Vec<F32>;
+  constexpr int kGroupThreads = kScanThreads / kGroups;
   constexpr int E = V::kElems;
   constexpr int kBatch = kScanThreads * kVec;  // vectors of a batch
-  __shared__ float s_max[32], s_warp_max[kWarps], s_bound;
+  __shared__ float s_max[kGroups], s_warp_max[kWarps], s_bound;
   __shared__ Sum s_sum[kWarps];
   __shared__ int s_count, s_hits;
   __shared__ int32_t s_hit[kRoom];
@@ -321,14 +329,14 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int K = a.out_beams;
   constexpr size_t kSize = F32 ? 4 : 2;
-  // the block's share: `left` tiles from tile `from` of row `row` on
-  const int64_t tile = static_cast<int64_t>(blockIdx.x) * a.per_block, all = static_cast<int64_t>(a.rows) * a.tiles;
-  int64_t left_tiles = min(static_cast<int64_t>(a.per_block), all - tile);
-  int row = static_cast<int>(all < (1ll << 32) ? static_cast<uint32_t>(tile) / static_cast<uint32_t>(a.tiles) : tile / a.tiles);
-  int from = static_cast<int>(tile - static_cast<int64_t>(row) * a.tiles), upto;
+  // the block's share: left_tiles tiles from tile `from` of row `row` on
+  const int64_t tile = static_cast<int64_t>(blockIdx.x) * a.per_block, all = static_cast<int64_t>(a.rows) * a.row_tiles;
+  int left_tiles = static_cast<int>(min(static_cast<int64_t>(a.per_block), all - tile));
+  int row = static_cast<int>(all < (1ll << 32) ? static_cast<uint32_t>(tile) / static_cast<uint32_t>(a.row_tiles) : tile / a.row_tiles);
+  int from = static_cast<int>(tile - static_cast<int64_t>(row) * a.row_tiles);
 #pragma unroll 1
-  for (; left_tiles > 0; left_tiles -= upto - from, from = 0, ++row) {
-    upto = static_cast<int>(min(static_cast<int64_t>(a.tiles), from + left_tiles));
+  for (; left_tiles > 0; left_tiles -= a.row_tiles - from, from = 0, ++row) {
+    const int upto = min(a.tiles, from + left_tiles);
     if (a.finished && a.finished[row]) continue;  // its one candidate needs no logits
     const int n = row / a.beams, b = row - n * a.beams;
     Piece p;
@@ -390,13 +398,13 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
       }
     }
     if (left < per_slot) s_slot[q++][tid] = slot;
-    // ---- the block's maximum and sum; the bound: the K-th largest of the maxima of 32 groups of 8 threads
+    // ---- the block's maximum and sum; the bound: the K-th largest of the groups' maxima
     float most = m;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if ((lane & 7) == 0) s_max[tid >> 3] = most;
+    for (int o = 1; o < kGroupThreads; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (tid % kGroupThreads == 0) s_max[tid / kGroupThreads] = most;
 #pragma unroll
-    for (int o = 8; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    for (int o = kGroupThreads; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     if (m != -INFINITY) s.scale(exp_below(m, most));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -425,7 +433,7 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
         a.part_sum[at] = s;
       }
     }
-    if (rank_of_32(s_max, tid) == K - 1 && tid % 8 == 0) s_bound = s_max[tid / 8];
+    if (holds_bound<kScanThreads, kGroups>(s_max, tid, K)) s_bound = s_max[tid / kGroupThreads];
     __syncthreads();
     const float bound = s_bound;
 
@@ -579,28 +587,32 @@ struct Lists {
   int count;
 };
 __device__ __forceinline__ Lists lists_of(const BeamArgs& a, int row) {
-  const int64_t lo = static_cast<int64_t>(row) * a.tiles;
+  const int64_t lo = static_cast<int64_t>(row) * a.row_tiles;
   int64_t b0, b1;
   if (lo + a.tiles < (1ll << 31)) b0 = static_cast<uint32_t>(lo) / a.per_block, b1 = static_cast<uint32_t>(lo + a.tiles - 1) / a.per_block;
   else b0 = lo / a.per_block, b1 = (lo + a.tiles - 1) / a.per_block;
   return Lists{b0 + row, static_cast<int>(b1 - b0) + 1};
 }
 
+// A group for each of consecutive numbers, as if drawn (Knuth's multiplicative hashing).
+template <int kGroups>
+__device__ __forceinline__ int scattered(int i) { return (static_cast<uint32_t>(i) * 2654435761u) / (0x100000000ull / kGroups); }
+
 // One block per request: every thread holds up to kPer candidates.
-template <int kPer>
+template <int kPer, int kGroups>
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
   constexpr int kThreads = kMergeThreads, kMergeWarps = kThreads / 32;
   __shared__ Lists s_lists[kMaxBeams];
   __shared__ bool s_ended[kMaxBeams];
   __shared__ Sum s_lse[kMaxBeams];  // log-sums in two terms
   __shared__ Best s_best[2][kMergeWarps], s_list[kMergeRoom];
-  __shared__ uint32_t s_group[32], s_bound;
+  __shared__ uint32_t s_group[kGroups], s_bound;
   __shared__ int s_count;
   const int n = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = a.beams, K = a.out_beams, S = a.most_lists;
   const int total = W * S * K;
   if (tid < W) s_lists[tid] = lists_of(a, n * W + tid);
-  if (tid < 32) s_group[tid] = 0;
+  if (tid < kGroups) s_group[tid] = 0;
   if (tid == 0) s_count = 0;
   __syncthreads();
   // Every load first, whether it will count or not: none depends on another's value, and the call's inputs do not
@@ -707,15 +719,15 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     a.out_parents[o] = none ? -1 : n * W + w;
     a.out_finished[o] = !none && (t == a.eos || s_ended[w]);
   };
-  // As in the scan: the K-th largest of 32 groups' maxima is a bound, and what reaches it is ranked.
-  uint32_t top = 0;
+  // As in the scan: the K-th largest of the groups' maxima is a bound, and what reaches it is ranked.
+  // (Candidate i is the i % K-th of its list: groups of i % 64 would hold the same places of all lists.)
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) top = max(top, mine[j].hi);
-  if (top) atomicMax(&s_group[lane], top);
+  for (int j = 0; j < kPer; ++j)
+    if (mine[j].hi) atomicMax(&s_group[scattered<kGroups>(j * kThreads + tid)], mine[j].hi);
   __syncthreads();
-  if (tid < 256 && rank_of_32(s_group, tid) == K - 1 && tid % 8 == 0) s_bound = s_group[tid / 8];
+  if (holds_bound<kThreads, kGroups>(s_group, tid, K)) s_bound = s_group[tid / (kThreads / kGroups)];
   __syncthreads();
-  top = s_bound;
+  const uint32_t top = s_bound;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     if (mine[j].hi && mine[j].hi >= top) {
@@ -758,7 +770,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
 }
 
 struct Shares {
-  int tiles, per_block, most_lists;
+  int tiles, row_tiles, per_block, most_lists;
   int64_t blocks, lists;
 };
 
@@ -776,7 +788,17 @@ Shares shares_of(int reqs, int beams, int out_beams, int vocab, int elem, int sm
   const int64_t least = most >= y.tiles ? 1 : (y.tiles - 2) / (most - 1) + 1;
   y.per_block = static_cast<int>(std::max<int64_t>({(total + wave - 1) / wave, least, 1}));
   y.most_lists = static_cast<int>(std::min<int64_t>(y.tiles, (y.tiles - 2 + y.per_block) / y.per_block + 1));
-  y.blocks = (total + y.per_block - 1) / y.per_block;
+  y.row_tiles = y.tiles;
+  // A block that holds the ends of two rows does everything behind the stream twice, which takes as long as two or
+  // three tiles: rows are filled up to whole shares where that makes the shares no more than two tiles longer
+  // (100 rows of 50000: 12.0 us laid end to end, 9.5 so; 300: 17.0, 13.7).
+  const int64_t cuts = rows > wave ? 0 : std::min<int64_t>({wave / rows, y.tiles, most});
+  if (cuts && (y.tiles + cuts - 1) / cuts <= y.per_block + 2) {
+    y.per_block = static_cast<int>((y.tiles + cuts - 1) / cuts);
+    y.most_lists = (y.tiles + y.per_block - 1) / y.per_block;
+    y.row_tiles = y.most_lists * y.per_block;
+  }
+  y.blocks = (rows * y.row_tiles + y.per_block - 1) / y.per_block;
   y.lists = y.blocks + rows;
   return y;
 }
@@ -837,7 +859,7 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   if (workspace_bytes < bytes_of(y, beams_out))
     return errorf(DFLASH_ERR_WORKSPACE, "workspace has %zu bytes; %zu are needed", workspace_bytes, bytes_of(y, beams_out));
   const size_t lists = static_cast<size_t>(y.lists);
-  a.rows = num_reqs * beams, a.tiles = y.tiles, a.per_block = y.per_block, a.most_lists = y.most_lists;
+  a.rows = num_reqs * beams, a.tiles = y.tiles, a.per_block = y.per_block, a.most_lists = y.most_lists, a.row_tiles = y.row_tiles;
   a.logits = logits, a.req_stride = req_stride, a.beam_stride = beam_stride;
   a.scores = scores, a.finished = finished;
   a.beams = beams, a.out_beams = beams_out, a.vocab = vocab, a.eos = eos;
@@ -848,8 +870,10 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   a.out_scores = out_scores, a.out_tokens = out_tokens, a.out_parents = out_parents, a.out_finished = out_finished;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(y.blocks);
-  if (es == 4) beam_scan_kernel<true><<<grid, kScanThreads, 0, st>>>(a);
-  else beam_scan_kernel<false><<<grid, kScanThreads, 0, st>>>(a);
+  const bool few = groups_of(beams_out) == kFewGroups;
+  auto scan = es == 4 ? (few ? beam_scan_kernel<true, kFewGroups> : beam_scan_kernel<true, kManyGroups>)
+                      : (few ? beam_scan_kernel<false, kFewGroups> : beam_scan_kernel<false, kManyGroups>);
+  scan<<<grid, kScanThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "beam scan launch: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg{};
@@ -862,9 +886,11 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // candidates a thread holds: 2 where they are enough (1 x 4 beams: 7.1 us, with 8 7.7), else 8
-  e = beams * y.most_lists * beams_out <= 2 * kMergeThreads
-          ? cudaLaunchKernelEx(&cfg, beam_merge_kernel<2>, a)
-          : cudaLaunchKernelEx(&cfg, beam_merge_kernel<kMaxCandidates / kMergeThreads>, a);
+  constexpr int kPer = kMaxCandidates / kMergeThreads;
+  auto merge = beams * y.most_lists * beams_out <= 2 * kMergeThreads
+                   ? (few ? beam_merge_kernel<2, kFewGroups> : beam_merge_kernel<2, kManyGroups>)
+                   : (few ? beam_merge_kernel<kPer, kFewGroups> : beam_merge_kernel<kPer, kManyGroups>);
+  e = cudaLaunchKernelEx(&cfg, merge, a);
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "beam merge launch: %s", cudaGetErrorString(e));
   return report_error(DFLASH_OK, "");
 }
