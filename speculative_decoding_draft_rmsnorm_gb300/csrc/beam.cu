@@ -49,6 +49,8 @@ constexpr int kMergeRoom = 256;            // and of a request, past the bound
 constexpr int kFewGroups = 32, kManyGroups = 64;
 int groups_of(int out_beams) { return out_beams <= 16 ? kFewGroups : kManyGroups; }
 constexpr int kTile = 512;            // vectors at most: 4096 bf16 or 2048 f32 elements
+constexpr int kNarrow = 1024;         // a row of up to so many elements is read one by one: as vectors they would lie
+                                      // with too few threads for a bound (2192 rows of 242: 93 us)
 constexpr int kBlocksPerSm = 5;
 constexpr int kVocabBits = 26;
 constexpr int kMaxVocab = 1 << kVocabBits;
@@ -367,20 +369,34 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
       }
     };
     // at most 14 elements at the ends of a row, one a thread
+    const bool narrow = a.vocab <= kNarrow;
     int edge_at = -1;
-    if (p.first && tid < p.head) edge_at = tid;
-    else if (p.last && tid >= 32 && p.tail + tid - 32 < a.vocab) edge_at = p.tail + tid - 32;
+    if (!narrow && p.first && tid < p.head) edge_at = tid;
+    else if (!narrow && p.last && tid >= 32 && p.tail + tid - 32 < a.vocab) edge_at = p.tail + tid - 32;
     float edge = -INFINITY;
     if (edge_at >= 0) {
       edge = V::one(p.base, edge_at);
       raise_max(edge);
       s.add(exp_below(edge, ref.ref));
     }
-    const int batches = (p.hi - p.lo + kBatch - 1) / kBatch, per_slot = (batches + kSlots - 1) / kSlots;
+    if (narrow) {
+      float x[kNarrow / kScanThreads], top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kNarrow / kScanThreads; ++j) {
+        const int i = j * kScanThreads + tid;
+        x[j] = i < a.vocab ? V::one(p.base, i) : -INFINITY;
+        top = fmaxf(top, x[j]);
+      }
+      raise_max(top);
+#pragma unroll
+      for (int j = 0; j < kNarrow / kScanThreads; ++j) s.add(exp_below(x[j], ref.ref));
+    }
+    const int end = narrow ? p.lo : p.hi;  // of the vectors
+    const int batches = (end - p.lo + kBatch - 1) / kBatch, per_slot = (batches + kSlots - 1) / kSlots;
     float slot = -INFINITY;
     int left = per_slot, q = 0;  // batches until the slot is full
 #pragma unroll 1
-    for (int v0 = p.lo + tid; v0 - tid < p.hi; v0 += kBatch) {
+    for (int v0 = p.lo + tid; v0 - tid < end; v0 += kBatch) {
       uint4 raw[kVec];
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
@@ -445,6 +461,13 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
       if (c < kRoom) s_val[c] = v, s_idx[c] = i;
     };
     if (edge >= bound && edge > -INFINITY) push(edge, edge_at);
+    if (narrow && m >= bound && m > -INFINITY) {
+#pragma unroll 1
+      for (int i = tid; i < a.vocab; i += kScanThreads) {
+        const float v = V::one(p.base, i);
+        if (v >= bound && v > -INFINITY) push(v, i);
+      }
+    }
 #pragma unroll 4
     for (int i = 0; i < q; ++i) {
       const float top = s_slot[i][tid];

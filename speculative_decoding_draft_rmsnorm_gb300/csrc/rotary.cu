@@ -49,7 +49,9 @@ struct RotaryArgs {
   int64_t n;
   // Threads of a token: `groups` share its heads in each range. Rotating: rot_units chunk pairs of the q and
   // k heads; copying: tail_units chunks of their elements behind rd, v_units chunks of the v heads.
+  // Blocks [0, rot_blocks) rotate, the next tail_blocks and the rest copy.
   int rot_units, tail_units, v_units, groups;
+  unsigned rot_blocks, tail_blocks;
   int tail_bytes, v_bytes;  // of a copied chunk
   int rd;
   const int32_t* pos;
@@ -147,35 +149,32 @@ __device__ __forceinline__ Chunk<T, E> pack_chunk(const float (&x)[E]) {
 
 template <typename T, bool INTER, int E>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int rot = a.rot_units * a.groups, tail = a.tail_units * a.groups, per_token = rot + tail + a.v_units * a.groups;
-  const int64_t t = item / per_token;
+  const bool rotates = blockIdx.x < a.rot_blocks, copies_v = blockIdx.x >= a.rot_blocks + a.tail_blocks;
+  const unsigned first = rotates ? 0 : copies_v ? a.rot_blocks + a.tail_blocks : a.rot_blocks;
+  const int units = rotates ? a.rot_units : copies_v ? a.v_units : a.tail_units, per_token = units * a.groups;
+  const int64_t item = static_cast<int64_t>(blockIdx.x - first) * kThreads + threadIdx.x;
+  const int64_t t = item < (1ll << 32) ? static_cast<uint32_t>(item) / static_cast<uint32_t>(per_token) : item / per_token;
   if (t >= a.n) return;
-  int rest = static_cast<int>(item - t * per_token);
+  const int rest = static_cast<int>(item - t * per_token), g = rest / units, u = rest - g * units;
   // where k and v of this token go
   int64_t row = t;
   bool stored = true;
   if (a.slot) {
     row = a.slot[t];
     stored = row >= 0 && row < a.capacity;
-    if (row >= a.capacity && rest == 0 && a.err) atomicOr(a.err, kErrMetadata);
+    if (row >= a.capacity && rotates && rest == 0 && a.err) atomicOr(a.err, kErrMetadata);
   }
-  if (rest >= rot) {  // a copied chunk
-    rest -= rot;
-    if (rest < tail) {
-      const int g = rest / a.tail_units, u = rest - g * a.tail_units;
-      const int64_t from = static_cast<int64_t>(a.rd) * sizeof(T);
-      if (a.hq && a.t[0].src != a.t[0].dst) copy_chunk(a.t[0], t, t, a.hq, sizeof(T), from, u, a.tail_bytes, g, a.groups);
-      if (a.hkv && a.t[1].src != a.t[1].dst && stored)
-        copy_chunk(a.t[1], t, row, a.hkv, sizeof(T), from, u, a.tail_bytes, g, a.groups);
-    } else if (stored) {
-      rest -= tail;
-      const int g = rest / a.v_units, u = rest - g * a.v_units;
-      copy_chunk(a.t[2], t, row, a.hv, sizeof(T), 0, u, a.v_bytes, g, a.groups);
-    }
+  if (copies_v) {
+    if (stored) copy_chunk(a.t[2], t, row, a.hv, sizeof(T), 0, u, a.v_bytes, g, a.groups);
     return;
   }
-  const int g = rest / a.rot_units, u = rest - g * a.rot_units;
+  if (!rotates) {
+    const int64_t from = static_cast<int64_t>(a.rd) * sizeof(T);
+    if (a.hq && a.t[0].src != a.t[0].dst) copy_chunk(a.t[0], t, t, a.hq, sizeof(T), from, u, a.tail_bytes, g, a.groups);
+    if (a.hkv && a.t[1].src != a.t[1].dst && stored)
+      copy_chunk(a.t[1], t, row, a.hkv, sizeof(T), from, u, a.tail_bytes, g, a.groups);
+    return;
+  }
   // this unit's elements: two chunks
   const bool pairwise = INTER && E == 1;  // one pair of neighbours
   const int e0 = pairwise ? 2 * u : u * E;
@@ -248,10 +247,12 @@ bool apart(int64_t rows, int64_t row_stride, int heads, int64_t head_stride, int
   return row_stride >= dh && (head_stride - dh) / row_stride >= rows - 1;
 }
 
+int64_t blocks_of(const RotaryArgs& a, int units) { return (a.n * units * a.groups + kThreads - 1) / kThreads; }
+
 template <typename T, bool INTER, int E>
 void launch(const RotaryArgs& a, cudaStream_t st) {
-  const int64_t items = a.n * (a.rot_units + a.tail_units + a.v_units) * a.groups;
-  rotary_kernel<T, INTER, E><<<static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
+  const unsigned v_blocks = static_cast<unsigned>(blocks_of(a, a.v_units));
+  rotary_kernel<T, INTER, E><<<a.rot_blocks + a.tail_blocks + v_blocks, kThreads, 0, st>>>(a);
 }
 
 template <typename T, bool INTER>
@@ -365,8 +366,9 @@ extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void*
   const int64_t want = static_cast<int64_t>(sms) * 2048, have = n * (a.rot_units + a.tail_units + a.v_units);
   const int64_t groups = (want + have - 1) / have;
   a.groups = static_cast<int>(std::min<int64_t>(groups, a.hq + a.hkv));
-  const int64_t items = have * a.groups;
-  if ((items + kThreads - 1) / kThreads > 0x7fffffff)
+  const int64_t rot_blocks = blocks_of(a, a.rot_units), tail_blocks = blocks_of(a, a.tail_units);
+  a.rot_blocks = static_cast<unsigned>(rot_blocks), a.tail_blocks = static_cast<unsigned>(tail_blocks);
+  if (rot_blocks + tail_blocks + blocks_of(a, a.v_units) > 0x7fffffff)
     return errorf(DFLASH_ERR_UNSUPPORTED, "too many rows for one call (%lld)", static_cast<long long>(n));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (es == 4)
