@@ -50,7 +50,8 @@ constexpr int kFewGroups = 32, kManyGroups = 64;
 int groups_of(int out_beams) { return out_beams <= 16 ? kFewGroups : kManyGroups; }
 constexpr int kTile = 512;            // vectors at most: 4096 bf16 or 2048 f32 elements
 constexpr int kNarrow = 1024;         // a row of up to so many elements is read one by one: as vectors they would lie
-                                      // with too few threads for a bound (2192 rows of 242: 93 us)
+                                      // with too few threads for a bound (2192 rows of 242: 93 us, 19 so; a
+                                      // warp a row was twice as long for few rows)
 constexpr int kBlocksPerSm = 5;
 constexpr int kVocabBits = 26;
 constexpr int kMaxVocab = 1 << kVocabBits;
@@ -379,11 +380,12 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
       raise_max(edge);
       s.add(exp_below(edge, ref.ref));
     }
+    const int mine = tid % kGroupThreads * kGroups + tid / kGroupThreads;  // neighbours go to different groups
     if (narrow) {
       float x[kNarrow / kScanThreads], top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < kNarrow / kScanThreads; ++j) {
-        const int i = j * kScanThreads + tid;
+        const int i = j * kScanThreads + mine;
         x[j] = i < a.vocab ? V::one(p.base, i) : -INFINITY;
         top = fmaxf(top, x[j]);
       }
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kScanThreads, kBlocksPerSm) beam_scan_kernel(c
     if (edge >= bound && edge > -INFINITY) push(edge, edge_at);
     if (narrow && m >= bound && m > -INFINITY) {
 #pragma unroll 1
-      for (int i = tid; i < a.vocab; i += kScanThreads) {
+      for (int i = mine; i < a.vocab; i += kScanThreads) {
         const float v = V::one(p.base, i);
         if (v >= bound && v > -INFINITY) push(v, i);
       }

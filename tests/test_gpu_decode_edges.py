@@ -122,6 +122,24 @@ def test_beams_of_the_largest_vocabulary(f32):
         D().beam_select(torch.empty(1, 1, vocab + 1, device="cuda", dtype=torch.bfloat16), s)
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("n,w,k,vocab", [
+    (140, 16, 16, 242), (12, 2, 16, 664), (256, 5, 16, 97),        # rows read one by one
+    (9, 4, 32, 1024), (9, 4, 32, 1025), (3, 8, 17, 1031),          # ... and just not; 64 groups
+    (2, 16, 32, 20011), (1, 1, 32, 60000), (1, 1, 31, 128001),     # many lists of many places
+    (100, 1, 1, 20000), (75, 4, 4, 20000), (200, 4, 4, 5000),      # rows cut each for itself, or laid end to end
+])
+def test_beams_of_every_cut(n, w, k, vocab, f32):
+    import torch
+    x, s = B.draw(n, w, vocab, f32, seed=vocab + k)
+    B.check(D().beam_select(x, s, beams_out=k), x, s, k)
+    x = x[:2].round()  # few distinct values
+    x[0, 0] = 0.5
+    x[-1, 0] = torch.sort(x[-1, 0]).values
+    s = -torch.arange(w, device="cuda", dtype=torch.float32).repeat(x.shape[0], 1)  # no two beams of equal scores
+    B.check(D().beam_select(x, s, beams_out=k), x, s, k)
+
+
 def test_as_many_beams_as_there_may_be_over_a_wide_vocabulary():
     x, s = B.draw(1, 32, 300007, False, seed=41)
     B.check(D().beam_select(x, s), x, s, 32)
