@@ -17,9 +17,9 @@
 // streaming instead cost 52 instructions an element against ~8. Only where ties flood the candidates
 // (a constant row) does a block go over its piece again with such lists, one a warp.
 //
-// Measured: 64 x 8 beams of 151936 bf16 logits (156 MB) 35.2 us, floor 22.9: the stream alone takes 25.6 (22.6
-// without exponentials), the blocks' ends with bound and second look 5.6, the merge 4.1. 1 x 4 beams 7.0 us and
-// 17 x 5 of 32000 f32 8.7 us (floors 0.2 and 1.6): two dependent launches.
+// Measured: 64 x 8 beams of 151936 bf16 logits (156 MB) 34.8 us, floor 22.9: the stream alone takes 25.6 (22.6
+// without exponentials), the blocks' ends with bound and second look 5.6, the merge 3.6. 1 x 4 beams 7.0 us and
+// 17 x 5 of 32003 f32 9.2 us (floors 0.2 and 1.6): two dependent launches.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -44,7 +44,7 @@ constexpr int kRoom = kWarps * kMaxBeams;  // candidates of a block
 constexpr int kMergeRoom = 256;            // and of a request, past the bound
 // Groups whose maxima give a bound. Of random elements about G log(G / (G - K)) reach the K-th largest of G
 // maxima: 9 of 32 groups for K = 8, 22 for K = 16, but 130 for K = 32 (44 of 64 groups). More take longer to rank.
-// 17 x 5 beams: 8.7 us with 32 groups, 9.7 with 64; 8 x 16 -> 32 beams of 100000: 73 and 17, since 32 groups let so
+// 17 x 5 beams: 8.7 us with 32 groups, 9.7 with 64; 8 x 16 -> 32 beams of 100000: 73 and 17 us, since 32 groups let so
 // many equal bf16 values through that blocks fall back to lists.
 constexpr int kFewGroups = 32, kManyGroups = 64;
 int groups_of(int out_beams) { return out_beams <= 16 ? kFewGroups : kManyGroups; }

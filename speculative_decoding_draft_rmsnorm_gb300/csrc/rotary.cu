@@ -18,6 +18,11 @@
 // chunks: the half layout pairs them with each other, the interleaved one pairs neighbours inside
 // each. E is the largest power of two that divides rd/2 and the rest of the head and that the
 // pointers' and strides' alignment allows, so odd sizes run the same code with narrower accesses.
+//
+// Measured: 32768 rows of 40 heads of 128 (671 MB) 104.2 us, 95% of the copy rate; 2001 rows of 20 heads, 20 of 80 elements, in f32
+// 5.3 us (floor 3.8); 32 rows into pages 3.0 us, a launch. Blocks of their own for what is copied:
+// threads of both kinds in a warp took 67 us instead of 42 for 26170 rows of 7 heads of 256 into pages, 27 instead of 14
+// for 6491 rows of 40 heads of 64.
 #include <cuda_runtime.h>
 
 #include <algorithm>
