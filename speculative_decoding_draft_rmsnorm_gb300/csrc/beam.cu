@@ -33,14 +33,15 @@
 namespace dflash {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;             // of a scan's block, and ten blocks an SM: 8 and five took 25.3 us where these take
+                                      // 21.3 (32 x 8 beams of 151936), 13.1 for 9.5 (800 rows of 5000)
 constexpr int kScanThreads = kWarps * 32;
 constexpr int kMergeThreads = 512;
 constexpr int kMaxBeams = 32;         // W and K
 constexpr int kMaxCandidates = 4096;  // per request, W * lists * K
 constexpr int kVec = 4;               // 16-byte loads a thread has in flight
 constexpr int kSlots = 16;            // maxima a thread keeps
-constexpr int kRoom = kWarps * kMaxBeams;  // candidates of a block
+constexpr int kRoom = 256;                 // candidates of a block, kWarps K at least
 constexpr int kMergeRoom = 256;            // and of a request, past the bound
 // Groups whose maxima give a bound. Of random elements about G log(G / (G - K)) reach the K-th largest of G
 // maxima: 9 of 32 groups for K = 8, 22 for K = 16, but 130 for K = 32 (44 of 64 groups). More take longer to rank.
@@ -48,11 +49,11 @@ constexpr int kMergeRoom = 256;            // and of a request, past the bound
 // many equal bf16 values through that blocks fall back to lists.
 constexpr int kFewGroups = 32, kManyGroups = 64;
 int groups_of(int out_beams) { return out_beams <= 16 ? kFewGroups : kManyGroups; }
-constexpr int kTile = 512;            // vectors at most: 4096 bf16 or 2048 f32 elements
+constexpr int kTile = 1024;           // vectors at most: 8192 bf16 or 4096 f32 elements
 constexpr int kNarrow = 1024;         // a row of up to so many elements is read one by one: as vectors they would lie
                                       // with too few threads for a bound (2192 rows of 242: 93 us, 19 so; a
                                       // warp a row was twice as long for few rows)
-constexpr int kBlocksPerSm = 5;
+constexpr int kBlocksPerSm = 10;
 constexpr int kVocabBits = 26;
 constexpr int kMaxVocab = 1 << kVocabBits;
 
