@@ -17,9 +17,9 @@
 // streaming instead cost 52 instructions an element against ~8. Only where ties flood the candidates
 // (a constant row) does a block go over its piece again with such lists, one a warp.
 //
-// Measured: 64 x 8 beams of 151936 bf16 logits (156 MB) 34.8 us, floor 22.9: the stream alone takes 25.6 (22.6
-// without exponentials), the blocks' ends with bound and second look 5.6, the merge 3.6. 1 x 4 beams 7.0 us and
-// 17 x 5 of 32003 f32 9.2 us (floors 0.2 and 1.6): two dependent launches.
+// Measured: 64 x 8 beams of 151936 bf16 logits (156 MB) 33.6 us, floor 22.9: the stream alone takes 25.6 (22.6
+// without exponentials), the blocks' ends with bound and second look 4.4, the merge 3.6. 1 x 4 beams 7.0 us and
+// 17 x 5 of 32003 f32 8.5 us (floors 0.2 and 1.6): two dependent launches.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -45,7 +45,7 @@ constexpr int kRoom = 256;                 // candidates of a block, kWarps K at
 constexpr int kMergeRoom = 256;            // and of a request, past the bound
 // Groups whose maxima give a bound. Of random elements about G log(G / (G - K)) reach the K-th largest of G
 // maxima: 9 of 32 groups for K = 8, 22 for K = 16, but 130 for K = 32 (44 of 64 groups). More take longer to rank.
-// 17 x 5 beams: 8.7 us with 32 groups, 9.7 with 64; 8 x 16 -> 32 beams of 100000: 73 and 17 us, since 32 groups let so
+// 17 x 5 beams: 9.0 us with 32 groups, 9.7 with 64; 8 x 16 -> 32 beams of 100000: 73 and 17 us, since 32 groups let so
 // many equal bf16 values through that blocks fall back to lists.
 constexpr int kFewGroups = 32, kManyGroups = 64;
 int groups_of(int out_beams) { return out_beams <= 16 ? kFewGroups : kManyGroups; }
@@ -815,11 +815,11 @@ Shares shares_of(int reqs, int beams, int out_beams, int vocab, int elem, int sm
   y.per_block = static_cast<int>(std::max<int64_t>({(total + wave - 1) / wave, least, 1}));
   y.most_lists = static_cast<int>(std::min<int64_t>(y.tiles, (y.tiles - 2 + y.per_block) / y.per_block + 1));
   y.row_tiles = y.tiles;
-  // A block that holds the ends of two rows does everything behind the stream twice, which takes as long as two or
-  // three tiles: rows are filled up to whole shares where that makes the shares no more than two tiles longer
-  // (100 rows of 50000: 12.0 us laid end to end, 9.5 so; 300: 17.0, 13.7).
+  // A block that holds the ends of two rows does everything behind the stream twice, which takes as long as a few
+  // tiles: rows are filled up to whole shares where that makes the shares no more than four tiles longer
+  // (256 rows of 151936: 23.1 us laid end to end, 21.3 so; 512 rows 34.1, 33.6; 200 of 128000 18.4, 17.0).
   const int64_t cuts = rows > wave ? 0 : std::min<int64_t>({wave / rows, y.tiles, most});
-  if (cuts && (y.tiles + cuts - 1) / cuts <= y.per_block + 2) {
+  if (cuts && (y.tiles + cuts - 1) / cuts <= y.per_block + 4) {
     y.per_block = static_cast<int>((y.tiles + cuts - 1) / cuts);
     y.most_lists = (y.tiles + y.per_block - 1) / y.per_block;
     y.row_tiles = y.most_lists * y.per_block;
