@@ -20,7 +20,7 @@
 // pointers' and strides' alignment allows, so odd sizes run the same code with narrower accesses.
 //
 // Measured: 32768 rows of 40 heads of 128 (671 MB) 104.2 us, 95% of the copy rate; 2001 rows of 20 heads, 20 of 80 elements, in f32
-// 5.3 us (floor 3.8); 32 rows into pages 3.0 us, a launch. Blocks of their own for what is copied:
+// 5.3 us (floor 3.8); 32 rows into pages 3.2 us, a launch. Blocks of their own for what is copied:
 // threads of both kinds in a warp took 67 us instead of 42 for 26170 rows of 7 heads of 256 into pages, 27 instead of 14
 // for 6491 rows of 40 heads of 64.
 #include <cuda_runtime.h>
@@ -64,7 +64,7 @@ struct RotaryArgs {
   int64_t capacity;
   float amp, sin_sign;
   uint32_t* err;
-  float hi[kMaxPairs], lo[kMaxPairs];  // turns per position, head and tail
+  float2 freq[kMaxPairs];  // turns per position, head and tail
 };
 
 // Copies a chunk of heads h, h + step, .. below end of one tensor, kUnroll loads in flight.
@@ -155,6 +155,13 @@ __device__ __forceinline__ Chunk<T, E> pack_chunk(const float (&x)[E]) {
 template <typename T, bool INTER, int E>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   const bool rotates = blockIdx.x < a.rot_blocks, copies_v = blockIdx.x >= a.rot_blocks + a.tail_blocks;
+  // The table in shared memory: lanes of different pairs read the parameters' bank one after the other (6426 rows of
+  // 5 heads of 256: 24 us, 12 so; 32 rows of 40 heads of 128 3.0, 3.2).
+  __shared__ float2 s_freq[kMaxPairs];
+  if (rotates) {
+    for (int i = threadIdx.x; i < a.rd / 2; i += kThreads) s_freq[i] = a.freq[i];
+    __syncthreads();
+  }
   const unsigned first = rotates ? 0 : copies_v ? a.rot_blocks + a.tail_blocks : a.rot_blocks;
   const int units = rotates ? a.rot_units : copies_v ? a.v_units : a.tail_units, per_token = units * a.groups;
   const int64_t item = static_cast<int64_t>(blockIdx.x - first) * kThreads + threadIdx.x;
@@ -192,7 +199,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     for (int e = 0; e < E; ++e) {
       // half layout and single pairs: pair u E + e; interleaved chunks: E/2 pairs of each chunk
       const int pair = (!INTER || E == 1) ? u * E + e : (e < E / 2 ? e0 / 2 + e : e1 / 2 + e - E / 2);
-      sincospif(2.0f * rope_turns(p, a.hi[pair], a.lo[pair]), &sn[e], &cs[e]);
+      const float2 f = s_freq[pair];
+      sincospif(2.0f * rope_turns(p, f.x, f.y), &sn[e], &cs[e]);
       cs[e] *= a.amp;
       sn[e] *= a.amp * a.sin_sign;
     }
@@ -360,8 +368,8 @@ extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void*
   a.err = reinterpret_cast<uint32_t*>(status);
   for (int i = 0; i < rotary_dim / 2; ++i) {
     const double turns = inv_freq[i] / 6.283185307179586476925286766559;
-    a.hi[i] = static_cast<float>(turns);
-    a.lo[i] = static_cast<float>(turns - static_cast<double>(a.hi[i]));
+    a.freq[i].x = static_cast<float>(turns);
+    a.freq[i].y = static_cast<float>(turns - static_cast<double>(a.freq[i].x));
   }
   int sms = 0;
   int rc = query_sms(&sms);
