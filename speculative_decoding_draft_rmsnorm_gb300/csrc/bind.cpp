@@ -54,6 +54,15 @@ struct Place {
                                                 type, std::nullopt));
   }
 
+  // A contiguous tensor in bytes [at, ..) of another's storage.
+  static at::Tensor slice(const at::Tensor& whole, int64_t at, at::IntArrayRef shape, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                            c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_storage_offset(at / static_cast<int64_t>(c10::elementSize(type)));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    return t;
+  }
+
   // The address of a tensor of that type on this device.
   void* plain(const char* name, const at::Tensor& t, at::ScalarType type, bool contiguous = true) const {
     if (t.scalar_type() != type)
@@ -284,11 +293,14 @@ PyObject* beam_select(PyObject* const* a) {
   if (k <= 0) raise(PyExc_ValueError, "beams_out must be positive");
   static const char* const names[4] = {"scores", "tokens", "parents", "finished"};
   static const at::ScalarType types[4] = {at::kFloat, at::kInt, at::kInt, at::kBool};
-  at::Tensor made[4];
+  // outputs that were not given lie side by side in one allocation
+  const int64_t each = (static_cast<int64_t>(n) * k * 4 + 15) / 16 * 16;
+  at::Tensor made[4], whole;
   void* out[4];
   for (int i = 0; i < 4; ++i) {
     if (a[5 + i] == Py_None) {
-      made[i] = at.empty({n, k}, types[i]);
+      if (!whole.defined()) whole = at.empty({4 * each}, at::kByte);
+      made[i] = Place::slice(whole, i * each, {n, k}, types[i]);
       out[i] = made[i].data_ptr();
     } else {
       out[i] = at.address(names[i], a[5 + i], types[i], {n, k});

@@ -188,7 +188,7 @@ def beam_select(logits, scores, *, beams_out=None, finished=None, eos=-1, out=No
     finished [N, W] bool; K = beams_out (default W) of W * vocab candidates are kept, best first, ties to
     the lowest index. Outputs [N, K]: scores f32, tokens int32, parents int32 (row r * W + w, as
     fork_pages takes them), finished bool; slots without a candidate hold -inf, -1, -1, False.
-    `out` may hold preallocated outputs, e.g. for graph capture.
+    `out` may hold preallocated outputs, e.g. for graph capture; the others share one allocation.
     """
     bind = _bind or _load()
     if stream is not None:
