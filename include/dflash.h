@@ -405,8 +405,8 @@ DFLASH_API size_t dflash_decode_workspace_size(int num_reqs, int hq, int hkv, in
  *   lse        f32 [num_reqs, Hq] or NULL: log sum_j p_j
  *   status     int32 device word or NULL: DFLASH_STATUS_METADATA is ORed in for a bad length or a
  *              table entry outside [0, num_pages) (page 0 is read in its place)
- *   Dh in {64, 128}; Hq % Hkv == 0, any group size. bf16 products are exact, sums f32; the weights
- *   keep 16 bits for a bf16 output and 24 for an f32 one. Two launches (attention, join), or one
+ *   Dh in {64, 128}; Hq % Hkv == 0, any group size. bf16 products are exact, sums f32, rounded once
+ *   every 16 rows; the weights keep 24 bits (16 for a bf16 output of more than 8 heads a group). Two launches (attention, join), or one
  *   where max_ctx_len (or the window) is at most 512 (less past 16 heads a group) and there are no
  *   more (sequence, kv head) pairs than SMs. Results do not depend on timing. Rows outside the lengths and the window may hold
  *   anything; a stored value that is infinite gives NaN in its column.

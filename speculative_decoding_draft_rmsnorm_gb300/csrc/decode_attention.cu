@@ -18,13 +18,16 @@
 //   permuted within a row so that the fragment reads are free of bank conflicts. The order of a
 //   contraction's terms is free, so a lane's fragment of Q and K is 8 consecutive elements of a row instead
 //   of the instruction's 2 + 2: one 16-byte read. V is read transposed (ldmatrix).
-// - The group's heads are the 16 rows of mma.m16n8k16 (K and V rows are its columns). At <= 8 heads the
-//   spare rows 8..15 carry the rounding remainder of P, so P has 16 significant bits at no cost; f32
-//   outputs add a third term (24 bits). The idle rows cost nothing that matters: the tensor pipe is active
-//   in 17% of a batch's cycles, waiting for the loads. Past 16 heads a group that ends: each tile of 16 heads is
-//   a warp that copies the same rows for itself (from L2), and 32 heads a group take 69 us where 16 take 52
-//   (32 sequences of 4096 rows, 537 MB; floor 39.5). Rings shared by such warps were slower (84 us): it is the
-//   work of a step that bounds them, not its copy.
+// - The group's heads are the 16 rows of mma.m16n8k16 (K and V rows are its columns). P goes in as bf16 terms, three
+//   of them (24 bits; at <= 8 heads the spare rows 8..15 carry the second). A bf16 output past 8 heads takes two, 16
+//   bits: what they leave out is a 256th of the output's own rounding. The matrix unit cuts sums off instead of
+//   rounding them, 3e-8 of the sum a step, always towards zero: 1e-4 over a warp's 3750 steps. So it only ever sums a
+//   step's 16 rows, and those sums are added with rounded additions (at most 0.8 us for 32 sequences of 4096 rows up to
+//   16 heads a group; 32 heads 69 -> 77 us, f32 outputs 85).
+//   The idle rows cost nothing that matters: the tensor pipe is active in a fifth of a batch's cycles, waiting for the
+//   loads. Past 16 heads a group that ends: each tile of 16 heads is a warp that copies the same rows for itself (from
+//   L2), and 32 heads a group take 77 us where 16 take 53 (32 sequences of 4096 rows, 537 MB; floor 39.5). Rings shared
+//   by such warps were slower still: it is the work of a step that bounds them, not its copy.
 // - A worker stores a group that it holds whole; of others it leaves (m, l, O), at its range's end in shared
 //   memory. The warps of a block hold consecutive ranges, so the block joins what its warps share, and the join
 //   kernel what blocks share: at most two parts a block. All merges go in a fixed order: the result does not
@@ -486,22 +489,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < KC; ++i)  // piece (4 i + t) ^ ((g & 1) * 4)
             kf[i] = lds128((k_read + stage + jt * 8 * kRowBytes) ^ (i * 64));
-          // f32 outputs: a chain of sums per 32 columns, so that no sum rounds at the size of all of them
-          float part[F32 ? KC : 1][4];
+          // a chain of sums per 32 columns, so that none is cut off at the size of all of them
+          float part[KC][4];
 #pragma unroll
           for (int i = 0; i < KC; ++i) {
-            float(&d)[4] = part[F32 ? i : 0];
-            if (F32 || i == 0) d[0] = d[1] = d[2] = d[3] = 0.0f;
+            float(&d)[4] = part[i];
+            d[0] = d[1] = d[2] = d[3] = 0.0f;
             mma_bf16(d, qf[0][i].x, R == 1 ? 0u : qf[R - 1][i].x, qf[0][i].y, R == 1 ? 0u : qf[R - 1][i].y, kf[i].x, kf[i].y);
             mma_bf16(d, qf[0][i].z, R == 1 ? 0u : qf[R - 1][i].z, qf[0][i].w, R == 1 ? 0u : qf[R - 1][i].w, kf[i].z, kf[i].w);
           }
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             sc[jt][x] = part[0][x];
-            if constexpr (F32) {
 #pragma unroll
-              for (int i = 1; i < KC; ++i) sc[jt][x] += part[i][x];
-            }
+            for (int i = 1; i < KC; ++i) sc[jt][x] += part[i][x];
           }
         }
         // rows past the length weigh nothing
@@ -536,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
             for (int y = 0; y < 4; ++y) acc[x][y] *= al[R == 1 ? 0 : y >> 1];
         }
-        // weights, as bf16 terms: hi (and, where rows are spare or the output is f32, remainders)
-        constexpr int kTerms = F32 ? 3 : 2;
+        // weights, as bf16 terms: the first and its remainders
+        constexpr int kTerms = F32 || R == 1 ? 3 : 2;
         uint32_t pw[R][kTerms][2];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -562,21 +563,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const uint32_t b0 = y ? v.z : v.x, b1 = y ? v.w : v.y;
-            // f32 outputs: a step's products by themselves, added with a rounded addition. The matrix unit cuts
-            // sums off instead of rounding them, which over hundreds of steps adds up (8e-6 over 270).
+            // a step's products by themselves, added with a rounded addition
             float step[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            float(&d)[4] = F32 ? step : acc[x + y];
             if constexpr (R == 1) {
-              mma_bf16(d, pw[0][0][0], pw[0][1][0], pw[0][0][1], pw[0][1][1], b0, b1);
-              if constexpr (F32) mma_bf16(d, pw[0][2][0], 0u, pw[0][2][1], 0u, b0, b1);
+              mma_bf16(step, pw[0][0][0], pw[0][1][0], pw[0][0][1], pw[0][1][1], b0, b1);
+              mma_bf16(step, pw[0][2][0], 0u, pw[0][2][1], 0u, b0, b1);
             } else {
 #pragma unroll
-              for (int z = 0; z < kTerms; ++z) mma_bf16(d, pw[0][z][0], pw[R - 1][z][0], pw[0][z][1], pw[R - 1][z][1], b0, b1);
+              for (int z = 0; z < kTerms; ++z) mma_bf16(step, pw[0][z][0], pw[R - 1][z][0], pw[0][z][1], pw[R - 1][z][1], b0, b1);
             }
-            if constexpr (F32) {
 #pragma unroll
-              for (int z = 0; z < 4; ++z) acc[x + y][z] += step[z];
-            }
+            for (int z = 0; z < 4; ++z) acc[x + y][z] += step[z];
           }
         }
         __syncwarp();  // every lane has read this stage
