@@ -5,8 +5,8 @@
 // (a finished beam has one candidate: the end token at its own score), and the best K of all W V are
 // kept in order, ties to the lowest w V + t. Inside a beam the order is the logits' own, so the scan
 // needs no logarithm: one pass finds each beam's maximum, sum of exponentials and K best logits, and a
-// second, tiny kernel turns W K candidates into scores -- in two f32 terms, 48 bits, so that candidates of
-// different beams are not reordered by rounding.
+// second, tiny kernel turns W K candidates into scores -- in two f32 terms, 48 bits, so that the additions reorder
+// no candidates of different beams. (The log-sums that they subtract carry their exponentials' error, 2^-19.)
 //
 // What bounds it: HBM, one read of the logits (2 or 4 bytes for ~6 operations and one exponential).
 // A block streams a piece of a row, 16 bytes a thread and kVec such loads in flight, and only keeps
@@ -235,17 +235,20 @@ __device__ __forceinline__ float max_of(const uint4& v) {
 }
 
 // What a thread takes exponentials relative to: the largest element so far (0 while all are -inf).
-// exp(x - ref) = 2^(x c - r) fix with c = log2(e) rounded, r = ref c rounded and fix the factor that the two
-// roundings leave out: the difference is one FMA, exact but for its last bit. Beyond 2^27 the last bit of r
-// is no small factor, and the difference is taken first.
+// With log2(e) = c + T, c its nearest f32, r = ref c rounded and d = r - ref c its rounding error,
+//     exp(x - ref) = 2^((x - ref) (c + T)) = 2^(x c - r) 2^d 2^((x - ref) T).
+// x c - r is one FMA, exact but for its last bit; the last factor is left out (1.3e-8 for every unit below ref, where
+// the terms fall by e). |d| <= 2^-12 below 2^12, and the 2^d that all terms share is its series to the square (the
+// cube is below 2^-40). From 2^12 on the difference x - ref is taken first.
 struct Reference {
   float ref, r, fix;
   bool direct;
   __device__ __forceinline__ void set(float m) {
     ref = m == -INFINITY ? 0.0f : m;
     r = ref * kLog2e;
-    fix = fmaf(fmaf(-ref, kLog2e, r) - ref * kLog2eTail, 0.693147180559945309f, 1.0f);
-    direct = !(fabsf(ref) < 134217728.0f);
+    const float y = fmaf(-ref, kLog2e, r) * 0.693147180559945309f;
+    fix = 1.0f + fmaf(0.5f * y, y, y);
+    direct = !(fabsf(ref) < 4096.0f);
   }
 };
 

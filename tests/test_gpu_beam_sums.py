@@ -1,0 +1,51 @@
+"""The log-sums of dflash_beam_select over logits of any size, against 64 bits.
+
+A log-sum is off by what its exponentials are: 2 ulp (2^-22) each, and as much again for every change of the maximum that a
+term is relative to (a few in a thread, then in the warp, the block and the merge): 2^-19 together. A score adds its
+own rounding, 2^-24."""
+import numpy as np
+import pytest
+
+from tests import decode_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+def D():
+    import speculative_decoding_draft_rmsnorm_gb300 as lib
+    return lib
+
+
+def check(got, x, s, k):
+    want = R.beams(x.double().cpu().numpy(), s.cpu().numpy(), k)
+    assert np.array_equal(got["tokens"].cpu().numpy(), want[1])
+    assert np.array_equal(got["parents"].cpu().numpy(), want[2])
+    have = got["scores"].double().cpu().numpy()
+    assert np.all(np.abs(have - want[0]) <= 2.0 ** -19 + 2.0 ** -24 * np.abs(want[0]))
+
+
+SIZES = [0.0, 100.0, 200.0, 1000.0, 4000.0, 1e4, 1e5, 1e6, 2.0 ** 24, 3e7, 5e7, 1.2e8, 1e9, 1e30]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("vocab", [1000, 5003, 151936])
+def test_log_sums_of_large_logits(vocab, f32):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    at = torch.tensor([sign * a for a in SIZES for sign in (1, -1)], device="cuda")
+    x = 2.5 * torch.randn(len(at), 2, vocab, device="cuda", generator=g) + at[:, None, None]
+    x = x.to(torch.float32 if f32 else torch.bfloat16)
+    s = -10 * torch.rand(len(at), 2, device="cuda", generator=g)
+    check(D().beam_select(x, s, beams_out=4), x, s, 4)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_beams_of_different_sizes_are_ranked_alike(f32):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n, vocab = 12, 20011
+    at = torch.tensor([[0.0, 300.0, -900.0, 3000.0]], device="cuda")
+    x = 2.5 * torch.randn(n, 4, vocab, device="cuda", generator=g) + at[..., None]
+    x = x.to(torch.float32 if f32 else torch.bfloat16)
+    s = -0.1 * torch.rand(n, 4, device="cuda", generator=g)
+    check(D().beam_select(x, s, beams_out=16), x, s, 16)
