@@ -440,7 +440,8 @@ DFLASH_API size_t dflash_beam_workspace_size(int num_reqs, int beams, int beams_
  *            dflash_fork_pages where K = W); finished uint8 = the parent's, or token == eos. Slots
  *            without a candidate hold -inf, -1, -1 and 0.
  *   1 <= W, K <= 32, vocab < 2^26. Logits of one beam are compared exactly; scores of different beams in 64 bits,
- *   each exponential within 2^-19 and their sum held in two f32 terms. Two launches.
+ *   each exponential within 2^-19 and their sum held in two f32 terms; beams of equal logits have equal log-sums,
+ *   however their rows are aligned. Two launches.
  */
 DFLASH_API int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stride, const float* scores,
                                   const uint8_t* finished, int num_reqs, int beams, int beams_out, int vocab, int eos,

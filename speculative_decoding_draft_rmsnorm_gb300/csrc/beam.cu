@@ -79,7 +79,7 @@ struct BeamArgs {
   int64_t req_stride, beam_stride;  // elements
   const float* scores;
   const uint8_t* finished;  // null: none
-  int beams, out_beams, vocab, eos;
+  int beams, out_beams, vocab, eos, f32;
   // The rows' tiles (kTile vectors) laid end to end are dealt out in equal consecutive shares, one a block;
   // what block b finds in row r goes to list b + r. (row_tiles >= tiles: rows may be filled up to whole shares.)
   int rows, tiles, row_tiles, per_block, most_lists;  // tiles of a row, of a block; most lists of a row
@@ -605,13 +605,89 @@ __device__ __forceinline__ Lists lists_of(const BeamArgs& a, int row) {
 template <int kGroups>
 __device__ __forceinline__ int scattered(int i) { return (static_cast<uint32_t>(i) * 2654435761u) / (0x100000000ull / kGroups); }
 
-// One block per request: every thread holds up to kPer candidates.
+// What the merge knows of a beam.
+struct alignas(16) BeamSum {
+  float hi, lo;  // log-sum in two terms; 0 where finished
+  float top;  // maximum
+  int ended;  // finished
+};
+
+// Whether the logits of two rows are equal, by the merge's block (0 and -0 are). T: their bits.
+template <typename T>
+__device__ __forceinline__ bool rows_equal(const BeamArgs& a, int n, int w0, int w1) {
+  constexpr int kStep = 8, kPer = 16 / static_cast<int>(sizeof(T));
+  constexpr uint32_t kSize = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;  // all bits but signs
+  const T* base = static_cast<const T*>(a.logits) + n * a.req_stride;
+  const T *x = base + w0 * a.beam_stride, *y = base + w1 * a.beam_stride;
+  auto differ = [](uint32_t u, uint32_t v) {
+    const uint32_t d = u ^ v, size = (u | v) & kSize;
+    if constexpr (sizeof(T) == 4) return (d != 0) & (size != 0);
+    else return ((d << 16 != 0) & (size << 16 != 0)) | ((d >> 16 != 0) & (size >> 16 != 0));
+  };
+  // 16-byte vectors between the ends, where both rows have them at the same elements
+  int head = a.vocab, vecs = 0;
+  if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15u) == 0) {
+    head = min(a.vocab, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15u)) % 16 / sizeof(T)));
+    vecs = (a.vocab - head) / kPer;
+  }
+  const uint4 *xv = reinterpret_cast<const uint4*>(x + head), *yv = reinterpret_cast<const uint4*>(y + head);
+  const int ends = a.vocab - vecs * kPer;
+  bool found = false;
+#pragma unroll 1
+  for (int i0 = 0; i0 < ends; i0 += kMergeThreads * kStep) {
+    T u[kStep], v[kStep];
+#pragma unroll
+    for (int j = 0; j < kStep; ++j) {
+      int i = min(i0 + j * kMergeThreads + static_cast<int>(threadIdx.x), ends - 1);
+      if (i >= head) i += vecs * kPer;
+      u[j] = x[i], v[j] = y[i];
+    }
+#pragma unroll
+    for (int j = 0; j < kStep; ++j) found |= differ(u[j], v[j]);
+    if (i0 == 0 && __syncthreads_or(found)) return false;  // rows that are not equal show it at once, as a rule
+  }
+#pragma unroll 4
+  for (int i = threadIdx.x; i < vecs; i += kMergeThreads) {
+    const uint4 u = xv[i], v = yv[i];
+    found |= differ(u.x, v.x) | differ(u.y, v.y) | differ(u.z, v.z) | differ(u.w, v.w);
+  }
+  return !__syncthreads_or(found);
+}
+
+// A row's sum carries its rounding, which depends on how the row is cut and aligned: beams of equal logits get log-sums
+// that differ by it, and their candidates would be ordered by it. Log-sums next to one another, of one maximum, may be
+// of equal rows, which a look at the rows decides. (Without equal beams this is 0.0-0.3 us a call; each of them costs a
+// comparison, 5 us for 32003 f32 logits, 30 for 151937 bf16 ones that are aligned differently.)
+__device__ __forceinline__ bool may_be_equal(const BeamSum& x, const BeamSum& y) {
+  const float d = (x.hi - y.hi) + (x.lo - y.lo);  // NaN for rows without candidates
+  return (x.top == y.top) & ((x.ended | y.ended) == 0) & (d != 0.0f) & (fabsf(d) <= 0x1p-17f);
+}
+
+// Gives beams of equal logits the log-sum of the first of them. (By the block; its threads agree on every branch.)
+__device__ __noinline__ void share_log_sums(const BeamArgs& a, int n, BeamSum* s_beam) {
+#pragma unroll 1
+  for (int w = 1; w < a.beams; ++w) {
+    if (!(a.scores[n * a.beams + w] > -INFINITY)) continue;
+#pragma unroll 1
+    for (int o = 0; o < w; ++o) {
+      if (!(a.scores[n * a.beams + o] > -INFINITY) || !may_be_equal(s_beam[o], s_beam[w])) continue;
+      if (!(a.f32 ? rows_equal<uint32_t>(a, n, o, w) : rows_equal<uint16_t>(a, n, o, w))) continue;
+      const float hi = s_beam[o].hi, lo = s_beam[o].lo;
+      __syncthreads();  // every thread has compared the old one
+      if (threadIdx.x == 0) s_beam[w].hi = hi, s_beam[w].lo = lo;
+      __syncthreads();
+      break;
+    }
+  }
+}
+
+// One block per request: every thread holds up to kPer candidates. 64 registers are enough for few; with many they
+// would spill (8 x 16 -> 32 beams of 100000: 16.9 us, 19.1 so).
 template <int kPer, int kGroups>
-__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
+__global__ void __launch_bounds__(kMergeThreads, kPer > 2 ? 1 : 2) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
   constexpr int kThreads = kMergeThreads, kMergeWarps = kThreads / 32;
   __shared__ Lists s_lists[kMaxBeams];
-  __shared__ bool s_ended[kMaxBeams];
-  __shared__ Sum s_lse[kMaxBeams];  // log-sums in two terms
+  __shared__ BeamSum s_beam[kMaxBeams];
   __shared__ Best s_best[2][kMergeWarps], s_list[kMergeRoom];
   __shared__ uint32_t s_group[kGroups], s_bound;
   __shared__ int s_count;
@@ -626,96 +702,114 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
   // wait for the scan. Candidate i is number
   // i % K of list i / K % S of beam i / (S K); i < 2^12, so that products with a reciprocal divide exactly
   const float per_beam = 1.0f / static_cast<float>(S * K), per_list = 1.0f / static_cast<float>(K);
-  float val[kPer], score[kPer];
-  int32_t idx[kPer];
-  uint8_t ended[kPer];
-  int64_t at[kPer];  // in the lists; -1: none
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = j * kThreads + tid;
-    at[j] = -1, score[j] = 0.0f, ended[j] = 0;
-    if (i < total) {
-      const int w = static_cast<int>((i + 0.5f) * per_beam), rest = i - w * S * K;
-      const int s = static_cast<int>((rest + 0.5f) * per_list), row = n * W + w;
-      const Lists lists = s_lists[w];
-      score[j] = a.scores[row];
-      ended[j] = a.finished ? a.finished[row] : 0;
-      if (s < lists.count) at[j] = (lists.first + s) * K + (rest - s * K);
-    }
-  }
-  const bool one = warp < W && lane < s_lists[warp].count;  // a list of the warp's first beam
-  const bool first_ended = warp < W && a.finished && a.finished[n * W + warp];
-  fetch(a.part_max), fetch(a.part_sum), fetch(a.part_val), fetch(a.part_idx);
-  fetch(a.out_scores), fetch(a.out_tokens), fetch(a.out_parents), fetch(a.out_finished);
-  grid_dependency_wait();
-  float first_max = -INFINITY;
-  Sum first_sum;
-  if (one) {
-    first_max = a.part_max[s_lists[warp].first + lane];
-    first_sum = a.part_sum[s_lists[warp].first + lane];
-  }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    idx[j] = at[j] < 0 ? -1 : a.part_idx[at[j]];
-    val[j] = at[j] < 0 ? 0.0f : a.part_val[at[j]];
-  }
-#pragma unroll 1
-  for (int w = warp; w < W; w += kMergeWarps) {
-    const Lists lists = s_lists[w];
-    const bool finished = w == warp ? first_ended : a.finished && a.finished[n * W + w];
-    float m = -INFINITY;
-    Sum sum;
-#pragma unroll 1
-    for (int i = lane; i < lists.count; i += 32) {
-      const bool here = w == warp && i == lane;
-      const float om = here ? first_max : a.part_max[lists.first + i];
-      Sum o = here ? first_sum : a.part_sum[lists.first + i];
-      const float top = fmaxf(m, om);
-      if (m != -INFINITY) sum.scale(exp_below(m, top));
-      if (om != -INFINITY) o.scale(exp_below(om, top));
-      sum.add(o.hi);
-      sum.lo += o.lo;
-      m = top;
-    }
-    float top = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (m != -INFINITY) sum.scale(exp_below(m, top));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float hi = __shfl_down_sync(0xffffffffu, sum.hi, o), lo = __shfl_down_sync(0xffffffffu, sum.lo, o);
-      sum.add(hi);
-      sum.lo += lo;
-    }
-    // a finished beam's candidate is its score
-    const Sum lse = finished ? Sum{0.0f, 0.0f} : log_plus(top, sum);
-    if (lane == 0) s_lse[w] = lse, s_ended[w] = finished;
-  }
-  __syncthreads();
   Best mine[kPer];
+  // Once; and once more where beams of equal logits turned up, whose log-sums are then the same.
+#pragma unroll 1
+  for (bool again = false;; again = true) {
+    float val[kPer], score[kPer];
+    int32_t idx[kPer];
+    uint8_t ended[kPer];
+    int64_t at[kPer];  // in the lists; -1: none
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = j * kThreads + tid;
-    const int w = min(W - 1, static_cast<int>((i + 0.5f) * per_beam));
-    mine[j] = Best{0, 0, 0x7fffffff};
-    if (ended[j]) idx[j] = i - w * S * K == 0 ? a.eos : -1, val[j] = 0.0f;
-    if (idx[j] >= 0 && i < total) {
-      // score + value - lse, each sum with its rounding error
-      const Sum lse = s_lse[w];
-      Sum c{score[j], 0.0f};
-      c.add(val[j]);
-      c.add(-lse.hi);
-      const float lo = c.lo - lse.lo;
-      float hi = c.hi + lo;
-      const float z = hi - c.hi;
-      float rest = (c.hi - (hi - z)) + (lo - z);
-      if (!(fabsf(hi) < INFINITY)) hi = score[j] + val[j] - lse.hi, rest = 0.0f;
-      if (hi > -INFINITY) {  // -inf and NaN are no candidates
-        mine[j].hi = order_key(hi + 0.0f);
-        mine[j].lo = order_key(rest + 0.0f);
-        mine[j].at = w << kVocabBits | idx[j];
+    for (int j = 0; j < kPer; ++j) {
+      const int i = j * kThreads + tid;
+      at[j] = -1, score[j] = 0.0f, ended[j] = 0;
+      if (i < total) {
+        const int w = static_cast<int>((i + 0.5f) * per_beam), rest = i - w * S * K;
+        const int s = static_cast<int>((rest + 0.5f) * per_list), row = n * W + w;
+        const Lists lists = s_lists[w];
+        score[j] = a.scores[row];
+        ended[j] = a.finished ? a.finished[row] : 0;
+        if (s < lists.count) at[j] = (lists.first + s) * K + (rest - s * K);
       }
     }
+    const bool one = warp < W && lane < s_lists[warp].count;  // a list of the warp's first beam
+    const bool first_ended = warp < W && a.finished && a.finished[n * W + warp];
+    fetch(a.part_max), fetch(a.part_sum), fetch(a.part_val), fetch(a.part_idx);
+    fetch(a.out_scores), fetch(a.out_tokens), fetch(a.out_parents), fetch(a.out_finished);
+    grid_dependency_wait();
+    float first_max = -INFINITY;
+    Sum first_sum;
+    if (one) {
+      first_max = a.part_max[s_lists[warp].first + lane];
+      first_sum = a.part_sum[s_lists[warp].first + lane];
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      idx[j] = at[j] < 0 ? -1 : a.part_idx[at[j]];
+      val[j] = at[j] < 0 ? 0.0f : a.part_val[at[j]];
+    }
+#pragma unroll 1
+    for (int w = again ? W : warp; w < W; w += kMergeWarps) {
+      const Lists lists = s_lists[w];
+      const bool finished = w == warp ? first_ended : a.finished && a.finished[n * W + w];
+      float m = -INFINITY;
+      Sum sum;
+#pragma unroll 1
+      for (int i = lane; i < lists.count; i += 32) {
+        const bool here = w == warp && i == lane;
+        const float om = here ? first_max : a.part_max[lists.first + i];
+        Sum o = here ? first_sum : a.part_sum[lists.first + i];
+        const float top = fmaxf(m, om);
+        if (m != -INFINITY) sum.scale(exp_below(m, top));
+        if (om != -INFINITY) o.scale(exp_below(om, top));
+        sum.add(o.hi);
+        sum.lo += o.lo;
+        m = top;
+      }
+      float top = m;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (m != -INFINITY) sum.scale(exp_below(m, top));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float hi = __shfl_down_sync(0xffffffffu, sum.hi, o), lo = __shfl_down_sync(0xffffffffu, sum.lo, o);
+        sum.add(hi);
+        sum.lo += lo;
+      }
+      // a finished beam's candidate is its score
+      const Sum lse = finished ? Sum{0.0f, 0.0f} : log_plus(top, sum);
+      if (lane == 0) s_beam[w] = BeamSum{lse.hi, lse.lo, top, finished};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = j * kThreads + tid;
+      const int w = min(W - 1, static_cast<int>((i + 0.5f) * per_beam));
+      mine[j] = Best{0, 0, 0x7fffffff};
+      if (ended[j]) idx[j] = i - w * S * K == 0 ? a.eos : -1, val[j] = 0.0f;
+      if (idx[j] >= 0 && i < total) {
+        // score + value - lse, each sum with its rounding error
+        const Sum lse{s_beam[w].hi, s_beam[w].lo};
+        Sum c{score[j], 0.0f};
+        c.add(val[j]);
+        c.add(-lse.hi);
+        const float lo = c.lo - lse.lo;
+        float hi = c.hi + lo;
+        const float z = hi - c.hi;
+        float rest = (c.hi - (hi - z)) + (lo - z);
+        if (!(fabsf(hi) < INFINITY)) hi = score[j] + val[j] - lse.hi, rest = 0.0f;
+        if (hi > -INFINITY) {  // -inf and NaN are no candidates
+          mine[j].hi = order_key(hi + 0.0f);
+          mine[j].lo = order_key(rest + 0.0f);
+          mine[j].at = w << kVocabBits | idx[j];
+        }
+      }
+    }
+    // As in the scan: the K-th largest of the groups' maxima is a bound, and what reaches it is ranked.
+    // (Candidate i is the i % K-th of its list: groups of i % 64 would hold the same places of all lists.)
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (mine[j].hi) atomicMax(&s_group[scattered<kGroups>(j * kThreads + tid)], mine[j].hi);
+    bool suspect = false;
+    for (int i = again ? W * kMaxBeams : tid; i < W * kMaxBeams; i += kThreads) {
+      const int w = i / kMaxBeams, o = i % kMaxBeams;
+      if (o < w) suspect |= may_be_equal(s_beam[o], s_beam[w]);
+    }
+    if (!__syncthreads_or(suspect)) break;
+    share_log_sums(a, n, s_beam);
+    if (tid < kGroups) s_group[tid] = 0;
+    __syncthreads();
   }
   auto write = [&](int k, const Best& b) {
     const int64_t o = static_cast<int64_t>(n) * K + k;
@@ -724,14 +818,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     a.out_scores[o] = none ? -INFINITY : from_key(b.hi);
     a.out_tokens[o] = t;
     a.out_parents[o] = none ? -1 : n * W + w;
-    a.out_finished[o] = !none && (t == a.eos || s_ended[w]);
+    a.out_finished[o] = !none && (t == a.eos || s_beam[w].ended);
   };
-  // As in the scan: the K-th largest of the groups' maxima is a bound, and what reaches it is ranked.
-  // (Candidate i is the i % K-th of its list: groups of i % 64 would hold the same places of all lists.)
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (mine[j].hi) atomicMax(&s_group[scattered<kGroups>(j * kThreads + tid)], mine[j].hi);
-  __syncthreads();
   if (holds_bound<kThreads, kGroups>(s_group, tid, K)) s_bound = s_group[tid / (kThreads / kGroups)];
   __syncthreads();
   const uint32_t top = s_bound;
@@ -869,7 +957,7 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   a.rows = num_reqs * beams, a.tiles = y.tiles, a.per_block = y.per_block, a.most_lists = y.most_lists, a.row_tiles = y.row_tiles;
   a.logits = logits, a.req_stride = req_stride, a.beam_stride = beam_stride;
   a.scores = scores, a.finished = finished;
-  a.beams = beams, a.out_beams = beams_out, a.vocab = vocab, a.eos = eos;
+  a.beams = beams, a.out_beams = beams_out, a.vocab = vocab, a.eos = eos, a.f32 = es == 4;
   a.part_sum = static_cast<Sum*>(workspace);
   a.part_max = reinterpret_cast<float*>(a.part_sum + lists);
   a.part_val = a.part_max + lists;

@@ -49,3 +49,28 @@ def test_beams_of_different_sizes_are_ranked_alike(f32):
     x = x.to(torch.float32 if f32 else torch.bfloat16)
     s = -0.1 * torch.rand(n, 4, device="cuda", generator=g)
     check(D().beam_select(x, s, beams_out=16), x, s, 16)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("n,w,k,vocab,pad", [
+    (6, 3, 8, 32003, 0), (3, 8, 8, 151936, 0), (40, 4, 8, 20000, 1), (75, 4, 4, 20003, 0), (200, 5, 7, 5000, 0), (1, 32, 32, 40001, 3),
+    (3, 4, 16, 1001, 0),
+])
+def test_equal_beams_tie_however_their_rows_lie(n, w, k, vocab, pad, f32):
+    """Beams of equal logits and equal scores: the candidates tie in pairs, the lower beam first. Rows of an odd length
+    (or stride) are aligned differently, and rows laid end to end are cut at different places."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    x = torch.empty(n, w, vocab + pad, device="cuda", dtype=torch.float32 if f32 else torch.bfloat16)[:, :, :vocab]
+    x.copy_(2.5 * torch.randn(n, 1, vocab, device="cuda", generator=g))
+    s = torch.full((n, w), -1.0, device="cuda")
+    x[::2, w - 1, ::7] = -float("inf")  # every other request: the last beam is another
+    if w > 2:
+        x[:, 1] = 2.5 * torch.randn(n, vocab, device="cuda", generator=g)  # and the second
+    x[:, :, 3] = 0.0
+    x[:, 0, 3] = -0.0
+    check(D().beam_select(x, s, beams_out=k), x, s, k)
+    s[:, 0] = -float("inf")             # not live: no candidates, whatever its logits
+    check(D().beam_select(x, s, beams_out=k), x, s, k)
+    s = -1.0 - 0.37 * torch.arange(w, device="cuda").float().repeat(n, 1)
+    check(D().beam_select(x, s, beams_out=k), x, s, k)
