@@ -420,7 +420,8 @@ DFLASH_API int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_str
                                              dflash_stream_t stream);
 
 /* Bytes of workspace of dflash_beam_select on the current device (0 and a message if the arguments
- * are invalid). It needs no initialisation; concurrent calls must not share one. */
+ * are invalid). It needs no initialisation; concurrent calls must not share one. The size grows with
+ * every argument: one workspace does for all calls of no more requests, beams and tokens. */
 DFLASH_API size_t dflash_beam_workspace_size(int num_reqs, int beams, int beams_out, int vocab, int dtype);
 
 /*

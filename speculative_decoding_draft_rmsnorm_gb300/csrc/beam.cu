@@ -910,8 +910,12 @@ int check(int reqs, int beams, int out_beams, int vocab, int dtype) {
   return DFLASH_OK;
 }
 
-size_t bytes_of(const Shares& y, int out_beams) {
-  return 256 + static_cast<size_t>(y.lists) * (12 + 8 * static_cast<size_t>(out_beams));
+// Bytes of a list for every block and row. There are at most a wave of blocks and at most one for every tile: a bound
+// that grows with every argument, unlike the shares, so that a workspace of the largest call does for the others.
+size_t bytes_of(int reqs, int beams, int out_beams, int vocab, int elem, int sms) {
+  const int64_t rows = static_cast<int64_t>(reqs) * beams, per_tile = kTile * (16 / elem);
+  const int64_t lists = rows + std::min(rows * ((vocab + per_tile - 1) / per_tile), static_cast<int64_t>(sms) * kBlocksPerSm);
+  return 256 + static_cast<size_t>(lists) * (12 + 8 * static_cast<size_t>(out_beams));
 }
 
 }  // namespace
@@ -925,7 +929,7 @@ size_t dflash_beam_workspace_size(int num_reqs, int beams, int beams_out, int vo
   int sms = 0;
   if (query_sms(&sms) != DFLASH_OK) return 0;
   report_error(DFLASH_OK, "");
-  return bytes_of(shares_of(std::max(num_reqs, 1), beams, beams_out, vocab, dtype == DFLASH_OUT_F32 ? 4 : 2, sms), beams_out);
+  return bytes_of(std::max(num_reqs, 1), beams, beams_out, vocab, dtype == DFLASH_OUT_F32 ? 4 : 2, sms);
 }
 
 int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stride, const float* scores,
@@ -951,8 +955,8 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   if (rc != DFLASH_OK) return rc;
   BeamArgs a{};
   const Shares y = shares_of(num_reqs, beams, beams_out, vocab, es, sms);
-  if (workspace_bytes < bytes_of(y, beams_out))
-    return errorf(DFLASH_ERR_WORKSPACE, "workspace has %zu bytes; %zu are needed", workspace_bytes, bytes_of(y, beams_out));
+  const size_t need = bytes_of(num_reqs, beams, beams_out, vocab, es, sms);
+  if (workspace_bytes < need) return errorf(DFLASH_ERR_WORKSPACE, "workspace has %zu bytes; %zu are needed", workspace_bytes, need);
   const size_t lists = static_cast<size_t>(y.lists);
   a.rows = num_reqs * beams, a.tiles = y.tiles, a.per_block = y.per_block, a.most_lists = y.most_lists, a.row_tiles = y.row_tiles;
   a.logits = logits, a.req_stride = req_stride, a.beam_stride = beam_stride;
