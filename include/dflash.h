@@ -379,7 +379,8 @@ DFLASH_API int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void*
                              int dtype, int32_t* status, dflash_stream_t stream);
 
 /* Bytes of workspace of dflash_decode_attention_paged on the current device (0 and a message if the
- * arguments are invalid). It needs no initialisation; concurrent calls must not share one. */
+ * arguments are invalid). It needs no initialisation; concurrent calls must not share one. The size
+ * grows with num_reqs and max_ctx_len. */
 DFLASH_API size_t dflash_decode_workspace_size(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int window);
 
 /*

@@ -794,8 +794,9 @@ int head_tile(int g) { return g <= 8 ? 8 : 16; }
 int head_tiles(int hq, int hkv) { return (hq / hkv + head_tile(hq / hkv) - 1) / head_tile(hq / hkv); }
 // units of a kv head: a unit's warps, at most a block's, read the same rows, so that they come from HBM once
 int tile_units(int hq, int hkv) { return (head_tiles(hq, hkv) + kWarps - 1) / kWarps; }
-int64_t most_steps(int max_ctx_len, int window) {  // of a sequence and kv head
-  return ((window > 0 ? std::min(max_ctx_len, window) : max_ctx_len) + static_cast<int64_t>(kStep) - 1) / kStep;
+// of a sequence and kv head; one for no rows at all too, so that a workspace's size grows with the batch there as well
+int64_t most_steps(int max_ctx_len, int window) {
+  return std::max<int64_t>(1, ((window > 0 ? std::min(max_ctx_len, window) : max_ctx_len) + static_cast<int64_t>(kStep) - 1) / kStep);
 }
 double most_steps_of_call(int num_reqs, int hq, int hkv, int max_ctx_len, int window) {
   return static_cast<double>(most_steps(max_ctx_len, window)) * hkv * tile_units(hq, hkv) * num_reqs;
