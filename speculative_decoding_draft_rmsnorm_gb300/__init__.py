@@ -65,7 +65,7 @@ def load(build_if_missing: bool = True):
         if not _build.up_to_date():
             if not build_if_missing:
                 raise RuntimeError(f"{_build.LIB_PATH} is not built; run __graft_entry__.build()")
-            _build.build()
+            _build.build(bind=False)
         lib = ctypes.CDLL(_build.LIB_PATH)
         P, I32, I64, F32, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
         lib.dflash_last_error.restype = ctypes.c_char_p

@@ -7,6 +7,10 @@ A second library, libdflash_gb300_waittest.so, is built from the same sources wi
 DFLASH_WAIT_TEST defined: device waits give up after 5 ms instead of 2 s, and a hook can
 withhold one V tile's copy, so that a test can watch a bounded wait run out and the
 kernel unwind. Only the tests load it; the package loads the product library.
+
+The marshalling module of decode.py (csrc/bind.cpp, host C++ against torch and the product
+library) is built last, and only decode.py's calls need it: the libraries build and load
+without torch.
 """
 from __future__ import annotations
 
@@ -52,11 +56,8 @@ def _inputs() -> list[str]:
     return files
 
 
-def up_to_date(path: str | None = None) -> bool:
-    """Whether a library is there and newer than its sources; without a path, the product library and the
-    marshalling module."""
-    if path is None:
-        return up_to_date(LIB_PATH) and up_to_date(BIND_PATH)
+def up_to_date(path: str = LIB_PATH) -> bool:
+    """Whether a library (or the marshalling module) is there and newer than its sources."""
     if not os.path.exists(path):
         return False
     t = os.path.getmtime(path)
@@ -94,11 +95,11 @@ def _link_bind(obj: str) -> None:
     os.replace(tmp, BIND_PATH)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Builds both libraries (every translation unit of both in one parallel pass) and
-    returns the product library's path."""
+def build(force: bool = False, verbose: bool = False, bind: bool = True) -> str:
+    """Builds both libraries (every translation unit of both in one parallel pass) and, unless
+    bind is False, the marshalling module; returns the product library's path."""
     todo = [t for t in TARGETS if force or not up_to_date(t[0])]
-    bind = force or not up_to_date(BIND_PATH)
+    bind = bind and (force or not up_to_date(BIND_PATH))
     if not todo and not bind:
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
@@ -124,7 +125,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(workers) as ex:
         bind_obj = ex.submit(_compile_bind) if bind else None
         objs = list(ex.map(compile_one, jobs))
-        bind_obj = bind_obj.result() if bind else None
     for i, (path, _, _) in enumerate(todo):
         tmp = path + f".tmp{os.getpid()}"
         mine = objs[i * len(SOURCES):(i + 1) * len(SOURCES)]
@@ -133,7 +133,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, path)
     if bind:
-        _link_bind(bind_obj)
+        _link_bind(bind_obj.result())  # its failure leaves the libraries built
     return LIB_PATH
 
 

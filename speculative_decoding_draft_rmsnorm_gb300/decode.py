@@ -62,11 +62,15 @@ def _load():
 
     from . import _build
     _base().load()
-    loader = importlib.machinery.ExtensionFileLoader("_decode_bind", _build.BIND_PATH)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_decode_bind", loader))
-    loader.exec_module(module)
-    _bind = module
-    return module
+    with _base()._lock:
+        if _bind is None:
+            if not _build.up_to_date(_build.BIND_PATH):
+                _build.build()
+            loader = importlib.machinery.ExtensionFileLoader("_decode_bind", _build.BIND_PATH)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_decode_bind", loader))
+            loader.exec_module(module)
+            _bind = module
+    return _bind
 
 
 def _fail(rc):
