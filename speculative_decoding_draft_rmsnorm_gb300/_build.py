@@ -31,7 +31,6 @@ SOURCES = ["api.cu", "attention.cu", "norm_rope.cu", "noalloc.cu", "draft_step.c
 HEADERS = ["ptx.cuh", "internal.h", "norm_rope.cuh", "decode_host.h"]
 # The marshalling module of decode.py: host C++ against torch and the product library.
 BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
-BIND_PATH = os.path.join(LIB_DIR, "_decode_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-DDFLASH_BUILD"]
@@ -42,6 +41,16 @@ def nvcc() -> str:
     if not os.path.exists(p):
         raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build the library")
     return p
+
+
+def bind_path() -> str:
+    """The marshalling module. It uses parts of torch that change between versions: the file is named after the
+    interpreter, the torch and the C++ ABI that it was built for."""
+    import sysconfig
+
+    import torch
+    return os.path.join(LIB_DIR, f"_decode_bind.{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}"
+                                 f"-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}.so")
 
 
 WAIT_TEST_LIB_PATH = os.path.join(LIB_DIR, "libdflash_gb300_waittest.so")
@@ -61,7 +70,8 @@ def up_to_date(path: str = LIB_PATH) -> bool:
     if not os.path.exists(path):
         return False
     t = os.path.getmtime(path)
-    files = [BIND_SOURCE, os.path.join(ROOT, "include", "dflash.h")] if path == BIND_PATH else _inputs()
+    bind = os.path.basename(path).startswith("_decode_bind.")
+    files = [BIND_SOURCE, os.path.join(ROOT, "include", "dflash.h")] if bind else _inputs()
     return all(os.path.getmtime(f) <= t for f in files)
 
 
@@ -86,20 +96,21 @@ def _compile_bind() -> str:
 def _link_bind(obj: str) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    path = bind_path()
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            "-L" + LIB_DIR, "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"linking the marshalling module failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BIND_PATH)
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False, bind: bool = True) -> str:
     """Builds both libraries (every translation unit of both in one parallel pass) and, unless
     bind is False, the marshalling module; returns the product library's path."""
     todo = [t for t in TARGETS if force or not up_to_date(t[0])]
-    bind = bind and (force or not up_to_date(BIND_PATH))
+    bind = bind and (force or not up_to_date(bind_path()))
     if not todo and not bind:
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)

@@ -64,9 +64,10 @@ def _load():
     _base().load()
     with _base()._lock:
         if _bind is None:
-            if not _build.up_to_date(_build.BIND_PATH):
+            path = _build.bind_path()
+            if not _build.up_to_date(path):
                 _build.build()
-            loader = importlib.machinery.ExtensionFileLoader("_decode_bind", _build.BIND_PATH)
+            loader = importlib.machinery.ExtensionFileLoader("_decode_bind", path)
             module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_decode_bind", loader))
             loader.exec_module(module)
             _bind = module

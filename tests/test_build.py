@@ -50,3 +50,13 @@ except RuntimeError as e:
     print("raised", "bind.cpp" in str(e), os.path.exists(_build.TARGETS[0][0]))
 """)
     assert out.split() == ["raised", "True", "True"]
+
+
+def test_a_marshalling_module_of_another_torch_is_not_taken(monkeypatch):
+    import torch
+    _build.build()
+    assert _build.up_to_date(_build.bind_path())
+    monkeypatch.setattr(torch, "__version__", "2.0.1+other")
+    assert not _build.up_to_date(_build.bind_path())
+    monkeypatch.undo()
+    assert _build.up_to_date(_build.bind_path())
