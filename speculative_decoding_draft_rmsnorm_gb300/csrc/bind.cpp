@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -225,6 +226,11 @@ PyObject* rotary(PyObject* const* a) {
     }
     ~Buffer() { PyBuffer_Release(this); }
   } freq(a[2]);
+  if (c10::GradMode::is_enabled())
+    for (int i : {0, 3, 4, 5, 6, 7})
+      if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad())
+        raise(PyExc_ValueError, "rotary records no gradient: call it under torch.no_grad() or with detached tensors "
+                                "(inverse=True gives the gradient of the inputs)");
   const int rc = run(at, [&](cudaStream_t stream) {
     return dflash_rotary(q.src, q.tok, q.head, q.dst, q.out_tok, q.out_head, hq, k.src, k.tok, k.head, k.dst, k.out_tok, k.out_head, hkv,
                          v.src, v.tok, v.head, v.dst, v.out_tok, v.out_head, pos, slot_p, n, capacity, d,

@@ -9,7 +9,8 @@
 
 Like the rest of the package these only marshal arguments (csrc/bind.cpp checks them and makes the call).
 All tensors of a call live on one device; the call runs there, on `stream` (default: that device's current
-stream). Outputs and workspaces that a call allocates belong to that stream.
+stream). Outputs and workspaces that a call allocates belong to that stream. No call records a gradient; rotary,
+whose inverse is one, refuses tensors that require it while gradients are recorded.
 """
 from __future__ import annotations
 
@@ -137,7 +138,8 @@ def rotary(q, positions, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_
     rotary_dim are copied. Outputs default to new contiguous tensors; q_out = q and k_out = k work in
     place. With slot [n] int32, k (and v) go to rows slot[t] of k_out (and v_out) [capacity, Hkv, Dh] or
     [num_pages, page_size, Hkv, Dh]; -1 = not stored. inverse=True applies the transpose: the gradient
-    of the inputs from that of the outputs. q may be None.
+    of the inputs from that of the outputs (none is recorded, so tensors that require one are refused
+    outside torch.no_grad()). q may be None.
     """
     bind = _bind or _load()
     if stream is not None:
