@@ -16,6 +16,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
 #include <string>
 #include <vector>
 
@@ -149,6 +150,15 @@ int run(const Place& at, F call) {
   return call(stream);
 }
 
+// Tensors that a call wrote (None: nothing): what autograd keeps of them for a backward pass is out of date.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(std::initializer_list<PyObject*> list) {
+  for (PyObject* o : list)
+    if (THPVariable_Check(o)) written(THPVariable_Unpack(o));
+}
+
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 // The object given, or the tensor made in its place.
 PyObject* given(PyObject* o, const at::Tensor& made) {
@@ -238,6 +248,9 @@ PyObject* rotary(PyObject* const* a) {
                          amplitude, inter, inverse, type == at::kFloat ? DFLASH_OUT_F32 : DFLASH_OUT_BF16, status, stream);
   });
   if (rc) return PyLong_FromLong(rc);
+  if (has_q) written({a[5]});
+  if (has_k) written({a[6], a[7]});
+  written({a[12]});
   return Py_BuildValue("(NN)", has_q ? given(a[5], new_q) : Py_NewRef(Py_None), has_k ? given(a[6], new_k) : Py_NewRef(Py_None));
 }
 
@@ -279,6 +292,7 @@ PyObject* decode_attention_paged(PyObject* const* a) {
                                          ws.bytes, status, stream);
   });
   if (rc) return PyLong_FromLong(rc);
+  written({a[6], a[7], a[9], a[13]});
   if (!lse && !(a[7] != Py_None || new_lse.defined())) return given(a[6], new_out);
   return Py_BuildValue("(NN)", given(a[6], new_out), given(a[7], new_lse));
 }
@@ -321,6 +335,7 @@ PyObject* beam_select(PyObject* const* a) {
                               stream);
   });
   if (rc) return PyLong_FromLong(rc);
+  written({a[5], a[6], a[7], a[8], a[9]});
   return Py_BuildValue("(NNNN)", given(a[5], made[0]), given(a[6], made[1]), given(a[7], made[2]), given(a[8], made[3]));
 }
 
@@ -343,6 +358,7 @@ struct Table {
 
 struct Pools {
   std::vector<void*> p;
+  std::vector<at::Tensor> tensors;
   int64_t bytes = 0, page = -1;
   Pools(const Place& at, PyObject* list, int64_t pages) {
     PyObject* seq = PySequence_Fast(list, "pools must be a list of tensors");
@@ -363,6 +379,7 @@ struct Pools {
         if (i && (b != bytes || t.size(1) != page)) bad = "all pools must have pages of the same size";
         bytes = b, page = t.size(1);
         p.push_back(t.data_ptr());
+        tensors.push_back(t);
       }
     }
     Py_DECREF(seq);
@@ -382,6 +399,7 @@ PyObject* fork_pages(PyObject* const* a) {
   auto* status = static_cast<int32_t*>(at.address("status", a[4], at::kInt, {1}));
   const int rc = run(at, [&](cudaStream_t stream) { return dflash_fork_pages(pp, lens, t.table, t.stride, t.refs, t.rows, t.width, t.pages, status, stream); });
   if (rc) return PyLong_FromLong(rc);
+  written({a[1], a[2], a[3], a[4]});
   Py_RETURN_NONE;
 }
 
@@ -417,6 +435,8 @@ PyObject* reserve_pages(PyObject* const* a) {
                                 num_new, t.width, page32, t.pages, advance, slots, pos, ws.p, ws.bytes, status, stream);
   });
   if (rc) return PyLong_FromLong(rc);
+  written({a[1], a[2], a[3], a[8], a[9], a[10], a[11]});
+  for (const at::Tensor& x : pools.tensors) written(x);
   return Py_BuildValue("(NN)", given(a[8], new_slots), given(a[9], new_pos));
 }
 
@@ -437,6 +457,8 @@ PyObject* compact_pages(PyObject* const* a) {
                                 t.pages, used, ws.p, ws.bytes, status, stream);
   });
   if (rc) return PyLong_FromLong(rc);
+  written({a[0], a[1], a[3], a[4], a[5]});
+  for (const at::Tensor& x : pools.tensors) written(x);
   return given(a[3], made);
 }
 

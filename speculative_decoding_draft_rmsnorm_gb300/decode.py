@@ -10,7 +10,8 @@
 Like the rest of the package these only marshal arguments (csrc/bind.cpp checks them and makes the call).
 All tensors of a call live on one device; the call runs there, on `stream` (default: that device's current
 stream). Outputs and workspaces that a call allocates belong to that stream. No call records a gradient; rotary,
-whose inverse is one, refuses tensors that require it while gradients are recorded.
+whose inverse is one, refuses tensors that require it while gradients are recorded. Tensors that a call writes count
+as changed in place.
 """
 from __future__ import annotations
 
