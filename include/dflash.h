@@ -440,7 +440,7 @@ DFLASH_API size_t dflash_beam_workspace_size(int num_reqs, int beams, int beams_
  *   eos      end token, or -1: none
  *   outputs  [num_reqs, K]: scores f32; tokens int32; parents int32 = r * W + w (the row of
  *            dflash_fork_pages where K = W); finished uint8 = the parent's, or token == eos. Slots
- *            without a candidate hold -inf, -1, -1 and 0.
+ *            without a candidate hold -inf, -1, -1 and 0. They may overlap neither scores and finished nor one another.
  *   1 <= W, K <= 32, vocab < 2^26. Logits of one beam are compared exactly; scores of different beams in 64 bits,
  *   each exponential within 2^-19 and their sum held in two f32 terms; beams of equal logits have equal log-sums,
  *   however their rows are aligned. Two launches.

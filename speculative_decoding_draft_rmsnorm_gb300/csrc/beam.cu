@@ -957,6 +957,19 @@ int dflash_beam_select(const void* logits, int64_t req_stride, int64_t beam_stri
   const Shares y = shares_of(num_reqs, beams, beams_out, vocab, es, sms);
   const size_t need = bytes_of(num_reqs, beams, beams_out, vocab, es, sms);
   if (workspace_bytes < need) return errorf(DFLASH_ERR_WORKSPACE, "workspace has %zu bytes; %zu are needed", workspace_bytes, need);
+  // a request's results may be written before another's inputs are read
+  auto overlap = [](const void* p, size_t np, const void* q, size_t nq) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), z = reinterpret_cast<uintptr_t>(q);
+    return x < z + nq && z < x + np;
+  };
+  const size_t in = static_cast<size_t>(num_reqs) * beams, outs = static_cast<size_t>(num_reqs) * beams_out;
+  const void* const out[4] = {out_scores, out_tokens, out_parents, out_finished};
+  for (int i = 0; i < 4; ++i) {
+    const size_t n = i < 3 ? outs * 4 : outs;
+    bool bad = overlap(out[i], n, scores, in * 4) || (finished && overlap(out[i], n, finished, in));
+    for (int j = i + 1; j < 4; ++j) bad |= overlap(out[i], n, out[j], j < 3 ? outs * 4 : outs);
+    if (bad) return errorf(DFLASH_ERR_INVALID_ARG, "outputs may overlap neither scores and finished nor one another");
+  }
   const size_t lists = static_cast<size_t>(y.lists);
   a.rows = num_reqs * beams, a.tiles = y.tiles, a.per_block = y.per_block, a.most_lists = y.most_lists, a.row_tiles = y.row_tiles;
   a.logits = logits, a.req_stride = req_stride, a.beam_stride = beam_stride;

@@ -74,3 +74,29 @@ def test_equal_beams_tie_however_their_rows_lie(n, w, k, vocab, pad, f32):
     check(D().beam_select(x, s, beams_out=k), x, s, k)
     s = -1.0 - 0.37 * torch.arange(w, device="cuda").float().repeat(n, 1)
     check(D().beam_select(x, s, beams_out=k), x, s, k)
+
+
+def test_overlapping_outputs_are_refused():
+    import torch
+    n, w, vocab = 6, 4, 500
+    x = torch.randn(n, w, vocab, device="cuda")
+    flat = torch.zeros(4 * n * w, device="cuda")
+    s = flat[:n * w].view(n, w)
+    ints = torch.zeros(2 * n * w, dtype=torch.int32, device="cuda")
+    flags = torch.zeros(2 * n * w, dtype=torch.bool, device="cuda")
+    fin = flags[:n * w].view(n, w)
+
+    def refused(**out):
+        with pytest.raises(D().DFlashError, match="overlap|alias"):
+            D().beam_select(x, s, finished=fin, eos=1, out=out)
+
+    for off in (0, 1, 5, n * w - 1):
+        refused(scores=flat[off:off + n * w].view(n, w))
+        refused(finished=flags[off:off + n * w].view(n, w))
+        refused(tokens=ints[:n * w].view(n, w), parents=ints[off:off + n * w].view(n, w))
+        refused(tokens=flat.view(torch.int32)[off:off + n * w].view(n, w))
+    want = D().beam_select(x, s, finished=fin, eos=1)
+    out = dict(scores=flat[n * w:2 * n * w].view(n, w), tokens=ints[:n * w].view(n, w), parents=ints[n * w:].view(n, w),
+               finished=flags[n * w:].view(n, w))
+    got = D().beam_select(x, s, finished=fin, eos=1, out=out)
+    assert all(torch.equal(got[k], want[k]) for k in want)
