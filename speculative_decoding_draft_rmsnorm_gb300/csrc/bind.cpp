@@ -297,7 +297,7 @@ PyObject* decode_attention_paged(PyObject* const* a) {
   return Py_BuildValue("(NN)", given(a[6], new_out), given(a[7], new_lse));
 }
 
-// logits, scores, beams_out (0: as many as in), finished, eos, scores out, tokens out, parents out, finished out, workspace
+// logits, scores, beams_out (None: as many as in), finished, eos, scores out, tokens out, parents out, finished out, workspace
 PyObject* beam_select(PyObject* const* a) {
   const at::Tensor& x = tensor(a[0], "logits");
   const Place at(x);
@@ -307,7 +307,7 @@ PyObject* beam_select(PyObject* const* a) {
   if (type != at::kBFloat16 && type != at::kFloat) raise(PyExc_TypeError, "logits must be bfloat16 or float32, got %s", c10::toString(type));
   const int dtype = type == at::kFloat ? DFLASH_OUT_F32 : DFLASH_OUT_BF16;
   const int n = dim32(x.size(0), "N"), w = dim32(x.size(1), "beams"), vocab = dim32(x.size(2), "vocab");
-  const int k = small(a[2], "beams_out"), eos = small(a[4], "eos");
+  const int k = a[2] == Py_None ? w : small(a[2], "beams_out"), eos = small(a[4], "eos");
   const auto* scores = static_cast<const float*>(at.address("scores", a[1], at::kFloat, {n, w}));
   const auto* finished = static_cast<const uint8_t*>(at.address("finished", a[3], at::kBool, {n, w}));
   if (k <= 0) raise(PyExc_ValueError, "beams_out must be positive");

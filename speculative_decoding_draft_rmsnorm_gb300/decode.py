@@ -196,15 +196,15 @@ def beam_select(logits, scores, *, beams_out=None, finished=None, eos=-1, out=No
     finished [N, W] bool; K = beams_out (default W) of W * vocab candidates are kept, best first, ties to
     the lowest index. Outputs [N, K]: scores f32, tokens int32, parents int32 (row r * W + w, as
     fork_pages takes them), finished bool; slots without a candidate hold -inf, -1, -1, False.
-    `out` may hold preallocated outputs, e.g. for graph capture; the others share one allocation.
+    `out` may hold preallocated outputs, e.g. for graph capture. Outputs that the call makes lie in one allocation:
+    each keeps all of it alive, and torch.save of one saves the storage of all (clone one to keep it alone).
     """
     bind = _bind or _load()
     if stream is not None:
         with _on(stream, logits):
             return beam_select(logits, scores, beams_out=beams_out, finished=finished, eos=eos, out=out, workspace=workspace)
     s, t, p, f = (out.get("scores"), out.get("tokens"), out.get("parents"), out.get("finished")) if out else (None,) * 4
-    got = bind.beam_select(logits, scores, scores.shape[1] if beams_out is None else int(beams_out), finished, int(eos), s, t, p, f,
-                           workspace)
+    got = bind.beam_select(logits, scores, None if beams_out is None else int(beams_out), finished, int(eos), s, t, p, f, workspace)
     if type(got) is int:
         _fail(got)
     return dict(zip(BEAM_OUTPUTS, got))
