@@ -45,3 +45,25 @@ def test_sums_of_a_long_range_do_not_drift(hq, f32):
     clear = np.abs(want - border) > tol * border
     assert clear.sum() > clear.size // 4 and (want[clear] < border + 1e-4).all()
     assert np.array_equal(have[clear], np.where(want > border, 1.0 + 2.0 ** -7, 1.0)[clear])
+
+
+@pytest.mark.parametrize("hq", [1, 8, 16])
+def test_weights_keep_24_bits_for_f32_outputs(hq):
+    """Two rows, with scores 0 and -t and values 0 and 1: the output is w / (1 + w), w = exp(-t).
+
+    Relative: the exponential 2^-22, its argument (the scale and one FMA) 2 t 2^-24 with t <= 2, the weight 2^-24, the
+    sum, its reciprocal and their product 2^-24 each: 2^-21 together. (16 bits of the weight are off by up to 2^-17.)"""
+    import torch
+    n, dh = 256, 64
+    t = torch.arange(1, n + 1).double() / 128  # exact in bf16
+    k, v = torch.zeros(n, 16, 1, dh, dtype=torch.bfloat16), torch.full((n, 16, 1, dh), float("nan"), dtype=torch.bfloat16)
+    k[:, 1, 0, 0] = -t.to(torch.bfloat16)
+    v[:, 0], v[:, 1] = 0.0, 1.0
+    q = torch.zeros(n, hq, dh, dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    table = torch.arange(n, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    lens = torch.full((n,), 2, dtype=torch.int32, device="cuda")
+    got = D().decode_attention_paged(q.cuda(), k.cuda(), v.cuda(), table, lens, max_ctx_len=16, scale=1.0, out_dtype=D().OUT_F32)
+    w = torch.exp(-t)
+    want = (w / (1 + w))[:, None, None]
+    assert bool(((got.double().cpu() - want).abs() <= 2.0 ** -21 * want).all())
