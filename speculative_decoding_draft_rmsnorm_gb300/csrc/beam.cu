@@ -17,9 +17,9 @@
 // streaming instead cost 52 instructions an element against ~8. Only where ties flood the candidates
 // (a constant row) does a block go over its piece again with such lists, one a warp.
 //
-// Measured: 64 x 8 beams of 151936 bf16 logits (156 MB) 33.6 us, floor 22.9: the stream alone takes 25.6 (22.6
-// without exponentials), the blocks' ends with bound and second look 4.4, the merge 3.6. 1 x 4 beams 7.0 us and
-// 17 x 5 of 32003 f32 8.5 us (floors 0.2 and 1.6): two dependent launches.
+// Measured: 64 x 8 beams of 151936 bf16 logits (156 MB) 33.8 us, floor 22.9: the stream takes about 25 of it, the
+// blocks' ends with bound and second look 4.4, the merge 4. 1 x 4 beams 6.9 us and 17 x 5 of 32003 f32 8.7 us (floors 0.2
+// and 1.6): two dependent launches.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -3,7 +3,7 @@
 // A decode step makes a handful of these calls, each a few microseconds of GPU time; checked and marshalled in
 // Python and ctypes one cost 22 us of host time on the Arm host (6 of them the call itself), here about 6.
 // Nothing is computed here: every function checks its tensors, allocates the outputs and the workspace that were
-// not given, and calls the C entry point on the current stream of the tensors' device. A function returns its
+// not given, calls the C entry point on the current stream of the tensors' device, and counts what it wrote as changed. A function returns its
 // outputs, or the C entry point's status where that is not 0; wrong arguments raise TypeError or ValueError.
 #include <Python.h>
 

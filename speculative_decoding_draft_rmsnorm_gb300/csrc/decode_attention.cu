@@ -24,8 +24,8 @@
 //   rounding them, 3e-8 of the sum a step, always towards zero: 1e-4 over a warp's 3750 steps. So it only ever sums a
 //   step's 16 rows, and those sums are added with rounded additions (at most 0.8 us for 32 sequences of 4096 rows up to
 //   16 heads a group; 32 heads 69 -> 77 us, f32 outputs 85).
-//   The idle rows cost nothing that matters: the tensor pipe is active in a fifth of a batch's cycles, waiting for the
-//   loads. Past 16 heads a group that ends: each tile of 16 heads is a warp that copies the same rows for itself (from
+//   The idle rows cost nothing that matters: the tensor pipe is active in a quarter of a batch's cycles, waiting for
+//   the loads. Past 16 heads a group that ends: each tile of 16 heads is a warp that copies the same rows for itself (from
 //   L2), and 32 heads a group take 77 us where 16 take 53 (32 sequences of 4096 rows, 537 MB; floor 39.5). Rings shared
 //   by such warps were slower still: it is the work of a step that bounds them, not its copy.
 // - A worker stores a group that it holds whole; of others it leaves (m, l, O), at its range's end in shared
@@ -33,9 +33,11 @@
 //   kernel what blocks share: at most two parts a block. All merges go in a fixed order: the result does not
 //   depend on timing. (Joining a lone 32000-row sequence from all warps' parts took 20 us more.)
 //
-// Measured: a ragged batch of 64 sequences, 610,000 rows of 8 kv heads (2.5 GB), 366-377 us, 98-100% of the copy
-// bandwidth; one sequence of 32000 rows (131 MB) 28.3 us, of which the floor is 19.3, the schedule before the first
-// load 2, the two joins 4, the launches the rest; one of 700 rows 8.5 us, of 16 rows 4.6: dependent latencies.
+// Measured: ragged batches of 64 sequences, 613,000 rows of 8 kv heads (2.5 GB; the mean of the three timed), 376 us, 98%
+// of the copy bandwidth; one sequence of 32000 rows (131 MB) 28.9 us, of which the floor is 19.3, the schedule before
+// the first load 2, the two joins 4, the launches the rest; one of 700 rows 8.7 us, of 16 rows 4.7: dependent latencies.
+// Sequences that share pages read them once each, from L2 where they come close together: 32 x 8 beams of 2048 rows
+// that share all but two pages 252 us, 326 with pages of their own.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -51,8 +53,8 @@ namespace {
 
 constexpr int kStep = 16;       // rows per step
 // A group of up to so many steps a unit of warps (512 rows at a unit a warp) has a block to itself where there are
-// SMs enough: no prefix over the sequences, no join. 256 rows of one sequence: 7.2 us against 8.2 cut; 700 rows:
-// 10.8 against 8.5; 500 rows of 32 heads a group (4 units a block): 15.7 against 14.0.
+// SMs enough: no prefix over the sequences, no join. 256 rows of one sequence: 7.2 us where cut ones took 8.2; 700 rows:
+// 10.8 and 8.5; 500 rows of 32 heads a group (4 units a block): 15.7 against 14.0.
 constexpr int kLoneSteps = 4;
 constexpr float kSlack = 8.0f;  // the running maximum may lag by 2^8
 
@@ -442,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     // One instruction copies kRows whole rows. 16-byte piece x of row y lies at piece x ^ f(y) of the row:
     // f(y) = (y & 1) * 4 for K, read 16 bytes a lane, and y & 7 for V, read as 8 x 8 blocks.
     constexpr int kRowBytes = DH * 2, kRowPieces = DH / 8, kRows = 32 / kRowPieces;
-    const uint64_t policy = l2_policy_evict_first();  // rows are read once: 1-2 us a call
+    // Rows of pages that are not shared are read once: 1-2 us a call (shared ones: 250-254 us with the policy, 249 without)
+    const uint64_t policy = l2_policy_evict_first();
     const int my_row = lane / kRowPieces, my_piece = lane % kRowPieces;
     const char* k_lane = reinterpret_cast<const char*>(a.k) + my_piece * 16;
     const char* v_lane = reinterpret_cast<const char*>(a.v) + my_piece * 16;

@@ -11,13 +11,15 @@
 // ~5 operations), so the arithmetic only has to stay out of the way. The sine and cosine are what
 // could get in it (~40 instructions a pair, against ~6 for the rotation): a thread therefore owns one
 // set of pairs of one token and walks over heads with it, so that each angle is computed once per
-// `head group` instead of once per head, and nothing is staged in shared memory.
+// `head group` instead of once per head. Only the frequency table is staged in shared memory: the lanes of a warp read
+// different pairs of it.
 //
 // A rotating thread's elements are two chunks of E: [uE, uE + E) and [rd/2 + uE, rd/2 + uE + E), each one load
 // of up to 16 bytes; lanes of consecutive u cover consecutive chunks. Both layouts use the same two
 // chunks: the half layout pairs them with each other, the interleaved one pairs neighbours inside
-// each. E is the largest power of two that divides rd/2 and the rest of the head and that the
-// pointers' and strides' alignment allows, so odd sizes run the same code with narrower accesses.
+// each. E is the largest power of two that divides rd/2 and that the alignment of q's and k's pointers and strides
+// allows, so odd sizes run the same code with narrower accesses. Elements that are only copied (behind rd, and v) go in
+// chunks of their own, of widths chosen in the same way.
 //
 // Measured: 32768 rows of 40 heads of 128 (671 MB) 104.2 us, 95% of the copy rate; 2001 rows of 20 heads, 20 of 80 elements, in f32
 // 5.3 us (floor 3.8); 32 rows into pages 3.2 us, a launch. Blocks of their own for what is copied:
