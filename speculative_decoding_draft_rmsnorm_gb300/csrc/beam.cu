@@ -605,11 +605,13 @@ __device__ __forceinline__ Lists lists_of(const BeamArgs& a, int row) {
 template <int kGroups>
 __device__ __forceinline__ int scattered(int i) { return (static_cast<uint32_t>(i) * 2654435761u) / (0x100000000ull / kGroups); }
 
+constexpr int kFinished = 1, kDead = 2;  // a dead beam's score is -inf or NaN
+
 // What the merge knows of a beam.
 struct alignas(16) BeamSum {
   float hi, lo;  // log-sum in two terms; 0 where finished
-  float top;  // maximum
-  int ended;  // finished
+  float top;     // maximum
+  int ended;     // kFinished, kDead
 };
 
 // Whether the logits of two rows are equal, by the merge's block (0 and -0 are). T: their bits.
@@ -667,10 +669,9 @@ __device__ __forceinline__ bool may_be_equal(const BeamSum& x, const BeamSum& y)
 __device__ __noinline__ void share_log_sums(const BeamArgs& a, int n, BeamSum* s_beam) {
 #pragma unroll 1
   for (int w = 1; w < a.beams; ++w) {
-    if (!(a.scores[n * a.beams + w] > -INFINITY)) continue;
 #pragma unroll 1
     for (int o = 0; o < w; ++o) {
-      if (!(a.scores[n * a.beams + o] > -INFINITY) || !may_be_equal(s_beam[o], s_beam[w])) continue;
+      if (!may_be_equal(s_beam[o], s_beam[w])) continue;
       if (!(a.f32 ? rows_equal<uint32_t>(a, n, o, w) : rows_equal<uint16_t>(a, n, o, w))) continue;
       const float hi = s_beam[o].hi, lo = s_beam[o].lo;
       __syncthreads();  // every thread has compared the old one
@@ -725,6 +726,7 @@ __global__ void __launch_bounds__(kMergeThreads, kPer > 2 ? 1 : 2) beam_merge_ke
     }
     const bool one = warp < W && lane < s_lists[warp].count;  // a list of the warp's first beam
     const bool first_ended = warp < W && a.finished && a.finished[n * W + warp];
+    const float first_score = warp < W ? a.scores[n * W + warp] : 0.0f;
     fetch(a.part_max), fetch(a.part_sum), fetch(a.part_val), fetch(a.part_idx);
     fetch(a.out_scores), fetch(a.out_tokens), fetch(a.out_parents), fetch(a.out_finished);
     grid_dependency_wait();
@@ -769,7 +771,8 @@ __global__ void __launch_bounds__(kMergeThreads, kPer > 2 ? 1 : 2) beam_merge_ke
       }
       // a finished beam's candidate is its score
       const Sum lse = finished ? Sum{0.0f, 0.0f} : log_plus(top, sum);
-      if (lane == 0) s_beam[w] = BeamSum{lse.hi, lse.lo, top, finished};
+      const float at = w == warp ? first_score : a.scores[n * W + w];
+      if (lane == 0) s_beam[w] = BeamSum{lse.hi, lse.lo, top, finished ? kFinished : at > -INFINITY ? 0 : kDead};
     }
     __syncthreads();
 #pragma unroll
@@ -818,7 +821,7 @@ __global__ void __launch_bounds__(kMergeThreads, kPer > 2 ? 1 : 2) beam_merge_ke
     a.out_scores[o] = none ? -INFINITY : from_key(b.hi);
     a.out_tokens[o] = t;
     a.out_parents[o] = none ? -1 : n * W + w;
-    a.out_finished[o] = !none && (t == a.eos || s_beam[w].ended);
+    a.out_finished[o] = !none && (t == a.eos || (s_beam[w].ended & kFinished));
   };
   if (holds_bound<kThreads, kGroups>(s_group, tid, K)) s_bound = s_group[tid / (kThreads / kGroups)];
   __syncthreads();
