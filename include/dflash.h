@@ -64,7 +64,8 @@ enum {
 
 enum {
   DFLASH_OUT_BF16 = 0,           /* out is bf16 [total_q, Hq, Dh]                       */
-  DFLASH_OUT_F32 = 1             /* out is f32; computed with split (hi+lo) bf16 operands */
+  DFLASH_OUT_F32 = 1,            /* out is f32; computed with split (hi+lo) bf16 operands */
+  DFLASH_OUT_E4M3 = 2            /* out is e4m3 with f32 scales (dflash_rms_norm only)    */
 };
 
 enum {
@@ -511,6 +512,74 @@ DFLASH_API int dflash_compact_pages(int32_t* block_table, int64_t block_table_st
                                     void* const* pools, int num_pools, int64_t page_bytes, int num_reqs,
                                     int max_pages_per_req, int64_t num_pages, int32_t* used, void* workspace,
                                     size_t workspace_bytes, int32_t* status, dflash_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * A layer's step of sequences that share a prompt: beams, samples of one prompt, a prompt with
+ * pictures. One such step is
+ *   dflash_shared_prefixes (once for all layers) -> per layer: dflash_rms_norm -> (projections) ->
+ *   dflash_rotary_axes (k and v to the slots) -> dflash_decode_attention_shared -> (projections)
+ * with every length, table and extent on the device: one captured graph replays it.
+ * ---------------------------------------------------------------------------------------
+ */
+
+/*
+ * dflash_rms_norm -- RMS norm with the residual's addition before it and an output in 8 bits.
+ *
+ *     h = x + residual (rounded to the type; h = x without a residual),  residual_out = h
+ *     y_c = h_c weight_c / sqrt(mean_c h_c^2 + eps)
+ *   and out = y, or with DFLASH_OUT_E4M3 out_c = e4m3(y_c / s), s = max |y| / 448 (at least 2^-126) over the
+ *   row, or over every group_size columns of it; y ~ out * s.
+ *
+ *   x, residual  [n, d] of `dtype` (DFLASH_OUT_BF16 or DFLASH_OUT_F32), rows *_stride elements apart
+ *                (0 repeats one row); residual may be NULL, then residual_out is too
+ *   weight       [d], of weight_dtype (bf16 or f32)
+ *   residual_out [n, d] of `dtype`; may be x or residual itself (same stride)
+ *   out          [n, d] of `dtype` or e4m3 (out_dtype); may be x or residual itself where it has their type.
+ *                Every other overlap of an output with a tensor of the call is refused.
+ *   scales       f32 [n, ceil(d / group_size)], or [n] with group_size 0; e4m3 only
+ *   group_size   0 or a multiple of 16; the last group may be short
+ *   d <= 65536. Sums in f32 (rows of values above 1e19 overflow them), one rounding to the output's type. A
+ *   scale is infinite or NaN where a y of its group is. One launch.
+ */
+DFLASH_API int dflash_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                               const void* weight, void* residual_out, int64_t residual_out_stride, void* out,
+                               int64_t out_stride, float* scales, int64_t n, int d, int dtype, int weight_dtype,
+                               int out_dtype, int group_size, float eps, dflash_stream_t stream);
+
+/*
+ * dflash_rotary_axes -- dflash_rotary with a position on each of several axes (time, height, width):
+ * pair i of token t turns by positions[pair_axis[i], t] * inv_freq[i].
+ *   positions  int32 [num_axes, n], axis_stride elements (at least n) between axes; num_axes in 1..4
+ *   pair_axis  HOST uint8 [rotary_dim / 2], each below num_axes: read during the call
+ * Everything else as dflash_rotary, the inverse (the gradient) included.
+ */
+DFLASH_API int dflash_rotary_axes(const void* q, int64_t q_tok, int64_t q_head, void* q_out, int64_t q_out_tok,
+                                  int64_t q_out_head, int hq, const void* k, int64_t k_tok, int64_t k_head,
+                                  void* k_out, int64_t k_out_tok, int64_t k_out_head, int hkv, const void* v,
+                                  int64_t v_tok, int64_t v_head, void* v_out, int64_t v_out_tok, int64_t v_out_head,
+                                  const int32_t* positions, int64_t axis_stride, int num_axes,
+                                  const uint8_t* pair_axis, const int32_t* slot, int64_t n, int64_t capacity, int dh,
+                                  int rotary_dim, const double* inv_freq, double amplitude, int interleaved,
+                                  int inverse, int dtype, int32_t* status, dflash_stream_t stream);
+
+/*
+ * dflash_shared_prefixes -- how many leading rows the sequences of a group hold in the same pages.
+ *
+ *   prefix_lens[g] = min(min_r seq_lens[r], page_size * c), over the rows r of group g with a length above 0; c =
+ *   the number of leading table entries that are >= 0 and the same in all of them. 0 for a group without any.
+ *
+ *   block_table, seq_lens  as dflash_decode_attention_paged
+ *   group_start_loc int32 [num_groups + 1] device: group g is the rows group_start_loc[g] .. [g + 1]
+ *   prefix_lens     int32 [num_groups] device; may not overlap the inputs
+ *   status          int32 device word or NULL: bounds outside 0 <= start <= end <= num_reqs (such a group's
+ *                   prefix is 0) and lengths that are negative or past the table (left out) are reported
+ *   One launch.
+ */
+DFLASH_API int dflash_shared_prefixes(const int32_t* block_table, int64_t block_table_stride, const int32_t* seq_lens,
+                                      const int32_t* group_start_loc, int num_reqs, int num_groups,
+                                      int max_pages_per_req, int page_size, int32_t* prefix_lens, int32_t* status,
+                                      dflash_stream_t stream);
 
 /*
  * Reads the device error word the last dflash_block_attention call on this workspace

@@ -16,6 +16,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
 #include <initializer_list>
 #include <string>
 #include <vector>
@@ -166,8 +167,33 @@ PyObject* given(PyObject* o, const at::Tensor& made) {
   return made.defined() ? wrap(made) : Py_NewRef(Py_None);
 }
 
+struct Buffer : Py_buffer {
+  explicit Buffer(PyObject* o, int flags = PyBUF_C_CONTIGUOUS) {
+    if (PyObject_GetBuffer(o, this, flags) != 0) throw Raised{};
+  }
+  ~Buffer() { PyBuffer_Release(this); }
+};
+
+// A small table of whole numbers in 0 .. 255 from a buffer of any integer type.
+std::vector<uint8_t> small_table(PyObject* o, const char* name) {
+  const Buffer b(o, PyBUF_C_CONTIGUOUS | PyBUF_FORMAT);
+  const std::string type = b.format ? b.format : "B";
+  if (type.size() != 1 || !std::strchr("bBhHiIlLqQ", type[0])) raise(PyExc_TypeError, "%s must hold integers", name);
+  const bool sign = std::strchr("bhilq", type[0]) != nullptr;
+  std::vector<uint8_t> out(static_cast<size_t>(b.len / b.itemsize));
+  for (size_t i = 0; i < out.size(); ++i) {
+    uint64_t x = 0;  // little-endian
+    std::memcpy(&x, static_cast<const char*>(b.buf) + i * b.itemsize, static_cast<size_t>(b.itemsize));
+    if (x > 255 || (sign && b.itemsize == 1 && x > 127)) raise(PyExc_ValueError, "%s: entry %d is out of range", name, static_cast<int>(i));
+    out[i] = static_cast<uint8_t>(x);
+  }
+  return out;
+}
+
 // q, positions, inv_freq (buffer of doubles), k, v, q_out, k_out, v_out, slot, amplitude, interleaved, inverse, status
-PyObject* rotary(PyObject* const* a) {
+// and with several axes: the axis of every pair (buffer of integers)
+template <bool AXES>
+PyObject* rotary_any(PyObject* const* a) {
   struct Part {
     const void* src = nullptr;
     void* dst = nullptr;
@@ -224,34 +250,146 @@ PyObject* rotary(PyObject* const* a) {
       v = Part{at.plain("v", x, type, false), at.plain("v_out", vo, type, false), x.stride(0), x.stride(1), vo.stride(0), vo.stride(1), 0};
     }
   }
-  const auto* pos = static_cast<const int32_t*>(at.address("positions", a[1], at::kInt, {n}));
+  const int32_t* pos;
+  int64_t axis_stride = 0;
+  int axes = 0;
+  std::vector<uint8_t> pair_axis;
+  if constexpr (AXES) {
+    const at::Tensor& p = tensor(a[1], "positions");
+    if (p.dim() != 2 || p.size(1) != n) raise(PyExc_ValueError, "positions must be [axes, n], got %s", text(p.sizes()).c_str());
+    pos = static_cast<const int32_t*>(at.plain("positions", p, at::kInt, false));
+    if (n > 1 && p.stride(1) != 1) raise(PyExc_ValueError, "positions: those of an axis must be contiguous");
+    axes = dim32(p.size(0), "axes"), axis_stride = axes > 1 ? p.stride(0) : n;
+    pair_axis = small_table(a[13], "axes");
+  } else {
+    pos = static_cast<const int32_t*>(at.address("positions", a[1], at::kInt, {n}));
+  }
   const auto* slot_p = static_cast<const int32_t*>(at.address("slot", slot, at::kInt, {n}));
   auto* status = static_cast<int32_t*>(at.address("status", a[12], at::kInt, {1}));
   const double amplitude = number(a[9]);
   const int inter = truth(a[10]), inverse = truth(a[11]);
   const int hq = dim32(q.heads, "Hq"), hkv = dim32(k.heads, "Hkv"), d = dim32(dh, "Dh");
-  struct Buffer : Py_buffer {
-    explicit Buffer(PyObject* o) {
-      if (PyObject_GetBuffer(o, this, PyBUF_C_CONTIGUOUS) != 0) throw Raised{};
-    }
-    ~Buffer() { PyBuffer_Release(this); }
-  } freq(a[2]);
+  const Buffer freq(a[2]);
+  const int rotary_dim = static_cast<int>(2 * (freq.len / static_cast<Py_ssize_t>(sizeof(double))));
+  if (AXES && pair_axis.size() * 2 != static_cast<size_t>(rotary_dim))
+    raise(PyExc_ValueError, "axes has %d entries, inv_freq %d", static_cast<int>(pair_axis.size()), rotary_dim / 2);
   if (c10::GradMode::is_enabled())
     for (int i : {0, 3, 4, 5, 6, 7})
       if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad())
         raise(PyExc_ValueError, "rotary records no gradient: call it under torch.no_grad() or with detached tensors "
                                 "(inverse=True gives the gradient of the inputs)");
   const int rc = run(at, [&](cudaStream_t stream) {
+    const auto* f = static_cast<const double*>(freq.buf);
+    const int dtype = type == at::kFloat ? DFLASH_OUT_F32 : DFLASH_OUT_BF16;
+    if constexpr (AXES)
+      return dflash_rotary_axes(q.src, q.tok, q.head, q.dst, q.out_tok, q.out_head, hq, k.src, k.tok, k.head, k.dst, k.out_tok, k.out_head,
+                                hkv, v.src, v.tok, v.head, v.dst, v.out_tok, v.out_head, pos, axis_stride, axes, pair_axis.data(), slot_p, n,
+                                capacity, d, rotary_dim, f, amplitude, inter, inverse, dtype, status, stream);
     return dflash_rotary(q.src, q.tok, q.head, q.dst, q.out_tok, q.out_head, hq, k.src, k.tok, k.head, k.dst, k.out_tok, k.out_head, hkv,
-                         v.src, v.tok, v.head, v.dst, v.out_tok, v.out_head, pos, slot_p, n, capacity, d,
-                         static_cast<int>(2 * (freq.len / static_cast<Py_ssize_t>(sizeof(double)))), static_cast<const double*>(freq.buf),
-                         amplitude, inter, inverse, type == at::kFloat ? DFLASH_OUT_F32 : DFLASH_OUT_BF16, status, stream);
+                         v.src, v.tok, v.head, v.dst, v.out_tok, v.out_head, pos, slot_p, n, capacity, d, rotary_dim, f, amplitude, inter,
+                         inverse, dtype, status, stream);
   });
   if (rc) return PyLong_FromLong(rc);
   if (has_q) written({a[5]});
   if (has_k) written({a[6], a[7]});
   written({a[12]});
   return Py_BuildValue("(NN)", has_q ? given(a[5], new_q) : Py_NewRef(Py_None), has_k ? given(a[6], new_k) : Py_NewRef(Py_None));
+}
+
+PyObject* rotary(PyObject* const* a) { return rotary_any<false>(a); }
+PyObject* rotary_axes(PyObject* const* a) { return rotary_any<true>(a); }
+
+// x, weight, residual, out dtype (None: x's), group_size, eps, out, residual_out, scales
+PyObject* rms_norm(PyObject* const* a) {
+  const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "weight");
+  const Place at(x);
+  const c10::cuda::OptionalCUDAGuard guard(at.device);
+  rows(x, "x", 2);
+  const at::ScalarType type = x.scalar_type();
+  if (type != at::kBFloat16 && type != at::kFloat) raise(PyExc_TypeError, "rms_norm takes bfloat16 or float32, got %s", c10::toString(type));
+  if (w.scalar_type() != at::kBFloat16 && w.scalar_type() != at::kFloat)
+    raise(PyExc_TypeError, "weight must be bfloat16 or float32, got %s", c10::toString(w.scalar_type()));
+  const int64_t n = x.size(0), d = x.size(1);
+  const auto code = [](at::ScalarType t) { return t == at::kFloat ? DFLASH_OUT_F32 : DFLASH_OUT_BF16; };
+  const int dtype = code(type), out_dtype = a[3] == Py_None ? dtype : small(a[3], "out_dtype");
+  const bool eight = out_dtype == DFLASH_OUT_E4M3;
+  if (!eight && out_dtype != dtype) raise(PyExc_ValueError, "out_dtype must be OUT_E4M3 or the input's type");
+  const at::ScalarType out_type = eight ? at::kFloat8_e4m3fn : type;
+  const int group = small(a[4], "group_size"), width = dim32(d, "d");
+  const float eps = static_cast<float>(number(a[5]));
+  const void* pw = at.address("weight", a[1], w.scalar_type(), {d});
+  struct Matrix {
+    at::Tensor t;
+    void* p = nullptr;
+    int64_t stride = 0;
+  };
+  auto matrix = [&](const char* name, PyObject* o, at::ScalarType t) {  // [n, d] that was given
+    const at::Tensor& m = tensor(o, name);
+    rows(m, name, 2);
+    if (m.sizes() != x.sizes()) raise(PyExc_ValueError, "%s has shape %s, expected %s", name, text(m.sizes()).c_str(), text(x.sizes()).c_str());
+    void* p = at.plain(name, m, t, false);
+    return Matrix{m, p, m.stride(0)};
+  };
+  auto made = [&](const char* name, PyObject* o, at::ScalarType t) {
+    if (o != Py_None) return matrix(name, o, t);
+    at::Tensor m = at.empty(x.sizes(), t);
+    return Matrix{m, m.data_ptr(), d};
+  };
+  if (a[2] == Py_None && a[7] != Py_None) raise(PyExc_ValueError, "residual_out needs a residual");
+  if (!eight && a[8] != Py_None) raise(PyExc_ValueError, "scales need out_dtype=OUT_E4M3");
+  if (group < 0 || group % 16) raise(PyExc_ValueError, "group_size must be 0 or a multiple of 16");
+  if (group && !eight) raise(PyExc_ValueError, "group_size needs out_dtype=OUT_E4M3");
+  if (c10::GradMode::is_enabled())
+    for (int i : {0, 1, 2, 6, 7})
+      if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad())
+        raise(PyExc_ValueError, "rms_norm records no gradient: call it under torch.no_grad() or with detached tensors");
+  Matrix r, ro;
+  if (a[2] != Py_None) r = matrix("residual", a[2], type), ro = made("residual_out", a[7], type);
+  const Matrix out = made("out", a[6], out_type);
+  at::Tensor new_scales;
+  float* scales = nullptr;
+  if (eight) {
+    if (a[8] == Py_None) {
+      if (group) new_scales = at.empty({n, (d + group - 1) / group}, at::kFloat);
+      else new_scales = at.empty({n, 1}, at::kFloat);
+      scales = static_cast<float*>(new_scales.data_ptr());
+    } else {
+      scales = static_cast<float*>(at.address("scales", a[8], at::kFloat, {n, group ? (d + group - 1) / group : 1}));
+    }
+  }
+  const int rc = run(at, [&](cudaStream_t stream) {
+    return dflash_rms_norm(x.data_ptr(), x.stride(0), r.p, r.stride, pw, ro.p, ro.stride, out.p, out.stride, scales, n, width, dtype,
+                           code(w.scalar_type()), out_dtype, group, eps, stream);
+  });
+  if (rc) return PyLong_FromLong(rc);
+  written({a[6], a[7], a[8]});
+  return Py_BuildValue("(NNN)", given(a[6], out.t), given(a[7], ro.t), given(a[8], new_scales));
+}
+
+// block_table, seq_lens, group_start_loc, page_size, out, status
+PyObject* shared_prefixes(PyObject* const* a) {
+  const at::Tensor &table = tensor(a[0], "block_table"), &starts = tensor(a[2], "group_start_loc");
+  const Place at(table);
+  const c10::cuda::OptionalCUDAGuard guard(at.device);
+  if (table.dim() != 2 || starts.dim() != 1 || starts.size(0) < 1)
+    raise(PyExc_ValueError, "block_table must be [N, max_pages] and group_start_loc [groups + 1]");
+  const int n = dim32(table.size(0), "N"), width = dim32(table.size(1), "max_pages"), groups = dim32(starts.size(0) - 1, "groups");
+  if (n && width > 1 && table.stride(1) != 1) raise(PyExc_ValueError, "block_table: a row must be contiguous");
+  const auto* pt = static_cast<const int32_t*>(at.plain("block_table", table, at::kInt, false));
+  tensor(a[1], "seq_lens");
+  const auto* pl = static_cast<const int32_t*>(at.address("seq_lens", a[1], at::kInt, {n}));
+  const auto* ps = static_cast<const int32_t*>(at.plain("group_start_loc", starts, at::kInt));
+  const int page = small(a[3], "page_size");
+  auto* status = static_cast<int32_t*>(at.address("status", a[5], at::kInt, {1}));
+  at::Tensor made;
+  if (a[4] == Py_None) made = at.empty({groups}, at::kInt);
+  auto* out = static_cast<int32_t*>(made.defined() ? made.data_ptr() : at.address("out", a[4], at::kInt, {groups}));
+  const int rc = run(at, [&](cudaStream_t stream) {
+    return dflash_shared_prefixes(pt, n > 1 ? table.stride(0) : width, pl, ps, n, groups, width, page, out, status, stream);
+  });
+  if (rc) return PyLong_FromLong(rc);
+  written({a[4], a[5]});
+  return given(a[4], made);
 }
 
 // q, k_pool, v_pool, block_table, seq_lens, max_ctx_len, out, lse, return_lse, workspace, scale, window, out_dtype, status
@@ -479,7 +617,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 #define ENTRY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(rotary, 13),       ENTRY(decode_attention_paged, 14), ENTRY(beam_select, 10), ENTRY(fork_pages, 5),
-                         ENTRY(reserve_pages, 12), ENTRY(compact_pages, 6),           {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(reserve_pages, 12), ENTRY(compact_pages, 6),           ENTRY(rotary_axes, 14), ENTRY(rms_norm, 9),
+                         ENTRY(shared_prefixes, 6), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_decode_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -21,6 +21,9 @@
 // allows, so odd sizes run the same code with narrower accesses. Elements that are only copied (behind rd, and v) go in
 // chunks of their own, of widths chosen in the same way.
 //
+// Several axes (time, height, width): t = p_axis(i) f_i, the axis of every pair in a table beside its frequency. A thread
+// loads its token's positions of all axes at once and picks one for each of its pairs.
+//
 // Measured: 32768 rows of 40 heads of 128 (671 MB) 104.2 us, 95% of the copy rate; 2001 rows of 20 heads, 20 of 80 elements, in f32
 // 5.3 us (floor 3.8); 32 rows into pages 3.2 us, a launch. Blocks of their own for what is copied:
 // threads of both kinds in a warp took 67 us instead of 42 for 26170 rows of 7 heads of 256 into pages, 27 instead of 14
@@ -30,6 +33,7 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <type_traits>
 
 #include "../../include/dflash.h"
 #include "decode_host.h"
@@ -68,6 +72,13 @@ struct RotaryArgs {
   uint32_t* err;
   float2 freq[kMaxPairs];  // turns per position, head and tail
 };
+// ... with a position on each of several axes
+struct RotaryAxesArgs : RotaryArgs {
+  int64_t pos_step;  // between a token's positions
+  int axes;
+  uint8_t axis[kMaxPairs];
+};
+constexpr int kMaxAxes = 4;
 
 // Copies a chunk of heads h, h + step, .. below end of one tensor, kUnroll loads in flight.
 template <typename W>
@@ -154,14 +165,19 @@ __device__ __forceinline__ Chunk<T, E> pack_chunk(const float (&x)[E]) {
   return c;
 }
 
-template <typename T, bool INTER, int E>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+template <typename T, bool INTER, int E, typename Args>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Args a) {
+  constexpr bool kAxes = std::is_same_v<Args, RotaryAxesArgs>;
   const bool rotates = blockIdx.x < a.rot_blocks, copies_v = blockIdx.x >= a.rot_blocks + a.tail_blocks;
   // The table in shared memory: lanes of different pairs read the parameters' bank one after the other (6426 rows of
   // 5 heads of 256: 24 us, 12 so; 32 rows of 40 heads of 128 3.0, 3.2).
   __shared__ float2 s_freq[kMaxPairs];
+  __shared__ uint8_t s_axis[kAxes ? kMaxPairs : 1];
   if (rotates) {
-    for (int i = threadIdx.x; i < a.rd / 2; i += kThreads) s_freq[i] = a.freq[i];
+    for (int i = threadIdx.x; i < a.rd / 2; i += kThreads) {
+      s_freq[i] = a.freq[i];
+      if constexpr (kAxes) s_axis[i] = a.axis[i];
+    }
     __syncthreads();
   }
   const unsigned first = rotates ? 0 : copies_v ? a.rot_blocks + a.tail_blocks : a.rot_blocks;
@@ -196,12 +212,21 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 
   float cs[E], sn[E];
   {
-    const int p = a.pos[t];
+    int p = a.pos[t];
+    int at[kAxes ? kMaxAxes : 1];
+    if constexpr (kAxes) {
+#pragma unroll
+      for (int x = 0; x < kMaxAxes; ++x) at[x] = x == 0 ? p : x < a.axes ? a.pos[x * a.pos_step + t] : 0;
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       // half layout and single pairs: pair u E + e; interleaved chunks: E/2 pairs of each chunk
       const int pair = (!INTER || E == 1) ? u * E + e : (e < E / 2 ? e0 / 2 + e : e1 / 2 + e - E / 2);
       const float2 f = s_freq[pair];
+      if constexpr (kAxes) {
+        const int x = s_axis[pair];
+        p = x < 2 ? (x == 0 ? at[0] : at[1]) : (x == 2 ? at[2] : at[3]);
+      }
       sincospif(2.0f * rope_turns(p, f.x, f.y), &sn[e], &cs[e]);
       cs[e] *= a.amp;
       sn[e] *= a.amp * a.sin_sign;
@@ -264,14 +289,14 @@ bool apart(int64_t rows, int64_t row_stride, int heads, int64_t head_stride, int
 
 int64_t blocks_of(const RotaryArgs& a, int units) { return (a.n * units * a.groups + kThreads - 1) / kThreads; }
 
-template <typename T, bool INTER, int E>
-void launch(const RotaryArgs& a, cudaStream_t st) {
+template <typename T, bool INTER, int E, typename Args>
+void launch(const Args& a, cudaStream_t st) {
   const unsigned v_blocks = static_cast<unsigned>(blocks_of(a, a.v_units));
-  rotary_kernel<T, INTER, E><<<a.rot_blocks + a.tail_blocks + v_blocks, kThreads, 0, st>>>(a);
+  rotary_kernel<T, INTER, E, Args><<<a.rot_blocks + a.tail_blocks + v_blocks, kThreads, 0, st>>>(a);
 }
 
-template <typename T, bool INTER>
-void launch_width(int e, const RotaryArgs& a, cudaStream_t st) {
+template <typename T, bool INTER, typename Args>
+void launch_width(int e, const Args& a, cudaStream_t st) {
   if constexpr (sizeof(T) == 2) {
     if (e == 8) return launch<T, INTER, 8>(a, st);
   }
@@ -280,17 +305,21 @@ void launch_width(int e, const RotaryArgs& a, cudaStream_t st) {
   launch<T, INTER, 1>(a, st);
 }
 
-}  // namespace
-}  // namespace dflash
+template <typename Args>
+void launch_type(bool f32, bool inter, int e, const Args& a, cudaStream_t st) {
+  if (f32)
+    inter ? launch_width<float, true>(e, a, st) : launch_width<float, false>(e, a, st);
+  else
+    inter ? launch_width<uint16_t, true>(e, a, st) : launch_width<uint16_t, false>(e, a, st);
+}
 
-extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void* q_out, int64_t q_out_tok,
-                             int64_t q_out_head, int hq, const void* k, int64_t k_tok, int64_t k_head, void* k_out,
-                             int64_t k_out_tok, int64_t k_out_head, int hkv, const void* v, int64_t v_tok,
-                             int64_t v_head, void* v_out, int64_t v_out_tok, int64_t v_out_head,
-                             const int32_t* positions, const int32_t* slot, int64_t n, int64_t capacity, int dh,
-                             int rotary_dim, const double* inv_freq, double amplitude, int interleaved, int inverse,
-                             int dtype, int32_t* status, dflash_stream_t stream) {
-  using namespace dflash;
+// A call; axes = 0: one position a token.
+int rotary_call(const void* q, int64_t q_tok, int64_t q_head, void* q_out, int64_t q_out_tok, int64_t q_out_head, int hq, const void* k,
+                int64_t k_tok, int64_t k_head, void* k_out, int64_t k_out_tok, int64_t k_out_head, int hkv, const void* v, int64_t v_tok,
+                int64_t v_head, void* v_out, int64_t v_out_tok, int64_t v_out_head, const int32_t* positions, int64_t pos_step, int axes,
+                const uint8_t* pair_axis, const int32_t* slot, int64_t n, int64_t capacity, int dh, int rotary_dim,
+                const double* inv_freq, double amplitude, int interleaved, int inverse, int dtype, int32_t* status,
+                dflash_stream_t stream) {
   if (dtype != DFLASH_OUT_BF16 && dtype != DFLASH_OUT_F32)
     return errorf(DFLASH_ERR_INVALID_ARG, "dtype %d is neither DFLASH_OUT_BF16 nor DFLASH_OUT_F32", dtype);
   if (hq < 0 || hkv < 0 || hq + static_cast<int64_t>(hkv) == 0)
@@ -309,6 +338,13 @@ extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void*
     if (std::fabs(inv_freq[i]) > 1.0) return errorf(DFLASH_ERR_UNSUPPORTED, "frequency %d exceeds 1", i);
   if (!std::isfinite(amplitude)) return errorf(DFLASH_ERR_INVALID_ARG, "amplitude is not finite");
   if ((interleaved & ~1) || (inverse & ~1)) return errorf(DFLASH_ERR_INVALID_ARG, "interleaved and inverse are 0 or 1");
+  if (axes) {
+    if (axes < 0 || axes > kMaxAxes) return errorf(axes < 0 ? DFLASH_ERR_INVALID_ARG : DFLASH_ERR_UNSUPPORTED, "%d axes: 1 to %d are implemented", axes, kMaxAxes);
+    if (!pair_axis) return errorf(DFLASH_ERR_INVALID_ARG, "null table of axes");
+    for (int i = 0; i < rotary_dim / 2; ++i)
+      if (pair_axis[i] >= axes) return errorf(DFLASH_ERR_INVALID_ARG, "pair %d has axis %d of %d", i, pair_axis[i], axes);
+    if (axes > 1 && pos_step < n) return errorf(DFLASH_ERR_INVALID_ARG, "the axes' positions overlap");
+  }
   if (n == 0) return report_error(DFLASH_OK, "");
   if (!positions || (hq && (!q || !q_out)) || (hkv && (!k || !k_out)) || (v && !v_out))
     return errorf(DFLASH_ERR_INVALID_ARG, "null pointer argument");
@@ -329,7 +365,7 @@ extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void*
       (v && !apart(stored, v_out_tok, hkv, v_out_head, dh)))
     return errorf(DFLASH_ERR_INVALID_ARG, "rows or heads of an output overlap");
   const size_t es = dtype == DFLASH_OUT_F32 ? 4 : 2;
-  RotaryArgs a{};
+  RotaryAxesArgs a{};
   a.t[0] = RotaryTensor{q, q_out, q_tok, q_head, q_out_tok, q_out_head};
   a.t[1] = RotaryTensor{k, k_out, k_tok, k_head, k_out_tok, k_out_head};
   a.t[2] = RotaryTensor{v, v_out, v_tok, v_head, v_out_tok, v_out_head};
@@ -386,11 +422,44 @@ extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void*
   if (rot_blocks + tail_blocks + blocks_of(a, a.v_units) > 0x7fffffff)
     return errorf(DFLASH_ERR_UNSUPPORTED, "too many rows for one call (%lld)", static_cast<long long>(n));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (es == 4)
-    interleaved ? launch_width<float, true>(e, a, st) : launch_width<float, false>(e, a, st);
-  else
-    interleaved ? launch_width<uint16_t, true>(e, a, st) : launch_width<uint16_t, false>(e, a, st);
+  if (axes) {
+    a.pos_step = pos_step, a.axes = axes;
+    std::copy(pair_axis, pair_axis + rotary_dim / 2, a.axis);
+    launch_type(es == 4, interleaved != 0, e, a, st);
+  } else {
+    launch_type(es == 4, interleaved != 0, e, static_cast<const RotaryArgs&>(a), st);
+  }
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "rotary launch: %s", cudaGetErrorString(err));
   return report_error(DFLASH_OK, "");
+}
+
+}  // namespace
+}  // namespace dflash
+
+extern "C" int dflash_rotary(const void* q, int64_t q_tok, int64_t q_head, void* q_out, int64_t q_out_tok,
+                             int64_t q_out_head, int hq, const void* k, int64_t k_tok, int64_t k_head, void* k_out,
+                             int64_t k_out_tok, int64_t k_out_head, int hkv, const void* v, int64_t v_tok,
+                             int64_t v_head, void* v_out, int64_t v_out_tok, int64_t v_out_head,
+                             const int32_t* positions, const int32_t* slot, int64_t n, int64_t capacity, int dh,
+                             int rotary_dim, const double* inv_freq, double amplitude, int interleaved, int inverse,
+                             int dtype, int32_t* status, dflash_stream_t stream) {
+  return dflash::rotary_call(q, q_tok, q_head, q_out, q_out_tok, q_out_head, hq, k, k_tok, k_head, k_out, k_out_tok, k_out_head, hkv, v, v_tok,
+                             v_head, v_out, v_out_tok, v_out_head, positions, 0, 0, nullptr, slot, n, capacity, dh, rotary_dim, inv_freq,
+                             amplitude, interleaved, inverse, dtype, status, stream);
+}
+
+extern "C" int dflash_rotary_axes(const void* q, int64_t q_tok, int64_t q_head, void* q_out, int64_t q_out_tok,
+                                  int64_t q_out_head, int hq, const void* k, int64_t k_tok, int64_t k_head, void* k_out,
+                                  int64_t k_out_tok, int64_t k_out_head, int hkv, const void* v, int64_t v_tok,
+                                  int64_t v_head, void* v_out, int64_t v_out_tok, int64_t v_out_head,
+                                  const int32_t* positions, int64_t axis_stride, int num_axes, const uint8_t* pair_axis,
+                                  const int32_t* slot, int64_t n, int64_t capacity, int dh, int rotary_dim,
+                                  const double* inv_freq, double amplitude, int interleaved, int inverse, int dtype,
+                                  int32_t* status, dflash_stream_t stream) {
+  using namespace dflash;
+  if (num_axes <= 0) return errorf(DFLASH_ERR_INVALID_ARG, "at least one axis is needed");
+  return rotary_call(q, q_tok, q_head, q_out, q_out_tok, q_out_head, hq, k, k_tok, k_head, k_out, k_out_tok, k_out_head, hkv, v, v_tok,
+                     v_head, v_out, v_out_tok, v_out_head, positions, axis_stride, num_axes, pair_axis, slot, n, capacity, dh, rotary_dim,
+                     inv_freq, amplitude, interleaved, inverse, dtype, status, stream);
 }

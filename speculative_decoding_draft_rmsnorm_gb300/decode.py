@@ -6,11 +6,15 @@
     fork_pages(...)             -> dflash_fork_pages
     reserve_pages(...)          -> dflash_reserve_pages
     compact_pages(...)          -> dflash_compact_pages
+and a step of sequences that share a prompt:
+    rms_norm(...)                -> dflash_rms_norm
+    rotary_axes(...)             -> dflash_rotary_axes
+    shared_prefixes(...)         -> dflash_shared_prefixes
 
 Like the rest of the package these only marshal arguments (csrc/bind.cpp checks them and makes the call).
 All tensors of a call live on one device; the call runs there, on `stream` (default: that device's current
 stream). Outputs and workspaces that a call allocates belong to that stream. No call records a gradient; rotary,
-whose inverse is one, refuses tensors that require it while gradients are recorded. Tensors that a call writes count
+whose inverse is one, and rms_norm refuse tensors that require it while gradients are recorded. Tensors that a call writes count
 as changed in place.
 """
 from __future__ import annotations
@@ -20,7 +24,7 @@ import math
 
 import numpy as np
 
-OUT_BF16, OUT_F32 = 0, 1
+OUT_BF16, OUT_F32, OUT_E4M3 = 0, 1, 2
 
 
 def declare(lib) -> None:
@@ -30,6 +34,10 @@ def declare(lib) -> None:
     sig = {
         "dflash_rotary": (I32, [P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, P,
                                 P, I64, I64, I32, I32, P, F64, I32, I32, I32, P, P]),
+        "dflash_rotary_axes": (I32, [P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, P,
+                                     I64, I32, P, P, I64, I64, I32, I32, P, F64, I32, I32, I32, P, P]),
+        "dflash_rms_norm": (I32, [P, I64, P, I64, P, P, I64, P, I64, P, I64, I32, I32, I32, I32, I32, F32, P]),
+        "dflash_shared_prefixes": (I32, [P, I64, P, P, I32, I32, I32, I32, P, P, P]),
         "dflash_decode_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32]),
         "dflash_decode_attention_paged": (I32, [P, I64, P, P, P, I64, P, I32, I32, I32, I32, I64, I32, I32, I32, F32, I32,
                                                 I32, P, P, P, SZ, P, P]),
@@ -155,6 +163,67 @@ def rotary(q, positions, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_
     return out
 
 
+def rotary_sections(sections, *, interleaved=False):
+    """The axis of every pair (uint8 numpy) for `rotary_axes`, from the number of pairs that each axis has.
+
+    sections (16, 24, 24): pairs 0-15 follow axis 0, 16-39 axis 1, 40-63 axis 2. interleaved=True deals the
+    axes out in turn, 0, 1, 2, 0, 1, 2, .., until each has its number.
+    """
+    left = [int(n) for n in sections]
+    if not left or min(left) < 0 or len(left) > 255:
+        raise ValueError("sections must be the axes' numbers of pairs")
+    if not interleaved:
+        return np.repeat(np.arange(len(left), dtype=np.uint8), left)
+    turn = np.concatenate([np.arange(n) for n in left])  # of an axis: its 1st, 2nd, .. pair
+    axis = np.repeat(np.arange(len(left), dtype=np.uint8), left)
+    return axis[np.lexsort((axis, turn))]
+
+
+def rotary_axes(q, positions, axes, inv_freq, *, k=None, v=None, q_out=None, k_out=None, v_out=None, slot=None, amplitude=1.0,
+                interleaved=False, inverse=False, status=None, stream=None):
+    """`rotary` with a position on each of several axes (time, height, width); returns (q_out, k_out).
+
+    positions [A, n] int32, A <= 4 (an axis's positions contiguous); axes: the axis of every pair, host integers
+    [rotary_dim / 2] (see rotary_sections). Pair i of token t turns by positions[axes[i], t] * inv_freq[i].
+    Everything else as in rotary; inverse=True is the gradient here too.
+    """
+    bind = _bind or _load()
+    if stream is not None:
+        with _on(stream, k if q is None else q):
+            return rotary_axes(q, positions, axes, inv_freq, k=k, v=v, q_out=q_out, k_out=k_out, v_out=v_out, slot=slot,
+                               amplitude=amplitude, interleaved=interleaved, inverse=inverse, status=status)
+    if type(inv_freq) is not np.ndarray or inv_freq.dtype != np.float64 or not inv_freq.flags.c_contiguous:
+        inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if type(axes) is not np.ndarray or not axes.flags.c_contiguous:
+        axes = np.ascontiguousarray(axes)
+    out = bind.rotary_axes(q, positions, inv_freq, k, v, q_out, k_out, v_out, slot, amplitude, interleaved, inverse, status, axes)
+    if type(out) is int:
+        _fail(out)
+    return out
+
+
+# ------------------------------------------------------------------------------------- norm
+def rms_norm(x, weight, *, residual=None, out_dtype=None, group_size=0, eps=1e-6, out=None, residual_out=None, scales=None,
+             stream=None):
+    """RMS norm of x [n, d] (bf16 or f32), or of x + residual; returns (out, residual_out, scales).
+
+    h = x + residual, rounded to their type, is residual_out (None without a residual) and what is normed:
+    y = h * weight / sqrt(mean(h^2) + eps). weight [d]: bf16 or f32. out: y in x's type, or with
+    out_dtype=OUT_E4M3 y / scale in 8 bits (torch.float8_e4m3fn) with scales f32 [n, 1], max |y| / 448 of every row,
+    or [n, ceil(d / group_size)], of every group_size columns (a multiple of 16); scales is None otherwise.
+    Rows may be strided; residual_out=residual, or =x, works in place, and so does out=x.
+    """
+    bind = _bind or _load()
+    if stream is not None:
+        with _on(stream, x):
+            return rms_norm(x, weight, residual=residual, out_dtype=out_dtype, group_size=group_size, eps=eps, out=out,
+                            residual_out=residual_out, scales=scales)
+    got = bind.rms_norm(x, weight, residual, out_dtype, group_size, eps, out, residual_out, scales)
+    if type(got) is int:
+        _fail(got)
+    return got
+
+
 # ------------------------------------------------------------------------------------- attention
 def decode_workspace_size(num_reqs, hq, hkv, dh, max_ctx_len, window=0) -> int:
     n = _base().load().dflash_decode_workspace_size(num_reqs, hq, hkv, dh, int(max_ctx_len), int(window))
@@ -180,6 +249,23 @@ def decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, *, max_ctx_
                                           out_dtype=out_dtype, status=status)
     got = bind.decode_attention_paged(q, k_pool, v_pool, block_table, seq_lens, int(max_ctx_len), out, lse, return_lse, workspace,
                                       scale, int(window), out_dtype, status)
+    if type(got) is int:
+        _fail(got)
+    return got
+
+
+def shared_prefixes(block_table, seq_lens, group_start_loc, *, page_size, out=None, status=None, stream=None):
+    """How many leading rows the sequences of every group hold in the same pages: int32 [groups].
+
+    Group g is the rows group_start_loc[g] .. group_start_loc[g + 1] (int32 [groups + 1] on the device) of block_table
+    [N, max_pages] and seq_lens [N]; sequences of length 0 are left out. What fork_pages shares, reserve_pages ends
+    at the page that a sequence writes: call this behind it, once a step for all layers.
+    """
+    bind = _bind or _load()
+    if stream is not None:
+        with _on(stream, block_table):
+            return shared_prefixes(block_table, seq_lens, group_start_loc, page_size=page_size, out=out, status=status)
+    got = bind.shared_prefixes(block_table, seq_lens, group_start_loc, page_size, out, status)
     if type(got) is int:
         _fail(got)
     return got
