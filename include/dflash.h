@@ -581,6 +581,38 @@ DFLASH_API int dflash_shared_prefixes(const int32_t* block_table, int64_t block_
                                       int max_pages_per_req, int page_size, int32_t* prefix_lens, int32_t* status,
                                       dflash_stream_t stream);
 
+/* Bytes of workspace of dflash_decode_attention_shared on the current device (0 and a message if the arguments are
+ * invalid). It needs no initialisation; concurrent calls must not share one. The size grows with num_reqs,
+ * num_groups and max_ctx_len. */
+DFLASH_API size_t dflash_shared_workspace_size(int num_reqs, int num_groups, int hq, int hkv, int dh, int max_ctx_len,
+                                               int window);
+
+/*
+ * dflash_decode_attention_shared -- dflash_decode_attention_paged where the rows that a group of sequences
+ * holds in the same pages are read, and multiplied with the queries of the whole group, once for all.
+ *
+ *   group_start_loc int32 [num_groups + 1] device: group g is the sequences group_start_loc[g] .. [g + 1];
+ *              sequences in no group read all their rows themselves. Not nondecreasing within
+ *              [0, num_reqs]: reported, and then no group shares anything.
+ *   prefix_lens int32 [num_groups] device: the first prefix_lens[g] rows of the group's sequences that are at
+ *              least that long lie in the same pages (dflash_shared_prefixes; any shorter prefix does too). They
+ *              are read in the pages of the first such sequence. Shorter sequences of the group read their own
+ *              rows. Negative or above max_ctx_len: reported and treated as 0.
+ *   Every other argument, and the result, as dflash_decode_attention_paged (the workspace as
+ *   dflash_shared_workspace_size says). The result does not depend on timing; another prefix gives another order of the
+ *   sums. What a row of the prefix holds that only some of the group's windows reach must be finite for the others
+ *   too: their weight 0 is multiplied with it. status also takes 1 where a bounded wait ran out (the output is
+ *   then not valid).
+ */
+DFLASH_API int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const dflash_bf16* k_pool,
+                                              const dflash_bf16* v_pool, const int32_t* block_table,
+                                              int64_t block_table_stride, const int32_t* seq_lens,
+                                              const int32_t* group_start_loc, const int32_t* prefix_lens, int num_reqs,
+                                              int num_groups, int hq, int hkv, int dh, int64_t num_pages, int page_size,
+                                              int max_pages_per_req, int max_ctx_len, float scale, int window,
+                                              int out_dtype, void* out, float* lse, void* workspace,
+                                              size_t workspace_bytes, int32_t* status, dflash_stream_t stream);
+
 /*
  * Reads the device error word the last dflash_block_attention call on this workspace
  * left (waits for `stream`). Returns DFLASH_OK, DFLASH_ERR_DEVICE_TIMEOUT or

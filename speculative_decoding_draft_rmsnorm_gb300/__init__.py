@@ -14,7 +14,7 @@ Entry points mirror include/dflash.h:
     check_error(workspace)   -> dflash_check_error
 and, from decode.py, a decode step over the paged store: rotary, decode_attention_paged, beam_select,
 fork_pages, reserve_pages, compact_pages; and a step of sequences that share a prompt: rms_norm, rotary_axes,
-shared_prefixes.
+shared_prefixes, decode_attention_shared.
 """
 from __future__ import annotations
 
@@ -24,8 +24,9 @@ import threading
 
 from . import decode as _decode
 from .decode import (OUT_E4M3, beam_select, beam_workspace_size, compact_pages, decode_attention_paged,  # noqa: F401
-                     decode_workspace_size, fork_pages, pages_workspace_size, reserve_pages, rms_norm, rotary,
-                     rotary_axes, rotary_frequencies, rotary_sections, shared_prefixes)
+                     decode_attention_shared, decode_workspace_size, fork_pages, pages_workspace_size, reserve_pages,
+                     rms_norm, rotary, rotary_axes, rotary_frequencies, rotary_sections, shared_prefixes,
+                     shared_workspace_size)
 
 __all__ = ["load", "lib_path", "context_kv", "paged_append", "prepare_inputs", "STATUS_METADATA", "block_attention", "block_attention_paged", "workspace_size", "plan",
            "alloc_workspace",
@@ -33,7 +34,8 @@ __all__ = ["load", "lib_path", "context_kv", "paged_append", "prepare_inputs", "
            "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_WORKSPACE", "ERR_CUDA", "ERR_DEVICE_TIMEOUT",
            "ERR_DEVICE_METADATA", "rotary", "rotary_frequencies", "decode_attention_paged", "decode_workspace_size",
            "beam_select", "beam_workspace_size", "fork_pages", "reserve_pages", "compact_pages",
-           "pages_workspace_size", "OUT_E4M3", "rms_norm", "rotary_axes", "rotary_sections", "shared_prefixes"]
+           "pages_workspace_size", "OUT_E4M3", "rms_norm", "rotary_axes", "rotary_sections", "shared_prefixes",
+           "decode_attention_shared", "shared_workspace_size"]
 
 OUT_BF16, OUT_F32 = 0, 1
 STATUS_METADATA = 2  # bit ORed into the status word of context_kv / paged_append / prepare_inputs

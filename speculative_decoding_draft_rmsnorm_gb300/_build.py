@@ -27,7 +27,8 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_NAME = "libdflash_gb300.so"
 LIB_PATH = os.path.join(LIB_DIR, LIB_NAME)
 SOURCES = ["api.cu", "attention.cu", "norm_rope.cu", "noalloc.cu", "draft_step.cu", "rotary.cu",
-           "decode_attention.cu", "beam.cu", "pages.cu", "rms_norm.cu", "shared_prefixes.cu"]
+           "decode_attention.cu", "beam.cu", "pages.cu", "rms_norm.cu", "shared_prefixes.cu",
+           "shared_attention.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "norm_rope.cuh", "decode_host.h"]
 # The marshalling module of decode.py: host C++ against torch and the product library.
 BIND_SOURCE = os.path.join(CSRC, "bind.cpp")

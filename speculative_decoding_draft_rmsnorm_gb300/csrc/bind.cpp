@@ -393,7 +393,9 @@ PyObject* shared_prefixes(PyObject* const* a) {
 }
 
 // q, k_pool, v_pool, block_table, seq_lens, max_ctx_len, out, lse, return_lse, workspace, scale, window, out_dtype, status
-PyObject* decode_attention_paged(PyObject* const* a) {
+// and of a call that shares prefixes: group_start_loc, prefix_lens
+template <bool SHARED>
+PyObject* decode_attention(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q");
   const Place at(q);
   const c10::cuda::OptionalCUDAGuard guard(at.device);
@@ -416,24 +418,43 @@ PyObject* decode_attention_paged(PyObject* const* a) {
   auto* status = static_cast<int32_t*>(at.address("status", a[13], at::kInt, {1}));
   const int longest = small(a[5], "max_ctx_len"), window = small(a[11], "window");
   const float scale = static_cast<float>(number(a[10]));
+  const int32_t *starts = nullptr, *prefixes = nullptr;
+  int groups = 0;
+  if constexpr (SHARED) {
+    const at::Tensor& t = tensor(a[14], "group_start_loc");
+    if (t.dim() != 1 || t.size(0) < 1) raise(PyExc_ValueError, "group_start_loc must be [groups + 1]");
+    groups = dim32(t.size(0) - 1, "groups");
+    starts = static_cast<const int32_t*>(at.plain("group_start_loc", t, at::kInt));
+    tensor(a[15], "prefix_lens");
+    prefixes = static_cast<const int32_t*>(at.address("prefix_lens", a[15], at::kInt, {groups}));
+  }
   at::Tensor new_out, new_lse;
   if (a[6] == Py_None) new_out = at.empty(q.sizes(), type);
   if (a[7] == Py_None && truth(a[8])) new_lse = at.empty({n, hq}, at::kFloat);
   void* out = a[6] == Py_None ? new_out.data_ptr() : at.address("out", a[6], type, q.sizes());
   auto* lse = static_cast<float*>(new_lse.defined() ? new_lse.data_ptr() : at.address("lse", a[7], at::kFloat, {n, hq}));
   Scratch ws;
-  if (!scratch(at, a[9], [&] { return dflash_decode_workspace_size(n, hq, hkv, dh, longest, window); }, &ws))
+  const auto need = [&] {
+    return SHARED ? dflash_shared_workspace_size(n, groups, hq, hkv, dh, longest, window)
+                  : dflash_decode_workspace_size(n, hq, hkv, dh, longest, window);
+  };
+  if (!scratch(at, a[9], need, &ws))
     return PyLong_FromLong(DFLASH_ERR_INVALID_ARG);
   const int rc = run(at, [&](cudaStream_t stream) {
-    return dflash_decode_attention_paged(pq, n > 1 ? q.stride(0) : static_cast<int64_t>(hq) * dh, pk, pv, pt, n > 1 ? table.stride(0) : width,
-                                         pl, n, hq, hkv, dh, kp.size(0), page, width, longest, scale, window, dtype, out, lse, ws.p,
-                                         ws.bytes, status, stream);
+    const int64_t q_stride = n > 1 ? q.stride(0) : static_cast<int64_t>(hq) * dh, table_stride = n > 1 ? table.stride(0) : width;
+    if constexpr (SHARED)
+      return dflash_decode_attention_shared(pq, q_stride, pk, pv, pt, table_stride, pl, starts, prefixes, n, groups, hq, hkv, dh, kp.size(0), page,
+                                            width, longest, scale, window, dtype, out, lse, ws.p, ws.bytes, status, stream);
+    return dflash_decode_attention_paged(pq, q_stride, pk, pv, pt, table_stride, pl, n, hq, hkv, dh, kp.size(0), page, width, longest, scale,
+                                         window, dtype, out, lse, ws.p, ws.bytes, status, stream);
   });
   if (rc) return PyLong_FromLong(rc);
   written({a[6], a[7], a[9], a[13]});
   if (!lse && !(a[7] != Py_None || new_lse.defined())) return given(a[6], new_out);
   return Py_BuildValue("(NN)", given(a[6], new_out), given(a[7], new_lse));
 }
+PyObject* decode_attention_paged(PyObject* const* a) { return decode_attention<false>(a); }
+PyObject* decode_attention_shared(PyObject* const* a) { return decode_attention<true>(a); }
 
 // logits, scores, beams_out (None: as many as in), finished, eos, scores out, tokens out, parents out, finished out, workspace
 PyObject* beam_select(PyObject* const* a) {
@@ -618,7 +639,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define ENTRY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(rotary, 13),       ENTRY(decode_attention_paged, 14), ENTRY(beam_select, 10), ENTRY(fork_pages, 5),
                          ENTRY(reserve_pages, 12), ENTRY(compact_pages, 6),           ENTRY(rotary_axes, 14), ENTRY(rms_norm, 9),
-                         ENTRY(shared_prefixes, 6), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(shared_prefixes, 6), ENTRY(decode_attention_shared, 16), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_decode_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

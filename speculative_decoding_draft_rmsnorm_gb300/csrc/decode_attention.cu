@@ -103,6 +103,10 @@ struct DecodeArgs {
   float scale_log2;
   int out_f32;
   int max_workers;
+  // OWN: a sequence's rows begin at own[r] (or the window), and a head's unnormalised sums, maximum and weight go to
+  // out (f32) and own_ml, to be joined with what came before
+  const int32_t* own;
+  float* own_ml;  // [num_reqs][Hq][2]
 };
 
 __device__ __forceinline__ int page_of(const DecodeArgs& a, int j) {
@@ -113,11 +117,15 @@ __device__ __forceinline__ int page_of(const DecodeArgs& a, int j) {
 __device__ __forceinline__ int valid_len(const DecodeArgs& a, int len) {
   return len < 0 || len > a.max_len ? 0 : len;
 }
-__device__ __forceinline__ int first_row(const DecodeArgs& a, int len) {
-  return a.window > 0 && len > a.window ? len - a.window : 0;
+template <bool OWN>
+__device__ __forceinline__ int first_row(const DecodeArgs& a, int r, int len) {
+  const int first = a.window > 0 && len > a.window ? len - a.window : 0;
+  if constexpr (OWN) return len > 0 ? max(first, a.own[r]) : 0;
+  return first;
 }
-__device__ __forceinline__ int steps_of(const DecodeArgs& a, int len) {
-  return (len - first_row(a, len) + kStep - 1) / kStep;
+template <bool OWN>
+__device__ __forceinline__ int steps_of(const DecodeArgs& a, int r, int len) {
+  return (len - first_row<OWN>(a, r, len) + kStep - 1) / kStep;
 }
 
 // The workers' ranges: equal to within one step. A call has fewer than 2^32 steps.
@@ -175,21 +183,23 @@ struct Cursor {
   int r, hh, len, first, steps, step;
 };
 
+template <bool OWN>
 __device__ __forceinline__ void set_len(const DecodeArgs& a, Cursor& c, int len) {
   c.len = len;
-  c.first = first_row(a, len);
+  c.first = first_row<OWN>(a, c.r, len);
   c.steps = (len - c.first + kStep - 1) / kStep;
 }
 
 // The next group with steps after c's; c.steps = 0 at the end of the batch (which a worker's range never
 // passes).
+template <bool OWN>
 __device__ __forceinline__ void next_group(const DecodeArgs& a, Cursor& c, int heads) {
   c.step = 0;
   if (++c.hh < heads) return;
   c.hh = 0;
   c.steps = 0;
 #pragma unroll 1
-  while (c.steps == 0 && ++c.r < a.num_reqs) set_len(a, c, valid_len(a, a.lens[c.r]));
+  while (c.steps == 0 && ++c.r < a.num_reqs) set_len<OWN>(a, c, valid_len(a, a.lens[c.r]));
 }
 
 // What a warp left to be joined: at its range's end in shared memory, or (mid) a group's end that it
@@ -271,9 +281,14 @@ __device__ __forceinline__ void store_row(float* dst, const float (&o)[DH / 32],
 }
 
 // A finished head: its output row and log-sum.
-template <int DH>
+template <int DH, bool OWN>
 __device__ __forceinline__ void store_head(const DecodeArgs& a, int64_t o_row, const float (&o)[DH / 32], float m, float l) {
   const int lane = threadIdx.x & 31;
+  if constexpr (OWN) {
+    store_row<DH>(static_cast<float*>(a.out) + o_row * DH, o, 1.0f);
+    if (lane == 0) a.own_ml[o_row * 2] = m, a.own_ml[o_row * 2 + 1] = l;
+    return;
+  }
   const float inv = 1.0f / l;
   if (a.out_f32) {
     store_row<DH>(static_cast<float*>(a.out) + o_row * DH, o, inv);
@@ -287,7 +302,26 @@ __device__ __forceinline__ void store_head(const DecodeArgs& a, int64_t o_row, c
   if (a.lse && lane == 0) a.lse[o_row] = (m + __log2f(l)) * 0.693147180559945309f;
 }
 
-template <int DH, int GT, bool F32>
+// Sequences without rows: zeros, and the log-sum of nothing.
+template <int DH, bool F32>
+__device__ __forceinline__ void empty_sequences(const DecodeArgs& a) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < a.num_reqs; r += static_cast<int64_t>(gridDim.x) * kWarps) {
+    if (valid_len(a, a.lens[r]) != 0) continue;
+    const int64_t n = static_cast<int64_t>(a.hq) * DH;
+#pragma unroll 1
+    for (int64_t i = lane; i < n; i += 32) {
+      if (F32) static_cast<float*>(a.out)[r * n + i] = 0.0f;
+      else static_cast<uint16_t*>(a.out)[r * n + i] = 0;
+    }
+    if (a.lse)
+#pragma unroll 1
+      for (int h = lane; h < a.hq; h += 32) a.lse[r * a.hq + h] = -INFINITY;
+  }
+}
+
+template <int DH, int GT, bool F32, bool OWN>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int KC = DH / 32;  // 16-byte pieces of a K row per lane
   constexpr int R = GT / 8;    // head rows per lane
@@ -317,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     c.r = blockIdx.x / heads, c.hh = blockIdx.x - c.r * heads;
     const int raw = a.lens[c.r], len = valid_len(a, raw);
     if (raw != len && tid == 0 && a.err) atomicOr(a.err, kErrMetadata);
-    set_len(a, c, len);
+    set_len<OWN>(a, c, len);
     active = min(kWarps / a.unit, c.steps);
     c.step = 0;
     if (my_unit < active) {
@@ -339,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         const int raw = a.lens[r], len = valid_len(a, raw);
         bad |= len != raw;
         if (i == 0) my_len = len;
-        upto += steps_of(a, len);
+        upto += steps_of<OWN>(a, r, len);
       }
     }
     if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, kErrMetadata);
@@ -379,13 +413,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         from += src;
       }
       c.r = from * per;
-      set_len(a, c, s_len[from]);
+      set_len<OWN>(a, c, s_len[from]);
       if (per > 1) {
 #pragma unroll 1
         for (int i = 0; i < per; i += 32) {
           const int r = from * per + i + lane;
           const int len = i + lane < per && r < a.num_reqs ? valid_len(a, a.lens[r]) : 0;
-          uint32_t x = steps_of(a, len);
+          uint32_t x = steps_of<OWN>(a, r, len);
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -395,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           if (hit) {
             const int src = __ffs(hit) - 1;
             c.r = from * per + i + src;
-            set_len(a, c, __shfl_sync(0xffffffffu, len, src));
+            set_len<OWN>(a, c, __shfl_sync(0xffffffffu, len, src));
             base += __shfl_sync(0xffffffffu, x, src) - c.steps;
             break;
           }
@@ -425,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       for (int u = 0; u < 2; ++u) {
         next_at[u] = (a.tile_units == 1 ? ld.hh : ld.hh / a.tile_units) * (DH * 2);
         if (u == 1 && lane >= 16) mine = ld, have = i + 1 < n_steps;
-        if (i + u < n_steps && ++ld.step == ld.steps) next_group(a, ld, heads);
+        if (i + u < n_steps && ++ld.step == ld.steps) next_group<OWN>(a, ld, heads);
       }
       const int j = mine.first + mine.step * kStep + (lane & 15);
       next_row = -1;
@@ -618,11 +652,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           const int h = h0 + g + 8 * i;
           if (h >= a.g) continue;
           const int64_t o_row = static_cast<int64_t>(c.r) * a.hq + static_cast<int64_t>(kvh) * a.g + h;
-          const float inv = whole ? 1.0f / l[i] : 1.0f;
+          const float inv = whole && !OWN ? 1.0f / l[i] : 1.0f;
           if (t == 0) {
             if (!whole) {
               keep_ml[(g + 8 * i) * 2] = m[i];
               keep_ml[(g + 8 * i) * 2 + 1] = l[i];
+            } else if (OWN) {
+              a.own_ml[o_row * 2] = m[i];
+              a.own_ml[o_row * 2 + 1] = l[i];
             } else if (a.lse) {
               a.lse[o_row] = (m[i] + __log2f(l[i])) * 0.693147180559945309f;
             }
@@ -643,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           }
         }
         if (!at_end) {
-          next_group(a, c, heads);
+          next_group<OWN>(a, c, heads);
           from_start = fresh = true;
         }
       } else {
@@ -698,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       return Part{base + h * DH, base + GT * DH + h * 2};
     }, o, m, l);
     if (!inherited && ended) {
-      store_head<DH>(a, static_cast<int64_t>(head.r_last) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + h, o, m, l);
+      store_head<DH, OWN>(a, static_cast<int64_t>(head.r_last) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + h, o, m, l);
     } else {
       const int64_t at = ((2 * static_cast<int64_t>(blockIdx.x) + (inherited ? 0 : 1)) * a.unit + tile) * GT + h;
       store_row<DH>(a.block_o + at * DH, o, 1.0f);
@@ -715,19 +752,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     a.rec[blockIdx.x] = rec;
   }
 
-  // ---- sequences without rows: zeros, and the log-sum of nothing
-#pragma unroll 1
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + warp; r < a.num_reqs; r += static_cast<int64_t>(gridDim.x) * kWarps) {
-    if (valid_len(a, a.lens[r]) != 0) continue;
-    const int64_t n = static_cast<int64_t>(a.hq) * DH;
-#pragma unroll 1
-    for (int64_t i = lane; i < n; i += 32) {
-      if (F32) static_cast<float*>(a.out)[r * n + i] = 0.0f;
-      else static_cast<uint16_t*>(a.out)[r * n + i] = 0;
-    }
-    if (a.lse)
-#pragma unroll 1
-      for (int h = lane; h < a.hq; h += 32) a.lse[r * a.hq + h] = -INFINITY;
+  if constexpr (OWN) {
+    grid_dependency_wait();  // what waits for this grid's end waits for the one before it too
+  } else {
+    empty_sequences<DH, F32>(a);
   }
 }
 
@@ -739,7 +767,7 @@ constexpr int kJoinWarps = 16;
 // rows of one kv head of 32: 17.6 us, a block a tile 34; 32000 of 8 of 4: 28.0, 28.2. Where groups have few parts more
 // blocks only cost (32 x 4 groups of 16 heads: 57.5 us, 51.3).
 constexpr int kJoinHeads = 2, kJoinParts = 8;
-template <int DH, int GT>
+template <int DH, int GT, bool OWN>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ DecodeArgs a) {
   __shared__ float s_o[kJoinWarps][DH];
   __shared__ float s_ml[kJoinWarps][2];
@@ -783,7 +811,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 #pragma unroll
     for (int x = 0; x < DH / 32; ++x) o[x] += s_o[at][lane * (DH / 32) + x] * e;
   }
-  store_head<DH>(a, static_cast<int64_t>(rec.r) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + from + h, o, top, l);
+  store_head<DH, OWN>(a, static_cast<int64_t>(rec.r) * a.hq + static_cast<int64_t>(kvh) * a.g + h0 + from + h, o, top, l);
 }
 
 struct Layout {
@@ -843,28 +871,99 @@ int check(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int window) {
   return DFLASH_OK;
 }
 
-template <int DH, int GT, bool F32>
-cudaError_t launch(const DecodeArgs& a, const Layout& y, cudaStream_t st) {
+template <int DH, int GT, bool F32, bool OWN = false>
+cudaError_t launch(const DecodeArgs& a, const Layout& y, cudaStream_t st, bool early = false) {
   constexpr int kBytes = kRingBytes<DH>;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<DH, GT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<DH, GT, F32, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  decode_kernel<DH, GT, F32><<<y.grid, kThreads, kBytes, st>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !y.split) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(y.grid - 1), static_cast<unsigned>(y.unit),
-                     static_cast<unsigned>((std::min(GT, a.g) + a.join_heads - 1) / a.join_heads));
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
   cfg.attrs = attr;
+  if (early) {  // may begin while the grid before it ends
+    cfg.gridDim = dim3(static_cast<unsigned>(y.grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kBytes;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<DH, GT, F32, OWN>, a);
+    cfg.dynamicSmemBytes = 0;
+  } else {
+    decode_kernel<DH, GT, F32, OWN><<<y.grid, kThreads, kBytes, st>>>(a);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess || !y.split) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(y.grid - 1), static_cast<unsigned>(y.unit),
+                     static_cast<unsigned>((std::min(GT, a.g) + a.join_heads - 1) / a.join_heads));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<DH, GT>, a);
+  return cudaLaunchKernelEx(&cfg, join_kernel<DH, GT, OWN>, a);
+}
+
+DecodeArgs args_of(const DecodeCall& c, const Layout& y, char* ws) {
+  DecodeArgs a{};
+  a.q = c.q, a.q_tok = c.q_stride, a.k = c.k_pool, a.v = c.v_pool;
+  a.table = c.block_table, a.table_stride = c.block_table_stride, a.lens = c.seq_lens;
+  a.err = reinterpret_cast<uint32_t*>(c.status);
+  a.rec = reinterpret_cast<Record*>(ws + y.rec);
+  a.block_ml = reinterpret_cast<float*>(ws + y.block_ml);
+  a.block_o = reinterpret_cast<float*>(ws + y.block_o);
+  a.part_ml = reinterpret_cast<float*>(ws + y.ml);
+  a.part_o = reinterpret_cast<float*>(ws + y.o);
+  a.num_reqs = c.num_reqs, a.hq = c.hq, a.hkv = c.hkv, a.g = c.hq / c.hkv;
+  a.unit = y.unit, a.tile_units = y.tile_units, a.lone = y.lone, a.join_heads = y.join_heads;
+  a.num_pages = c.num_pages, a.page = c.page_size, a.window = c.window;
+  a.max_len = c.max_ctx_len;
+  divide_by_page(c.page_size, &a.page_mul, &a.page_shift);
+  a.scale_log2 = scale_log2_of(c);
+  a.max_workers = y.workers;
+  return a;
 }
 
 }  // namespace
+
+int check_call(const DecodeCall& c) {
+  int rc = check(c.num_reqs, c.hq, c.hkv, c.dh, c.max_ctx_len, c.window);
+  if (rc != DFLASH_OK) return rc;
+  if (c.out_dtype != DFLASH_OUT_BF16 && c.out_dtype != DFLASH_OUT_F32)
+    return errorf(DFLASH_ERR_INVALID_ARG, "out_dtype %d is neither DFLASH_OUT_BF16 nor DFLASH_OUT_F32", c.out_dtype);
+  if (!std::isfinite(c.scale)) return errorf(DFLASH_ERR_INVALID_ARG, "scale must be finite");
+  if (c.page_size <= 0 || c.max_pages_per_req < 0 || c.num_pages < 0 || c.block_table_stride < c.max_pages_per_req)
+    return errorf(DFLASH_ERR_INVALID_ARG, "page_size must be positive, page counts >= 0, the table's stride >= its width");
+  if (c.num_pages > 0x7fffffffLL / c.page_size)
+    return errorf(DFLASH_ERR_UNSUPPORTED, "the pools must hold fewer than 2^31 rows (num_pages=%lld)",
+                  static_cast<long long>(c.num_pages));
+  if (static_cast<int64_t>(c.max_pages_per_req) * c.page_size < c.max_ctx_len)
+    return errorf(DFLASH_ERR_INVALID_ARG, "max_ctx_len %d exceeds max_pages_per_req x page_size", c.max_ctx_len);
+  if (c.max_ctx_len > 0 && c.num_pages == 0) return errorf(DFLASH_ERR_INVALID_ARG, "max_ctx_len > 0 needs pages");
+  if (c.num_reqs == 0) return report_error(DFLASH_OK, "");
+  if (!c.q || !c.seq_lens || !c.out || !c.workspace || (c.max_ctx_len > 0 && (!c.block_table || !c.k_pool || !c.v_pool)))
+    return errorf(DFLASH_ERR_INVALID_ARG, "null pointer argument");
+  auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  if (!aligned(c.q) || !aligned(c.k_pool) || !aligned(c.v_pool) || !aligned(c.out) || c.q_stride % 8)
+    return errorf(DFLASH_ERR_INVALID_ARG, "tensor pointers and rows of q must be 16-byte aligned");
+  if (c.num_reqs > 1 && c.q_stride < static_cast<int64_t>(c.hq) * c.dh && c.q_stride != 0)
+    return errorf(DFLASH_ERR_INVALID_ARG, "rows of q overlap");
+  if ((reinterpret_cast<uintptr_t>(c.workspace) & 255u) != 0)
+    return errorf(DFLASH_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  return report_error(DFLASH_OK, "");
+}
+
+size_t own_rows_workspace(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int window, int sms) {
+  return layout_of(num_reqs, hq, hkv, dh, max_ctx_len, window, sms).total;
+}
+
+cudaError_t launch_own_rows(const DecodeCall& c, const int32_t* own, float* o, float* ml, char* workspace, int sms, bool early,
+                            cudaStream_t st) {
+  const Layout y = layout_of(c.num_reqs, c.hq, c.hkv, c.dh, c.max_ctx_len, c.window, sms);
+  DecodeArgs a = args_of(c, y, workspace);
+  a.own = own, a.out = o, a.own_ml = ml;
+  a.out_f32 = 1;
+  if (c.dh == 128) return y.gt == 8 ? launch<128, 8, true, true>(a, y, st, early) : launch<128, 16, true, true>(a, y, st, early);
+  return y.gt == 8 ? launch<64, 8, true, true>(a, y, st, early) : launch<64, 16, true, true>(a, y, st, early);
+}
+
 }  // namespace dflash
 
 extern "C" {
@@ -885,61 +984,19 @@ int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const 
                                   int out_dtype, void* out, float* lse, void* workspace, size_t workspace_bytes,
                                   int32_t* status, dflash_stream_t stream) {
   using namespace dflash;
-  int rc = check(num_reqs, hq, hkv, dh, max_ctx_len, window);
-  if (rc != DFLASH_OK) return rc;
-  if (out_dtype != DFLASH_OUT_BF16 && out_dtype != DFLASH_OUT_F32)
-    return errorf(DFLASH_ERR_INVALID_ARG, "out_dtype %d is neither DFLASH_OUT_BF16 nor DFLASH_OUT_F32", out_dtype);
-  if (!std::isfinite(scale)) return errorf(DFLASH_ERR_INVALID_ARG, "scale must be finite");
-  if (page_size <= 0 || max_pages_per_req < 0 || num_pages < 0 || block_table_stride < max_pages_per_req)
-    return errorf(DFLASH_ERR_INVALID_ARG, "page_size must be positive, page counts >= 0, the table's stride >= its width");
-  if (num_pages > 0x7fffffffLL / page_size)
-    return errorf(DFLASH_ERR_UNSUPPORTED, "the pools must hold fewer than 2^31 rows (num_pages=%lld)",
-                  static_cast<long long>(num_pages));
-  if (static_cast<int64_t>(max_pages_per_req) * page_size < max_ctx_len)
-    return errorf(DFLASH_ERR_INVALID_ARG, "max_ctx_len %d exceeds max_pages_per_req x page_size", max_ctx_len);
-  if (max_ctx_len > 0 && num_pages == 0) return errorf(DFLASH_ERR_INVALID_ARG, "max_ctx_len > 0 needs pages");
-  if (num_reqs == 0) return report_error(DFLASH_OK, "");
-  if (!q || !seq_lens || !out || !workspace || (max_ctx_len > 0 && (!block_table || !k_pool || !v_pool)))
-    return errorf(DFLASH_ERR_INVALID_ARG, "null pointer argument");
-  auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  if (!aligned(q) || !aligned(k_pool) || !aligned(v_pool) || !aligned(out) || q_stride % 8)
-    return errorf(DFLASH_ERR_INVALID_ARG, "tensor pointers and rows of q must be 16-byte aligned");
-  if (num_reqs > 1 && q_stride < static_cast<int64_t>(hq) * dh && q_stride != 0)
-    return errorf(DFLASH_ERR_INVALID_ARG, "rows of q overlap");
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-    return errorf(DFLASH_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const DecodeCall c{q, q_stride, k_pool, v_pool, block_table, block_table_stride, seq_lens, num_reqs, hq, hkv, dh, num_pages, page_size,
+                     max_pages_per_req, max_ctx_len, scale, window, out_dtype, out, lse, workspace, workspace_bytes, status};
+  int rc = check_call(c);
+  if (rc != DFLASH_OK || num_reqs == 0) return rc;
   int sms = 0;
   rc = query_sms(&sms);
   if (rc != DFLASH_OK) return rc;
   const Layout y = layout_of(num_reqs, hq, hkv, dh, max_ctx_len, window, sms);
   if (workspace_bytes < y.total)
     return errorf(DFLASH_ERR_WORKSPACE, "workspace has %zu bytes; %zu are needed", workspace_bytes, y.total);
-  char* ws = static_cast<char*>(workspace);
-  DecodeArgs a{};
-  a.q = q, a.q_tok = q_stride, a.k = k_pool, a.v = v_pool;
-  a.table = block_table, a.table_stride = block_table_stride, a.lens = seq_lens;
-  a.out = out, a.lse = lse, a.err = reinterpret_cast<uint32_t*>(status);
-  a.rec = reinterpret_cast<Record*>(ws + y.rec);
-  a.block_ml = reinterpret_cast<float*>(ws + y.block_ml);
-  a.block_o = reinterpret_cast<float*>(ws + y.block_o);
-  a.part_ml = reinterpret_cast<float*>(ws + y.ml);
-  a.part_o = reinterpret_cast<float*>(ws + y.o);
-  a.num_reqs = num_reqs, a.hq = hq, a.hkv = hkv, a.g = hq / hkv;
-  a.unit = y.unit, a.tile_units = y.tile_units, a.lone = y.lone, a.join_heads = y.join_heads;
-  a.num_pages = num_pages, a.page = page_size, a.window = window;
-  a.max_len = max_ctx_len;
-  if ((page_size & (page_size - 1)) == 0) {
-    while ((1 << a.page_shift) < page_size) ++a.page_shift;
-  } else {  // j / page for j < 2^31: multiply by ceil(2^(31 + bits) / page) (Granlund and Montgomery, 1994)
-    uint32_t bits = 0;
-    while ((1u << bits) < static_cast<uint32_t>(page_size)) ++bits;
-    a.page_mul = static_cast<uint32_t>(((1ull << (31 + bits)) + page_size - 1) / page_size);
-    a.page_shift = bits - 1;
-  }
-  const float sc = scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(dh));
-  a.scale_log2 = sc * 1.4426950408889634f;
+  DecodeArgs a = args_of(c, y, static_cast<char*>(workspace));
+  a.out = out, a.lse = lse;
   a.out_f32 = out_dtype == DFLASH_OUT_F32;
-  a.max_workers = y.workers;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dh == 128)

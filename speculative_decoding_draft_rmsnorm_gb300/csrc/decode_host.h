@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 
 #include "../../include/dflash.h"
@@ -36,5 +37,52 @@ inline int query_sms(int* out) {
   if (dev < 64) known[dev].store(*out, std::memory_order_relaxed);
   return DFLASH_OK;
 }
+
+// j / page = umulhi(j, *mul) >> *shift, or j >> *shift where *mul is 0, for j < 2^31.
+inline void divide_by_page(int page, uint32_t* mul, uint32_t* shift) {
+  *mul = *shift = 0;
+  if ((page & (page - 1)) == 0) {
+    while ((1 << *shift) < page) ++*shift;
+  } else {  // multiply by ceil(2^(31 + bits) / page) (Granlund and Montgomery, 1994)
+    uint32_t bits = 0;
+    while ((1u << bits) < static_cast<uint32_t>(page)) ++bits;
+    *mul = static_cast<uint32_t>(((1ull << (31 + bits)) + page - 1) / page);
+    *shift = bits - 1;
+  }
+}
+
+// The arguments that the attention calls of a decode step share (see include/dflash.h).
+struct DecodeCall {
+  const uint16_t* q;
+  int64_t q_stride;
+  const uint16_t *k_pool, *v_pool;
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  const int32_t* seq_lens;
+  int num_reqs, hq, hkv, dh;
+  int64_t num_pages;
+  int page_size, max_pages_per_req, max_ctx_len;
+  float scale;
+  int window, out_dtype;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* status;
+};
+
+// Refuses what an attention call of a decode step may not be given; its workspace's size is not looked at.
+int check_call(const DecodeCall& c);
+
+inline float scale_log2_of(const DecodeCall& c) {
+  return (c.scale > 0.0f ? c.scale : 1.0f / std::sqrt(static_cast<float>(c.dh))) * 1.4426950408889634f;
+}
+
+// Attention of every sequence over its rows from own[r] on (or from the window's first), unnormalised: o [num_reqs, Hq, Dh]
+// f32, ml [num_reqs, Hq, 2] its maximum (base 2) and weight; heads without such rows are left as they are. early: the grids
+// may begin while the one before them on the stream runs, which must have waited for what wrote own; they end after it.
+size_t own_rows_workspace(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int window, int sms);
+cudaError_t launch_own_rows(const DecodeCall& c, const int32_t* own, float* o, float* ml, char* workspace, int sms, bool early,
+                            cudaStream_t st);
 
 }  // namespace dflash

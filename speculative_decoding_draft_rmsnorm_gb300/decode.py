@@ -10,6 +10,7 @@ and a step of sequences that share a prompt:
     rms_norm(...)                -> dflash_rms_norm
     rotary_axes(...)             -> dflash_rotary_axes
     shared_prefixes(...)         -> dflash_shared_prefixes
+    decode_attention_shared(...) -> dflash_decode_attention_shared
 
 Like the rest of the package these only marshal arguments (csrc/bind.cpp checks them and makes the call).
 All tensors of a call live on one device; the call runs there, on `stream` (default: that device's current
@@ -41,6 +42,9 @@ def declare(lib) -> None:
         "dflash_decode_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32]),
         "dflash_decode_attention_paged": (I32, [P, I64, P, P, P, I64, P, I32, I32, I32, I32, I64, I32, I32, I32, F32, I32,
                                                 I32, P, P, P, SZ, P, P]),
+        "dflash_shared_workspace_size": (SZ, [I32] * 7),
+        "dflash_decode_attention_shared": (I32, [P, I64, P, P, P, I64, P, P, P, I32, I32, I32, I32, I32, I64, I32, I32, I32, F32,
+                                                 I32, I32, P, P, P, SZ, P, P]),
         "dflash_beam_workspace_size": (SZ, [I32, I32, I32, I32, I32]),
         "dflash_beam_select": (I32, [P, I64, I64, P, P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, SZ, P]),
         "dflash_pages_workspace_size": (SZ, [I32, I64]),
@@ -266,6 +270,35 @@ def shared_prefixes(block_table, seq_lens, group_start_loc, *, page_size, out=No
         with _on(stream, block_table):
             return shared_prefixes(block_table, seq_lens, group_start_loc, page_size=page_size, out=out, status=status)
     got = bind.shared_prefixes(block_table, seq_lens, group_start_loc, page_size, out, status)
+    if type(got) is int:
+        _fail(got)
+    return got
+
+
+def shared_workspace_size(num_reqs, num_groups, hq, hkv, dh, max_ctx_len, window=0) -> int:
+    n = _base().load().dflash_shared_workspace_size(num_reqs, num_groups, hq, hkv, dh, int(max_ctx_len), int(window))
+    if n == 0:
+        _base()._raise(_base().ERR_INVALID_ARG)
+    return int(n)
+
+
+def decode_attention_shared(q, k_pool, v_pool, block_table, seq_lens, group_start_loc, prefix_lens, *, max_ctx_len, out=None,
+                            lse=None, return_lse=False, workspace=None, scale=0.0, window=0, out_dtype=OUT_BF16, status=None,
+                            stream=None):
+    """`decode_attention_paged` where the rows that a group of sequences shares are read once for all of them.
+
+    Group g is the sequences group_start_loc[g] .. group_start_loc[g + 1] (int32 [groups + 1]); the first prefix_lens[g]
+    rows (int32 [groups], see shared_prefixes) of its sequences that are so long lie in the same pages. Everything
+    else, and the result, as in decode_attention_paged; the workspace is shared_workspace_size's.
+    """
+    bind = _bind or _load()
+    if stream is not None:
+        with _on(stream, q):
+            return decode_attention_shared(q, k_pool, v_pool, block_table, seq_lens, group_start_loc, prefix_lens,
+                                           max_ctx_len=max_ctx_len, out=out, lse=lse, return_lse=return_lse, workspace=workspace,
+                                           scale=scale, window=window, out_dtype=out_dtype, status=status)
+    got = bind.decode_attention_shared(q, k_pool, v_pool, block_table, seq_lens, int(max_ctx_len), out, lse, return_lse, workspace,
+                                       scale, int(window), out_dtype, status, group_start_loc, prefix_lens)
     if type(got) is int:
         _fail(got)
     return got

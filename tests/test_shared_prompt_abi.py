@@ -92,3 +92,26 @@ def test_bindings_refuse_what_is_no_cuda_tensor():
                  lambda: D.shared_prefixes(i.view(1, 2), i, i, page_size=16), lambda: D.shared_prefixes(None, i, i, page_size=16)):
         with pytest.raises((TypeError, ValueError)):
             call()
+
+
+def _shared(n=2, groups=1, hq=8, hkv=2, dh=64, pages=8, page=16, width=4, most=64, scale=0.0, window=0, dt=0, stride=4, qs=512, ws=256, q=P(1 << 20),
+            starts=P(4096), prefixes=P(8192)):
+    F = P(1 << 20)
+    return D.load().dflash_decode_attention_shared(q, qs, F, F, F, stride, F, starts, prefixes, n, groups, hq, hkv, dh, pages, page, width, most, scale, window,
+                                                   dt, F, None, P(ws), 0, None, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dh=96), D.ERR_UNSUPPORTED), (dict(hq=7), D.ERR_INVALID_ARG), (dict(hkv=0), D.ERR_INVALID_ARG), (dict(n=-1), D.ERR_INVALID_ARG),
+    (dict(groups=-1), D.ERR_INVALID_ARG), (dict(groups=(1 << 24) + 1), D.ERR_UNSUPPORTED), (dict(starts=None), D.ERR_INVALID_ARG),
+    (dict(prefixes=None), D.ERR_INVALID_ARG), (dict(page=0), D.ERR_INVALID_ARG), (dict(most=65), D.ERR_INVALID_ARG),
+    (dict(window=-1), D.ERR_INVALID_ARG), (dict(scale=math.inf), D.ERR_INVALID_ARG), (dict(dt=2), D.ERR_INVALID_ARG),
+    (dict(stride=3), D.ERR_INVALID_ARG), (dict(pages=0), D.ERR_INVALID_ARG), (dict(qs=100), D.ERR_INVALID_ARG), (dict(q=None), D.ERR_INVALID_ARG),
+    (dict(ws=128), D.ERR_WORKSPACE),
+])
+def test_shared_refusals(kw, code):
+    assert _shared(**kw) == code and D.load().dflash_last_error()
+
+
+def test_shared_nothing_to_do():
+    assert _shared(n=0) == 0
