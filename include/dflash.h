@@ -596,7 +596,7 @@ DFLASH_API size_t dflash_shared_workspace_size(int num_reqs, int num_groups, int
  *              [0, num_reqs]: reported, and then no group shares anything.
  *   prefix_lens int32 [num_groups] device: the first prefix_lens[g] rows of the group's sequences that are at
  *              least that long lie in the same pages (dflash_shared_prefixes; any shorter prefix does too). They
- *              are read in the pages of the first such sequence. Shorter sequences of the group read their own
+ *              are read in the pages of the shortest such sequence. Shorter sequences of the group read their own
  *              rows. Negative or above max_ctx_len: reported and treated as 0.
  *   Every other argument, and the result, as dflash_decode_attention_paged (the workspace as
  *   dflash_shared_workspace_size says). The result does not depend on timing; another prefix gives another order of the

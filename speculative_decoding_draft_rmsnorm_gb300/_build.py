@@ -29,7 +29,7 @@ LIB_PATH = os.path.join(LIB_DIR, LIB_NAME)
 SOURCES = ["api.cu", "attention.cu", "norm_rope.cu", "noalloc.cu", "draft_step.cu", "rotary.cu",
            "decode_attention.cu", "beam.cu", "pages.cu", "rms_norm.cu", "shared_prefixes.cu",
            "shared_attention.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "norm_rope.cuh", "decode_host.h"]
+HEADERS = ["ptx.cuh", "internal.h", "norm_rope.cuh", "decode_host.h", "attention_parts.cuh"]
 # The marshalling module of decode.py: host C++ against torch and the product library.
 BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -9,6 +9,7 @@
 #include <cmath>
 
 #include "../../include/dflash.h"
+#include "attention_parts.cuh"
 #include "decode_host.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -26,7 +27,7 @@ constexpr int kLeastPrefix = 64;
 struct SharedGroup {
   int first, rows;  // its first sequence; sequences x heads of a kv head
   int prefix, lo;
-  int leader;       // the sequence whose pages are read
+  int leader;       // the shortest sequence that shares: its pages are read
   int tiles_m, n;
   uint32_t start;
 };
@@ -48,10 +49,17 @@ struct SharedArgs {
   uint32_t* err;
   Header* header;
   SharedGroup* groups;
-  int32_t* seen;  // [num_groups][2]: first visible row and leader, while the plan is made
+  unsigned long long* least;  // [num_groups]: length and index of the shortest sequence that shares, while the plan is made
   int32_t* own;   // [num_reqs]: rows before it are the prefix's
   float* own_o;   // [num_reqs][Hq][Dh], a head's sums over its own rows
   float* own_ml;  // [num_reqs][Hq][2]
+  // a head's sums over the prefix: where one block had them all, `pre`, else the parts of blocks first .. last; the first
+  // block's in its slot 2b + 1, the others' in theirs, 2b
+  int2* where;     // [num_reqs][Hq]: (first or -1, last and the row in the slots << 16)
+  float* pre_o;    // [num_reqs][Hq][Dh]
+  float* pre_ml;   // [num_reqs][Hq][2]
+  float* part_o;   // [2 * blocks][kRows][Dh]
+  float* part_ml;  // [2 * blocks][kRows][2]
   void* out;
   float* lse;
   int num_reqs, num_groups, hq, hkv, g;
@@ -66,19 +74,21 @@ __device__ __forceinline__ int valid_len(const SharedArgs& a, int len) { return 
 __device__ __forceinline__ int first_row(const SharedArgs& a, int len) { return a.window > 0 && len > a.window ? len - a.window : 0; }
 
 // The plan, by one block: which groups share, and from where to where; where every sequence's own rows begin. A
-// sequence shares if it is at least as long as the prefix; the tiles start at the first row that any of them sees.
+// sequence shares if it is at least as long as the prefix. The shortest that does sees the first row that any of them
+// sees, where the tiles start, and every row from there on: its pages are read.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ SharedArgs a) {
   __shared__ int s_bad, s_groups;
   __shared__ uint32_t s_tiles;
   __shared__ uint32_t s_warp[32];
   __shared__ int s_count[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dependents_launch();
   if (tid == 0) s_bad = 0, s_tiles = 0, s_groups = 0;
   __syncthreads();
   for (int g = tid; g < a.num_groups; g += kPlanThreads) {
     const int from = a.starts[g], to = a.starts[g + 1];
     if (from < 0 || from > to || to > a.num_reqs) s_bad = 1;
-    a.seen[2 * g] = a.seen[2 * g + 1] = 0x7fffffff;
+    a.least[g] = ~0ull;
   }
   __syncthreads();
   const int groups = s_bad ? 0 : a.num_groups;
@@ -100,8 +110,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       }
       const int p = shared_rows(lo, a.starts[lo + 1] - a.starts[lo]);
       if (p > 0 && len >= p) {
-        atomicMin(&a.seen[2 * lo], first_row(a, len));
-        atomicMin(&a.seen[2 * lo + 1], r);
+        own = p;
+        atomicMin(&a.least[lo], static_cast<unsigned long long>(len) << 32 | static_cast<uint32_t>(r));
       }
     }
     a.own[r] = own;
@@ -118,10 +128,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       x.first = a.starts[g];
       const int members = a.starts[g + 1] - x.first;
       x.prefix = shared_rows(g, members);
-      x.lo = *static_cast<volatile int*>(&a.seen[2 * g]), x.leader = *static_cast<volatile int*>(&a.seen[2 * g + 1]);
+      const unsigned long long least = *static_cast<volatile unsigned long long*>(&a.least[g]);
+      x.lo = first_row(a, static_cast<int>(least >> 32)), x.leader = static_cast<int>(least & 0xffffffffu);
       x.rows = members * a.g;
       x.tiles_m = (x.rows + kRows - 1) / kRows;
-      if (x.lo < x.prefix) {
+      if (least != ~0ull && x.lo < x.prefix) {
         x.n = (x.prefix - x.lo + kKeys - 1) / kKeys;
         tiles = static_cast<uint32_t>(x.n) * x.tiles_m * a.hkv;
       }
@@ -151,34 +162,507 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   if (tid == 0) *a.header = Header{s_tiles, s_groups};
 }
 
-// Joins the parts of a head and stores it; a warp a head.
+// The blocks' ranges of tiles: equal to within one.
+struct TileRanges {
+  uint32_t each, extra;  // the first `extra` blocks take each + 1
+  __device__ __forceinline__ TileRanges(uint32_t total, uint32_t blocks) : each(total / blocks), extra(total % blocks) {}
+  __device__ __forceinline__ uint32_t start(uint32_t b) const { return b * each + min(b, extra); }
+  __device__ __forceinline__ int owner(uint32_t x) const {  // of tile x
+    const uint32_t cut = extra * (each + 1);
+    return static_cast<int>(x < cut ? x / (each + 1) : extra + (x - cut) / each);
+  }
+};
+
+// Tiles [t0, t1) of a unit: kv head kvh, rows m0 .. of its group.
+struct Unit {
+  int first, rows, prefix, lo, leader;
+  int kvh, m0, t0, t1, n;
+  uint32_t start;  // its tile 0
+};
+
+// A block's units, one after the other. Every role walks them for itself.
+struct Walk {
+  const SharedGroup* groups;
+  uint32_t x, hi;
+  int at, hkv;
+  SharedGroup g;
+  __device__ __forceinline__ Walk(const SharedArgs& a, int first, uint32_t lo, uint32_t hi_) : groups(a.groups), x(lo), hi(hi_), at(first), hkv(a.hkv) {
+    g = groups[at];
+  }
+  __device__ __forceinline__ bool next(Unit& u) {
+    if (x >= hi) return false;
+    if (x - g.start >= static_cast<uint32_t>(g.n) * g.tiles_m * hkv) g = groups[++at];
+    const uint32_t rel = x - g.start, unit = rel / static_cast<uint32_t>(g.n);
+    u.first = g.first, u.rows = g.rows, u.prefix = g.prefix, u.lo = g.lo, u.leader = g.leader, u.n = g.n;
+    u.kvh = static_cast<int>(unit) / g.tiles_m;
+    u.m0 = (static_cast<int>(unit) - u.kvh * g.tiles_m) * kRows;
+    u.t0 = static_cast<int>(rel - unit * g.n);
+    u.t1 = static_cast<int>(min(static_cast<uint32_t>(u.n), u.t0 + (hi - x)));
+    u.start = x - u.t0;
+    x += u.t1 - u.t0;
+    return true;
+  }
+};
+
+// Warps 0 and 1 copy, 3 issues products, 4-7 and 8-11 make weights, 12-15 add the sums up.
+constexpr int kProducers = 2, kMine = kRows / kProducers / 32, kIssuer = 3;
+constexpr int kThreads = 16 * 32;
+// Registers of a thread in the three kinds of warpgroups: together at most what the block is launched with, 4 x 128.
+constexpr int kCopyRegs = 80, kSumRegs = 176;
+static_assert(kCopyRegs + 2 * 128 + kSumRegs <= 4 * 128, "the block's registers");
+
+// Shared memory: two Q tiles and a ring of K and V tiles, in 64-column blocks of 128 rows x 128 bytes (128-byte
+// swizzle). Tensor memory: kBufs buffers of scores, whose columns the weights take (a chunk of 32 rows' scores
+// becomes its 16 columns of high and 16 of middle terms; low terms lie behind the 128), and a tile's P V.
+template <int DH, bool F32>
+struct Shape {
+  static constexpr int kTile = kKeys * DH * 2;
+  static constexpr int kSlots = DH == 128 ? 5 : 10;
+  static constexpr int kAhead = kSlots - 2;
+  static constexpr int kTerms = F32 ? 3 : 2;
+  static constexpr int kBufs = F32 ? 2 : 3;
+  static constexpr int kBufCols = F32 ? 192 : 128;
+  static constexpr int kOut = 384;
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kStats = kRing + kSlots * kTile;
+  static constexpr int kBars = kStats + 2 * kRows * 8;
+  static constexpr int kFull = 0, kEmpty = kSlots, kQEmpty = 2 * kSlots, kSFull = kQEmpty + 2, kPFull = kSFull + 3, kOFull = kPFull + 3,
+                       kOEmpty = kOFull + 1, kDrain = kOEmpty + 2, kNumBars = kDrain + 1;
+  static constexpr int kMisc = kBars + kNumBars * 8;
+  static constexpr int kBytes = kMisc + 32;
+  static_assert(kBytes <= 232448, "a block's shared memory");
+};
+
+__device__ __forceinline__ int page_of(const SharedArgs& a, int j) {
+  return a.page_mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(j), a.page_mul) >> a.page_shift) : j >> a.page_shift;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int size, uint64_t policy) {  // size 0: zeros
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(size), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int DH, bool F32>
+__global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ SharedArgs a) {
+  using S = Shape<DH, F32>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + S::kBars + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
+  int* first_group = reinterpret_cast<int*>(smem + S::kMisc + 8);
+  float2* stats = reinterpret_cast<float2*>(smem + S::kStats);  // [2][kRows]: a tile's reference and weight
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots; ++i) mbar_init(bar(S::kFull + i), kProducers), mbar_init(bar(S::kEmpty + i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(S::kQEmpty + i), 1), mbar_init(bar(S::kOEmpty + i), 4);
+    for (int i = 0; i < 3; ++i) mbar_init(bar(S::kSFull + i), 1), mbar_init(bar(S::kPFull + i), 4);
+    mbar_init(bar(S::kOFull), 1), mbar_init(bar(S::kDrain), 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == kIssuer) tmem_alloc(smem_u32(tmem_slot), 512);
+  grid_dependency_wait();  // the plan
+  grid_dependents_launch();
+  const Header head = *a.header;
+  const TileRanges ranges(head.tiles, gridDim.x);
+  const uint32_t lo = ranges.start(blockIdx.x), hi = ranges.start(blockIdx.x + 1);
+  if (warp == 0 && lo < hi) {  // the group that holds tile lo, 32 at a time
+    int from = 0, n = head.groups;
+    while (n > 1) {
+      const int step = (n + 31) / 32, i = lane * step;
+      const uint32_t le = __ballot_sync(0xffffffffu, i < n && a.groups[from + min(i, n - 1)].start <= lo);
+      const int k = 31 - __clz(le);
+      from += k * step, n = min(step, n - k * step);
+    }
+    if (lane == 0) *first_group = from;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait_warp = [&](uint32_t b, uint32_t parity) -> bool {
+    int r = 1;
+    if (lane == 0) r = mbar_wait(b, parity, abort_flag) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, r, 0) != 0;
+  };
+  bool ok = true;
+  if (warp < 4) registers_down<kCopyRegs>();
+
+  if (lo >= hi) {
+    // no tiles
+  } else if (warp < kProducers) {
+    // ------------------------------------------------------------ copies: warp w has rows 64 w .. of every tile
+    // Stages in the order in which products take them: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
+    constexpr int kPieces = DH / 8, kAtOnce = 32 / kPieces;  // 16-byte pieces of a row; rows of an instruction
+    const int64_t row_bytes = static_cast<int64_t>(a.hkv) * DH * 2;
+    const uint64_t policy = l2_policy_evict_first();
+    const int piece = lane % kPieces, sub = lane / kPieces;
+    // row r's piece p lies in block p / 8, at piece (p % 8) ^ (r % 8) of the row's 128 bytes
+    const uint32_t dst_lane = sbase + (piece / 8) * (kKeys * 128) + (warp * 32 * kMine + sub) * 128;
+    const int swz = (piece % 8) ^ sub;
+    uint32_t c = 0, told = 0;  // stages so far; those that the products know of
+    auto tell = [&](uint32_t upto) {  // stages below it have landed
+      if (told >= upto) return;
+      fence_proxy_async_smem();
+      __syncwarp();
+      for (; told < upto; ++told)
+        if (lane == 0) mbar_arrive(bar(S::kFull + told % S::kSlots));
+    };
+    auto open_stage = [&]() -> bool {
+      if (c > S::kAhead) {
+        cp_async_wait<S::kAhead>();
+        tell(c - S::kAhead);
+      }
+      return c < S::kSlots || wait_warp(bar(S::kEmpty + c % S::kSlots), (c / S::kSlots - 1) & 1);
+    };
+    // kAtOnce rows from row i kAtOnce of this warp's on
+    auto copy = [&](const void* src, bool have, uint32_t off, int i) {
+      cp_async16(dst_lane + off + i * kAtOnce * 128 + ((swz ^ (i * kAtOnce & 7)) << 4), src, have ? 16 : 0, policy);
+    };
+    auto copy_rows = [&](const char* base, const int (&row)[kMine], int head_bytes, uint32_t off) {  // rows of the lanes; -1: zeros
+      const char* src = base + head_bytes + piece * 16;
+#pragma unroll
+      for (int y = 0; y < kMine; ++y)
+#pragma unroll 8
+        for (int i = 0; i < 32 / kAtOnce; ++i) {
+          const int x = __shfl_sync(0xffffffffu, row[y], i * kAtOnce + sub);
+          copy(src + max(x, 0) * row_bytes, x >= 0, off, y * (32 / kAtOnce) + i);
+        }
+    };
+    Walk walk(a, *first_group, lo, hi);
+    Unit u;
+    int t = 0, end = 0, iu = -1;  // the tile looked up next; its unit's end
+    int id[kMine], key[kMine];    // its pages and rows
+    bool fresh = false;           // it begins a unit
+    auto look_up = [&]() -> bool {
+      fresh = t >= end;
+      if (fresh) {
+        if (!walk.next(u)) return false;
+        t = u.t0, end = u.t1;
+      }
+#pragma unroll
+      for (int y = 0; y < kMine; ++y) {
+        key[y] = u.lo + t * kKeys + (warp * kMine + y) * 32 + lane;
+        if (key[y] < u.prefix) id[y] = a.table[u.leader * a.table_stride + page_of(a, key[y])];
+        else key[y] = -1;
+      }
+      ++t;
+      return true;
+    };
+    bool have = look_up();
+    int v_row[kMine], v_head = 0;
+    for (bool more = false; ok && (have || more);) {
+      int row[kMine], head_bytes = 0;
+      const bool now = have;
+      if (now) {
+        head_bytes = u.kvh * (DH * 2);
+#pragma unroll
+        for (int y = 0; y < kMine; ++y) {
+          row[y] = -1;
+          if (key[y] < 0) continue;
+          if (id[y] < 0 || id[y] >= a.num_pages) {
+            if (a.err) atomicOr(a.err, kErrMetadata);
+            id[y] = 0;
+          }
+          row[y] = id[y] * a.page + (key[y] - page_of(a, key[y]) * a.page);
+        }
+        if (!(ok = open_stage())) break;
+        if (fresh) {  // Q, in its first K tile's stage
+          ++iu;
+          if (iu >= 2) {
+            const uint32_t b = bar(S::kQEmpty + (iu & 1)), parity = ((iu >> 1) - 1) & 1;
+            if (!__any_sync(0xffffffffu, lane == 0 && mbar_test_wait(b, parity))) {
+              // the products that free it may wait for stages that have landed untold
+              cp_async_wait<0>();
+              tell(c);
+              if (!(ok = wait_warp(b, parity))) break;
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < kMine; ++y) {
+            const int at = u.m0 + (warp * kMine + y) * 32 + lane, s = at / a.g;
+            const int64_t mine = at < u.rows ? (u.first + s) * a.q_tok + static_cast<int64_t>(u.kvh * a.g + at - s * a.g) * DH : -1;
+#pragma unroll 4
+            for (int i = 0; i < 32 / kAtOnce; ++i) {
+              const int64_t x = __shfl_sync(0xffffffffu, mine, i * kAtOnce + sub);
+              copy(a.q + (x < 0 ? 0 : x) + piece * 8, x >= 0, (iu & 1) * S::kTile, y * (32 / kAtOnce) + i);
+            }
+          }
+        }
+        copy_rows(reinterpret_cast<const char*>(a.k), row, head_bytes, S::kRing + (c % S::kSlots) * S::kTile);
+        cp_async_commit();
+        ++c;
+        have = look_up();
+      }
+      if (more) {  // V of the tile before
+        if (!(ok = open_stage())) break;
+        copy_rows(reinterpret_cast<const char*>(a.v), v_row, v_head, S::kRing + (c % S::kSlots) * S::kTile);
+        cp_async_commit();
+        ++c;
+      }
+      more = now, v_head = head_bytes;
+#pragma unroll
+      for (int y = 0; y < kMine; ++y) v_row[y] = row[y];
+    }
+    cp_async_wait<0>();
+    if (ok) tell(c);
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      const uint32_t idesc_s = umma_idesc_bf16(kRows, kKeys, 0, 0), idesc_o = umma_idesc_bf16(kRows, DH, 0, 1);
+      const uint32_t n = hi - lo;
+      uint32_t c = 0;
+      Walk walk(a, *first_group, lo, hi);
+      Unit u;
+      int iu = -1;
+      uint32_t left = 0;  // tiles of the unit whose scores are to come
+      auto full = [&]() { return mbar_wait(bar(S::kFull + c % S::kSlots), (c / S::kSlots) & 1, abort_flag); };
+      auto scores = [&](uint32_t t) -> bool {
+        if (left == 0) {
+          walk.next(u);
+          left = u.t1 - u.t0;
+          ++iu;
+        }
+        // the buffer's weights have been used: with three buffers two tiles' sums came between
+        if (F32 && t >= 2 && !mbar_wait(bar(S::kOFull), (t - 2) & 1, abort_flag)) return false;
+        if (!full()) return false;
+        tc_fence_after();
+        const uint64_t q = umma_desc_sw128(sbase + (iu & 1) * S::kTile, 16, 1024), k = umma_desc_sw128(sbase + S::kRing + (c % S::kSlots) * S::kTile, 16, 1024);
+        const uint32_t d = tmem + t % S::kBufs * S::kBufCols;
+#pragma unroll
+        for (int i = 0; i < DH / 16; ++i) {
+          const uint32_t off = ((i >> 2) * (kKeys * 128) + (i & 3) * 32) >> 4;  // in the descriptors' 16 bytes
+          umma_bf16_ss(d, q + off, k + off, idesc_s, i > 0 ? 1u : 0u);
+        }
+        umma_commit(bar(S::kSFull + t % S::kBufs));
+        umma_commit(bar(S::kEmpty + c % S::kSlots));
+        ++c;
+        if (--left == 0) umma_commit(bar(S::kQEmpty + (iu & 1)));
+        return true;
+      };
+      ok = scores(0);
+      for (uint32_t t = 0; ok && t < n; ++t) {
+        if (t + 1 < n && !(ok = scores(t + 1))) break;
+        if (!(ok = mbar_wait(bar(S::kPFull + t % S::kBufs), (t / S::kBufs) & 1, abort_flag))) break;
+        if (t > 0 && !(ok = mbar_wait(bar(S::kOEmpty + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag))) break;
+        if (!(ok = full())) break;
+        tc_fence_after();
+        const uint32_t p = tmem + t % S::kBufs * S::kBufCols;
+        const uint64_t v = umma_desc_sw128(sbase + S::kRing + (c % S::kSlots) * S::kTile, kKeys * 128, 1024);
+        // the smallest terms first: the unit cuts a sum off at the size that it has reached
+#pragma unroll 1
+        for (int x = S::kTerms - 1; x >= 0; --x)
+#pragma unroll
+          for (int i = 0; i < kKeys / 16; ++i) {
+            const uint32_t at = x == 2 ? 128 + i * 8 : (i >> 1) * 32 + x * 16 + (i & 1) * 8;
+            umma_bf16_ts(tmem + S::kOut, p + at, v + (i * 16 * 128 >> 4), idesc_o,
+                         x < S::kTerms - 1 || i > 0 ? 1u : 0u);
+          }
+        umma_commit(bar(S::kOFull));
+        umma_commit(bar(S::kEmpty + c % S::kSlots));
+        ++c;
+      }
+      // every product has ended before the block gives its tensor memory back
+      umma_commit(bar(S::kDrain));
+      int dummy = 0;
+      mbar_wait(bar(S::kDrain), 0, &dummy);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ weights: tile t by warps 4-7 (even) or 8-11, a row a thread
+    const int half = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    Walk walk(a, *first_group, lo, hi);
+    Unit u;
+    uint32_t t = 0;
+    while (ok && walk.next(u)) {
+      // the rows of the prefix that this thread's sequence sees, from lo on
+      const int at = u.m0 + row;
+      int from = 0x7fffffff;
+      if (at < u.rows) {
+        const int len = valid_len(a, a.lens[u.first + at / a.g]);
+        if (len >= u.prefix) from = first_row(a, len) - u.lo;
+      }
+      float m = -INFINITY;
+#pragma unroll 1
+      for (int i = u.t0; i < u.t1; ++i, ++t) {
+        if ((t & 1) != static_cast<uint32_t>(half)) continue;
+        const int buf = t % S::kBufs;
+        const uint32_t s = tmem + lanes + buf * S::kBufCols;
+        if (!(ok = wait_warp(bar(S::kSFull + buf), (t / S::kBufs) & 1))) break;
+        tc_fence_after();
+        const int c_lo = from - i * kKeys, c_hi = u.prefix - u.lo - i * kKeys;  // columns [c_lo, c_hi) are seen
+        const bool whole = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kKeys);
+        auto mask = [&](float (&x)[32], int base) {
+          if (whole) return;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (base + j < c_lo || base + j >= c_hi) x[j] = -INFINITY;
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t r[32];
+          tmem_ld_32x32b<32>(s + b * 32, r);
+          tmem_wait_ld();
+          float(&x)[32] = reinterpret_cast<float(&)[32]>(r);
+          mask(x, b * 32);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) top = fmax3(top, x[j], x[j + 1]);
+        }
+        m = fmaxf(m, top * a.scale_log2);
+        const float ref = m == -INFINITY ? 0.0f : m;
+        const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2), ref2 = f32x2(-ref, -ref);
+        uint64_t sum2 = f32x2(0.0f, 0.0f);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t r[32], terms[32], low[16];
+          tmem_ld_32x32b<32>(s + b * 32, r);
+          tmem_wait_ld();
+          float(&x)[32] = reinterpret_cast<float(&)[32]>(r);
+          mask(x, b * 32);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float p0, p1;
+            f32x2_split(fma_f32x2(f32x2(x[j], x[j + 1]), scale2, ref2), p0, p1);
+            p0 = ex2_approx(p0), p1 = ex2_approx(p1);
+            sum2 = add_f32x2(sum2, f32x2(p0, p1));
+            const uint32_t h = pack_bf16x2(p0, p1);
+            p0 -= bf16lo_to_f32(h), p1 -= bf16hi_to_f32(h);
+            const uint32_t mid = pack_bf16x2(p0, p1);
+            terms[j / 2] = h, terms[16 + j / 2] = mid;
+            if (F32) low[j / 2] = pack_bf16x2(p0 - bf16lo_to_f32(mid), p1 - bf16hi_to_f32(mid));
+          }
+          tmem_st_32x32b<32>(s + b * 32, terms);
+          if (F32) tmem_st_32x32b<16>(s + 128 + b * 16, low);
+        }
+        float s0, s1;
+        f32x2_split(sum2, s0, s1);
+        // the sums of tile t - 2 have been taken: its place here is free
+        if (t >= 2 && !(ok = wait_warp(bar(S::kOEmpty + (t & 1)), ((t >> 1) - 1) & 1))) break;
+        stats[(t & 1) * kRows + row] = make_float2(m, s0 + s1);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::kPFull + buf));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ sums: a row a thread, every tile's products added in registers
+    registers_up<kSumRegs>();
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    Walk walk(a, *first_group, lo, hi);
+    Unit u;
+    uint32_t t = 0;
+    while (ok && walk.next(u)) {
+      float acc[DH], m = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int j = 0; j < DH; ++j) acc[j] = 0.0f;
+#pragma unroll 1
+      for (int i = u.t0; i < u.t1; ++i, ++t) {
+        const int buf = t % S::kBufs;
+        if (!(ok = wait_warp(bar(S::kPFull + buf), (t / S::kBufs) & 1))) break;
+        if (!(ok = wait_warp(bar(S::kOFull), t & 1))) break;
+        tc_fence_after();
+        const float2 st = stats[(t & 1) * kRows + row];
+        const float top = fmaxf(m, st.x);
+        const float old = m == -INFINITY ? 0.0f : ex2_approx(m - top), now = st.x == -INFINITY ? 0.0f : ex2_approx(st.x - top);
+        m = top;
+        l = fmaf(l, old, st.y * now);
+        if (__any_sync(0xffffffffu, old != 1.0f)) {
+#pragma unroll
+          for (int j = 0; j < DH; ++j) acc[j] *= old;
+        }
+#pragma unroll
+        for (int b = 0; b < DH / 16; ++b) {
+          uint32_t r[16];
+          tmem_ld_32x32b<16>(tmem + lanes + S::kOut + b * 16, r);
+          tmem_wait_ld();
+          if (b == DH / 16 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(S::kOEmpty + (t & 1)));
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[b * 16 + j] = fmaf(__uint_as_float(r[j]), now, acc[b * 16 + j]);
+        }
+      }
+      if (!ok) break;
+      const int at = u.m0 + row;
+      if (at < u.rows) {
+        const int s = at / a.g;
+        const int64_t head_at = static_cast<int64_t>(u.first + s) * a.hq + u.kvh * a.g + at - s * a.g;
+        const bool from_start = u.t0 == 0, whole = from_start && u.t1 == u.n;
+        const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (from_start ? 1 : 0)) * kRows + row;
+        float* o = whole ? a.pre_o + head_at * DH : a.part_o + slot * DH;
+        *reinterpret_cast<float2*>(whole ? a.pre_ml + head_at * 2 : a.part_ml + slot * 2) = make_float2(m, l);
+        if (from_start) a.where[head_at] = whole ? make_int2(-1, 0) : make_int2(static_cast<int>(blockIdx.x), ranges.owner(u.start + u.n - 1) | row << 16);
+#pragma unroll
+        for (int j = 0; j < DH; j += 4) *reinterpret_cast<float4*>(o + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+      }
+    }
+  }
+  if (!ok && lane == 0 && a.err) atomicOr(a.err, kErrTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) tmem_dealloc(tmem, 512);
+}
+
+// Joins a head's parts, the prefix's and its own rows', and stores it; a warp a head.
 template <int DH, bool F32>
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ SharedArgs a) {
   constexpr int C = DH / 32;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (row >= static_cast<int64_t>(a.num_reqs) * a.hq) return;
   grid_dependency_wait();
-  const int r = static_cast<int>(row / a.hq), len = valid_len(a, a.lens[r]);
-  float o[C], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int x = 0; x < C; ++x) o[x] = 0.0f;
-  if (len > a.own[r]) {
-    m = a.own_ml[row * 2], l = a.own_ml[row * 2 + 1];
-#pragma unroll
-    for (int x = 0; x < C; ++x) o[x] = a.own_o[row * DH + lane * C + x];
+  if (row >= static_cast<int64_t>(a.num_reqs) * a.hq) return;
+  const int r = static_cast<int>(row / a.hq), len = valid_len(a, a.lens[r]), own = a.own[r], first = first_row(a, len);
+  const bool has_own = len > max(own, first), has_prefix = own > first;
+  int parts = 0;
+  int2 where = make_int2(-1, 0);
+  if (has_prefix) {
+    where = a.where[row];
+    parts = where.x < 0 ? 1 : (where.y & 0xffff) - where.x + 1;
   }
+  const int slot_row = where.y >> 16;
+  float o[C], m, l;
+  merge_parts<DH>(parts + has_own, 0, 1, [&](int p) {
+    if (p == parts) return Part{a.own_o + row * DH, a.own_ml + row * 2};
+    if (where.x < 0) return Part{a.pre_o + row * DH, a.pre_ml + row * 2};
+    const int64_t at = (2 * static_cast<int64_t>(where.x + p) + (p == 0 ? 1 : 0)) * kRows + slot_row;
+    return Part{a.part_o + at * DH, a.part_ml + at * 2};
+  }, o, m, l);
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-  for (int x = 0; x < C; ++x) {
-    if (F32) static_cast<float*>(a.out)[row * DH + lane * C + x] = o[x] * inv;
-    else static_cast<uint16_t*>(a.out)[row * DH + lane * C + x] = static_cast<uint16_t>(pack_bf16x2(o[x] * inv, 0.0f));
+  if (F32) {
+    store_row<DH>(static_cast<float*>(a.out) + row * DH, o, inv);
+  } else {
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + row * DH;
+    if constexpr (C == 4)
+      *reinterpret_cast<uint2*>(dst + lane * 4) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst + lane * 2) = pack_bf16x2(o[0] * inv, o[1] * inv);
   }
   if (a.lse && lane == 0) a.lse[row] = l > 0.0f ? (m + __log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
 
 struct SharedLayout {
-  size_t header, groups, seen, own, own_ml, own_o, rows, total;
+  size_t header, groups, least, own, own_ml, own_o, where, pre_ml, pre_o, part_ml, part_o, rows, total;
 };
 
 SharedLayout shared_layout(int num_reqs, int num_groups, int hq, int hkv, int dh, int max_ctx_len, int window, int sms) {
@@ -187,11 +671,16 @@ SharedLayout shared_layout(int num_reqs, int num_groups, int hq, int hkv, int dh
   const size_t heads = static_cast<size_t>(num_reqs) * hq;
   y.header = 0;
   y.groups = y.header + 256;
-  y.seen = y.groups + up(num_groups * sizeof(SharedGroup));
-  y.own = y.seen + up(num_groups * 2 * sizeof(int32_t));
+  y.least = y.groups + up(num_groups * sizeof(SharedGroup));
+  y.own = y.least + up(num_groups * sizeof(unsigned long long));
   y.own_ml = y.own + up(num_reqs * sizeof(int32_t));
   y.own_o = y.own_ml + up(heads * 2 * sizeof(float));
-  y.rows = y.own_o + up(heads * dh * sizeof(float));
+  y.where = y.own_o + up(heads * dh * sizeof(float));
+  y.pre_ml = y.where + up(heads * sizeof(int2));
+  y.pre_o = y.pre_ml + up(heads * 2 * sizeof(float));
+  y.part_ml = y.pre_o + up(heads * dh * sizeof(float));
+  y.part_o = y.part_ml + up(static_cast<size_t>(sms) * 2 * kRows * 2 * sizeof(float));
+  y.rows = y.part_o + up(static_cast<size_t>(sms) * 2 * kRows * dh * sizeof(float));
   y.total = y.rows + own_rows_workspace(num_reqs, hq, hkv, dh, max_ctx_len, window, sms);
   return y;
 }
@@ -205,6 +694,14 @@ cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, int bytes, cudaS
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr, cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int DH, bool F32>
+cudaError_t launch_prefix(const SharedArgs& a, int sms, cudaStream_t st) {
+  constexpr int kBytes = Shape<DH, F32>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<DH, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_after(prefix_kernel<DH, F32>, dim3(static_cast<unsigned>(sms)), kThreads, kBytes, st, a);
 }
 
 }  // namespace
@@ -251,20 +748,28 @@ int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const
   a.num_pages = num_pages, a.page = page_size, a.scale_log2 = scale_log2_of(c);
   divide_by_page(page_size, &a.page_mul, &a.page_shift);
   a.header = reinterpret_cast<Header*>(ws + y.header), a.groups = reinterpret_cast<SharedGroup*>(ws + y.groups);
-  a.seen = reinterpret_cast<int32_t*>(ws + y.seen);
+  a.least = reinterpret_cast<unsigned long long*>(ws + y.least);
   a.lens = seq_lens, a.starts = group_start_loc, a.prefixes = prefix_lens, a.err = reinterpret_cast<uint32_t*>(status);
   a.own = reinterpret_cast<int32_t*>(ws + y.own);
   a.own_ml = reinterpret_cast<float*>(ws + y.own_ml), a.own_o = reinterpret_cast<float*>(ws + y.own_o);
+  a.where = reinterpret_cast<int2*>(ws + y.where);
+  a.pre_ml = reinterpret_cast<float*>(ws + y.pre_ml), a.pre_o = reinterpret_cast<float*>(ws + y.pre_o);
+  a.part_ml = reinterpret_cast<float*>(ws + y.part_ml), a.part_o = reinterpret_cast<float*>(ws + y.part_o);
   a.out = out, a.lse = lse;
   a.num_reqs = num_reqs, a.num_groups = num_groups, a.hq = hq, a.hkv = hkv, a.g = hq / hkv;
   a.max_len = max_ctx_len, a.window = window;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  plan_kernel<<<1, 1024, 0, st>>>(a);
+  plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_own_rows(c, a.own, a.own_o, a.own_ml, ws + y.rows, sms, false, st);
+  const bool f32 = out_dtype == DFLASH_OUT_F32;
+  if (e == cudaSuccess) {
+    if (dh == 128) e = f32 ? launch_prefix<128, true>(a, sms, st) : launch_prefix<128, false>(a, sms, st);
+    else e = f32 ? launch_prefix<64, true>(a, sms, st) : launch_prefix<64, false>(a, sms, st);
+  }
+  if (e == cudaSuccess) e = launch_own_rows(c, a.own, a.own_o, a.own_ml, ws + y.rows, sms, true, st);
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(num_reqs) * hq + 7) / 8));
-  auto finish = dh == 128 ? (out_dtype == DFLASH_OUT_F32 ? finish_kernel<128, true> : finish_kernel<128, false>)
-                          : (out_dtype == DFLASH_OUT_F32 ? finish_kernel<64, true> : finish_kernel<64, false>);
+  auto finish = dh == 128 ? (f32 ? finish_kernel<128, true> : finish_kernel<128, false>)
+                          : (f32 ? finish_kernel<64, true> : finish_kernel<64, false>);
   if (e == cudaSuccess) e = launch_after(finish, grid, 256, 0, st, a);
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "shared attention launch: %s", cudaGetErrorString(e));
   return report_error(DFLASH_OK, "");
