@@ -1373,7 +1373,7 @@ static bool encode_rows_map(CUtensorMap* m, const void* base, int dh, int heads,
 // 8 rows, 2 column blocks, rows / 8 groups, heads} (strides: row 2 KB-ish, column block 128 B,
 // group 8 rows, head dh * 2), box {64, 8, 2, page_size / 8, 1}: one box lands as the page's
 // 8-row groups, each as its two column blocks one after the other.
-static bool encode_group_major_map(CUtensorMap* m, const void* base, int dh, int heads, int64_t rows, int page_size) {
+bool encode_group_major_map(CUtensorMap* m, const void* base, int dh, int heads, int64_t rows, int page_size) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   const cuuint64_t row_bytes = static_cast<cuuint64_t>(dh) * heads * 2;

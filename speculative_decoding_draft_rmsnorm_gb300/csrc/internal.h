@@ -133,6 +133,10 @@ WorkspacePlan plan_workspace(int num_reqs, int64_t total_q, int hq, int hkv, int
 
 cudaError_t launch_attention(const AttnHost& h, cudaStream_t stream, char* msg, size_t msg_len);
 
+// Tensor map of a pool [rows, heads, dh] of bf16 whose boxes are page_size rows of one head, landing in 8-row groups of
+// dh / 64 blocks of 64 columns: coordinates (0, 0, 0, first row / 8, head).
+bool encode_group_major_map(CUtensorMap* m, const void* base, int dh, int heads, int64_t rows, int page_size);
+
 // Records `msg` as the thread's last error (what dflash_last_error returns) and returns code.
 int report_error(int code, const char* msg);
 

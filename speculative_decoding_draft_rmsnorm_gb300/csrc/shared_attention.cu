@@ -26,9 +26,9 @@ constexpr int kLeastPrefix = 64;
 // A group that shares: `n` tiles of rows [lo, prefix) for each of hkv x tiles_m units, from tile `start` of the call on.
 struct SharedGroup {
   int first, rows;  // its first sequence; sequences x heads of a kv head
-  int prefix, lo;
+  int prefix, lo;   // lo: where the tiles begin, the start of a box
   int leader;       // the shortest sequence that shares: its pages are read
-  int tiles_m, n;
+  int tiles_m, n;   // tiles_m = rows / kRows, up
   uint32_t start;
 };
 struct Header {
@@ -37,6 +37,8 @@ struct Header {
 };
 
 struct SharedArgs {
+  CUtensorMap k_map, v_map;  // boxes of `box` rows of a head
+  int box, box_shift;        // rows of a box, 1 << box_shift; or 0: pages that are no multiple of 8 rows
   const uint16_t* q;
   int64_t q_tok;
   const uint16_t* k;
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const int members = a.starts[g + 1] - x.first;
       x.prefix = shared_rows(g, members);
       const unsigned long long least = *static_cast<volatile unsigned long long*>(&a.least[g]);
-      x.lo = first_row(a, static_cast<int>(least >> 32)), x.leader = static_cast<int>(least & 0xffffffffu);
+      x.lo = first_row(a, static_cast<int>(least >> 32)) & -max(a.box, 1), x.leader = static_cast<int>(least & 0xffffffffu);
       x.rows = members * a.g;
       x.tiles_m = (x.rows + kRows - 1) / kRows;
       if (least != ~0ull && x.lo < x.prefix) {
@@ -180,53 +182,60 @@ struct Unit {
   uint32_t start;  // its tile 0
 };
 
+// Where a block's tiles begin.
+struct First {
+  int group, kvh, m0, t;
+};
+
 // A block's units, one after the other. Every role walks them for itself.
 struct Walk {
   const SharedGroup* groups;
   uint32_t x, hi;
-  int at, hkv;
+  int hkv, kvh, m0, t;  // the next unit and its first tile here
   SharedGroup g;
-  __device__ __forceinline__ Walk(const SharedArgs& a, int first, uint32_t lo, uint32_t hi_) : groups(a.groups), x(lo), hi(hi_), at(first), hkv(a.hkv) {
-    g = groups[at];
+  __device__ __forceinline__ Walk(const SharedArgs& a, const First& f, uint32_t lo, uint32_t hi_)
+      : groups(a.groups + f.group), x(lo), hi(hi_), hkv(a.hkv), kvh(f.kvh), m0(f.m0), t(f.t) {
+    g = *groups;
   }
   __device__ __forceinline__ bool next(Unit& u) {
     if (x >= hi) return false;
-    if (x - g.start >= static_cast<uint32_t>(g.n) * g.tiles_m * hkv) g = groups[++at];
-    const uint32_t rel = x - g.start, unit = rel / static_cast<uint32_t>(g.n);
+    if (kvh == hkv) kvh = 0, g = *++groups;
     u.first = g.first, u.rows = g.rows, u.prefix = g.prefix, u.lo = g.lo, u.leader = g.leader, u.n = g.n;
-    u.kvh = static_cast<int>(unit) / g.tiles_m;
-    u.m0 = (static_cast<int>(unit) - u.kvh * g.tiles_m) * kRows;
-    u.t0 = static_cast<int>(rel - unit * g.n);
-    u.t1 = static_cast<int>(min(static_cast<uint32_t>(u.n), u.t0 + (hi - x)));
-    u.start = x - u.t0;
-    x += u.t1 - u.t0;
+    u.kvh = kvh, u.m0 = m0, u.t0 = t;
+    u.t1 = static_cast<int>(min(static_cast<uint32_t>(u.n), t + (hi - x)));
+    u.start = x - t;
+    x += u.t1 - t;
+    t = 0, m0 += kRows;
+    if (m0 >= g.rows) m0 = 0, ++kvh;
     return true;
   }
 };
 
-// Warps 0 and 1 copy, 3 issues products, 4-7 and 8-11 make weights, 12-15 add the sums up.
-constexpr int kProducers = 2, kMine = kRows / kProducers / 32, kIssuer = 3;
+// Warps 0, 1 and 2 copy K, V and Q, 3 issues products, 4-7 and 8-11 make weights, 12-15 add the sums up.
+constexpr int kIssuer = 3;
 constexpr int kThreads = 16 * 32;
 // Registers of a thread in the three kinds of warpgroups: together at most what the block is launched with, 4 x 128.
 constexpr int kCopyRegs = 80, kSumRegs = 176;
 static_assert(kCopyRegs + 2 * 128 + kSumRegs <= 4 * 128, "the block's registers");
 
-// Shared memory: two Q tiles and a ring of K and V tiles, in 64-column blocks of 128 rows x 128 bytes (128-byte
-// swizzle). Tensor memory: kBufs buffers of scores, whose columns the weights take (a chunk of 32 rows' scores
-// becomes its 16 columns of high and 16 of middle terms; low terms lie behind the 128), and a tile's P V.
+// Shared memory: two Q tiles and a ring of K and V tiles, each in 8-row groups of DH / 64 blocks of 8 rows x 128 bytes
+// (128-byte swizzle): as a box of a page lands. Tensor memory: kBufs buffers of scores, whose columns the weights take (16 rows'
+// scores become 8 columns of high and 8 of middle terms; low terms lie behind the 128), and a tile's P V.
 template <int DH, bool F32>
 struct Shape {
   static constexpr int kTile = kKeys * DH * 2;
+  static constexpr int kGroup = 8 * DH * 2;  // bytes of 8 rows
   static constexpr int kSlots = DH == 128 ? 5 : 10;
-  static constexpr int kAhead = kSlots - 2;
+  static constexpr int kByRow = DH == 128 ? 2 : 4;  // stages of K, and of V, that are copied row by row at once
   static constexpr int kTerms = F32 ? 3 : 2;
   static constexpr int kBufs = F32 ? 2 : 3;
+  static constexpr int kLead = kBufs - 1;  // tiles whose scores come before a tile's sums
   static constexpr int kBufCols = F32 ? 192 : 128;
   static constexpr int kOut = 384;
   static constexpr int kRing = 2 * kTile;
   static constexpr int kStats = kRing + kSlots * kTile;
   static constexpr int kBars = kStats + 2 * kRows * 8;
-  static constexpr int kFull = 0, kEmpty = kSlots, kQEmpty = 2 * kSlots, kSFull = kQEmpty + 2, kPFull = kSFull + 3, kOFull = kPFull + 3,
+  static constexpr int kFull = 0, kEmpty = kSlots, kQFull = 2 * kSlots, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 3, kOFull = kPFull + 3,
                        kOEmpty = kOFull + 1, kDrain = kOEmpty + 2, kNumBars = kDrain + 1;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kBytes = kMisc + 32;
@@ -262,13 +271,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   auto bar = [&](int i) { return sbase + S::kBars + 8u * static_cast<uint32_t>(i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
-  int* first_group = reinterpret_cast<int*>(smem + S::kMisc + 8);
+  First* first = reinterpret_cast<First*>(smem + S::kMisc + 16);
   float2* stats = reinterpret_cast<float2*>(smem + S::kStats);  // [2][kRows]: a tile's reference and weight
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < S::kSlots; ++i) mbar_init(bar(S::kFull + i), kProducers), mbar_init(bar(S::kEmpty + i), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(S::kQEmpty + i), 1), mbar_init(bar(S::kOEmpty + i), 4);
+    for (int i = 0; i < S::kSlots; ++i) mbar_init(bar(S::kFull + i), 1), mbar_init(bar(S::kEmpty + i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(S::kQFull + i), 1), mbar_init(bar(S::kQEmpty + i), 1), mbar_init(bar(S::kOEmpty + i), 4);
     for (int i = 0; i < 3; ++i) mbar_init(bar(S::kSFull + i), 1), mbar_init(bar(S::kPFull + i), 4);
     mbar_init(bar(S::kOFull), 1), mbar_init(bar(S::kDrain), 1);
     *abort_flag = 0;
@@ -289,204 +298,256 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       const int k = 31 - __clz(le);
       from += k * step, n = min(step, n - k * step);
     }
-    if (lane == 0) *first_group = from;
+    if (lane == 0) {
+      const SharedGroup g = a.groups[from];
+      const uint32_t rel = lo - g.start, unit = rel / static_cast<uint32_t>(g.n), kvh = unit / static_cast<uint32_t>(g.tiles_m);
+      *first = First{from, static_cast<int>(kvh), static_cast<int>(unit - kvh * g.tiles_m) * kRows, static_cast<int>(rel - unit * g.n)};
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto wait_warp = [&](uint32_t b, uint32_t parity) -> bool {
-    int r = 1;
-    if (lane == 0) r = mbar_wait(b, parity, abort_flag) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, r, 0) != 0;
+  auto wait = [&](uint32_t b, uint32_t parity) -> bool {  // by all lanes or by one; bounded like mbar_wait, in less code
+    uint64_t t0 = 0;
+    for (uint32_t i = 0; !mbar_try_wait(b, parity); ++i) {
+      if ((i & 255) != 255) continue;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort_flag || now - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        return false;
+      }
+    }
+    return true;
   };
+  auto wait_warp = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
   bool ok = true;
   if (warp < 4) registers_down<kCopyRegs>();
 
   if (lo >= hi) {
     // no tiles
-  } else if (warp < kProducers) {
-    // ------------------------------------------------------------ copies: warp w has rows 64 w .. of every tile
-    // Stages in the order in which products take them: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
+  } else if (warp < kIssuer) {
+    // ------------------------------------------------------------ copies
     constexpr int kPieces = DH / 8, kAtOnce = 32 / kPieces;  // 16-byte pieces of a row; rows of an instruction
-    const int64_t row_bytes = static_cast<int64_t>(a.hkv) * DH * 2;
-    const uint64_t policy = l2_policy_evict_first();
     const int piece = lane % kPieces, sub = lane / kPieces;
-    // row r's piece p lies in block p / 8, at piece (p % 8) ^ (r % 8) of the row's 128 bytes
-    const uint32_t dst_lane = sbase + (piece / 8) * (kKeys * 128) + (warp * 32 * kMine + sub) * 128;
+    // row r's piece p lies in group r / 8, block p / 8, at piece (p % 8) ^ (r % 8) of the row's 128 bytes
+    const uint32_t dst_lane = sbase + (piece / 8) * 1024 + sub * 128;
     const int swz = (piece % 8) ^ sub;
-    uint32_t c = 0, told = 0;  // stages so far; those that the products know of
-    auto tell = [&](uint32_t upto) {  // stages below it have landed
-      if (told >= upto) return;
-      fence_proxy_async_smem();
-      __syncwarp();
-      for (; told < upto; ++told)
-        if (lane == 0) mbar_arrive(bar(S::kFull + told % S::kSlots));
+    const uint64_t once = l2_policy_evict_first(), often = l2_policy_evict_normal();
+    uint64_t policy = once;
+    auto copy = [&](const void* src, bool have, uint32_t off, int r) {  // kAtOnce rows from row r of the tile at off on
+      cp_async16(dst_lane + off + (r >> 3) * S::kGroup + (r & 7) * 128 + ((swz ^ (r & 7)) << 4), src, have ? 16 : 0, policy);
     };
-    auto open_stage = [&]() -> bool {
-      if (c > S::kAhead) {
-        cp_async_wait<S::kAhead>();
-        tell(c - S::kAhead);
-      }
-      return c < S::kSlots || wait_warp(bar(S::kEmpty + c % S::kSlots), (c / S::kSlots - 1) & 1);
-    };
-    // kAtOnce rows from row i kAtOnce of this warp's on
-    auto copy = [&](const void* src, bool have, uint32_t off, int i) {
-      cp_async16(dst_lane + off + i * kAtOnce * 128 + ((swz ^ (i * kAtOnce & 7)) << 4), src, have ? 16 : 0, policy);
-    };
-    auto copy_rows = [&](const char* base, const int (&row)[kMine], int head_bytes, uint32_t off) {  // rows of the lanes; -1: zeros
-      const char* src = base + head_bytes + piece * 16;
-#pragma unroll
-      for (int y = 0; y < kMine; ++y)
-#pragma unroll 8
-        for (int i = 0; i < 32 / kAtOnce; ++i) {
-          const int x = __shfl_sync(0xffffffffu, row[y], i * kAtOnce + sub);
-          copy(src + max(x, 0) * row_bytes, x >= 0, off, y * (32 / kAtOnce) + i);
-        }
-    };
-    Walk walk(a, *first_group, lo, hi);
+    Walk walk(a, *first, lo, hi);
     Unit u;
-    int t = 0, end = 0, iu = -1;  // the tile looked up next; its unit's end
-    int id[kMine], key[kMine];    // its pages and rows
-    bool fresh = false;           // it begins a unit
-    auto look_up = [&]() -> bool {
-      fresh = t >= end;
-      if (fresh) {
-        if (!walk.next(u)) return false;
-        t = u.t0, end = u.t1;
-      }
-#pragma unroll
-      for (int y = 0; y < kMine; ++y) {
-        key[y] = u.lo + t * kKeys + (warp * kMine + y) * 32 + lane;
-        if (key[y] < u.prefix) id[y] = a.table[u.leader * a.table_stride + page_of(a, key[y])];
-        else key[y] = -1;
-      }
-      ++t;
-      return true;
-    };
-    bool have = look_up();
-    int v_row[kMine], v_head = 0;
-    for (bool more = false; ok && (have || more);) {
-      int row[kMine], head_bytes = 0;
-      const bool now = have;
-      if (now) {
-        head_bytes = u.kvh * (DH * 2);
-#pragma unroll
-        for (int y = 0; y < kMine; ++y) {
-          row[y] = -1;
-          if (key[y] < 0) continue;
-          if (id[y] < 0 || id[y] >= a.num_pages) {
-            if (a.err) atomicOr(a.err, kErrMetadata);
-            id[y] = 0;
-          }
-          row[y] = id[y] * a.page + (key[y] - page_of(a, key[y]) * a.page);
+    if (warp == 2) {
+      // ---- Q, a unit's rows at a time
+      for (uint32_t iu = 0; walk.next(u); ++iu) {
+        if (iu >= 2 && !(ok = wait_warp(bar(S::kQEmpty + (iu & 1)), ((iu >> 1) - 1) & 1))) break;
+#pragma unroll 2
+        for (int r = 0; r < kRows; r += kAtOnce) {
+          const int at = u.m0 + r + sub, s = at / a.g;
+          copy(a.q + (at < u.rows ? (u.first + s) * a.q_tok + static_cast<int64_t>(u.kvh * a.g + at - s * a.g) * DH : 0) + piece * 8, at < u.rows,
+               (iu & 1) * S::kTile, r);
         }
-        if (!(ok = open_stage())) break;
-        if (fresh) {  // Q, in its first K tile's stage
-          ++iu;
-          if (iu >= 2) {
-            const uint32_t b = bar(S::kQEmpty + (iu & 1)), parity = ((iu >> 1) - 1) & 1;
-            if (!__any_sync(0xffffffffu, lane == 0 && mbar_test_wait(b, parity))) {
-              // the products that free it may wait for stages that have landed untold
-              cp_async_wait<0>();
-              tell(c);
-              if (!(ok = wait_warp(b, parity))) break;
-            }
-          }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::kQFull + (iu & 1)));
+      }
+    } else {
+      // ---- K (warp 0) or V (warp 1). The ring has them in the order in which products take them: K of kLead tiles, then
+      // K and V in turn, then V of the last ones. A tile that is whole boxes of rows that some sequence sees goes by TMA; any other (its
+      // first and last rows, pages that are no multiple of 8 rows) row by row with cp.async, zeros where there is no row.
+      // A warp each: the TMA unit takes some 130 cycles a box, and what the one does between boxes the other fills.
+      const bool is_v = warp == 1;
+      const char* base = reinterpret_cast<const char*>(is_v ? a.v : a.k) + piece * 16;
+      const CUtensorMap* map = is_v ? &a.v_map : &a.k_map;
+      const int64_t row_bytes = static_cast<int64_t>(a.hkv) * DH * 2;
+      const uint32_t box_bytes = (S::kGroup / 8) << a.box_shift, n = hi - lo;
+      int t = 0, end = 0;         // the tile looked up next; its unit's end
+      int id[4], key[4];          // its rows, and their pages: lane + 32 y, or the first of box `lane`
+      int see = 0, boxes = 0;     // the unit's first row that is seen; the tile's boxes, 0: row by row
+      auto look_up = [&]() {
+        if (t >= end) {
+          if (!walk.next(u)) return;
+          t = u.t0, end = u.t1;
+          see = first_row(a, valid_len(a, a.lens[u.leader]));
+        }
+        const int from = u.lo + t * kKeys, rows = min(kKeys, u.prefix - from);
+        const int32_t* pages = a.table + u.leader * a.table_stride;
+        boxes = a.box && from >= see && (rows & (max(16, a.box) - 1)) == 0 ? rows >> a.box_shift : 0;
+        if (boxes) {
+          key[0] = from + (min(lane, boxes - 1) << a.box_shift);
+          id[0] = pages[page_of(a, key[0])];
+        } else {
 #pragma unroll
-          for (int y = 0; y < kMine; ++y) {
-            const int at = u.m0 + (warp * kMine + y) * 32 + lane, s = at / a.g;
-            const int64_t mine = at < u.rows ? (u.first + s) * a.q_tok + static_cast<int64_t>(u.kvh * a.g + at - s * a.g) * DH : -1;
+          for (int y = 0; y < 4; ++y) {
+            key[y] = from + y * 32 + lane;
+            if (key[y] >= see && key[y] < u.prefix) id[y] = pages[page_of(a, key[y])];
+            else key[y] = -1;
+          }
+        }
+        ++t;
+      };
+      auto row_of = [&](int y) {
+        if (id[y] < 0 || id[y] >= a.num_pages) {
+          if (a.err) atomicOr(a.err, kErrMetadata);
+          id[y] = 0;
+        }
+        return id[y] * a.page + (key[y] - page_of(a, key[y]) * a.page);
+      };
+      uint32_t untold = 0, slots = 0;  // stages copied row by row that products do not know of; their slots, 4 bits each
+      auto tell = [&](uint32_t but) {  // they have landed, but for the last
+        fence_proxy_async_smem();
+        __syncwarp();
+        for (; untold > but; --untold, slots >>= 4)
+          if (lane == 0) mbar_arrive(bar(S::kFull + (slots & 15)));
+      };
+      uint32_t by_tma = 0, parities = 0;  // slots that this warp filled by TMA; the parity of the last time
+      look_up();
+#pragma unroll 1
+      for (uint32_t i = 0; i < n; ++i) {
+        const uint32_t c = is_v ? min(2 * i + S::kLead + 1, n + i) : (i < S::kLead ? i : 2 * i - S::kLead), slot = c % S::kSlots;
+        const int now = boxes, kvh = u.kvh;
+        int row[4];
+        row[0] = key[0] < 0 ? -1 : row_of(0);
+        if (!now) {
+#pragma unroll
+          for (int y = 1; y < 4; ++y) row[y] = key[y] < 0 ? -1 : row_of(y);
+        }
+        policy = u.rows > kRows ? often : once;
+        look_up();  // the next tile's pages are on their way meanwhile
+        if (c >= S::kSlots) {
+          const uint32_t b = bar(S::kEmpty + slot), parity = (c / S::kSlots - 1) & 1;
+          if (untold && !__any_sync(0xffffffffu, lane == 0 && mbar_test_wait(b, parity))) {
+            // the products that empty it may wait for stages that have landed untold
+            cp_async_wait<0>();
+            tell(0);
+          }
+          if (!(ok = wait_warp(b, parity))) break;
+        }
+        const uint32_t off = S::kRing + slot * S::kTile, b = bar(S::kFull + slot);
+        if (now) {
+          by_tma |= 1u << slot, parities = (parities & ~(1u << slot)) | (c / S::kSlots & 1) << slot;
+          if (lane == 0) mbar_arrive_expect_tx(b, now * box_bytes);
+          uint32_t dst = sbase + off;
+#pragma unroll 1
+          for (int j = 0; j < now; j += 4, dst += 4 * box_bytes) {  // issued by one lane
+            int at[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) at[x] = __shfl_sync(0xffffffffu, row[0] >> 3, j + x);
+            if (lane == 0) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (j + x < now) tma_load_5d_hint(dst + x * box_bytes, map, b, 0, 0, 0, at[x], kvh, policy);
+            }
+            __syncwarp();
+          }
+        } else {
+          if (untold == S::kByRow) {
+            cp_async_wait<S::kByRow - 1>();
+            tell(S::kByRow - 1);
+          }
+          const char* src = base + kvh * (DH * 2);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
 #pragma unroll 4
-            for (int i = 0; i < 32 / kAtOnce; ++i) {
-              const int64_t x = __shfl_sync(0xffffffffu, mine, i * kAtOnce + sub);
-              copy(a.q + (x < 0 ? 0 : x) + piece * 8, x >= 0, (iu & 1) * S::kTile, y * (32 / kAtOnce) + i);
+            for (int r = 0; r < 32; r += kAtOnce) {
+              const int x = __shfl_sync(0xffffffffu, row[y], r + sub);
+              copy(src + max(x, 0) * row_bytes, x >= 0, off, y * 32 + r);
             }
-          }
+          cp_async_commit();
+          slots |= slot << (4 * untold++);
         }
-        copy_rows(reinterpret_cast<const char*>(a.k), row, head_bytes, S::kRing + (c % S::kSlots) * S::kTile);
-        cp_async_commit();
-        ++c;
-        have = look_up();
       }
-      if (more) {  // V of the tile before
-        if (!(ok = open_stage())) break;
-        copy_rows(reinterpret_cast<const char*>(a.v), v_row, v_head, S::kRing + (c % S::kSlots) * S::kTile);
-        cp_async_commit();
-        ++c;
+      cp_async_wait<0>();
+      if (ok) {
+        tell(0);
+      } else if (lane == 0) {  // copies by TMA land before the block ends
+        for (int i = 0; i < S::kSlots; ++i) {
+          int dummy = 0;
+          if (by_tma >> i & 1) mbar_wait(bar(S::kFull + i), parities >> i & 1, &dummy);
+        }
       }
-      more = now, v_head = head_bytes;
-#pragma unroll
-      for (int y = 0; y < kMine; ++y) v_row[y] = row[y];
     }
-    cp_async_wait<0>();
-    if (ok) tell(c);
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      const uint32_t idesc_s = umma_idesc_bf16(kRows, kKeys, 0, 0), idesc_o = umma_idesc_bf16(kRows, DH, 0, 1);
-      const uint32_t n = hi - lo;
-      uint32_t c = 0;
-      Walk walk(a, *first_group, lo, hi);
-      Unit u;
-      int iu = -1;
-      uint32_t left = 0;  // tiles of the unit whose scores are to come
-      auto full = [&]() { return mbar_wait(bar(S::kFull + c % S::kSlots), (c / S::kSlots) & 1, abort_flag); };
-      auto scores = [&](uint32_t t) -> bool {
+    const uint32_t idesc_s = umma_idesc_bf16(kRows, kKeys, 0, 0), idesc_o = umma_idesc_bf16(kRows, DH, 0, 1);
+    const uint32_t n = hi - lo, by = elect_one();
+    Walk walk(a, *first, lo, hi);
+    Unit u;
+    int iu = -1;
+    uint32_t left = 0;  // tiles of the unit whose scores are to come
+    int steps[S::kLead + 1];  // rows / 16 of the tile whose sums come next, and of those behind it
+    uint32_t slot = 0, round = 0, t_buf = 0, w_buf = 0, w_round = 0;  // rings: where, and the parity there
+    auto next_slot = [&]() {
+      umma_commit_by(by, bar(S::kEmpty) + 8 * slot);
+      if (++slot == S::kSlots) slot = 0, round ^= 1;
+    };
+#pragma unroll 1
+    for (uint32_t t = 0; t < n + S::kLead; ++t) {  // the scores of tile t, then the sums of tile t - kLead
+#pragma unroll
+      for (int x = 0; x < S::kLead; ++x) steps[x] = steps[x + 1];
+      if (t < n) {
         if (left == 0) {
           walk.next(u);
           left = u.t1 - u.t0;
           ++iu;
+          if (!(ok = wait_warp(bar(S::kQFull + (iu & 1)), (iu >> 1) & 1))) break;
         }
-        // the buffer's weights have been used: with three buffers two tiles' sums came between
-        if (F32 && t >= 2 && !mbar_wait(bar(S::kOFull), (t - 2) & 1, abort_flag)) return false;
-        if (!full()) return false;
+        // what lies behind a tile's rows may be anything
+        steps[S::kLead] = (min(kKeys, u.prefix - u.lo - static_cast<int>(u.t1 - left) * kKeys) + 15) / 16;
+        // the buffer's weights have been used. (Its sums are still being taken: these scores are computed meanwhile.)
+        if (t >= S::kBufs && !(ok = wait_warp(bar(S::kOFull), (t - S::kBufs) & 1))) break;
+        if (!(ok = wait_warp(bar(S::kFull) + 8 * slot, round))) break;
         tc_fence_after();
-        const uint64_t q = umma_desc_sw128(sbase + (iu & 1) * S::kTile, 16, 1024), k = umma_desc_sw128(sbase + S::kRing + (c % S::kSlots) * S::kTile, 16, 1024);
-        const uint32_t d = tmem + t % S::kBufs * S::kBufCols;
+        const uint64_t q = umma_desc_sw128(sbase + (iu & 1) * S::kTile, 16, S::kGroup),
+                       k = umma_desc_sw128(sbase + S::kRing + slot * S::kTile, 16, S::kGroup);
 #pragma unroll
         for (int i = 0; i < DH / 16; ++i) {
-          const uint32_t off = ((i >> 2) * (kKeys * 128) + (i & 3) * 32) >> 4;  // in the descriptors' 16 bytes
-          umma_bf16_ss(d, q + off, k + off, idesc_s, i > 0 ? 1u : 0u);
+          const uint32_t off = ((i >> 2) * 1024 + (i & 3) * 32) >> 4;  // in the descriptors' 16 bytes
+          umma_bf16_ss_by(by, tmem + t_buf * S::kBufCols, q + off, k + off, idesc_s, i > 0 ? 1u : 0u);
         }
-        umma_commit(bar(S::kSFull + t % S::kBufs));
-        umma_commit(bar(S::kEmpty + c % S::kSlots));
-        ++c;
-        if (--left == 0) umma_commit(bar(S::kQEmpty + (iu & 1)));
-        return true;
-      };
-      ok = scores(0);
-      for (uint32_t t = 0; ok && t < n; ++t) {
-        if (t + 1 < n && !(ok = scores(t + 1))) break;
-        if (!(ok = mbar_wait(bar(S::kPFull + t % S::kBufs), (t / S::kBufs) & 1, abort_flag))) break;
-        if (t > 0 && !(ok = mbar_wait(bar(S::kOEmpty + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag))) break;
-        if (!(ok = full())) break;
-        tc_fence_after();
-        const uint32_t p = tmem + t % S::kBufs * S::kBufCols;
-        const uint64_t v = umma_desc_sw128(sbase + S::kRing + (c % S::kSlots) * S::kTile, kKeys * 128, 1024);
-        // the smallest terms first: the unit cuts a sum off at the size that it has reached
-#pragma unroll 1
-        for (int x = S::kTerms - 1; x >= 0; --x)
-#pragma unroll
-          for (int i = 0; i < kKeys / 16; ++i) {
-            const uint32_t at = x == 2 ? 128 + i * 8 : (i >> 1) * 32 + x * 16 + (i & 1) * 8;
-            umma_bf16_ts(tmem + S::kOut, p + at, v + (i * 16 * 128 >> 4), idesc_o,
-                         x < S::kTerms - 1 || i > 0 ? 1u : 0u);
-          }
-        umma_commit(bar(S::kOFull));
-        umma_commit(bar(S::kEmpty + c % S::kSlots));
-        ++c;
+        umma_commit_by(by, bar(S::kSFull) + 8 * t_buf);
+        next_slot();
+        if (++t_buf == S::kBufs) t_buf = 0;
+        if (--left == 0) umma_commit_by(by, bar(S::kQEmpty + (iu & 1)));
       }
-      // every product has ended before the block gives its tensor memory back
-      umma_commit(bar(S::kDrain));
+      if (t < S::kLead) continue;
+      const uint32_t w = t - S::kLead;
+      if (!(ok = wait_warp(bar(S::kPFull) + 8 * w_buf, w_round))) break;
+      if (w > 0 && !(ok = wait_warp(bar(S::kOEmpty + ((w - 1) & 1)), ((w - 1) >> 1) & 1))) break;
+      if (!(ok = wait_warp(bar(S::kFull) + 8 * slot, round))) break;
+      tc_fence_after();
+      const uint32_t p = tmem + w_buf * S::kBufCols;
+      const uint64_t v = umma_desc_sw128(sbase + S::kRing + slot * S::kTile, 1024, S::kGroup);
+      // the smallest terms first: the unit cuts a sum off at the size that it has reached
+#pragma unroll
+      for (int x = S::kTerms - 1; x >= 0; --x)
+#pragma unroll
+        for (int i = 0; i < kKeys / 16; ++i) {
+          const uint32_t at = x == 2 ? 128 + i * 8 : i * 16 + x * 8;
+          if (i < steps[0]) umma_bf16_ts_by(by, tmem + S::kOut, p + at, v + (i * 2 * S::kGroup >> 4), idesc_o, x < S::kTerms - 1 || i > 0 ? 1u : 0u);
+        }
+      umma_commit_by(by, bar(S::kOFull));
+      next_slot();
+      if (++w_buf == S::kBufs) w_buf = 0, w_round ^= 1;
+    }
+    // every product has ended before the block gives its tensor memory back
+    umma_commit_by(by, bar(S::kDrain));
+    if (lane == 0) {
       int dummy = 0;
       mbar_wait(bar(S::kDrain), 0, &dummy);
     }
+    __syncwarp();
   } else if (warp < 12) {
     // ------------------------------------------------------------ weights: tile t by warps 4-7 (even) or 8-11, a row a thread
     const int half = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    Walk walk(a, *first_group, lo, hi);
+    Walk walk(a, *first, lo, hi);
     Unit u;
     uint32_t t = 0;
     while (ok && walk.next(u)) {
@@ -507,48 +568,60 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         tc_fence_after();
         const int c_lo = from - i * kKeys, c_hi = u.prefix - u.lo - i * kKeys;  // columns [c_lo, c_hi) are seen
         const bool whole = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kKeys);
-        auto mask = [&](float (&x)[32], int base) {
+        // 16 columns at a time, the next ones on their way; first for the maximum, then for the weights
+        auto masked = [&](uint32_t (&r)[16], int b) {
           if (whole) return;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (base + j < c_lo || base + j >= c_hi) x[j] = -INFINITY;
+          for (int j = 0; j < 16; ++j)
+            if (b * 16 + j < c_lo || b * 16 + j >= c_hi) r[j] = 0xff800000u;
         };
         float top = -INFINITY;
+        auto highest = [&](uint32_t (&r)[16], int b) {
+          masked(r, b);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t r[32];
-          tmem_ld_32x32b<32>(s + b * 32, r);
+          for (int j = 0; j < 16; j += 2) top = fmax3(top, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+        };
+        uint32_t r0[16], r1[16];
+        tmem_ld_32x32b<16>(s, r0);
+#pragma unroll 1
+        for (int b = 0; b < 8; b += 2) {
           tmem_wait_ld();
-          float(&x)[32] = reinterpret_cast<float(&)[32]>(r);
-          mask(x, b * 32);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) top = fmax3(top, x[j], x[j + 1]);
+          tmem_ld_32x32b<16>(s + (b + 1) * 16, r1);
+          highest(r0, b);
+          tmem_wait_ld();
+          tmem_ld_32x32b<16>(s + (b + 2 & 7) * 16, r0);  // 0 again behind the last
+          highest(r1, b + 1);
         }
         m = fmaxf(m, top * a.scale_log2);
         const float ref = m == -INFINITY ? 0.0f : m;
         const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2), ref2 = f32x2(-ref, -ref);
         uint64_t sum2 = f32x2(0.0f, 0.0f);
+        auto weigh = [&](uint32_t (&r)[16], int b) {
+          masked(r, b);
+          uint32_t terms[16], low[8];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t r[32], terms[32], low[16];
-          tmem_ld_32x32b<32>(s + b * 32, r);
-          tmem_wait_ld();
-          float(&x)[32] = reinterpret_cast<float(&)[32]>(r);
-          mask(x, b * 32);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
+          for (int j = 0; j < 16; j += 2) {
             float p0, p1;
-            f32x2_split(fma_f32x2(f32x2(x[j], x[j + 1]), scale2, ref2), p0, p1);
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), scale2, ref2), p0, p1);
             p0 = ex2_approx(p0), p1 = ex2_approx(p1);
             sum2 = add_f32x2(sum2, f32x2(p0, p1));
             const uint32_t h = pack_bf16x2(p0, p1);
             p0 -= bf16lo_to_f32(h), p1 -= bf16hi_to_f32(h);
             const uint32_t mid = pack_bf16x2(p0, p1);
-            terms[j / 2] = h, terms[16 + j / 2] = mid;
+            terms[j / 2] = h, terms[8 + j / 2] = mid;
             if (F32) low[j / 2] = pack_bf16x2(p0 - bf16lo_to_f32(mid), p1 - bf16hi_to_f32(mid));
           }
-          tmem_st_32x32b<32>(s + b * 32, terms);
-          if (F32) tmem_st_32x32b<16>(s + 128 + b * 16, low);
+          tmem_st_32x32b<16>(s + b * 16, terms);
+          if (F32) tmem_st_32x32b<8>(s + 128 + b * 8, low);
+        };
+#pragma unroll 1
+        for (int b = 0; b < 8; b += 2) {
+          tmem_wait_ld();
+          tmem_ld_32x32b<16>(s + (b + 1) * 16, r1);
+          weigh(r0, b);
+          tmem_wait_ld();
+          if (b < 6) tmem_ld_32x32b<16>(s + (b + 2) * 16, r0);
+          weigh(r1, b + 1);
         }
         float s0, s1;
         f32x2_split(sum2, s0, s1);
@@ -566,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     registers_up<kSumRegs>();
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    Walk walk(a, *first_group, lo, hi);
+    Walk walk(a, *first, lo, hi);
     Unit u;
     uint32_t t = 0;
     while (ok && walk.next(u)) {
@@ -745,6 +818,12 @@ int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const
   char* ws = static_cast<char*>(workspace);
   SharedArgs a{};
   a.q = q, a.q_tok = q_stride, a.k = k_pool, a.v = v_pool, a.table = block_table, a.table_stride = block_table_stride;
+  // boxes: the largest power of two that divides a page's rows, of 8 to 128
+  a.box = page_size % 8 ? 0 : std::min(page_size & -page_size, kKeys);
+  while ((1 << a.box_shift) < a.box) ++a.box_shift;
+  if (a.box && num_pages && !(encode_group_major_map(&a.k_map, k_pool, dh, hkv, num_pages * page_size, a.box) &&
+                              encode_group_major_map(&a.v_map, v_pool, dh, hkv, num_pages * page_size, a.box)))
+    return errorf(DFLASH_ERR_CUDA, "shared attention: no tensor map of the pools");
   a.num_pages = num_pages, a.page = page_size, a.scale_log2 = scale_log2_of(c);
   divide_by_page(page_size, &a.page_mul, &a.page_shift);
   a.header = reinterpret_cast<Header*>(ws + y.header), a.groups = reinterpret_cast<SharedGroup*>(ws + y.groups);
