@@ -559,12 +559,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         if (len >= u.prefix) from = first_row(a, len) - u.lo;
       }
       float m = -INFINITY;
+      const bool idle = u.m0 + (warp & 3) * 32 >= u.rows;  // lanes that hold no rows may hold anything
 #pragma unroll 1
       for (int i = u.t0; i < u.t1; ++i, ++t) {
         if ((t & 1) != static_cast<uint32_t>(half)) continue;
         const int buf = t % S::kBufs;
         const uint32_t s = tmem + lanes + buf * S::kBufCols;
         if (!(ok = wait_warp(bar(S::kSFull + buf), (t / S::kBufs) & 1))) break;
+        if (idle) {
+          if (lane == 0) mbar_arrive(bar(S::kPFull + buf));
+          continue;
+        }
         tc_fence_after();
         const int c_lo = from - i * kKeys, c_hi = u.prefix - u.lo - i * kKeys;  // columns [c_lo, c_hi) are seen
         const bool whole = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kKeys);
@@ -595,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         m = fmaxf(m, top * a.scale_log2);
         const float ref = m == -INFINITY ? 0.0f : m;
         const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2), ref2 = f32x2(-ref, -ref);
+        const uint64_t minus2 = f32x2(-1.0f, -1.0f);
         uint64_t sum2 = f32x2(0.0f, 0.0f);
         auto weigh = [&](uint32_t (&r)[16], int b) {
           masked(r, b);
@@ -603,13 +609,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           for (int j = 0; j < 16; j += 2) {
             float p0, p1;
             f32x2_split(fma_f32x2(f32x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), scale2, ref2), p0, p1);
-            p0 = ex2_approx(p0), p1 = ex2_approx(p1);
-            sum2 = add_f32x2(sum2, f32x2(p0, p1));
-            const uint32_t h = pack_bf16x2(p0, p1);
-            p0 -= bf16lo_to_f32(h), p1 -= bf16hi_to_f32(h);
-            const uint32_t mid = pack_bf16x2(p0, p1);
-            terms[j / 2] = h, terms[8 + j / 2] = mid;
-            if (F32) low[j / 2] = pack_bf16x2(p0 - bf16lo_to_f32(mid), p1 - bf16hi_to_f32(mid));
+            uint64_t p = f32x2(ex2_approx(p0), ex2_approx(p1));
+            sum2 = add_f32x2(sum2, p);
+            auto term = [&]() {  // the next 8 bits of p, and what they leave
+              float x, y;
+              f32x2_split(p, x, y);
+              const uint32_t h = pack_bf16x2(x, y);
+              p = fma_f32x2(f32x2(bf16lo_to_f32(h), bf16hi_to_f32(h)), minus2, p);
+              return h;
+            };
+            terms[j / 2] = term();
+            terms[8 + j / 2] = term();
+            if (F32) low[j / 2] = term();
           }
           tmem_st_32x32b<16>(s + b * 16, terms);
           if (F32) tmem_st_32x32b<8>(s + 128 + b * 8, low);
@@ -643,23 +654,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     Unit u;
     uint32_t t = 0;
     while (ok && walk.next(u)) {
-      float acc[DH], m = -INFINITY, l = 0.0f;
+      uint64_t acc[DH / 2];  // two columns each
+      float m = -INFINITY, l = 0.0f;
+      const bool idle = u.m0 + (warp & 3) * 32 >= u.rows;
 #pragma unroll
-      for (int j = 0; j < DH; ++j) acc[j] = 0.0f;
+      for (int j = 0; j < DH / 2; ++j) acc[j] = f32x2(0.0f, 0.0f);
 #pragma unroll 1
       for (int i = u.t0; i < u.t1; ++i, ++t) {
         const int buf = t % S::kBufs;
         if (!(ok = wait_warp(bar(S::kPFull + buf), (t / S::kBufs) & 1))) break;
         if (!(ok = wait_warp(bar(S::kOFull), t & 1))) break;
+        if (idle) {
+          if (lane == 0) mbar_arrive(bar(S::kOEmpty + (t & 1)));
+          continue;
+        }
         tc_fence_after();
         const float2 st = stats[(t & 1) * kRows + row];
         const float top = fmaxf(m, st.x);
         const float old = m == -INFINITY ? 0.0f : ex2_approx(m - top), now = st.x == -INFINITY ? 0.0f : ex2_approx(st.x - top);
         m = top;
         l = fmaf(l, old, st.y * now);
+        const uint64_t old2 = f32x2(old, old), now2 = f32x2(now, now);
         if (__any_sync(0xffffffffu, old != 1.0f)) {
 #pragma unroll
-          for (int j = 0; j < DH; ++j) acc[j] *= old;
+          for (int j = 0; j < DH / 2; ++j) acc[j] = mul_f32x2(acc[j], old2);
         }
 #pragma unroll
         for (int b = 0; b < DH / 16; ++b) {
@@ -672,7 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             if (lane == 0) mbar_arrive(bar(S::kOEmpty + (t & 1)));
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[b * 16 + j] = fmaf(__uint_as_float(r[j]), now, acc[b * 16 + j]);
+          for (int j = 0; j < 8; ++j)
+            acc[b * 8 + j] = fma_f32x2(f32x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), now2, acc[b * 8 + j]);
         }
       }
       if (!ok) break;
@@ -686,7 +705,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         *reinterpret_cast<float2*>(whole ? a.pre_ml + head_at * 2 : a.part_ml + slot * 2) = make_float2(m, l);
         if (from_start) a.where[head_at] = whole ? make_int2(-1, 0) : make_int2(static_cast<int>(blockIdx.x), ranges.owner(u.start + u.n - 1) | row << 16);
 #pragma unroll
-        for (int j = 0; j < DH; j += 4) *reinterpret_cast<float4*>(o + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        for (int j = 0; j < DH / 4; ++j) {
+          float4 x;
+          f32x2_split(acc[2 * j], x.x, x.y), f32x2_split(acc[2 * j + 1], x.z, x.w);
+          *reinterpret_cast<float4*>(o + 4 * j) = x;
+        }
       }
     }
   }
