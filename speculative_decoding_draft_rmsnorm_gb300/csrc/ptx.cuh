@@ -168,6 +168,13 @@ __device__ __forceinline__ void st_global_v2_hint(float* ptr, float a, float b, 
                : "memory");
 }
 
+// 32 bytes in one store: a whole sector.
+__device__ __forceinline__ void st_global_256(float* ptr, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(ptr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]),
+               "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // Starts bringing a global line into L1 (no wait).
 __device__ __forceinline__ void prefetch_l1(const void* ptr) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<uint64_t>(ptr)));

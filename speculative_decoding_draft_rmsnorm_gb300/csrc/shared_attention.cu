@@ -24,9 +24,10 @@ constexpr int kPlanThreads = 1024;
 constexpr int kLeastPrefix = 64;
 
 // A group that shares: `n` tiles of rows [lo, prefix) for each of hkv x tiles_m units, from tile `start` of the call on.
-struct SharedGroup {
+struct alignas(16) SharedGroup {
   int first, rows;  // its first sequence; sequences x heads of a kv head
-  int prefix, lo;   // lo: where the tiles begin, the start of a box
+  int prefix, lo;   // lo: where the tiles begin
+  int see;          // the first row that any of its sequences sees; lo is the start of its box
   int leader;       // the shortest sequence that shares: its pages are read
   int tiles_m, n;   // tiles_m = rows / kRows, up
   uint32_t start;
@@ -60,7 +61,7 @@ struct SharedArgs {
   int2* where;     // [num_reqs][Hq]: (first or -1, last and the row in the slots << 16)
   float* pre_o;    // [num_reqs][Hq][Dh]
   float* pre_ml;   // [num_reqs][Hq][2]
-  float* part_o;   // [2 * blocks][kRows][Dh]
+  float* part_o;   // [2 * blocks][Dh / 8][kRows][8]
   float* part_ml;  // [2 * blocks][kRows][2]
   void* out;
   float* lse;
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const int members = a.starts[g + 1] - x.first;
       x.prefix = shared_rows(g, members);
       const unsigned long long least = *static_cast<volatile unsigned long long*>(&a.least[g]);
-      x.lo = first_row(a, static_cast<int>(least >> 32)) & -max(a.box, 1), x.leader = static_cast<int>(least & 0xffffffffu);
+      x.see = first_row(a, static_cast<int>(least >> 32)), x.lo = x.see & -max(a.box, 1), x.leader = static_cast<int>(least & 0xffffffffu);
       x.rows = members * a.g;
       x.tiles_m = (x.rows + kRows - 1) / kRows;
       if (least != ~0ull && x.lo < x.prefix) {
@@ -177,7 +178,7 @@ struct TileRanges {
 
 // Tiles [t0, t1) of a unit: kv head kvh, rows m0 .. of its group.
 struct Unit {
-  int first, rows, prefix, lo, leader;
+  int first, rows, prefix, lo, see, leader;
   int kvh, m0, t0, t1, n;
   uint32_t start;  // its tile 0
 };
@@ -192,15 +193,19 @@ struct Walk {
   const SharedGroup* groups;
   uint32_t x, hi;
   int hkv, kvh, m0, t;  // the next unit and its first tile here
-  SharedGroup g;
+  SharedGroup g;        // (the next one is on its way to L1)
   __device__ __forceinline__ Walk(const SharedArgs& a, const First& f, uint32_t lo, uint32_t hi_)
       : groups(a.groups + f.group), x(lo), hi(hi_), hkv(a.hkv), kvh(f.kvh), m0(f.m0), t(f.t) {
     g = *groups;
+    prefetch_l1(groups + 1);
   }
   __device__ __forceinline__ bool next(Unit& u) {
     if (x >= hi) return false;
-    if (kvh == hkv) kvh = 0, g = *++groups;
-    u.first = g.first, u.rows = g.rows, u.prefix = g.prefix, u.lo = g.lo, u.leader = g.leader, u.n = g.n;
+    if (kvh == hkv) {
+      kvh = 0, g = *++groups;
+      prefetch_l1(groups + 1);
+    }
+    u.first = g.first, u.rows = g.rows, u.prefix = g.prefix, u.lo = g.lo, u.see = g.see, u.leader = g.leader, u.n = g.n;
     u.kvh = kvh, u.m0 = m0, u.t0 = t;
     u.t1 = static_cast<int>(min(static_cast<uint32_t>(u.n), t + (hi - x)));
     u.start = x - t;
@@ -369,24 +374,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       const uint32_t box_bytes = (S::kGroup / 8) << a.box_shift, n = hi - lo;
       int t = 0, end = 0;         // the tile looked up next; its unit's end
       int id[4], key[4];          // its rows, and their pages: lane + 32 y, or the first of box `lane`
-      int see = 0, boxes = 0;     // the unit's first row that is seen; the tile's boxes, 0: row by row
+      int boxes = 0;              // the tile's boxes, 0: row by row
       auto look_up = [&]() {
         if (t >= end) {
           if (!walk.next(u)) return;
           t = u.t0, end = u.t1;
-          see = first_row(a, valid_len(a, a.lens[u.leader]));
         }
         const int from = u.lo + t * kKeys, rows = min(kKeys, u.prefix - from);
         const int32_t* pages = a.table + u.leader * a.table_stride;
-        boxes = a.box && from >= see && (rows & (max(16, a.box) - 1)) == 0 ? rows >> a.box_shift : 0;
+        boxes = a.box && from >= u.see && (rows & (max(16, a.box) - 1)) == 0 ? rows >> a.box_shift : 0;
         if (boxes) {
           key[0] = from + (min(lane, boxes - 1) << a.box_shift);
-          id[0] = pages[page_of(a, key[0])];
+          const int at = page_of(a, key[0]);
+          id[0] = pages[at];
+          if (at + 64 < page_of(a, u.prefix)) prefetch_l1(pages + at + 64);
         } else {
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             key[y] = from + y * 32 + lane;
-            if (key[y] >= see && key[y] < u.prefix) id[y] = pages[page_of(a, key[y])];
+            if (key[y] >= u.see && key[y] < u.prefix) id[y] = pages[page_of(a, key[y])];
             else key[y] = -1;
           }
         }
@@ -701,14 +707,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const int64_t head_at = static_cast<int64_t>(u.first + s) * a.hq + u.kvh * a.g + at - s * a.g;
         const bool from_start = u.t0 == 0, whole = from_start && u.t1 == u.n;
         const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (from_start ? 1 : 0)) * kRows + row;
-        float* o = whole ? a.pre_o + head_at * DH : a.part_o + slot * DH;
+        // the lanes of a store are neighbours in a part; in `pre` each has a row of its own
+        float* o = whole ? a.pre_o + head_at * DH : a.part_o + (slot - row) * DH + row * 8;
+        const int step = whole ? 8 : kRows * 8;
         *reinterpret_cast<float2*>(whole ? a.pre_ml + head_at * 2 : a.part_ml + slot * 2) = make_float2(m, l);
         if (from_start) a.where[head_at] = whole ? make_int2(-1, 0) : make_int2(static_cast<int>(blockIdx.x), ranges.owner(u.start + u.n - 1) | row << 16);
 #pragma unroll
-        for (int j = 0; j < DH / 4; ++j) {
-          float4 x;
-          f32x2_split(acc[2 * j], x.x, x.y), f32x2_split(acc[2 * j + 1], x.z, x.w);
-          *reinterpret_cast<float4*>(o + 4 * j) = x;
+        for (int j = 0; j < DH / 8; ++j) {
+          float x[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) f32x2_split(acc[4 * j + y], x[2 * y], x[2 * y + 1]);
+          st_global_256(o + j * step, x);
         }
       }
     }
@@ -738,11 +747,13 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Sha
   }
   const int slot_row = where.y >> 16;
   float o[C], m, l;
+  // a lane's columns in a part lie kRows rows of 8 apart
+  const int64_t lane_at = static_cast<int64_t>(lane * C / 8) * (kRows * 8) + lane * C % 8 - lane * C;
   merge_parts<DH>(parts + has_own, 0, 1, [&](int p) {
     if (p == parts) return Part{a.own_o + row * DH, a.own_ml + row * 2};
     if (where.x < 0) return Part{a.pre_o + row * DH, a.pre_ml + row * 2};
-    const int64_t at = (2 * static_cast<int64_t>(where.x + p) + (p == 0 ? 1 : 0)) * kRows + slot_row;
-    return Part{a.part_o + at * DH, a.part_ml + at * 2};
+    const int64_t slot = 2 * static_cast<int64_t>(where.x + p) + (p == 0 ? 1 : 0);
+    return Part{a.part_o + slot * (kRows * DH) + slot_row * 8 + lane_at, a.part_ml + (slot * kRows + slot_row) * 2};
   }, o, m, l);
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   if (F32) {
