@@ -23,19 +23,42 @@ constexpr int kPlanThreads = 1024;
 // A prefix of fewer rows is left to the sequences: half a tile.
 constexpr int kLeastPrefix = 64;
 
+// Blocks take ranges of equal cost: a tile's is kTileCost, and a unit's start (its queries, the sums of the one before
+// written out, the ends of prefixes that are no whole tiles) takes kUnitCost more. Where there are fewer than
+// kFewTiles tiles a block, only tiles count, so that every block in use has one.
+constexpr uint32_t kTileCost = 8, kUnitCost = 16, kFewTiles = 4;
+static_assert(kFewTiles * kTileCost >= kTileCost + kUnitCost, "no block's range may lie between two tiles");
+
 // A group that shares: `n` tiles of rows [lo, prefix) for each of hkv x tiles_m units, from tile `start` of the call on.
 struct alignas(16) SharedGroup {
-  int first, rows;  // its first sequence; sequences x heads of a kv head
-  int prefix, lo;   // lo: where the tiles begin
-  int see;          // the first row that any of its sequences sees; lo is the start of its box
-  int leader;       // the shortest sequence that shares: its pages are read
-  int tiles_m, n;   // tiles_m = rows / kRows, up
-  uint32_t start;
+  int first, end, rows;  // its sequences; sequences x heads of a kv head
+  int prefix, lo;        // lo: where the tiles begin
+  int see;               // the first row that any of its sequences sees; lo is the start of its box
+  int leader;            // the shortest sequence that shares: its pages are read
+  int n;
+  uint32_t start, units; // tiles and units before it
+  uint32_t pad[2];
 };
-struct Header {
-  uint32_t tiles;
-  int groups;
+struct Totals {
+  uint32_t tiles, unit_cost, blocks;  // blocks: that have tiles
+  uint64_t cost;
 };
+// A block's tiles, and where in their group they begin.
+struct alignas(16) BlockRange {
+  uint32_t lo, hi;
+  int group, kvh, m0, t;
+  int pad[2];
+};
+// Where a head's sums over the prefix are: first < 0: in `pre`; else in the slots of blocks from `first` to the one that has
+// tile `last`, the last of unit `unit`, in row `row`.
+struct alignas(16) Where {
+  int first, row;
+  uint32_t last, unit;
+};
+// Tile t of the call, in unit i, lies at this cost; block b has those in [b, b + 1) cost / blocks of the totals.
+__device__ __forceinline__ uint64_t cost_of(const Totals& z, uint32_t t, uint32_t i) {
+  return static_cast<uint64_t>(kTileCost) * t + static_cast<uint64_t>(z.unit_cost) * (i + 1ull);
+}
 
 struct SharedArgs {
   CUtensorMap k_map, v_map;  // boxes of `box` rows of a head
@@ -50,18 +73,18 @@ struct SharedArgs {
   const int32_t* starts;    // [num_groups + 1]
   const int32_t* prefixes;  // [num_groups]
   uint32_t* err;
-  Header* header;
+  Totals* totals;
   SharedGroup* groups;
+  BlockRange* ranges;  // [blocks]
+  int blocks;          // of the prefix kernel
   unsigned long long* least;  // [num_groups]: length and index of the shortest sequence that shares, while the plan is made
   int32_t* own;   // [num_reqs]: rows before it are the prefix's
   float* own_o;   // [num_reqs][Hq][Dh], a head's sums over its own rows
   float* own_ml;  // [num_reqs][Hq][2]
-  // a head's sums over the prefix: where one block had them all, `pre`, else the parts of blocks first .. last; the first
-  // block's in its slot 2b + 1, the others' in theirs, 2b
-  int2* where;     // [num_reqs][Hq]: (first or -1, last and the row in the slots << 16)
+  Where* where;    // [num_reqs][Hq]
   float* pre_o;    // [num_reqs][Hq][Dh]
   float* pre_ml;   // [num_reqs][Hq][2]
-  float* part_o;   // [2 * blocks][Dh / 8][kRows][8]
+  float* part_o;   // [2 * blocks][Dh / 8][kRows][8]: block b's unit that began before it, and (2b + 1) the one that goes on behind
   float* part_ml;  // [2 * blocks][kRows][2]
   void* out;
   float* lse;
@@ -70,9 +93,15 @@ struct SharedArgs {
   int64_t num_pages;
   int page;
   uint32_t page_mul, page_shift;  // j / page
+  uint32_t g_mul, g_shift;        // j / g
   float scale_log2;
 };
 
+// j / d for j < 2^31, with what divide_by_page made of d.
+__device__ __forceinline__ int divided(int j, uint32_t mul, uint32_t shift) {
+  return mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(j), mul) >> shift) : j >> shift;
+}
+__device__ __forceinline__ int page_of(const SharedArgs& a, int j) { return divided(j, a.page_mul, a.page_shift); }
 __device__ __forceinline__ int valid_len(const SharedArgs& a, int len) { return len < 0 || len > a.max_len ? 0 : len; }
 __device__ __forceinline__ int first_row(const SharedArgs& a, int len) { return a.window > 0 && len > a.window ? len - a.window : 0; }
 
@@ -81,12 +110,13 @@ __device__ __forceinline__ int first_row(const SharedArgs& a, int len) { return 
 // sees, where the tiles start, and every row from there on: its pages are read.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ SharedArgs a) {
   __shared__ int s_bad, s_groups;
-  __shared__ uint32_t s_tiles;
-  __shared__ uint32_t s_warp[32];
+  __shared__ uint32_t s_tiles, s_units, s_warp[32], s_warp_units[32];
+  __shared__ uint2 s_at[kPlanThreads];  // tiles and units before the first groups
+  __shared__ uint32_t s_lo[kPlanThreads];
   __shared__ int s_count[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dependents_launch();
-  if (tid == 0) s_bad = 0, s_tiles = 0, s_groups = 0;
+  if (tid == 0) s_bad = 0, s_tiles = 0, s_units = 0, s_groups = 0;
   __syncthreads();
   for (int g = tid; g < a.num_groups; g += kPlanThreads) {
     const int from = a.starts[g], to = a.starts[g + 1];
@@ -124,68 +154,99 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   for (int base = 0; base < groups; base += kPlanThreads) {
     const int g = base + tid;
     SharedGroup x{};
-    uint32_t tiles = 0;
+    uint32_t tiles = 0, units = 0;
     if (g < groups) {
       const int raw = a.prefixes[g];
       if ((raw < 0 || raw > a.max_len) && a.err) atomicOr(a.err, kErrMetadata);
-      x.first = a.starts[g];
-      const int members = a.starts[g + 1] - x.first;
+      x.first = a.starts[g], x.end = a.starts[g + 1];
+      const int members = x.end - x.first;
       x.prefix = shared_rows(g, members);
       const unsigned long long least = *static_cast<volatile unsigned long long*>(&a.least[g]);
       x.see = first_row(a, static_cast<int>(least >> 32)), x.lo = x.see & -max(a.box, 1), x.leader = static_cast<int>(least & 0xffffffffu);
       x.rows = members * a.g;
-      x.tiles_m = (x.rows + kRows - 1) / kRows;
-      if (least != ~0ull && x.lo < x.prefix) {
+      if (least != ~0ull && x.see < x.prefix) {
         x.n = (x.prefix - x.lo + kKeys - 1) / kKeys;
-        tiles = static_cast<uint32_t>(x.n) * x.tiles_m * a.hkv;
+        units = static_cast<uint32_t>((x.rows + kRows - 1) / kRows) * a.hkv;
+        tiles = units * x.n;
       }
     }
-    // the groups that share, close together, and their tiles laid end to end
+    // the groups that share, close together, and their tiles and units laid end to end
     const uint32_t have = __ballot_sync(0xffffffffu, tiles != 0);
-    uint32_t upto = tiles;
+    uint32_t upto = tiles, units_to = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o), z = __shfl_up_sync(0xffffffffu, units_to, o);
+      if (lane >= o) upto += y, units_to += z;
     }
-    if (lane == 31) s_warp[warp] = upto, s_count[warp] = __popc(have);
+    if (lane == 31) s_warp[warp] = upto, s_warp_units[warp] = units_to, s_count[warp] = __popc(have);
     __syncthreads();
-    uint32_t before = s_tiles;
+    uint32_t before = s_tiles, units_before = s_units;
     int at = s_groups + __popc(have & ((1u << lane) - 1));
-    for (int i = 0; i < warp; ++i) before += s_warp[i], at += s_count[i];
+    for (int i = 0; i < warp; ++i) before += s_warp[i], units_before += s_warp_units[i], at += s_count[i];
     if (tiles) {
       x.start = before + upto - tiles;
+      x.units = units_before + units_to - units;
       a.groups[at] = x;
+      if (at < kPlanThreads) s_at[at] = make_uint2(x.start, x.units);
     }
     __syncthreads();
     if (tid == 0)
-      for (int i = 0; i < 32; ++i) s_tiles += s_warp[i], s_groups += s_count[i];
+      for (int i = 0; i < 32; ++i) s_tiles += s_warp[i], s_units += s_warp_units[i], s_groups += s_count[i];
     __syncthreads();
   }
-  if (tid == 0) *a.header = Header{s_tiles, s_groups};
-}
-
-// The blocks' ranges of tiles: equal to within one.
-struct TileRanges {
-  uint32_t each, extra;  // the first `extra` blocks take each + 1
-  __device__ __forceinline__ TileRanges(uint32_t total, uint32_t blocks) : each(total / blocks), extra(total % blocks) {}
-  __device__ __forceinline__ uint32_t start(uint32_t b) const { return b * each + min(b, extra); }
-  __device__ __forceinline__ int owner(uint32_t x) const {  // of tile x
-    const uint32_t cut = extra * (each + 1);
-    return static_cast<int>(x < cut ? x / (each + 1) : extra + (x - cut) / each);
+  Totals z;
+  z.tiles = s_tiles;
+  z.unit_cost = z.tiles < kFewTiles * a.blocks ? 0 : kUnitCost;
+  z.blocks = min(static_cast<uint32_t>(a.blocks), max(z.tiles, 1u));
+  z.cost = static_cast<uint64_t>(kTileCost) * z.tiles + static_cast<uint64_t>(z.unit_cost) * s_units;
+  if (tid == 0) *a.totals = z;
+  // ---- the blocks' ranges
+  __threadfence_block();
+  const int sharing = s_groups;
+  for (int base = 0; base < a.blocks; base += kPlanThreads - 1) {
+    const int b = base + tid;
+    BlockRange r{};
+    if (b <= a.blocks) {
+      r.lo = z.tiles;
+      if (b < static_cast<int>(z.blocks) && sharing) {
+        const uint64_t w = (z.cost * b + z.blocks - 1) / z.blocks;
+        int lo = 0, hi = sharing - 1;  // the last group that begins at or before w
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          uint2 c;
+          if (mid < kPlanThreads) c = s_at[mid];
+          else c = make_uint2(*const_cast<const volatile uint32_t*>(&a.groups[mid].start), *const_cast<const volatile uint32_t*>(&a.groups[mid].units));
+          if (static_cast<uint64_t>(kTileCost) * c.x + static_cast<uint64_t>(z.unit_cost) * c.y <= w) lo = mid;
+          else hi = mid - 1;
+        }
+        const SharedGroup g = a.groups[lo];
+        const uint32_t unit_cost = kTileCost * g.n + z.unit_cost, tiles_m = static_cast<uint32_t>((g.rows + kRows - 1) / kRows);
+        const uint64_t d = w - (static_cast<uint64_t>(kTileCost) * g.start + static_cast<uint64_t>(z.unit_cost) * g.units);
+        uint32_t unit = static_cast<uint32_t>(d / unit_cost), t = static_cast<uint32_t>(d - static_cast<uint64_t>(unit) * unit_cost);
+        t = t <= z.unit_cost ? 0 : (t - z.unit_cost + kTileCost - 1) / kTileCost;
+        if (t >= static_cast<uint32_t>(g.n)) t = 0, ++unit;
+        r.lo = g.start + unit * g.n + t;
+        r.group = lo;
+        if (unit == tiles_m * a.hkv) unit = 0, ++r.group;  // the next group's first
+        else r.kvh = static_cast<int>(unit / tiles_m), r.m0 = static_cast<int>(unit - r.kvh * tiles_m) * kRows;
+        r.t = static_cast<int>(t);
+      }
+      s_lo[tid] = r.lo;
+    }
+    __syncthreads();
+    if (b < a.blocks && tid + 1 < kPlanThreads) {
+      r.hi = s_lo[tid + 1];
+      a.ranges[b] = r;
+    }
+    __syncthreads();
   }
-};
+}
 
 // Tiles [t0, t1) of a unit: kv head kvh, rows m0 .. of its group.
 struct Unit {
   int first, rows, prefix, lo, see, leader;
   int kvh, m0, t0, t1, n;
-  uint32_t start;  // its tile 0
-};
-
-// Where a block's tiles begin.
-struct First {
-  int group, kvh, m0, t;
+  uint32_t tile, unit;  // tiles and units of the call before it
 };
 
 // A block's units, one after the other. Every role walks them for itself.
@@ -193,22 +254,27 @@ struct Walk {
   const SharedGroup* groups;
   uint32_t x, hi;
   int hkv, kvh, m0, t;  // the next unit and its first tile here
-  SharedGroup g;        // (the next one is on its way to L1)
-  __device__ __forceinline__ Walk(const SharedArgs& a, const First& f, uint32_t lo, uint32_t hi_)
-      : groups(a.groups + f.group), x(lo), hi(hi_), hkv(a.hkv), kvh(f.kvh), m0(f.m0), t(f.t) {
+  uint32_t unit;        // of the call
+  SharedGroup g;        // (the next one is on its way to L1, and its sequences' lengths)
+  const int32_t* lens;
+  __device__ __forceinline__ Walk(const SharedArgs& a, const BlockRange& r)
+      : groups(a.groups + r.group), x(r.lo), hi(r.hi), hkv(a.hkv), kvh(r.kvh), m0(r.m0), t(r.t), lens(a.lens) {
     g = *groups;
     prefetch_l1(groups + 1);
+    prefetch_l1(lens + g.end - 1);
+    unit = g.units + (x - t - g.start) / static_cast<uint32_t>(g.n);
   }
   __device__ __forceinline__ bool next(Unit& u) {
     if (x >= hi) return false;
     if (kvh == hkv) {
       kvh = 0, g = *++groups;
       prefetch_l1(groups + 1);
+      prefetch_l1(lens + g.end - 1);
     }
     u.first = g.first, u.rows = g.rows, u.prefix = g.prefix, u.lo = g.lo, u.see = g.see, u.leader = g.leader, u.n = g.n;
     u.kvh = kvh, u.m0 = m0, u.t0 = t;
     u.t1 = static_cast<int>(min(static_cast<uint32_t>(u.n), t + (hi - x)));
-    u.start = x - t;
+    u.tile = x - t, u.unit = unit++;
     x += u.t1 - t;
     t = 0, m0 += kRows;
     if (m0 >= g.rows) m0 = 0, ++kvh;
@@ -247,9 +313,6 @@ struct Shape {
   static_assert(kBytes <= 232448, "a block's shared memory");
 };
 
-__device__ __forceinline__ int page_of(const SharedArgs& a, int j) {
-  return a.page_mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(j), a.page_mul) >> a.page_shift) : j >> a.page_shift;
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int size, uint64_t policy) {  // size 0: zeros
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(size), "l"(policy)
                : "memory");
@@ -276,7 +339,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   auto bar = [&](int i) { return sbase + S::kBars + 8u * static_cast<uint32_t>(i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
-  First* first = reinterpret_cast<First*>(smem + S::kMisc + 16);
   float2* stats = reinterpret_cast<float2*>(smem + S::kStats);  // [2][kRows]: a tile's reference and weight
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -292,23 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   if (warp == kIssuer) tmem_alloc(smem_u32(tmem_slot), 512);
   grid_dependency_wait();  // the plan
   grid_dependents_launch();
-  const Header head = *a.header;
-  const TileRanges ranges(head.tiles, gridDim.x);
-  const uint32_t lo = ranges.start(blockIdx.x), hi = ranges.start(blockIdx.x + 1);
-  if (warp == 0 && lo < hi) {  // the group that holds tile lo, 32 at a time
-    int from = 0, n = head.groups;
-    while (n > 1) {
-      const int step = (n + 31) / 32, i = lane * step;
-      const uint32_t le = __ballot_sync(0xffffffffu, i < n && a.groups[from + min(i, n - 1)].start <= lo);
-      const int k = 31 - __clz(le);
-      from += k * step, n = min(step, n - k * step);
-    }
-    if (lane == 0) {
-      const SharedGroup g = a.groups[from];
-      const uint32_t rel = lo - g.start, unit = rel / static_cast<uint32_t>(g.n), kvh = unit / static_cast<uint32_t>(g.tiles_m);
-      *first = First{from, static_cast<int>(kvh), static_cast<int>(unit - kvh * g.tiles_m) * kRows, static_cast<int>(rel - unit * g.n)};
-    }
-  }
+  const BlockRange range = a.ranges[blockIdx.x];
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -330,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   bool ok = true;
   if (warp < 4) registers_down<kCopyRegs>();
 
-  if (lo >= hi) {
+  if (range.lo >= range.hi) {
     // no tiles
   } else if (warp < kIssuer) {
     // ------------------------------------------------------------ copies
@@ -344,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     auto copy = [&](const void* src, bool have, uint32_t off, int r) {  // kAtOnce rows from row r of the tile at off on
       cp_async16(dst_lane + off + (r >> 3) * S::kGroup + (r & 7) * 128 + ((swz ^ (r & 7)) << 4), src, have ? 16 : 0, policy);
     };
-    Walk walk(a, *first, lo, hi);
+    Walk walk(a, range);
     Unit u;
     if (warp == 2) {
       // ---- Q, a unit's rows at a time
@@ -352,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         if (iu >= 2 && !(ok = wait_warp(bar(S::kQEmpty + (iu & 1)), ((iu >> 1) - 1) & 1))) break;
 #pragma unroll 2
         for (int r = 0; r < kRows; r += kAtOnce) {
-          const int at = u.m0 + r + sub, s = at / a.g;
+          const int at = u.m0 + r + sub, s = divided(at, a.g_mul, a.g_shift);
           copy(a.q + (at < u.rows ? (u.first + s) * a.q_tok + static_cast<int64_t>(u.kvh * a.g + at - s * a.g) * DH : 0) + piece * 8, at < u.rows,
                (iu & 1) * S::kTile, r);
         }
@@ -371,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       const char* base = reinterpret_cast<const char*>(is_v ? a.v : a.k) + piece * 16;
       const CUtensorMap* map = is_v ? &a.v_map : &a.k_map;
       const int64_t row_bytes = static_cast<int64_t>(a.hkv) * DH * 2;
-      const uint32_t box_bytes = (S::kGroup / 8) << a.box_shift, n = hi - lo;
+      const uint32_t box_bytes = (S::kGroup / 8) << a.box_shift, n = range.hi - range.lo;
       int t = 0, end = 0;         // the tile looked up next; its unit's end
       int id[4], key[4];          // its rows, and their pages: lane + 32 y, or the first of box `lane`
       int boxes = 0;              // the tile's boxes, 0: row by row
@@ -482,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ products
     const uint32_t idesc_s = umma_idesc_bf16(kRows, kKeys, 0, 0), idesc_o = umma_idesc_bf16(kRows, DH, 0, 1);
-    const uint32_t n = hi - lo, by = elect_one();
-    Walk walk(a, *first, lo, hi);
+    const uint32_t n = range.hi - range.lo, by = elect_one();
+    Walk walk(a, range);
     Unit u;
     int iu = -1;
     uint32_t left = 0;  // tiles of the unit whose scores are to come
@@ -553,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     // ------------------------------------------------------------ weights: tile t by warps 4-7 (even) or 8-11, a row a thread
     const int half = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    Walk walk(a, *first, lo, hi);
+    Walk walk(a, range);
     Unit u;
     uint32_t t = 0;
     while (ok && walk.next(u)) {
@@ -561,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       const int at = u.m0 + row;
       int from = 0x7fffffff;
       if (at < u.rows) {
-        const int len = valid_len(a, a.lens[u.first + at / a.g]);
+        const int len = valid_len(a, a.lens[u.first + divided(at, a.g_mul, a.g_shift)]);
         if (len >= u.prefix) from = first_row(a, len) - u.lo;
       }
       float m = -INFINITY;
@@ -581,11 +627,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const bool whole = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kKeys);
         // 16 columns at a time, the next ones on their way; first for the maximum, then for the weights
         auto masked = [&](uint32_t (&r)[16], int b) {
-          if (whole) return;
+          if (whole || __all_sync(0xffffffffu, c_lo <= b * 16 && b * 16 + 16 <= c_hi)) return;
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             if (b * 16 + j < c_lo || b * 16 + j >= c_hi) r[j] = 0xff800000u;
         };
+        const int steps = min(8, (c_hi + 15) >> 4);  // products with what lies behind are not made
         float top = -INFINITY;
         auto highest = [&](uint32_t (&r)[16], int b) {
           masked(r, b);
@@ -595,12 +642,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         uint32_t r0[16], r1[16];
         tmem_ld_32x32b<16>(s, r0);
 #pragma unroll 1
-        for (int b = 0; b < 8; b += 2) {
+        for (int b = 0; b < steps; b += 2) {
           tmem_wait_ld();
           tmem_ld_32x32b<16>(s + (b + 1) * 16, r1);
           highest(r0, b);
           tmem_wait_ld();
-          tmem_ld_32x32b<16>(s + (b + 2 & 7) * 16, r0);  // 0 again behind the last
+          tmem_ld_32x32b<16>(s + (b + 2 < steps ? b + 2 : 0) * 16, r0);  // 0 again behind the last
           highest(r1, b + 1);
         }
         m = fmaxf(m, top * a.scale_log2);
@@ -632,12 +679,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           if (F32) tmem_st_32x32b<8>(s + 128 + b * 8, low);
         };
 #pragma unroll 1
-        for (int b = 0; b < 8; b += 2) {
+        for (int b = 0; b < steps; b += 2) {
           tmem_wait_ld();
           tmem_ld_32x32b<16>(s + (b + 1) * 16, r1);
           weigh(r0, b);
           tmem_wait_ld();
-          if (b < 6) tmem_ld_32x32b<16>(s + (b + 2) * 16, r0);
+          if (b + 2 < steps) tmem_ld_32x32b<16>(s + (b + 2) * 16, r0);
           weigh(r1, b + 1);
         }
         float s0, s1;
@@ -656,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     registers_up<kSumRegs>();
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    Walk walk(a, *first, lo, hi);
+    Walk walk(a, range);
     Unit u;
     uint32_t t = 0;
     while (ok && walk.next(u)) {
@@ -703,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       if (!ok) break;
       const int at = u.m0 + row;
       if (at < u.rows) {
-        const int s = at / a.g;
+        const int s = divided(at, a.g_mul, a.g_shift);
         const int64_t head_at = static_cast<int64_t>(u.first + s) * a.hq + u.kvh * a.g + at - s * a.g;
         const bool from_start = u.t0 == 0, whole = from_start && u.t1 == u.n;
         const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (from_start ? 1 : 0)) * kRows + row;
@@ -711,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         float* o = whole ? a.pre_o + head_at * DH : a.part_o + (slot - row) * DH + row * 8;
         const int step = whole ? 8 : kRows * 8;
         *reinterpret_cast<float2*>(whole ? a.pre_ml + head_at * 2 : a.part_ml + slot * 2) = make_float2(m, l);
-        if (from_start) a.where[head_at] = whole ? make_int2(-1, 0) : make_int2(static_cast<int>(blockIdx.x), ranges.owner(u.start + u.n - 1) | row << 16);
+        if (from_start) a.where[head_at] = Where{whole ? -1 : static_cast<int>(blockIdx.x), row, u.tile + u.n - 1, u.unit};
 #pragma unroll
         for (int j = 0; j < DH / 8; ++j) {
           float x[8];
@@ -740,20 +787,23 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Sha
   const int r = static_cast<int>(row / a.hq), len = valid_len(a, a.lens[r]), own = a.own[r], first = first_row(a, len);
   const bool has_own = len > max(own, first), has_prefix = own > first;
   int parts = 0;
-  int2 where = make_int2(-1, 0);
+  Where where{-1, 0, 0, 0};
   if (has_prefix) {
     where = a.where[row];
-    parts = where.x < 0 ? 1 : (where.y & 0xffff) - where.x + 1;
+    parts = 1;
+    if (where.first >= 0) {
+      const Totals z = *a.totals;
+      parts = static_cast<int>(cost_of(z, where.last, where.unit) * z.blocks / z.cost) - where.first + 1;
+    }
   }
-  const int slot_row = where.y >> 16;
   float o[C], m, l;
   // a lane's columns in a part lie kRows rows of 8 apart
   const int64_t lane_at = static_cast<int64_t>(lane * C / 8) * (kRows * 8) + lane * C % 8 - lane * C;
   merge_parts<DH>(parts + has_own, 0, 1, [&](int p) {
     if (p == parts) return Part{a.own_o + row * DH, a.own_ml + row * 2};
-    if (where.x < 0) return Part{a.pre_o + row * DH, a.pre_ml + row * 2};
-    const int64_t slot = 2 * static_cast<int64_t>(where.x + p) + (p == 0 ? 1 : 0);
-    return Part{a.part_o + slot * (kRows * DH) + slot_row * 8 + lane_at, a.part_ml + (slot * kRows + slot_row) * 2};
+    if (where.first < 0) return Part{a.pre_o + row * DH, a.pre_ml + row * 2};
+    const int64_t slot = 2 * static_cast<int64_t>(where.first + p) + (p == 0 ? 1 : 0);
+    return Part{a.part_o + slot * (kRows * DH) + where.row * 8 + lane_at, a.part_ml + (slot * kRows + where.row) * 2};
   }, o, m, l);
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   if (F32) {
@@ -769,21 +819,22 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Sha
 }
 
 struct SharedLayout {
-  size_t header, groups, least, own, own_ml, own_o, where, pre_ml, pre_o, part_ml, part_o, rows, total;
+  size_t totals, groups, ranges, least, own, own_ml, own_o, where, pre_ml, pre_o, part_ml, part_o, rows, total;
 };
 
 SharedLayout shared_layout(int num_reqs, int num_groups, int hq, int hkv, int dh, int max_ctx_len, int window, int sms) {
   SharedLayout y{};
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   const size_t heads = static_cast<size_t>(num_reqs) * hq;
-  y.header = 0;
-  y.groups = y.header + 256;
-  y.least = y.groups + up(num_groups * sizeof(SharedGroup));
+  y.totals = 0;
+  y.ranges = y.totals + 256;
+  y.groups = y.ranges + up(sms * sizeof(BlockRange));
+  y.least = y.groups + up((num_groups + 1) * sizeof(SharedGroup));
   y.own = y.least + up(num_groups * sizeof(unsigned long long));
   y.own_ml = y.own + up(num_reqs * sizeof(int32_t));
   y.own_o = y.own_ml + up(heads * 2 * sizeof(float));
   y.where = y.own_o + up(heads * dh * sizeof(float));
-  y.pre_ml = y.where + up(heads * sizeof(int2));
+  y.pre_ml = y.where + up(heads * sizeof(Where));
   y.pre_o = y.pre_ml + up(heads * 2 * sizeof(float));
   y.part_ml = y.pre_o + up(heads * dh * sizeof(float));
   y.part_o = y.part_ml + up(static_cast<size_t>(sms) * 2 * kRows * 2 * sizeof(float));
@@ -858,18 +909,21 @@ int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const
   if (a.box && num_pages && !(encode_group_major_map(&a.k_map, k_pool, dh, hkv, num_pages * page_size, a.box) &&
                               encode_group_major_map(&a.v_map, v_pool, dh, hkv, num_pages * page_size, a.box)))
     return errorf(DFLASH_ERR_CUDA, "shared attention: no tensor map of the pools");
+  a.g = hq / hkv;
   a.num_pages = num_pages, a.page = page_size, a.scale_log2 = scale_log2_of(c);
   divide_by_page(page_size, &a.page_mul, &a.page_shift);
-  a.header = reinterpret_cast<Header*>(ws + y.header), a.groups = reinterpret_cast<SharedGroup*>(ws + y.groups);
+  divide_by_page(a.g, &a.g_mul, &a.g_shift);
+  a.totals = reinterpret_cast<Totals*>(ws + y.totals), a.ranges = reinterpret_cast<BlockRange*>(ws + y.ranges), a.blocks = sms;
+  a.groups = reinterpret_cast<SharedGroup*>(ws + y.groups);
   a.least = reinterpret_cast<unsigned long long*>(ws + y.least);
   a.lens = seq_lens, a.starts = group_start_loc, a.prefixes = prefix_lens, a.err = reinterpret_cast<uint32_t*>(status);
   a.own = reinterpret_cast<int32_t*>(ws + y.own);
   a.own_ml = reinterpret_cast<float*>(ws + y.own_ml), a.own_o = reinterpret_cast<float*>(ws + y.own_o);
-  a.where = reinterpret_cast<int2*>(ws + y.where);
+  a.where = reinterpret_cast<Where*>(ws + y.where);
   a.pre_ml = reinterpret_cast<float*>(ws + y.pre_ml), a.pre_o = reinterpret_cast<float*>(ws + y.pre_o);
   a.part_ml = reinterpret_cast<float*>(ws + y.part_ml), a.part_o = reinterpret_cast<float*>(ws + y.part_o);
   a.out = out, a.lse = lse;
-  a.num_reqs = num_reqs, a.num_groups = num_groups, a.hq = hq, a.hkv = hkv, a.g = hq / hkv;
+  a.num_reqs = num_reqs, a.num_groups = num_groups, a.hq = hq, a.hkv = hkv;
   a.max_len = max_ctx_len, a.window = window;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
