@@ -539,13 +539,14 @@ DFLASH_API int dflash_compact_pages(int32_t* block_table, int64_t block_table_st
  *                Every other overlap of an output with a tensor of the call is refused.
  *   scales       f32 [n, ceil(d / group_size)], or [n] with group_size 0; e4m3 only
  *   group_size   0 or a multiple of 16; the last group may be short
+ *   status       int32 device word or NULL: 1 is ORed in where a bounded wait ran out (rows are missing then)
  *   d <= 65536. Sums in f32 (rows of values above 1e19 overflow them), one rounding to the output's type. A
  *   scale is infinite or NaN where a y of its group is. One launch.
  */
 DFLASH_API int dflash_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                                const void* weight, void* residual_out, int64_t residual_out_stride, void* out,
                                int64_t out_stride, float* scales, int64_t n, int d, int dtype, int weight_dtype,
-                               int out_dtype, int group_size, float eps, dflash_stream_t stream);
+                               int out_dtype, int group_size, float eps, int32_t* status, dflash_stream_t stream);
 
 /*
  * dflash_rotary_axes -- dflash_rotary with a position on each of several axes (time, height, width):

@@ -299,7 +299,7 @@ PyObject* rotary_any(PyObject* const* a) {
 PyObject* rotary(PyObject* const* a) { return rotary_any<false>(a); }
 PyObject* rotary_axes(PyObject* const* a) { return rotary_any<true>(a); }
 
-// x, weight, residual, out dtype (None: x's), group_size, eps, out, residual_out, scales
+// x, weight, residual, out dtype (None: x's), group_size, eps, out, residual_out, scales, status
 PyObject* rms_norm(PyObject* const* a) {
   const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "weight");
   const Place at(x);
@@ -317,6 +317,7 @@ PyObject* rms_norm(PyObject* const* a) {
   const at::ScalarType out_type = eight ? at::kFloat8_e4m3fn : type;
   const int group = small(a[4], "group_size"), width = dim32(d, "d");
   const float eps = static_cast<float>(number(a[5]));
+  auto* status = static_cast<int32_t*>(at.address("status", a[9], at::kInt, {1}));
   const void* pw = at.address("weight", a[1], w.scalar_type(), {d});
   struct Matrix {
     at::Tensor t;
@@ -359,10 +360,10 @@ PyObject* rms_norm(PyObject* const* a) {
   }
   const int rc = run(at, [&](cudaStream_t stream) {
     return dflash_rms_norm(x.data_ptr(), x.stride(0), r.p, r.stride, pw, ro.p, ro.stride, out.p, out.stride, scales, n, width, dtype,
-                           code(w.scalar_type()), out_dtype, group, eps, stream);
+                           code(w.scalar_type()), out_dtype, group, eps, status, stream);
   });
   if (rc) return PyLong_FromLong(rc);
-  written({a[6], a[7], a[8]});
+  written({a[6], a[7], a[8], a[9]});
   return Py_BuildValue("(NNN)", given(a[6], out.t), given(a[7], ro.t), given(a[8], new_scales));
 }
 
@@ -638,7 +639,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 #define ENTRY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(rotary, 13),       ENTRY(decode_attention_paged, 14), ENTRY(beam_select, 10), ENTRY(fork_pages, 5),
-                         ENTRY(reserve_pages, 12), ENTRY(compact_pages, 6),           ENTRY(rotary_axes, 14), ENTRY(rms_norm, 9),
+                         ENTRY(reserve_pages, 12), ENTRY(compact_pages, 6),           ENTRY(rotary_axes, 14), ENTRY(rms_norm, 10),
                          ENTRY(shared_prefixes, 6), ENTRY(decode_attention_shared, 16), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_decode_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -10,12 +10,14 @@
 // same factor for every column. Maxima are taken as integers over the bits of |h w|, so that a NaN is the
 // largest value there is and turns up in its row's scale instead of getting lost.
 //
-// A block has one row: as many threads as hold it with two 16-byte chunks each (kHeld at most; what does not fit is
-// read again for the output), so that an SM's blocks have some 100 KB of loads in flight between them.
+// A block has one row at a time, a 16-byte chunk a thread where that fits (rows of more than two chunks a thread are
+// read again for the output), and loads the next row before it reduces this one. Blocks stay for as many rows as there
+// are, with the weights in registers.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/dflash.h"
 #include "decode_host.h"
@@ -41,6 +43,11 @@ struct NormArgs {
   int d, chunks;          // chunks of V elements
   int group, groups;      // columns of a scale (d: one for the row)
   int lanes, shift;       // lanes that hold a group between them (1 << shift), where shuffles reduce it; 0: shared memory
+  int warp_groups;        // a group is some warps' chunks
+  uint32_t group_mul, group_shift;  // column / group
+  int slots;              // rows in a ring
+  int w32;
+  uint32_t* err;
   float eps, inv_d;
 };
 
@@ -106,39 +113,76 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&v)[V]) {
   }
 }
 
-// Chunk c of h = x + r, and of the stream's copy.
-template <typename T, int V>
-__device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c, bool again, float (&h)[V]) {
-  if (again && a.r) {  // stored already: r_out may be x or r
-    load_vec<T, V>(static_cast<const T*>(a.r_out) + row * a.r_out_row + static_cast<int64_t>(c) * V, h);
-    return;
-  }
-  load_vec<T, V>(static_cast<const T*>(a.x) + row * a.x_row + static_cast<int64_t>(c) * V, h);
-  if (a.r) {
-    float r[V];
-    load_vec<T, V>(static_cast<const T*>(a.r) + row * a.r_row + static_cast<int64_t>(c) * V, r);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      h[i] += r[i];
-      if constexpr (sizeof(T) == 2) h[i] = bf16lo_to_f32(pack_bf16x2(h[i], 0.0f));
-    }
-    store_vec<T, V>(static_cast<T*>(a.r_out) + row * a.r_out_row + static_cast<int64_t>(c) * V, h);
-  }
+// j / d for j < 2^31, with what divide_by_page made of d.
+__device__ __forceinline__ int divided(int j, uint32_t mul, uint32_t shift) {
+  return mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(j), mul) >> shift) : j >> shift;
 }
 
-template <int V, bool W32>
-__device__ __forceinline__ void load_w(const NormArgs& a, int c, float (&w)[V]) {
-  if constexpr (W32) load_vec<float, V>(static_cast<const float*>(a.w) + c * V, w);
-  else load_vec<uint16_t, V>(static_cast<const uint16_t*>(a.w) + c * V, w);
+// The scale that makes y = v factor at most kLargest, from the bits of the largest |v|.
+__device__ __forceinline__ float scale_of(uint32_t top, float factor) {
+  const float s = __uint_as_float(top) * factor * (1.0f / kLargest);
+  return s < kLeastScale ? kLeastScale : s;  // a NaN stays
+}
+
+// A chunk as it lies in memory.
+template <typename T, int V>
+struct Raw {
+  static constexpr int kWords = (static_cast<int>(sizeof(T)) * V + 3) / 4;
+  uint32_t w[kWords];
+};
+template <typename T, int V>
+__device__ __forceinline__ void load_raw(const T* p, Raw<T, V>& x) {
+  constexpr int kBytes = sizeof(T) * V;
+  if constexpr (kBytes == 16) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w;
+  } else if constexpr (kBytes == 8) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    x.w[0] = a.x, x.w[1] = a.y;
+  } else if constexpr (kBytes == 4) {
+    x.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    x.w[0] = *reinterpret_cast<const uint16_t*>(p);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ float element(const Raw<T, V>& x, int i) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(x.w[i]);
+  else return (i & 1) ? bf16hi_to_f32(x.w[i / 2]) : bf16lo_to_f32(x.w[i / 2]);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void load_in(const NormArgs& a, int64_t row, int c, Raw<T, V>& x, Raw<T, V>& r) {
+  load_raw<T, V>(static_cast<const T*>(a.x) + row * a.x_row + static_cast<int64_t>(c) * V, x);
+  if (a.r) load_raw<T, V>(static_cast<const T*>(a.r) + row * a.r_row + static_cast<int64_t>(c) * V, r);
+}
+// h = x + r of a chunk, stored as the stream.
+template <typename T, int V>
+__device__ __forceinline__ void make_h(const NormArgs& a, int64_t row, int c, const Raw<T, V>& x, const Raw<T, V>& r, float (&h)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) h[i] = element<T, V>(x, i);
+  if (!a.r) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) h[i] += element<T, V>(r, i);
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const uint32_t p = pack_bf16x2(h[i], i + 1 < V ? h[(i + 1) % V] : 0.0f);
+      h[i] = bf16lo_to_f32(p);
+      if (i + 1 < V) h[(i + 1) % V] = bf16hi_to_f32(p);
+    }
+  }
+  store_vec<T, V>(static_cast<T*>(a.r_out) + row * a.r_out_row + static_cast<int64_t>(c) * V, h);
 }
 
 // EIGHT: 0 = the input's type, 1 = e4m3 with a scale a row, 2 = ... a group of columns
 template <typename T, int V, int HELD, bool W32, int EIGHT>
 __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a) {
+  using W = std::conditional_t<W32, float, uint16_t>;
   __shared__ float s_sum[32];
   __shared__ uint32_t s_top[32];
   __shared__ uint32_t s_group[EIGHT == 2 ? kMaxGroups : 1];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
   const int64_t row = blockIdx.x;
   if constexpr (EIGHT == 2) {
     if (!a.lanes) {
@@ -149,83 +193,113 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
   float h[HELD][V];  // h, then h w
   float sum = 0.0f;
   uint32_t top = 0, mine[HELD];  // bits of the largest |h w|: of the row, of this thread's chunk
+  {
+    Raw<T, V> x[HELD], r[HELD];
 #pragma unroll
-  for (int i = 0; i < HELD; ++i)
-    if (i * threads + tid < a.chunks) load_h<T, V>(a, row, i * threads + tid, false, h[i]);
-  auto weigh = [&](float (&x)[V], int c) {  // x <- x w; the largest of it
-    float w[V];
-    load_w<V, W32>(a, c, w);
+    for (int i = 0; i < HELD; ++i)
+      if (i * threads + tid < a.chunks) load_in<T, V>(a, row, i * threads + tid, x[i], r[i]);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (i * threads + tid < a.chunks) make_h<T, V>(a, row, i * threads + tid, x[i], r[i], h[i]);
+  }
+  auto weigh = [&](float (&y)[V], const float (&by)[V]) {  // y <- y w; the largest of it
     uint32_t t = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      sum = fmaf(x[j], x[j], sum);
-      x[j] *= w[j];
-      if constexpr (EIGHT != 0) t = max(t, __float_as_uint(x[j]) & 0x7fffffffu);
+      sum = fmaf(y[j], y[j], sum);
+      y[j] *= by[j];
+      if constexpr (EIGHT != 0) t = max(t, __float_as_uint(y[j]) & 0x7fffffffu);
     }
     return t;
   };
-  auto into_group = [&](uint32_t t, int c) {  // no shuffle reduces it
-    atomicMax(&s_group[c * V / a.group], t);
+  auto group_of = [&](int c) { return divided(c * V, a.group_mul, a.group_shift); };
+  auto into_group = [&](uint32_t t, int c, bool have) {  // where no shuffles hold a group
+    if (a.warp_groups) {  // ... a warp's chunks lie in one
+      t = __reduce_max_sync(0xffffffffu, have ? t : 0u);
+      if (lane == 0 && have) atomicMax(&s_group[group_of(c)], t);
+    } else if (have) {
+      atomicMax(&s_group[group_of(c)], t);
+    }
   };
 #pragma unroll
   for (int i = 0; i < HELD; ++i) {
     const int c = i * threads + tid;
     mine[i] = 0;
     if (c < a.chunks) {
-      mine[i] = weigh(h[i], c);
-      if constexpr (EIGHT == 1) top = max(top, mine[i]);
-      if constexpr (EIGHT == 2)
-        if (!a.lanes) into_group(mine[i], c);
+      float w[V];
+      load_vec<W, V>(static_cast<const W*>(a.w) + c * V, w);
+      mine[i] = weigh(h[i], w);
     }
+    if constexpr (EIGHT == 1) top = max(top, mine[i]);
+    if constexpr (EIGHT == 2)
+      if (!a.lanes) into_group(mine[i], c, c < a.chunks);
   }
 #pragma unroll 1
-  for (int c = HELD * threads + tid; c < a.chunks; c += threads) {
-    float x[V];
-    load_h<T, V>(a, row, c, false, x);
-    const uint32_t t = weigh(x, c);
+  for (int c0 = HELD * threads; c0 < a.chunks; c0 += threads) {  // what does not fit
+    const int c = c0 + tid;
+    uint32_t t = 0;
+    if (c < a.chunks) {
+      Raw<T, V> p, q;
+      float y[V], by[V];
+      load_in<T, V>(a, row, c, p, q);
+      make_h<T, V>(a, row, c, p, q, y);
+      load_vec<W, V>(static_cast<const W*>(a.w) + c * V, by);
+      t = weigh(y, by);
+    }
     if constexpr (EIGHT == 1) top = max(top, t);
-    if constexpr (EIGHT == 2) into_group(t, c);  // such rows take no shuffles
+    if constexpr (EIGHT == 2) into_group(t, c, c < a.chunks);  // such rows take no shuffles
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if constexpr (EIGHT == 1) top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) {
-    s_sum[warp] = sum;
-    if constexpr (EIGHT == 1) s_top[warp] = top;
-  }
-  __syncthreads();
-  const int warps = threads >> 5;
-  sum = lane < warps ? s_sum[lane] : 0.0f;
+  if (warps > 1 || EIGHT == 2) {
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      if constexpr (EIGHT == 1) s_top[warp] = top;
+    }
+    __syncthreads();
+    sum = lane < warps ? s_sum[lane] : 0.0f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if constexpr (EIGHT == 1) top = __reduce_max_sync(0xffffffffu, lane < warps ? s_top[lane] : 0u);
+  }
   const float factor = 1.0f / sqrtf(fmaf(sum, a.inv_d, a.eps));
   float scale = 0.0f;
-  auto scale_of = [&](uint32_t t) {
-    const float s = __uint_as_float(t) * factor / kLargest;
-    return s < kLeastScale ? kLeastScale : s;  // a NaN stays
-  };
   if constexpr (EIGHT == 1) {
-    top = __reduce_max_sync(0xffffffffu, lane < warps ? s_top[lane] : 0u);
-    scale = scale_of(top);
+    scale = scale_of(top, factor);
     if (tid == 0) a.scale[row] = scale;
   }
-  auto put = [&](float (&x)[V], int c, uint32_t t) {  // x = h w
+  if constexpr (EIGHT == 2) {
+    if (!a.lanes) {  // the groups' scales once each, and their inverses
+      for (int g = tid; g < a.groups; g += threads) {
+        const float s = scale_of(s_group[g], factor);
+        a.scale[row * a.groups + g] = s;
+        s_group[g] = __float_as_uint(__fdividef(1.0f, s));
+      }
+      __syncthreads();
+    }
+  }
+  auto put = [&](float (&y)[V], int c, uint32_t t) {  // y = h w
     if constexpr (EIGHT == 0) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) x[j] *= factor;
-      store_vec<T, V>(static_cast<T*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, x);
+      for (int j = 0; j < V; ++j) y[j] *= factor;
+      store_vec<T, V>(static_cast<T*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, y);
     } else {
-      float s = scale;
-      if constexpr (EIGHT == 2) {
-        const int g = a.lanes ? c >> a.shift : c * V / a.group;
-        s = scale_of(a.lanes ? t : s_group[g]);
-        if (c * V == g * a.group) a.scale[row * a.groups + g] = s;
+      float by;
+      if (EIGHT == 1 || a.lanes) {
+        float s = scale;
+        if constexpr (EIGHT == 2) {
+          s = scale_of(t, factor);
+          if ((c & (a.lanes - 1)) == 0) a.scale[row * a.groups + (c >> a.shift)] = s;
+        }
+        // one division a chunk: y times the inverse is off by 2^-24 before it is rounded to 4 bits
+        by = __fdividef(1.0f, s);
+      } else {
+        by = __uint_as_float(s_group[group_of(c)]);
       }
-      // one division a chunk: y times the inverse is off by 2^-24 before it is rounded to 4 bits
-      const float inv = 1.0f / s;
 #pragma unroll
-      for (int j = 0; j < V; ++j) x[j] = x[j] * factor * inv;
-      store_e4m3<V>(static_cast<uint8_t*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, x);
+      for (int j = 0; j < V; ++j) y[j] = y[j] * factor * by;
+      store_e4m3<V>(static_cast<uint8_t*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, y);
     }
   };
 #pragma unroll
@@ -239,12 +313,131 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
   }
 #pragma unroll 1
   for (int c = HELD * threads + tid; c < a.chunks; c += threads) {
-    float x[V], w[V];
-    load_h<T, V>(a, row, c, true, x);
-    load_w<V, W32>(a, c, w);
+    Raw<T, V> p;
+    float y[V], by[V];
+    // the stream as it was stored: r_out may be x or r
+    load_raw<T, V>(a.r ? static_cast<const T*>(a.r_out) + row * a.r_out_row + static_cast<int64_t>(c) * V
+                       : static_cast<const T*>(a.x) + row * a.x_row + static_cast<int64_t>(c) * V, p);
+    load_vec<W, V>(static_cast<const W*>(a.w) + c * V, by);
 #pragma unroll
-    for (int j = 0; j < V; ++j) x[j] *= w[j];
-    put(x, c, 0);
+    for (int j = 0; j < V; ++j) y[j] = element<T, V>(p, j) * by[j];
+    put(y, c, 0);
+  }
+}
+
+// ---- Many rows: a block stays on an SM, with teams of TEAM warps, and the rows of a team come by bulk copies into a ring of
+// its own, so that what is in flight does not go by the registers that wait for it.
+constexpr int kRingThreads = 1024, kHeld = 4;    // chunks of a row that a thread holds
+constexpr int kRingBytes = 200 * 1024;
+constexpr int kRingRows = 2;  // rows a team, at least
+template <int TEAM>
+struct Ring {
+  static constexpr int kTeams = kRingThreads / 32 / TEAM, kThreads = 32 * TEAM, kMost = 8;  // rows in a team's ring
+};
+
+template <typename T, int EIGHT, int TEAM>
+__global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_constant__ NormArgs a) {
+  using R = Ring<TEAM>;
+  constexpr int V = 16 / sizeof(T);
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t s_bar[R::kTeams * R::kMost];
+  __shared__ float s_sum[2][R::kTeams][TEAM];
+  __shared__ uint32_t s_top[2][R::kTeams][TEAM];
+  __shared__ int s_abort;
+  const int team = threadIdx.x / R::kThreads, tid = threadIdx.x % R::kThreads, lane = tid & 31, warp = tid >> 5;
+  const uint32_t row_bytes = static_cast<uint32_t>(a.d) * sizeof(T), slot_bytes = a.r ? 2 * row_bytes : row_bytes;
+  const uint32_t ring = smem_u32(smem) + team * a.slots * slot_bytes, bars = smem_u32(s_bar) + team * R::kMost * 8;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R::kTeams * R::kMost; ++i) mbar_init(smem_u32(s_bar) + 8 * i, 1);
+    s_abort = 0;
+    mbar_fence_init();
+  }
+  __syncthreads();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * R::kTeams;
+  auto fetch = [&](int64_t row, int slot) {  // by one thread
+    const uint32_t dst = ring + slot * slot_bytes, b = bars + 8 * slot;
+    mbar_arrive_expect_tx(b, slot_bytes);
+    bulk_load(dst, static_cast<const T*>(a.x) + row * a.x_row, row_bytes, b);
+    if (a.r) bulk_load(dst + row_bytes, static_cast<const T*>(a.r) + row * a.r_row, row_bytes, b);
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * R::kTeams + team;
+  if (tid == 0)
+    for (int i = 0; i < a.slots && row + i * step < a.n; ++i) fetch(row + i * step, i);
+  uint32_t slot = 0, parity = 0;
+  int side = 0;
+#pragma unroll 1
+  for (; row < a.n; row += step, side ^= 1) {
+    // where the wait runs out the row is left out, and the team stays together
+    const bool ok = mbar_wait(bars + 8 * slot, parity, &s_abort);
+    if (!ok && a.err) atomicOr(a.err, kErrTimeout);
+    const int chunks = ok ? a.chunks : 0;
+    const uint8_t* here = smem + (ring - smem_u32(smem)) + slot * slot_bytes;
+    float h[kHeld][V], sum = 0.0f;
+    uint32_t top = 0, mine[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (i * R::kThreads >= a.chunks) break;
+      const int c = i * R::kThreads + tid;
+      mine[i] = 0;
+      if (c < chunks) {
+        Raw<T, V> x, r;
+        float w[V];
+        load_raw<T, V>(reinterpret_cast<const T*>(here) + c * V, x);
+        if (a.r) load_raw<T, V>(reinterpret_cast<const T*>(here + row_bytes) + c * V, r);
+        make_h<T, V>(a, row, c, x, r, h[i]);
+        if (a.w32) load_vec<float, V>(static_cast<const float*>(a.w) + c * V, w);
+        else load_vec<uint16_t, V>(static_cast<const uint16_t*>(a.w) + c * V, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          sum = fmaf(h[i][j], h[i][j], sum);
+          h[i][j] *= w[j];
+          if constexpr (EIGHT != 0) mine[i] = max(mine[i], __float_as_uint(h[i][j]) & 0x7fffffffu);
+        }
+        if constexpr (EIGHT == 1) top = max(top, mine[i]);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if constexpr (EIGHT == 1) top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) {
+      s_sum[side][team][warp] = sum;
+      if constexpr (EIGHT == 1) s_top[side][team][warp] = top;
+    }
+    if constexpr (TEAM == 1) __syncwarp();
+    else named_barrier(team, R::kThreads);  // and the row has been read
+    if (tid == 0 && ok && row + a.slots * step < a.n) fetch(row + a.slots * step, slot);
+    if (++slot == static_cast<uint32_t>(a.slots)) slot = 0, parity ^= 1;
+    sum = lane < TEAM ? s_sum[side][team][lane] : 0.0f;
+#pragma unroll
+    for (int o = TEAM / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum = __shfl_sync(0xffffffffu, sum, 0);
+    const float factor = 1.0f / sqrtf(fmaf(sum, a.inv_d, a.eps));
+    float scale = 0.0f;
+    if constexpr (EIGHT == 1) {
+      scale = scale_of(__reduce_max_sync(0xffffffffu, lane < TEAM ? s_top[side][team][lane] : 0u), factor);
+      if (tid == 0 && ok) a.scale[row] = scale;
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (i * R::kThreads >= a.chunks) break;
+      const int c = i * R::kThreads + tid;
+      if constexpr (EIGHT == 2) {
+        for (int o = a.lanes / 2; o; o >>= 1) mine[i] = max(mine[i], __shfl_xor_sync(0xffffffffu, mine[i], o));
+        scale = scale_of(mine[i], factor);
+        if (c < chunks && (c & (a.lanes - 1)) == 0) a.scale[row * a.groups + (c >> a.shift)] = scale;
+      }
+      if (c >= chunks) continue;
+      if constexpr (EIGHT == 0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[i][j] *= factor;
+        store_vec<T, V>(static_cast<T*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, h[i]);
+      } else {
+        const float by = __fdividef(1.0f, scale);
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[i][j] = h[i][j] * factor * by;
+        store_e4m3<V>(static_cast<uint8_t*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, h[i]);
+      }
+    }
   }
 }
 
@@ -272,11 +465,50 @@ void launch(const NormArgs& a, int threads, int eight, cudaStream_t st) {
 }
 
 template <typename T, bool W32>
-void launch_width(int v, const NormArgs& a, int threads, int eight, cudaStream_t st) {
+void launch_width(int v, int held, const NormArgs& a, int threads, int eight, cudaStream_t st) {
   constexpr int kMost = 16 / sizeof(T);
-  if (v == kMost) return launch<T, kMost, 2, W32>(a, threads, eight, st);
+  if (v == kMost) return held == 1 ? launch<T, kMost, 1, W32>(a, threads, eight, st) : launch<T, kMost, 2, W32>(a, threads, eight, st);
   if (v > 1) return launch<T, 2, 4, W32>(a, threads, eight, st);
   launch<T, 1, 8, W32>(a, threads, eight, st);
+}
+
+template <typename T, int EIGHT, int TEAM>
+cudaError_t launch_ring(const NormArgs& a, int grid, int bytes, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(ring_kernel<T, EIGHT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e != cudaSuccess) return e;
+  ring_kernel<T, EIGHT, TEAM><<<grid, kRingThreads, bytes, st>>>(a);
+  return cudaSuccess;
+}
+template <typename T, int TEAM>
+cudaError_t launch_ring_kind(const NormArgs& a, int eight, int grid, int bytes, cudaStream_t st) {
+  if (eight == 0) return launch_ring<T, 0, TEAM>(a, grid, bytes, st);
+  if (eight == 1) return launch_ring<T, 1, TEAM>(a, grid, bytes, st);
+  return launch_ring<T, 2, TEAM>(a, grid, bytes, st);
+}
+// The rows' ring, where they suit it: whether it was launched (or failed). Teams are as small as hold a row and leave
+// a ring of two.
+template <typename T>
+bool try_ring(NormArgs a, int v, int eight, int sms, cudaStream_t st, cudaError_t* e) {
+  *e = cudaSuccess;
+  if (v != static_cast<int>(16 / sizeof(T)) || (eight == 2 && !a.lanes)) return false;
+  const int64_t row = static_cast<int64_t>(a.d) * sizeof(T) * (a.r ? 2 : 1);
+  int team = 1;
+  for (; team <= 32; team *= 2) {
+    a.slots = static_cast<int>(std::min<int64_t>(Ring<1>::kMost, kRingBytes / (row * (kRingThreads / 32 / team))));
+    if (a.chunks <= kHeld * 32 * team && a.slots >= 2) break;
+  }
+  const int teams = kRingThreads / 32 / team;
+  if (team > 32 || a.n < static_cast<int64_t>(kRingRows) * teams * sms) return false;
+  const int bytes = static_cast<int>(row * teams * a.slots);
+  switch (team) {
+    case 1: *e = launch_ring_kind<T, 1>(a, eight, sms, bytes, st); break;
+    case 2: *e = launch_ring_kind<T, 2>(a, eight, sms, bytes, st); break;
+    case 4: *e = launch_ring_kind<T, 4>(a, eight, sms, bytes, st); break;
+    case 8: *e = launch_ring_kind<T, 8>(a, eight, sms, bytes, st); break;
+    case 16: *e = launch_ring_kind<T, 16>(a, eight, sms, bytes, st); break;
+    default: *e = launch_ring_kind<T, 32>(a, eight, sms, bytes, st);
+  }
+  return true;
 }
 
 }  // namespace
@@ -285,7 +517,7 @@ void launch_width(int v, const NormArgs& a, int threads, int eight, cudaStream_t
 extern "C" int dflash_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const void* weight,
                                void* residual_out, int64_t residual_out_stride, void* out, int64_t out_stride, float* scales,
                                int64_t n, int d, int dtype, int weight_dtype, int out_dtype, int group_size, float eps,
-                               dflash_stream_t stream) {
+                               int32_t* status, dflash_stream_t stream) {
   using namespace dflash;
   if (dtype != DFLASH_OUT_BF16 && dtype != DFLASH_OUT_F32)
     return errorf(DFLASH_ERR_INVALID_ARG, "dtype %d is neither DFLASH_OUT_BF16 nor DFLASH_OUT_F32", dtype);
@@ -341,21 +573,29 @@ extern "C" int dflash_rms_norm(const void* x, int64_t x_stride, const void* resi
   a.x = x, a.r = residual, a.w = weight, a.r_out = residual_out, a.out = out, a.scale = scales;
   a.x_row = x_stride, a.r_row = residual_stride, a.r_out_row = residual_out_stride, a.out_row = out_stride;
   a.n = n, a.d = d, a.chunks = d / v, a.group = group, a.groups = groups;
+  a.err = reinterpret_cast<uint32_t*>(status);
   a.eps = eps, a.inv_d = static_cast<float>(1.0 / d);
-  const int held = v == 1 ? 8 : v == 2 ? 4 : 2;
+  const int held = v == 1 ? 8 : v == 2 ? 4 : a.chunks <= 1024 ? 1 : 2;
   const int threads = std::min(1024, std::max(32, ((a.chunks + held - 1) / held + 31) / 32 * 32));
   const int lanes = group % v ? 0 : group / v;
   if (eight && group_size && lanes >= 1 && lanes <= 32 && (lanes & (lanes - 1)) == 0 && a.chunks <= held * threads) {
     a.lanes = lanes;
     while ((1 << a.shift) < lanes) ++a.shift;
   }
+  divide_by_page(group, &a.group_mul, &a.group_shift);
+  a.warp_groups = lanes > 0 && lanes % 32 == 0;
   const int kind = !eight ? 0 : group_size ? 2 : 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (es == 4)
-    ws == 4 ? launch_width<float, true>(v, a, threads, kind, st) : launch_width<float, false>(v, a, threads, kind, st);
-  else
-    ws == 4 ? launch_width<uint16_t, true>(v, a, threads, kind, st) : launch_width<uint16_t, false>(v, a, threads, kind, st);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  a.w32 = ws == 4;
+  const bool ring = es == 4 ? try_ring<float>(a, v, kind, sms, st, &e) : try_ring<uint16_t>(a, v, kind, sms, st, &e);
+  if (!ring) {
+    if (es == 4)
+      ws == 4 ? launch_width<float, true>(v, held, a, threads, kind, st) : launch_width<float, false>(v, held, a, threads, kind, st);
+    else
+      ws == 4 ? launch_width<uint16_t, true>(v, held, a, threads, kind, st) : launch_width<uint16_t, false>(v, held, a, threads, kind, st);
+  }
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "rms norm launch: %s", cudaGetErrorString(e));
   return report_error(DFLASH_OK, "");
 }

@@ -37,7 +37,7 @@ def declare(lib) -> None:
                                 P, I64, I64, I32, I32, P, F64, I32, I32, I32, P, P]),
         "dflash_rotary_axes": (I32, [P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, P,
                                      I64, I32, P, P, I64, I64, I32, I32, P, F64, I32, I32, I32, P, P]),
-        "dflash_rms_norm": (I32, [P, I64, P, I64, P, P, I64, P, I64, P, I64, I32, I32, I32, I32, I32, F32, P]),
+        "dflash_rms_norm": (I32, [P, I64, P, I64, P, P, I64, P, I64, P, I64, I32, I32, I32, I32, I32, F32, P, P]),
         "dflash_shared_prefixes": (I32, [P, I64, P, P, I32, I32, I32, I32, P, P, P]),
         "dflash_decode_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32]),
         "dflash_decode_attention_paged": (I32, [P, I64, P, P, P, I64, P, I32, I32, I32, I32, I64, I32, I32, I32, F32, I32,
@@ -208,7 +208,7 @@ def rotary_axes(q, positions, axes, inv_freq, *, k=None, v=None, q_out=None, k_o
 
 # ------------------------------------------------------------------------------------- norm
 def rms_norm(x, weight, *, residual=None, out_dtype=None, group_size=0, eps=1e-6, out=None, residual_out=None, scales=None,
-             stream=None):
+             status=None, stream=None):
     """RMS norm of x [n, d] (bf16 or f32), or of x + residual; returns (out, residual_out, scales).
 
     h = x + residual, rounded to their type, is residual_out (None without a residual) and what is normed:
@@ -221,8 +221,8 @@ def rms_norm(x, weight, *, residual=None, out_dtype=None, group_size=0, eps=1e-6
     if stream is not None:
         with _on(stream, x):
             return rms_norm(x, weight, residual=residual, out_dtype=out_dtype, group_size=group_size, eps=eps, out=out,
-                            residual_out=residual_out, scales=scales)
-    got = bind.rms_norm(x, weight, residual, out_dtype, group_size, eps, out, residual_out, scales)
+                            residual_out=residual_out, scales=scales, status=status)
+    got = bind.rms_norm(x, weight, residual, out_dtype, group_size, eps, out, residual_out, scales, status)
     if type(got) is int:
         _fail(got)
     return got

@@ -191,3 +191,20 @@ def test_no_rows_streams_versions_and_graphs():
     assert torch.equal(out, want[0]) and torch.equal(stream, want[1])
     g.replay()
     assert torch.equal(stream, (want[1].float() + x.float()).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("f32,d", [(False, 5120), (False, 256), (False, 8192), (False, 16384), (False, 1032), (True, 4096), (True, 128), (True, 12000)])
+@pytest.mark.parametrize("eight,group", [(False, 0), (True, 0), (True, 128), (True, 16), (True, 80)])
+def test_many_rows(f32, d, eight, group, residual):
+    import torch
+    n = 3001
+    x, r, w = inputs(n, d, f32, seed=d + group)
+    kw = dict(out_dtype=D().OUT_E4M3, group_size=group) if eight else {}
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = D().rms_norm(x, w, residual=r if residual else None, status=status, **kw)
+    check(got, x, r if residual else None, w, group)
+    assert status.item() == 0
+    y, s = x.clone(), r.clone()  # in place
+    out, stream, _ = D().rms_norm(y, w, residual=s, residual_out=s, out=None if eight else y, **kw)
+    check((out, stream, _), x, r, w, group)

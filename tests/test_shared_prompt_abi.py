@@ -15,7 +15,7 @@ def P(x):
 
 def _norm(x=P(1 << 20), xs=64, r=None, rs=64, w=P(1 << 12), ro=None, ros=64, out=P(2 << 20), outs=64, scales=None, n=4, d=64, dt=0, wdt=0, odt=0, group=0,
           eps=1e-6):
-    return D.load().dflash_rms_norm(x, xs, r, rs, w, ro, ros, out, outs, scales, n, d, dt, wdt, odt, group, eps, None)
+    return D.load().dflash_rms_norm(x, xs, r, rs, w, ro, ros, out, outs, scales, n, d, dt, wdt, odt, group, eps, None, None)
 
 
 @pytest.mark.parametrize("kw,code", [
