@@ -151,6 +151,12 @@ __device__ __forceinline__ float element(const Raw<T, V>& x, int i) {
   else return (i & 1) ? bf16hi_to_f32(x.w[i / 2]) : bf16lo_to_f32(x.w[i / 2]);
 }
 
+template <typename T>
+__device__ __forceinline__ float rounded_as(float x) {
+  if constexpr (sizeof(T) == 4) return x;
+  else return bf16lo_to_f32(pack_bf16x2(x, 0.0f));
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void load_in(const NormArgs& a, int64_t row, int c, Raw<T, V>& x, Raw<T, V>& r) {
   load_raw<T, V>(static_cast<const T*>(a.x) + row * a.x_row + static_cast<int64_t>(c) * V, x);
@@ -441,6 +447,140 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
   }
 }
 
+// ---- Rows whose width is no multiple of a 16-byte chunk, so that each begins somewhere else in one: chunks are cut where memory
+// is aligned, columns c V - shift on, and only those at a row's ends go element by element. Weights and groups go by columns:
+// the weights one by one (from L1), and a chunk may have the end of one group and the beginning of the next.
+constexpr int kShiftedHeld = 2;
+
+template <typename T, int EIGHT>
+__global__ void __launch_bounds__(1024) shifted_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int V = 16 / sizeof(T);
+  __shared__ float s_sum[32];
+  __shared__ uint32_t s_top[32];
+  __shared__ uint32_t s_group[EIGHT == 2 ? kMaxGroups : 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
+  const int64_t row = blockIdx.x;
+  const int shift = static_cast<int>(static_cast<uint64_t>(row * a.x_row) % V);
+  const T* x_row = static_cast<const T*>(a.x) + row * a.x_row;
+  const T* r_row = static_cast<const T*>(a.r) + (a.r ? row * a.r_row : 0);
+  T* r_out = static_cast<T*>(a.r_out) + (a.r ? row * a.r_out_row : 0);
+  if constexpr (EIGHT == 2) {
+    for (int i = tid; i < a.groups; i += threads) s_group[i] = 0;
+    __syncthreads();
+  }
+  float h[kShiftedHeld][V], sum = 0.0f;
+  uint32_t top = 0;
+  auto edge = [&](int c0) { return c0 < 0 || c0 + V > a.d; };
+#pragma unroll
+  for (int i = 0; i < kShiftedHeld; ++i) {
+    const int c0 = (i * threads + tid) * V - shift;
+    if (c0 >= a.d) continue;
+    Raw<T, V> x{}, r{};
+    if (!edge(c0)) {
+      load_raw<T, V>(x_row + c0, x);
+      if (a.r) load_raw<T, V>(r_row + c0, r);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) h[i][j] = element<T, V>(x, j);
+    if (edge(c0)) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = c0 + j;
+        if (c < 0 || c >= a.d) continue;
+        Raw<T, 1> x1, r1;
+        float y[1];
+        load_raw<T, 1>(x_row + c, x1);
+        if (a.r) load_raw<T, 1>(r_row + c, r1);
+        make_h<T, 1>(a, row, c, x1, r1, y);
+        h[i][j] = y[0];
+      }
+    } else if (a.r) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) h[i][j] = rounded_as<T>(h[i][j] + element<T, V>(r, j));
+      store_vec<T, V>(r_out + c0, h[i]);
+    }
+    uint32_t t[2] = {0, 0};  // largest |h w| of the group that begins the chunk, and of the next
+    int g = 0, next = V;
+    if constexpr (EIGHT == 2) g = divided(max(c0, 0), a.group_mul, a.group_shift), next = (g + 1) * a.group - c0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = c0 + j;
+      const float y = h[i][j];
+      float w = 0.0f;
+      if (c >= 0 && c < a.d) w = a.w32 ? static_cast<const float*>(a.w)[c] : bf16lo_to_f32(static_cast<const uint16_t*>(a.w)[c]);
+      sum = fmaf(y, y, sum);
+      h[i][j] = y * w;
+      if constexpr (EIGHT != 0) {
+        const uint32_t u = __float_as_uint(h[i][j]) & 0x7fffffffu;
+        if (j < next) t[0] = max(t[0], u);
+        else t[1] = max(t[1], u);
+      }
+    }
+    if constexpr (EIGHT == 1) top = max(top, t[0]);
+    if constexpr (EIGHT == 2) {
+      atomicMax(&s_group[g], t[0]);
+      if (next < V && c0 + next < a.d) atomicMax(&s_group[g + 1], t[1]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if constexpr (EIGHT == 1) top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) {
+    s_sum[warp] = sum;
+    if constexpr (EIGHT == 1) s_top[warp] = top;
+  }
+  __syncthreads();
+  sum = lane < warps ? s_sum[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float factor = 1.0f / sqrtf(fmaf(sum, a.inv_d, a.eps));
+  float by = 1.0f;
+  if constexpr (EIGHT == 1) {
+    const float s = scale_of(__reduce_max_sync(0xffffffffu, lane < warps ? s_top[lane] : 0u), factor);
+    if (tid == 0) a.scale[row] = s;
+    by = __fdividef(1.0f, s);
+  }
+  if constexpr (EIGHT == 2) {
+    for (int g = tid; g < a.groups; g += threads) {
+      const float s = scale_of(s_group[g], factor);
+      a.scale[row * a.groups + g] = s;
+      s_group[g] = __float_as_uint(__fdividef(1.0f, s));
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < kShiftedHeld; ++i) {
+    const int c0 = (i * threads + tid) * V - shift;
+    if (c0 >= a.d) continue;
+    float by_next = by;
+    int next = V;
+    if constexpr (EIGHT == 2) {
+      const int g = divided(max(c0, 0), a.group_mul, a.group_shift);
+      next = (g + 1) * a.group - c0;
+      by = __uint_as_float(s_group[g]);
+      by_next = next < V && c0 + next < a.d ? __uint_as_float(s_group[g + 1]) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      h[i][j] *= factor;
+      if constexpr (EIGHT != 0) h[i][j] *= j < next ? by : by_next;
+    }
+    if (!edge(c0)) {
+      if constexpr (EIGHT == 0) store_vec<T, V>(static_cast<T*>(a.out) + row * a.out_row + c0, h[i]);
+      else store_e4m3<V>(static_cast<uint8_t*>(a.out) + row * a.out_row + c0, h[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = c0 + j;
+        if (c < 0 || c >= a.d) continue;
+        const float y[1] = {h[i][j]};
+        if constexpr (EIGHT == 0) store_vec<T, 1>(static_cast<T*>(a.out) + row * a.out_row + c, y);
+        else store_e4m3<1>(static_cast<uint8_t*>(a.out) + row * a.out_row + c, y);
+      }
+    }
+  }
+}
+
 // Bytes [lo, hi) of n rows of a strided tensor.
 struct Range {
   uintptr_t at;
@@ -470,6 +610,22 @@ void launch_width(int v, int held, const NormArgs& a, int threads, int eight, cu
   if (v == kMost) return held == 1 ? launch<T, kMost, 1, W32>(a, threads, eight, st) : launch<T, kMost, 2, W32>(a, threads, eight, st);
   if (v > 1) return launch<T, 2, 4, W32>(a, threads, eight, st);
   launch<T, 1, 8, W32>(a, threads, eight, st);
+}
+
+// Rows that begin anywhere in a chunk: whether they were launched. Every tensor's rows must begin at the same place.
+template <typename T>
+bool try_shifted(const NormArgs& a, int v, int eight, int out_size, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const int chunks = a.d / V + 2, threads = std::min(1024, (chunks + 32 * kShiftedHeld - 1) / (32 * kShiftedHeld) * 32);
+  if (v >= V || a.d < 4 * V || chunks > kShiftedHeld * 1024) return false;
+  auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  if (at(a.x) % 16 || at(a.out) % (V * out_size) || a.out_row % V != a.x_row % V) return false;
+  if (a.r && (at(a.r) % 16 || at(a.r_out) % 16 || a.r_row % V != a.x_row % V || a.r_out_row % V != a.x_row % V)) return false;
+  const unsigned grid = static_cast<unsigned>(a.n);
+  if (eight == 0) shifted_kernel<T, 0><<<grid, threads, 0, st>>>(a);
+  else if (eight == 1) shifted_kernel<T, 1><<<grid, threads, 0, st>>>(a);
+  else shifted_kernel<T, 2><<<grid, threads, 0, st>>>(a);
+  return true;
 }
 
 template <typename T, int EIGHT, int TEAM>
@@ -589,7 +745,7 @@ extern "C" int dflash_rms_norm(const void* x, int64_t x_stride, const void* resi
   cudaError_t e = cudaSuccess;
   a.w32 = ws == 4;
   const bool ring = es == 4 ? try_ring<float>(a, v, kind, sms, st, &e) : try_ring<uint16_t>(a, v, kind, sms, st, &e);
-  if (!ring) {
+  if (!ring && !(es == 4 ? try_shifted<float>(a, v, kind, static_cast<int>(os), st) : try_shifted<uint16_t>(a, v, kind, static_cast<int>(os), st))) {
     if (es == 4)
       ws == 4 ? launch_width<float, true>(v, held, a, threads, kind, st) : launch_width<float, false>(v, held, a, threads, kind, st);
     else

@@ -208,3 +208,24 @@ def test_many_rows(f32, d, eight, group, residual):
     y, s = x.clone(), r.clone()  # in place
     out, stream, _ = D().rms_norm(y, w, residual=s, residual_out=s, out=None if eight else y, **kw)
     check((out, stream, _), x, r, w, group)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("d", [33, 65, 127, 1001, 2562, 5003, 8191, 8193, 16383, 16385])
+@pytest.mark.parametrize("eight,group", [(False, 0), (True, 0), (True, 16), (True, 112), (True, 128)])
+def test_odd_widths(d, f32, eight, group, residual):
+    import torch
+    n = 37
+    x, r, w = inputs(n, d, f32, w32=d % 4 == 1, seed=d + group)
+    kw = dict(out_dtype=D().OUT_E4M3, group_size=group) if eight else {}
+    check(D().rms_norm(x, w, residual=r if residual else None, **kw), x, r if residual else None, w, group)
+    y, s = x.clone(), r.clone()  # in place
+    out, stream, _ = D().rms_norm(y, w, residual=s, residual_out=s, out=None if eight else y, **kw)
+    check((out, stream, _), x, r, w, group)
+    wide = torch.zeros(n, d + 8, device="cuda", dtype=x.dtype)  # rows that lie elsewhere in the stream than in x
+    out, stream, _ = D().rms_norm(x, w, residual=r, residual_out=wide[:, 3:3 + d], **kw)
+    check((out, stream, _), x, r, w, group)
+    assert not wide[:, :3].any() and not wide[:, 3 + d:].any()
+    out, stream, _ = D().rms_norm(x[:1].expand(n, d), w, residual=r, **kw)
+    check((out, stream, _), x[:1].expand(n, d), r, w, group)
