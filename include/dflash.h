@@ -70,7 +70,8 @@ enum {
 
 enum {
   DFLASH_FLAG_FORCE_SPLIT = 1,   /* always split each request's keys over several CTAs  */
-  DFLASH_FLAG_NO_SPLIT = 2       /* never split (one CTA per request x kv head x q tile)*/
+  DFLASH_FLAG_NO_SPLIT = 2,      /* never split (one CTA per request x kv head x q tile)*/
+  DFLASH_FLAG_FORCE_SHARE = 4    /* dflash_decode_attention_shared: share however few rows the call reads */
 };
 
 /* Message describing the last failing call on this thread ("" after success). */
@@ -599,6 +600,8 @@ DFLASH_API size_t dflash_shared_workspace_size(int num_reqs, int num_groups, int
  *              least that long lie in the same pages (dflash_shared_prefixes; any shorter prefix does too). They
  *              are read in the pages of the shortest such sequence. Shorter sequences of the group read their own
  *              rows. Negative or above max_ctx_len: reported and treated as 0.
+ *   flags      0 or DFLASH_FLAG_FORCE_SHARE. Without it, calls that could read at most 160 MB if every sequence read its own
+ *              rows (num_reqs x Hkv x Dh x 4 bytes x max_ctx_len, or the window) let them do so, and only report bad groups.
  *   Every other argument, and the result, as dflash_decode_attention_paged (the workspace as
  *   dflash_shared_workspace_size says). The result does not depend on timing; another prefix gives another order of the
  *   sums. What a row of the prefix holds that only some of the group's windows reach must be finite for the others
@@ -612,7 +615,8 @@ DFLASH_API int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_st
                                               int num_groups, int hq, int hkv, int dh, int64_t num_pages, int page_size,
                                               int max_pages_per_req, int max_ctx_len, float scale, int window,
                                               int out_dtype, void* out, float* lse, void* workspace,
-                                              size_t workspace_bytes, int32_t* status, dflash_stream_t stream);
+                                              size_t workspace_bytes, int flags, int32_t* status,
+                                              dflash_stream_t stream);
 
 /*
  * Reads the device error word the last dflash_block_attention call on this workspace

@@ -394,7 +394,7 @@ PyObject* shared_prefixes(PyObject* const* a) {
 }
 
 // q, k_pool, v_pool, block_table, seq_lens, max_ctx_len, out, lse, return_lse, workspace, scale, window, out_dtype, status
-// and of a call that shares prefixes: group_start_loc, prefix_lens
+// and of a call that shares prefixes: group_start_loc, prefix_lens, flags
 template <bool SHARED>
 PyObject* decode_attention(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q");
@@ -420,8 +420,9 @@ PyObject* decode_attention(PyObject* const* a) {
   const int longest = small(a[5], "max_ctx_len"), window = small(a[11], "window");
   const float scale = static_cast<float>(number(a[10]));
   const int32_t *starts = nullptr, *prefixes = nullptr;
-  int groups = 0;
+  int groups = 0, flags = 0;
   if constexpr (SHARED) {
+    flags = small(a[16], "flags");
     const at::Tensor& t = tensor(a[14], "group_start_loc");
     if (t.dim() != 1 || t.size(0) < 1) raise(PyExc_ValueError, "group_start_loc must be [groups + 1]");
     groups = dim32(t.size(0) - 1, "groups");
@@ -445,7 +446,7 @@ PyObject* decode_attention(PyObject* const* a) {
     const int64_t q_stride = n > 1 ? q.stride(0) : static_cast<int64_t>(hq) * dh, table_stride = n > 1 ? table.stride(0) : width;
     if constexpr (SHARED)
       return dflash_decode_attention_shared(pq, q_stride, pk, pv, pt, table_stride, pl, starts, prefixes, n, groups, hq, hkv, dh, kp.size(0), page,
-                                            width, longest, scale, window, dtype, out, lse, ws.p, ws.bytes, status, stream);
+                                            width, longest, scale, window, dtype, out, lse, ws.p, ws.bytes, flags, status, stream);
     return dflash_decode_attention_paged(pq, q_stride, pk, pv, pt, table_stride, pl, n, hq, hkv, dh, kp.size(0), page, width, longest, scale,
                                          window, dtype, out, lse, ws.p, ws.bytes, status, stream);
   });
@@ -640,7 +641,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define ENTRY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(rotary, 13),       ENTRY(decode_attention_paged, 14), ENTRY(beam_select, 10), ENTRY(fork_pages, 5),
                          ENTRY(reserve_pages, 12), ENTRY(compact_pages, 6),           ENTRY(rotary_axes, 14), ENTRY(rms_norm, 10),
-                         ENTRY(shared_prefixes, 6), ENTRY(decode_attention_shared, 16), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(shared_prefixes, 6), ENTRY(decode_attention_shared, 17), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_decode_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -22,6 +22,10 @@ constexpr int kRows = 128;   // (sequence, head) pairs of a unit: the lanes of t
 constexpr int kPlanThreads = 1024;
 // A prefix of fewer rows is left to the sequences: half a tile.
 constexpr int kLeastPrefix = 64;
+// Calls that read no more than this when each sequence reads its own rows do so: the shared rows come from L2 then, and
+// the launches here take longer. 4 x 4 sequences of 1000 rows (62 MB): 19 us each for itself, 29 shared; of 2000 27 and 31, of
+// 4000 43 and 36; 64 sequences of 2000 rows of 2 kv heads (125 MB) 27 and 31, of 4000 42 and 33.
+constexpr int64_t kAloneBytes = 160 << 20;
 
 // Blocks take ranges of equal cost: a tile's is kTileCost, and a unit's start (its queries, the sums of the one before
 // written out, the ends of prefixes that are no whole tiles) takes kUnitCost more. Where there are fewer than
@@ -603,9 +607,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     Unit u;
     uint32_t t = 0;
     while (ok && walk.next(u)) {
-      // the rows of the prefix that this thread's sequence sees, from lo on
+      // the rows of the prefix that this thread's sequence sees, from lo on. Lanes without a sequence that shares see all of
+      // them: what they get is not used, and masks cost a warp more than its products (8 rows of 32 lanes: 9200 cycles a tile, 4400)
       const int at = u.m0 + row;
-      int from = 0x7fffffff;
+      int from = 0;
       if (at < u.rows) {
         const int len = valid_len(a, a.lens[u.first + divided(at, a.g_mul, a.g_shift)]);
         if (len >= u.prefix) from = first_row(a, len) - u.lo;
@@ -776,6 +781,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   if (warp == kIssuer) tmem_dealloc(tmem, 512);
 }
 
+// The groups' checks alone, for calls that do not look at them otherwise.
+__global__ void __launch_bounds__(kPlanThreads) check_kernel(const __grid_constant__ SharedArgs a) {
+  bool bad = false;
+  for (int g = threadIdx.x; g < a.num_groups; g += kPlanThreads) {
+    const int from = a.starts[g], to = a.starts[g + 1], p = a.prefixes[g];
+    bad |= from < 0 || from > to || to > a.num_reqs || p < 0 || p > a.max_len;
+  }
+  if (bad) atomicOr(a.err, kErrMetadata);
+}
+
 // Joins a head's parts, the prefix's and its own rows', and stores it; a warp a head.
 template <int DH, bool F32>
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ SharedArgs a) {
@@ -885,11 +900,12 @@ int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const
                                    const int32_t* group_start_loc, const int32_t* prefix_lens, int num_reqs, int num_groups, int hq,
                                    int hkv, int dh, int64_t num_pages, int page_size, int max_pages_per_req, int max_ctx_len, float scale,
                                    int window, int out_dtype, void* out, float* lse, void* workspace, size_t workspace_bytes,
-                                   int32_t* status, dflash_stream_t stream) {
+                                   int flags, int32_t* status, dflash_stream_t stream) {
   using namespace dflash;
   const DecodeCall c{q, q_stride, k_pool, v_pool, block_table, block_table_stride, seq_lens, num_reqs, hq, hkv, dh, num_pages, page_size,
                      max_pages_per_req, max_ctx_len, scale, window, out_dtype, out, lse, workspace, workspace_bytes, status};
   if (num_groups < 0) return errorf(DFLASH_ERR_INVALID_ARG, "negative size argument");
+  if (flags & ~DFLASH_FLAG_FORCE_SHARE) return errorf(DFLASH_ERR_INVALID_ARG, "unknown flags %d", flags);
   if (num_groups > (1 << 24)) return errorf(DFLASH_ERR_UNSUPPORTED, "more than 2^24 groups");
   int rc = check_call(c);
   if (rc != DFLASH_OK || num_reqs == 0) return rc;
@@ -926,6 +942,16 @@ int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const
   a.num_reqs = num_reqs, a.num_groups = num_groups, a.hq = hq, a.hkv = hkv;
   a.max_len = max_ctx_len, a.window = window;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Few rows, whoever shares them: each sequence reads its own
+  const int64_t longest = window > 0 ? std::min(max_ctx_len, window) : max_ctx_len;
+  if (!(flags & DFLASH_FLAG_FORCE_SHARE) && longest * num_reqs * hkv * dh * 4 <= kAloneBytes) {
+    if (status && num_groups) check_kernel<<<1, kPlanThreads, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "shared attention launch: %s", cudaGetErrorString(e));
+    return dflash_decode_attention_paged(q, q_stride, k_pool, v_pool, block_table, block_table_stride, seq_lens, num_reqs, hq, hkv, dh, num_pages,
+                                         page_size, max_pages_per_req, max_ctx_len, scale, window, out_dtype, out, lse, ws + y.rows,
+                                         workspace_bytes - y.rows, status, stream);
+  }
   plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   const bool f32 = out_dtype == DFLASH_OUT_F32;

@@ -44,7 +44,7 @@ def declare(lib) -> None:
                                                 I32, P, P, P, SZ, P, P]),
         "dflash_shared_workspace_size": (SZ, [I32] * 7),
         "dflash_decode_attention_shared": (I32, [P, I64, P, P, P, I64, P, P, P, I32, I32, I32, I32, I32, I64, I32, I32, I32, F32,
-                                                 I32, I32, P, P, P, SZ, P, P]),
+                                                 I32, I32, P, P, P, SZ, I32, P, P]),
         "dflash_beam_workspace_size": (SZ, [I32, I32, I32, I32, I32]),
         "dflash_beam_select": (I32, [P, I64, I64, P, P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, SZ, P]),
         "dflash_pages_workspace_size": (SZ, [I32, I64]),
@@ -283,22 +283,23 @@ def shared_workspace_size(num_reqs, num_groups, hq, hkv, dh, max_ctx_len, window
 
 
 def decode_attention_shared(q, k_pool, v_pool, block_table, seq_lens, group_start_loc, prefix_lens, *, max_ctx_len, out=None,
-                            lse=None, return_lse=False, workspace=None, scale=0.0, window=0, out_dtype=OUT_BF16, status=None,
-                            stream=None):
+                            lse=None, return_lse=False, workspace=None, scale=0.0, window=0, out_dtype=OUT_BF16, flags=0,
+                            status=None, stream=None):
     """`decode_attention_paged` where the rows that a group of sequences shares are read once for all of them.
 
     Group g is the sequences group_start_loc[g] .. group_start_loc[g + 1] (int32 [groups + 1]); the first prefix_lens[g]
     rows (int32 [groups], see shared_prefixes) of its sequences that are so long lie in the same pages. Everything
-    else, and the result, as in decode_attention_paged; the workspace is shared_workspace_size's.
+    else, and the result, as in decode_attention_paged; the workspace is shared_workspace_size's. Calls with few rows let
+    every sequence read its own, unless flags=FLAG_FORCE_SHARE.
     """
     bind = _bind or _load()
     if stream is not None:
         with _on(stream, q):
             return decode_attention_shared(q, k_pool, v_pool, block_table, seq_lens, group_start_loc, prefix_lens,
                                            max_ctx_len=max_ctx_len, out=out, lse=lse, return_lse=return_lse, workspace=workspace,
-                                           scale=scale, window=window, out_dtype=out_dtype, status=status)
+                                           scale=scale, window=window, out_dtype=out_dtype, flags=flags, status=status)
     got = bind.decode_attention_shared(q, k_pool, v_pool, block_table, seq_lens, int(max_ctx_len), out, lse, return_lse, workspace,
-                                       scale, int(window), out_dtype, status, group_start_loc, prefix_lens)
+                                       scale, int(window), out_dtype, status, group_start_loc, prefix_lens, flags)
     if type(got) is int:
         _fail(got)
     return got

@@ -71,11 +71,11 @@ class Batch:
     def args(self):
         return self.q, self.k, self.v, self.table, self.ln, self.st, self.px
 
-    def run(self, f32=False, longest=None, **kw):
+    def run(self, f32=False, longest=None, flags=4, **kw):
         import torch
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         got = D().decode_attention_shared(*self.args(), max_ctx_len=int(self.lens.max(initial=0)) if longest is None else longest, return_lse=True,
-                                          out_dtype=D().OUT_F32 if f32 else D().OUT_BF16, status=status, **kw)
+                                          out_dtype=D().OUT_F32 if f32 else D().OUT_BF16, status=status, flags=flags, **kw)
         self.status = status.item()
         return got
 
@@ -119,9 +119,9 @@ def check(got, b, window=0, scale=0.0, rows=None):
 ])
 def test_matches_definition(groups, ps, hq, hkv, dh, f32):
     b = Batch(groups, ps, hq, hkv, dh, seed=len(groups))
-    got = b.run(f32)
-    b.check(got)
-    assert b.status == 0
+    for flags in (D().FLAG_FORCE_SHARE, 0):
+        b.check(b.run(f32, flags=flags))
+        assert b.status == 0
 
 
 @pytest.mark.parametrize("prefix", [1, 2, 15, 16, 17, 63, 64, 65, 100, 127, 128, 129, 143, 144, 255, 256, 257, 384, 500])
@@ -197,9 +197,9 @@ def test_any_shorter_prefix_gives_the_result():
 def test_bad_groups_are_reported_and_share_nothing(starts, prefix):
     b = Batch([(300, [400, 320, 310, 330]), (300, [400, 320, 310, 300])], 16, 8, 2, 64, seed=10)
     b.st, b.px = cu(starts), cu(prefix)
-    got = b.run(True)
-    b.check(got)
-    assert b.status == D().STATUS_METADATA
+    for flags in (D().FLAG_FORCE_SHARE, 0):
+        b.check(b.run(True, flags=flags))
+        assert b.status == D().STATUS_METADATA
 
 
 def test_bad_pages_and_lengths_are_reported():
@@ -249,7 +249,8 @@ def test_one_graph_follows_lengths_prefixes_and_tables():
     out, lse = torch.empty_like(q), torch.empty(7, 8, device="cuda")
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        D().decode_attention_shared(q, k, v, table, ln, b.st, px, max_ctx_len=1401, out=out, lse=lse, workspace=ws)
+        D().decode_attention_shared(q, k, v, table, ln, b.st, px, max_ctx_len=1401, out=out, lse=lse, workspace=ws,
+                                    flags=D().FLAG_FORCE_SHARE)
     for x in (a, b, a):
         table.fill_(-1)
         table[:, :x.table.shape[1]] = x.table
@@ -270,7 +271,7 @@ def test_two_calls_at_once():
     for _ in range(10):
         got = []
         for s, st in zip(sets, streams):
-            got.append(D().decode_attention_shared(*s.args(), max_ctx_len=2800, return_lse=True, stream=st))
+            got.append(D().decode_attention_shared(*s.args(), max_ctx_len=2800, return_lse=True, stream=st, flags=4))
         torch.cuda.synchronize()
         for x, y in zip(got, want):
             assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
@@ -299,7 +300,7 @@ def test_a_smaller_batch_in_the_largest_ones_workspace():
     b.check(b.run(True, workspace=ws))
     for m in (30, 7, 1):
         out, lse = D().decode_attention_shared(b.q[:m], b.k, b.v, b.table[:m], b.ln[:m], cu([0, m]), b.px[:1], max_ctx_len=729, return_lse=True,
-                                               workspace=ws, out_dtype=D().OUT_F32)
+                                               workspace=ws, out_dtype=D().OUT_F32, flags=4)
         s = Batch.__new__(Batch)
         s.q, s.k, s.v, s.table, s.lens = b.q[:m], b.k, b.v, b.table[:m], b.lens[:m]
         s.check((out, lse))
@@ -315,6 +316,17 @@ def test_padded_and_empty_batches():
     pool, table = torch.zeros(2, 16, 2, 64, device="cuda", dtype=torch.bfloat16), torch.zeros(0, 2, device="cuda", dtype=torch.int32)
     out = D().decode_attention_shared(q, pool, pool, table, cu([]), cu([0]), cu([]), max_ctx_len=20)
     assert out.shape == (0, 8, 64)
+
+
+def test_enough_rows_to_share_unasked():
+    import torch
+    b = Batch([(2100, [2110 + i for i in range(12)]), (1500, [1600, 1700])], 16, 8, 2, 64, seed=17)
+    wide = torch.full((14, 200000 // 16), -1, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    got = b.run(longest=100000, flags=0)
+    b.check(got)
+    assert all(torch.equal(x, y) for x, y in zip(got, b.run(longest=100000)))
 
 
 def test_many_groups():

@@ -95,10 +95,10 @@ def test_bindings_refuse_what_is_no_cuda_tensor():
 
 
 def _shared(n=2, groups=1, hq=8, hkv=2, dh=64, pages=8, page=16, width=4, most=64, scale=0.0, window=0, dt=0, stride=4, qs=512, ws=256, q=P(1 << 20),
-            starts=P(4096), prefixes=P(8192)):
+            starts=P(4096), prefixes=P(8192), flags=0):
     F = P(1 << 20)
     return D.load().dflash_decode_attention_shared(q, qs, F, F, F, stride, F, starts, prefixes, n, groups, hq, hkv, dh, pages, page, width, most, scale, window,
-                                                   dt, F, None, P(ws), 0, None, None)
+                                                   dt, F, None, P(ws), 0, flags, None, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -107,7 +107,7 @@ def _shared(n=2, groups=1, hq=8, hkv=2, dh=64, pages=8, page=16, width=4, most=6
     (dict(prefixes=None), D.ERR_INVALID_ARG), (dict(page=0), D.ERR_INVALID_ARG), (dict(most=65), D.ERR_INVALID_ARG),
     (dict(window=-1), D.ERR_INVALID_ARG), (dict(scale=math.inf), D.ERR_INVALID_ARG), (dict(dt=2), D.ERR_INVALID_ARG),
     (dict(stride=3), D.ERR_INVALID_ARG), (dict(pages=0), D.ERR_INVALID_ARG), (dict(qs=100), D.ERR_INVALID_ARG), (dict(q=None), D.ERR_INVALID_ARG),
-    (dict(ws=128), D.ERR_WORKSPACE),
+    (dict(ws=128), D.ERR_WORKSPACE), (dict(flags=1), D.ERR_INVALID_ARG), (dict(flags=6), D.ERR_INVALID_ARG),
 ])
 def test_shared_refusals(kw, code):
     assert _shared(**kw) == code and D.load().dflash_last_error()
