@@ -604,9 +604,10 @@ DFLASH_API size_t dflash_shared_workspace_size(int num_reqs, int num_groups, int
  *              rows (num_reqs x Hkv x Dh x 4 bytes x max_ctx_len, or the window) let them do so, and only report bad groups.
  *   Every other argument, and the result, as dflash_decode_attention_paged (the workspace as
  *   dflash_shared_workspace_size says). The result does not depend on timing; another prefix gives another order of the
- *   sums. What a row of the prefix holds that only some of the group's windows reach must be finite for the others
- *   too: their weight 0 is multiplied with it. status also takes 1 where a bounded wait ran out (the output is
- *   then not valid).
+ *   sums. With a window, rows are read once for all where the windows of all that share reach them; a sequence whose
+ *   window has left more than half of the prefix (or of what a window holds) behind reads all its rows itself. A sequence
+ *   sees nothing of what rows hold that are outside its length and window, whatever that is. status also takes 1 where a
+ *   bounded wait ran out (the output is then not valid).
  */
 DFLASH_API int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const dflash_bf16* k_pool,
                                               const dflash_bf16* v_pool, const int32_t* block_table,

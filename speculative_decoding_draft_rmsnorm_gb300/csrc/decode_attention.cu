@@ -104,9 +104,9 @@ struct DecodeArgs {
   float scale_log2;
   int out_f32;
   int max_workers;
-  // OWN: a sequence's rows begin at own[r] (or the window), and a head's unnormalised sums, maximum and weight go to
-  // out (f32) and own_ml, to be joined with what came before
-  const int32_t* own;
+  // OWN: a sequence leaves out the y rows before row x of it, {x, y} = own[r] (and what its window does), and a head's
+  // unnormalised sums, maximum and weight go to out (f32) and own_ml, to be joined with those of the rows left out
+  const int2* own;
   float* own_ml;  // [num_reqs][Hq][2]
 };
 
@@ -121,7 +121,7 @@ __device__ __forceinline__ int valid_len(const DecodeArgs& a, int len) {
 template <bool OWN>
 __device__ __forceinline__ int first_row(const DecodeArgs& a, int r, int len) {
   const int first = a.window > 0 && len > a.window ? len - a.window : 0;
-  if constexpr (OWN) return len > 0 ? max(first, a.own[r]) : 0;
+  if constexpr (OWN) return len > 0 ? first + a.own[r].y : 0;  // the rows from its first to x - y count as those up to x
   return first;
 }
 template <bool OWN>
@@ -401,9 +401,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         if (u == 1 && lane >= 16) mine = ld, have = i + 1 < n_steps;
         if (i + u < n_steps && ++ld.step == ld.steps) next_group<OWN>(a, ld, heads);
       }
-      const int j = mine.first + mine.step * kStep + (lane & 15);
+      int j = mine.first + mine.step * kStep + (lane & 15);
       next_row = -1;
       if (have && j < mine.len) {
+        if constexpr (OWN) {
+          if (a.window > 0) {
+            const int2 own = a.own[mine.r];
+            if (j < own.x) j -= own.y;
+          }
+        }
         const int p = page_of(a, j);
         int id = a.table[static_cast<int64_t>(mine.r) * a.table_stride + p];
         if (id < 0 || id >= a.num_pages) {
@@ -894,7 +900,7 @@ size_t own_rows_workspace(int num_reqs, int hq, int hkv, int dh, int max_ctx_len
   return layout_of(num_reqs, hq, hkv, dh, max_ctx_len, window, sms).total;
 }
 
-cudaError_t launch_own_rows(const DecodeCall& c, const int32_t* own, float* o, float* ml, char* workspace, int sms, bool early,
+cudaError_t launch_own_rows(const DecodeCall& c, const int2* own, float* o, float* ml, char* workspace, int sms, bool early,
                             cudaStream_t st) {
   const Layout y = layout_of(c.num_reqs, c.hq, c.hkv, c.dh, c.max_ctx_len, c.window, sms);
   DecodeArgs a = args_of(c, y, workspace);

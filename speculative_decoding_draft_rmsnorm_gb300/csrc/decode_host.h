@@ -78,11 +78,12 @@ inline float scale_log2_of(const DecodeCall& c) {
   return (c.scale > 0.0f ? c.scale : 1.0f / std::sqrt(static_cast<float>(c.dh))) * 1.4426950408889634f;
 }
 
-// Attention of every sequence over its rows from own[r] on (or from the window's first), unnormalised: o [num_reqs, Hq, Dh]
-// f32, ml [num_reqs, Hq, 2] its maximum (base 2) and weight; heads without such rows are left as they are. early: the grids
-// may begin while the one before them on the stream runs, which must have waited for what wrote own; they end after it.
+// Attention of every sequence over its rows (in its window) but the y before row x, {x, y} = own[r], which it sees all of;
+// unnormalised: o [num_reqs, Hq, Dh] f32, ml [num_reqs, Hq, 2] its maximum (base 2) and weight; heads without such rows are left
+// as they are. early: the grids may begin while the one before them on the stream runs, which must have waited for what wrote
+// own; they end after it.
 size_t own_rows_workspace(int num_reqs, int hq, int hkv, int dh, int max_ctx_len, int window, int sms);
-cudaError_t launch_own_rows(const DecodeCall& c, const int32_t* own, float* o, float* ml, char* workspace, int sms, bool early,
+cudaError_t launch_own_rows(const DecodeCall& c, const int2* own, float* o, float* ml, char* workspace, int sms, bool early,
                             cudaStream_t st);
 
 }  // namespace dflash

@@ -37,7 +37,7 @@ static_assert(kFewTiles * kTileCost >= kTileCost + kUnitCost, "no block's range 
 struct alignas(16) SharedGroup {
   int first, end, rows;  // its sequences; sequences x heads of a kv head
   int prefix, lo;        // lo: where the tiles begin
-  int see;               // the first row that any of its sequences sees; lo is the start of its box
+  int see;               // the first row that all that share see; lo is the start of its box
   int leader;            // the shortest sequence that shares: its pages are read
   int n;
   uint32_t start, units; // tiles and units before it
@@ -82,7 +82,8 @@ struct SharedArgs {
   BlockRange* ranges;  // [blocks]
   int blocks;          // of the prefix kernel
   unsigned long long* least;  // [num_groups]: length and index of the shortest sequence that shares, while the plan is made
-  int32_t* own;   // [num_reqs]: rows before it are the prefix's
+  int32_t* most;              // [num_groups]: length of the longest
+  int2* own;      // [num_reqs]: rows before x are the prefix's, and the last y of those are the group's: see launch_own_rows
   float* own_o;   // [num_reqs][Hq][Dh], a head's sums over its own rows
   float* own_ml;  // [num_reqs][Hq][2]
   Where* where;    // [num_reqs][Hq]
@@ -109,66 +110,98 @@ __device__ __forceinline__ int page_of(const SharedArgs& a, int j) { return divi
 __device__ __forceinline__ int valid_len(const SharedArgs& a, int len) { return len < 0 || len > a.max_len ? 0 : len; }
 __device__ __forceinline__ int first_row(const SharedArgs& a, int len) { return a.window > 0 && len > a.window ? len - a.window : 0; }
 
-// The plan, by one block: which groups share, and from where to where; where every sequence's own rows begin. A
-// sequence shares if it is at least as long as the prefix. The shortest that does sees the first row that any of them
-// sees, where the tiles start, and every row from there on: its pages are read.
+// The plan, by one block: which groups share, and from where to where; what every sequence reads for itself. A sequence
+// shares if it is at least as long as the prefix and sees at least half as much of it as windows leave of it. What is shared
+// are the rows that all of those see: what a window leaves out, whatever it holds, is in no product of its sequence. The
+// others of the prefix that some of them see, at most as many as in half a window, they read like rows of their own.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ SharedArgs a) {
   __shared__ int s_bad, s_groups;
   __shared__ uint32_t s_tiles, s_units, s_warp[32], s_warp_units[32];
   __shared__ uint2 s_at[kPlanThreads];  // tiles and units before the first groups
   __shared__ uint32_t s_lo[kPlanThreads];
   __shared__ int s_count[32];
+  // the groups, where they fit: looked up again and again
+  __shared__ int32_t s_starts[kPlanThreads + 1], s_prefixes[kPlanThreads];
+  __shared__ unsigned long long s_least[kPlanThreads];
+  __shared__ int32_t s_most[kPlanThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dependents_launch();
+  const bool fit = a.num_groups <= kPlanThreads;
+  const int32_t* starts = fit ? s_starts : a.starts;
+  const int32_t* prefixes = fit ? s_prefixes : a.prefixes;
+  unsigned long long* least = fit ? s_least : a.least;
+  int32_t* most = fit ? s_most : a.most;
   if (tid == 0) s_bad = 0, s_tiles = 0, s_units = 0, s_groups = 0;
+  const int raw_len = tid < a.num_reqs ? a.lens[tid] : 0;
   __syncthreads();
   for (int g = tid; g < a.num_groups; g += kPlanThreads) {
-    const int from = a.starts[g], to = a.starts[g + 1];
+    const int from = a.starts[g], to = a.starts[g + 1], p = a.prefixes[g];
     if (from < 0 || from > to || to > a.num_reqs) s_bad = 1;
-    a.least[g] = ~0ull;
-  }
-  __syncthreads();
-  const int groups = s_bad ? 0 : a.num_groups;
-  if (s_bad && tid == 0 && a.err) atomicOr(a.err, kErrMetadata);
-  // what group g shares
-  auto shared_rows = [&](int g, int members) {
-    const int p = a.prefixes[g];
-    return members > 1 && p >= kLeastPrefix && p <= a.max_len ? p : 0;
-  };
-  for (int r = tid; r < a.num_reqs; r += kPlanThreads) {
-    const int len = valid_len(a, a.lens[r]);
-    int own = 0;
-    if (groups && r >= a.starts[0] && r < a.starts[groups]) {
-      int lo = 0, hi = groups - 1;  // the last group that starts at or before r
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.starts[mid] <= r) lo = mid;
-        else hi = mid - 1;
-      }
-      const int p = shared_rows(lo, a.starts[lo + 1] - a.starts[lo]);
-      if (p > 0 && len >= p) {
-        own = p;
-        atomicMin(&a.least[lo], static_cast<unsigned long long>(len) << 32 | static_cast<uint32_t>(r));
-      }
-    }
-    a.own[r] = own;
+    if ((p < 0 || p > a.max_len) && a.err) atomicOr(a.err, kErrMetadata);
+    least[g] = ~0ull, most[g] = 0;
+    if (!fit) continue;
+    s_starts[g] = from, s_prefixes[g] = p;
+    if (g + 1 == a.num_groups) s_starts[g + 1] = to;
   }
   __threadfence_block();
   __syncthreads();
+  const int groups = s_bad ? 0 : a.num_groups;
+  if (s_bad && tid == 0 && a.err) atomicOr(a.err, kErrMetadata);
+  // what group g may share
+  auto shared_rows = [&](int g, int members) {
+    const int p = prefixes[g];
+    return members > 1 && p >= kLeastPrefix && p <= a.max_len ? p : 0;
+  };
+  // sequence r's group if it shares, else -1
+  auto shares_in = [&](int r, int len, int& p) {
+    if (!groups || r < starts[0] || r >= starts[groups]) return -1;
+    int lo = 0, hi = groups - 1;  // the last group that starts at or before r
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (starts[mid] <= r) lo = mid;
+      else hi = mid - 1;
+    }
+    p = shared_rows(lo, starts[lo + 1] - starts[lo]);
+    if (p == 0 || len < p) return -1;
+    return p - first_row(a, len) >= ((a.window > 0 ? min(p, a.window) : p) + 1) / 2 ? lo : -1;
+  };
+  for (int base = tid - lane; base < a.num_reqs; base += kPlanThreads) {
+    const int r = base + lane, len = r < a.num_reqs ? valid_len(a, r == tid ? raw_len : a.lens[r]) : 0;
+    int p = 0;
+    const int g = r < a.num_reqs ? shares_in(r, len, p) : -1;
+    // of a warp's sequences of a group one speaks for all: 256 that take turns at one word take 4 us
+    const uint32_t mates = __match_any_sync(0xffffffffu, g);
+    const int low = __reduce_min_sync(mates, len), high = __reduce_max_sync(mates, len);
+    const uint32_t lowest = __ballot_sync(0xffffffffu, len == low);
+    if (g >= 0 && lane == __ffs(mates & lowest) - 1) {
+      atomicMin(&least[g], static_cast<unsigned long long>(low) << 32 | static_cast<uint32_t>(r));
+      atomicMax(&most[g], high);
+    }
+    if (a.window <= 0 && r < a.num_reqs) a.own[r] = g < 0 ? make_int2(0, 0) : make_int2(p, p);
+  }
+  __threadfence_block();
+  __syncthreads();
+  auto first_for_all = [&](int g) { return first_row(a, *static_cast<const volatile int32_t*>(&most[g])); };
+  if (a.window > 0) {
+    for (int r = tid; r < a.num_reqs; r += kPlanThreads) {
+      const int len = valid_len(a, r == tid ? raw_len : a.lens[r]);
+      int p = 0;
+      const int g = shares_in(r, len, p);
+      a.own[r] = g < 0 ? make_int2(0, 0) : make_int2(p, p - first_for_all(g));
+    }
+  }
   for (int base = 0; base < groups; base += kPlanThreads) {
     const int g = base + tid;
     SharedGroup x{};
     uint32_t tiles = 0, units = 0;
     if (g < groups) {
-      const int raw = a.prefixes[g];
-      if ((raw < 0 || raw > a.max_len) && a.err) atomicOr(a.err, kErrMetadata);
-      x.first = a.starts[g], x.end = a.starts[g + 1];
+      x.first = starts[g], x.end = starts[g + 1];
       const int members = x.end - x.first;
       x.prefix = shared_rows(g, members);
-      const unsigned long long least = *static_cast<volatile unsigned long long*>(&a.least[g]);
-      x.see = first_row(a, static_cast<int>(least >> 32)), x.lo = x.see & -max(a.box, 1), x.leader = static_cast<int>(least & 0xffffffffu);
+      const unsigned long long shortest = *static_cast<const volatile unsigned long long*>(&least[g]);
+      x.see = first_for_all(g), x.lo = x.see & -max(a.box, 1), x.leader = static_cast<int>(shortest & 0xffffffffu);
       x.rows = members * a.g;
-      if (least != ~0ull && x.see < x.prefix) {
+      if (shortest != ~0ull) {
         x.n = (x.prefix - x.lo + kKeys - 1) / kKeys;
         units = static_cast<uint32_t>((x.rows + kRows - 1) / kRows) * a.hkv;
         tiles = units * x.n;
@@ -259,13 +292,11 @@ struct Walk {
   uint32_t x, hi;
   int hkv, kvh, m0, t;  // the next unit and its first tile here
   uint32_t unit;        // of the call
-  SharedGroup g;        // (the next one is on its way to L1, and its sequences' lengths)
-  const int32_t* lens;
+  SharedGroup g;        // (the next one is on its way to L1)
   __device__ __forceinline__ Walk(const SharedArgs& a, const BlockRange& r)
-      : groups(a.groups + r.group), x(r.lo), hi(r.hi), hkv(a.hkv), kvh(r.kvh), m0(r.m0), t(r.t), lens(a.lens) {
+      : groups(a.groups + r.group), x(r.lo), hi(r.hi), hkv(a.hkv), kvh(r.kvh), m0(r.m0), t(r.t) {
     g = *groups;
     prefetch_l1(groups + 1);
-    prefetch_l1(lens + g.end - 1);
     unit = g.units + (x - t - g.start) / static_cast<uint32_t>(g.n);
   }
   __device__ __forceinline__ bool next(Unit& u) {
@@ -273,7 +304,6 @@ struct Walk {
     if (kvh == hkv) {
       kvh = 0, g = *++groups;
       prefetch_l1(groups + 1);
-      prefetch_l1(lens + g.end - 1);
     }
     u.first = g.first, u.rows = g.rows, u.prefix = g.prefix, u.lo = g.lo, u.see = g.see, u.leader = g.leader, u.n = g.n;
     u.kvh = kvh, u.m0 = m0, u.t0 = t;
@@ -607,14 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     Unit u;
     uint32_t t = 0;
     while (ok && walk.next(u)) {
-      // the rows of the prefix that this thread's sequence sees, from lo on. Lanes without a sequence that shares see all of
-      // them: what they get is not used, and masks cost a warp more than its products (8 rows of 32 lanes: 9200 cycles a tile, 4400)
-      const int at = u.m0 + row;
-      int from = 0;
-      if (at < u.rows) {
-        const int len = valid_len(a, a.lens[u.first + divided(at, a.g_mul, a.g_shift)]);
-        if (len >= u.prefix) from = first_row(a, len) - u.lo;
-      }
+      const int from = u.see - u.lo;
       float m = -INFINITY;
       const bool idle = u.m0 + (warp & 3) * 32 >= u.rows;  // lanes that hold no rows may hold anything
 #pragma unroll 1
@@ -629,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         }
         tc_fence_after();
         const int c_lo = from - i * kKeys, c_hi = u.prefix - u.lo - i * kKeys;  // columns [c_lo, c_hi) are seen
+        // (votes, though all lanes agree: as plain conditions the compiler's loops are slower, 256 sequences 140 us, 136)
         const bool whole = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kKeys);
         // 16 columns at a time, the next ones on their way; first for the maximum, then for the weights
         auto masked = [&](uint32_t (&r)[16], int b) {
@@ -799,8 +823,8 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Sha
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   if (row >= static_cast<int64_t>(a.num_reqs) * a.hq) return;
-  const int r = static_cast<int>(row / a.hq), len = valid_len(a, a.lens[r]), own = a.own[r], first = first_row(a, len);
-  const bool has_own = len > max(own, first), has_prefix = own > first;
+  const int r = static_cast<int>(row / a.hq), len = valid_len(a, a.lens[r]), shared = a.own[r].y;
+  const bool has_own = len > first_row(a, len) + shared, has_prefix = shared > 0;
   int parts = 0;
   Where where{-1, 0, 0, 0};
   if (has_prefix) {
@@ -834,7 +858,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Sha
 }
 
 struct SharedLayout {
-  size_t totals, groups, ranges, least, own, own_ml, own_o, where, pre_ml, pre_o, part_ml, part_o, rows, total;
+  size_t totals, groups, ranges, least, most, own, own_ml, own_o, where, pre_ml, pre_o, part_ml, part_o, rows, total;
 };
 
 SharedLayout shared_layout(int num_reqs, int num_groups, int hq, int hkv, int dh, int max_ctx_len, int window, int sms) {
@@ -845,8 +869,9 @@ SharedLayout shared_layout(int num_reqs, int num_groups, int hq, int hkv, int dh
   y.ranges = y.totals + 256;
   y.groups = y.ranges + up(sms * sizeof(BlockRange));
   y.least = y.groups + up((num_groups + 1) * sizeof(SharedGroup));
-  y.own = y.least + up(num_groups * sizeof(unsigned long long));
-  y.own_ml = y.own + up(num_reqs * sizeof(int32_t));
+  y.most = y.least + up(num_groups * sizeof(unsigned long long));
+  y.own = y.most + up(num_groups * sizeof(int32_t));
+  y.own_ml = y.own + up(num_reqs * sizeof(int2));
   y.own_o = y.own_ml + up(heads * 2 * sizeof(float));
   y.where = y.own_o + up(heads * dh * sizeof(float));
   y.pre_ml = y.where + up(heads * sizeof(Where));
@@ -931,9 +956,9 @@ int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const
   divide_by_page(a.g, &a.g_mul, &a.g_shift);
   a.totals = reinterpret_cast<Totals*>(ws + y.totals), a.ranges = reinterpret_cast<BlockRange*>(ws + y.ranges), a.blocks = sms;
   a.groups = reinterpret_cast<SharedGroup*>(ws + y.groups);
-  a.least = reinterpret_cast<unsigned long long*>(ws + y.least);
+  a.least = reinterpret_cast<unsigned long long*>(ws + y.least), a.most = reinterpret_cast<int32_t*>(ws + y.most);
   a.lens = seq_lens, a.starts = group_start_loc, a.prefixes = prefix_lens, a.err = reinterpret_cast<uint32_t*>(status);
-  a.own = reinterpret_cast<int32_t*>(ws + y.own);
+  a.own = reinterpret_cast<int2*>(ws + y.own);
   a.own_ml = reinterpret_cast<float*>(ws + y.own_ml), a.own_o = reinterpret_cast<float*>(ws + y.own_o);
   a.where = reinterpret_cast<Where*>(ws + y.where);
   a.pre_ml = reinterpret_cast<float*>(ws + y.pre_ml), a.pre_o = reinterpret_cast<float*>(ws + y.pre_o);

@@ -169,6 +169,19 @@ def test_scale_and_peaked_scores(scale):
     b.check(b.run(False, scale=scale), scale=scale)
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("at", [0, 5, 16, 100, 127, 128, 140, 300, 999])
+def test_scores_that_leap(at, f32):
+    # one key far above all others, in some heads' eyes only: what came before weighs nothing, whatever tile it came in
+    import torch
+    b = Batch([(1000, [1001, 1005, 1003, 1009])], 16, 8, 2, 128, seed=at)
+    page, off = b.table[0, at // 16].item(), at % 16
+    q = b.q.view(4, 2, 4, 128)
+    b.k[page, off, 0] = (q[1, 0, 2].float() * 20).to(torch.bfloat16)
+    b.k[page, off, 1] = (q[3, 1, 0].float() * 5).to(torch.bfloat16)
+    b.check(b.run(f32))
+
+
 def test_masked_keys_hold_anything():
     # keys of the last tile that lie behind the prefix are NaN (Batch) and inf here
     import torch
@@ -178,6 +191,38 @@ def test_masked_keys_hold_anything():
     b.k[bad], b.v[bad] = float("inf"), float("-inf")
     got = b.run(True)
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("window", [1, 20, 128, 300, 400, 611, 1000])
+@pytest.mark.parametrize("ps", [5, 16])
+def test_rows_that_other_windows_see_hold_anything(window, ps):
+    # lengths 600 to 1400 on 600 shared rows: what the longest do not see is inf or NaN to them, in K and V
+    import torch
+    b = Batch([(600, [600, 601, 617, 650, 700, 790, 899, 900, 901, 1100, 1199, 1200, 1400])], ps, 16, 2, 64, seed=window)
+    b.check(b.run(True, window=window), window=window)
+    assert b.status == 0
+    want = b.run(window=window)
+    for r in (3, 6, 11, 12):
+        end = b.lens[r] - window  # rows before it are outside the windows of r and of all behind it
+        if end <= 0:
+            continue
+        keep = b.k.clone(), b.v.clone()
+        j = torch.arange(end, device="cuda")
+        pages, rows = b.table[r, (j // ps).long()].long(), (j % ps).long()
+        for bad in (float("nan"), float("inf")):
+            b.k[pages, rows], b.v[pages, rows] = bad, -bad
+            got = b.run(window=window)
+            assert all(torch.equal(x[r:], y[r:]) for x, y in zip(got, want))
+        b.k, b.v = keep
+
+
+@pytest.mark.parametrize("window", [0, 300])
+def test_more_groups_than_a_block_of_threads(window):
+    rng = np.random.default_rng(3)
+    groups = [(int(rng.integers(50, 200)), [200 + int(x) for x in rng.integers(0, 160, rng.integers(0, 3))]) for _ in range(1500)]
+    b = Batch(groups, 16, 2, 1, 64, seed=21, before=3, after=2)
+    b.check(b.run(True, window=window), window=window)
+    assert b.status == 0
 
 
 def test_any_shorter_prefix_gives_the_result():
