@@ -83,6 +83,9 @@ DFLASH_API int dflash_version(void);
 /* Bit that dflash_context_kv, dflash_paged_append and dflash_prepare_inputs OR into their
  * `status` word. */
 enum { DFLASH_STATUS_METADATA = 2 /* a device index or length was out of range; see the call */ };
+/* Bit that dflash_rms_norm and dflash_decode_attention_shared OR into theirs where a bounded wait ran out: the output is not
+ * valid then. */
+enum { DFLASH_STATUS_TIMEOUT = 1 };
 
 /*
  * dflash_context_kv -- write rows into the draft model's context K/V store.
@@ -540,7 +543,7 @@ DFLASH_API int dflash_compact_pages(int32_t* block_table, int64_t block_table_st
  *                Every other overlap of an output with a tensor of the call is refused.
  *   scales       f32 [n, ceil(d / group_size)], or [n] with group_size 0; e4m3 only
  *   group_size   0 or a multiple of 16; the last group may be short
- *   status       int32 device word or NULL: 1 is ORed in where a bounded wait ran out (rows are missing then)
+ *   status       int32 device word or NULL: DFLASH_STATUS_TIMEOUT is ORed in where a bounded wait ran out (rows are missing)
  *   d <= 65536. Sums in f32 (rows of values above 1e19 overflow them), one rounding to the output's type. A
  *   scale is infinite or NaN where a y of its group is. One launch.
  */
@@ -606,8 +609,8 @@ DFLASH_API size_t dflash_shared_workspace_size(int num_reqs, int num_groups, int
  *   dflash_shared_workspace_size says). The result does not depend on timing; another prefix gives another order of the
  *   sums. With a window, rows are read once for all where the windows of all that share reach them; a sequence whose
  *   window has left more than half of the prefix (or of what a window holds) behind reads all its rows itself. A sequence
- *   sees nothing of what rows hold that are outside its length and window, whatever that is. status also takes 1 where a
- *   bounded wait ran out (the output is then not valid).
+ *   sees nothing of what rows hold that are outside its length and window, whatever that is. status also takes
+ *   DFLASH_STATUS_TIMEOUT, where a bounded wait ran out.
  */
 DFLASH_API int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const dflash_bf16* k_pool,
                                               const dflash_bf16* v_pool, const int32_t* block_table,

@@ -28,7 +28,7 @@ from .decode import (OUT_E4M3, beam_select, beam_workspace_size, compact_pages, 
                      rms_norm, rotary, rotary_axes, rotary_frequencies, rotary_sections, shared_prefixes,
                      shared_workspace_size)
 
-__all__ = ["load", "lib_path", "context_kv", "paged_append", "prepare_inputs", "STATUS_METADATA", "block_attention", "block_attention_paged", "workspace_size", "plan",
+__all__ = ["load", "lib_path", "context_kv", "paged_append", "prepare_inputs", "STATUS_METADATA", "STATUS_TIMEOUT", "block_attention", "block_attention_paged", "workspace_size", "plan",
            "alloc_workspace",
            "check_error", "DFlashError", "OUT_BF16", "OUT_F32", "FLAG_FORCE_SPLIT", "FLAG_NO_SPLIT",
            "FLAG_FORCE_SHARE",
@@ -40,6 +40,7 @@ __all__ = ["load", "lib_path", "context_kv", "paged_append", "prepare_inputs", "
 
 OUT_BF16, OUT_F32 = 0, 1
 STATUS_METADATA = 2  # bit ORed into the status word of context_kv / paged_append / prepare_inputs
+STATUS_TIMEOUT = 1  # ... of rms_norm / decode_attention_shared: a bounded wait ran out, the output is not valid
 FLAG_FORCE_SPLIT, FLAG_NO_SPLIT, FLAG_FORCE_SHARE = 1, 2, 4
 ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT, ERR_DEVICE_METADATA = \
     -1, -2, -3, -4, -5, -6
