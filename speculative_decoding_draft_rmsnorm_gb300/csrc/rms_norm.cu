@@ -10,9 +10,16 @@
 // same factor for every column. Maxima are taken as integers over the bits of |h w|, so that a NaN is the
 // largest value there is and turns up in its row's scale instead of getting lost.
 //
-// A block has one row at a time, a 16-byte chunk a thread where that fits (rows of more than two chunks a thread are
-// read again for the output), and loads the next row before it reduces this one. Blocks stay for as many rows as there
-// are, with the weights in registers.
+// Five kernels, all with the same sums; which one is a question of how a row lies and how many there are:
+// - norm_kernel: a block a row, a 16-byte chunk a thread where that fits (rows of more than two chunks a thread are read again
+//   for the output). 1 x 2560 with residual and e4m3 2.0 us, which is a launch and two dependent latencies; 64 x 4096 2.3.
+// - ring_kernel: many aligned rows, through rings that bulk copies fill. 16384 x 5120 with residual and e4m3 by 128 108 us, 80 %
+//   of the copy rate (norm_kernel 136).
+// - shifted_kernel: odd widths, in chunks cut where memory is aligned. 333 x 5003 in f32 10.2 us (element by element 16.6), 16384 x 5119 in
+//   bf16 123 (224).
+// - narrow_kernel: aligned rows of at most 32 chunks, or few narrow odd ones, several a warp. 312500 x 128 in bf16 32 us,
+//   73 % of the copy rate, with residual and e4m3 52 us (ring_kernel 82 and 118).
+// - tile_kernel: many narrow odd rows, worked on in shared memory. 2.35 million x 17 in f32 52 us, 91 % (norm_kernel 1190).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -50,6 +57,11 @@ struct NormArgs {
   uint32_t* err;
   float eps, inv_d;
 };
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <typename T, int V>
 __device__ __forceinline__ void load_vec(const T* p, float (&v)[V]) {
@@ -581,6 +593,197 @@ __global__ void __launch_bounds__(1024) shifted_kernel(const __grid_constant__ N
   }
 }
 
+// ---- Narrow rows: `team` lanes (a power of two) have a row, at most kNarrowHeld chunks each, always the same columns: their
+// weights stay in registers. The next rows are on their way while these are worked on.
+constexpr int kNarrowThreads = 256;
+template <int V>
+constexpr int kNarrowHeld = V >= 4 ? 1 : 4;
+template <int V>
+constexpr int kNarrowBlocks = V >= 4 ? 5 : 4;  // of an SM
+
+template <typename T, int V, int EIGHT>
+__global__ void __launch_bounds__(kNarrowThreads, kNarrowBlocks<V>) narrow_kernel(const __grid_constant__ NormArgs a, int team, int team_shift) {
+  constexpr int kHeld = kNarrowHeld<V>;
+  const int lane = threadIdx.x & 31, sub = lane & (team - 1);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kNarrowThreads >> team_shift;
+  int64_t row = (static_cast<int64_t>(blockIdx.x) * kNarrowThreads + threadIdx.x) >> team_shift;
+  float w[kHeld][V];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = i * team + sub;
+    if (c >= a.chunks) continue;
+    if (a.w32) load_vec<float, V>(static_cast<const float*>(a.w) + c * V, w[i]);
+    else load_vec<uint16_t, V>(static_cast<const uint16_t*>(a.w) + c * V, w[i]);
+  }
+  Raw<T, V> x[kHeld], r[kHeld];
+  auto fetch = [&]() {
+    if (row >= a.n) return;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * team + sub < a.chunks) load_in<T, V>(a, row, i * team + sub, x[i], r[i]);
+  };
+  fetch();
+#pragma unroll 1
+  while (__any_sync(0xffffffffu, row < a.n)) {
+    const int64_t now = row;
+    const int chunks = now < a.n ? a.chunks : 0;
+    float h[kHeld][V], sum = 0.0f;
+    uint32_t mine[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * team + sub < chunks) make_h<T, V>(a, now, i * team + sub, x[i], r[i], h[i]);
+    row += step;
+    fetch();
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      mine[i] = 0;
+      if (i * team + sub >= chunks) continue;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        sum = fmaf(h[i][j], h[i][j], sum);
+        h[i][j] *= w[i][j];
+        if constexpr (EIGHT != 0) mine[i] = max(mine[i], __float_as_uint(h[i][j]) & 0x7fffffffu);
+      }
+    }
+    uint32_t top = 0;
+    if constexpr (EIGHT == 1) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) top = max(top, mine[i]);
+    }
+#pragma unroll 1
+    for (int o = team / 2; o; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if constexpr (EIGHT == 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if constexpr (EIGHT == 2) {
+        if (o < a.lanes) {
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i) mine[i] = max(mine[i], __shfl_xor_sync(0xffffffffu, mine[i], o));
+        }
+      }
+    }
+    const float factor = 1.0f / sqrtf(fmaf(sum, a.inv_d, a.eps));
+    float scale = 0.0f;
+    if constexpr (EIGHT == 1) {
+      scale = scale_of(top, factor);
+      if (sub < chunks && sub == 0) a.scale[now] = scale;
+    }
+    if constexpr (EIGHT == 2 && kHeld == 4) {
+      if (a.lanes > team) mine[0] = mine[1] = max(mine[0], mine[1]), mine[2] = mine[3] = max(mine[2], mine[3]);  // groups of two
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int c = i * team + sub;
+      if (c >= chunks) continue;
+      if constexpr (EIGHT == 0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[i][j] *= factor;
+        store_vec<T, V>(static_cast<T*>(a.out) + now * a.out_row + static_cast<int64_t>(c) * V, h[i]);
+      } else {
+        if constexpr (EIGHT == 2) {
+          scale = scale_of(mine[i], factor);
+          if ((c & (a.lanes - 1)) == 0) a.scale[now * a.groups + (c >> a.shift)] = scale;
+        }
+        const float by = __fdividef(1.0f, scale);
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[i][j] = h[i][j] * factor * by;
+        store_e4m3<V>(static_cast<uint8_t*>(a.out) + now * a.out_row + static_cast<int64_t>(c) * V, h[i]);
+      }
+    }
+  }
+}
+
+// ---- Rows of odd widths that lie end to end: 16 rows or more are whole 16-byte pieces wherever they begin. A block takes some to
+// shared memory as they lie, `team` threads work on a row there, and what they make goes back the same way.
+constexpr int kTileThreads = 256, kTileTeam = 16;  // threads of a row at most: columns of a group of 16 are as many for each
+constexpr int kTileBytes = 100 * 1024;
+// Where chunks cut at a row's own alignment are slower: 62402 rows of 641 columns in bf16 with residual and e4m3 82 us here, 105
+// there; 52151 of 767 88, 81. Fewer rows (of an SM) than kTileRows have less to wait for elsewhere: 4000 of 17 2.3 us, 3.6 here;
+// of 257 4.9, 5.7.
+constexpr int kTileWidth = 640, kTileRows = 32;
+
+template <typename T, int EIGHT>
+__global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constant__ NormArgs a, int team, int team_shift) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, most = kTileThreads >> team_shift;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * most;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(most), a.n - row0)), items = rows * a.d;
+  T* xs = reinterpret_cast<T*>(smem);  // x, then y
+  T* rs = xs + most * a.d;             // r, then h
+  float* ws = reinterpret_cast<float*>(a.r ? rs + most * a.d : rs);
+  uint8_t* os = reinterpret_cast<uint8_t*>(ws + (a.d + 3) / 4 * 4);
+  auto take = [&](T* to, const void* from) {
+    const T* p = static_cast<const T*>(from) + row0 * a.d;
+    constexpr int V = 16 / sizeof(T);
+    for (int i = tid; i < items / V; i += kTileThreads) cp_async16(smem_u32(to + i * V), p + i * V);
+    for (int i = items / V * V + tid; i < items; i += kTileThreads) to[i] = p[i];
+  };
+  auto give = [&](void* to, const auto* from) {
+    using U = std::remove_const_t<std::remove_pointer_t<decltype(from)>>;
+    constexpr int V = 16 / sizeof(U);
+    U* p = static_cast<U*>(to) + row0 * a.d;
+    for (int i = tid; i < items / V; i += kTileThreads) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(from)[i];
+    for (int i = items / V * V + tid; i < items; i += kTileThreads) p[i] = from[i];
+  };
+  take(xs, a.x);
+  if (a.r) take(rs, a.r);
+  for (int c = tid; c < a.d; c += kTileThreads)
+    ws[c] = a.w32 ? static_cast<const float*>(a.w)[c] : bf16lo_to_f32(static_cast<const uint16_t*>(a.w)[c]);
+  cp_async_wait_all();
+  __syncthreads();
+  const int row = tid >> team_shift, sub = tid & (team - 1), d = row < rows ? a.d : 0;
+  T* x = xs + row * a.d;
+  T* h = (a.r ? rs : xs) + row * a.d;
+  auto value = [](const T* p) {
+    if constexpr (sizeof(T) == 4) return *p;
+    else return bf16lo_to_f32(*p);
+  };
+  auto set = [](T* p, float v) {
+    if constexpr (sizeof(T) == 4) *p = v;
+    else *p = static_cast<uint16_t>(pack_bf16x2(v, 0.0f));
+  };
+  float sum = 0.0f;
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int c = sub; c < d; c += team) {
+    float v = value(x + c);
+    if (a.r) {
+      set(h + c, v + value(h + c));
+      v = value(h + c);
+    }
+    sum = fmaf(v, v, sum);
+    if constexpr (EIGHT == 1) top = max(top, __float_as_uint(v * ws[c]) & 0x7fffffffu);
+  }
+  for (int o = team / 2; o; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if constexpr (EIGHT == 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+  const float factor = 1.0f / sqrtf(fmaf(sum, a.inv_d, a.eps));
+  if constexpr (EIGHT == 0) {
+#pragma unroll 4
+    for (int c = sub; c < d; c += team) set(x + c, value(h + c) * ws[c] * factor);
+  } else {
+    const int groups = EIGHT == 2 ? a.groups : 1;
+#pragma unroll 1
+    for (int g = 0; g < groups; ++g) {
+      const int lo = g * a.group + sub, hi = EIGHT == 2 ? min(d, (g + 1) * a.group) : d;
+      if constexpr (EIGHT == 2) {
+        top = 0;
+#pragma unroll 4
+        for (int c = lo; c < hi; c += team) top = max(top, __float_as_uint(value(h + c) * ws[c]) & 0x7fffffffu);
+        for (int o = team / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      const float scale = scale_of(top, factor), by = __fdividef(1.0f, scale);
+      if (sub < d && sub == 0) a.scale[(row0 + row) * groups + g] = scale;
+#pragma unroll 4
+      for (int c = lo; c < hi; c += team) os[row * a.d + c] = static_cast<uint8_t>(pack_e4m3x2(value(h + c) * ws[c] * factor * by, 0.0f));
+    }
+  }
+  __syncthreads();
+  if (a.r) give(a.r_out, rs);
+  if constexpr (EIGHT == 0) give(a.out, xs);
+  else give(a.out, os);
+}
+
 // Bytes [lo, hi) of n rows of a strided tensor.
 struct Range {
   uintptr_t at;
@@ -628,6 +831,64 @@ bool try_shifted(const NormArgs& a, int v, int eight, int out_size, cudaStream_t
   return true;
 }
 
+// Narrow rows: whether they were launched. Of the teams whose lanes hold a row the one that leaves fewest places empty.
+template <typename T, int V>
+bool try_narrow(NormArgs a, int eight, int sms, cudaStream_t st) {
+  if (a.chunks > 32 * kNarrowHeld<V>) return false;
+  int team = 0, places = 0;
+  for (int t = 32; t; t /= 2) {
+    const int held = (a.chunks + t - 1) / t;
+    if (held <= kNarrowHeld<V> && (team == 0 || held * t < places)) team = t, places = held * t;
+  }
+  if (eight == 2) {  // groups that neighbouring lanes hold, or, twice as large, a team's chunks of two turns
+    const int lanes = a.group % V ? 0 : a.group / V;
+    if (lanes == 0 || (lanes & (lanes - 1))) return false;
+    team = std::max(team, std::min(lanes, 32));
+    if (lanes > team * (kNarrowHeld<V> == 4 ? 2 : 1)) return false;
+    a.lanes = lanes, a.shift = 0;
+    while ((1 << a.shift) < lanes) ++a.shift;
+  }
+  int shift = 0;
+  while ((1 << shift) < team) ++shift;
+  const int64_t blocks = (a.n * team + kNarrowThreads - 1) / kNarrowThreads;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(sms) * kNarrowBlocks<V>));
+  if (eight == 0) narrow_kernel<T, V, 0><<<grid, kNarrowThreads, 0, st>>>(a, team, shift);
+  else if (eight == 1) narrow_kernel<T, V, 1><<<grid, kNarrowThreads, 0, st>>>(a, team, shift);
+  else narrow_kernel<T, V, 2><<<grid, kNarrowThreads, 0, st>>>(a, team, shift);
+  return true;
+}
+
+template <typename T, int EIGHT>
+cudaError_t launch_tile(const NormArgs& a, int team, int bytes, cudaStream_t st) {
+  int shift = 0;
+  while ((1 << shift) < team) ++shift;
+  const cudaError_t e = cudaFuncSetAttribute(tile_kernel<T, EIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileBytes);
+  if (e != cudaSuccess) return e;
+  const int rows = kTileThreads / team;
+  tile_kernel<T, EIGHT><<<static_cast<unsigned>((a.n + rows - 1) / rows), kTileThreads, bytes, st>>>(a, team, shift);
+  return cudaSuccess;
+}
+// Odd widths, end to end: whether they were launched (or failed). As few threads a row as leave an SM four blocks.
+template <typename T>
+bool try_tile(const NormArgs& a, int v, int eight, int sms, cudaStream_t st, cudaError_t* e) {
+  if (a.d > kTileWidth || a.n < static_cast<int64_t>(kTileRows) * sms) return false;
+  auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  if (v == static_cast<int>(16 / sizeof(T)) || a.x_row != a.d || a.out_row != a.d || !aligned(a.x) || !aligned(a.out)) return false;
+  if (a.r && (a.r_row != a.d || a.r_out_row != a.d || !aligned(a.r) || !aligned(a.r_out))) return false;
+  int team = 1;
+  int64_t bytes = 0;
+  for (; team <= kTileTeam; team *= 2) {
+    bytes = static_cast<int64_t>(kTileThreads / team) * a.d * (sizeof(T) * (a.r ? 2 : 1) + (eight ? 1 : 0)) + (a.d + 3) / 4 * 16;
+    if (bytes <= kTileBytes / 2) break;
+  }
+  if (team > kTileTeam) team = kTileTeam;
+  if (bytes > kTileBytes) return false;
+  if (eight == 0) *e = launch_tile<T, 0>(a, team, static_cast<int>(bytes), st);
+  else if (eight == 1) *e = launch_tile<T, 1>(a, team, static_cast<int>(bytes), st);
+  else *e = launch_tile<T, 2>(a, team, static_cast<int>(bytes), st);
+  return true;
+}
+
 template <typename T, int EIGHT, int TEAM>
 cudaError_t launch_ring(const NormArgs& a, int grid, int bytes, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(ring_kernel<T, EIGHT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
@@ -665,6 +926,19 @@ bool try_ring(NormArgs a, int v, int eight, int sms, cudaStream_t st, cudaError_
     default: *e = launch_ring_kind<T, 32>(a, eight, sms, bytes, st);
   }
   return true;
+}
+
+// A launch of the kernel that suits the rows.
+template <typename T>
+cudaError_t launch_norm(NormArgs& a, int v, int held, int threads, int kind, int out_size, int sms, cudaStream_t st) {
+  constexpr int kMost = 16 / sizeof(T);
+  cudaError_t e = cudaSuccess;
+  if (kind == 2 && a.groups == 1) kind = 1;
+  if (try_tile<T>(a, v, kind, sms, st, &e)) return e;
+  if (v == kMost ? try_narrow<T, kMost>(a, kind, sms, st) : v == 2 ? try_narrow<T, 2>(a, kind, sms, st) : try_narrow<T, 1>(a, kind, sms, st)) return e;
+  if (try_ring<T>(a, v, kind, sms, st, &e) || try_shifted<T>(a, v, kind, out_size, st)) return e;
+  a.w32 ? launch_width<T, true>(v, held, a, threads, kind, st) : launch_width<T, false>(v, held, a, threads, kind, st);
+  return e;
 }
 
 }  // namespace
@@ -744,13 +1018,8 @@ extern "C" int dflash_rms_norm(const void* x, int64_t x_stride, const void* resi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   a.w32 = ws == 4;
-  const bool ring = es == 4 ? try_ring<float>(a, v, kind, sms, st, &e) : try_ring<uint16_t>(a, v, kind, sms, st, &e);
-  if (!ring && !(es == 4 ? try_shifted<float>(a, v, kind, static_cast<int>(os), st) : try_shifted<uint16_t>(a, v, kind, static_cast<int>(os), st))) {
-    if (es == 4)
-      ws == 4 ? launch_width<float, true>(v, held, a, threads, kind, st) : launch_width<float, false>(v, held, a, threads, kind, st);
-    else
-      ws == 4 ? launch_width<uint16_t, true>(v, held, a, threads, kind, st) : launch_width<uint16_t, false>(v, held, a, threads, kind, st);
-  }
+  e = es == 4 ? launch_norm<float>(a, v, held, threads, kind, static_cast<int>(os), sms, st)
+              : launch_norm<uint16_t>(a, v, held, threads, kind, static_cast<int>(os), sms, st);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "rms norm launch: %s", cudaGetErrorString(e));
   return report_error(DFLASH_OK, "");

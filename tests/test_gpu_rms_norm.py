@@ -229,3 +229,47 @@ def test_odd_widths(d, f32, eight, group, residual):
     assert not wide[:, :3].any() and not wide[:, 3 + d:].any()
     out, stream, _ = D().rms_norm(x[:1].expand(n, d), w, residual=r, **kw)
     check((out, stream, _), x[:1].expand(n, d), r, w, group)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("group", [None, 0, 16, 48, 64, 128])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("n,d", [(5003, 17), (4870, 50), (5001, 97), (4999, 100), (5000, 129), (4900, 257), (4867, 511), (5001, 640), (5003, 16), (5001, 64),
+                                 (4999, 128), (5000, 200), (4990, 256), (700, 33), (33, 127), (1, 65), (9, 250)])
+def test_narrow_rows(n, d, f32, group, residual):
+    import torch
+    x, r, w = inputs(n, d, f32, w32=d % 2 == 0, seed=d)
+    kw = {} if group is None else dict(out_dtype=D().OUT_E4M3, group_size=group)
+    res = r if residual else None
+    got = D().rms_norm(x, w, residual=res, **kw)
+    check(got, x, res, w, group or 0)
+    # the same rows, far apart and out of step with memory's alignment: the same values to within the order of their sums
+    wide = torch.zeros(n, d + 37, device="cuda", dtype=x.dtype)
+    wide[:, 5:5 + d] = x
+    check(D().rms_norm(wide[:, 5:5 + d], w, residual=res, **kw), x, res, w, group or 0)
+    wide = torch.zeros(n, (d + 23) // 8 * 8, device="cuda", dtype=x.dtype)  # aligned and apart
+    wide[:, :d] = x
+    check(D().rms_norm(wide[:, :d], w, residual=res, **kw), x, res, w, group or 0)
+    if residual:  # in place
+        x1, r1 = x.clone(), r.clone()
+        same = D().rms_norm(x1, w, residual=r1, residual_out=x1, **kw)
+        assert torch.equal(same[0].float(), got[0].float()) and torch.equal(x1, got[1]) and torch.equal(r1, r)
+
+
+@pytest.mark.parametrize("d", [17, 64, 130])
+@pytest.mark.parametrize("eight", [False, True])
+def test_narrow_rows_of_zeros_nans_and_infinities(d, eight):
+    import torch
+    n = 6000
+    x, _, w = inputs(n, d, False, seed=d)
+    kw = dict(out_dtype=D().OUT_E4M3) if eight else {}
+    want = D().rms_norm(x, w, **kw)
+    x[1::7], x[2::7, 3], x[3::7, 1] = 0.0, float("nan"), float("inf")
+    got = D().rms_norm(x, w, **kw)
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[1::7] = rest[2::7] = rest[3::7] = False
+    assert torch.equal(got[0].float()[rest], want[0].float()[rest])
+    assert bool((got[0].float()[1::7] == 0).all())
+    assert bool(torch.isnan(got[0].float()[2::7]).all())
+    if eight:
+        assert torch.equal(got[2][rest], want[2][rest]) and bool((got[2][1::7] == 2.0 ** -126).all()) and bool(torch.isnan(got[2][2::7]).all())
