@@ -13,7 +13,7 @@
 // Five kernels, all with the same sums; which one is a question of how a row lies and how many there are:
 // - norm_kernel: a block a row, a 16-byte chunk a thread where that fits (rows of more than two chunks a thread are read again
 //   for the output). 1 x 2560 with residual and e4m3 2.0 us, which is a launch and two dependent latencies; 64 x 4096 2.3.
-// - ring_kernel: many aligned rows, through rings that bulk copies fill. 16384 x 5120 with residual and e4m3 by 128 108 us, 80 %
+// - ring_kernel: many aligned rows, through rings that bulk copies fill. 16384 x 5120 with residual and e4m3 by 128 100 us, 87 %
 //   of the copy rate (norm_kernel 136).
 // - shifted_kernel: odd widths, in chunks cut where memory is aligned. 333 x 5003 in f32 10.2 us (element by element 16.6), 16384 x 5119 in
 //   bf16 123 (224).
@@ -123,6 +123,19 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&v)[V]) {
     if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(p) = w[0];
   }
+}
+
+// The largest of |a|, |b| and |c|; NaN where one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Sums of two bf16, rounded to bf16 (as their sum in f32 is: where that is inexact the lesser addend is below a 2^16th of the larger).
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 // j / d for j < 2^31, with what divide_by_page made of d.
@@ -345,6 +358,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
 
 // ---- Many rows: a block stays on an SM, with teams of TEAM warps, and the rows of a team come by bulk copies into a ring of
 // its own, so that what is in flight does not go by the registers that wait for it.
+// Two columns an instruction: with one it was short of issue slots (71 % of them taken) before it was short of HBM, 108 us, not
+// 100 (16384 x 5120).
 constexpr int kRingThreads = 1024, kHeld = 4;    // chunks of a row that a thread holds
 constexpr int kRingBytes = 200 * 1024;
 constexpr int kRingRows = 2;  // rows a team, at least
@@ -390,7 +405,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
     if (!ok && a.err) atomicOr(a.err, kErrTimeout);
     const int chunks = ok ? a.chunks : 0;
     const uint8_t* here = smem + (ring - smem_u32(smem)) + slot * slot_bytes;
-    float h[kHeld][V], sum = 0.0f;
+    uint64_t h[kHeld][V / 2], sum2 = f32x2(0.0f, 0.0f);  // two columns each
     uint32_t top = 0, mine[kHeld];
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
@@ -399,21 +414,34 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       mine[i] = 0;
       if (c < chunks) {
         Raw<T, V> x, r;
-        float w[V];
+        float w[V], largest = 0.0f;
         load_raw<T, V>(reinterpret_cast<const T*>(here) + c * V, x);
-        if (a.r) load_raw<T, V>(reinterpret_cast<const T*>(here + row_bytes) + c * V, r);
-        make_h<T, V>(a, row, c, x, r, h[i]);
+        if (a.r) {
+          load_raw<T, V>(reinterpret_cast<const T*>(here + row_bytes) + c * V, r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x.w[j] = sizeof(T) == 4 ? __float_as_uint(__uint_as_float(x.w[j]) + __uint_as_float(r.w[j])) : add_bf16x2(x.w[j], r.w[j]);
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.r_out) + row * a.r_out_row + static_cast<int64_t>(c) * V) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+        }
         if (a.w32) load_vec<float, V>(static_cast<const float*>(a.w) + c * V, w);
         else load_vec<uint16_t, V>(static_cast<const uint16_t*>(a.w) + c * V, w);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          sum = fmaf(h[i][j], h[i][j], sum);
-          h[i][j] *= w[j];
-          if constexpr (EIGHT != 0) mine[i] = max(mine[i], __float_as_uint(h[i][j]) & 0x7fffffffu);
+        for (int j = 0; j < V / 2; ++j) {
+          const uint64_t v = f32x2(element<T, V>(x, 2 * j), element<T, V>(x, 2 * j + 1));
+          sum2 = fma_f32x2(v, v, sum2);
+          h[i][j] = mul_f32x2(v, f32x2(w[2 * j], w[2 * j + 1]));
+          if constexpr (EIGHT != 0) {
+            float p, q;
+            f32x2_split(h[i][j], p, q);
+            largest = max_abs(largest, p, q);
+          }
         }
+        mine[i] = __float_as_uint(largest);
         if constexpr (EIGHT == 1) top = max(top, mine[i]);
       }
     }
+    float sum, odd;
+    f32x2_split(sum2, sum, odd);
+    sum += odd;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if constexpr (EIGHT == 1) top = __reduce_max_sync(0xffffffffu, top);
@@ -445,16 +473,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
         if (c < chunks && (c & (a.lanes - 1)) == 0) a.scale[row * a.groups + (c >> a.shift)] = scale;
       }
       if (c >= chunks) continue;
-      if constexpr (EIGHT == 0) {
+      const float by = EIGHT == 0 ? 1.0f : __fdividef(1.0f, scale);
+      float y[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) h[i][j] *= factor;
-        store_vec<T, V>(static_cast<T*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, h[i]);
-      } else {
-        const float by = __fdividef(1.0f, scale);
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[i][j] = h[i][j] * factor * by;
-        store_e4m3<V>(static_cast<uint8_t*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, h[i]);
+      for (int j = 0; j < V / 2; ++j) {
+        uint64_t v = mul_f32x2(h[i][j], f32x2(factor, factor));
+        if constexpr (EIGHT != 0) v = mul_f32x2(v, f32x2(by, by));
+        f32x2_split(v, y[2 * j], y[2 * j + 1]);
       }
+      if constexpr (EIGHT == 0) store_vec<T, V>(static_cast<T*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, y);
+      else store_e4m3<V>(static_cast<uint8_t*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, y);
     }
   }
 }
