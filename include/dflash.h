@@ -604,7 +604,8 @@ DFLASH_API size_t dflash_shared_workspace_size(int num_reqs, int num_groups, int
  *              are read in the pages of the shortest such sequence. Shorter sequences of the group read their own
  *              rows. Negative or above max_ctx_len: reported and treated as 0.
  *   flags      0 or DFLASH_FLAG_FORCE_SHARE. Without it, calls that could read at most 160 MB if every sequence read its own
- *              rows (num_reqs x Hkv x Dh x 4 bytes x max_ctx_len, or the window) let them do so, and only report bad groups.
+ *              rows (num_reqs x Hkv x Dh x 4 bytes x max_ctx_len, or the window) let them do so, and only report bad groups;
+ *              and so do groups whose (sequences - 1) x prefix is below 512 rows. Prefixes below 64 rows are never shared.
  *   Every other argument, and the result, as dflash_decode_attention_paged (the workspace as
  *   dflash_shared_workspace_size says). The result does not depend on timing; another prefix gives another order of the
  *   sums. With a window, rows are read once for all where the windows of all that share reach them; a sequence whose

@@ -25,7 +25,8 @@
 // loads its token's positions of all axes at once and picks one for each of its pairs.
 //
 // Measured: 32768 rows of 40 heads of 128 (671 MB) 104.2 us, 95% of the copy rate; 2001 rows of 20 heads, 20 of 80 elements, in f32
-// 5.3 us (floor 3.8); 32 rows into pages 3.2 us, a launch. Blocks of their own for what is copied:
+// 5.3 us (floor 3.8); 32 rows into pages 3.2 us, a launch. Over three axes: the gradient of 16384 rows of 40 heads of 128 (336 MB)
+// 56.5 us, 88 %; 32 rows into pages 3.4. Blocks of their own for what is copied:
 // threads of both kinds in a warp took 67 us instead of 42 for 26170 rows of 7 heads of 256 into pages, 27 instead of 14
 // for 6491 rows of 40 heads of 64.
 #include <cuda_runtime.h>

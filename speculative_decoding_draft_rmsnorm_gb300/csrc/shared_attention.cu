@@ -3,6 +3,27 @@
 // As in decode_attention.cu, head h of sequence r attends to its stored rows first <= j < L:
 //     o = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j - m),  s_j = scale log2(e) <q, k_j>,  m = max_j s_j
 // and partial results (m, l, O) over disjoint rows join as M = max m_i, l = sum l_i 2^(m_i - M), O = sum O_i 2^(m_i - M).
+//
+// Over a prefix that a group holds in the same pages, the (sequence, head) pairs of a kv head are the rows of one matrix: S =
+// Q K^T and O = P V on the tensor cores, K and V read once for up to 128 pairs. Five launches, each beginning while the one
+// before it ends:
+//   plan      one block: which groups share and how much, and equal parts of all their tiles for the blocks (5 us)
+//   prefix    a block an SM: units of (kv head, up to 128 pairs), tiles of 128 rows; a unit may be cut between blocks
+//   own       every sequence's other rows: decode_attention.cu's two kernels
+//   finish    a warp a head: the parts of the prefix and the own rows, normalised
+//
+// What bounds it. Up to some 128 pairs a group HBM does: a tile of K and V is 64 KB, 1.45 us of an SM's share. Beyond, tiles
+// come from L2 for the second unit on, and the chain from scores by way of weights to sums does: per tile the products take 1570
+// cycles of the tensor pipe (the weights are two bf16 terms, hence two products for O; three for f32 outputs), the exponentials and roundings 2400 of
+// two warpgroups that take tiles in turn, and a tile's sums have to be in registers before the next one's products may
+// begin; measured 2900 (tensor pipe 52 % active, issue slots 46 %). The rest is fixed: plan 5 us, a block's first tile 4, the own rows'
+// join 3, the finish 5.
+//
+// Why it is cut like this. Weights keep 16 bits (24), as in decode_attention.cu: with 8 each would be rounded as coarsely as
+// the output is. A tile's sums are taken out and added in registers, rounded, because the unit cuts its sums off (and a maximum
+// that grows costs registers only). Warps have one job each, and the copies three: the unit takes some 130 cycles a
+// box. Measured (us, plain floor in brackets): 32 groups of 8 beams on prompts of 512 to 8192 rows 101 (65), 64 samples of a prompt of 32000
+// rows 103 (48.5), 16 x 5 in windows of 4096, f32 100 (48.6), 256 on 16384 rows 136 (36.8, by its products).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -20,8 +41,11 @@ namespace {
 constexpr int kKeys = 128;   // rows of a tile
 constexpr int kRows = 128;   // (sequence, head) pairs of a unit: the lanes of tensor memory
 constexpr int kPlanThreads = 1024;
-// A prefix of fewer rows is left to the sequences: half a tile.
-constexpr int kLeastPrefix = 64;
+// A prefix of fewer rows is left to the sequences: half a tile. And, unless sharing is asked for, one that saves fewer reads of
+// rows, (sequences - 1) x prefix: a unit's start costs as much. 64 groups of 8 with 400 rows of their own and prefixes of 64 139 us shared,
+// 129 each for itself; of 128 140 and 142; of 256 142 and 174. 64 of 4: of 128 89 and 83, of 192 92 and 90, of 256 93 and 98;
+// 128 of 2: of 256 108 and 102; 16 of 32: of 64 83 and 79, of 96 83 and 87.
+constexpr int kLeastPrefix = 64, kLeastSaved = 512;
 // Calls that read no more than this when each sequence reads its own rows do so: the shared rows come from L2 then, and
 // the launches here take longer. 4 x 4 sequences of 1000 rows (62 MB): 19 us each for itself, 29 shared; of 2000 27 and 31, of
 // 4000 43 and 36; 64 sequences of 2000 rows of 2 kv heads (125 MB) 27 and 31, of 4000 42 and 33.
@@ -95,6 +119,7 @@ struct SharedArgs {
   float* lse;
   int num_reqs, num_groups, hq, hkv, g;
   int max_len, window;
+  int least_saved;  // rows that sharing has to save
   int64_t num_pages;
   int page;
   uint32_t page_mul, page_shift;  // j / page
@@ -150,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   // what group g may share
   auto shared_rows = [&](int g, int members) {
     const int p = prefixes[g];
-    return members > 1 && p >= kLeastPrefix && p <= a.max_len ? p : 0;
+    return members > 1 && p >= kLeastPrefix && p <= a.max_len && (members - 1ll) * p >= a.least_saved ? p : 0;
   };
   // sequence r's group if it shares, else -1
   auto shares_in = [&](int r, int len, int& p) {
@@ -966,6 +991,7 @@ int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const
   a.out = out, a.lse = lse;
   a.num_reqs = num_reqs, a.num_groups = num_groups, a.hq = hq, a.hkv = hkv;
   a.max_len = max_ctx_len, a.window = window;
+  a.least_saved = flags & DFLASH_FLAG_FORCE_SHARE ? 0 : kLeastSaved;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Few rows, whoever shares them: each sequence reads its own
   const int64_t longest = window > 0 ? std::min(max_ctx_len, window) : max_ctx_len;

