@@ -281,6 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   const int g = lane >> 2, t = lane & 3;
   const int heads = a.hkv * a.tile_units;
   grid_dependents_launch();  // the join's launch overlaps; it waits for this grid's end
+  // This grid may begin before the one before it has ended, and reads what the one before that wrote: not from an L1 that has
+  // an older state of it
+  if constexpr (OWN) __threadfence();
 
   const int my_unit = warp / a.unit, tile_in_unit = warp - my_unit * a.unit;
   if (lane == 0) s_seg[warp] = Segments{};
