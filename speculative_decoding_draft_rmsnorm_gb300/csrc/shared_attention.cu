@@ -140,8 +140,8 @@ __device__ __forceinline__ int first_row(const SharedArgs& a, int len) { return 
 // are the rows that all of those see: what a window leaves out, whatever it holds, is in no product of its sequence. The
 // others of the prefix that some of them see, at most as many as in half a window, they read like rows of their own.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ SharedArgs a) {
-  __shared__ int s_bad, s_groups;
-  __shared__ uint32_t s_tiles, s_units, s_warp[32], s_warp_units[32];
+  __shared__ int s_bad;
+  __shared__ uint32_t s_warp[32], s_warp_units[32];
   __shared__ uint2 s_at[kPlanThreads];  // tiles and units before the first groups
   __shared__ uint32_t s_lo[kPlanThreads];
   __shared__ int s_count[32];
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   const int32_t* prefixes = fit ? s_prefixes : a.prefixes;
   unsigned long long* least = fit ? s_least : a.least;
   int32_t* most = fit ? s_most : a.most;
-  if (tid == 0) s_bad = 0, s_tiles = 0, s_units = 0, s_groups = 0;
+  if (tid == 0) s_bad = 0;
   const int raw_len = tid < a.num_reqs ? a.lens[tid] : 0;
   __syncthreads();
   for (int g = tid; g < a.num_groups; g += kPlanThreads) {
@@ -215,6 +215,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       a.own[r] = g < 0 ? make_int2(0, 0) : make_int2(p, p - first_for_all(g));
     }
   }
+  uint32_t all_tiles = 0, all_units = 0;
+  int sharing = 0;
   for (int base = 0; base < groups; base += kPlanThreads) {
     const int g = base + tid;
     SharedGroup x{};
@@ -242,29 +244,34 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     if (lane == 31) s_warp[warp] = upto, s_warp_units[warp] = units_to, s_count[warp] = __popc(have);
     __syncthreads();
-    uint32_t before = s_tiles, units_before = s_units;
-    int at = s_groups + __popc(have & ((1u << lane) - 1));
-    for (int i = 0; i < warp; ++i) before += s_warp[i], units_before += s_warp_units[i], at += s_count[i];
+    uint32_t w_tiles = s_warp[lane], w_units = s_warp_units[lane], w_count = static_cast<uint32_t>(s_count[lane]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x1 = __shfl_up_sync(0xffffffffu, w_tiles, o), x2 = __shfl_up_sync(0xffffffffu, w_units, o),
+                     x3 = __shfl_up_sync(0xffffffffu, w_count, o);
+      if (lane >= o) w_tiles += x1, w_units += x2, w_count += x3;
+    }
+    const int last = max(warp - 1, 0);
+    const uint32_t t0 = __shfl_sync(0xffffffffu, w_tiles, last), u0 = __shfl_sync(0xffffffffu, w_units, last), c0 = __shfl_sync(0xffffffffu, w_count, last);
     if (tiles) {
-      x.start = before + upto - tiles;
-      x.units = units_before + units_to - units;
+      const int at = sharing + (warp ? static_cast<int>(c0) : 0) + __popc(have & ((1u << lane) - 1));
+      x.start = all_tiles + (warp ? t0 : 0) + upto - tiles;
+      x.units = all_units + (warp ? u0 : 0) + units_to - units;
       a.groups[at] = x;
       if (at < kPlanThreads) s_at[at] = make_uint2(x.start, x.units);
     }
-    __syncthreads();
-    if (tid == 0)
-      for (int i = 0; i < 32; ++i) s_tiles += s_warp[i], s_units += s_warp_units[i], s_groups += s_count[i];
+    all_tiles += __shfl_sync(0xffffffffu, w_tiles, 31), all_units += __shfl_sync(0xffffffffu, w_units, 31);
+    sharing += static_cast<int>(__shfl_sync(0xffffffffu, w_count, 31));
     __syncthreads();
   }
   Totals z;
-  z.tiles = s_tiles;
+  z.tiles = all_tiles;
   z.unit_cost = z.tiles < kFewTiles * a.blocks ? 0 : kUnitCost;
   z.blocks = min(static_cast<uint32_t>(a.blocks), max(z.tiles, 1u));
-  z.cost = static_cast<uint64_t>(kTileCost) * z.tiles + static_cast<uint64_t>(z.unit_cost) * s_units;
+  z.cost = static_cast<uint64_t>(kTileCost) * z.tiles + static_cast<uint64_t>(z.unit_cost) * all_units;
   if (tid == 0) *a.totals = z;
   // ---- the blocks' ranges
   __threadfence_block();
-  const int sharing = s_groups;
   for (int base = 0; base < a.blocks; base += kPlanThreads - 1) {
     const int b = base + tid;
     BlockRange r{};
