@@ -490,9 +490,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
 // ---- Rows whose width is no multiple of a 16-byte chunk, so that each begins somewhere else in one: chunks are cut where memory
 // is aligned, columns c V - shift on, and only those at a row's ends go element by element. Weights and groups go by columns:
 // the weights one by one (from L1), and a chunk may have the end of one group and the beginning of the next.
-constexpr int kShiftedHeld = 2;
-
-template <typename T, int EIGHT>
+// A thread holds HELD chunks: two, or in the widest rows four (element by element 4883 x 8191 in f32 took 193 us).
+template <typename T, int EIGHT, int HELD>
 __global__ void __launch_bounds__(1024) shifted_kernel(const __grid_constant__ NormArgs a) {
   constexpr int V = 16 / sizeof(T);
   __shared__ float s_sum[32];
@@ -508,11 +507,11 @@ __global__ void __launch_bounds__(1024) shifted_kernel(const __grid_constant__ N
     for (int i = tid; i < a.groups; i += threads) s_group[i] = 0;
     __syncthreads();
   }
-  float h[kShiftedHeld][V], sum = 0.0f;
+  float h[HELD][V], sum = 0.0f;
   uint32_t top = 0;
   auto edge = [&](int c0) { return c0 < 0 || c0 + V > a.d; };
 #pragma unroll
-  for (int i = 0; i < kShiftedHeld; ++i) {
+  for (int i = 0; i < HELD; ++i) {
     const int c0 = (i * threads + tid) * V - shift;
     if (c0 >= a.d) continue;
     Raw<T, V> x{}, r{};
@@ -589,7 +588,7 @@ __global__ void __launch_bounds__(1024) shifted_kernel(const __grid_constant__ N
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < kShiftedHeld; ++i) {
+  for (int i = 0; i < HELD; ++i) {
     const int c0 = (i * threads + tid) * V - shift;
     if (c0 >= a.d) continue;
     float by_next = by;
@@ -844,18 +843,24 @@ void launch_width(int v, int held, const NormArgs& a, int threads, int eight, cu
 }
 
 // Rows that begin anywhere in a chunk: whether they were launched. Every tensor's rows must begin at the same place.
+template <typename T, int HELD>
+void launch_shifted(const NormArgs& a, int chunks, int eight, cudaStream_t st) {
+  const int threads = std::min(1024, (chunks + 32 * HELD - 1) / (32 * HELD) * 32);
+  const unsigned grid = static_cast<unsigned>(a.n);
+  if (eight == 0) shifted_kernel<T, 0, HELD><<<grid, threads, 0, st>>>(a);
+  else if (eight == 1) shifted_kernel<T, 1, HELD><<<grid, threads, 0, st>>>(a);
+  else shifted_kernel<T, 2, HELD><<<grid, threads, 0, st>>>(a);
+}
 template <typename T>
 bool try_shifted(const NormArgs& a, int v, int eight, int out_size, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const int chunks = a.d / V + 2, threads = std::min(1024, (chunks + 32 * kShiftedHeld - 1) / (32 * kShiftedHeld) * 32);
-  if (v >= V || a.d < 4 * V || chunks > kShiftedHeld * 1024) return false;
+  const int chunks = a.d / V + 2;
+  if (v >= V || a.d < 4 * V || chunks > 4 * 1024) return false;
   auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
   if (at(a.x) % 16 || at(a.out) % (V * out_size) || a.out_row % V != a.x_row % V) return false;
   if (a.r && (at(a.r) % 16 || at(a.r_out) % 16 || a.r_row % V != a.x_row % V || a.r_out_row % V != a.x_row % V)) return false;
-  const unsigned grid = static_cast<unsigned>(a.n);
-  if (eight == 0) shifted_kernel<T, 0><<<grid, threads, 0, st>>>(a);
-  else if (eight == 1) shifted_kernel<T, 1><<<grid, threads, 0, st>>>(a);
-  else shifted_kernel<T, 2><<<grid, threads, 0, st>>>(a);
+  if (chunks <= 2 * 1024) launch_shifted<T, 2>(a, chunks, eight, st);
+  else launch_shifted<T, 4>(a, chunks, eight, st);
   return true;
 }
 
