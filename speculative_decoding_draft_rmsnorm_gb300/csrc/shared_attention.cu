@@ -14,16 +14,16 @@
 //
 // What bounds it. Up to some 128 pairs a group HBM does: a tile of K and V is 64 KB, 1.45 us of an SM's share. Beyond, tiles
 // come from L2 for the second unit on, and the chain from scores by way of weights to sums does: per tile the products take 1570
-// cycles of the tensor pipe (the weights are two bf16 terms, hence two products for O; three for f32 outputs), the exponentials and roundings 2400 of
-// two warpgroups that take tiles in turn, and a tile's sums have to be in registers before the next one's products may
-// begin; measured 2900 (tensor pipe 52 % active, issue slots 46 %). The rest is fixed: plan 5 us, a block's first tile 4, the own rows'
+// cycles of the tensor pipe (the weights are two bf16 terms, hence two products for O; three for f32 outputs), the exponentials and
+// roundings some 5000 of a warpgroup, which take tiles in turn, and a tile's sums have to be in registers before the next
+// one's products may begin; measured 2900 (tensor pipe 52 % active, issue slots 46 %). The rest is fixed: plan 5 us, a block's first tile 4, the own rows'
 // join 3, the finish 5.
 //
 // Why it is cut like this. Weights keep 16 bits (24), as in decode_attention.cu: with 8 each would be rounded as coarsely as
 // the output is. A tile's sums are taken out and added in registers, rounded, because the unit cuts its sums off (and a maximum
 // that grows costs registers only). Warps have one job each, and the copies three: the unit takes some 130 cycles a
-// box. Measured (us, plain floor in brackets): 32 groups of 8 beams on prompts of 512 to 8192 rows 101 (65), 64 samples of a prompt of 32000
-// rows 103 (48.5), 16 x 5 in windows of 4096, f32 100 (48.6), 256 on 16384 rows 136 (36.8, by its products).
+// box. Measured (us, plain floor in brackets): 32 groups of 8 beams on prompts of 512 to 8192 rows 99 (65), 64 samples of a prompt of 32000
+// rows 100 (48.5), 16 x 5 in windows of 4096, f32 89 (48.6), 256 on 16384 rows 132 (36.8, by its products).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -348,12 +348,8 @@ struct Walk {
   }
 };
 
-// Warps 0, 1 and 2 copy K, V and Q, 3 issues products, 4-7 and 8-11 make weights, 12-15 add the sums up.
+// Warps 0, 1 and 2 copy K, V and Q, 3 issues products; then come the warpgroups that make weights, and one that adds the sums up.
 constexpr int kIssuer = 3;
-constexpr int kThreads = 16 * 32;
-// Registers of a thread in the three kinds of warpgroups: together at most what the block is launched with, 4 x 128.
-constexpr int kCopyRegs = 80, kSumRegs = 176;
-static_assert(kCopyRegs + 2 * 128 + kSumRegs <= 4 * 128, "the block's registers");
 
 // Shared memory: two Q tiles and a ring of K and V tiles, each in 8-row groups of DH / 64 blocks of 8 rows x 128 bytes
 // (128-byte swizzle): as a box of a page lands. Tensor memory: kBufs buffers of scores, whose columns the weights take (16 rows'
@@ -367,6 +363,13 @@ struct Shape {
   static constexpr int kTerms = F32 ? 3 : 2;
   static constexpr int kBufs = F32 ? 2 : 3;
   static constexpr int kLead = kBufs - 1;  // tiles whose scores come before a tile's sums
+  // warpgroups that make weights, a buffer each. They load 16 columns and wait for them: with the next ones on their way they need
+  // registers that spill (f32 outputs 98 us instead of 89, 16 x 5 in windows); three of them so 157 instead of 132 (256 sequences).
+  static constexpr int kWeighers = kBufs;
+  static constexpr int kThreads = (2 + kWeighers) * 128;
+  // Registers of a thread: at the launch, and in the three kinds of warpgroups, together at most the block's
+  static constexpr int kLaunchRegs = F32 ? 128 : 96, kCopyRegs = F32 ? 80 : 64, kWeighRegs = F32 ? 128 : 80, kSumRegs = 176;
+  static_assert(kCopyRegs + kWeighers * kWeighRegs + kSumRegs <= (2 + kWeighers) * kLaunchRegs, "the block's registers");
   static constexpr int kBufCols = F32 ? 192 : 128;
   static constexpr int kOut = 384;
   static constexpr int kRing = 2 * kTile;
@@ -398,7 +401,7 @@ __device__ __forceinline__ void registers_up() {
 }
 
 template <int DH, bool F32>
-__global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ SharedArgs a) {
+__global__ void __launch_bounds__(Shape<DH, F32>::kThreads, 1) prefix_kernel(const __grid_constant__ SharedArgs a) {
   using S = Shape<DH, F32>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -440,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   };
   auto wait_warp = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
   bool ok = true;
-  if (warp < 4) registers_down<kCopyRegs>();
+  if (warp < 4) registers_down<S::kCopyRegs>();
+  else if (warp < 4 + 4 * S::kWeighers && S::kWeighRegs < S::kLaunchRegs) registers_down<S::kWeighRegs>();
 
   if (range.lo >= range.hi) {
     // no tiles
@@ -661,9 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       mbar_wait(bar(S::kDrain), 0, &dummy);
     }
     __syncwarp();
-  } else if (warp < 12) {
-    // ------------------------------------------------------------ weights: tile t by warps 4-7 (even) or 8-11, a row a thread
-    const int half = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
+  } else if (warp < 4 + 4 * S::kWeighers) {
+    // ------------------------------------------------------------ weights: tile t by warpgroup t % kWeighers of them, a row a thread
+    const int mine = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     Walk walk(a, range);
     Unit u;
@@ -674,8 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       const bool idle = u.m0 + (warp & 3) * 32 >= u.rows;  // lanes that hold no rows may hold anything
 #pragma unroll 1
       for (int i = u.t0; i < u.t1; ++i, ++t) {
-        if ((t & 1) != static_cast<uint32_t>(half)) continue;
         const int buf = t % S::kBufs;
+        if (buf != mine) continue;
         const uint32_t s = tmem + lanes + buf * S::kBufCols;
         if (!(ok = wait_warp(bar(S::kSFull + buf), (t / S::kBufs) & 1))) break;
         if (idle) {
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const int c_lo = from - i * kKeys, c_hi = u.prefix - u.lo - i * kKeys;  // columns [c_lo, c_hi) are seen
         // (votes, though all lanes agree: as plain conditions the compiler's loops are slower, 256 sequences 140 us, 136)
         const bool whole = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kKeys);
-        // 16 columns at a time, the next ones on their way; first for the maximum, then for the weights
+        // 16 columns at a time, first for the maximum, then for the weights
         auto masked = [&](uint32_t (&r)[16], int b) {
           if (whole || __all_sync(0xffffffffu, c_lo <= b * 16 && b * 16 + 16 <= c_hi)) return;
 #pragma unroll
@@ -700,16 +704,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 #pragma unroll
           for (int j = 0; j < 16; j += 2) top = fmax3(top, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
         };
-        uint32_t r0[16], r1[16];
-        tmem_ld_32x32b<16>(s, r0);
+        uint32_t r[16];
 #pragma unroll 1
-        for (int b = 0; b < steps; b += 2) {
+        for (int b = 0; b < steps; ++b) {
+          tmem_ld_32x32b<16>(s + b * 16, r);
           tmem_wait_ld();
-          tmem_ld_32x32b<16>(s + (b + 1) * 16, r1);
-          highest(r0, b);
-          tmem_wait_ld();
-          tmem_ld_32x32b<16>(s + (b + 2 < steps ? b + 2 : 0) * 16, r0);  // 0 again behind the last
-          highest(r1, b + 1);
+          highest(r, b);
         }
         m = fmaxf(m, top * a.scale_log2);
         const float ref = m == -INFINITY ? 0.0f : m;
@@ -740,13 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           if (F32) tmem_st_32x32b<8>(s + 128 + b * 8, low);
         };
 #pragma unroll 1
-        for (int b = 0; b < steps; b += 2) {
+        for (int b = 0; b < steps; ++b) {
+          tmem_ld_32x32b<16>(s + b * 16, r);
           tmem_wait_ld();
-          tmem_ld_32x32b<16>(s + (b + 1) * 16, r1);
-          weigh(r0, b);
-          tmem_wait_ld();
-          if (b + 2 < steps) tmem_ld_32x32b<16>(s + (b + 2) * 16, r0);
-          weigh(r1, b + 1);
+          weigh(r, b);
         }
         float s0, s1;
         f32x2_split(sum2, s0, s1);
@@ -761,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     }
   } else {
     // ------------------------------------------------------------ sums: a row a thread, every tile's products added in registers
-    registers_up<kSumRegs>();
+    registers_up<S::kSumRegs>();
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     Walk walk(a, range);
@@ -777,12 +774,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       for (int i = u.t0; i < u.t1; ++i, ++t) {
         const int buf = t % S::kBufs;
         if (!(ok = wait_warp(bar(S::kPFull + buf), (t / S::kBufs) & 1))) break;
-        if (!(ok = wait_warp(bar(S::kOFull), t & 1))) break;
         if (idle) {
+          if (!(ok = wait_warp(bar(S::kOFull), t & 1))) break;
           if (lane == 0) mbar_arrive(bar(S::kOEmpty + (t & 1)));
           continue;
         }
-        tc_fence_after();
         const float2 st = stats[(t & 1) * kRows + row];
         const float top = fmaxf(m, st.x);
         const float old = m == -INFINITY ? 0.0f : ex2_approx(m - top), now = st.x == -INFINITY ? 0.0f : ex2_approx(st.x - top);
@@ -793,19 +789,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 #pragma unroll
           for (int j = 0; j < DH / 2; ++j) acc[j] = mul_f32x2(acc[j], old2);
         }
+        // from here until the last load has landed the next products wait
+        if (!(ok = wait_warp(bar(S::kOFull), t & 1))) break;
+        tc_fence_after();
+        uint32_t r[2][16];
+        tmem_ld_32x32b<16>(tmem + lanes + S::kOut, r[0]);
 #pragma unroll
         for (int b = 0; b < DH / 16; ++b) {
-          uint32_t r[16];
-          tmem_ld_32x32b<16>(tmem + lanes + S::kOut + b * 16, r);
           tmem_wait_ld();
-          if (b == DH / 16 - 1) {
+          if (b + 1 < DH / 16) {
+            tmem_ld_32x32b<16>(tmem + lanes + S::kOut + (b + 1) * 16, r[(b + 1) & 1]);
+          } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(S::kOEmpty + (t & 1)));
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            acc[b * 8 + j] = fma_f32x2(f32x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), now2, acc[b * 8 + j]);
+            acc[b * 8 + j] = fma_f32x2(f32x2(__uint_as_float(r[b & 1][2 * j]), __uint_as_float(r[b & 1][2 * j + 1])), now2, acc[b * 8 + j]);
         }
       }
       if (!ok) break;
@@ -928,10 +929,16 @@ cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, int bytes, cudaS
 
 template <int DH, bool F32>
 cudaError_t launch_prefix(const SharedArgs& a, int sms, cudaStream_t st) {
-  constexpr int kBytes = Shape<DH, F32>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<DH, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  using S = Shape<DH, F32>;
+  // The split of the block's registers goes by what it is launched with: warps would wait for more for ever
+  static const int regs = [] {
+    cudaFuncAttributes f{};
+    return cudaFuncGetAttributes(&f, prefix_kernel<DH, F32>) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (regs != S::kLaunchRegs) return cudaErrorInvalidKernelImage;
+  const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<DH, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_after(prefix_kernel<DH, F32>, dim3(static_cast<unsigned>(sms)), kThreads, kBytes, st, a);
+  return launch_after(prefix_kernel<DH, F32>, dim3(static_cast<unsigned>(sms)), S::kThreads, S::kBytes, st, a);
 }
 
 }  // namespace
