@@ -368,7 +368,7 @@ struct Shape {
   static constexpr int kWeighers = kBufs;
   static constexpr int kThreads = (2 + kWeighers) * 128;
   // Registers of a thread: at the launch, and in the three kinds of warpgroups, together at most the block's
-  static constexpr int kLaunchRegs = F32 ? 128 : 96, kCopyRegs = F32 ? 80 : 64, kWeighRegs = F32 ? 128 : 80, kSumRegs = 176;
+  static constexpr int kLaunchRegs = F32 ? 128 : 96, kCopyRegs = F32 ? 96 : 72, kWeighRegs = F32 ? 104 : 72, kSumRegs = F32 ? 208 : 192;
   static_assert(kCopyRegs + kWeighers * kWeighRegs + kSumRegs <= (2 + kWeighers) * kLaunchRegs, "the block's registers");
   static constexpr int kBufCols = F32 ? 192 : 128;
   static constexpr int kOut = 384;
