@@ -611,7 +611,7 @@ DFLASH_API size_t dflash_shared_workspace_size(int num_reqs, int num_groups, int
  *   sums. With a window, rows are read once for all where the windows of all that share reach them; a sequence whose
  *   window has left more than half of the prefix (or of what a window holds) behind reads all its rows itself. A sequence
  *   sees nothing of what rows hold that are outside its length and window, whatever that is. status also takes
- *   DFLASH_STATUS_TIMEOUT, where a bounded wait ran out.
+ *   DFLASH_STATUS_TIMEOUT, where a bounded wait ran out: sequences that share a prefix are NaN then (out and lse).
  */
 DFLASH_API int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const dflash_bf16* k_pool,
                                               const dflash_bf16* v_pool, const int32_t* block_table,

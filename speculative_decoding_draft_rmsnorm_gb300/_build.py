@@ -4,8 +4,8 @@ Translation units are compiled in parallel, then linked with nvcc -shared. The o
 lands in speculative_decoding_draft_rmsnorm_gb300/_lib/; objects go to _build/.
 
 A second library, libdflash_gb300_waittest.so, is built from the same sources with
-DFLASH_WAIT_TEST defined: device waits give up after 5 ms instead of 2 s, and a hook can
-withhold one V tile's copy, so that a test can watch a bounded wait run out and the
+DFLASH_WAIT_TEST defined: device waits give up after 5 ms instead of 2 s, and hooks can
+withhold one copy of a kernel, so that a test can watch a bounded wait run out and the
 kernel unwind. Only the tests load it; the package loads the product library.
 
 The marshalling module of decode.py (csrc/bind.cpp, host C++ against torch and the product

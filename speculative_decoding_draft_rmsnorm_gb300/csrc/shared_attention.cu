@@ -69,6 +69,7 @@ struct alignas(16) SharedGroup {
 };
 struct Totals {
   uint32_t tiles, unit_cost, blocks;  // blocks: that have tiles
+  uint32_t failed;                    // a wait of the prefix kernel ran out
   uint64_t cost;
 };
 // A block's tiles, and where in their group they begin.
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __syncthreads();
   }
   Totals z;
-  z.tiles = all_tiles;
+  z.tiles = all_tiles, z.failed = 0;
   z.unit_cost = z.tiles < kFewTiles * a.blocks ? 0 : kUnitCost;
   z.blocks = min(static_cast<uint32_t>(a.blocks), max(z.tiles, 1u));
   z.cost = static_cast<uint64_t>(kTileCost) * z.tiles + static_cast<uint64_t>(z.unit_cost) * all_units;
@@ -350,6 +351,11 @@ struct Walk {
 
 // Warps 0, 1 and 2 copy K, V and Q, 3 issues products; then come the warpgroups that make weights, and one that adds the sums up.
 constexpr int kIssuer = 3;
+
+#ifdef DFLASH_WAIT_TEST
+// Test build only: (block, tile of its own) whose copy of K is withheld.
+__device__ int2 g_withhold_k = {-1, -1};
+#endif
 
 // Shared memory: two Q tiles and a ring of K and V tiles, each in 8-row groups of DH / 64 blocks of 8 rows x 128 bytes
 // (128-byte swizzle): as a box of a page lands. Tensor memory: kBufs buffers of scores, whose columns the weights take (16 rows'
@@ -551,6 +557,9 @@ __global__ void __launch_bounds__(Shape<DH, F32>::kThreads, 1) prefix_kernel(con
           }
           if (!(ok = wait_warp(b, parity))) break;
         }
+#ifdef DFLASH_WAIT_TEST
+        if (!is_v && static_cast<int>(blockIdx.x) == g_withhold_k.x && static_cast<int>(i) == g_withhold_k.y) continue;
+#endif
         const uint32_t off = S::kRing + slot * S::kTile, b = bar(S::kFull + slot);
         if (now) {
           by_tma |= 1u << slot, parities = (parities & ~(1u << slot)) | (c / S::kSlots & 1) << slot;
@@ -831,7 +840,10 @@ __global__ void __launch_bounds__(Shape<DH, F32>::kThreads, 1) prefix_kernel(con
       }
     }
   }
-  if (!ok && lane == 0 && a.err) atomicOr(a.err, kErrTimeout);
+  if (!ok && lane == 0) {
+    a.totals->failed = 1;
+    if (a.err) atomicOr(a.err, kErrTimeout);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -848,7 +860,9 @@ __global__ void __launch_bounds__(kPlanThreads) check_kernel(const __grid_consta
   if (bad) atomicOr(a.err, kErrMetadata);
 }
 
-// Joins a head's parts, the prefix's and its own rows', and stores it; a warp a head.
+// Joins a head's parts, the prefix's and its own rows', and stores it; a warp a head. Where a wait of the prefix kernel ran out,
+// parts and the notes of where they are may be missing, and what lies in their places is another call's: none is looked at,
+// and heads with a prefix become NaN.
 template <int DH, bool F32>
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ SharedArgs a) {
   constexpr int C = DH / 32;
@@ -857,16 +871,14 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Sha
   grid_dependency_wait();
   if (row >= static_cast<int64_t>(a.num_reqs) * a.hq) return;
   const int r = static_cast<int>(row / a.hq), len = valid_len(a, a.lens[r]), shared = a.own[r].y;
-  const bool has_own = len > first_row(a, len) + shared, has_prefix = shared > 0;
+  const Totals z = *a.totals;
+  const bool has_prefix = shared > 0, lost = has_prefix && z.failed, has_own = !lost && len > first_row(a, len) + shared;
   int parts = 0;
   Where where{-1, 0, 0, 0};
-  if (has_prefix) {
+  if (has_prefix && !lost) {
     where = a.where[row];
     parts = 1;
-    if (where.first >= 0) {
-      const Totals z = *a.totals;
-      parts = static_cast<int>(cost_of(z, where.last, where.unit) * z.blocks / z.cost) - where.first + 1;
-    }
+    if (where.first >= 0) parts = static_cast<int>(cost_of(z, where.last, where.unit) * z.blocks / z.cost) - where.first + 1;
   }
   float o[C], m, l;
   // a lane's columns in a part lie kRows rows of 8 apart
@@ -877,7 +889,8 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Sha
     const int64_t slot = 2 * static_cast<int64_t>(where.first + p) + (p == 0 ? 1 : 0);
     return Part{a.part_o + slot * (kRows * DH) + where.row * 8 + lane_at, a.part_ml + (slot * kRows + where.row) * 2};
   }, o, m, l);
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  if (lost) l = __int_as_float(0x7fffffff);
+  const float inv = lost ? l : l > 0.0f ? 1.0f / l : 0.0f;
   if (F32) {
     store_row<DH>(static_cast<float*>(a.out) + row * DH, o, inv);
   } else {
@@ -887,7 +900,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Sha
     else
       *reinterpret_cast<uint32_t*>(dst + lane * 2) = pack_bf16x2(o[0] * inv, o[1] * inv);
   }
-  if (a.lse && lane == 0) a.lse[row] = l > 0.0f ? (m + __log2f(l)) * 0.693147180559945309f : -INFINITY;
+  if (a.lse && lane == 0) a.lse[row] = lost ? l : l > 0.0f ? (m + __log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
 
 struct SharedLayout {
@@ -1034,3 +1047,12 @@ int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const
 }
 
 }  // extern "C"
+
+#ifdef DFLASH_WAIT_TEST
+// Test build only: makes block `block` of the prefix kernel skip the copy of K of its `tile`-th tile in the following calls; -1
+// turns it off. Returns a cudaError_t.
+extern "C" __attribute__((visibility("default"))) int dflash_test_withhold_prefix_tile(int block, int tile) {
+  const int2 v = make_int2(block, tile);
+  return static_cast<int>(cudaMemcpyToSymbol(dflash::g_withhold_k, &v, sizeof v));
+}
+#endif
