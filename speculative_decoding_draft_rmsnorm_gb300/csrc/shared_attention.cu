@@ -890,7 +890,9 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Sha
     return Part{a.part_o + slot * (kRows * DH) + where.row * 8 + lane_at, a.part_ml + (slot * kRows + where.row) * 2};
   }, o, m, l);
   if (lost) l = __int_as_float(0x7fffffff);
-  const float inv = lost ? l : l > 0.0f ? 1.0f / l : 0.0f;
+  // nothing to attend to: zeros, and the log-sum of nothing. That goes by rows: a NaN among the scores makes l NaN
+  const bool none = parts + has_own == 0 && !lost;
+  const float inv = none ? 0.0f : 1.0f / l;
   if (F32) {
     store_row<DH>(static_cast<float*>(a.out) + row * DH, o, inv);
   } else {
@@ -900,7 +902,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Sha
     else
       *reinterpret_cast<uint32_t*>(dst + lane * 2) = pack_bf16x2(o[0] * inv, o[1] * inv);
   }
-  if (a.lse && lane == 0) a.lse[row] = lost ? l : l > 0.0f ? (m + __log2f(l)) * 0.693147180559945309f : -INFINITY;
+  if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (m + __log2f(l)) * 0.693147180559945309f;
 }
 
 struct SharedLayout {
