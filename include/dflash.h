@@ -543,7 +543,8 @@ DFLASH_API int dflash_compact_pages(int32_t* block_table, int64_t block_table_st
  *                Every other overlap of an output with a tensor of the call is refused.
  *   scales       f32 [n, ceil(d / group_size)], or [n] with group_size 0; e4m3 only
  *   group_size   0 or a multiple of 16; the last group may be short
- *   status       int32 device word or NULL: DFLASH_STATUS_TIMEOUT is ORed in where a bounded wait ran out (rows are missing)
+ *   status       int32 device word or NULL: DFLASH_STATUS_TIMEOUT is ORed in where a bounded wait ran out: rows of out (and
+ *                scales) are NaN then, and rows of residual_out missing
  *   d <= 65536. Sums in f32 (rows of values above 1e19 overflow them), one rounding to the output's type. A
  *   scale is infinite or NaN where a y of its group is. One launch.
  */

@@ -360,6 +360,12 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
 // its own, so that what is in flight does not go by the registers that wait for it.
 // Two columns an instruction: with one it was short of issue slots (71 % of them taken) before it was short of HBM, 108 us, not
 // 100 (16384 x 5120).
+// Where a team's wait runs out it takes no more rows: that row and the team's later ones become NaN, and copies that were begun
+// have landed (or were waited for once more) before the block ends.
+#ifdef DFLASH_WAIT_TEST
+// Test build only: a row that is not fetched.
+__device__ long long g_withhold_row = -1;
+#endif
 constexpr int kRingThreads = 1024, kHeld = 4;    // chunks of a row that a thread holds
 constexpr int kRingBytes = 200 * 1024;
 constexpr int kRingRows = 2;  // rows a team, at least
@@ -376,18 +382,21 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
   __shared__ uint64_t s_bar[R::kTeams * R::kMost];
   __shared__ float s_sum[2][R::kTeams][TEAM];
   __shared__ uint32_t s_top[2][R::kTeams][TEAM];
-  __shared__ int s_abort;
+  __shared__ int s_abort[R::kTeams];
   const int team = threadIdx.x / R::kThreads, tid = threadIdx.x % R::kThreads, lane = tid & 31, warp = tid >> 5;
   const uint32_t row_bytes = static_cast<uint32_t>(a.d) * sizeof(T), slot_bytes = a.r ? 2 * row_bytes : row_bytes;
   const uint32_t ring = smem_u32(smem) + team * a.slots * slot_bytes, bars = smem_u32(s_bar) + team * R::kMost * 8;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R::kTeams * R::kMost; ++i) mbar_init(smem_u32(s_bar) + 8 * i, 1);
-    s_abort = 0;
+    for (int i = 0; i < R::kTeams; ++i) s_abort[i] = 0;
     mbar_fence_init();
   }
   __syncthreads();
   const int64_t step = static_cast<int64_t>(gridDim.x) * R::kTeams;
   auto fetch = [&](int64_t row, int slot) {  // by one thread
+#ifdef DFLASH_WAIT_TEST
+    if (row == g_withhold_row) return;
+#endif
     const uint32_t dst = ring + slot * slot_bytes, b = bars + 8 * slot;
     mbar_arrive_expect_tx(b, slot_bytes);
     bulk_load(dst, static_cast<const T*>(a.x) + row * a.x_row, row_bytes, b);
@@ -398,11 +407,22 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
     for (int i = 0; i < a.slots && row + i * step < a.n; ++i) fetch(row + i * step, i);
   uint32_t slot = 0, parity = 0;
   int side = 0;
+  bool ok = true;  // this thread's waits, up to now
 #pragma unroll 1
   for (; row < a.n; row += step, side ^= 1) {
-    // where the wait runs out the row is left out, and the team stays together
-    const bool ok = mbar_wait(bars + 8 * slot, parity, &s_abort);
-    if (!ok && a.err) atomicOr(a.err, kErrTimeout);
+    if (ok && !mbar_wait(bars + 8 * slot, parity, &s_abort[team])) {
+      ok = false;  // the team stays together: its barriers are still passed
+      if (a.err) atomicOr(a.err, kErrTimeout);
+      if (tid == 0) {  // what it has fetched: this row and those in the slots behind
+        uint32_t at = slot, p = parity;
+#pragma unroll 1
+        for (int i = 0; i < a.slots && row + i * step < a.n; ++i) {
+          int dummy = 0;
+          mbar_wait(bars + 8 * at, p, &dummy);
+          if (++at == static_cast<uint32_t>(a.slots)) at = 0, p ^= 1;
+        }
+      }
+    }
     const int chunks = ok ? a.chunks : 0;
     const uint8_t* here = smem + (ring - smem_u32(smem)) + slot * slot_bytes;
     uint64_t h[kHeld][V / 2], sum2 = f32x2(0.0f, 0.0f);  // two columns each
@@ -437,11 +457,15 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
         }
         mine[i] = __float_as_uint(largest);
         if constexpr (EIGHT == 1) top = max(top, mine[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) h[i][j] = f32x2(0.0f, 0.0f);
       }
     }
     float sum, odd;
     f32x2_split(sum2, sum, odd);
     sum += odd;
+    if (!ok) sum = __int_as_float(0x7fffffff);  // and with it the row's factor and scales
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if constexpr (EIGHT == 1) top = __reduce_max_sync(0xffffffffu, top);
@@ -450,7 +474,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       if constexpr (EIGHT == 1) s_top[side][team][warp] = top;
     }
     if constexpr (TEAM == 1) __syncwarp();
-    else named_barrier(team, R::kThreads);  // and the row has been read
+    else named_barrier(team, R::kThreads);  // and the row has been read (team 0's is __syncthreads' barrier: none may follow)
     if (tid == 0 && ok && row + a.slots * step < a.n) fetch(row + a.slots * step, slot);
     if (++slot == static_cast<uint32_t>(a.slots)) slot = 0, parity ^= 1;
     sum = lane < TEAM ? s_sum[side][team][lane] : 0.0f;
@@ -461,7 +485,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
     float scale = 0.0f;
     if constexpr (EIGHT == 1) {
       scale = scale_of(__reduce_max_sync(0xffffffffu, lane < TEAM ? s_top[side][team][lane] : 0u), factor);
-      if (tid == 0 && ok) a.scale[row] = scale;
+      if (tid == 0) a.scale[row] = scale;
     }
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
@@ -470,9 +494,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       if constexpr (EIGHT == 2) {
         for (int o = a.lanes / 2; o; o >>= 1) mine[i] = max(mine[i], __shfl_xor_sync(0xffffffffu, mine[i], o));
         scale = scale_of(mine[i], factor);
-        if (c < chunks && (c & (a.lanes - 1)) == 0) a.scale[row * a.groups + (c >> a.shift)] = scale;
+        if (c < a.chunks && (c & (a.lanes - 1)) == 0) a.scale[row * a.groups + (c >> a.shift)] = scale;
       }
-      if (c >= chunks) continue;
+      if (c >= a.chunks) continue;
       const float by = EIGHT == 0 ? 1.0f : __fdividef(1.0f, scale);
       float y[V];
 #pragma unroll
@@ -1057,3 +1081,10 @@ extern "C" int dflash_rms_norm(const void* x, int64_t x_stride, const void* resi
   if (e != cudaSuccess) return errorf(DFLASH_ERR_CUDA, "rms norm launch: %s", cudaGetErrorString(e));
   return report_error(DFLASH_OK, "");
 }
+
+#ifdef DFLASH_WAIT_TEST
+// Test build only: row `row` is not fetched in the following calls, where they take the rings; -1 turns it off. Returns a cudaError_t.
+extern "C" __attribute__((visibility("default"))) int dflash_test_withhold_norm_row(long long row) {
+  return static_cast<int>(cudaMemcpyToSymbol(dflash::g_withhold_row, &row, sizeof row));
+}
+#endif

@@ -28,7 +28,8 @@ def _lib():
 def test_the_hooks_are_in_the_test_library_only():
     D, lib = _lib()
     product = ctypes.CDLL(D.lib_path())
-    for name in ("dflash_test_withhold_prefix_tile",):
+    lib.dflash_test_withhold_norm_row.argtypes = [ctypes.c_longlong]
+    for name in ("dflash_test_withhold_prefix_tile", "dflash_test_withhold_norm_row"):
         assert hasattr(lib, name) and not hasattr(product, name)
 
 
@@ -90,3 +91,65 @@ def test_a_withheld_tile_of_a_prefix(groups, ps, hq, hkv, dh, window, block, til
     got = _attend(lib, D, b, f32, window, ws, status)  # the same workspace
     assert status.item() == 0
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@gpu
+@pytest.mark.parametrize("n,d,f32,residual,group,row", [
+    (3000, 4096, False, True, 128, 0),        # 8 warps a row, e4m3 by groups
+    (3000, 4096, False, True, 128, 2000),
+    (20001, 512, True, False, 0, 7777),       # a warp a row, e4m3 by rows
+    (16000, 1024, False, True, None, 15999),  # the last row, its own type
+    (1000, 16384, True, False, None, 400),    # a block a row
+    (9000, 2560, False, False, 64, 160),
+])
+def test_a_withheld_row_of_the_norm(n, d, f32, residual, group, row):
+    import torch
+    D, lib = _lib()
+    lib.dflash_test_withhold_norm_row.argtypes = [ctypes.c_longlong]
+    gen = torch.Generator(device="cuda").manual_seed(row)
+    dt = torch.float32 if f32 else torch.bfloat16
+    x = torch.randn(n, d, device="cuda", generator=gen).to(dt)
+    r = torch.randn(n, d, device="cuda", generator=gen).to(dt) if residual else None
+    w = torch.randn(d, device="cuda", generator=gen)
+    eight = group is not None
+    kind = D.OUT_E4M3 if eight else D.OUT_F32 if f32 else D.OUT_BF16
+    want = D.rms_norm(x, w, residual=r, out_dtype=kind, group_size=group or 0)  # the product's
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+
+    def call(st):
+        got = [None if t is None else torch.zeros_like(t) for t in want]
+        rc = lib.dflash_rms_norm(p(x), d, p(r), d, p(w), p(got[1]), d, p(got[0]), d, p(got[2]), n, d, D.OUT_F32 if f32 else D.OUT_BF16,
+                                 D.OUT_F32, kind, group or 0, 1e-6, p(st), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0, lib.dflash_last_error().decode()
+        return got
+
+    for st in (status, None):
+        status.zero_()
+        assert lib.dflash_test_withhold_norm_row(row) == 0
+        try:
+            torch.cuda.synchronize()
+            t0 = time.perf_counter()
+            got = call(st)
+            torch.cuda.synchronize()
+            took = time.perf_counter() - t0
+        finally:
+            assert lib.dflash_test_withhold_norm_row(-1) == 0
+        assert took < 1.0, f"the timed-out call took {took:.3f} s"
+        assert st is None or status.item() == D.STATUS_TIMEOUT
+        # the row and those behind it of the same warps are NaN, every other row is right
+        lost = got[0].float().isnan().all(1)
+        at = lost.nonzero()[:, 0].tolist()
+        step = at[1] - at[0] if len(at) > 1 else n
+        assert at == list(range(row, n, step))
+        assert step >= torch.cuda.get_device_properties(0).multi_processor_count
+        for a, b in zip(got, want):
+            if a is not None:
+                assert torch.equal(a[~lost].view(torch.uint8), b[~lost].view(torch.uint8))
+        if eight:
+            assert bool(got[2][lost].isnan().all())
+    status.zero_()
+    got = call(status)
+    assert status.item() == 0
+    for a, b in zip(got, want):
+        assert (a is None) == (b is None) and (a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8)))
