@@ -360,8 +360,6 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
 // its own, so that what is in flight does not go by the registers that wait for it.
 // Two columns an instruction: with one it was short of issue slots (71 % of them taken) before it was short of HBM, 108 us, not
 // 100 (16384 x 5120).
-// Where a team's wait runs out it takes no more rows: that row and the team's later ones become NaN, and copies that were begun
-// have landed (or were waited for once more) before the block ends.
 #ifdef DFLASH_WAIT_TEST
 // Test build only: a row that is not fetched.
 __device__ long long g_withhold_row = -1;
@@ -373,6 +371,44 @@ template <int TEAM>
 struct Ring {
   static constexpr int kTeams = kRingThreads / 32 / TEAM, kThreads = 32 * TEAM, kMost = 8;  // rows in a team's ring
 };
+
+// What is left to a warp whose wait for `row` ran out, or for a copy that was not fetched after that: the row and its team's later ones
+// become NaN, and the warp that fetches waits once more for what it has fetched, so that no copy is on its way when the block ends.
+// The team's other warps may be here too or not: the barriers are the same. Not inlined: with this, or a flag, in the loop over rows that one was
+// slower (16384 x 5120 with residual and e4m3 by 128 98 us, 94 so; 4000 x 16384 up to 90, 73).
+template <typename T, int EIGHT, int TEAM>
+__device__ __noinline__ void lost_rows(const NormArgs& a, int64_t row, float* my_sum, int side, uint32_t bars, uint32_t slot, uint32_t parity) {
+  using R = Ring<TEAM>;
+  constexpr int V = 16 / sizeof(T);
+  const int team = threadIdx.x / R::kThreads, tid = threadIdx.x % R::kThreads, lane = tid & 31;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * R::kTeams;
+  if (lane == 0 && a.err) atomicOr(a.err, kErrTimeout);
+  if (tid == 0) {  // this row, and those in the slots behind
+#pragma unroll 1
+    for (int i = 0; i < a.slots && row + i * step < a.n; ++i) {
+      int dummy = 0;
+      mbar_wait(bars + 8 * slot, parity, &dummy);
+      if (++slot == static_cast<uint32_t>(a.slots)) slot = 0, parity ^= 1;
+    }
+  }
+  __syncwarp();
+  const float nan = __int_as_float(0x7fffffff);
+#pragma unroll 1
+  for (; row < a.n; row += step, side ^= 1) {
+    if (lane == 0) my_sum[side * R::kTeams * TEAM] = nan;  // the row's factor, and with it its scales, is NaN in the other warps
+    if constexpr (TEAM > 1) named_barrier(team, R::kThreads);
+    if (EIGHT == 1 && tid == 0) a.scale[row] = nan;
+#pragma unroll 1
+    for (int c = tid; c < a.chunks; c += R::kThreads) {
+      float y[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) y[j] = nan;
+      if (EIGHT == 2 && (c & (a.lanes - 1)) == 0) a.scale[row * a.groups + (c >> a.shift)] = nan;
+      if constexpr (EIGHT == 0) store_vec<T, V>(static_cast<T*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, y);
+      else store_e4m3<V>(static_cast<uint8_t*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, y);
+    }
+  }
+}
 
 template <typename T, int EIGHT, int TEAM>
 __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_constant__ NormArgs a) {
@@ -407,29 +443,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
     for (int i = 0; i < a.slots && row + i * step < a.n; ++i) fetch(row + i * step, i);
   uint32_t slot = 0, parity = 0;
   int side = 0;
-  bool ok = true;  // this thread's waits, up to now
 #pragma unroll 1
   for (; row < a.n; row += step, side ^= 1) {
-    if (ok && !mbar_wait(bars + 8 * slot, parity, &s_abort[team])) {
-      ok = false;  // the team stays together: its barriers are still passed
-      if (a.err) atomicOr(a.err, kErrTimeout);
-      if (tid == 0) {  // what it has fetched: this row and those in the slots behind
-        uint32_t at = slot, p = parity;
-#pragma unroll 1
-        for (int i = 0; i < a.slots && row + i * step < a.n; ++i) {
-          int dummy = 0;
-          mbar_wait(bars + 8 * at, p, &dummy);
-          if (++at == static_cast<uint32_t>(a.slots)) at = 0, p ^= 1;
-        }
-      }
-    }
-    const int chunks = ok ? a.chunks : 0;
+    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * slot, parity, &s_abort[team]))) break;  // it ran out
+    const int chunks = a.chunks;
     const uint8_t* here = smem + (ring - smem_u32(smem)) + slot * slot_bytes;
     uint64_t h[kHeld][V / 2], sum2 = f32x2(0.0f, 0.0f);  // two columns each
     uint32_t top = 0, mine[kHeld];
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-      if (i * R::kThreads >= a.chunks) break;
+      if (i * R::kThreads >= chunks) break;
       const int c = i * R::kThreads + tid;
       mine[i] = 0;
       if (c < chunks) {
@@ -457,15 +480,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
         }
         mine[i] = __float_as_uint(largest);
         if constexpr (EIGHT == 1) top = max(top, mine[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) h[i][j] = f32x2(0.0f, 0.0f);
       }
     }
     float sum, odd;
     f32x2_split(sum2, sum, odd);
     sum += odd;
-    if (!ok) sum = __int_as_float(0x7fffffff);  // and with it the row's factor and scales
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if constexpr (EIGHT == 1) top = __reduce_max_sync(0xffffffffu, top);
@@ -475,7 +494,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
     }
     if constexpr (TEAM == 1) __syncwarp();
     else named_barrier(team, R::kThreads);  // and the row has been read (team 0's is __syncthreads' barrier: none may follow)
-    if (tid == 0 && ok && row + a.slots * step < a.n) fetch(row + a.slots * step, slot);
+    if (tid == 0 && row + a.slots * step < a.n) fetch(row + a.slots * step, slot);
     if (++slot == static_cast<uint32_t>(a.slots)) slot = 0, parity ^= 1;
     sum = lane < TEAM ? s_sum[side][team][lane] : 0.0f;
 #pragma unroll
@@ -489,14 +508,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
     }
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-      if (i * R::kThreads >= a.chunks) break;
+      if (i * R::kThreads >= chunks) break;
       const int c = i * R::kThreads + tid;
       if constexpr (EIGHT == 2) {
         for (int o = a.lanes / 2; o; o >>= 1) mine[i] = max(mine[i], __shfl_xor_sync(0xffffffffu, mine[i], o));
         scale = scale_of(mine[i], factor);
-        if (c < a.chunks && (c & (a.lanes - 1)) == 0) a.scale[row * a.groups + (c >> a.shift)] = scale;
+        if (c < chunks && (c & (a.lanes - 1)) == 0) a.scale[row * a.groups + (c >> a.shift)] = scale;
       }
-      if (c >= a.chunks) continue;
+      if (c >= chunks) continue;
       const float by = EIGHT == 0 ? 1.0f : __fdividef(1.0f, scale);
       float y[V];
 #pragma unroll
@@ -509,6 +528,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       else store_e4m3<V>(static_cast<uint8_t*>(a.out) + row * a.out_row + static_cast<int64_t>(c) * V, y);
     }
   }
+  if (row < a.n) lost_rows<T, EIGHT, TEAM>(a, row, s_sum[0][team] + warp, side, bars, slot, parity);
 }
 
 // ---- Rows whose width is no multiple of a 16-byte chunk, so that each begins somewhere else in one: chunks are cut where memory
