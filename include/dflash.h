@@ -414,8 +414,9 @@ DFLASH_API size_t dflash_decode_workspace_size(int num_reqs, int hq, int hkv, in
  *   Dh in {64, 128}; Hq % Hkv == 0, any group size. bf16 products are exact, sums f32, rounded once
  *   every 16 rows; the weights keep 24 bits (16 for a bf16 output of more than 8 heads a group). Two launches (attention, join), or one
  *   where max_ctx_len (or the window) is at most 512 (less past 16 heads a group) and there are no
- *   more (sequence, kv head) pairs than SMs. Results do not depend on timing. Rows outside the lengths and the window may hold
- *   anything; a stored value that is infinite gives NaN in its column.
+ *   more (sequence, kv head) pairs than SMs. Results do not depend on timing. Rows outside the lengths and the window
+ *   may hold anything. A NaN among a head's scores makes its output and lse NaN; a seen value of V that is infinite
+ *   gives NaN or that infinity in its column.
  */
 DFLASH_API int dflash_decode_attention_paged(const dflash_bf16* q, int64_t q_stride, const dflash_bf16* k_pool,
                                              const dflash_bf16* v_pool, const int32_t* block_table,
@@ -556,7 +557,8 @@ DFLASH_API int dflash_rms_norm(const void* x, int64_t x_stride, const void* resi
 /*
  * dflash_rotary_axes -- dflash_rotary with a position on each of several axes (time, height, width):
  * pair i of token t turns by positions[pair_axis[i], t] * inv_freq[i].
- *   positions  int32 [num_axes, n], axis_stride elements (at least n) between axes; num_axes in 1..4
+ *   positions  int32 [num_axes, n], axis_stride elements (at least n: one row for all axes is refused) between
+ *              axes; num_axes in 1..4
  *   pair_axis  HOST uint8 [rotary_dim / 2], each below num_axes: read during the call
  * Everything else as dflash_rotary, the inverse (the gradient) included.
  */
@@ -608,11 +610,12 @@ DFLASH_API size_t dflash_shared_workspace_size(int num_reqs, int num_groups, int
  *              rows (num_reqs x Hkv x Dh x 4 bytes x max_ctx_len, or the window) let them do so, and only report bad groups;
  *              and so do groups whose (sequences - 1) x prefix is below 512 rows. Prefixes below 64 rows are never shared.
  *   Every other argument, and the result, as dflash_decode_attention_paged (the workspace as
- *   dflash_shared_workspace_size says). The result does not depend on timing; another prefix gives another order of the
- *   sums. With a window, rows are read once for all where the windows of all that share reach them; a sequence whose
- *   window has left more than half of the prefix (or of what a window holds) behind reads all its rows itself. A sequence
- *   sees nothing of what rows hold that are outside its length and window, whatever that is. status also takes
- *   DFLASH_STATUS_TIMEOUT, where a bounded wait ran out: sequences that share a prefix are NaN then (out and lse).
+ *   dflash_shared_workspace_size says); weights of rows that are read once for a group keep 16 bits, 24 for f32 outputs.
+ *   The result does not depend on timing; another prefix gives another order of the sums. With a window, rows are read
+ *   once for all where the windows of all that share reach them; a sequence whose window has left more than half of the
+ *   prefix (or of what a window holds) behind reads all its rows itself. A sequence sees nothing of what rows hold that
+ *   are outside its length and window, whatever that is. status also takes DFLASH_STATUS_TIMEOUT, where a bounded wait
+ *   ran out: sequences that share a prefix are NaN then (out and lse).
  */
 DFLASH_API int dflash_decode_attention_shared(const dflash_bf16* q, int64_t q_stride, const dflash_bf16* k_pool,
                                               const dflash_bf16* v_pool, const int32_t* block_table,

@@ -187,7 +187,7 @@ def rotary_axes(q, positions, axes, inv_freq, *, k=None, v=None, q_out=None, k_o
                 interleaved=False, inverse=False, status=None, stream=None):
     """`rotary` with a position on each of several axes (time, height, width); returns (q_out, k_out).
 
-    positions [A, n] int32, A <= 4 (an axis's positions contiguous); axes: the axis of every pair, host integers
+    positions [A, n] int32, A <= 4 (an axis's positions contiguous, each axis with its own: no expanded row); axes: the axis of every pair, host integers
     [rotary_dim / 2] (see rotary_sections). Pair i of token t turns by positions[axes[i], t] * inv_freq[i].
     Everything else as in rotary; inverse=True is the gradient here too.
     """
