@@ -361,10 +361,6 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
 // its own, so that what is in flight does not go by the registers that wait for it.
 // Two columns an instruction: with one it was short of issue slots (71 % of them taken) before it was short of HBM, 108 us, not
 // 100 (16384 x 5120).
-#ifdef DFLASH_WAIT_TEST
-// Test build only: a row that is not fetched.
-__device__ long long g_withhold_row = -1;
-#endif
 constexpr int kRingThreads = 1024, kHeld = 4;    // chunks of a row that a thread holds
 constexpr int kRingBytes = 200 * 1024;
 constexpr int kRingRows = 2;  // rows a team, at least
@@ -373,10 +369,15 @@ struct Ring {
   static constexpr int kTeams = kRingThreads / 32 / TEAM, kThreads = 32 * TEAM, kMost = 8;  // rows in a team's ring
 };
 
+#ifdef DFLASH_WAIT_TEST
+// Test build only: a row that is not fetched.
+__device__ long long g_withhold_row = -1;
+#endif
+
 // What is left to a warp whose wait for `row` ran out, or for a copy that was not fetched after that: the row and its team's later ones
 // become NaN, and the warp that fetches waits once more for what it has fetched, so that no copy is on its way when the block ends.
-// The team's other warps may be here too or not: the barriers are the same. Not inlined: with this, or a flag, in the loop over rows that one was
-// slower (16384 x 5120 with residual and e4m3 by 128 98 us, 94 so; 4000 x 16384 up to 90, 73).
+// The team's other warps may be here too or not: the barriers are the same. Not inlined: with this, or a flag, in it the loop over
+// rows was slower (16384 x 5120 with residual and e4m3 by 128 98 us, 94 so; 4000 x 16384 up to 90, 73).
 template <typename T, int EIGHT, int TEAM>
 __device__ __noinline__ void lost_rows(const NormArgs& a, int64_t row, float* my_sum, int side, uint32_t bars, uint32_t slot, uint32_t parity) {
   using R = Ring<TEAM>;

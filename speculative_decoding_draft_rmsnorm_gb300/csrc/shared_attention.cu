@@ -20,10 +20,11 @@
 // join 3, the finish 5.
 //
 // Why it is cut like this. Weights keep 16 bits (24 for f32 outputs; decode_attention.cu keeps 24 for bf16 too up to 8 heads a
-// group): with 8 each would be rounded as coarsely as the output is. A tile's sums are taken out and added in registers, rounded, because the unit cuts its sums off (and a maximum
-// that grows costs registers only). Warps have one job each, and the copies three: the unit takes some 130 cycles a
-// box. Measured (us, plain floor in brackets): 32 groups of 8 beams on prompts of 512 to 8192 rows 97-99 (65), 64 samples of a prompt of 32000
-// rows 99 (48.5), 16 x 5 in windows of 4096, f32 87 (48.6), 256 on 16384 rows 130 (36.8, by its products).
+// group): with 8 each would be rounded as coarsely as the output is. A tile's sums are taken out and added in registers,
+// rounded, because the unit cuts its sums off (and a maximum that grows costs registers only). Warps have one job each, and
+// the copies three: the unit takes some 130 cycles a box. Measured (us, plain floor in brackets): 32 groups of 8 beams on
+// prompts of 512 to 8192 rows 97-99 (65), 64 samples of a prompt of 32000 rows 99 (48.5), 16 x 5 in windows of 4096, f32 87
+// (48.6), 256 on 16384 rows 130 (36.8, by its products).
 #include <cuda_runtime.h>
 
 #include <algorithm>
